@@ -13,6 +13,15 @@ an exception is raised.
     gemm_f16_nn(A, B, C, alpha, beta)  C = alpha*A@B + beta*C    (FP16, B is K x N)
     gemm_bf16_tn / gemm_bf16_nn         the same with bfloat16
 
+Linear layers in 8-bit integers (int8 rows with one FP32 scale a row):
+
+    quantize_i8(X, Q, scale)                     X as int8 rows
+    rmsnorm_i8(X, gamma, Q, scale, residual, H)  norm of X + residual as int8 rows
+    swiglu_i8(G, U, Q, scale)                    silu(G) * U as int8 rows
+    gemm_i8_tn(A, B, C, scale_a, scale_b, bias, beta)
+                                                 C = scale_a scale_b A@B.T + bias + beta*C
+    dequantize_i8(Q, scale, X)                   X = scale * Q
+
 Matrices are 2-D tensors with unit column stride; a row stride larger than
 the width is passed on as the leading dimension.  C is updated in place and
 returned.
@@ -97,6 +106,13 @@ def _load(path: str):
     L.gemm_tf32_workspace_bytes.restype = i64
     L.gemm_tf32_noalloc.argtypes = sig
     L.gemm_tf32_noalloc.restype = ci
+    L.gemm_i8_tn.argtypes = [i64, i64, i64, vp, i64, vp, vp, i64, vp, vp, f32, vp, i64, ci, vp]
+    L.quantize_i8.argtypes = [i64, i64, vp, i64, ci, vp, i64, vp, vp]
+    L.rmsnorm_i8.argtypes = [i64, i64, vp, i64, vp, i64, vp, ci, f32, ci, vp, i64, vp, i64, vp, vp]
+    L.swiglu_i8.argtypes = [i64, i64, vp, i64, vp, i64, ci, vp, i64, vp, vp]
+    L.dequantize_i8.argtypes = [i64, i64, vp, i64, vp, vp, i64, ci, vp]
+    for name in ("gemm_i8_tn", "quantize_i8", "rmsnorm_i8", "swiglu_i8", "dequantize_i8"):
+        getattr(L, name).restype = ci
     L.dgemm_test_pair_units.argtypes = [i64, i64, i64, i64, i64, vp, i64]
     L.dgemm_test_pair_units.restype = i64
     L.dgemm_test_stream_k_tiles.argtypes = [i64, i64, i64, ci, ci]
@@ -295,3 +311,111 @@ def gemm_bf16_tn(A, B, C, alpha: float = 1.0, beta: float = 0.0, stream=None):
 def gemm_bf16_nn(A, B, C, alpha: float = 1.0, beta: float = 0.0, stream=None):
     """C = alpha * A @ B + beta * C with bfloat16 A, B (K x N) and C."""
     return _gemm16("gemm_bf16_nn", torch.bfloat16, False, A, B, C, alpha, beta, stream)
+
+
+# ---- linear layers in 8-bit integers
+
+_TYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # dgemm_type
+
+
+def _type(t: torch.Tensor, name: str) -> int:
+    code = _TYPE.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if code is None:
+        raise TypeError("%s must be a float32, float16 or bfloat16 tensor" % name)
+    return code
+
+
+def _vec(t, name: str, dtype: torch.dtype, n: int) -> int:
+    if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.shape[0] != n:
+        raise ValueError("%s must be a 1-D tensor of %d" % (name, n))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_cuda or (n > 1 and t.stride(0) != 1):
+        raise ValueError("%s must be a contiguous CUDA tensor" % name)
+    return t.data_ptr()
+
+
+def _like(t, name: str, dtype: torch.dtype, shape):
+    r = _mat(t, name, dtype)
+    if t.shape != shape:
+        raise ValueError("shape mismatch: %s %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    return r
+
+
+def _status(st: int, name: str) -> None:
+    if st != OK:
+        raise DgemmError(st, name)
+
+
+def quantize_i8(X, Q, scale, stream=None):
+    """Each row of X (float32, float16 or bfloat16) as int8 with one FP32 scale:
+    scale = max|x| / 127, Q = rint(x / scale).  Writes and returns (Q, scale);
+    a row of zeros gets scale 0, a row with a NaN or an infinity scale NaN."""
+    ty = _type(X, "X")
+    px, ldx = _mat(X, "X", X.dtype)
+    pq, ldq = _like(Q, "Q", torch.int8, X.shape)
+    rows, cols = X.shape
+    _status(lib().quantize_i8(rows, cols, px, ldx, ty, pq, ldq, _vec(scale, "scale", torch.float32, rows),
+                              _stream(stream)), "quantize_i8")
+    return Q, scale
+
+
+def rmsnorm_i8(X, gamma, Q, scale, residual=None, H=None, eps: float = 1e-6, stream=None):
+    """h = X + residual; y = h * gamma / sqrt(mean(h^2) + eps); the rows of y as
+    int8 in Q with their FP32 scales.  H, if given, receives h in X's type (it
+    may be X or residual itself).  gamma has X's type or float32.  Returns
+    (Q, scale)."""
+    ty = _type(X, "X")
+    px, ldx = _mat(X, "X", X.dtype)
+    rows, cols = X.shape
+    pq, ldq = _like(Q, "Q", torch.int8, X.shape)
+    pr, ldr = _like(residual, "residual", X.dtype, X.shape) if residual is not None else (None, 0)
+    ph, ldh = _like(H, "H", X.dtype, X.shape) if H is not None else (None, 0)
+    tg = _type(gamma, "gamma")
+    pg = _vec(gamma, "gamma", torch.float32 if tg == 0 else X.dtype, cols)
+    _status(lib().rmsnorm_i8(rows, cols, px, ldx, pr, ldr, pg, tg, eps, ty, ph, ldh, pq, ldq,
+                             _vec(scale, "scale", torch.float32, rows), _stream(stream)), "rmsnorm_i8")
+    return Q, scale
+
+
+def swiglu_i8(G, U, Q, scale, stream=None):
+    """y = G / (1 + exp(-G)) * U; the rows of y as int8 in Q with their FP32
+    scales.  G and U may be column slices of one tensor.  Returns (Q, scale)."""
+    ty = _type(G, "G")
+    pg, ldg = _mat(G, "G", G.dtype)
+    pu, ldu = _like(U, "U", G.dtype, G.shape)
+    pq, ldq = _like(Q, "Q", torch.int8, G.shape)
+    rows, cols = G.shape
+    _status(lib().swiglu_i8(rows, cols, pg, ldg, pu, ldu, ty, pq, ldq, _vec(scale, "scale", torch.float32, rows),
+                            _stream(stream)), "swiglu_i8")
+    return Q, scale
+
+
+def dequantize_i8(Q, scale, X, stream=None):
+    """X = Q * scale (a scale for each row), rounded once to X's type."""
+    ty = _type(X, "X")
+    px, ldx = _mat(X, "X", X.dtype)
+    pq, ldq = _like(Q, "Q", torch.int8, X.shape)
+    rows, cols = X.shape
+    _status(lib().dequantize_i8(rows, cols, pq, ldq, _vec(scale, "scale", torch.float32, rows), px, ldx, ty,
+                                _stream(stream)), "dequantize_i8")
+    return X
+
+
+def gemm_i8_tn(A, B, C, scale_a, scale_b, bias=None, beta: float = 0.0, stream=None):
+    """C[m, n] = scale_a[m] * scale_b[n] * (A @ B.T)[m, n] + bias[n] + beta * C[m, n];
+    A: M x K and B: N x K int8, C: M x N float32, float16 or bfloat16; scales
+    and bias float32."""
+    ty = _type(C, "C")
+    pa, lda = _mat(A, "A", torch.int8)
+    pb, ldb = _mat(B, "B", torch.int8)
+    pc, ldc = _mat(C, "C", C.dtype)
+    M, K = A.shape
+    N, K2 = B.shape
+    if K2 != K or tuple(C.shape) != (M, N):
+        raise ValueError("shape mismatch: A %s, B %s, C %s" % (tuple(A.shape), tuple(B.shape), tuple(C.shape)))
+    _status(lib().gemm_i8_tn(M, N, K, pa, lda, _vec(scale_a, "scale_a", torch.float32, M), pb, ldb,
+                             _vec(scale_b, "scale_b", torch.float32, N),
+                             None if bias is None else _vec(bias, "bias", torch.float32, N), beta, pc, ldc, ty,
+                             _stream(stream)), "gemm_i8_tn")
+    return C

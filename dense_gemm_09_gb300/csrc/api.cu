@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include "dgemm.h"
+#include "i8_gemm.h"
 #include "internal.h"
 
 namespace dgemm {
@@ -69,7 +70,8 @@ int validate(int64_t M, int64_t N, int64_t K, float alpha, const void *A, int64_
 int checks_failed(int clear, int *site)
 {
     int (*const readers[])(int, int *) = {check_status_simt, check_status_tma, check_status_umma,
-                                          check_status_scale, check_status_repack};
+                                          check_status_scale, check_status_repack, check_status_i8_rows,
+                                          check_status_i8_gemm};
     int status = DGEMM_OK, where = 0;
     for (auto rd : readers) {
         int s = 0;
@@ -284,6 +286,90 @@ extern "C" int gemm_f32_ws(int64_t M, int64_t N, int64_t K, float alpha, const f
         }
     }
     return finish(launch_sgemm_simt(M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, stream, dev));
+}
+
+namespace {
+
+bool known_type(int type)
+{
+    return type == DGEMM_TYPE_F32 || type == DGEMM_TYPE_F16 || type == DGEMM_TYPE_BF16;
+}
+
+// Sizes of a row operator; *empty when there is nothing to do.
+bool rows_ok(int64_t rows, int64_t cols, int type, bool *empty)
+{
+    *empty = rows == 0 || cols == 0;
+    return rows >= 0 && cols >= 0 && rows <= INT32_MAX && known_type(type);
+}
+
+}  // namespace
+
+extern "C" int gemm_i8_tn(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, const float *scale_a,
+                          const int8_t *B, int64_t ldb, const float *scale_b, const float *bias, float beta, void *C,
+                          int64_t ldc, int c_type, cudaStream_t stream)
+{
+    int st = validate(M, N, K, 1.f, A, lda, B, ldb, K, C, ldc);
+    if (st != DGEMM_OK) return st;
+    if (!known_type(c_type)) return DGEMM_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return DGEMM_OK;
+    if (!scale_a || !scale_b) return DGEMM_ERR_INVALID_ARG;
+    if ((M + 63) / 64 > INT32_MAX / ((N + 63) / 64)) return DGEMM_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if ((st = check_device(dev)) != DGEMM_OK) return st;
+    const I8Params p{M, N, K, A, B, lda, ldb, scale_a, scale_b, bias, beta, C, ldc};
+    return finish(launch_gemm_i8(p, c_type, stream, dev));
+}
+
+extern "C" int quantize_i8(int64_t rows, int64_t cols, const void *X, int64_t ldx, int type, int8_t *Q, int64_t ldq,
+                           float *scale, cudaStream_t stream)
+{
+    bool empty;
+    if (!rows_ok(rows, cols, type, &empty) || ldx < cols || ldq < cols) return DGEMM_ERR_INVALID_ARG;
+    if (empty) return DGEMM_OK;
+    if (!X || !Q || !scale) return DGEMM_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int st = check_device(dev); st != DGEMM_OK) return st;
+    return finish(launch_quantize_i8(rows, cols, X, ldx, type, Q, ldq, scale, stream));
+}
+
+extern "C" int rmsnorm_i8(int64_t rows, int64_t cols, const void *X, int64_t ldx, const void *residual, int64_t ldr,
+                          const void *gamma, int gamma_type, float eps, int type, void *H, int64_t ldh, int8_t *Q,
+                          int64_t ldq, float *scale, cudaStream_t stream)
+{
+    bool empty;
+    if (!rows_ok(rows, cols, type, &empty) || ldx < cols || ldq < cols || (residual && ldr < cols) ||
+        (H && ldh < cols) || (gamma_type != type && gamma_type != DGEMM_TYPE_F32) || !(eps >= 0.f))
+        return DGEMM_ERR_INVALID_ARG;
+    if (empty) return DGEMM_OK;
+    if (!X || !gamma || !Q || !scale) return DGEMM_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int st = check_device(dev); st != DGEMM_OK) return st;
+    return finish(launch_rmsnorm_i8(rows, cols, X, ldx, residual, ldr, gamma, gamma_type == DGEMM_TYPE_F32, eps,
+                                    type, H, ldh, Q, ldq, scale, stream));
+}
+
+extern "C" int swiglu_i8(int64_t rows, int64_t cols, const void *G, int64_t ldg, const void *U, int64_t ldu, int type,
+                         int8_t *Q, int64_t ldq, float *scale, cudaStream_t stream)
+{
+    bool empty;
+    if (!rows_ok(rows, cols, type, &empty) || ldg < cols || ldu < cols || ldq < cols) return DGEMM_ERR_INVALID_ARG;
+    if (empty) return DGEMM_OK;
+    if (!G || !U || !Q || !scale) return DGEMM_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int st = check_device(dev); st != DGEMM_OK) return st;
+    return finish(launch_swiglu_i8(rows, cols, G, ldg, U, ldu, type, Q, ldq, scale, stream));
+}
+
+extern "C" int dequantize_i8(int64_t rows, int64_t cols, const int8_t *Q, int64_t ldq, const float *scale, void *X,
+                             int64_t ldx, int type, cudaStream_t stream)
+{
+    bool empty;
+    if (!rows_ok(rows, cols, type, &empty) || ldx < cols || ldq < cols) return DGEMM_ERR_INVALID_ARG;
+    if (empty) return DGEMM_OK;
+    if (!X || !Q || !scale) return DGEMM_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int st = check_device(dev); st != DGEMM_OK) return st;
+    return finish(launch_dequantize_i8(rows, cols, Q, ldq, scale, X, ldx, type, stream, dev));
 }
 
 extern "C" const char *dgemm_status_string(int status)

@@ -1,0 +1,192 @@
+// i8_gemm.cu -- gemm_i8_tn: the product of two int8 matrices with an FP32
+// scale for each row of either,
+//
+//   C[m, n] = scale_a[m] * scale_b[n] * sum_k A[m, k] B[n, k] + bias[n] + beta * C[m, n].
+//
+// i8_mma_kernel is the kernel for every case: operands of any alignment and
+// pitch, any sizes.  64 x 64 output tiles, four warps of 32 x 32; K in chunks
+// of 64 bytes staged in shared memory through registers (the next chunk's
+// loads are in flight while a chunk is multiplied); mma.sync m16n8k32 on
+// int8 with exact int32 sums.
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "dgemm.h"
+#include "i8_gemm.h"
+#include "internal.h"
+
+#define DGEMM_UNIT 7
+#include "checked.cuh"
+
+namespace dgemm {
+namespace {
+
+constexpr int kTile = 64;       // rows of A and of B in a block's tile
+constexpr int kChunk = 64;      // K bytes of one stage
+constexpr int kPitch = 80;      // bytes between staged rows: 8 rows x 4 words fall in 32 distinct banks
+constexpr int kThreads = 128;
+// K a whole number of chunks below which an int32 sum cannot overflow:
+// 2^16 * 128 * 128 = 2^30
+constexpr int64_t kFlush = 1 << 16;
+
+// C[row, col] from the sum of products.
+template <typename T>
+__device__ __forceinline__ void store_one(const I8Params &p, int64_t row, int64_t col, float sum)
+{
+    if (row >= p.M || col >= p.N || !DGEMM_CHECK(row >= 0 && col >= 0)) return;
+    T *dst = static_cast<T *>(p.C) + row * p.ldc + col;
+    float v = sum * p.scale_a[row] * p.scale_b[col];
+    if (p.bias) v += p.bias[col];
+    if (p.beta != 0.f) v = fmaf(p.beta, i8_to_f32(*dst), v);
+    *dst = i8_from_f32<T>(v);
+}
+
+// The 32 bytes of one thread's half row of a chunk, as kW-byte loads; bytes
+// past the row's end (left) or of rows outside the matrix are zeros.
+template <int kW>
+__device__ __forceinline__ void load_half_row(const int8_t *p, bool row_ok, int64_t left, uint32_t (&w)[8])
+{
+    if (row_ok && left >= 32 && kW == 16) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p)), b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+        w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+        return;
+    }
+    if (row_ok && left >= 32 && kW == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t v = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+            if (row_ok && i * 4 + b < left) v |= static_cast<uint32_t>(static_cast<uint8_t>(p[i * 4 + b])) << (8 * b);
+        w[i] = v;
+    }
+}
+
+__device__ __forceinline__ void mma_s8(int32_t (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2])
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+template <typename T, int kW>
+__global__ void __launch_bounds__(kThreads) i8_mma_kernel(const I8Params p, int64_t tiles_n)
+{
+    __shared__ __align__(16) uint8_t sa[kTile * kPitch], sb[kTile * kPitch];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int64_t m0 = blockIdx.x / tiles_n * kTile, n0 = blockIdx.x % tiles_n * kTile;
+    const int wm = (warp & 1) * 32, wn = (warp >> 1) * 32;
+    // this thread stages half a row (32 bytes) of either tile
+    const int srow = tid >> 1, sbyte = (tid & 1) * 32;
+    const bool a_ok = m0 + srow < p.M, b_ok = n0 + srow < p.N;
+    const int8_t *ap = p.A + (a_ok ? (m0 + srow) * p.lda : 0) + sbyte;
+    const int8_t *bp = p.B + (b_ok ? (n0 + srow) * p.ldb : 0) + sbyte;
+    int32_t acc[2][4][4] = {};
+    float sum[2][4][4] = {};
+    uint32_t wa[8], wb[8];
+    auto fetch = [&](int64_t k) {
+        load_half_row<kW>(ap + k, a_ok, p.K - k - sbyte, wa);
+        load_half_row<kW>(bp + k, b_ok, p.K - k - sbyte, wb);
+    };
+    if (p.K > 0) fetch(0);
+    for (int64_t k = 0; k < p.K; k += kChunk) {
+        __syncthreads();  // the previous chunk has been read
+        if (DGEMM_CHECK(srow * kPitch + sbyte + 32 <= kTile * kPitch)) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                *reinterpret_cast<uint4 *>(sa + srow * kPitch + sbyte + i * 16) =
+                    make_uint4(wa[4 * i], wa[4 * i + 1], wa[4 * i + 2], wa[4 * i + 3]);
+                *reinterpret_cast<uint4 *>(sb + srow * kPitch + sbyte + i * 16) =
+                    make_uint4(wb[4 * i], wb[4 * i + 1], wb[4 * i + 2], wb[4 * i + 3]);
+            }
+        }
+        __syncthreads();
+        if (k + kChunk < p.K) fetch(k + kChunk);
+#pragma unroll
+        for (int kk = 0; kk < kChunk; kk += 32) {
+            uint32_t a[2][4], b[4][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                    a[i][h] = *reinterpret_cast<const uint32_t *>(sa + (wm + i * 16 + g + (h & 1) * 8) * kPitch + kk +
+                                                                  t * 4 + (h >> 1) * 16);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    b[j][h] =
+                        *reinterpret_cast<const uint32_t *>(sb + (wn + j * 8 + g) * kPitch + kk + t * 4 + h * 16);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mma_s8(acc[i][j], a[i], b[j]);
+        }
+        if ((k + kChunk) % kFlush == 0 || k + kChunk >= p.K) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        sum[i][j][e] += static_cast<float>(acc[i][j][e]);
+                        acc[i][j][e] = 0;
+                    }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                store_one<T>(p, m0 + wm + i * 16 + g + (e >> 1) * 8, n0 + wn + j * 8 + t * 2 + (e & 1), sum[i][j][e]);
+}
+
+template <typename T>
+const char *launch_mma(const I8Params &p, cudaStream_t stream)
+{
+    const int64_t tiles_m = (p.M + kTile - 1) / kTile, tiles_n = (p.N + kTile - 1) / kTile;
+    if (tiles_m > INT32_MAX / tiles_n) return nullptr;
+    const unsigned grid = static_cast<unsigned>(tiles_m * tiles_n);
+    auto on = [&](int to) {
+        return reinterpret_cast<uintptr_t>(p.A) % to == 0 && reinterpret_cast<uintptr_t>(p.B) % to == 0 &&
+               p.lda % to == 0 && p.ldb % to == 0;
+    };
+    if (on(16)) {
+        i8_mma_kernel<T, 16><<<grid, kThreads, 0, stream>>>(p, tiles_n);
+        return "i8_mma_64x64x64_ld16";
+    }
+    if (on(4)) {
+        i8_mma_kernel<T, 4><<<grid, kThreads, 0, stream>>>(p, tiles_n);
+        return "i8_mma_64x64x64_ld4";
+    }
+    i8_mma_kernel<T, 1><<<grid, kThreads, 0, stream>>>(p, tiles_n);
+    return "i8_mma_64x64x64_ld1";
+}
+
+}  // namespace
+
+const char *launch_gemm_i8(const I8Params &p, int c_type, cudaStream_t stream, const DeviceInfo &)
+{
+    switch (c_type) {
+    case DGEMM_TYPE_F32: return launch_mma<float>(p, stream);
+    case DGEMM_TYPE_F16: return launch_mma<__half>(p, stream);
+    case DGEMM_TYPE_BF16: return launch_mma<__nv_bfloat16>(p, stream);
+    default: return nullptr;
+    }
+}
+
+}  // namespace dgemm
+
+DGEMM_DEFINE_CHECK_READER(check_status_i8_gemm)

@@ -71,6 +71,8 @@ int check_status_tma(int clear, int *site);
 int check_status_umma(int clear, int *site);
 int check_status_scale(int clear, int *site);
 int check_status_repack(int clear, int *site);
+int check_status_i8_rows(int clear, int *site);
+int check_status_i8_gemm(int clear, int *site);
 
 // Rows taken off M for the C-store checks of the next TMA-fed SIMT launch
 // on this host thread (dgemm_test_shrink_bounds); taking it clears it.
@@ -95,6 +97,22 @@ bool launch_repack_f32(const float *src, int64_t rows, int64_t cols, int64_t ld_
 
 // Device status word of the tensor-core kernels (see dgemm_device_status).
 int umma_read_status(int clear);
+
+// The 8-bit row operators (i8_rows.cu); type is a dgemm_type.  residual and h
+// may be null; gamma has the rows' type, or FP32 with gamma_f32.
+const char *launch_quantize_i8(int64_t rows, int64_t cols, const void *x, int64_t ldx, int type, int8_t *q,
+                               int64_t ldq, float *scale, cudaStream_t stream);
+const char *launch_rmsnorm_i8(int64_t rows, int64_t cols, const void *x, int64_t ldx, const void *residual,
+                              int64_t ldr, const void *gamma, bool gamma_f32, float eps, int type, void *h,
+                              int64_t ldh, int8_t *q, int64_t ldq, float *scale, cudaStream_t stream);
+const char *launch_swiglu_i8(int64_t rows, int64_t cols, const void *g, int64_t ldg, const void *u, int64_t ldu,
+                             int type, int8_t *q, int64_t ldq, float *scale, cudaStream_t stream);
+const char *launch_dequantize_i8(int64_t rows, int64_t cols, const int8_t *q, int64_t ldq, const float *scale,
+                                 void *x, int64_t ldx, int type, cudaStream_t stream, const DeviceInfo &dev);
+
+// The 8-bit product (i8_gemm.cu); c_type is a dgemm_type.
+struct I8Params;
+const char *launch_gemm_i8(const I8Params &p, int c_type, cudaStream_t stream, const DeviceInfo &dev);
 
 // Test hook behind dgemm_test_inject_stall.
 void umma_inject_stall(uint64_t wait_limit_ns);

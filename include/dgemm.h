@@ -2,11 +2,13 @@
  * dgemm.h -- C ABI of libdgemm, a dense row-major GEMM library for one
  * NVIDIA GB300 (compute capability 10.3, sm_103a).
  *
- * Every entry point computes
+ * Every gemm_f32, gemm_tf32, gemm_f16 and gemm_bf16 entry point computes
  *
  *     C = alpha * op(A) * op(B) + beta * C
  *
- * on the GPU, asynchronously on the caller's CUDA stream, and returns a
+ * (the 8-bit product gemm_i8_tn has a scale for each row of A and of B in
+ * alpha's place, and row operators around it; they follow the 16-bit calls
+ * below) on the GPU, asynchronously on the caller's CUDA stream, and returns a
  * dgemm_status.  The operation is the one the pages define:
  *   - "CUDA GEMM：从基础写法到工程优化", opening definition: C = alpha*A*B +
  *     beta*C with A (M x K), B (K x N), C (M x N), all row-major;
@@ -258,6 +260,86 @@ int gemm_bf16_nn(int64_t M, int64_t N, int64_t K, float alpha,
                  const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb,
                  float beta, uint16_t *C, int64_t ldc, cudaStream_t stream);
 
+/*
+ * Linear layers in 8-bit integers
+ * -------------------------------
+ * A matrix of values is held as int8 rows with one float scale a row: element
+ * (i, j) stands for scale[i] * Q[i, j].  A is quantised a token at a time,
+ * the weights B (stored N x K, a row for each output channel) a channel at a
+ * time.  quantize_i8, rmsnorm_i8 and swiglu_i8 write such matrices,
+ * gemm_i8_tn multiplies two of them, dequantize_i8 reads one back.
+ * The row operators form, in FP32, a row y of `cols` values, then
+ *
+ *     a = max |y|,   scale = a / 127,   q = rint(y * 127 / a)   (ties to even)
+ *
+ * A row of zeros gets scale 0 and zeros.  A row with a NaN or an infinity in
+ * it (or, in rmsnorm_i8, a sum of squares past FP32's range) gets the scale
+ * NaN and zeros, so everything that is made from it is NaN.
+ * Conventions of these calls, beyond those at the top: row-major operands
+ *   with leading dimensions in elements, at least the row length; rows == 0
+ *   or cols == 0 returns DGEMM_OK and writes nothing; DGEMM_ERR_INVALID_ARG
+ *   for negative sizes, more than 2^31 - 1 rows, a leading dimension below
+ *   the row length, an unknown type or a NULL pointer that is not said to be
+ *   optional.  Pointers are aligned to their element type; rows that start
+ *   on 16-byte boundaries (int8 outputs: 8-byte) take the fastest kernels.
+ *   Outputs must not overlap inputs, except where a call allows it.
+ * Source: none on the pages (their products are floating-point).
+ */
+typedef enum {
+    DGEMM_TYPE_F32 = 0,
+    DGEMM_TYPE_F16 = 1,
+    DGEMM_TYPE_BF16 = 2
+} dgemm_type;
+
+/* quantize_i8 -- y = X (rows x cols of `type`). */
+int quantize_i8(int64_t rows, int64_t cols, const void *X, int64_t ldx, int type,
+                int8_t *Q, int64_t ldq, float *scale, cudaStream_t stream);
+
+/*
+ * rmsnorm_i8 -- root-mean-square norm with the residual's addition:
+ *     h = X + residual,   y = h * gamma / sqrt(mean(h^2) + eps)
+ *   residual : same type as X; NULL for none.
+ *   gamma    : `cols` weights of gamma_type, which is `type` or DGEMM_TYPE_F32.
+ *   eps      : >= 0 (DGEMM_ERR_INVALID_ARG otherwise, NaN too).
+ *   H        : if not NULL, receives h rounded to `type`; may be X's or the
+ *              residual's own buffer (with the same leading dimension).  The
+ *              norm is taken of the unrounded h.
+ */
+int rmsnorm_i8(int64_t rows, int64_t cols, const void *X, int64_t ldx, const void *residual, int64_t ldr,
+               const void *gamma, int gamma_type, float eps, int type, void *H, int64_t ldh,
+               int8_t *Q, int64_t ldq, float *scale, cudaStream_t stream);
+
+/*
+ * swiglu_i8 -- gated activation: y = G / (1 + exp(-G)) * U, elementwise.  G
+ * and U may be column ranges of one wider matrix (ldg == ldu).
+ */
+int swiglu_i8(int64_t rows, int64_t cols, const void *G, int64_t ldg, const void *U, int64_t ldu, int type,
+              int8_t *Q, int64_t ldq, float *scale, cudaStream_t stream);
+
+/* dequantize_i8 -- X = scale * Q, formed in FP32 and rounded once to `type`. */
+int dequantize_i8(int64_t rows, int64_t cols, const int8_t *Q, int64_t ldq, const float *scale,
+                  void *X, int64_t ldx, int type, cudaStream_t stream);
+
+/*
+ * gemm_i8_tn -- product of two 8-bit matrices, in the TN layout:
+ *     C[m, n] = scale_a[m] * scale_b[n] * sum_k A[m, k] B[n, k] + bias[n] + beta * C[m, n]
+ *   A, lda  : device, int8, M x K row-major (lda >= K).
+ *   B, ldb  : device, int8, stored N x K row-major (ldb >= K).
+ *   scale_a : M floats;  scale_b: N floats.
+ *   bias    : N floats, or NULL for none.
+ *   beta    : scale of the old C, which is not read when beta == 0.
+ *   C, ldc  : device, c_type (a dgemm_type), M x N row-major (ldc >= N).
+ * The sum is exact wherever its partial sums stay below 2^24 (always for K
+ * <= 1024), and within FP32 rounding of each partial sum beyond; the rest is
+ * formed in FP32 and rounded once to c_type.
+ * K == 0 gives bias + beta * C (A and B are not read; the scales are).
+ * DGEMM_ERR_INVALID_ARG as above, and for more than 2^31 - 1 tiles of 64 x 64
+ * of C.
+ */
+int gemm_i8_tn(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, const float *scale_a,
+               const int8_t *B, int64_t ldb, const float *scale_b, const float *bias, float beta,
+               void *C, int64_t ldc, int c_type, cudaStream_t stream);
+
 /* A static, NUL-terminated description of a dgemm_status value. */
 const char *dgemm_status_string(int status);
 
@@ -287,8 +369,8 @@ int dgemm_device_status(int clear);
  * dgemm_check_site -- the site of the first failed check since the last
  * clear of the device status: (translation unit x 100000 + source line) of
  * the library's sources, units 1 sgemm_simt.cu, 2 sgemm_tma.cu,
- * 3 umma_gemm.cu, 4 scale_c.cu, 5 repack.cu; 0 if none failed, and always 0
- * in libdgemm.so.  Synchronises the device.  Source: none on the pages.
+ * 3 umma_gemm.cu, 4 scale_c.cu, 5 repack.cu, 6 i8_rows.cu, 7 i8_gemm.cu; 0 if
+ * none failed, and always 0 in libdgemm.so.  Synchronises the device.  Source: none on the pages.
  */
 int dgemm_check_site(void);
 
