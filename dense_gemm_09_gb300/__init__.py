@@ -98,6 +98,8 @@ def _load(path: str):
     L.dgemm_last_kernel.restype = ctypes.c_char_p
     L.dgemm_tune_next.argtypes = [ci, ci, ci]
     L.dgemm_tune_next.restype = ci
+    L.dgemm_tune_i8_next.argtypes = [ci, ci, ci]
+    L.dgemm_tune_i8_next.restype = ci
     L.gemm_tf32_ws.argtypes = sig[:11] + [vp, i64, vp]
     L.gemm_tf32_ws.restype = ci
     L.gemm_f32_ws.argtypes = sig[:11] + [vp, i64, vp]
@@ -419,3 +421,13 @@ def gemm_i8_tn(A, B, C, scale_a, scale_b, bias=None, beta: float = 0.0, stream=N
                              None if bias is None else _vec(bias, "bias", torch.float32, N), beta, pc, ldc, ty,
                              _stream(stream)), "gemm_i8_tn")
     return C
+
+
+# Kernels for tune_i8_next (see dgemm_tune_i8_next in include/dgemm.h)
+TUNE_I8_MMA, TUNE_I8_PAIR_TOKENS, TUNE_I8_PAIR_CHANNELS, TUNE_I8_SPLIT = 1, 2, 3, 4
+
+
+def tune_i8_next(variant: int, bn: int = 0, split: int = 1) -> None:
+    """Tuning hook: fix the kernel of the next gemm_i8_tn call on this thread
+    (variant TUNE_I8_* or TUNE_AUTO, tile width bn, CTAs sharing a tile)."""
+    _status(lib().dgemm_tune_i8_next(int(variant), int(bn), int(split)), "dgemm_tune_i8_next")

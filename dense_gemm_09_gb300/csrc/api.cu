@@ -71,7 +71,7 @@ int checks_failed(int clear, int *site)
 {
     int (*const readers[])(int, int *) = {check_status_simt, check_status_tma, check_status_umma,
                                           check_status_scale, check_status_repack, check_status_i8_rows,
-                                          check_status_i8_gemm};
+                                          check_status_i8_gemm, check_status_i8_umma};
     int status = DGEMM_OK, where = 0;
     for (auto rd : readers) {
         int s = 0;
@@ -393,8 +393,10 @@ extern "C" int dgemm_device_status(int clear)
     if (cudaDeviceSynchronize() != cudaSuccess) return DGEMM_ERR_LAUNCH;
     const int a = umma_read_status(clear);
     const int b = simt_read_status(clear);
+    const int c = i8_read_status(clear);
     if (a != DGEMM_OK) return a;
     if (b != DGEMM_OK) return b;
+    if (c != DGEMM_OK) return c;
     return checks_failed(clear, nullptr);
 }
 
@@ -425,6 +427,11 @@ int64_t dgemm::take_shrink_bounds()
 extern "C" int dgemm_tune_next(int variant, int bn, int split)
 {
     return umma_tune_next(variant, bn, split);
+}
+
+extern "C" int dgemm_tune_i8_next(int variant, int bn, int split)
+{
+    return i8_tune_next(variant, bn, split);
 }
 
 extern "C" int64_t dgemm_test_pair_units(int64_t tiles, int64_t pairs, int64_t num_kb, int64_t sk_tiles,

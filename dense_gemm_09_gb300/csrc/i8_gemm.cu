@@ -9,6 +9,8 @@
 // loads are in flight while a chunk is multiplied); mma.sync m16n8k32 on
 // int8 with exact int32 sums.
 #include <cstdint>
+#include <mutex>
+#include <string>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -175,16 +177,73 @@ const char *launch_mma(const I8Params &p, cudaStream_t stream)
     return "i8_mma_64x64x64_ld1";
 }
 
+// One-shot override of the next call on this host thread (dgemm_tune_i8_next).
+thread_local I8Config t_tune = {kI8Auto, 0, 1};
+
+// Whether TMA can describe both operands.
+bool tma_ok(const I8Params &p)
+{
+    constexpr int64_t kMax = INT32_MAX - 512;
+    return p.K > 0 && aligned16(p.A) && aligned16(p.B) && p.lda % 16 == 0 && p.ldb % 16 == 0 && p.M <= kMax &&
+           p.N <= kMax && p.K <= kMax;
+}
+
+I8Config choose_config(const I8Params &p, int sm_count)
+{
+    if (p.M > 128) return {kI8PairTokens, 192, 1};
+    const int bn = static_cast<int>((p.M + 15) / 16 * 16);
+    const int64_t tiles = (p.N + 127) / 128, kb = (p.K + 127) / 128;
+    int split = 1;
+    while (split < 8 && tiles * (split + 1) <= sm_count && kb >= 4 * (split + 1)) ++split;
+    return {kI8Split, bn, split};
+}
+
+// Kernel names by configuration, built once.
+const char *config_name(const I8Config &c)
+{
+    static std::string names[13][9][2];
+    static std::once_flag once;
+    std::call_once(once, [] {
+        for (int w = 1; w <= 12; ++w) {
+            const std::string bn = std::to_string(16 * w);
+            names[w][0][0] = "i8_umma_pair_256x" + bn + "_tokens";
+            names[w][0][1] = "i8_umma_pair_256x" + bn + "_channels";
+            for (int S = 1; S <= 8; ++S) names[w][S][0] = "i8_umma_128x" + bn + "_channels_split" + std::to_string(S);
+        }
+    });
+    if (c.variant == kI8Split) return names[c.bn / 16][c.split][0].c_str();
+    return names[c.bn / 16][0][c.variant == kI8PairChannels ? 1 : 0].c_str();
+}
+
 }  // namespace
 
-const char *launch_gemm_i8(const I8Params &p, int c_type, cudaStream_t stream, const DeviceInfo &)
+const char *launch_gemm_i8(const I8Params &q, int c_type, cudaStream_t stream, const DeviceInfo &dev)
 {
+    I8Params p = q;
+    // the pitch of a single row is never used
+    if (p.M == 1) p.lda = (p.K + 15) / 16 * 16;
+    if (p.N == 1) p.ldb = (p.K + 15) / 16 * 16;
+    I8Config cfg = t_tune;
+    t_tune = {kI8Auto, 0, 1};
+    if (tma_ok(p) && cfg.variant != kI8Mma) {
+        if (cfg.variant != kI8Auto && launch_i8_umma(p, c_type, cfg, stream)) return config_name(cfg);
+        cfg = choose_config(p, dev.sm_count);
+        if (launch_i8_umma(p, c_type, cfg, stream)) return config_name(cfg);
+    }
     switch (c_type) {
     case DGEMM_TYPE_F32: return launch_mma<float>(p, stream);
     case DGEMM_TYPE_F16: return launch_mma<__half>(p, stream);
     case DGEMM_TYPE_BF16: return launch_mma<__nv_bfloat16>(p, stream);
     default: return nullptr;
     }
+}
+
+int i8_tune_next(int variant, int bn, int split)
+{
+    const I8Config cfg{variant, bn, split};
+    if (variant != kI8Auto && variant != kI8Mma && !i8_umma_config_ok(cfg)) return DGEMM_ERR_INVALID_ARG;
+    t_tune = cfg;
+    return DGEMM_OK;
 }
 
 }  // namespace dgemm

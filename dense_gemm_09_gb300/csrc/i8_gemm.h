@@ -20,6 +20,20 @@ struct I8Params {
     int64_t ldc;
 };
 
+// Kernel of one call: variant, tile width and split (as dgemm_tune_i8_next
+// numbers them).
+enum { kI8Auto = 0, kI8Mma = 1, kI8PairTokens = 2, kI8PairChannels = 3, kI8Split = 4 };
+struct I8Config {
+    int variant;
+    int bn;     // tile columns: channels (kI8PairTokens) or tokens
+    int split;  // kI8Split: CTAs that share a tile along K
+};
+
+// The tensor-core kernels (i8_umma.cu), for operands TMA can describe: false,
+// and nothing launched, where the configuration cannot run.
+bool i8_umma_config_ok(const I8Config &cfg);
+bool launch_i8_umma(const I8Params &c, int c_type, const I8Config &cfg, cudaStream_t stream);
+
 __device__ __forceinline__ float i8_to_f32(float v) { return v; }
 __device__ __forceinline__ float i8_to_f32(__half v) { return __half2float(v); }
 __device__ __forceinline__ float i8_to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }

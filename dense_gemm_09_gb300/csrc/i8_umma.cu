@@ -1,0 +1,1039 @@
+// i8_umma.cu -- gemm_i8_tn on the tensor cores (tcgen05).
+//
+//   C[m, n] = scale_a[m] * scale_b[n] * sum_k A[m, k] B[n, k] + bias[n] + beta * C[m, n]
+//
+// The mathematics.  GB300's integer tensor rate is a small fraction of its
+// FP16 rate, but every int8 value is exact in FP16, a product of two is exact
+// in FP32, and sums of such products are exact while they stay below 2^24
+// (K <= 1024 always; real data far longer), so the product runs on
+// kind::f16 with FP32 accumulators in tensor memory and loses nothing to an
+// integer one.  Operands stay int8 in HBM and L2 and on their way into the
+// SM; they are widened to FP16 inside it.
+//
+// What bounds it.  Shared memory: each SM moves 128 bytes a clock through it,
+// and a K step of 64 costs a CTA of a pair (256 x 192 tiles) 14 KB written by
+// TMA, 14 KB read by the converters, 12 KB of widened columns written and
+// 12 KB read by the MMAs, against 384 clocks of MMA.  So the operand that
+// supplies the MMA's rows never goes back to shared memory: its converter
+// warps store it to tensor memory (tcgen05.st) and the MMAs take A from there.
+// That leaves 52 KB, 416 clocks; with both operands widened in shared memory
+// it would be 84 KB, 672 clocks.
+//
+// Roles (16 warps, one CTA an SM):
+//   warp 0       TMA producer: 128-byte rows (128 K values) of both operands
+//                into a ring of raw stages (128-byte swizzle);
+//   warps 8-11   row converters: warp w widens rows 32 (w mod 4) .. of the raw
+//                tile into its own TMEM lanes, 32 columns for each half (64 K
+//                values) of a raw stage;
+//   warps 12-15  column converters: the other operand, into a ring of four
+//                K-major FP16 stages in shared memory (128-byte swizzle);
+//   warp 2       waits for each converted half and hands it on through a named
+//                barrier (a probe of an mbarrier by the MMA thread between
+//                stages starves the tensor pipe);
+//   warp 1       MMA issuer: four tcgen05.mma of K = 16 a half;
+//   warps 4-7    epilogue: accumulator -> scale, bias, beta -> C.
+// A CTA pair (cta_group::2) shares one MMA: each CTA widens its own 128 rows
+// and half of the columns, and all of the pair's converters arrive on the
+// leader's barrier.
+//
+// "Rows" are A's tokens (kSwap = false) or B's channels (kSwap = true: the
+// accumulator holds C^T, for few tokens).
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+#include <mutex>
+#include <type_traits>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "bounded_wait.cuh"
+#include "dgemm.h"
+#include "i8_gemm.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+#define DGEMM_UNIT 8
+#include "checked.cuh"
+
+namespace dgemm {
+namespace {
+
+constexpr int kRows = 128;                      // accumulator rows of a CTA: TMEM lanes
+constexpr int kRowBytes = 128;                  // K values of a raw stage, one byte each
+constexpr int kRawRowsBytes = kRows * kRowBytes;
+constexpr int kHalfK = 64;                      // K values of a converted stage
+constexpr int kMaxBn = 192;                     // tile columns
+constexpr int kMaxSplitBn = 128;                // of a single CTA's tile
+constexpr int kMaxRaw = 8;                      // raw stages
+constexpr int kConv = 4;                        // converted stages
+constexpr int kAccCols = 192;                   // TMEM columns of an accumulator (two of them)
+constexpr int kConvCol = 2 * kAccCols;          // first TMEM column of the converted rows
+constexpr int kConvCols = kHalfK / 2;           // two FP16 values a column
+constexpr int kTmemCols = 512;
+static_assert(kConvCol + kConv * kConvCols <= kTmemCols, "accumulators and converted rows fit in TMEM");
+constexpr int kBoxBytes = 4096;                 // epilogue staging: 32 rows x 128 bytes
+constexpr int kEpiWarps = 4;
+constexpr int kThreads = 512;
+constexpr int kSmemLimit = 227 * 1024;
+
+struct Ctrl {
+    uint64_t raw_full[kMaxRaw];    // a raw stage has landed
+    uint64_t raw_empty[kMaxRaw];   // its eight converter warps have read it
+    uint64_t conv_full[kConv];     // leader: every converter warp of the pair has stored its part
+    uint64_t conv_empty[kConv];    // the MMAs have read this converted stage
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];         // leader: every epilogue warp of the pair has read the accumulator
+    uint64_t mma_done;
+    uint64_t never;                // test hook: a barrier nothing arrives at
+    WaitCtl wait;
+    uint32_t tmem_base;
+    alignas(16) float scale[kMaxBn];  // of the tile's columns (kSwap = false)
+    alignas(16) float bias[kMaxBn];
+};
+
+struct Params {
+    I8Params c;
+    int64_t rows, cols;            // of the accumulator matrix: (M, N), or (N, M) with kSwap
+    int64_t tiles_r, tiles_c;
+    int bn;                        // tile columns; a CTA of a pair converts half of them
+    int num_kb, tail_halves;       // raw K blocks; halves of the last one (1 or 2)
+    int raw_stages, raw_bytes;
+    int splitk;                    // CTAs of a cluster that share a tile (single CTAs)
+    int tma_store;
+    uint64_t wait_limit_ns;
+    int inject_stall;
+};
+
+// ---- PTX beyond ptx.cuh
+
+// As ptx::umma<0> / ptx::umma_pair<0> with A in tensor memory.
+template <int kCtas>
+__device__ __forceinline__ void umma_a_tmem(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate)
+{
+    if constexpr (kCtas == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
+// Arrive on the barrier at this offset in every CTA of the pair (or in this
+// CTA) when the MMAs issued so far by this thread complete.
+template <int kCtas>
+__device__ __forceinline__ void commit_all(uint32_t bar)
+{
+    if constexpr (kCtas == 2)
+        ptx::umma_commit_pair_multicast(bar, 0x3);
+    else
+        ptx::umma_commit(bar);
+}
+
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void named_barrier(uint32_t id, uint32_t threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// ---- int8 -> FP16
+
+// Four int8 values as two FP16 pairs, exactly: flipping the sign bit gives
+// v + 128 as an unsigned byte; under the exponent byte 0x64 it is the FP16
+// number 1024 + (v + 128), from which 1152 is subtracted without rounding.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x5140), b = __byte_perm(u, 0x64646464u, 0x7362);
+    const uint32_t bias = 0x64806480u;  // 1152, 1152
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&bias));
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&b), *reinterpret_cast<const __half2 *>(&bias));
+    lo = *reinterpret_cast<const uint32_t *>(&x);
+    hi = *reinterpret_cast<const uint32_t *>(&y);
+}
+
+// Sixteen int8 values (one chunk of a raw row) as eight FP16 pairs.
+__device__ __forceinline__ void widen16(const uint4 &c, uint32_t *out)
+{
+    widen4(c.x, out[0], out[1]);
+    widen4(c.y, out[2], out[3]);
+    widen4(c.z, out[4], out[5]);
+    widen4(c.w, out[6], out[7]);
+}
+
+// ---- schedule
+
+// The work of one CTA (pair): tiles t0, t0 + dt, ..., and of each the raw K
+// blocks [kb0, kb1) (all of them, or with split-K the r-th of S near-equal
+// ranges for rank r of the cluster).
+struct Sched {
+    int64_t t0, dt;
+    int kb0, kb1;
+};
+
+template <int kCtas>
+__device__ __forceinline__ Sched schedule(const Params &p)
+{
+    Sched s;
+    const int S = kCtas == 1 ? p.splitk : 1;
+    const int64_t per = kCtas == 2 ? 2 : S;  // CTAs that share a tile
+    s.t0 = blockIdx.x / per;
+    s.dt = gridDim.x / per;
+    s.kb0 = 0;
+    s.kb1 = p.num_kb;
+    if (S > 1) {
+        const int64_t r = ptx::cluster_ctarank();
+        s.kb0 = static_cast<int>(r * p.num_kb / S);
+        s.kb1 = static_cast<int>((r + 1) * p.num_kb / S);
+    }
+    return s;
+}
+
+// Tile t in groups of 8 tile columns: tiles in flight together share a few
+// bands of either operand.
+__device__ __forceinline__ void tile_origin(const Params &p, int64_t t, int tile_rows, int64_t &r0, int64_t &c0)
+{
+    constexpr int64_t kGroup = 8;
+    const int64_t per_group = kGroup * p.tiles_r;
+    const int64_t g = t / per_group, r = t % per_group;
+    const int64_t left = p.tiles_c - g * kGroup;
+    const int64_t gc = left < kGroup ? left : kGroup;
+    c0 = (g * kGroup + r % gc) * p.bn;
+    r0 = (r / gc) * tile_rows;
+}
+
+__device__ __forceinline__ int halves(const Params &p, int kb)
+{
+    return kb + 1 == p.num_kb ? p.tail_halves : 2;
+}
+
+// ---- roles
+
+template <int kCtas>
+__device__ __forceinline__ void run_producer(const CUtensorMap *tmap_r, const CUtensorMap *tmap_c, const Params &p,
+                                             uint32_t raw, Ctrl *ctrl, uint32_t rank, WaitCtl *wc)
+{
+    const Sched sc = schedule<kCtas>(p);
+    const int64_t tiles = p.tiles_r * p.tiles_c;
+    const int cols = p.bn / kCtas;  // columns this CTA converts
+    uint32_t stage = 0, phase = 0, issued = 0, issued_phase = 0;
+    bool ok = true;
+    for (int64_t t = sc.t0; ok && t < tiles; t += sc.dt) {
+        int64_t r0, c0;
+        tile_origin(p, t, kRows * kCtas, r0, c0);
+        for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
+            if (!wait_bounded(ptx::smem_addr(&ctrl->raw_empty[stage]), phase ^ 1u, wc)) {
+                ok = false;
+                break;
+            }
+            const uint32_t full = ptx::smem_addr(&ctrl->raw_full[stage]);
+            const uint32_t dst = raw + stage * static_cast<uint32_t>(p.raw_bytes);
+            ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(p.raw_bytes));
+            // the innermost coordinate is a multiple of 128 bytes
+            ptx::tma_load_2d(dst, tmap_r, full, kb * kRowBytes, static_cast<int32_t>(r0 + rank * kRows));
+            ptx::tma_load_2d(dst + kRawRowsBytes, tmap_c, full, kb * kRowBytes,
+                             static_cast<int32_t>(c0 + rank * cols));
+            issued |= 1u << stage;
+            issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+            if (++stage == static_cast<uint32_t>(p.raw_stages)) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    }
+    if (!ok) {
+        // do not leave while TMA may still be writing into this CTA's memory
+        for (int s = 0; s < p.raw_stages; ++s)
+            if ((issued >> s) & 1u) drain_wait(ptx::smem_addr(&ctrl->raw_full[s]), (issued_phase >> s) & 1u);
+    }
+}
+
+// A converter warp's arrival on a barrier of the pair's leader.
+template <int kCtas>
+__device__ __forceinline__ void arrive_leader(uint32_t bar)
+{
+    if constexpr (kCtas == 2)
+        ptx::mbar_arrive_cluster(ptx::mapa(bar, 0));
+    else
+        ptx::mbar_arrive(bar);
+}
+
+template <int kCtas>
+__device__ __forceinline__ bool wait_peer(uint32_t bar, uint32_t parity, WaitCtl *wc)
+{
+    return kCtas == 2 ? wait_bounded_cluster(bar, parity, wc) : wait_bounded(bar, parity, wc);
+}
+
+// Row converters: thread = row.  A raw row is 128 bytes, its 16-byte chunk j
+// stored at chunk position j ^ (row mod 8), so that the eight rows of a
+// wavefront read distinct banks.
+template <int kCtas>
+__device__ __forceinline__ void run_row_converter(const Params &p, uint32_t raw, Ctrl *ctrl, uint32_t tmem_base,
+                                                  int warp, int lane, WaitCtl *wc)
+{
+    const Sched sc = schedule<kCtas>(p);
+    const int64_t tiles = p.tiles_r * p.tiles_c;
+    const uint32_t quarter = static_cast<uint32_t>(warp & 3);
+    const uint32_t row = quarter * 32 + lane;
+    const uint32_t lanes = tmem_base + ((quarter * 32u) << 16) + kConvCol;
+    uint32_t stage = 0, phase = 0, cs = 0, cphase = 0;
+    for (int64_t t = sc.t0; t < tiles; t += sc.dt) {
+        for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
+            bool ok = wait_bounded(ptx::smem_addr(&ctrl->raw_full[stage]), phase, wc);
+            if (!__all_sync(0xFFFFFFFFu, ok)) return;
+            const uint32_t src = raw + stage * static_cast<uint32_t>(p.raw_bytes) + row * kRowBytes;
+            uint4 c[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) c[j] = ld_shared_v4(src + ((static_cast<uint32_t>(j) ^ (row & 7u)) << 4));
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctrl->raw_empty[stage]));
+            const int nh = halves(p, kb);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (h >= nh) break;
+                ok = wait_peer<kCtas>(ptx::smem_addr(&ctrl->conv_empty[cs]), cphase ^ 1u, wc);
+                if (!__all_sync(0xFFFFFFFFu, ok)) return;
+                uint32_t w[32];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) widen16(c[h * 4 + j], w + j * 8);
+                ptx::tc_fence_after();
+                __syncwarp();
+                ptx::tmem_st_32x32b_x32(lanes + cs * kConvCols, w);
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_leader<kCtas>(ptx::smem_addr(&ctrl->conv_full[cs]));
+                if (++cs == kConv) {
+                    cs = 0;
+                    cphase ^= 1u;
+                }
+            }
+            if (++stage == static_cast<uint32_t>(p.raw_stages)) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    }
+}
+
+// Column converters: the CTA's bn / kCtas columns x 64 K values of a half are
+// cols x 4 chunks of 16 bytes, dealt over 128 threads (consecutive threads
+// take consecutive columns of one chunk position).  A widened column is a
+// 128-byte K-major row under the 128-byte swizzle.
+template <int kCtas>
+__device__ __forceinline__ void run_col_converter(const Params &p, uint32_t raw, uint32_t conv, Ctrl *ctrl, int tid,
+                                                  int lane, WaitCtl *wc)
+{
+    constexpr int kTasks = (kCtas == 2 ? kMaxBn / 2 : kMaxSplitBn) * 4 / 128;  // chunks a thread takes at most
+    const Sched sc = schedule<kCtas>(p);
+    const int64_t tiles = p.tiles_r * p.tiles_c;
+    const int cols = p.bn / kCtas;
+    const uint32_t conv_bytes = static_cast<uint32_t>(cols) * 128u;
+    // offsets of this thread's chunks in a raw row tile (first half; the
+    // second is 64 bytes on, which flips bit 2 of the chunk position) and in a
+    // converted stage
+    uint32_t src_off[kTasks], dst_off[kTasks];
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kTasks; ++i) {
+        const int task = i * 128 + tid;
+        const uint32_t col = static_cast<uint32_t>(task % cols), j = static_cast<uint32_t>(task / cols);
+        if (task < cols * 4) ++n;
+        src_off[i] = kRawRowsBytes + col * kRowBytes + ((j ^ (col & 7u)) << 4);
+        dst_off[i] = col * 128u + (((2 * j) ^ (col & 7u)) << 4);  // the chunk's pair of 16-byte words: this, and this ^ 16
+    }
+    uint32_t stage = 0, phase = 0, cs = 0, cphase = 0;
+    for (int64_t t = sc.t0; t < tiles; t += sc.dt) {
+        for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
+            bool ok = wait_bounded(ptx::smem_addr(&ctrl->raw_full[stage]), phase, wc);
+            if (!__all_sync(0xFFFFFFFFu, ok)) return;
+            const uint32_t src = raw + stage * static_cast<uint32_t>(p.raw_bytes);
+            uint4 c[2][kTasks];
+            const int nh = halves(p, kb);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < kTasks; ++i)
+                    if (i < n && DGEMM_CHECK((src_off[i] ^ (h << 6)) + 16 <= static_cast<uint32_t>(p.raw_bytes)))
+                        c[h][i] = ld_shared_v4(src + (src_off[i] ^ (static_cast<uint32_t>(h) << 6)));
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctrl->raw_empty[stage]));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (h >= nh) break;
+                ok = wait_peer<kCtas>(ptx::smem_addr(&ctrl->conv_empty[cs]), cphase ^ 1u, wc);
+                if (!__all_sync(0xFFFFFFFFu, ok)) return;
+                const uint32_t dst = conv + cs * conv_bytes;
+#pragma unroll
+                for (int i = 0; i < kTasks; ++i) {
+                    if (i < n && DGEMM_CHECK((dst_off[i] | 16u) + 16 <= conv_bytes)) {
+                        uint32_t w[8];
+                        widen16(c[h][i], w);
+                        ptx::st_shared_v4(dst + dst_off[i], make_uint4(w[0], w[1], w[2], w[3]));
+                        ptx::st_shared_v4(dst + (dst_off[i] ^ 16u), make_uint4(w[4], w[5], w[6], w[7]));
+                    }
+                }
+                ptx::fence_proxy_async_smem();  // the MMAs read through the async proxy
+                __syncwarp();
+                if (lane == 0) arrive_leader<kCtas>(ptx::smem_addr(&ctrl->conv_full[cs]));
+                if (++cs == kConv) {
+                    cs = 0;
+                    cphase ^= 1u;
+                }
+            }
+            if (++stage == static_cast<uint32_t>(p.raw_stages)) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    }
+}
+
+constexpr uint32_t kHandoff = 64;  // warps 1 and 2 on named barriers 1 .. kConv
+constexpr uint32_t kEpiBarrier = 1 + kConv;
+
+// Waits for each converted half and meets the MMA warp on named barrier
+// 1 + stage, whose OR carries an abort both ways: both sides make the same
+// number of hand-offs whatever happens.
+template <int kCtas>
+__device__ __forceinline__ void run_waiter(const Params &p, Ctrl *ctrl, int lane, WaitCtl *wc)
+{
+    const Sched sc = schedule<kCtas>(p);
+    const int64_t tiles = p.tiles_r * p.tiles_c;
+    uint32_t cs = 0, cphase = 0;
+    bool abort = false;
+    for (int64_t t = sc.t0; t < tiles; t += sc.dt) {
+        for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
+            const int nh = halves(p, kb);
+            for (int h = 0; h < nh; ++h) {
+                if (!abort) {
+                    bool ok = true;
+                    if (lane == 0) ok = wait_peer<kCtas>(ptx::smem_addr(&ctrl->conv_full[cs]), cphase, wc);
+                    abort = __shfl_sync(0xFFFFFFFFu, ok ? 0 : 1, 0) != 0;
+                }
+                abort = ptx::bar_red_or(1 + cs, kHandoff, abort);
+                if (++cs == kConv) {
+                    cs = 0;
+                    cphase ^= 1u;
+                }
+            }
+        }
+    }
+}
+
+template <int kCtas>
+__device__ __forceinline__ void run_mma(const Params &p, uint32_t conv, Ctrl *ctrl, uint32_t tmem_base, int lane,
+                                        WaitCtl *wc)
+{
+    const Sched sc = schedule<kCtas>(p);
+    const int64_t tiles = p.tiles_r * p.tiles_c;
+    const uint32_t conv_bytes = static_cast<uint32_t>(p.bn / kCtas) * 128u;
+    // D f32, A and B f16 and K-major, N = bn, M = 128 rows a CTA
+    const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(p.bn >> 3) << 17) |
+                           (static_cast<uint32_t>(kRows * kCtas >> 4) << 24);
+    uint32_t cs = 0, acc = 0, acc_phase = 0;
+    // test hook: wait on a barrier nothing arrives at, so the wait runs out
+    bool ok = true;
+    if (lane == 0 && p.inject_stall) ok = wait_bounded(ptx::smem_addr(&ctrl->never), 0, wc);
+    bool abort = __shfl_sync(0xFFFFFFFFu, ok ? 0 : 1, 0) != 0;
+    for (int64_t t = sc.t0; t < tiles; t += sc.dt) {
+        if (!abort) {
+            ok = true;
+            if (lane == 0) ok = wait_peer<kCtas>(ptx::smem_addr(&ctrl->acc_empty[acc]), acc_phase ^ 1u, wc);
+            abort = __shfl_sync(0xFFFFFFFFu, ok ? 0 : 1, 0) != 0;
+        }
+        const uint32_t d = tmem_base + acc * kAccCols;
+        for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
+            const int nh = halves(p, kb);
+            for (int h = 0; h < nh; ++h) {
+                abort = ptx::bar_red_or(1 + cs, kHandoff, abort);
+                if (!abort) {
+                    ptx::tc_fence_after();
+                    if (lane == 0) {
+                        const uint32_t a = tmem_base + kConvCol + cs * kConvCols;
+                        const uint32_t b = conv + cs * conv_bytes;
+#pragma unroll
+                        for (int k = 0; k < kHalfK / 16; ++k)
+                            umma_a_tmem<kCtas>(d, a + k * 8, ptx::smem_desc(b + k * 32, 16, 1024, ptx::kSw128), idesc,
+                                               (kb != sc.kb0 || h != 0 || k != 0) ? 1u : 0u);
+                        commit_all<kCtas>(ptx::smem_addr(&ctrl->conv_empty[cs]));
+                    }
+                    __syncwarp();
+                }
+                if (++cs == kConv) cs = 0;
+            }
+        }
+        if (!abort && lane == 0) commit_all<kCtas>(ptx::smem_addr(&ctrl->acc_full[acc]));
+        __syncwarp();
+        acc ^= 1u;
+        if (acc == 0) acc_phase ^= 1u;
+    }
+    // every MMA this thread issued has finished before TMEM can be released
+    if (lane == 0) {
+        if constexpr (kCtas == 2)
+            ptx::umma_commit_pair_multicast(ptx::smem_addr(&ctrl->mma_done), 0x1);
+        else
+            ptx::umma_commit(ptx::smem_addr(&ctrl->mma_done));
+        drain_wait(ptx::smem_addr(&ctrl->mma_done), 0);
+    }
+    __syncwarp();
+}
+
+// ---- epilogues
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack_bits(T a, T b)
+{
+    static_assert(sizeof(T) == 2, "two 16-bit values");
+    return static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(&a)) |
+           static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(&b)) << 16;
+}
+
+// Rows = tokens: the warp's 32 rows x bn columns from (row0, c0), by boxes of
+// 128 bytes of columns staged in shared memory (128-byte swizzle) and stored
+// by TMA, or, where TMA cannot describe C, by rows of 32 columns.
+template <typename T>
+__device__ __forceinline__ void drain_tokens(const Params &p, const CUtensorMap *tmap_o, const Ctrl *ctrl,
+                                             uint32_t taddr, int64_t row0, int64_t c0, uint32_t box, int lane,
+                                             uint32_t &nbox)
+{
+    constexpr int kCols = 128 / sizeof(T);  // columns of a box
+    const int64_t row = row0 + lane;
+    const float sa = row < p.rows ? __ldg(p.c.scale_a + row) : 0.f;
+    const float beta = p.c.beta;
+    const uint32_t scale = ptx::smem_addr(ctrl->scale), bias = ptx::smem_addr(ctrl->bias);
+    T *crow = static_cast<T *>(p.c.C) + row * p.c.ldc;
+    if (!DGEMM_CHECK((taddr & 0xFFFFu) + static_cast<uint32_t>(p.bn) <= static_cast<uint32_t>(kConvCol))) return;
+    if (p.tma_store) {
+#pragma unroll 1
+        for (int b = 0; b < p.bn / kCols; ++b) {
+            const int64_t col0 = c0 + b * kCols;
+            const uint32_t buf = box + (nbox & 1u) * kBoxBytes;
+            uint32_t r[kCols];
+            __syncwarp();
+            ptx::tmem_ld_32x32b_x32(taddr + b * kCols, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+            if constexpr (kCols == 64)
+                ptx::tmem_ld_32x32b_x32(taddr + b * kCols + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+            ptx::tmem_ld_wait();
+            if (row0 >= p.rows || col0 >= p.cols) continue;  // warp-uniform: nothing of C here
+            if (lane == 0 && nbox >= 2) ptx::bulk_wait_read<1>();  // this box's last store has read it
+            __syncwarp();
+            const uint32_t dst = buf + static_cast<uint32_t>(lane) * 128u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                constexpr int kPer = 16 / sizeof(T);
+                float v[kPer];
+#pragma unroll
+                for (int e = 0; e < kPer; e += 4) {
+                    const uint32_t at = static_cast<uint32_t>(b * kCols + j * kPer + e) * 4u;
+                    const float4 s = ptx::ld_shared_v4f(scale + at), o = ptx::ld_shared_v4f(bias + at);
+                    const uint32_t *a = r + j * kPer + e;
+                    v[e] = fmaf(__uint_as_float(a[0]) * sa, s.x, o.x);
+                    v[e + 1] = fmaf(__uint_as_float(a[1]) * sa, s.y, o.y);
+                    v[e + 2] = fmaf(__uint_as_float(a[2]) * sa, s.z, o.z);
+                    v[e + 3] = fmaf(__uint_as_float(a[3]) * sa, s.w, o.w);
+                }
+                if (beta != 0.f && row < p.rows) {
+                    const int64_t col = col0 + j * kPer;
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e)
+                        if (col + e < p.cols) v[e] = fmaf(beta, i8_to_f32(crow[col + e]), v[e]);
+                }
+                uint4 q;
+                if constexpr (sizeof(T) == 2)
+                    q = make_uint4(pack_bits(i8_from_f32<T>(v[0]), i8_from_f32<T>(v[1])),
+                                   pack_bits(i8_from_f32<T>(v[2]), i8_from_f32<T>(v[3])),
+                                   pack_bits(i8_from_f32<T>(v[4]), i8_from_f32<T>(v[5])),
+                                   pack_bits(i8_from_f32<T>(v[6]), i8_from_f32<T>(v[7])));
+                else
+                    q = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                   __float_as_uint(v[3]));
+                ptx::st_shared_v4(dst + ((static_cast<uint32_t>(j) ^ (static_cast<uint32_t>(lane) & 7u)) << 4), q);
+            }
+            ptx::fence_proxy_async_smem();  // the TMA store reads through the async proxy
+            __syncwarp();
+            if (lane == 0 && DGEMM_CHECK(row0 >= 0 && col0 >= 0 && row0 < p.rows && col0 < p.cols)) {
+                ptx::tma_store_2d(tmap_o, buf, static_cast<int32_t>(col0), static_cast<int32_t>(row0));
+                ptx::bulk_commit();
+            }
+            ++nbox;
+        }
+        return;
+    }
+    // value e of row t sits at word e ^ t of the staged row, so both the
+    // row-wise writes and the column-wise reads hit 32 different banks
+#pragma unroll 1
+    for (int b = 0; b < p.bn / 32; ++b) {
+        uint32_t r[32];
+        __syncwarp();
+        ptx::tmem_ld_32x32b_x32(taddr + b * 32, r);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            const float v = fmaf(__uint_as_float(r[e]) * sa, ctrl->scale[b * 32 + e], ctrl->bias[b * 32 + e]);
+            ptx::st_shared_f32(box + (static_cast<uint32_t>(lane) * 32u + (static_cast<uint32_t>(e) ^ lane)) * 4u, v);
+        }
+        __syncwarp();
+        const int64_t col = c0 + b * 32 + lane;
+#pragma unroll 4
+        for (int i = 0; i < 32; ++i) {
+            if (row0 + i >= p.rows) break;  // warp-uniform
+            float v = ptx::ld_shared_f32(box + (static_cast<uint32_t>(i) * 32u + (lane ^ static_cast<uint32_t>(i))) * 4u);
+            if (col < p.cols && DGEMM_CHECK(row0 + i >= 0 && col >= 0)) {
+                T *dst = static_cast<T *>(p.c.C) + (row0 + i) * p.c.ldc + col;
+                if (beta != 0.f) v = fmaf(beta, i8_to_f32(*dst), v);
+                *dst = i8_from_f32<T>(v);
+            }
+        }
+        __syncwarp();  // the buffer is reused by the next chunk
+    }
+}
+
+// Rows = channels: v[j] is the sum for channel n (this lane's) and token
+// m0 + j; for each token the warp's lanes store consecutive channels.
+template <typename T, int kCount>
+__device__ __forceinline__ void store_channels(const Params &p, int64_t n, int64_t m0, int count, float sb, float bn,
+                                               const float (&v)[kCount])
+{
+#pragma unroll
+    for (int j = 0; j < kCount; ++j) {
+        const int64_t m = m0 + j;
+        if (j < count && m < p.cols && n < p.rows && DGEMM_CHECK(m >= 0 && n >= 0)) {
+            T *dst = static_cast<T *>(p.c.C) + m * p.c.ldc + n;
+            float x = fmaf(v[j] * __ldg(p.c.scale_a + m), sb, bn);
+            if (p.c.beta != 0.f) x = fmaf(p.c.beta, i8_to_f32(*dst), x);
+            *dst = i8_from_f32<T>(x);
+        }
+    }
+}
+
+template <int kCtas, bool kSwap, typename T>
+__device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap *tmap_o, Ctrl *ctrl,
+                                             uint32_t tmem_base, uint32_t box, uint32_t rank, int warp, int lane,
+                                             WaitCtl *wc)
+{
+    const Sched sc = schedule<kCtas>(p);
+    const int64_t tiles = p.tiles_r * p.tiles_c;
+    const uint32_t quarter = static_cast<uint32_t>(warp & 3);  // the TMEM lanes this warp may read
+    box += quarter * 2 * kBoxBytes;
+    uint32_t acc = 0, acc_phase = 0, nbox = 0;
+    for (int64_t t = sc.t0; t < tiles; t += sc.dt) {
+        int64_t r0, c0;
+        tile_origin(p, t, kRows * kCtas, r0, c0);
+        const int64_t row0 = r0 + rank * kRows + quarter * 32;
+        if constexpr (!kSwap) {
+            __syncwarp();
+            named_barrier(kEpiBarrier, 32 * kEpiWarps);  // the last tile's values have been read
+            for (int c = quarter * 32 + lane; c < p.bn; c += 32 * kEpiWarps) {
+                const bool in = c0 + c < p.cols && c < kMaxBn;
+                ctrl->scale[c] = in ? __ldg(p.c.scale_b + c0 + c) : 0.f;
+                ctrl->bias[c] = in && p.c.bias ? __ldg(p.c.bias + c0 + c) : 0.f;
+            }
+            __syncwarp();
+            named_barrier(kEpiBarrier, 32 * kEpiWarps);
+        }
+        bool ok = wait_peer<kCtas>(ptx::smem_addr(&ctrl->acc_full[acc]), acc_phase, wc);
+        // every epilogue warp leaves together, so none waits for another at
+        // the named barrier
+        __syncwarp();
+        ok = !ptx::bar_red_or(kEpiBarrier, 32 * kEpiWarps, !ok);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t taddr = tmem_base + ((quarter * 32u) << 16) + acc * kAccCols;
+        if constexpr (!kSwap) {
+            drain_tokens<T>(p, tmap_o, ctrl, taddr, row0, c0, box, lane, nbox);
+        } else {
+            const int64_t n = row0 + lane;
+            const float sb = n < p.rows ? __ldg(p.c.scale_b + n) : 0.f;
+            const float bias = p.c.bias && n < p.rows ? __ldg(p.c.bias + n) : 0.f;
+#pragma unroll 1
+            for (int b = 0; b < p.bn; b += 16) {
+                uint32_t r[2][8];
+                __syncwarp();
+                tmem_ld_32x32b_x8(taddr + b, r[0]);
+                tmem_ld_32x32b_x8(taddr + b + 8, r[1]);
+                ptx::tmem_ld_wait();
+                float v[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j >> 3][j & 7]);
+                store_channels<T>(p, n, c0 + b, 16, sb, bias, v);
+            }
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_leader<kCtas>(ptx::smem_addr(&ctrl->acc_empty[acc]));
+        acc ^= 1u;
+        if (acc == 0) acc_phase ^= 1u;
+    }
+    if (lane == 0) ptx::bulk_wait<0>();  // stores done before the CTA leaves
+}
+
+// ---- split-K (kSwap, single CTAs): the S CTAs of a cluster have each summed
+// a K range of one tile.  Groups of 8 columns are owned round-robin by the
+// ranks; each CTA pushes the groups it does not own into the owner's idle raw
+// ring, [sender slot][owned group][column quad][row] in 16-byte units, and
+// the owner adds the partials in rank order, so the sum does not depend on
+// timing.
+
+__device__ __forceinline__ uint32_t recv_offset(uint32_t groups, uint32_t slot, uint32_t idx, uint32_t S, int q,
+                                                int row)
+{
+    const uint32_t owned = (groups + S - 1) / S;
+    return (((slot * owned + idx) * 2u + static_cast<uint32_t>(q)) * kRows + static_cast<uint32_t>(row)) * 16u;
+}
+
+__device__ __forceinline__ void splitk_push(const Params &p, uint32_t tmem_base, uint32_t raw, int warp, int lane,
+                                            WaitCtl *wc)
+{
+    if (__any_sync(0xFFFFFFFFu, aborted(wc))) return;
+    ptx::tc_fence_after();
+    const uint32_t quarter = static_cast<uint32_t>(warp & 3);
+    const uint32_t S = static_cast<uint32_t>(p.splitk), rank = ptx::cluster_ctarank();
+    const uint32_t groups = static_cast<uint32_t>(p.bn) / 8;
+    const int row = static_cast<int>(quarter * 32 + lane);
+#pragma unroll 1
+    for (uint32_t g = 0; g < groups; ++g) {
+        const uint32_t owner = g % S;
+        if (owner == rank) continue;
+        uint32_t r[8];
+        __syncwarp();
+        tmem_ld_32x32b_x8(tmem_base + ((quarter * 32u) << 16) + g * 8, r);
+        ptx::tmem_ld_wait();
+        const uint32_t slot = rank < owner ? rank : rank - 1;
+        if (!DGEMM_CHECK(recv_offset(groups, slot, g / S, S, 1, row) + 16 <= static_cast<uint32_t>(p.raw_stages * p.raw_bytes))) continue;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            ptx::st_shared_cluster_v4(ptx::mapa(raw + recv_offset(groups, slot, g / S, S, q, row), owner),
+                                      make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                                                  __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3])));
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void splitk_reduce(const Params &p, uint32_t tmem_base, uint32_t raw, int warp, int lane,
+                                              WaitCtl *wc)
+{
+    if (__any_sync(0xFFFFFFFFu, aborted(wc))) return;
+    ptx::tc_fence_after();
+    const uint32_t quarter = static_cast<uint32_t>(warp & 3);
+    const uint32_t S = static_cast<uint32_t>(p.splitk), rank = ptx::cluster_ctarank();
+    const uint32_t groups = static_cast<uint32_t>(p.bn) / 8;
+    const int row = static_cast<int>(quarter * 32 + lane);
+    int64_t r0, c0;
+    tile_origin(p, blockIdx.x / S, kRows, r0, c0);
+    const int64_t n = r0 + row;
+    const float sb = n < p.rows ? __ldg(p.c.scale_b + n) : 0.f;
+    const float bias = p.c.bias && n < p.rows ? __ldg(p.c.bias + n) : 0.f;
+#pragma unroll 1
+    for (uint32_t g = rank; g < groups; g += S) {
+        uint32_t own[8];
+        __syncwarp();
+        tmem_ld_32x32b_x8(tmem_base + ((quarter * 32u) << 16) + g * 8, own);
+        ptx::tmem_ld_wait();
+        float v[8] = {};
+        for (uint32_t s = 0; s < S; ++s) {
+            if (s == rank) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] += __uint_as_float(own[j]);
+                continue;
+            }
+            const uint32_t slot = s < rank ? s : s - 1;
+            if (!DGEMM_CHECK(recv_offset(groups, slot, g / S, S, 1, row) + 16 <= static_cast<uint32_t>(p.raw_stages * p.raw_bytes))) continue;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const float4 f = ptx::ld_shared_v4f(raw + recv_offset(groups, slot, g / S, S, q, row));
+                v[4 * q] += f.x;
+                v[4 * q + 1] += f.y;
+                v[4 * q + 2] += f.z;
+                v[4 * q + 3] += f.w;
+            }
+        }
+        store_channels<T>(p, n, c0 + g * 8, 8, sb, bias, v);
+    }
+}
+
+__host__ __device__ constexpr uint32_t conv_ring_bytes(int bn, int ctas)
+{
+    return static_cast<uint32_t>(kConv * (bn / ctas) * 128);
+}
+
+template <int kCtas, bool kSwap, typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    i8_umma_kernel(const __grid_constant__ CUtensorMap tmap_r, const __grid_constant__ CUtensorMap tmap_c,
+                   const __grid_constant__ CUtensorMap tmap_o, const Params p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    // converted columns | epilogue boxes (kSwap: none) | raw ring | control
+    const uint32_t conv = ptx::smem_addr(smem);
+    const uint32_t box = conv + conv_ring_bytes(p.bn, kCtas);
+    const uint32_t raw = box + (kSwap ? 0 : kEpiWarps * 2 * kBoxBytes);
+    Ctrl *ctrl = reinterpret_cast<Ctrl *>(smem + (raw - conv) + p.raw_stages * p.raw_bytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = kCtas == 2 ? (ptx::cluster_ctarank() & 1u) : 0u;
+    const bool leader = rank == 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kMaxRaw; ++s) {
+            ptx::mbar_init(ptx::smem_addr(&ctrl->raw_full[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&ctrl->raw_empty[s]), 8);
+        }
+        for (int s = 0; s < kConv; ++s) {
+            ptx::mbar_init(ptx::smem_addr(&ctrl->conv_full[s]), 8 * kCtas);
+            ptx::mbar_init(ptx::smem_addr(&ctrl->conv_empty[s]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            ptx::mbar_init(ptx::smem_addr(&ctrl->acc_full[a]), 1);
+            ptx::mbar_init(ptx::smem_addr(&ctrl->acc_empty[a]), kEpiWarps * kCtas);
+        }
+        ptx::mbar_init(ptx::smem_addr(&ctrl->mma_done), 1);
+        ptx::mbar_init(ptx::smem_addr(&ctrl->never), 1);
+        ctrl->wait.abort = 0;
+        ctrl->wait.limit_ns = p.wait_limit_ns;
+        ptx::fence_mbarrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        ptx::prefetch_tmap(&tmap_r);
+        ptx::prefetch_tmap(&tmap_c);
+        if (p.tma_store) ptx::prefetch_tmap(&tmap_o);
+    }
+    if (warp == 1) {
+        if constexpr (kCtas == 2) {
+            ptx::tmem_alloc_pair(ptx::smem_addr(&ctrl->tmem_base), kTmemCols);
+            ptx::tmem_relinquish_pair();
+        } else {
+            ptx::tmem_alloc(ptx::smem_addr(&ctrl->tmem_base), kTmemCols);
+            ptx::tmem_relinquish();
+        }
+    }
+    ptx::tc_fence_before();
+    if constexpr (kCtas == 2)
+        ptx::cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
+    else
+        __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = ctrl->tmem_base;
+    WaitCtl *wc = &ctrl->wait;
+
+    if (warp == 0) {
+        if (lane == 0) run_producer<kCtas>(&tmap_r, &tmap_c, p, raw, ctrl, rank, wc);
+    } else if (warp == 1) {
+        if (leader) run_mma<kCtas>(p, conv, ctrl, tmem_base, lane, wc);
+    } else if (warp == 2) {
+        if (leader) run_waiter<kCtas>(p, ctrl, lane, wc);
+    } else if (warp >= 12) {
+        run_col_converter<kCtas>(p, raw, conv, ctrl, threadIdx.x - 12 * 32, lane, wc);
+    } else if (warp >= 8) {
+        run_row_converter<kCtas>(p, raw, ctrl, tmem_base, warp, lane, wc);
+    } else if (warp >= 4) {
+        if (kCtas == 1 && p.splitk > 1)
+            wait_bounded(ptx::smem_addr(&ctrl->acc_full[0]), 0, wc);  // a time-out raises the abort flag
+        else
+            run_epilogue<kCtas, kSwap, T>(p, &tmap_o, ctrl, tmem_base, box, rank, warp, lane, wc);
+    }
+
+    if constexpr (kCtas == 1 && kSwap) {
+        if (p.splitk > 1) {  // uniform over the cluster
+            __syncwarp();
+            ptx::tc_fence_before();
+            ptx::cluster_sync();  // every CTA's sums are complete: the raw rings are idle
+            if (warp >= 4 && warp < 8) splitk_push(p, tmem_base, raw, warp, lane, wc);
+            __syncwarp();
+            ptx::tc_fence_before();
+            ptx::cluster_sync();  // every partial has landed in its owner
+            if (warp >= 4 && warp < 8) splitk_reduce<T>(p, tmem_base, raw, warp, lane, wc);
+        }
+    }
+
+    __syncwarp();  // the barrier below is warp-aligned: reconverge the single-lane roles
+    ptx::tc_fence_before();
+    if constexpr (kCtas == 2)
+        ptx::cluster_sync();  // no CTA leaves while the other may still signal or read it
+    else
+        __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        if constexpr (kCtas == 2)
+            ptx::tmem_dealloc_pair(tmem_base, kTmemCols);
+        else
+            ptx::tmem_dealloc(tmem_base, kTmemCols);
+    }
+}
+
+// ---- host side
+
+// Dynamic shared memory of a launch, and its raw ring: as many stages as fit.
+int set_ring(Params &p, int ctas, bool swap)
+{
+    const int fixed = static_cast<int>(conv_ring_bytes(p.bn, ctas)) + (swap ? 0 : kEpiWarps * 2 * kBoxBytes) + 1024 +
+                      static_cast<int>(sizeof(Ctrl));
+    p.raw_bytes = kRawRowsBytes + p.bn / ctas * kRowBytes;
+    p.raw_stages = std::min(kMaxRaw, (kSmemLimit - fixed) / p.raw_bytes);
+    return fixed + p.raw_stages * p.raw_bytes;
+}
+
+// CTAs (kCtas == 1) or clusters of `cluster` CTAs of the kernel that can be
+// resident at once on the current device, cached; 0 if it cannot run.
+template <int kCtas, bool kSwap, typename T>
+int capacity(int cluster)
+{
+    constexpr int kMaxDevices = 64;
+    static int cached[kMaxDevices][9];
+    static std::once_flag once[kMaxDevices];
+    int dev = 0;
+    if (cluster < 1 || cluster > 8 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+    std::call_once(once[dev], [dev] {
+        auto kernel = i8_umma_kernel<kCtas, kSwap, T>;
+        int sms = 0;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) == cudaSuccess &&
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) {
+            cached[dev][1] = sms;
+            for (int s = 2; s <= (kCtas == 2 ? 2 : 8); ++s) {
+                cudaLaunchConfig_t cfg = {};
+                cudaLaunchAttribute attr[1];
+                attr[0].id = cudaLaunchAttributeClusterDimension;
+                attr[0].val.clusterDim.x = static_cast<unsigned>(s);
+                attr[0].val.clusterDim.y = 1;
+                attr[0].val.clusterDim.z = 1;
+                cfg.gridDim = dim3(static_cast<unsigned>(sms - sms % s));
+                cfg.blockDim = dim3(kThreads);
+                cfg.dynamicSmemBytes = kSmemLimit;
+                cfg.attrs = attr;
+                cfg.numAttrs = 1;
+                int n = 0;
+                if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
+                cached[dev][s] = n;
+            }
+        }
+        cudaGetLastError();  // a failed query leaves no sticky error behind
+    });
+    return cached[dev][cluster];
+}
+
+template <int kCtas, bool kSwap, typename T>
+bool launch(const I8Params &c, int bn, int splitk, cudaStream_t stream)
+{
+    Params p{};
+    p.c = c;
+    p.rows = kSwap ? c.N : c.M;
+    p.cols = kSwap ? c.M : c.N;
+    p.bn = bn;
+    p.tiles_r = (p.rows + kRows * kCtas - 1) / (kRows * kCtas);
+    p.tiles_c = (p.cols + bn - 1) / bn;
+    p.num_kb = static_cast<int>((c.K + kRowBytes - 1) / kRowBytes);
+    p.tail_halves = c.K % kRowBytes > 0 && c.K % kRowBytes <= kHalfK ? 1 : 2;
+    p.splitk = std::min(splitk, p.num_kb);
+    const int smem = set_ring(p, kCtas, kSwap);
+    const int cluster = kCtas == 2 ? 2 : p.splitk;
+    const int fit = capacity<kCtas, kSwap, T>(cluster);
+    const int64_t tiles = p.tiles_r * p.tiles_c;
+    if (fit < 1 || p.raw_stages < 2 || (p.splitk > 1 && tiles > fit)) return false;
+    CUtensorMap mr{}, mc{}, mo{};
+    const void *pr = kSwap ? c.B : c.A, *pc = kSwap ? c.A : c.B;
+    const int64_t ldr = kSwap ? c.ldb : c.lda, ldc = kSwap ? c.lda : c.ldb;
+    if (!encode_tiled_2d(&mr, CU_TENSOR_MAP_DATA_TYPE_UINT8, pr, c.K, p.rows, ldr, kRowBytes, kRows,
+                         CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tiled_2d(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, pc, c.K, p.cols, ldc, kRowBytes, bn / kCtas,
+                         CU_TENSOR_MAP_SWIZZLE_128B))
+        return false;
+    if constexpr (!kSwap) {
+        constexpr int kCols = 128 / sizeof(T);
+        const CUtensorMapDataType dt = std::is_same<T, float>::value    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                       : std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        p.tma_store = bn % kCols == 0 && aligned16(c.C) && c.ldc * sizeof(T) % 16 == 0 &&
+                      encode_tiled_2d(&mo, dt, c.C, c.N, c.M, c.ldc * sizeof(T), kCols, 32,
+                                      CU_TENSOR_MAP_SWIZZLE_128B);
+    }
+    const uint64_t stall = take_injected_stall();
+    p.inject_stall = stall ? 1 : 0;
+    p.wait_limit_ns = stall ? stall : kWaitLimitNs;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(cluster * std::min<int64_t>(tiles, fit)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, i8_umma_kernel<kCtas, kSwap, T>, mr, mc, mo, p) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return true;
+}
+
+template <typename T>
+bool launch_typed(const I8Params &c, const I8Config &cfg, cudaStream_t stream)
+{
+    switch (cfg.variant) {
+    case kI8PairTokens: return launch<2, false, T>(c, cfg.bn, 1, stream);
+    case kI8PairChannels: return launch<2, true, T>(c, cfg.bn, 1, stream);
+    case kI8Split: return launch<1, true, T>(c, cfg.bn, cfg.split, stream);
+    default: return false;
+    }
+}
+
+}  // namespace
+
+bool i8_umma_config_ok(const I8Config &cfg)
+{
+    switch (cfg.variant) {
+    case kI8PairTokens: return cfg.bn == 64 || cfg.bn == 128 || cfg.bn == 192;
+    case kI8PairChannels: return cfg.bn >= 32 && cfg.bn <= kMaxBn && cfg.bn % 32 == 0;
+    case kI8Split: return cfg.bn >= 16 && cfg.bn <= kMaxSplitBn && cfg.bn % 16 == 0 && cfg.split >= 1 && cfg.split <= 8;
+    default: return false;
+    }
+}
+
+bool launch_i8_umma(const I8Params &c, int c_type, const I8Config &cfg, cudaStream_t stream)
+{
+    if (!i8_umma_config_ok(cfg)) return false;
+    switch (c_type) {
+    case DGEMM_TYPE_F32: return launch_typed<float>(c, cfg, stream);
+    case DGEMM_TYPE_F16: return launch_typed<__half>(c, cfg, stream);
+    case DGEMM_TYPE_BF16: return launch_typed<__nv_bfloat16>(c, cfg, stream);
+    default: return false;
+    }
+}
+
+int i8_read_status(int clear)
+{
+    return read_wait_status(clear);
+}
+
+}  // namespace dgemm
+
+DGEMM_DEFINE_CHECK_READER(check_status_i8_umma)

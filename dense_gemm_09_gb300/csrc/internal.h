@@ -73,6 +73,7 @@ int check_status_scale(int clear, int *site);
 int check_status_repack(int clear, int *site);
 int check_status_i8_rows(int clear, int *site);
 int check_status_i8_gemm(int clear, int *site);
+int check_status_i8_umma(int clear, int *site);
 
 // Rows taken off M for the C-store checks of the next TMA-fed SIMT launch
 // on this host thread (dgemm_test_shrink_bounds); taking it clears it.
@@ -113,6 +114,12 @@ const char *launch_dequantize_i8(int64_t rows, int64_t cols, const int8_t *q, in
 // The 8-bit product (i8_gemm.cu); c_type is a dgemm_type.
 struct I8Params;
 const char *launch_gemm_i8(const I8Params &p, int c_type, cudaStream_t stream, const DeviceInfo &dev);
+
+// Tuning hook behind dgemm_tune_i8_next.
+int i8_tune_next(int variant, int bn, int split);
+
+// Device status word of the 8-bit tensor-core kernels.
+int i8_read_status(int clear);
 
 // Test hook behind dgemm_test_inject_stall.
 void umma_inject_stall(uint64_t wait_limit_ns);

@@ -52,6 +52,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "bounded_wait.cuh"
 #include "dgemm.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -60,9 +61,6 @@
 #include "checked.cuh"
 
 namespace dgemm {
-
-__device__ int g_umma_status;
-
 namespace {
 
 constexpr int BM = 128;
@@ -79,8 +77,6 @@ constexpr int STAGE_BYTES = A_TILE_BYTES + B_TILE_BYTES;
 constexpr int MAX_STAGES = 8;
 constexpr int TMEM_COLS = 2 * BN;                  // two f32 accumulators
 constexpr int kGroupN = 8;                         // tile-order group width
-constexpr uint64_t kWaitLimitNs = 4000000000ull;   // 4 s, default wait bound
-constexpr uint64_t kDrainLimitNs = 1000000000ull;  // 1 s
 
 // Operand kinds.  TN: B stored N x K (K-major); NN: B stored K x N
 // (N-major).  TF32 reads FP32 storage; all kinds accumulate in FP32.
@@ -157,13 +153,6 @@ __device__ __forceinline__ uint16_t round1(float v)
         return *reinterpret_cast<const uint16_t *>(&h);
     }
 }
-
-// Per-CTA wait control: the abort flag every role polls and the wait limit.
-struct WaitCtl {
-    int abort;
-    int pad;
-    uint64_t limit_ns;
-};
 
 struct Ctrl {
     uint64_t full[MAX_STAGES];
@@ -272,62 +261,6 @@ __device__ __forceinline__ Sched schedule(const Params &p)
         s.kb1 = p.num_kb;
     }
     return s;
-}
-
-__device__ __forceinline__ bool aborted(const WaitCtl *wc)
-{
-    return *reinterpret_cast<const volatile int *>(&wc->abort) != 0;
-}
-
-__device__ __forceinline__ void raise_abort(WaitCtl *wc)
-{
-    if (atomicExch(&g_umma_status, DGEMM_ERR_TIMEOUT) == 0) __threadfence();
-    *reinterpret_cast<volatile int *>(&wc->abort) = 1;
-}
-
-// Bounded wait for the phase of the given parity; false on time-out or when
-// another role raised the abort flag.
-__device__ __noinline__ bool wait_bounded(uint32_t bar, uint32_t parity, WaitCtl *wc)
-{
-    if (ptx::mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = ptx::globaltimer_ns(), limit = wc->limit_ns;
-    for (;;) {
-#pragma unroll 1
-        for (int i = 0; i < 32; ++i)
-            if (ptx::mbar_try_wait(bar, parity)) return true;
-        if (aborted(wc)) return false;
-        if (ptx::globaltimer_ns() - t0 > limit) {
-            raise_abort(wc);
-            return false;
-        }
-    }
-}
-
-// Same, with cluster-scope acquire (barriers that the other CTA of a pair
-// arrives on, directly or through a multicast commit).
-__device__ __noinline__ bool wait_bounded_cluster(uint32_t bar, uint32_t parity, WaitCtl *wc)
-{
-    if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
-    const uint64_t t0 = ptx::globaltimer_ns(), limit = wc->limit_ns;
-    for (;;) {
-#pragma unroll 1
-        for (int i = 0; i < 32; ++i)
-            if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
-        if (aborted(wc)) return false;
-        if (ptx::globaltimer_ns() - t0 > limit) {
-            raise_abort(wc);
-            return false;
-        }
-    }
-}
-
-// Bounded wait used on the way out, after an abort: ignores the abort flag.
-__device__ __noinline__ bool drain_wait(uint32_t bar, uint32_t parity)
-{
-    const uint64_t t0 = ptx::globaltimer_ns();
-    while (!ptx::mbar_try_wait(bar, parity))
-        if (ptx::globaltimer_ns() - t0 > kDrainLimitNs) return false;
-    return true;
 }
 
 template <int kKind, int kKpb>
@@ -2901,14 +2834,7 @@ bool encode_tiled_2d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, u
 
 int umma_read_status(int clear)
 {
-    int v = 0;
-    if (cudaMemcpyFromSymbol(&v, g_umma_status, sizeof(int)) != cudaSuccess) return DGEMM_ERR_LAUNCH;
-    if (clear) {
-        const int zero = 0;
-        if (cudaMemcpyToSymbol(g_umma_status, &zero, sizeof(int)) != cudaSuccess)
-            return DGEMM_ERR_LAUNCH;
-    }
-    return v;
+    return read_wait_status(clear);
 }
 
 }  // namespace dgemm

@@ -369,8 +369,8 @@ int dgemm_device_status(int clear);
  * dgemm_check_site -- the site of the first failed check since the last
  * clear of the device status: (translation unit x 100000 + source line) of
  * the library's sources, units 1 sgemm_simt.cu, 2 sgemm_tma.cu,
- * 3 umma_gemm.cu, 4 scale_c.cu, 5 repack.cu, 6 i8_rows.cu, 7 i8_gemm.cu; 0 if
- * none failed, and always 0 in libdgemm.so.  Synchronises the device.  Source: none on the pages.
+ * 3 umma_gemm.cu, 4 scale_c.cu, 5 repack.cu, 6 i8_rows.cu, 7 i8_gemm.cu,
+ * 8 i8_umma.cu; 0 if none failed, and always 0 in libdgemm.so.  Synchronises the device.  Source: none on the pages.
  */
 int dgemm_check_site(void);
 
@@ -479,6 +479,21 @@ int dgemm_test_choose_config(int kind, int64_t M, int64_t N, int64_t K, int sm_c
  * Autotuning" (searching tile parameters per problem instead of fixing one).
  */
 int dgemm_tune_next(int variant, int bn, int split);
+
+/*
+ * dgemm_tune_i8_next -- TUNING HOOK: as dgemm_tune_next, for the next
+ * gemm_i8_tn call made by the calling host thread.
+ *   variant 0: automatic (the default);
+ *           1: the mma.sync kernel for operands of any alignment;
+ *           2: CTA pair, 256 tokens x bn channels (bn 64, 128 or 192);
+ *           3: CTA pair, 256 channels x bn tokens (bn 32..192 in steps of 32);
+ *           4: one CTA per 128 channels x bn tokens (bn 16..128 in steps of
+ *              16), `split` (1..8) CTAs of a cluster sharing it along K.
+ * Returns DGEMM_ERR_INVALID_ARG (and records nothing) for values outside
+ * these ranges, else DGEMM_OK.  A configuration the next call cannot take is
+ * ignored; dgemm_last_kernel() names what ran.  Source: as dgemm_tune_next.
+ */
+int dgemm_tune_i8_next(int variant, int bn, int split);
 
 /*
  * dgemm_last_kernel -- name of the kernel variant the last successful call

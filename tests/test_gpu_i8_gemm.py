@@ -50,6 +50,49 @@ def _check(M, N, K, ty="f32", bias=False, beta=0.0, pad=(0, 0), offset=(0, 0), c
     return name
 
 
+# every kernel and tile width on request: (variant, bn, split), name
+KERNELS = [((1, 0, 1), "i8_mma_"), ((2, 64, 1), "pair_256x64_tokens"), ((2, 128, 1), "pair_256x128_tokens"),
+           ((2, 192, 1), "pair_256x192_tokens"), ((3, 32, 1), "pair_256x32_channels"),
+           ((3, 96, 1), "pair_256x96_channels"), ((3, 128, 1), "pair_256x128_channels"),
+           ((3, 192, 1), "pair_256x192_channels"), ((4, 16, 1), "128x16_channels_split1"),
+           ((4, 48, 3), "128x48_channels_split3"), ((4, 64, 8), "128x64_channels_split8"),
+           ((4, 112, 5), "128x112_channels_split5"), ((4, 128, 2), "128x128_channels_split2")]
+
+
+@pytest.mark.parametrize("tune,name", KERNELS, ids=[n for _, n in KERNELS])
+def test_every_kernel(tune, name):
+    import dense_gemm_09_gb300 as dg
+
+    def call(*a, **k):
+        dg.tune_i8_next(*tune)
+        return dg.gemm_i8_tn(*a, **k)
+
+    # one K block (whole, half, a tail in either half), many; one tile, ragged
+    # edges both ways, several tiles
+    for M, N, K in ((128, 128, 128), (1, 1, 16), (16, 128, 64), (30, 500, 48), (130, 129, 80), (256, 192, 1024),
+                    (100, 300, 2064), (257, 513, 1000), (300, 700, 4096)):
+        for ty, bias, beta in (("f32", True, 0.5), ("bf16", False, 0.0)):
+            got = _check(M, N, K, ty, bias, beta, pad=((-K) % 16, (-K) % 16), call=call)
+            split = tune[2]
+            if tune[0] == 4 and (-(-M // tune[1])) * (-(-N // 128)) * split > 128:
+                continue  # more clusters than fit at once: the automatic choice
+            assert name in got, got
+    assert dg.device_status() == dg.OK
+
+
+@pytest.mark.parametrize("tune,name", KERNELS[1:], ids=[n for _, n in KERNELS[1:]])
+@pytest.mark.parametrize("c_pad,c_offset", [(0, 0), (1, 0), (8, 3)])
+def test_every_kernel_stores_any_pitch(tune, name, c_pad, c_offset):
+    import dense_gemm_09_gb300 as dg
+
+    def call(*a, **k):
+        dg.tune_i8_next(*tune)
+        return dg.gemm_i8_tn(*a, **k)
+
+    for ty in ref.TYPES:
+        _check(70, 333, 256, ty, True, 0.5, c_pad=c_pad, c_offset=c_offset, call=call)
+
+
 SMALL = [(1, 1, 1), (1, 1, 64), (2, 3, 5), (7, 9, 33), (16, 16, 16), (17, 65, 129), (64, 64, 64), (65, 63, 127),
          (128, 128, 128), (129, 127, 255), (31, 300, 1024), (200, 33, 1000)]
 
