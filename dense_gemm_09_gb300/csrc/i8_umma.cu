@@ -147,6 +147,25 @@ __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[
                  : "memory");
 }
 
+// Arrive on an mbarrier of another CTA of the cluster with release at CTA
+// scope: what it publishes is this CTA's tensor memory and, fenced to the async
+// proxy, its shared memory, which this SM's own half of the pair's MMA reads;
+// no thread of the other CTA does.  (A release at cluster scope waits ~650
+// clocks for every earlier store of the thread to be acknowledged.)
+__device__ __forceinline__ void arrive_remote(uint32_t cluster_addr)
+{
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// True in one thread of the (converged) warp.  The compiler keeps the operands
+// of tcgen05 instructions under this predicate in uniform registers.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr)
 {
     uint4 v;
@@ -279,7 +298,7 @@ template <int kCtas>
 __device__ __forceinline__ void arrive_leader(uint32_t bar)
 {
     if constexpr (kCtas == 2)
-        ptx::mbar_arrive_cluster(ptx::mapa(bar, 0));
+        arrive_remote(ptx::mapa(bar, 0));
     else
         ptx::mbar_arrive(bar);
 }
@@ -457,45 +476,51 @@ __device__ __forceinline__ void run_mma(const Params &p, uint32_t conv, Ctrl *ct
     // D f32, A and B f16 and K-major, N = bn, M = 128 rows a CTA
     const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(p.bn >> 3) << 17) |
                            (static_cast<uint32_t>(kRows * kCtas >> 4) << 24);
+    // one column of the ring's descriptors: a stage on is conv_bytes / 16, an
+    // MMA's K step 2, in their address field
+    const uint64_t b_desc = ptx::smem_desc(conv, 16, 1024, ptx::kSw128);
+    tmem_base = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);  // a uniform value for the compiler
     uint32_t cs = 0, acc = 0, acc_phase = 0;
     // test hook: wait on a barrier nothing arrives at, so the wait runs out
     bool ok = true;
     if (lane == 0 && p.inject_stall) ok = wait_bounded(ptx::smem_addr(&ctrl->never), 0, wc);
-    bool abort = __shfl_sync(0xFFFFFFFFu, ok ? 0 : 1, 0) != 0;
+    bool abort = __any_sync(0xFFFFFFFFu, !ok);
     for (int64_t t = sc.t0; t < tiles; t += sc.dt) {
         if (!abort) {
             ok = true;
             if (lane == 0) ok = wait_peer<kCtas>(ptx::smem_addr(&ctrl->acc_empty[acc]), acc_phase ^ 1u, wc);
-            abort = __shfl_sync(0xFFFFFFFFu, ok ? 0 : 1, 0) != 0;
+            abort = __any_sync(0xFFFFFFFFu, !ok);
         }
         const uint32_t d = tmem_base + acc * kAccCols;
+        uint32_t accumulate = 0;
         for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
             const int nh = halves(p, kb);
             for (int h = 0; h < nh; ++h) {
-                abort = ptx::bar_red_or(1 + cs, kHandoff, abort);
+                abort = __any_sync(0xFFFFFFFFu, ptx::bar_red_or(1 + cs, kHandoff, abort));
                 if (!abort) {
                     ptx::tc_fence_after();
-                    if (lane == 0) {
+                    if (elect_one()) {
                         const uint32_t a = tmem_base + kConvCol + cs * kConvCols;
-                        const uint32_t b = conv + cs * conv_bytes;
+                        const uint64_t b = b_desc + cs * (conv_bytes >> 4);
 #pragma unroll
                         for (int k = 0; k < kHalfK / 16; ++k)
-                            umma_a_tmem<kCtas>(d, a + k * 8, ptx::smem_desc(b + k * 32, 16, 1024, ptx::kSw128), idesc,
-                                               (kb != sc.kb0 || h != 0 || k != 0) ? 1u : 0u);
+                            umma_a_tmem<kCtas>(d, a + k * 8, b + k * 2, idesc, k == 0 ? accumulate : 1u);
                         commit_all<kCtas>(ptx::smem_addr(&ctrl->conv_empty[cs]));
                     }
                     __syncwarp();
                 }
+                accumulate = 1;
                 if (++cs == kConv) cs = 0;
             }
         }
-        if (!abort && lane == 0) commit_all<kCtas>(ptx::smem_addr(&ctrl->acc_full[acc]));
+        if (!abort && elect_one()) commit_all<kCtas>(ptx::smem_addr(&ctrl->acc_full[acc]));
         __syncwarp();
         acc ^= 1u;
         if (acc == 0) acc_phase ^= 1u;
     }
     // every MMA this thread issued has finished before TMEM can be released
-    if (lane == 0) {
+    // (the elected thread is the same one each time)
+    if (elect_one()) {
         if constexpr (kCtas == 2)
             ptx::umma_commit_pair_multicast(ptx::smem_addr(&ctrl->mma_done), 0x1);
         else
