@@ -44,6 +44,9 @@ __device__ __forceinline__ void raise_abort(WaitCtl *wc)
 __device__ __noinline__ bool wait_bounded(uint32_t bar, uint32_t parity, WaitCtl *wc)
 {
     if (ptx::mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i)  // most waits end here, before the first look at the clock
+        if (ptx::mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = ptx::globaltimer_ns(), limit = wc->limit_ns;
     for (;;) {
 #pragma unroll 1
@@ -62,6 +65,9 @@ __device__ __noinline__ bool wait_bounded(uint32_t bar, uint32_t parity, WaitCtl
 __device__ __noinline__ bool wait_bounded_cluster(uint32_t bar, uint32_t parity, WaitCtl *wc)
 {
     if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i)  // most waits end here, before the first look at the clock
+        if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
     const uint64_t t0 = ptx::globaltimer_ns(), limit = wc->limit_ns;
     for (;;) {
 #pragma unroll 1

@@ -19,19 +19,24 @@
 // That leaves 52 KB, 416 clocks; with both operands widened in shared memory
 // it would be 84 KB, 672 clocks.
 //
-// Roles (16 warps, one CTA an SM):
+// Roles (24 warps, one CTA an SM):
 //   warp 0       TMA producer: 128-byte rows (128 K values) of both operands
 //                into a ring of raw stages (128-byte swizzle);
-//   warps 8-11   row converters: warp w widens rows 32 (w mod 4) .. of the raw
-//                tile into its own TMEM lanes, 32 columns for each half (64 K
-//                values) of a raw stage;
-//   warps 12-15  column converters: the other operand, into a ring of four
-//                K-major FP16 stages in shared memory (128-byte swizzle);
-//   warp 2       waits for each converted half and hands it on through a named
+//   warps 8-15   row converters, four for either half (64 K values) of a raw
+//                stage: warp w widens rows 32 (w mod 4) .. into its own TMEM
+//                lanes, 32 columns a half;
+//   warps 16-23  column converters, four for either half: the other operand,
+//                K-major FP16 in shared memory (128-byte swizzle);
+//   warp 2       waits for each converted stage and hands it on through a named
 //                barrier (a probe of an mbarrier by the MMA thread between
 //                stages starves the tensor pipe);
-//   warp 1       MMA issuer: four tcgen05.mma of K = 16 a half;
+//   warp 1       MMA issuer: four tcgen05.mma of K = 16 a half, each half
+//                released by a commit of its own;
 //   warps 4-7    epilogue: accumulator -> scale, bias, beta -> C.
+// There are two converted stages (four halves).  A converter reads and widens
+// its part of a stage into registers before it waits for the half's MMAs of
+// two stages ago, so that only the store, the hand-off and the commit lie
+// between the release of a half and its next use.
 // A CTA pair (cta_group::2) shares one MMA: each CTA widens its own 128 rows
 // and half of the columns, and all of the pair's converters arrive on the
 // leader's barrier.
@@ -62,26 +67,26 @@ namespace {
 constexpr int kRows = 128;                      // accumulator rows of a CTA: TMEM lanes
 constexpr int kRowBytes = 128;                  // K values of a raw stage, one byte each
 constexpr int kRawRowsBytes = kRows * kRowBytes;
-constexpr int kHalfK = 64;                      // K values of a converted stage
+constexpr int kHalfK = 64;                      // K values of a converted half
 constexpr int kMaxBn = 192;                     // tile columns
 constexpr int kMaxSplitBn = 128;                // of a single CTA's tile
 constexpr int kMaxRaw = 8;                      // raw stages
-constexpr int kConv = 4;                        // converted stages
+constexpr int kConv = 2;                        // converted stages, of two halves each
 constexpr int kAccCols = 192;                   // TMEM columns of an accumulator (two of them)
 constexpr int kConvCol = 2 * kAccCols;          // first TMEM column of the converted rows
 constexpr int kConvCols = kHalfK / 2;           // two FP16 values a column
 constexpr int kTmemCols = 512;
-static_assert(kConvCol + kConv * kConvCols <= kTmemCols, "accumulators and converted rows fit in TMEM");
+static_assert(kConvCol + 2 * kConv * kConvCols <= kTmemCols, "accumulators and converted rows fit in TMEM");
 constexpr int kBoxBytes = 4096;                 // epilogue staging: 32 rows x 128 bytes
 constexpr int kEpiWarps = 4;
-constexpr int kThreads = 512;
+constexpr int kThreads = 768;
 constexpr int kSmemLimit = 227 * 1024;
 
 struct Ctrl {
     uint64_t raw_full[kMaxRaw];    // a raw stage has landed
-    uint64_t raw_empty[kMaxRaw];   // its eight converter warps have read it
+    uint64_t raw_empty[kMaxRaw];   // its 16 converter warps have read it
     uint64_t conv_full[kConv];     // leader: every converter warp of the pair has stored its part
-    uint64_t conv_empty[kConv];    // the MMAs have read this converted stage
+    uint64_t conv_empty[2 * kConv];  // the MMAs have read this converted half
     uint64_t acc_full[2];
     uint64_t acc_empty[2];         // leader: every epilogue warp of the pair has read the accumulator
     uint64_t mma_done;
@@ -97,7 +102,7 @@ struct Params {
     int64_t rows, cols;            // of the accumulator matrix: (M, N), or (N, M) with kSwap
     int64_t tiles_r, tiles_c;
     int bn;                        // tile columns; a CTA of a pair converts half of them
-    int num_kb, tail_halves;       // raw K blocks; halves of the last one (1 or 2)
+    int num_kb;                    // K blocks of 128
     int raw_stages, raw_bytes;
     int splitk;                    // CTAs of a cluster that share a tile (single CTAs)
     int tma_store;
@@ -247,12 +252,21 @@ __device__ __forceinline__ void tile_origin(const Params &p, int64_t t, int tile
     r0 = (r / gc) * tile_rows;
 }
 
-__device__ __forceinline__ int halves(const Params &p, int kb)
+// ---- roles
+
+// Bounded waits whose first probe is inlined: a call costs ~200 clocks even
+// when the barrier's phase is over already.
+__device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, WaitCtl *wc)
 {
-    return kb + 1 == p.num_kb ? p.tail_halves : 2;
+    return ptx::mbar_try_wait(bar, parity) || wait_bounded(bar, parity, wc);
 }
 
-// ---- roles
+template <int kCtas>
+__device__ __forceinline__ bool wait_peer(uint32_t bar, uint32_t parity, WaitCtl *wc)
+{
+    if constexpr (kCtas == 2) return ptx::mbar_try_wait_cluster(bar, parity) || wait_bounded_cluster(bar, parity, wc);
+    return wait_here(bar, parity, wc);
+}
 
 template <int kCtas>
 __device__ __forceinline__ void run_producer(const CUtensorMap *tmap_r, const CUtensorMap *tmap_c, const Params &p,
@@ -267,7 +281,7 @@ __device__ __forceinline__ void run_producer(const CUtensorMap *tmap_r, const CU
         int64_t r0, c0;
         tile_origin(p, t, kRows * kCtas, r0, c0);
         for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
-            if (!wait_bounded(ptx::smem_addr(&ctrl->raw_empty[stage]), phase ^ 1u, wc)) {
+            if (!wait_here(ptx::smem_addr(&ctrl->raw_empty[stage]), phase ^ 1u, wc)) {
                 ok = false;
                 break;
             }
@@ -303,55 +317,43 @@ __device__ __forceinline__ void arrive_leader(uint32_t bar)
         ptx::mbar_arrive(bar);
 }
 
-template <int kCtas>
-__device__ __forceinline__ bool wait_peer(uint32_t bar, uint32_t parity, WaitCtl *wc)
-{
-    return kCtas == 2 ? wait_bounded_cluster(bar, parity, wc) : wait_bounded(bar, parity, wc);
-}
-
-// Row converters: thread = row.  A raw row is 128 bytes, its 16-byte chunk j
-// stored at chunk position j ^ (row mod 8), so that the eight rows of a
+// Row converters of half h: thread = row.  A raw row is 128 bytes, its 16-byte
+// chunk j stored at chunk position j ^ (row mod 8), so that the eight rows of a
 // wavefront read distinct banks.
 template <int kCtas>
 __device__ __forceinline__ void run_row_converter(const Params &p, uint32_t raw, Ctrl *ctrl, uint32_t tmem_base,
-                                                  int warp, int lane, WaitCtl *wc)
+                                                  int warp, uint32_t h, int lane, WaitCtl *wc)
 {
     const Sched sc = schedule<kCtas>(p);
     const int64_t tiles = p.tiles_r * p.tiles_c;
     const uint32_t quarter = static_cast<uint32_t>(warp & 3);
     const uint32_t row = quarter * 32 + lane;
-    const uint32_t lanes = tmem_base + ((quarter * 32u) << 16) + kConvCol;
+    const uint32_t lanes = tmem_base + ((quarter * 32u) << 16) + kConvCol + h * kConvCols;
     uint32_t stage = 0, phase = 0, cs = 0, cphase = 0;
     for (int64_t t = sc.t0; t < tiles; t += sc.dt) {
         for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
-            bool ok = wait_bounded(ptx::smem_addr(&ctrl->raw_full[stage]), phase, wc);
+            bool ok = wait_here(ptx::smem_addr(&ctrl->raw_full[stage]), phase, wc);
             if (!__all_sync(0xFFFFFFFFu, ok)) return;
             const uint32_t src = raw + stage * static_cast<uint32_t>(p.raw_bytes) + row * kRowBytes;
-            uint4 c[8];
+            uint4 c[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) c[j] = ld_shared_v4(src + ((static_cast<uint32_t>(j) ^ (row & 7u)) << 4));
+            for (uint32_t j = 0; j < 4; ++j) c[j] = ld_shared_v4(src + (((h * 4 + j) ^ (row & 7u)) << 4));
+            uint32_t w[32];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) widen16(c[j], w + j * 8);
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctrl->raw_empty[stage]));
-            const int nh = halves(p, kb);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (h >= nh) break;
-                ok = wait_peer<kCtas>(ptx::smem_addr(&ctrl->conv_empty[cs]), cphase ^ 1u, wc);
-                if (!__all_sync(0xFFFFFFFFu, ok)) return;
-                uint32_t w[32];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) widen16(c[h * 4 + j], w + j * 8);
-                ptx::tc_fence_after();
-                __syncwarp();
-                ptx::tmem_st_32x32b_x32(lanes + cs * kConvCols, w);
-                ptx::tmem_st_wait();
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_leader<kCtas>(ptx::smem_addr(&ctrl->conv_full[cs]));
-                if (++cs == kConv) {
-                    cs = 0;
-                    cphase ^= 1u;
-                }
+            ok = wait_peer<kCtas>(ptx::smem_addr(&ctrl->conv_empty[2 * cs + h]), cphase ^ 1u, wc);
+            if (!__all_sync(0xFFFFFFFFu, ok)) return;
+            ptx::tc_fence_after();
+            ptx::tmem_st_32x32b_x32(lanes + cs * 2 * kConvCols, w);
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_leader<kCtas>(ptx::smem_addr(&ctrl->conv_full[cs]));
+            if (++cs == kConv) {
+                cs = 0;
+                cphase ^= 1u;
             }
             if (++stage == static_cast<uint32_t>(p.raw_stages)) {
                 stage = 0;
@@ -361,22 +363,21 @@ __device__ __forceinline__ void run_row_converter(const Params &p, uint32_t raw,
     }
 }
 
-// Column converters: the CTA's bn / kCtas columns x 64 K values of a half are
+// Column converters of half h: the CTA's bn / kCtas columns x 64 K values are
 // cols x 4 chunks of 16 bytes, dealt over 128 threads (consecutive threads
 // take consecutive columns of one chunk position).  A widened column is a
 // 128-byte K-major row under the 128-byte swizzle.
 template <int kCtas>
 __device__ __forceinline__ void run_col_converter(const Params &p, uint32_t raw, uint32_t conv, Ctrl *ctrl, int tid,
-                                                  int lane, WaitCtl *wc)
+                                                  uint32_t h, int lane, WaitCtl *wc)
 {
     constexpr int kTasks = (kCtas == 2 ? kMaxBn / 2 : kMaxSplitBn) * 4 / 128;  // chunks a thread takes at most
     const Sched sc = schedule<kCtas>(p);
     const int64_t tiles = p.tiles_r * p.tiles_c;
     const int cols = p.bn / kCtas;
-    const uint32_t conv_bytes = static_cast<uint32_t>(cols) * 128u;
-    // offsets of this thread's chunks in a raw row tile (first half; the
-    // second is 64 bytes on, which flips bit 2 of the chunk position) and in a
-    // converted stage
+    const uint32_t half_bytes = static_cast<uint32_t>(cols) * 128u;
+    // offsets of this thread's chunks in a raw stage and in a converted half
+    // (a chunk widens to two 16-byte words: there, and there ^ 16)
     uint32_t src_off[kTasks], dst_off[kTasks];
     int n = 0;
 #pragma unroll
@@ -384,47 +385,42 @@ __device__ __forceinline__ void run_col_converter(const Params &p, uint32_t raw,
         const int task = i * 128 + tid;
         const uint32_t col = static_cast<uint32_t>(task % cols), j = static_cast<uint32_t>(task / cols);
         if (task < cols * 4) ++n;
-        src_off[i] = kRawRowsBytes + col * kRowBytes + ((j ^ (col & 7u)) << 4);
-        dst_off[i] = col * 128u + (((2 * j) ^ (col & 7u)) << 4);  // the chunk's pair of 16-byte words: this, and this ^ 16
+        src_off[i] = kRawRowsBytes + col * kRowBytes + (((h * 4 + j) ^ (col & 7u)) << 4);
+        dst_off[i] = col * 128u + (((2 * j) ^ (col & 7u)) << 4);
     }
     uint32_t stage = 0, phase = 0, cs = 0, cphase = 0;
     for (int64_t t = sc.t0; t < tiles; t += sc.dt) {
         for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
-            bool ok = wait_bounded(ptx::smem_addr(&ctrl->raw_full[stage]), phase, wc);
+            bool ok = wait_here(ptx::smem_addr(&ctrl->raw_full[stage]), phase, wc);
             if (!__all_sync(0xFFFFFFFFu, ok)) return;
             const uint32_t src = raw + stage * static_cast<uint32_t>(p.raw_bytes);
-            uint4 c[2][kTasks];
-            const int nh = halves(p, kb);
+            uint4 c[kTasks];
+            uint32_t w[kTasks][8];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int i = 0; i < kTasks; ++i)
+                if (i < n && DGEMM_CHECK(src_off[i] + 16 <= static_cast<uint32_t>(p.raw_bytes)))
+                    c[i] = ld_shared_v4(src + src_off[i]);
 #pragma unroll
-                for (int i = 0; i < kTasks; ++i)
-                    if (i < n && DGEMM_CHECK((src_off[i] ^ (h << 6)) + 16 <= static_cast<uint32_t>(p.raw_bytes)))
-                        c[h][i] = ld_shared_v4(src + (src_off[i] ^ (static_cast<uint32_t>(h) << 6)));
+            for (int i = 0; i < kTasks; ++i)
+                if (i < n) widen16(c[i], w[i]);
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctrl->raw_empty[stage]));
+            ok = wait_peer<kCtas>(ptx::smem_addr(&ctrl->conv_empty[2 * cs + h]), cphase ^ 1u, wc);
+            if (!__all_sync(0xFFFFFFFFu, ok)) return;
+            const uint32_t dst = conv + (2 * cs + h) * half_bytes;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (h >= nh) break;
-                ok = wait_peer<kCtas>(ptx::smem_addr(&ctrl->conv_empty[cs]), cphase ^ 1u, wc);
-                if (!__all_sync(0xFFFFFFFFu, ok)) return;
-                const uint32_t dst = conv + cs * conv_bytes;
-#pragma unroll
-                for (int i = 0; i < kTasks; ++i) {
-                    if (i < n && DGEMM_CHECK((dst_off[i] | 16u) + 16 <= conv_bytes)) {
-                        uint32_t w[8];
-                        widen16(c[h][i], w);
-                        ptx::st_shared_v4(dst + dst_off[i], make_uint4(w[0], w[1], w[2], w[3]));
-                        ptx::st_shared_v4(dst + (dst_off[i] ^ 16u), make_uint4(w[4], w[5], w[6], w[7]));
-                    }
+            for (int i = 0; i < kTasks; ++i) {
+                if (i < n && DGEMM_CHECK((dst_off[i] | 16u) + 16 <= half_bytes)) {
+                    ptx::st_shared_v4(dst + dst_off[i], make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]));
+                    ptx::st_shared_v4(dst + (dst_off[i] ^ 16u), make_uint4(w[i][4], w[i][5], w[i][6], w[i][7]));
                 }
-                ptx::fence_proxy_async_smem();  // the MMAs read through the async proxy
-                __syncwarp();
-                if (lane == 0) arrive_leader<kCtas>(ptx::smem_addr(&ctrl->conv_full[cs]));
-                if (++cs == kConv) {
-                    cs = 0;
-                    cphase ^= 1u;
-                }
+            }
+            ptx::fence_proxy_async_smem();  // the MMAs read through the async proxy
+            __syncwarp();
+            if (lane == 0) arrive_leader<kCtas>(ptx::smem_addr(&ctrl->conv_full[cs]));
+            if (++cs == kConv) {
+                cs = 0;
+                cphase ^= 1u;
             }
             if (++stage == static_cast<uint32_t>(p.raw_stages)) {
                 stage = 0;
@@ -437,7 +433,7 @@ __device__ __forceinline__ void run_col_converter(const Params &p, uint32_t raw,
 constexpr uint32_t kHandoff = 64;  // warps 1 and 2 on named barriers 1 .. kConv
 constexpr uint32_t kEpiBarrier = 1 + kConv;
 
-// Waits for each converted half and meets the MMA warp on named barrier
+// Waits for each converted stage and meets the MMA warp on named barrier
 // 1 + stage, whose OR carries an abort both ways: both sides make the same
 // number of hand-offs whatever happens.
 template <int kCtas>
@@ -449,18 +445,15 @@ __device__ __forceinline__ void run_waiter(const Params &p, Ctrl *ctrl, int lane
     bool abort = false;
     for (int64_t t = sc.t0; t < tiles; t += sc.dt) {
         for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
-            const int nh = halves(p, kb);
-            for (int h = 0; h < nh; ++h) {
-                if (!abort) {
-                    bool ok = true;
-                    if (lane == 0) ok = wait_peer<kCtas>(ptx::smem_addr(&ctrl->conv_full[cs]), cphase, wc);
-                    abort = __shfl_sync(0xFFFFFFFFu, ok ? 0 : 1, 0) != 0;
-                }
-                abort = ptx::bar_red_or(1 + cs, kHandoff, abort);
-                if (++cs == kConv) {
-                    cs = 0;
-                    cphase ^= 1u;
-                }
+            if (!abort) {
+                bool ok = true;
+                if (lane == 0) ok = wait_peer<kCtas>(ptx::smem_addr(&ctrl->conv_full[cs]), cphase, wc);
+                abort = __shfl_sync(0xFFFFFFFFu, ok ? 0 : 1, 0) != 0;
+            }
+            abort = ptx::bar_red_or(1 + cs, kHandoff, abort);
+            if (++cs == kConv) {
+                cs = 0;
+                cphase ^= 1u;
             }
         }
     }
@@ -472,12 +465,12 @@ __device__ __forceinline__ void run_mma(const Params &p, uint32_t conv, Ctrl *ct
 {
     const Sched sc = schedule<kCtas>(p);
     const int64_t tiles = p.tiles_r * p.tiles_c;
-    const uint32_t conv_bytes = static_cast<uint32_t>(p.bn / kCtas) * 128u;
+    const uint32_t half_bytes = static_cast<uint32_t>(p.bn / kCtas) * 128u;
     // D f32, A and B f16 and K-major, N = bn, M = 128 rows a CTA
     const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(p.bn >> 3) << 17) |
                            (static_cast<uint32_t>(kRows * kCtas >> 4) << 24);
-    // one column of the ring's descriptors: a stage on is conv_bytes / 16, an
-    // MMA's K step 2, in their address field
+    // the descriptor of the first MMA's columns; a half on is half_bytes / 16,
+    // an MMA's K step 2, in its address field
     const uint64_t b_desc = ptx::smem_desc(conv, 16, 1024, ptx::kSw128);
     tmem_base = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);  // a uniform value for the compiler
     uint32_t cs = 0, acc = 0, acc_phase = 0;
@@ -494,24 +487,24 @@ __device__ __forceinline__ void run_mma(const Params &p, uint32_t conv, Ctrl *ct
         const uint32_t d = tmem_base + acc * kAccCols;
         uint32_t accumulate = 0;
         for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
-            const int nh = halves(p, kb);
-            for (int h = 0; h < nh; ++h) {
-                abort = __any_sync(0xFFFFFFFFu, ptx::bar_red_or(1 + cs, kHandoff, abort));
-                if (!abort) {
-                    ptx::tc_fence_after();
-                    if (elect_one()) {
-                        const uint32_t a = tmem_base + kConvCol + cs * kConvCols;
-                        const uint64_t b = b_desc + cs * (conv_bytes >> 4);
+            abort = __any_sync(0xFFFFFFFFu, ptx::bar_red_or(1 + cs, kHandoff, abort));
+            if (!abort) {
+                ptx::tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (uint32_t h = 0; h < 2; ++h) {
+                        const uint32_t a = tmem_base + kConvCol + (2 * cs + h) * kConvCols;
+                        const uint64_t b = b_desc + (2 * cs + h) * (half_bytes >> 4);
 #pragma unroll
                         for (int k = 0; k < kHalfK / 16; ++k)
-                            umma_a_tmem<kCtas>(d, a + k * 8, b + k * 2, idesc, k == 0 ? accumulate : 1u);
-                        commit_all<kCtas>(ptx::smem_addr(&ctrl->conv_empty[cs]));
+                            umma_a_tmem<kCtas>(d, a + k * 8, b + k * 2, idesc, h == 0 && k == 0 ? accumulate : 1u);
+                        commit_all<kCtas>(ptx::smem_addr(&ctrl->conv_empty[2 * cs + h]));
                     }
-                    __syncwarp();
                 }
-                accumulate = 1;
-                if (++cs == kConv) cs = 0;
+                __syncwarp();
             }
+            accumulate = 1;
+            if (++cs == kConv) cs = 0;
         }
         if (!abort && elect_one()) commit_all<kCtas>(ptx::smem_addr(&ctrl->acc_full[acc]));
         __syncwarp();
@@ -560,46 +553,47 @@ __device__ __forceinline__ void drain_tokens(const Params &p, const CUtensorMap 
         for (int b = 0; b < p.bn / kCols; ++b) {
             const int64_t col0 = c0 + b * kCols;
             const uint32_t buf = box + (nbox & 1u) * kBoxBytes;
-            uint32_t r[kCols];
-            __syncwarp();
-            ptx::tmem_ld_32x32b_x32(taddr + b * kCols, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
-            if constexpr (kCols == 64)
-                ptx::tmem_ld_32x32b_x32(taddr + b * kCols + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
-            ptx::tmem_ld_wait();
-            if (row0 >= p.rows || col0 >= p.cols) continue;  // warp-uniform: nothing of C here
+            if (row0 >= p.rows || col0 >= p.cols) break;  // warp-uniform: nothing of C here
             if (lane == 0 && nbox >= 2) ptx::bulk_wait_read<1>();  // this box's last store has read it
             __syncwarp();
             const uint32_t dst = buf + static_cast<uint32_t>(lane) * 128u;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                constexpr int kPer = 16 / sizeof(T);
-                float v[kPer];
+            for (int half = 0; half < kCols / 32; ++half) {
+                uint32_t r[32];
+                ptx::tmem_ld_32x32b_x32(taddr + b * kCols + half * 32, r);
+                ptx::tmem_ld_wait();
+                constexpr int kPer = 16 / sizeof(T);  // values of a 16-byte word
 #pragma unroll
-                for (int e = 0; e < kPer; e += 4) {
-                    const uint32_t at = static_cast<uint32_t>(b * kCols + j * kPer + e) * 4u;
-                    const float4 s = ptx::ld_shared_v4f(scale + at), o = ptx::ld_shared_v4f(bias + at);
-                    const uint32_t *a = r + j * kPer + e;
-                    v[e] = fmaf(__uint_as_float(a[0]) * sa, s.x, o.x);
-                    v[e + 1] = fmaf(__uint_as_float(a[1]) * sa, s.y, o.y);
-                    v[e + 2] = fmaf(__uint_as_float(a[2]) * sa, s.z, o.z);
-                    v[e + 3] = fmaf(__uint_as_float(a[3]) * sa, s.w, o.w);
-                }
-                if (beta != 0.f && row < p.rows) {
-                    const int64_t col = col0 + j * kPer;
+                for (int j = 0; j < 32 / kPer; ++j) {
+                    float v[kPer];
 #pragma unroll
-                    for (int e = 0; e < kPer; ++e)
-                        if (col + e < p.cols) v[e] = fmaf(beta, i8_to_f32(crow[col + e]), v[e]);
+                    for (int e = 0; e < kPer; e += 4) {
+                        const uint32_t at = static_cast<uint32_t>(b * kCols + half * 32 + j * kPer + e) * 4u;
+                        const float4 s = ptx::ld_shared_v4f(scale + at), o = ptx::ld_shared_v4f(bias + at);
+                        const uint32_t *a = r + j * kPer + e;
+                        v[e] = fmaf(__uint_as_float(a[0]) * sa, s.x, o.x);
+                        v[e + 1] = fmaf(__uint_as_float(a[1]) * sa, s.y, o.y);
+                        v[e + 2] = fmaf(__uint_as_float(a[2]) * sa, s.z, o.z);
+                        v[e + 3] = fmaf(__uint_as_float(a[3]) * sa, s.w, o.w);
+                    }
+                    if (beta != 0.f && row < p.rows) {
+                        const int64_t col = col0 + half * 32 + j * kPer;
+#pragma unroll
+                        for (int e = 0; e < kPer; ++e)
+                            if (col + e < p.cols) v[e] = fmaf(beta, i8_to_f32(crow[col + e]), v[e]);
+                    }
+                    uint4 q;
+                    if constexpr (sizeof(T) == 2)
+                        q = make_uint4(pack_bits(i8_from_f32<T>(v[0]), i8_from_f32<T>(v[1])),
+                                       pack_bits(i8_from_f32<T>(v[2]), i8_from_f32<T>(v[3])),
+                                       pack_bits(i8_from_f32<T>(v[4]), i8_from_f32<T>(v[5])),
+                                       pack_bits(i8_from_f32<T>(v[6]), i8_from_f32<T>(v[7])));
+                    else
+                        q = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                       __float_as_uint(v[3]));
+                    const uint32_t word = static_cast<uint32_t>(half * 32 / kPer + j);
+                    ptx::st_shared_v4(dst + ((word ^ (static_cast<uint32_t>(lane) & 7u)) << 4), q);
                 }
-                uint4 q;
-                if constexpr (sizeof(T) == 2)
-                    q = make_uint4(pack_bits(i8_from_f32<T>(v[0]), i8_from_f32<T>(v[1])),
-                                   pack_bits(i8_from_f32<T>(v[2]), i8_from_f32<T>(v[3])),
-                                   pack_bits(i8_from_f32<T>(v[4]), i8_from_f32<T>(v[5])),
-                                   pack_bits(i8_from_f32<T>(v[6]), i8_from_f32<T>(v[7])));
-                else
-                    q = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                   __float_as_uint(v[3]));
-                ptx::st_shared_v4(dst + ((static_cast<uint32_t>(j) ^ (static_cast<uint32_t>(lane) & 7u)) << 4), q);
             }
             ptx::fence_proxy_async_smem();  // the TMA store reads through the async proxy
             __syncwarp();
@@ -805,7 +799,7 @@ __device__ __forceinline__ void splitk_reduce(const Params &p, uint32_t tmem_bas
 
 __host__ __device__ constexpr uint32_t conv_ring_bytes(int bn, int ctas)
 {
-    return static_cast<uint32_t>(kConv * (bn / ctas) * 128);
+    return static_cast<uint32_t>(2 * kConv * (bn / ctas) * 128);
 }
 
 template <int kCtas, bool kSwap, typename T>
@@ -828,11 +822,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMaxRaw; ++s) {
             ptx::mbar_init(ptx::smem_addr(&ctrl->raw_full[s]), 1);
-            ptx::mbar_init(ptx::smem_addr(&ctrl->raw_empty[s]), 8);
+            ptx::mbar_init(ptx::smem_addr(&ctrl->raw_empty[s]), 16);
         }
         for (int s = 0; s < kConv; ++s) {
-            ptx::mbar_init(ptx::smem_addr(&ctrl->conv_full[s]), 8 * kCtas);
-            ptx::mbar_init(ptx::smem_addr(&ctrl->conv_empty[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&ctrl->conv_full[s]), 16 * kCtas);
+            ptx::mbar_init(ptx::smem_addr(&ctrl->conv_empty[2 * s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&ctrl->conv_empty[2 * s + 1]), 1);
         }
         for (int a = 0; a < 2; ++a) {
             ptx::mbar_init(ptx::smem_addr(&ctrl->acc_full[a]), 1);
@@ -873,10 +868,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (leader) run_mma<kCtas>(p, conv, ctrl, tmem_base, lane, wc);
     } else if (warp == 2) {
         if (leader) run_waiter<kCtas>(p, ctrl, lane, wc);
-    } else if (warp >= 12) {
-        run_col_converter<kCtas>(p, raw, conv, ctrl, threadIdx.x - 12 * 32, lane, wc);
+    } else if (warp >= 16) {
+        run_col_converter<kCtas>(p, raw, conv, ctrl, threadIdx.x & 127, (warp - 16) >> 2, lane, wc);
     } else if (warp >= 8) {
-        run_row_converter<kCtas>(p, raw, ctrl, tmem_base, warp, lane, wc);
+        run_row_converter<kCtas>(p, raw, ctrl, tmem_base, warp, (warp - 8) >> 2, lane, wc);
     } else if (warp >= 4) {
         if (kCtas == 1 && p.splitk > 1)
             wait_bounded(ptx::smem_addr(&ctrl->acc_full[0]), 0, wc);  // a time-out raises the abort flag
@@ -974,7 +969,6 @@ bool launch(const I8Params &c, int bn, int splitk, cudaStream_t stream)
     p.tiles_r = (p.rows + kRows * kCtas - 1) / (kRows * kCtas);
     p.tiles_c = (p.cols + bn - 1) / bn;
     p.num_kb = static_cast<int>((c.K + kRowBytes - 1) / kRowBytes);
-    p.tail_halves = c.K % kRowBytes > 0 && c.K % kRowBytes <= kHalfK ? 1 : 2;
     p.splitk = std::min(splitk, p.num_kb);
     const int smem = set_ring(p, kCtas, kSwap);
     const int cluster = kCtas == 2 ? 2 : p.splitk;
