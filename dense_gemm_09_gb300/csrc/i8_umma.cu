@@ -364,14 +364,14 @@ __device__ __forceinline__ void run_row_converter(const Params &p, uint32_t raw,
 }
 
 // Column converters of half h: the CTA's bn / kCtas columns x 64 K values are
-// cols x 4 chunks of 16 bytes, dealt over 128 threads (consecutive threads
-// take consecutive columns of one chunk position).  A widened column is a
-// 128-byte K-major row under the 128-byte swizzle.
-template <int kCtas>
+// cols x 4 chunks of 16 bytes, kTasks of them a thread (consecutive threads
+// take consecutive columns of one chunk position; where cols is no multiple
+// of 32, some chunks are widened twice, to the same words).  A widened column
+// is a 128-byte K-major row under the 128-byte swizzle.
+template <int kCtas, int kTasks>
 __device__ __forceinline__ void run_col_converter(const Params &p, uint32_t raw, uint32_t conv, Ctrl *ctrl, int tid,
                                                   uint32_t h, int lane, WaitCtl *wc)
 {
-    constexpr int kTasks = (kCtas == 2 ? kMaxBn / 2 : kMaxSplitBn) * 4 / 128;  // chunks a thread takes at most
     const Sched sc = schedule<kCtas>(p);
     const int64_t tiles = p.tiles_r * p.tiles_c;
     const int cols = p.bn / kCtas;
@@ -379,12 +379,10 @@ __device__ __forceinline__ void run_col_converter(const Params &p, uint32_t raw,
     // offsets of this thread's chunks in a raw stage and in a converted half
     // (a chunk widens to two 16-byte words: there, and there ^ 16)
     uint32_t src_off[kTasks], dst_off[kTasks];
-    int n = 0;
 #pragma unroll
     for (int i = 0; i < kTasks; ++i) {
         const int task = i * 128 + tid;
-        const uint32_t col = static_cast<uint32_t>(task % cols), j = static_cast<uint32_t>(task / cols);
-        if (task < cols * 4) ++n;
+        const uint32_t col = static_cast<uint32_t>(task % cols), j = static_cast<uint32_t>(task / cols) & 3u;
         src_off[i] = kRawRowsBytes + col * kRowBytes + (((h * 4 + j) ^ (col & 7u)) << 4);
         dst_off[i] = col * 128u + (((2 * j) ^ (col & 7u)) << 4);
     }
@@ -398,11 +396,10 @@ __device__ __forceinline__ void run_col_converter(const Params &p, uint32_t raw,
             uint32_t w[kTasks][8];
 #pragma unroll
             for (int i = 0; i < kTasks; ++i)
-                if (i < n && DGEMM_CHECK(src_off[i] + 16 <= static_cast<uint32_t>(p.raw_bytes)))
+                if (DGEMM_CHECK(src_off[i] + 16 <= static_cast<uint32_t>(p.raw_bytes)))
                     c[i] = ld_shared_v4(src + src_off[i]);
 #pragma unroll
-            for (int i = 0; i < kTasks; ++i)
-                if (i < n) widen16(c[i], w[i]);
+            for (int i = 0; i < kTasks; ++i) widen16(c[i], w[i]);
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctrl->raw_empty[stage]));
             ok = wait_peer<kCtas>(ptx::smem_addr(&ctrl->conv_empty[2 * cs + h]), cphase ^ 1u, wc);
@@ -410,7 +407,7 @@ __device__ __forceinline__ void run_col_converter(const Params &p, uint32_t raw,
             const uint32_t dst = conv + (2 * cs + h) * half_bytes;
 #pragma unroll
             for (int i = 0; i < kTasks; ++i) {
-                if (i < n && DGEMM_CHECK((dst_off[i] | 16u) + 16 <= half_bytes)) {
+                if (DGEMM_CHECK((dst_off[i] | 16u) + 16 <= half_bytes)) {
                     ptx::st_shared_v4(dst + dst_off[i], make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]));
                     ptx::st_shared_v4(dst + (dst_off[i] ^ 16u), make_uint4(w[i][4], w[i][5], w[i][6], w[i][7]));
                 }
@@ -869,7 +866,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 2) {
         if (leader) run_waiter<kCtas>(p, ctrl, lane, wc);
     } else if (warp >= 16) {
-        run_col_converter<kCtas>(p, raw, conv, ctrl, threadIdx.x & 127, (warp - 16) >> 2, lane, wc);
+        const int tid = threadIdx.x & 127, h = (warp - 16) >> 2;
+        switch ((p.bn / kCtas + 31) / 32) {  // chunks a thread takes; uniform
+        case 1: run_col_converter<kCtas, 1>(p, raw, conv, ctrl, tid, h, lane, wc); break;
+        case 2: run_col_converter<kCtas, 2>(p, raw, conv, ctrl, tid, h, lane, wc); break;
+        case 3: run_col_converter<kCtas, 3>(p, raw, conv, ctrl, tid, h, lane, wc); break;
+        default:
+            if constexpr (kCtas == 1) run_col_converter<kCtas, 4>(p, raw, conv, ctrl, tid, h, lane, wc);
+        }
     } else if (warp >= 8) {
         run_row_converter<kCtas>(p, raw, ctrl, tmem_base, warp, (warp - 8) >> 2, lane, wc);
     } else if (warp >= 4) {
