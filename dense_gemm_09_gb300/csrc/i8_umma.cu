@@ -19,24 +19,23 @@
 // That leaves 52 KB, 416 clocks; with both operands widened in shared memory
 // it would be 84 KB, 672 clocks.
 //
-// Roles (24 warps, one CTA an SM):
+// Roles (32 warps, one CTA an SM):
 //   warp 0       TMA producer: 128-byte rows (128 K values) of both operands
 //                into a ring of raw stages (128-byte swizzle);
-//   warps 8-15   row converters, four for either half (64 K values) of a raw
-//                stage: warp w widens rows 32 (w mod 4) .. into its own TMEM
-//                lanes, 32 columns a half;
-//   warps 16-23  column converters, four for either half: the other operand,
-//                K-major FP16 in shared memory (128-byte swizzle);
-//   warp 2       waits for each converted stage and hands it on through a named
-//                barrier (a probe of an mbarrier by the MMA thread between
-//                stages starves the tensor pipe);
-//   warp 1       MMA issuer: four tcgen05.mma of K = 16 a half, each half
-//                released by a commit of its own;
+//   warps 8-19   row converters, three groups of four that take the halves (64
+//                K values) of the raw stages in turn: warp w widens rows 32 (w
+//                mod 4) .. into its own TMEM lanes, 32 columns a half;
+//   warps 20-31  column converters, in turn too: the other operand, K-major
+//                FP16 in shared memory (128-byte swizzle);
+//   warp 1       MMA issuer: four tcgen05.mma of K = 16 a half, then a commit that
+//                releases the half;
 //   warps 4-7    epilogue: accumulator -> scale, bias, beta -> C.
-// There are two converted stages (four halves).  A converter reads and widens
-// its part of a stage into registers before it waits for the half's MMAs of
-// two stages ago, so that only the store, the hand-off and the commit lie
-// between the release of a half and its next use.
+// Four halves are in flight between converters and MMAs.  A converter reads and widens
+// its part of a stage into registers before it waits for the MMAs of
+// four halves ago, so that only the store, the hand-off and the commit lie
+// between the release of a half and its next use.  A half takes a converter
+// group ~700 clocks from its first wait to its arrival, nearly all of it
+// latency; three groups keep a stage at 2/3 of that.
 // A CTA pair (cta_group::2) shares one MMA: each CTA widens its own 128 rows
 // and half of the columns, and all of the pair's converters arrive on the
 // leader's barrier.
@@ -71,30 +70,32 @@ constexpr int kHalfK = 64;                      // K values of a converted half
 constexpr int kMaxBn = 192;                     // tile columns
 constexpr int kMaxSplitBn = 128;                // of a single CTA's tile
 constexpr int kMaxRaw = 8;                      // raw stages
-constexpr int kConv = 2;                        // converted stages, of two halves each
+constexpr int kConv = 4;                        // converted halves in flight
 constexpr int kAccCols = 192;                   // TMEM columns of an accumulator (two of them)
 constexpr int kConvCol = 2 * kAccCols;          // first TMEM column of the converted rows
 constexpr int kConvCols = kHalfK / 2;           // two FP16 values a column
 constexpr int kTmemCols = 512;
-static_assert(kConvCol + 2 * kConv * kConvCols <= kTmemCols, "accumulators and converted rows fit in TMEM");
+static_assert(kConvCol + kConv * kConvCols <= kTmemCols, "accumulators and converted rows fit in TMEM");
 constexpr int kBoxBytes = 4096;                 // epilogue staging: 32 rows x 128 bytes
 constexpr int kEpiWarps = 4;
-constexpr int kThreads = 768;
+constexpr int kConvGroups = 3;                  // converter groups of four warps, of either kind
+constexpr int kThreads = 32 * (8 + 2 * 4 * kConvGroups);
+static_assert(kThreads <= 1024, "one CTA");
 constexpr int kSmemLimit = 227 * 1024;
 
 struct Ctrl {
     uint64_t raw_full[kMaxRaw];    // a raw stage has landed
     uint64_t raw_empty[kMaxRaw];   // its 16 converter warps have read it
-    uint64_t conv_full[kConv];     // leader: every converter warp of the pair has stored its part
-    uint64_t conv_empty[2 * kConv];  // the MMAs have read this converted half
+    uint64_t conv_full[kConv];     // leader: every converter warp of the pair has stored its part of the half
+    uint64_t conv_empty[kConv];    // the MMAs have read this converted half
     uint64_t acc_full[2];
     uint64_t acc_empty[2];         // leader: every epilogue warp of the pair has read the accumulator
     uint64_t mma_done;
     uint64_t never;                // test hook: a barrier nothing arrives at
     WaitCtl wait;
     uint32_t tmem_base;
-    alignas(16) float scale[kMaxBn];  // of the tile's columns (kSwap = false)
-    alignas(16) float bias[kMaxBn];
+    alignas(16) float scale[kMaxBn];  // of the tile's columns
+    alignas(16) float bias[kMaxBn];   // (kSwap = false)
 };
 
 struct Params {
@@ -169,6 +170,17 @@ __device__ __forceinline__ bool elect_one()
     uint32_t p;
     asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
     return p != 0;
+}
+
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
 }
 
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr)
@@ -254,18 +266,39 @@ __device__ __forceinline__ void tile_origin(const Params &p, int64_t t, int tile
 
 // ---- roles
 
-// Bounded waits whose first probe is inlined: a call costs ~200 clocks even
-// when the barrier's phase is over already.
-__device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, WaitCtl *wc)
+// Bounded waits of a whole converged warp.  Every step is decided by a vote, so
+// that no branch diverges: a divergent wait (one lane probing, or a per-thread
+// loop) costs hundreds of clocks in reconvergence on each half.  False for the
+// whole warp on time-out or abort.
+template <bool kCluster>
+__device__ __forceinline__ bool probe(uint32_t bar, uint32_t parity)
 {
-    return ptx::mbar_try_wait(bar, parity) || wait_bounded(bar, parity, wc);
+    return __all_sync(0xFFFFFFFFu, kCluster ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity));
+}
+
+template <bool kCluster>
+__device__ __noinline__ bool warp_wait_slow(uint32_t bar, uint32_t parity, WaitCtl *wc)
+{
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i)
+        if (probe<kCluster>(bar, parity)) return true;
+    const uint64_t t0 = ptx::globaltimer_ns(), limit = wc->limit_ns;
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (probe<kCluster>(bar, parity)) return true;
+        if (__any_sync(0xFFFFFFFFu, aborted(wc))) return false;
+        if (__any_sync(0xFFFFFFFFu, ptx::globaltimer_ns() - t0 > limit)) {
+            raise_abort(wc);
+            return false;
+        }
+    }
 }
 
 template <int kCtas>
-__device__ __forceinline__ bool wait_peer(uint32_t bar, uint32_t parity, WaitCtl *wc)
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, WaitCtl *wc)
 {
-    if constexpr (kCtas == 2) return ptx::mbar_try_wait_cluster(bar, parity) || wait_bounded_cluster(bar, parity, wc);
-    return wait_here(bar, parity, wc);
+    return probe<kCtas == 2>(bar, parity) || warp_wait_slow<kCtas == 2>(bar, parity, wc);
 }
 
 template <int kCtas>
@@ -281,7 +314,7 @@ __device__ __forceinline__ void run_producer(const CUtensorMap *tmap_r, const CU
         int64_t r0, c0;
         tile_origin(p, t, kRows * kCtas, r0, c0);
         for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
-            if (!wait_here(ptx::smem_addr(&ctrl->raw_empty[stage]), phase ^ 1u, wc)) {
+            if (!wait_bounded(ptx::smem_addr(&ctrl->raw_empty[stage]), phase ^ 1u, wc)) {
                 ok = false;
                 break;
             }
@@ -317,148 +350,129 @@ __device__ __forceinline__ void arrive_leader(uint32_t bar)
         ptx::mbar_arrive(bar);
 }
 
-// Row converters of half h: thread = row.  A raw row is 128 bytes, its 16-byte
-// chunk j stored at chunk position j ^ (row mod 8), so that the eight rows of a
+// A converter group's walk over the halves of the CTA's raw stages, in the
+// order the producer fills them: halves group, group + 3, ...
+struct HalfIter {
+    int64_t i, end;          // half index over all of the CTA's tiles
+    uint32_t stage, phase;   // of the raw ring
+    uint32_t stages;
+
+    __device__ __forceinline__ HalfIter(const Params &p, const Sched &sc, int group)
+    {
+        const int64_t tiles = p.tiles_r * p.tiles_c;
+        const int64_t mine = sc.t0 < tiles ? (tiles - sc.t0 + sc.dt - 1) / sc.dt : 0;
+        i = group;
+        end = mine * (sc.kb1 - sc.kb0) * 2;
+        stages = static_cast<uint32_t>(p.raw_stages);
+        stage = 0;
+        phase = 0;
+        step(static_cast<uint32_t>(group) >> 1);
+    }
+    __device__ __forceinline__ void step(uint32_t n)
+    {
+        stage += n;
+        if (stage >= stages) {
+            stage -= stages;
+            phase ^= 1u;
+        }
+    }
+    __device__ __forceinline__ bool more() const { return i < end; }
+    __device__ __forceinline__ void next()
+    {
+        step(static_cast<uint32_t>(((i + kConvGroups) >> 1) - (i >> 1)));
+        i += kConvGroups;
+    }
+    __device__ __forceinline__ uint32_t half() const { return static_cast<uint32_t>(i) & 1u; }
+    // where the half is converted to, and that slot's phase
+    __device__ __forceinline__ uint32_t slot() const { return static_cast<uint32_t>(i) % kConv; }
+    __device__ __forceinline__ uint32_t slot_phase() const { return static_cast<uint32_t>(i / kConv) & 1u; }
+};
+
+// Row converters: thread = row.  A raw row is 128 bytes, its 16-byte chunk j
+// stored at chunk position j ^ (row mod 8), so that the eight rows of a
 // wavefront read distinct banks.
 template <int kCtas>
 __device__ __forceinline__ void run_row_converter(const Params &p, uint32_t raw, Ctrl *ctrl, uint32_t tmem_base,
-                                                  int warp, uint32_t h, int lane, WaitCtl *wc)
+                                                  int warp, int group, int lane, WaitCtl *wc)
 {
-    const Sched sc = schedule<kCtas>(p);
-    const int64_t tiles = p.tiles_r * p.tiles_c;
     const uint32_t quarter = static_cast<uint32_t>(warp & 3);
     const uint32_t row = quarter * 32 + lane;
-    const uint32_t lanes = tmem_base + ((quarter * 32u) << 16) + kConvCol + h * kConvCols;
-    uint32_t stage = 0, phase = 0, cs = 0, cphase = 0;
-    for (int64_t t = sc.t0; t < tiles; t += sc.dt) {
-        for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
-            bool ok = wait_here(ptx::smem_addr(&ctrl->raw_full[stage]), phase, wc);
-            if (!__all_sync(0xFFFFFFFFu, ok)) return;
-            const uint32_t src = raw + stage * static_cast<uint32_t>(p.raw_bytes) + row * kRowBytes;
-            uint4 c[4];
+    const uint32_t lanes = tmem_base + ((quarter * 32u) << 16) + kConvCol;
+    for (HalfIter it(p, schedule<kCtas>(p), group); it.more(); it.next()) {
+        if (!warp_wait<1>(ptx::smem_addr(&ctrl->raw_full[it.stage]), it.phase, wc)) return;
+        const uint32_t src = raw + it.stage * static_cast<uint32_t>(p.raw_bytes) + row * kRowBytes;
+        uint4 c[4];
 #pragma unroll
-            for (uint32_t j = 0; j < 4; ++j) c[j] = ld_shared_v4(src + (((h * 4 + j) ^ (row & 7u)) << 4));
-            uint32_t w[32];
+        for (uint32_t j = 0; j < 4; ++j) c[j] = ld_shared_v4(src + (((it.half() * 4 + j) ^ (row & 7u)) << 4));
+        uint32_t w[32];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) widen16(c[j], w + j * 8);
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctrl->raw_empty[stage]));
-            ok = wait_peer<kCtas>(ptx::smem_addr(&ctrl->conv_empty[2 * cs + h]), cphase ^ 1u, wc);
-            if (!__all_sync(0xFFFFFFFFu, ok)) return;
-            ptx::tc_fence_after();
-            ptx::tmem_st_32x32b_x32(lanes + cs * 2 * kConvCols, w);
-            ptx::tmem_st_wait();
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_leader<kCtas>(ptx::smem_addr(&ctrl->conv_full[cs]));
-            if (++cs == kConv) {
-                cs = 0;
-                cphase ^= 1u;
-            }
-            if (++stage == static_cast<uint32_t>(p.raw_stages)) {
-                stage = 0;
-                phase ^= 1u;
-            }
-        }
+        for (int j = 0; j < 4; ++j) widen16(c[j], w + j * 8);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctrl->raw_empty[it.stage]));
+        if (!warp_wait<kCtas>(ptx::smem_addr(&ctrl->conv_empty[it.slot()]), it.slot_phase() ^ 1u, wc)) return;
+        ptx::tc_fence_after();
+        ptx::tmem_st_32x32b_x32(lanes + it.slot() * kConvCols, w);
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_leader<kCtas>(ptx::smem_addr(&ctrl->conv_full[it.slot()]));
     }
 }
 
-// Column converters of half h: the CTA's bn / kCtas columns x 64 K values are
-// cols x 4 chunks of 16 bytes, kTasks of them a thread (consecutive threads
-// take consecutive columns of one chunk position; where cols is no multiple
-// of 32, some chunks are widened twice, to the same words).  A widened column
-// is a 128-byte K-major row under the 128-byte swizzle.
+// Column converters: a half is the CTA's cols = bn / kCtas columns x 64 K
+// values, cols x 4 chunks of 16 bytes, kTasks of them a thread (consecutive
+// threads take consecutive columns of one chunk position; where cols is no
+// multiple of 32, some chunks are widened twice, to the same words).  A
+// widened column is a 128-byte K-major row under the 128-byte swizzle.
 template <int kCtas, int kTasks>
 __device__ __forceinline__ void run_col_converter(const Params &p, uint32_t raw, uint32_t conv, Ctrl *ctrl, int tid,
-                                                  uint32_t h, int lane, WaitCtl *wc)
+                                                  int group, int lane, WaitCtl *wc)
 {
-    const Sched sc = schedule<kCtas>(p);
-    const int64_t tiles = p.tiles_r * p.tiles_c;
     const int cols = p.bn / kCtas;
     const uint32_t half_bytes = static_cast<uint32_t>(cols) * 128u;
-    // offsets of this thread's chunks in a raw stage and in a converted half
-    // (a chunk widens to two 16-byte words: there, and there ^ 16)
+    // offsets of this thread's chunks in a raw stage's first half (the second
+    // half's differ in bit 6) and in a converted half (a chunk widens to two
+    // 16-byte words: there, and there ^ 16)
     uint32_t src_off[kTasks], dst_off[kTasks];
 #pragma unroll
     for (int i = 0; i < kTasks; ++i) {
         const int task = i * 128 + tid;
         const uint32_t col = static_cast<uint32_t>(task % cols), j = static_cast<uint32_t>(task / cols) & 3u;
-        src_off[i] = kRawRowsBytes + col * kRowBytes + (((h * 4 + j) ^ (col & 7u)) << 4);
+        src_off[i] = kRawRowsBytes + col * kRowBytes + ((j ^ (col & 7u)) << 4);
         dst_off[i] = col * 128u + (((2 * j) ^ (col & 7u)) << 4);
     }
-    uint32_t stage = 0, phase = 0, cs = 0, cphase = 0;
-    for (int64_t t = sc.t0; t < tiles; t += sc.dt) {
-        for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
-            bool ok = wait_here(ptx::smem_addr(&ctrl->raw_full[stage]), phase, wc);
-            if (!__all_sync(0xFFFFFFFFu, ok)) return;
-            const uint32_t src = raw + stage * static_cast<uint32_t>(p.raw_bytes);
-            uint4 c[kTasks];
-            uint32_t w[kTasks][8];
+    for (HalfIter it(p, schedule<kCtas>(p), group); it.more(); it.next()) {
+        if (!warp_wait<1>(ptx::smem_addr(&ctrl->raw_full[it.stage]), it.phase, wc)) return;
+        const uint32_t src = raw + it.stage * static_cast<uint32_t>(p.raw_bytes);
+        uint4 c[kTasks];
+        uint32_t w[kTasks][8];
 #pragma unroll
-            for (int i = 0; i < kTasks; ++i)
-                if (DGEMM_CHECK(src_off[i] + 16 <= static_cast<uint32_t>(p.raw_bytes)))
-                    c[i] = ld_shared_v4(src + src_off[i]);
+        for (int i = 0; i < kTasks; ++i)
+            if (DGEMM_CHECK((src_off[i] | 64u) + 16 <= static_cast<uint32_t>(p.raw_bytes)))
+                c[i] = ld_shared_v4(src + (src_off[i] ^ (it.half() << 6)));
 #pragma unroll
-            for (int i = 0; i < kTasks; ++i) widen16(c[i], w[i]);
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctrl->raw_empty[stage]));
-            ok = wait_peer<kCtas>(ptx::smem_addr(&ctrl->conv_empty[2 * cs + h]), cphase ^ 1u, wc);
-            if (!__all_sync(0xFFFFFFFFu, ok)) return;
-            const uint32_t dst = conv + (2 * cs + h) * half_bytes;
+        for (int i = 0; i < kTasks; ++i) widen16(c[i], w[i]);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctrl->raw_empty[it.stage]));
+        if (!warp_wait<kCtas>(ptx::smem_addr(&ctrl->conv_empty[it.slot()]), it.slot_phase() ^ 1u, wc)) return;
+        const uint32_t dst = conv + it.slot() * half_bytes;
 #pragma unroll
-            for (int i = 0; i < kTasks; ++i) {
-                if (DGEMM_CHECK((dst_off[i] | 16u) + 16 <= half_bytes)) {
-                    ptx::st_shared_v4(dst + dst_off[i], make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]));
-                    ptx::st_shared_v4(dst + (dst_off[i] ^ 16u), make_uint4(w[i][4], w[i][5], w[i][6], w[i][7]));
-                }
-            }
-            ptx::fence_proxy_async_smem();  // the MMAs read through the async proxy
-            __syncwarp();
-            if (lane == 0) arrive_leader<kCtas>(ptx::smem_addr(&ctrl->conv_full[cs]));
-            if (++cs == kConv) {
-                cs = 0;
-                cphase ^= 1u;
-            }
-            if (++stage == static_cast<uint32_t>(p.raw_stages)) {
-                stage = 0;
-                phase ^= 1u;
+        for (int i = 0; i < kTasks; ++i) {
+            if (DGEMM_CHECK((dst_off[i] | 16u) + 16 <= half_bytes)) {
+                ptx::st_shared_v4(dst + dst_off[i], make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]));
+                ptx::st_shared_v4(dst + (dst_off[i] ^ 16u), make_uint4(w[i][4], w[i][5], w[i][6], w[i][7]));
             }
         }
+        ptx::fence_proxy_async_smem();  // the MMAs read through the async proxy
+        __syncwarp();
+        if (lane == 0) arrive_leader<kCtas>(ptx::smem_addr(&ctrl->conv_full[it.slot()]));
     }
 }
 
-constexpr uint32_t kHandoff = 64;  // warps 1 and 2 on named barriers 1 .. kConv
-constexpr uint32_t kEpiBarrier = 1 + kConv;
-
-// Waits for each converted stage and meets the MMA warp on named barrier
-// 1 + stage, whose OR carries an abort both ways: both sides make the same
-// number of hand-offs whatever happens.
-template <int kCtas>
-__device__ __forceinline__ void run_waiter(const Params &p, Ctrl *ctrl, int lane, WaitCtl *wc)
-{
-    const Sched sc = schedule<kCtas>(p);
-    const int64_t tiles = p.tiles_r * p.tiles_c;
-    uint32_t cs = 0, cphase = 0;
-    bool abort = false;
-    for (int64_t t = sc.t0; t < tiles; t += sc.dt) {
-        for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
-            if (!abort) {
-                bool ok = true;
-                if (lane == 0) ok = wait_peer<kCtas>(ptx::smem_addr(&ctrl->conv_full[cs]), cphase, wc);
-                abort = __shfl_sync(0xFFFFFFFFu, ok ? 0 : 1, 0) != 0;
-            }
-            abort = ptx::bar_red_or(1 + cs, kHandoff, abort);
-            if (++cs == kConv) {
-                cs = 0;
-                cphase ^= 1u;
-            }
-        }
-    }
-}
+constexpr uint32_t kEpiBarrier = 1;  // named barrier of the epilogue warps
 
 template <int kCtas>
-__device__ __forceinline__ void run_mma(const Params &p, uint32_t conv, Ctrl *ctrl, uint32_t tmem_base, int lane,
-                                        WaitCtl *wc)
+__device__ __forceinline__ void run_mma(const Params &p, uint32_t conv, Ctrl *ctrl, uint32_t tmem_base, WaitCtl *wc)
 {
     const Sched sc = schedule<kCtas>(p);
     const int64_t tiles = p.tiles_r * p.tiles_c;
@@ -470,44 +484,39 @@ __device__ __forceinline__ void run_mma(const Params &p, uint32_t conv, Ctrl *ct
     // an MMA's K step 2, in its address field
     const uint64_t b_desc = ptx::smem_desc(conv, 16, 1024, ptx::kSw128);
     tmem_base = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);  // a uniform value for the compiler
-    uint32_t cs = 0, acc = 0, acc_phase = 0;
+    uint32_t cs = 0, cphase = 0, acc = 0, acc_phase = 0;
     // test hook: wait on a barrier nothing arrives at, so the wait runs out
-    bool ok = true;
-    if (lane == 0 && p.inject_stall) ok = wait_bounded(ptx::smem_addr(&ctrl->never), 0, wc);
-    bool abort = __any_sync(0xFFFFFFFFu, !ok);
-    for (int64_t t = sc.t0; t < tiles; t += sc.dt) {
-        if (!abort) {
-            ok = true;
-            if (lane == 0) ok = wait_peer<kCtas>(ptx::smem_addr(&ctrl->acc_empty[acc]), acc_phase ^ 1u, wc);
-            abort = __any_sync(0xFFFFFFFFu, !ok);
-        }
+    bool ok = !p.inject_stall || warp_wait<1>(ptx::smem_addr(&ctrl->never), 0, wc);
+    for (int64_t t = sc.t0; ok && t < tiles; t += sc.dt) {
+        ok = warp_wait<kCtas>(ptx::smem_addr(&ctrl->acc_empty[acc]), acc_phase ^ 1u, wc);
+        if (!ok) break;
         const uint32_t d = tmem_base + acc * kAccCols;
-        uint32_t accumulate = 0;
-        for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
-            abort = __any_sync(0xFFFFFFFFu, ptx::bar_red_or(1 + cs, kHandoff, abort));
-            if (!abort) {
-                ptx::tc_fence_after();
-                if (elect_one()) {
+        const int n = 2 * (sc.kb1 - sc.kb0);
+        for (int i = 0; i < n; ++i) {
+            ok = warp_wait<kCtas>(ptx::smem_addr(&ctrl->conv_full[cs]), cphase, wc);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            if (elect_one()) {
+                const uint32_t a = tmem_base + kConvCol + cs * kConvCols;
+                const uint64_t b = b_desc + cs * (half_bytes >> 4);
 #pragma unroll
-                    for (uint32_t h = 0; h < 2; ++h) {
-                        const uint32_t a = tmem_base + kConvCol + (2 * cs + h) * kConvCols;
-                        const uint64_t b = b_desc + (2 * cs + h) * (half_bytes >> 4);
-#pragma unroll
-                        for (int k = 0; k < kHalfK / 16; ++k)
-                            umma_a_tmem<kCtas>(d, a + k * 8, b + k * 2, idesc, h == 0 && k == 0 ? accumulate : 1u);
-                        commit_all<kCtas>(ptx::smem_addr(&ctrl->conv_empty[2 * cs + h]));
-                    }
-                }
-                __syncwarp();
+                for (int k = 0; k < kHalfK / 16; ++k)
+                    umma_a_tmem<kCtas>(d, a + k * 8, b + k * 2, idesc, i == 0 && k == 0 ? 0u : 1u);
+                commit_all<kCtas>(ptx::smem_addr(&ctrl->conv_empty[cs]));
             }
-            accumulate = 1;
-            if (++cs == kConv) cs = 0;
+            __syncwarp();
+            if (++cs == kConv) {
+                cs = 0;
+                cphase ^= 1u;
+            }
         }
-        if (!abort && elect_one()) commit_all<kCtas>(ptx::smem_addr(&ctrl->acc_full[acc]));
+        if (!ok) break;
+        if (elect_one()) commit_all<kCtas>(ptx::smem_addr(&ctrl->acc_full[acc]));
         __syncwarp();
         acc ^= 1u;
         if (acc == 0) acc_phase ^= 1u;
     }
+    __syncwarp();
     // every MMA this thread issued has finished before TMEM can be released
     // (the elected thread is the same one each time)
     if (elect_one()) {
@@ -555,17 +564,18 @@ __device__ __forceinline__ void drain_tokens(const Params &p, const CUtensorMap 
             __syncwarp();
             const uint32_t dst = buf + static_cast<uint32_t>(lane) * 128u;
 #pragma unroll
-            for (int half = 0; half < kCols / 32; ++half) {
-                uint32_t r[32];
-                ptx::tmem_ld_32x32b_x32(taddr + b * kCols + half * 32, r);
+            for (int part = 0; part < kCols / 16; ++part) {
+                uint32_t r[16];
+                tmem_ld_32x32b_x16(taddr + b * kCols + part * 16, r);
                 ptx::tmem_ld_wait();
                 constexpr int kPer = 16 / sizeof(T);  // values of a 16-byte word
 #pragma unroll
-                for (int j = 0; j < 32 / kPer; ++j) {
+                for (int j = 0; j < 16 / kPer; ++j) {
+                    const int c = part * 16 + j * kPer;
                     float v[kPer];
 #pragma unroll
                     for (int e = 0; e < kPer; e += 4) {
-                        const uint32_t at = static_cast<uint32_t>(b * kCols + half * 32 + j * kPer + e) * 4u;
+                        const uint32_t at = static_cast<uint32_t>(b * kCols + c + e) * 4u;
                         const float4 s = ptx::ld_shared_v4f(scale + at), o = ptx::ld_shared_v4f(bias + at);
                         const uint32_t *a = r + j * kPer + e;
                         v[e] = fmaf(__uint_as_float(a[0]) * sa, s.x, o.x);
@@ -574,10 +584,9 @@ __device__ __forceinline__ void drain_tokens(const Params &p, const CUtensorMap 
                         v[e + 3] = fmaf(__uint_as_float(a[3]) * sa, s.w, o.w);
                     }
                     if (beta != 0.f && row < p.rows) {
-                        const int64_t col = col0 + half * 32 + j * kPer;
 #pragma unroll
                         for (int e = 0; e < kPer; ++e)
-                            if (col + e < p.cols) v[e] = fmaf(beta, i8_to_f32(crow[col + e]), v[e]);
+                            if (col0 + c + e < p.cols) v[e] = fmaf(beta, i8_to_f32(crow[col0 + c + e]), v[e]);
                     }
                     uint4 q;
                     if constexpr (sizeof(T) == 2)
@@ -588,8 +597,8 @@ __device__ __forceinline__ void drain_tokens(const Params &p, const CUtensorMap 
                     else
                         q = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
                                        __float_as_uint(v[3]));
-                    const uint32_t word = static_cast<uint32_t>(half * 32 / kPer + j);
-                    ptx::st_shared_v4(dst + ((word ^ (static_cast<uint32_t>(lane) & 7u)) << 4), q);
+                    ptx::st_shared_v4(dst + ((static_cast<uint32_t>(c / kPer) ^ (static_cast<uint32_t>(lane) & 7u)) << 4),
+                                      q);
                 }
             }
             ptx::fence_proxy_async_smem();  // the TMA store reads through the async proxy
@@ -606,14 +615,19 @@ __device__ __forceinline__ void drain_tokens(const Params &p, const CUtensorMap 
     // row-wise writes and the column-wise reads hit 32 different banks
 #pragma unroll 1
     for (int b = 0; b < p.bn / 32; ++b) {
-        uint32_t r[32];
-        __syncwarp();
-        ptx::tmem_ld_32x32b_x32(taddr + b * 32, r);
-        ptx::tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-            const float v = fmaf(__uint_as_float(r[e]) * sa, ctrl->scale[b * 32 + e], ctrl->bias[b * 32 + e]);
-            ptx::st_shared_f32(box + (static_cast<uint32_t>(lane) * 32u + (static_cast<uint32_t>(e) ^ lane)) * 4u, v);
+        for (int part = 0; part < 2; ++part) {
+            uint32_t r[16];
+            __syncwarp();
+            tmem_ld_32x32b_x16(taddr + b * 32 + part * 16, r);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int e = part * 16 + i;
+                const float v = fmaf(__uint_as_float(r[i]) * sa, ctrl->scale[b * 32 + e], ctrl->bias[b * 32 + e]);
+                ptx::st_shared_f32(box + (static_cast<uint32_t>(lane) * 32u + (static_cast<uint32_t>(e) ^ lane)) * 4u,
+                                   v);
+            }
         }
         __syncwarp();
         const int64_t col = c0 + b * 32 + lane;
@@ -632,21 +646,41 @@ __device__ __forceinline__ void drain_tokens(const Params &p, const CUtensorMap 
 }
 
 // Rows = channels: v[j] is the sum for channel n (this lane's) and token
-// m0 + j; for each token the warp's lanes store consecutive channels.
+// m0 + j, whose scale is at sa[j]; for each token the warp's lanes store
+// consecutive channels.
 template <typename T, int kCount>
-__device__ __forceinline__ void store_channels(const Params &p, int64_t n, int64_t m0, int count, float sb, float bn,
-                                               const float (&v)[kCount])
+__device__ __forceinline__ void store_channels(const Params &p, int64_t n, int64_t m0, const float *sa, float sb,
+                                               float bias, const float (&v)[kCount])
 {
+    const int64_t left = p.cols - m0;
+    T *dst = static_cast<T *>(p.c.C) + m0 * p.c.ldc + n;
+    const bool in = n < p.rows && DGEMM_CHECK(m0 >= 0 && n >= 0);
+    if (p.c.beta != 0.f) {
 #pragma unroll
-    for (int j = 0; j < kCount; ++j) {
-        const int64_t m = m0 + j;
-        if (j < count && m < p.cols && n < p.rows && DGEMM_CHECK(m >= 0 && n >= 0)) {
-            T *dst = static_cast<T *>(p.c.C) + m * p.c.ldc + n;
-            float x = fmaf(v[j] * __ldg(p.c.scale_a + m), sb, bn);
-            if (p.c.beta != 0.f) x = fmaf(p.c.beta, i8_to_f32(*dst), x);
-            *dst = i8_from_f32<T>(x);
-        }
+        for (int j = 0; j < kCount; ++j)
+            if (in && j < left) {
+                T *d = dst + j * p.c.ldc;
+                *d = i8_from_f32<T>(fmaf(p.c.beta, i8_to_f32(*d), fmaf(v[j] * sa[j], sb, bias)));
+            }
+        return;
     }
+#pragma unroll
+    for (int j = 0; j < kCount; ++j)
+        if (in && j < left) dst[j * p.c.ldc] = i8_from_f32<T>(fmaf(v[j] * sa[j], sb, bias));
+}
+
+// The scales (and biases) of the tile's columns, by the 128 epilogue threads;
+// whole warps leave together at the named barrier.
+template <bool kSwap>
+__device__ __forceinline__ void load_column_values(const Params &p, Ctrl *ctrl, int64_t c0, int tid)
+{
+    for (int c = tid; c < p.bn; c += 32 * kEpiWarps) {
+        const bool in = c0 + c < p.cols && c < kMaxBn;
+        ctrl->scale[c] = in ? __ldg((kSwap ? p.c.scale_a : p.c.scale_b) + c0 + c) : 0.f;
+        if constexpr (!kSwap) ctrl->bias[c] = in && p.c.bias ? __ldg(p.c.bias + c0 + c) : 0.f;
+    }
+    __syncwarp();
+    named_barrier(kEpiBarrier, 32 * kEpiWarps);
 }
 
 template <int kCtas, bool kSwap, typename T>
@@ -663,18 +697,10 @@ __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap 
         int64_t r0, c0;
         tile_origin(p, t, kRows * kCtas, r0, c0);
         const int64_t row0 = r0 + rank * kRows + quarter * 32;
-        if constexpr (!kSwap) {
-            __syncwarp();
-            named_barrier(kEpiBarrier, 32 * kEpiWarps);  // the last tile's values have been read
-            for (int c = quarter * 32 + lane; c < p.bn; c += 32 * kEpiWarps) {
-                const bool in = c0 + c < p.cols && c < kMaxBn;
-                ctrl->scale[c] = in ? __ldg(p.c.scale_b + c0 + c) : 0.f;
-                ctrl->bias[c] = in && p.c.bias ? __ldg(p.c.bias + c0 + c) : 0.f;
-            }
-            __syncwarp();
-            named_barrier(kEpiBarrier, 32 * kEpiWarps);
-        }
-        bool ok = wait_peer<kCtas>(ptx::smem_addr(&ctrl->acc_full[acc]), acc_phase, wc);
+        __syncwarp();
+        named_barrier(kEpiBarrier, 32 * kEpiWarps);  // the last tile's values have been read
+        load_column_values<kSwap>(p, ctrl, c0, quarter * 32 + lane);
+        bool ok = warp_wait<kCtas>(ptx::smem_addr(&ctrl->acc_full[acc]), acc_phase, wc);
         // every epilogue warp leaves together, so none waits for another at
         // the named barrier
         __syncwarp();
@@ -698,7 +724,7 @@ __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap 
                 float v[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j >> 3][j & 7]);
-                store_channels<T>(p, n, c0 + b, 16, sb, bias, v);
+                store_channels<T>(p, n, c0 + b, ctrl->scale + b, sb, bias, v);
             }
         }
         ptx::tc_fence_before();
@@ -752,7 +778,7 @@ __device__ __forceinline__ void splitk_push(const Params &p, uint32_t tmem_base,
 }
 
 template <typename T>
-__device__ __forceinline__ void splitk_reduce(const Params &p, uint32_t tmem_base, uint32_t raw, int warp, int lane,
+__device__ __forceinline__ void splitk_reduce(const Params &p, const Ctrl *ctrl, uint32_t tmem_base, uint32_t raw, int warp, int lane,
                                               WaitCtl *wc)
 {
     if (__any_sync(0xFFFFFFFFu, aborted(wc))) return;
@@ -790,13 +816,13 @@ __device__ __forceinline__ void splitk_reduce(const Params &p, uint32_t tmem_bas
                 v[4 * q + 3] += f.w;
             }
         }
-        store_channels<T>(p, n, c0 + g * 8, 8, sb, bias, v);
+        store_channels<T>(p, n, c0 + g * 8, ctrl->scale + g * 8, sb, bias, v);
     }
 }
 
 __host__ __device__ constexpr uint32_t conv_ring_bytes(int bn, int ctas)
 {
-    return static_cast<uint32_t>(2 * kConv * (bn / ctas) * 128);
+    return static_cast<uint32_t>(kConv * (bn / ctas) * 128);
 }
 
 template <int kCtas, bool kSwap, typename T>
@@ -822,9 +848,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(ptx::smem_addr(&ctrl->raw_empty[s]), 16);
         }
         for (int s = 0; s < kConv; ++s) {
-            ptx::mbar_init(ptx::smem_addr(&ctrl->conv_full[s]), 16 * kCtas);
-            ptx::mbar_init(ptx::smem_addr(&ctrl->conv_empty[2 * s]), 1);
-            ptx::mbar_init(ptx::smem_addr(&ctrl->conv_empty[2 * s + 1]), 1);
+            ptx::mbar_init(ptx::smem_addr(&ctrl->conv_full[s]), 8 * kCtas);
+            ptx::mbar_init(ptx::smem_addr(&ctrl->conv_empty[s]), 1);
         }
         for (int a = 0; a < 2; ++a) {
             ptx::mbar_init(ptx::smem_addr(&ctrl->acc_full[a]), 1);
@@ -862,24 +887,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         if (lane == 0) run_producer<kCtas>(&tmap_r, &tmap_c, p, raw, ctrl, rank, wc);
     } else if (warp == 1) {
-        if (leader) run_mma<kCtas>(p, conv, ctrl, tmem_base, lane, wc);
-    } else if (warp == 2) {
-        if (leader) run_waiter<kCtas>(p, ctrl, lane, wc);
-    } else if (warp >= 16) {
-        const int tid = threadIdx.x & 127, h = (warp - 16) >> 2;
+        if (leader) run_mma<kCtas>(p, conv, ctrl, tmem_base, wc);
+    } else if (warp >= 8 + 4 * kConvGroups) {
+        const int tid = threadIdx.x & 127, group = (warp - 8 - 4 * kConvGroups) >> 2;
         switch ((p.bn / kCtas + 31) / 32) {  // chunks a thread takes; uniform
-        case 1: run_col_converter<kCtas, 1>(p, raw, conv, ctrl, tid, h, lane, wc); break;
-        case 2: run_col_converter<kCtas, 2>(p, raw, conv, ctrl, tid, h, lane, wc); break;
-        case 3: run_col_converter<kCtas, 3>(p, raw, conv, ctrl, tid, h, lane, wc); break;
+        case 1: run_col_converter<kCtas, 1>(p, raw, conv, ctrl, tid, group, lane, wc); break;
+        case 2: run_col_converter<kCtas, 2>(p, raw, conv, ctrl, tid, group, lane, wc); break;
+        case 3: run_col_converter<kCtas, 3>(p, raw, conv, ctrl, tid, group, lane, wc); break;
         default:
-            if constexpr (kCtas == 1) run_col_converter<kCtas, 4>(p, raw, conv, ctrl, tid, h, lane, wc);
+            if constexpr (kCtas == 1) run_col_converter<kCtas, 4>(p, raw, conv, ctrl, tid, group, lane, wc);
         }
     } else if (warp >= 8) {
         run_row_converter<kCtas>(p, raw, ctrl, tmem_base, warp, (warp - 8) >> 2, lane, wc);
     } else if (warp >= 4) {
-        if (kCtas == 1 && p.splitk > 1)
+        if (kCtas == 1 && p.splitk > 1) {
+            int64_t r0, c0;
+            tile_origin(p, blockIdx.x / p.splitk, kRows, r0, c0);
+            load_column_values<kSwap>(p, ctrl, c0, threadIdx.x & 127);
             wait_bounded(ptx::smem_addr(&ctrl->acc_full[0]), 0, wc);  // a time-out raises the abort flag
-        else
+        } else
             run_epilogue<kCtas, kSwap, T>(p, &tmap_o, ctrl, tmem_base, box, rank, warp, lane, wc);
     }
 
@@ -892,7 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             ptx::tc_fence_before();
             ptx::cluster_sync();  // every partial has landed in its owner
-            if (warp >= 4 && warp < 8) splitk_reduce<T>(p, tmem_base, raw, warp, lane, wc);
+            if (warp >= 4 && warp < 8) splitk_reduce<T>(p, ctrl, tmem_base, raw, warp, lane, wc);
         }
     }
 
