@@ -70,7 +70,7 @@ constexpr int kHalfK = 64;                      // K values of a converted half
 constexpr int kMaxBn = 192;                     // tile columns
 constexpr int kMaxSplitBn = 128;                // of a single CTA's tile
 constexpr int kMaxRaw = 8;                      // raw stages
-constexpr int kConv = 4;                        // converted halves in flight
+constexpr int kConv = 4;                        // converted halves in flight: two stages
 constexpr int kAccCols = 192;                   // TMEM columns of an accumulator (two of them)
 constexpr int kConvCol = 2 * kAccCols;          // first TMEM column of the converted rows
 constexpr int kConvCols = kHalfK / 2;           // two FP16 values a column
@@ -78,7 +78,7 @@ constexpr int kTmemCols = 512;
 static_assert(kConvCol + kConv * kConvCols <= kTmemCols, "accumulators and converted rows fit in TMEM");
 constexpr int kBoxBytes = 4096;                 // epilogue staging: 32 rows x 128 bytes
 constexpr int kEpiWarps = 4;
-constexpr int kConvGroups = 3;                  // converter groups of four warps, of either kind
+constexpr int kConvGroups = 2;                  // converter groups of four warps, of either kind: one a half
 constexpr int kThreads = 32 * (8 + 2 * 4 * kConvGroups);
 static_assert(kThreads <= 1024, "one CTA");
 constexpr int kSmemLimit = 227 * 1024;
@@ -86,7 +86,7 @@ constexpr int kSmemLimit = 227 * 1024;
 struct Ctrl {
     uint64_t raw_full[kMaxRaw];    // a raw stage has landed
     uint64_t raw_empty[kMaxRaw];   // its 16 converter warps have read it
-    uint64_t conv_full[kConv];     // leader: every converter warp of the pair has stored its part of the half
+    uint64_t conv_full[kConv / 2];  // leader: every converter warp of the pair has stored its part of the stage
     uint64_t conv_empty[kConv];    // the MMAs have read this converted half
     uint64_t acc_full[2];
     uint64_t acc_empty[2];         // leader: every epilogue warp of the pair has read the accumulator
@@ -350,42 +350,35 @@ __device__ __forceinline__ void arrive_leader(uint32_t bar)
         ptx::mbar_arrive(bar);
 }
 
-// A converter group's walk over the halves of the CTA's raw stages, in the
-// order the producer fills them: halves group, group + 3, ...
+// A converter group's walk over half `half` of each of the CTA's raw stages, in
+// the order the producer fills them.
 struct HalfIter {
-    int64_t i, end;          // half index over all of the CTA's tiles
-    uint32_t stage, phase;   // of the raw ring
+    uint32_t left;          // stages to go
+    uint32_t stage, phase;  // of the raw ring
+    uint32_t slot;          // where the half is converted to
+    uint32_t slot_phase;
     uint32_t stages;
 
-    __device__ __forceinline__ HalfIter(const Params &p, const Sched &sc, int group)
+    __device__ __forceinline__ HalfIter(const Params &p, const Sched &sc, uint32_t half)
     {
         const int64_t tiles = p.tiles_r * p.tiles_c;
         const int64_t mine = sc.t0 < tiles ? (tiles - sc.t0 + sc.dt - 1) / sc.dt : 0;
-        i = group;
-        end = mine * (sc.kb1 - sc.kb0) * 2;
+        left = static_cast<uint32_t>(mine * (sc.kb1 - sc.kb0));
         stages = static_cast<uint32_t>(p.raw_stages);
-        stage = 0;
-        phase = 0;
-        step(static_cast<uint32_t>(group) >> 1);
+        stage = phase = slot_phase = 0;
+        slot = half;
     }
-    __device__ __forceinline__ void step(uint32_t n)
-    {
-        stage += n;
-        if (stage >= stages) {
-            stage -= stages;
-            phase ^= 1u;
-        }
-    }
-    __device__ __forceinline__ bool more() const { return i < end; }
+    __device__ __forceinline__ bool more() const { return left != 0; }
     __device__ __forceinline__ void next()
     {
-        step(static_cast<uint32_t>(((i + kConvGroups) >> 1) - (i >> 1)));
-        i += kConvGroups;
+        --left;
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+        if (slot >= 2) slot_phase ^= 1u;
+        slot ^= 2u;
     }
-    __device__ __forceinline__ uint32_t half() const { return static_cast<uint32_t>(i) & 1u; }
-    // where the half is converted to, and that slot's phase
-    __device__ __forceinline__ uint32_t slot() const { return static_cast<uint32_t>(i) % kConv; }
-    __device__ __forceinline__ uint32_t slot_phase() const { return static_cast<uint32_t>(i / kConv) & 1u; }
 };
 
 // Row converters: thread = row.  A raw row is 128 bytes, its 16-byte chunk j
@@ -393,29 +386,29 @@ struct HalfIter {
 // wavefront read distinct banks.
 template <int kCtas>
 __device__ __forceinline__ void run_row_converter(const Params &p, uint32_t raw, Ctrl *ctrl, uint32_t tmem_base,
-                                                  int warp, int group, int lane, WaitCtl *wc)
+                                                  int warp, uint32_t half, int lane, WaitCtl *wc)
 {
     const uint32_t quarter = static_cast<uint32_t>(warp & 3);
     const uint32_t row = quarter * 32 + lane;
     const uint32_t lanes = tmem_base + ((quarter * 32u) << 16) + kConvCol;
-    for (HalfIter it(p, schedule<kCtas>(p), group); it.more(); it.next()) {
+    for (HalfIter it(p, schedule<kCtas>(p), half); it.more(); it.next()) {
         if (!warp_wait<1>(ptx::smem_addr(&ctrl->raw_full[it.stage]), it.phase, wc)) return;
         const uint32_t src = raw + it.stage * static_cast<uint32_t>(p.raw_bytes) + row * kRowBytes;
         uint4 c[4];
 #pragma unroll
-        for (uint32_t j = 0; j < 4; ++j) c[j] = ld_shared_v4(src + (((it.half() * 4 + j) ^ (row & 7u)) << 4));
+        for (uint32_t j = 0; j < 4; ++j) c[j] = ld_shared_v4(src + (((half * 4 + j) ^ (row & 7u)) << 4));
         uint32_t w[32];
 #pragma unroll
         for (int j = 0; j < 4; ++j) widen16(c[j], w + j * 8);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctrl->raw_empty[it.stage]));
-        if (!warp_wait<kCtas>(ptx::smem_addr(&ctrl->conv_empty[it.slot()]), it.slot_phase() ^ 1u, wc)) return;
+        if (!warp_wait<kCtas>(ptx::smem_addr(&ctrl->conv_empty[it.slot]), it.slot_phase ^ 1u, wc)) return;
         ptx::tc_fence_after();
-        ptx::tmem_st_32x32b_x32(lanes + it.slot() * kConvCols, w);
+        ptx::tmem_st_32x32b_x32(lanes + it.slot * kConvCols, w);
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_leader<kCtas>(ptx::smem_addr(&ctrl->conv_full[it.slot()]));
+        if (lane == 0) arrive_leader<kCtas>(ptx::smem_addr(&ctrl->conv_full[it.slot >> 1]));
     }
 }
 
@@ -426,7 +419,7 @@ __device__ __forceinline__ void run_row_converter(const Params &p, uint32_t raw,
 // widened column is a 128-byte K-major row under the 128-byte swizzle.
 template <int kCtas, int kTasks>
 __device__ __forceinline__ void run_col_converter(const Params &p, uint32_t raw, uint32_t conv, Ctrl *ctrl, int tid,
-                                                  int group, int lane, WaitCtl *wc)
+                                                  uint32_t half, int lane, WaitCtl *wc)
 {
     const int cols = p.bn / kCtas;
     const uint32_t half_bytes = static_cast<uint32_t>(cols) * 128u;
@@ -441,7 +434,7 @@ __device__ __forceinline__ void run_col_converter(const Params &p, uint32_t raw,
         src_off[i] = kRawRowsBytes + col * kRowBytes + ((j ^ (col & 7u)) << 4);
         dst_off[i] = col * 128u + (((2 * j) ^ (col & 7u)) << 4);
     }
-    for (HalfIter it(p, schedule<kCtas>(p), group); it.more(); it.next()) {
+    for (HalfIter it(p, schedule<kCtas>(p), half); it.more(); it.next()) {
         if (!warp_wait<1>(ptx::smem_addr(&ctrl->raw_full[it.stage]), it.phase, wc)) return;
         const uint32_t src = raw + it.stage * static_cast<uint32_t>(p.raw_bytes);
         uint4 c[kTasks];
@@ -449,13 +442,13 @@ __device__ __forceinline__ void run_col_converter(const Params &p, uint32_t raw,
 #pragma unroll
         for (int i = 0; i < kTasks; ++i)
             if (DGEMM_CHECK((src_off[i] | 64u) + 16 <= static_cast<uint32_t>(p.raw_bytes)))
-                c[i] = ld_shared_v4(src + (src_off[i] ^ (it.half() << 6)));
+                c[i] = ld_shared_v4(src + (src_off[i] ^ (half << 6)));
 #pragma unroll
         for (int i = 0; i < kTasks; ++i) widen16(c[i], w[i]);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctrl->raw_empty[it.stage]));
-        if (!warp_wait<kCtas>(ptx::smem_addr(&ctrl->conv_empty[it.slot()]), it.slot_phase() ^ 1u, wc)) return;
-        const uint32_t dst = conv + it.slot() * half_bytes;
+        if (!warp_wait<kCtas>(ptx::smem_addr(&ctrl->conv_empty[it.slot]), it.slot_phase ^ 1u, wc)) return;
+        const uint32_t dst = conv + it.slot * half_bytes;
 #pragma unroll
         for (int i = 0; i < kTasks; ++i) {
             if (DGEMM_CHECK((dst_off[i] | 16u) + 16 <= half_bytes)) {
@@ -465,7 +458,7 @@ __device__ __forceinline__ void run_col_converter(const Params &p, uint32_t raw,
         }
         ptx::fence_proxy_async_smem();  // the MMAs read through the async proxy
         __syncwarp();
-        if (lane == 0) arrive_leader<kCtas>(ptx::smem_addr(&ctrl->conv_full[it.slot()]));
+        if (lane == 0) arrive_leader<kCtas>(ptx::smem_addr(&ctrl->conv_full[it.slot >> 1]));
     }
 }
 
@@ -491,24 +484,24 @@ __device__ __forceinline__ void run_mma(const Params &p, uint32_t conv, Ctrl *ct
         ok = warp_wait<kCtas>(ptx::smem_addr(&ctrl->acc_empty[acc]), acc_phase ^ 1u, wc);
         if (!ok) break;
         const uint32_t d = tmem_base + acc * kAccCols;
-        const int n = 2 * (sc.kb1 - sc.kb0);
-        for (int i = 0; i < n; ++i) {
+        for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
             ok = warp_wait<kCtas>(ptx::smem_addr(&ctrl->conv_full[cs]), cphase, wc);
             if (!ok) break;
             ptx::tc_fence_after();
             if (elect_one()) {
-                const uint32_t a = tmem_base + kConvCol + cs * kConvCols;
-                const uint64_t b = b_desc + cs * (half_bytes >> 4);
 #pragma unroll
-                for (int k = 0; k < kHalfK / 16; ++k)
-                    umma_a_tmem<kCtas>(d, a + k * 8, b + k * 2, idesc, i == 0 && k == 0 ? 0u : 1u);
-                commit_all<kCtas>(ptx::smem_addr(&ctrl->conv_empty[cs]));
+                for (uint32_t h = 0; h < 2; ++h) {
+                    const uint32_t a = tmem_base + kConvCol + (2 * cs + h) * kConvCols;
+                    const uint64_t b = b_desc + (2 * cs + h) * (half_bytes >> 4);
+#pragma unroll
+                    for (int k = 0; k < kHalfK / 16; ++k)
+                        umma_a_tmem<kCtas>(d, a + k * 8, b + k * 2, idesc, kb == sc.kb0 && h == 0 && k == 0 ? 0u : 1u);
+                    commit_all<kCtas>(ptx::smem_addr(&ctrl->conv_empty[2 * cs + h]));
+                }
             }
             __syncwarp();
-            if (++cs == kConv) {
-                cs = 0;
-                cphase ^= 1u;
-            }
+            cphase ^= cs;
+            cs ^= 1u;
         }
         if (!ok) break;
         if (elect_one()) commit_all<kCtas>(ptx::smem_addr(&ctrl->acc_full[acc]));
@@ -847,10 +840,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(ptx::smem_addr(&ctrl->raw_full[s]), 1);
             ptx::mbar_init(ptx::smem_addr(&ctrl->raw_empty[s]), 16);
         }
-        for (int s = 0; s < kConv; ++s) {
-            ptx::mbar_init(ptx::smem_addr(&ctrl->conv_full[s]), 8 * kCtas);
-            ptx::mbar_init(ptx::smem_addr(&ctrl->conv_empty[s]), 1);
-        }
+        for (int s = 0; s < kConv / 2; ++s) ptx::mbar_init(ptx::smem_addr(&ctrl->conv_full[s]), 16 * kCtas);
+        for (int s = 0; s < kConv; ++s) ptx::mbar_init(ptx::smem_addr(&ctrl->conv_empty[s]), 1);
         for (int a = 0; a < 2; ++a) {
             ptx::mbar_init(ptx::smem_addr(&ctrl->acc_full[a]), 1);
             ptx::mbar_init(ptx::smem_addr(&ctrl->acc_empty[a]), kEpiWarps * kCtas);
@@ -889,13 +880,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         if (leader) run_mma<kCtas>(p, conv, ctrl, tmem_base, wc);
     } else if (warp >= 8 + 4 * kConvGroups) {
-        const int tid = threadIdx.x & 127, group = (warp - 8 - 4 * kConvGroups) >> 2;
+        const int tid = threadIdx.x & 127, half = (warp - 8 - 4 * kConvGroups) >> 2;
         switch ((p.bn / kCtas + 31) / 32) {  // chunks a thread takes; uniform
-        case 1: run_col_converter<kCtas, 1>(p, raw, conv, ctrl, tid, group, lane, wc); break;
-        case 2: run_col_converter<kCtas, 2>(p, raw, conv, ctrl, tid, group, lane, wc); break;
-        case 3: run_col_converter<kCtas, 3>(p, raw, conv, ctrl, tid, group, lane, wc); break;
+        case 1: run_col_converter<kCtas, 1>(p, raw, conv, ctrl, tid, half, lane, wc); break;
+        case 2: run_col_converter<kCtas, 2>(p, raw, conv, ctrl, tid, half, lane, wc); break;
+        case 3: run_col_converter<kCtas, 3>(p, raw, conv, ctrl, tid, half, lane, wc); break;
         default:
-            if constexpr (kCtas == 1) run_col_converter<kCtas, 4>(p, raw, conv, ctrl, tid, group, lane, wc);
+            if constexpr (kCtas == 1) run_col_converter<kCtas, 4>(p, raw, conv, ctrl, tid, half, lane, wc);
         }
     } else if (warp >= 8) {
         run_row_converter<kCtas>(p, raw, ctrl, tmem_base, warp, (warp - 8) >> 2, lane, wc);
