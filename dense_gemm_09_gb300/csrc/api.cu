@@ -71,7 +71,7 @@ int checks_failed(int clear, int *site)
 {
     int (*const readers[])(int, int *) = {check_status_simt, check_status_tma, check_status_umma,
                                           check_status_scale, check_status_repack, check_status_i8_rows,
-                                          check_status_i8_gemm, check_status_i8_umma};
+                                          check_status_i8_gemm, check_status_i8_umma, check_status_i8_decode};
     int status = DGEMM_OK, where = 0;
     for (auto rd : readers) {
         int s = 0;

@@ -211,8 +211,15 @@ const char *config_name(const I8Config &c)
             for (int S = 1; S <= 8; ++S) names[w][S][0] = "i8_umma_128x" + bn + "_channels_split" + std::to_string(S);
         }
     });
+    if (c.variant == kI8Decode) return c.split == 8 ? "i8_decode_16_channels_8_warps" : "i8_decode_16_channels_16_warps";
     if (c.variant == kI8Split) return names[c.bn / 16][c.split][0].c_str();
     return names[c.bn / 16][0][c.variant == kI8PairChannels ? 1 : 0].c_str();
+}
+
+bool launch_config(const I8Params &p, int c_type, const I8Config &cfg, cudaStream_t stream)
+{
+    return cfg.variant == kI8Decode ? launch_i8_decode(p, c_type, cfg.split, stream)
+                                    : launch_i8_umma(p, c_type, cfg, stream);
 }
 
 }  // namespace
@@ -226,9 +233,9 @@ const char *launch_gemm_i8(const I8Params &q, int c_type, cudaStream_t stream, c
     I8Config cfg = t_tune;
     t_tune = {kI8Auto, 0, 1};
     if (tma_ok(p) && cfg.variant != kI8Mma) {
-        if (cfg.variant != kI8Auto && launch_i8_umma(p, c_type, cfg, stream)) return config_name(cfg);
+        if (cfg.variant != kI8Auto && launch_config(p, c_type, cfg, stream)) return config_name(cfg);
         cfg = choose_config(p, dev.sm_count);
-        if (launch_i8_umma(p, c_type, cfg, stream)) return config_name(cfg);
+        if (launch_config(p, c_type, cfg, stream)) return config_name(cfg);
     }
     switch (c_type) {
     case DGEMM_TYPE_F32: return launch_mma<float>(p, stream);
@@ -241,7 +248,9 @@ const char *launch_gemm_i8(const I8Params &q, int c_type, cudaStream_t stream, c
 int i8_tune_next(int variant, int bn, int split)
 {
     const I8Config cfg{variant, bn, split};
-    if (variant != kI8Auto && variant != kI8Mma && !i8_umma_config_ok(cfg)) return DGEMM_ERR_INVALID_ARG;
+    const bool ok = variant == kI8Auto || variant == kI8Mma || i8_umma_config_ok(cfg) ||
+                    (variant == kI8Decode && (split == 8 || split == 16));
+    if (!ok) return DGEMM_ERR_INVALID_ARG;
     t_tune = cfg;
     return DGEMM_OK;
 }

@@ -30,9 +30,9 @@
 //   warp 1       MMA issuer: four tcgen05.mma of K = 16 a half, then a commit that
 //                releases the half;
 //   warps 4-7    epilogue: accumulator -> scale, bias, beta -> C.
-// Four halves are in flight between converters and MMAs.  A converter reads and widens
-// its part of a stage into registers before it waits for the MMAs of
-// four halves ago, so that only the store, the hand-off and the commit lie
+// Two to four converted stages are in flight.  A converter reads and widens
+// its part of a stage into registers before it waits for the
+// half's last MMAs, so that only the store, the hand-off and the commit lie
 // between the release of a half and its next use.  A half takes a converter
 // group ~700 clocks from its first wait to its arrival, nearly all of it
 // latency; three groups keep a stage at 2/3 of that.
@@ -70,12 +70,10 @@ constexpr int kHalfK = 64;                      // K values of a converted half
 constexpr int kMaxBn = 192;                     // tile columns
 constexpr int kMaxSplitBn = 128;                // of a single CTA's tile
 constexpr int kMaxRaw = 8;                      // raw stages
-constexpr int kConv = 4;                        // converted halves in flight: two stages
-constexpr int kAccCols = 192;                   // TMEM columns of an accumulator (two of them)
-constexpr int kConvCol = 2 * kAccCols;          // first TMEM column of the converted rows
-constexpr int kConvCols = kHalfK / 2;           // two FP16 values a column
-constexpr int kTmemCols = 512;
-static_assert(kConvCol + kConv * kConvCols <= kTmemCols, "accumulators and converted rows fit in TMEM");
+constexpr int kMaxConv = 4;                     // converted stages, of two halves each
+constexpr int kConvCols = kHalfK / 2;           // TMEM columns of a half's rows: two FP16 values a column
+constexpr int kTmemCols = 512;                  // two accumulators of bn columns, then the converted rows
+static_assert(2 * kMaxBn + 2 * 2 * kConvCols <= kTmemCols, "two converted stages fit beside any accumulators");
 constexpr int kBoxBytes = 4096;                 // epilogue staging: 32 rows x 128 bytes
 constexpr int kEpiWarps = 4;
 constexpr int kConvGroups = 2;                  // converter groups of four warps, of either kind: one a half
@@ -86,8 +84,8 @@ constexpr int kSmemLimit = 227 * 1024;
 struct Ctrl {
     uint64_t raw_full[kMaxRaw];    // a raw stage has landed
     uint64_t raw_empty[kMaxRaw];   // its 16 converter warps have read it
-    uint64_t conv_full[kConv / 2];  // leader: every converter warp of the pair has stored its part of the stage
-    uint64_t conv_empty[kConv];    // the MMAs have read this converted half
+    uint64_t conv_full[kMaxConv];  // leader: every converter warp of the pair has stored its part of the stage
+    uint64_t conv_empty[2 * kMaxConv];  // the MMAs have read this converted half
     uint64_t acc_full[2];
     uint64_t acc_empty[2];         // leader: every epilogue warp of the pair has read the accumulator
     uint64_t mma_done;
@@ -105,6 +103,7 @@ struct Params {
     int bn;                        // tile columns; a CTA of a pair converts half of them
     int num_kb;                    // K blocks of 128
     int raw_stages, raw_bytes;
+    int conv_stages;               // 2 .. kMaxConv
     int splitk;                    // CTAs of a cluster that share a tile (single CTAs)
     int tma_store;
     uint64_t wait_limit_ns;
@@ -308,36 +307,39 @@ __device__ __forceinline__ void run_producer(const CUtensorMap *tmap_r, const CU
     const Sched sc = schedule<kCtas>(p);
     const int64_t tiles = p.tiles_r * p.tiles_c;
     const int cols = p.bn / kCtas;  // columns this CTA converts
-    uint32_t stage = 0, phase = 0, issued = 0, issued_phase = 0;
+    uint32_t stage = 0, phase = 0;
     bool ok = true;
     for (int64_t t = sc.t0; ok && t < tiles; t += sc.dt) {
         int64_t r0, c0;
         tile_origin(p, t, kRows * kCtas, r0, c0);
+        const int32_t rr = static_cast<int32_t>(r0 + rank * kRows), cc = static_cast<int32_t>(c0 + rank * cols);
         for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
-            if (!wait_bounded(ptx::smem_addr(&ctrl->raw_empty[stage]), phase ^ 1u, wc)) {
-                ok = false;
-                break;
+            ok = warp_wait<1>(ptx::smem_addr(&ctrl->raw_empty[stage]), phase ^ 1u, wc);
+            if (!ok) break;
+            if (elect_one()) {
+                const uint32_t full = ptx::smem_addr(&ctrl->raw_full[stage]);
+                const uint32_t dst = raw + stage * static_cast<uint32_t>(p.raw_bytes);
+                ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(p.raw_bytes));
+                // the innermost coordinate is a multiple of 128 bytes
+                ptx::tma_load_2d(dst, tmap_r, full, kb * kRowBytes, rr);
+                ptx::tma_load_2d(dst + kRawRowsBytes, tmap_c, full, kb * kRowBytes, cc);
             }
-            const uint32_t full = ptx::smem_addr(&ctrl->raw_full[stage]);
-            const uint32_t dst = raw + stage * static_cast<uint32_t>(p.raw_bytes);
-            ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(p.raw_bytes));
-            // the innermost coordinate is a multiple of 128 bytes
-            ptx::tma_load_2d(dst, tmap_r, full, kb * kRowBytes, static_cast<int32_t>(r0 + rank * kRows));
-            ptx::tma_load_2d(dst + kRawRowsBytes, tmap_c, full, kb * kRowBytes,
-                             static_cast<int32_t>(c0 + rank * cols));
-            issued |= 1u << stage;
-            issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+            __syncwarp();
             if (++stage == static_cast<uint32_t>(p.raw_stages)) {
                 stage = 0;
                 phase ^= 1u;
             }
         }
     }
-    if (!ok) {
-        // do not leave while TMA may still be writing into this CTA's memory
-        for (int s = 0; s < p.raw_stages; ++s)
-            if ((issued >> s) & 1u) drain_wait(ptx::smem_addr(&ctrl->raw_full[s]), (issued_phase >> s) & 1u);
+    if (!ok && elect_one()) {
+        // Do not leave while TMA may still be writing into this CTA's memory:
+        // stages before `stage` were last filled in this phase, the others (if
+        // at all: a barrier's phase 1 counts as over before its first) in the one
+        // before.
+        for (uint32_t s = 0; s < static_cast<uint32_t>(p.raw_stages); ++s)
+            drain_wait(ptx::smem_addr(&ctrl->raw_full[s]), s < stage ? phase : phase ^ 1u);
     }
+    __syncwarp();
 }
 
 // A converter warp's arrival on a barrier of the pair's leader.
@@ -350,23 +352,22 @@ __device__ __forceinline__ void arrive_leader(uint32_t bar)
         ptx::mbar_arrive(bar);
 }
 
-// A converter group's walk over half `half` of each of the CTA's raw stages, in
-// the order the producer fills them.
+// A converter group's walk over the CTA's raw stages, in the order the producer
+// fills them, and the converted stages they go to.
 struct HalfIter {
     uint32_t left;          // stages to go
     uint32_t stage, phase;  // of the raw ring
-    uint32_t slot;          // where the half is converted to
-    uint32_t slot_phase;
-    uint32_t stages;
+    uint32_t conv, conv_phase;  // converted stage
+    uint32_t stages, conv_stages;
 
-    __device__ __forceinline__ HalfIter(const Params &p, const Sched &sc, uint32_t half)
+    __device__ __forceinline__ HalfIter(const Params &p, const Sched &sc)
     {
         const int64_t tiles = p.tiles_r * p.tiles_c;
         const int64_t mine = sc.t0 < tiles ? (tiles - sc.t0 + sc.dt - 1) / sc.dt : 0;
         left = static_cast<uint32_t>(mine * (sc.kb1 - sc.kb0));
         stages = static_cast<uint32_t>(p.raw_stages);
-        stage = phase = slot_phase = 0;
-        slot = half;
+        conv_stages = static_cast<uint32_t>(p.conv_stages);
+        stage = phase = conv = conv_phase = 0;
     }
     __device__ __forceinline__ bool more() const { return left != 0; }
     __device__ __forceinline__ void next()
@@ -376,8 +377,10 @@ struct HalfIter {
             stage = 0;
             phase ^= 1u;
         }
-        if (slot >= 2) slot_phase ^= 1u;
-        slot ^= 2u;
+        if (++conv == conv_stages) {
+            conv = 0;
+            conv_phase ^= 1u;
+        }
     }
 };
 
@@ -390,8 +393,8 @@ __device__ __forceinline__ void run_row_converter(const Params &p, uint32_t raw,
 {
     const uint32_t quarter = static_cast<uint32_t>(warp & 3);
     const uint32_t row = quarter * 32 + lane;
-    const uint32_t lanes = tmem_base + ((quarter * 32u) << 16) + kConvCol;
-    for (HalfIter it(p, schedule<kCtas>(p), half); it.more(); it.next()) {
+    const uint32_t lanes = tmem_base + ((quarter * 32u) << 16) + 2 * static_cast<uint32_t>(p.bn) + half * kConvCols;
+    for (HalfIter it(p, schedule<kCtas>(p)); it.more(); it.next()) {
         if (!warp_wait<1>(ptx::smem_addr(&ctrl->raw_full[it.stage]), it.phase, wc)) return;
         const uint32_t src = raw + it.stage * static_cast<uint32_t>(p.raw_bytes) + row * kRowBytes;
         uint4 c[4];
@@ -402,13 +405,13 @@ __device__ __forceinline__ void run_row_converter(const Params &p, uint32_t raw,
         for (int j = 0; j < 4; ++j) widen16(c[j], w + j * 8);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctrl->raw_empty[it.stage]));
-        if (!warp_wait<kCtas>(ptx::smem_addr(&ctrl->conv_empty[it.slot]), it.slot_phase ^ 1u, wc)) return;
+        if (!warp_wait<kCtas>(ptx::smem_addr(&ctrl->conv_empty[2 * it.conv + half]), it.conv_phase ^ 1u, wc)) return;
         ptx::tc_fence_after();
-        ptx::tmem_st_32x32b_x32(lanes + it.slot * kConvCols, w);
+        ptx::tmem_st_32x32b_x32(lanes + it.conv * 2 * kConvCols, w);
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_leader<kCtas>(ptx::smem_addr(&ctrl->conv_full[it.slot >> 1]));
+        if (lane == 0) arrive_leader<kCtas>(ptx::smem_addr(&ctrl->conv_full[it.conv]));
     }
 }
 
@@ -434,7 +437,7 @@ __device__ __forceinline__ void run_col_converter(const Params &p, uint32_t raw,
         src_off[i] = kRawRowsBytes + col * kRowBytes + ((j ^ (col & 7u)) << 4);
         dst_off[i] = col * 128u + (((2 * j) ^ (col & 7u)) << 4);
     }
-    for (HalfIter it(p, schedule<kCtas>(p), half); it.more(); it.next()) {
+    for (HalfIter it(p, schedule<kCtas>(p)); it.more(); it.next()) {
         if (!warp_wait<1>(ptx::smem_addr(&ctrl->raw_full[it.stage]), it.phase, wc)) return;
         const uint32_t src = raw + it.stage * static_cast<uint32_t>(p.raw_bytes);
         uint4 c[kTasks];
@@ -447,8 +450,8 @@ __device__ __forceinline__ void run_col_converter(const Params &p, uint32_t raw,
         for (int i = 0; i < kTasks; ++i) widen16(c[i], w[i]);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctrl->raw_empty[it.stage]));
-        if (!warp_wait<kCtas>(ptx::smem_addr(&ctrl->conv_empty[it.slot]), it.slot_phase ^ 1u, wc)) return;
-        const uint32_t dst = conv + it.slot * half_bytes;
+        if (!warp_wait<kCtas>(ptx::smem_addr(&ctrl->conv_empty[2 * it.conv + half]), it.conv_phase ^ 1u, wc)) return;
+        const uint32_t dst = conv + (2 * it.conv + half) * half_bytes;
 #pragma unroll
         for (int i = 0; i < kTasks; ++i) {
             if (DGEMM_CHECK((dst_off[i] | 16u) + 16 <= half_bytes)) {
@@ -458,7 +461,7 @@ __device__ __forceinline__ void run_col_converter(const Params &p, uint32_t raw,
         }
         ptx::fence_proxy_async_smem();  // the MMAs read through the async proxy
         __syncwarp();
-        if (lane == 0) arrive_leader<kCtas>(ptx::smem_addr(&ctrl->conv_full[it.slot >> 1]));
+        if (lane == 0) arrive_leader<kCtas>(ptx::smem_addr(&ctrl->conv_full[it.conv]));
     }
 }
 
@@ -477,13 +480,14 @@ __device__ __forceinline__ void run_mma(const Params &p, uint32_t conv, Ctrl *ct
     // an MMA's K step 2, in its address field
     const uint64_t b_desc = ptx::smem_desc(conv, 16, 1024, ptx::kSw128);
     tmem_base = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);  // a uniform value for the compiler
+    const uint32_t a_base = tmem_base + 2 * static_cast<uint32_t>(p.bn);
     uint32_t cs = 0, cphase = 0, acc = 0, acc_phase = 0;
     // test hook: wait on a barrier nothing arrives at, so the wait runs out
     bool ok = !p.inject_stall || warp_wait<1>(ptx::smem_addr(&ctrl->never), 0, wc);
     for (int64_t t = sc.t0; ok && t < tiles; t += sc.dt) {
         ok = warp_wait<kCtas>(ptx::smem_addr(&ctrl->acc_empty[acc]), acc_phase ^ 1u, wc);
         if (!ok) break;
-        const uint32_t d = tmem_base + acc * kAccCols;
+        const uint32_t d = tmem_base + acc * static_cast<uint32_t>(p.bn);
         for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
             ok = warp_wait<kCtas>(ptx::smem_addr(&ctrl->conv_full[cs]), cphase, wc);
             if (!ok) break;
@@ -491,7 +495,7 @@ __device__ __forceinline__ void run_mma(const Params &p, uint32_t conv, Ctrl *ct
             if (elect_one()) {
 #pragma unroll
                 for (uint32_t h = 0; h < 2; ++h) {
-                    const uint32_t a = tmem_base + kConvCol + (2 * cs + h) * kConvCols;
+                    const uint32_t a = a_base + (2 * cs + h) * kConvCols;
                     const uint64_t b = b_desc + (2 * cs + h) * (half_bytes >> 4);
 #pragma unroll
                     for (int k = 0; k < kHalfK / 16; ++k)
@@ -500,8 +504,10 @@ __device__ __forceinline__ void run_mma(const Params &p, uint32_t conv, Ctrl *ct
                 }
             }
             __syncwarp();
-            cphase ^= cs;
-            cs ^= 1u;
+            if (++cs == static_cast<uint32_t>(p.conv_stages)) {
+                cs = 0;
+                cphase ^= 1u;
+            }
         }
         if (!ok) break;
         if (elect_one()) commit_all<kCtas>(ptx::smem_addr(&ctrl->acc_full[acc]));
@@ -546,7 +552,7 @@ __device__ __forceinline__ void drain_tokens(const Params &p, const CUtensorMap 
     const float beta = p.c.beta;
     const uint32_t scale = ptx::smem_addr(ctrl->scale), bias = ptx::smem_addr(ctrl->bias);
     T *crow = static_cast<T *>(p.c.C) + row * p.c.ldc;
-    if (!DGEMM_CHECK((taddr & 0xFFFFu) + static_cast<uint32_t>(p.bn) <= static_cast<uint32_t>(kConvCol))) return;
+    if (!DGEMM_CHECK((taddr & 0xFFFFu) + static_cast<uint32_t>(p.bn) <= 2u * static_cast<uint32_t>(p.bn))) return;
     if (p.tma_store) {
 #pragma unroll 1
         for (int b = 0; b < p.bn / kCols; ++b) {
@@ -700,7 +706,7 @@ __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap 
         ok = !ptx::bar_red_or(kEpiBarrier, 32 * kEpiWarps, !ok);
         if (!ok) break;
         ptx::tc_fence_after();
-        const uint32_t taddr = tmem_base + ((quarter * 32u) << 16) + acc * kAccCols;
+        const uint32_t taddr = tmem_base + ((quarter * 32u) << 16) + acc * static_cast<uint32_t>(p.bn);
         if constexpr (!kSwap) {
             drain_tokens<T>(p, tmap_o, ctrl, taddr, row0, c0, box, lane, nbox);
         } else {
@@ -813,11 +819,6 @@ __device__ __forceinline__ void splitk_reduce(const Params &p, const Ctrl *ctrl,
     }
 }
 
-__host__ __device__ constexpr uint32_t conv_ring_bytes(int bn, int ctas)
-{
-    return static_cast<uint32_t>(kConv * (bn / ctas) * 128);
-}
-
 template <int kCtas, bool kSwap, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     i8_umma_kernel(const __grid_constant__ CUtensorMap tmap_r, const __grid_constant__ CUtensorMap tmap_c,
@@ -828,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                 ~static_cast<uintptr_t>(1023));
     // converted columns | epilogue boxes (kSwap: none) | raw ring | control
     const uint32_t conv = ptx::smem_addr(smem);
-    const uint32_t box = conv + conv_ring_bytes(p.bn, kCtas);
+    const uint32_t box = conv + static_cast<uint32_t>(p.conv_stages * 2 * (p.bn / kCtas) * 128);
     const uint32_t raw = box + (kSwap ? 0 : kEpiWarps * 2 * kBoxBytes);
     Ctrl *ctrl = reinterpret_cast<Ctrl *>(smem + (raw - conv) + p.raw_stages * p.raw_bytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -840,8 +841,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(ptx::smem_addr(&ctrl->raw_full[s]), 1);
             ptx::mbar_init(ptx::smem_addr(&ctrl->raw_empty[s]), 16);
         }
-        for (int s = 0; s < kConv / 2; ++s) ptx::mbar_init(ptx::smem_addr(&ctrl->conv_full[s]), 16 * kCtas);
-        for (int s = 0; s < kConv; ++s) ptx::mbar_init(ptx::smem_addr(&ctrl->conv_empty[s]), 1);
+        for (int s = 0; s < kMaxConv; ++s) ptx::mbar_init(ptx::smem_addr(&ctrl->conv_full[s]), 16 * kCtas);
+        for (int s = 0; s < 2 * kMaxConv; ++s) ptx::mbar_init(ptx::smem_addr(&ctrl->conv_empty[s]), 1);
         for (int a = 0; a < 2; ++a) {
             ptx::mbar_init(ptx::smem_addr(&ctrl->acc_full[a]), 1);
             ptx::mbar_init(ptx::smem_addr(&ctrl->acc_empty[a]), kEpiWarps * kCtas);
@@ -876,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     WaitCtl *wc = &ctrl->wait;
 
     if (warp == 0) {
-        if (lane == 0) run_producer<kCtas>(&tmap_r, &tmap_c, p, raw, ctrl, rank, wc);
+        run_producer<kCtas>(&tmap_r, &tmap_c, p, raw, ctrl, rank, wc);
     } else if (warp == 1) {
         if (leader) run_mma<kCtas>(p, conv, ctrl, tmem_base, wc);
     } else if (warp >= 8 + 4 * kConvGroups) {
@@ -931,14 +932,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---- host side
 
-// Dynamic shared memory of a launch, and its raw ring: as many stages as fit.
-int set_ring(Params &p, int ctas, bool swap)
+// Dynamic shared memory of a launch, and its rings.  Converted stages first:
+// between the release of one and its next MMAs lie ~1500 clocks of hand-offs,
+// so more of them pay until TMEM or the raw ring runs short (it keeps at least
+// three stages).
+int set_rings(Params &p, int ctas, bool swap)
 {
-    const int fixed = static_cast<int>(conv_ring_bytes(p.bn, ctas)) + (swap ? 0 : kEpiWarps * 2 * kBoxBytes) + 1024 +
-                      static_cast<int>(sizeof(Ctrl));
+    const int conv_bytes = 2 * (p.bn / ctas) * 128;
     p.raw_bytes = kRawRowsBytes + p.bn / ctas * kRowBytes;
-    p.raw_stages = std::min(kMaxRaw, (kSmemLimit - fixed) / p.raw_bytes);
-    return fixed + p.raw_stages * p.raw_bytes;
+    const int space = kSmemLimit - (swap ? 0 : kEpiWarps * 2 * kBoxBytes) - 1024 - static_cast<int>(sizeof(Ctrl));
+    p.conv_stages = std::min({kMaxConv, (kTmemCols - 2 * p.bn) / (2 * kConvCols), (space - 3 * p.raw_bytes) / conv_bytes});
+    p.raw_stages = std::min(kMaxRaw, (space - p.conv_stages * conv_bytes) / p.raw_bytes);
+    return kSmemLimit - space + p.conv_stages * conv_bytes + p.raw_stages * p.raw_bytes;
 }
 
 // CTAs (kCtas == 1) or clusters of `cluster` CTAs of the kernel that can be
@@ -991,11 +996,11 @@ bool launch(const I8Params &c, int bn, int splitk, cudaStream_t stream)
     p.tiles_c = (p.cols + bn - 1) / bn;
     p.num_kb = static_cast<int>((c.K + kRowBytes - 1) / kRowBytes);
     p.splitk = std::min(splitk, p.num_kb);
-    const int smem = set_ring(p, kCtas, kSwap);
+    const int smem = set_rings(p, kCtas, kSwap);
     const int cluster = kCtas == 2 ? 2 : p.splitk;
     const int fit = capacity<kCtas, kSwap, T>(cluster);
     const int64_t tiles = p.tiles_r * p.tiles_c;
-    if (fit < 1 || p.raw_stages < 2 || (p.splitk > 1 && tiles > fit)) return false;
+    if (fit < 1 || p.raw_stages < 2 || p.conv_stages < 2 || (p.splitk > 1 && tiles > fit)) return false;
     CUtensorMap mr{}, mc{}, mo{};
     const void *pr = kSwap ? c.B : c.A, *pc = kSwap ? c.A : c.B;
     const int64_t ldr = kSwap ? c.ldb : c.lda, ldc = kSwap ? c.lda : c.ldb;

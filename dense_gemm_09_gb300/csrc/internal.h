@@ -74,6 +74,7 @@ int check_status_repack(int clear, int *site);
 int check_status_i8_rows(int clear, int *site);
 int check_status_i8_gemm(int clear, int *site);
 int check_status_i8_umma(int clear, int *site);
+int check_status_i8_decode(int clear, int *site);
 
 // Rows taken off M for the C-store checks of the next TMA-fed SIMT launch
 // on this host thread (dgemm_test_shrink_bounds); taking it clears it.

@@ -370,7 +370,7 @@ int dgemm_device_status(int clear);
  * clear of the device status: (translation unit x 100000 + source line) of
  * the library's sources, units 1 sgemm_simt.cu, 2 sgemm_tma.cu,
  * 3 umma_gemm.cu, 4 scale_c.cu, 5 repack.cu, 6 i8_rows.cu, 7 i8_gemm.cu,
- * 8 i8_umma.cu; 0 if none failed, and always 0 in libdgemm.so.  Synchronises the device.  Source: none on the pages.
+ * 8 i8_umma.cu, 9 i8_decode.cu; 0 if none failed, and always 0 in libdgemm.so.  Synchronises the device.  Source: none on the pages.
  */
 int dgemm_check_site(void);
 
@@ -488,7 +488,9 @@ int dgemm_tune_next(int variant, int bn, int split);
  *           2: CTA pair, 256 tokens x bn channels (bn 64, 128 or 192);
  *           3: CTA pair, 256 channels x bn tokens (bn 32..192 in steps of 32);
  *           4: one CTA per 128 channels x bn tokens (bn 16..128 in steps of
- *              16), `split` (1..8) CTAs of a cluster sharing it along K.
+ *              16), `split` (1..8) CTAs of a cluster sharing it along K;
+ *           5: at most 16 tokens, blocks of 16 channels and `split` (8 or 16)
+ *              warps.
  * Returns DGEMM_ERR_INVALID_ARG (and records nothing) for values outside
  * these ranges, else DGEMM_OK.  A configuration the next call cannot take is
  * ignored; dgemm_last_kernel() names what ran.  Source: as dgemm_tune_next.
