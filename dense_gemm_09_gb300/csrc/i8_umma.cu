@@ -76,7 +76,7 @@ constexpr int kTmemCols = 512;                  // two accumulators of bn column
 static_assert(2 * kMaxBn + 2 * 2 * kConvCols <= kTmemCols, "two converted stages fit beside any accumulators");
 constexpr int kBoxBytes = 4096;                 // epilogue staging: 32 rows x 128 bytes
 constexpr int kEpiWarps = 4;
-constexpr int kConvGroups = 2;                  // converter groups of four warps, of either kind: one a half
+constexpr int kConvGroups = 3;                  // converter groups of four warps, of either kind
 constexpr int kThreads = 32 * (8 + 2 * 4 * kConvGroups);
 static_assert(kThreads <= 1024, "one CTA");
 constexpr int kSmemLimit = 227 * 1024;
@@ -352,62 +352,74 @@ __device__ __forceinline__ void arrive_leader(uint32_t bar)
         ptx::mbar_arrive(bar);
 }
 
-// A converter group's walk over the CTA's raw stages, in the order the producer
-// fills them, and the converted stages they go to.
+// A converter group's walk over the halves of the CTA's raw stages, in the order
+// the producer fills them, and the converted stages they go to: group g takes
+// halves g, g + 3, ... (two a stage).
 struct HalfIter {
-    uint32_t left;          // stages to go
-    uint32_t stage, phase;  // of the raw ring
-    uint32_t conv, conv_phase;  // converted stage
+    int32_t left;               // stages to go, this one included
+    uint32_t half;
+    uint32_t stage, phase;      // raw ring
+    uint32_t conv, conv_phase;  // converted ring
     uint32_t stages, conv_stages;
 
-    __device__ __forceinline__ HalfIter(const Params &p, const Sched &sc)
+    __device__ __forceinline__ HalfIter(const Params &p, const Sched &sc, uint32_t group)
     {
         const int64_t tiles = p.tiles_r * p.tiles_c;
         const int64_t mine = sc.t0 < tiles ? (tiles - sc.t0 + sc.dt - 1) / sc.dt : 0;
-        left = static_cast<uint32_t>(mine * (sc.kb1 - sc.kb0));
+        left = static_cast<int32_t>(mine * (sc.kb1 - sc.kb0));
         stages = static_cast<uint32_t>(p.raw_stages);
         conv_stages = static_cast<uint32_t>(p.conv_stages);
         stage = phase = conv = conv_phase = 0;
+        half = group & 1u;
+        advance(group >> 1);
     }
-    __device__ __forceinline__ bool more() const { return left != 0; }
-    __device__ __forceinline__ void next()
+    __device__ __forceinline__ void advance(uint32_t n)  // n <= 2 <= conv_stages, stages
     {
-        --left;
-        if (++stage == stages) {
-            stage = 0;
+        left -= static_cast<int32_t>(n);
+        stage += n;
+        if (stage >= stages) {
+            stage -= stages;
             phase ^= 1u;
         }
-        if (++conv == conv_stages) {
-            conv = 0;
+        conv += n;
+        if (conv >= conv_stages) {
+            conv -= conv_stages;
             conv_phase ^= 1u;
         }
     }
+    __device__ __forceinline__ bool more() const { return left > 0; }
+    __device__ __forceinline__ void next()
+    {
+        advance(1u + half);
+        half ^= 1u;
+    }
 };
+static_assert(kConvGroups == 3, "HalfIter::next steps by three halves");
 
 // Row converters: thread = row.  A raw row is 128 bytes, its 16-byte chunk j
 // stored at chunk position j ^ (row mod 8), so that the eight rows of a
 // wavefront read distinct banks.
 template <int kCtas>
 __device__ __forceinline__ void run_row_converter(const Params &p, uint32_t raw, Ctrl *ctrl, uint32_t tmem_base,
-                                                  int warp, uint32_t half, int lane, WaitCtl *wc)
+                                                  int warp, uint32_t group, int lane, WaitCtl *wc)
 {
     const uint32_t quarter = static_cast<uint32_t>(warp & 3);
     const uint32_t row = quarter * 32 + lane;
-    const uint32_t lanes = tmem_base + ((quarter * 32u) << 16) + 2 * static_cast<uint32_t>(p.bn) + half * kConvCols;
-    for (HalfIter it(p, schedule<kCtas>(p)); it.more(); it.next()) {
+    const uint32_t lanes = tmem_base + ((quarter * 32u) << 16) + 2 * static_cast<uint32_t>(p.bn);
+    for (HalfIter it(p, schedule<kCtas>(p), group); it.more(); it.next()) {
         if (!warp_wait<1>(ptx::smem_addr(&ctrl->raw_full[it.stage]), it.phase, wc)) return;
         const uint32_t src = raw + it.stage * static_cast<uint32_t>(p.raw_bytes) + row * kRowBytes;
         uint4 c[4];
 #pragma unroll
-        for (uint32_t j = 0; j < 4; ++j) c[j] = ld_shared_v4(src + (((half * 4 + j) ^ (row & 7u)) << 4));
+        for (uint32_t j = 0; j < 4; ++j) c[j] = ld_shared_v4(src + (((it.half * 4 + j) ^ (row & 7u)) << 4));
         uint32_t w[32];
 #pragma unroll
         for (int j = 0; j < 4; ++j) widen16(c[j], w + j * 8);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctrl->raw_empty[it.stage]));
-        if (!warp_wait<kCtas>(ptx::smem_addr(&ctrl->conv_empty[2 * it.conv + half]), it.conv_phase ^ 1u, wc)) return;
+        if (!warp_wait<kCtas>(ptx::smem_addr(&ctrl->conv_empty[2 * it.conv + it.half]), it.conv_phase ^ 1u, wc)) return;
         ptx::tc_fence_after();
-        ptx::tmem_st_32x32b_x32(lanes + it.conv * 2 * kConvCols, w);
+        ptx::tmem_st_32x32b_x32(lanes + (2 * it.conv + it.half) * kConvCols, w);
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         __syncwarp();
@@ -422,7 +434,7 @@ __device__ __forceinline__ void run_row_converter(const Params &p, uint32_t raw,
 // widened column is a 128-byte K-major row under the 128-byte swizzle.
 template <int kCtas, int kTasks>
 __device__ __forceinline__ void run_col_converter(const Params &p, uint32_t raw, uint32_t conv, Ctrl *ctrl, int tid,
-                                                  uint32_t half, int lane, WaitCtl *wc)
+                                                  uint32_t group, int lane, WaitCtl *wc)
 {
     const int cols = p.bn / kCtas;
     const uint32_t half_bytes = static_cast<uint32_t>(cols) * 128u;
@@ -437,7 +449,7 @@ __device__ __forceinline__ void run_col_converter(const Params &p, uint32_t raw,
         src_off[i] = kRawRowsBytes + col * kRowBytes + ((j ^ (col & 7u)) << 4);
         dst_off[i] = col * 128u + (((2 * j) ^ (col & 7u)) << 4);
     }
-    for (HalfIter it(p, schedule<kCtas>(p)); it.more(); it.next()) {
+    for (HalfIter it(p, schedule<kCtas>(p), group); it.more(); it.next()) {
         if (!warp_wait<1>(ptx::smem_addr(&ctrl->raw_full[it.stage]), it.phase, wc)) return;
         const uint32_t src = raw + it.stage * static_cast<uint32_t>(p.raw_bytes);
         uint4 c[kTasks];
@@ -445,13 +457,13 @@ __device__ __forceinline__ void run_col_converter(const Params &p, uint32_t raw,
 #pragma unroll
         for (int i = 0; i < kTasks; ++i)
             if (DGEMM_CHECK((src_off[i] | 64u) + 16 <= static_cast<uint32_t>(p.raw_bytes)))
-                c[i] = ld_shared_v4(src + (src_off[i] ^ (half << 6)));
+                c[i] = ld_shared_v4(src + (src_off[i] ^ (it.half << 6)));
 #pragma unroll
         for (int i = 0; i < kTasks; ++i) widen16(c[i], w[i]);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctrl->raw_empty[it.stage]));
-        if (!warp_wait<kCtas>(ptx::smem_addr(&ctrl->conv_empty[2 * it.conv + half]), it.conv_phase ^ 1u, wc)) return;
-        const uint32_t dst = conv + (2 * it.conv + half) * half_bytes;
+        if (!warp_wait<kCtas>(ptx::smem_addr(&ctrl->conv_empty[2 * it.conv + it.half]), it.conv_phase ^ 1u, wc)) return;
+        const uint32_t dst = conv + (2 * it.conv + it.half) * half_bytes;
 #pragma unroll
         for (int i = 0; i < kTasks; ++i) {
             if (DGEMM_CHECK((dst_off[i] | 16u) + 16 <= half_bytes)) {
@@ -543,12 +555,11 @@ __device__ __forceinline__ uint32_t pack_bits(T a, T b)
 // by TMA, or, where TMA cannot describe C, by rows of 32 columns.
 template <typename T>
 __device__ __forceinline__ void drain_tokens(const Params &p, const CUtensorMap *tmap_o, const Ctrl *ctrl,
-                                             uint32_t taddr, int64_t row0, int64_t c0, uint32_t box, int lane,
-                                             uint32_t &nbox)
+                                             uint32_t taddr, int64_t row0, int64_t c0, float sa, uint32_t box,
+                                             int lane, uint32_t &nbox)
 {
     constexpr int kCols = 128 / sizeof(T);  // columns of a box
     const int64_t row = row0 + lane;
-    const float sa = row < p.rows ? __ldg(p.c.scale_a + row) : 0.f;
     const float beta = p.c.beta;
     const uint32_t scale = ptx::smem_addr(ctrl->scale), bias = ptx::smem_addr(ctrl->bias);
     T *crow = static_cast<T *>(p.c.C) + row * p.c.ldc;
@@ -699,6 +710,11 @@ __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap 
         __syncwarp();
         named_barrier(kEpiBarrier, 32 * kEpiWarps);  // the last tile's values have been read
         load_column_values<kSwap>(p, ctrl, c0, quarter * 32 + lane);
+        // this lane's row, loaded while the MMAs run: a token's scale, or a
+        // channel's scale and bias
+        const int64_t row = row0 + lane;
+        const float rs = row < p.rows ? __ldg((kSwap ? p.c.scale_b : p.c.scale_a) + row) : 0.f;
+        const float rb = kSwap && p.c.bias && row < p.rows ? __ldg(p.c.bias + row) : 0.f;
         bool ok = warp_wait<kCtas>(ptx::smem_addr(&ctrl->acc_full[acc]), acc_phase, wc);
         // every epilogue warp leaves together, so none waits for another at
         // the named barrier
@@ -708,11 +724,8 @@ __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap 
         ptx::tc_fence_after();
         const uint32_t taddr = tmem_base + ((quarter * 32u) << 16) + acc * static_cast<uint32_t>(p.bn);
         if constexpr (!kSwap) {
-            drain_tokens<T>(p, tmap_o, ctrl, taddr, row0, c0, box, lane, nbox);
+            drain_tokens<T>(p, tmap_o, ctrl, taddr, row0, c0, rs, box, lane, nbox);
         } else {
-            const int64_t n = row0 + lane;
-            const float sb = n < p.rows ? __ldg(p.c.scale_b + n) : 0.f;
-            const float bias = p.c.bias && n < p.rows ? __ldg(p.c.bias + n) : 0.f;
 #pragma unroll 1
             for (int b = 0; b < p.bn; b += 16) {
                 uint32_t r[2][8];
@@ -723,7 +736,7 @@ __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap 
                 float v[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j >> 3][j & 7]);
-                store_channels<T>(p, n, c0 + b, ctrl->scale + b, sb, bias, v);
+                store_channels<T>(p, row, c0 + b, ctrl->scale + b, rs, rb, v);
             }
         }
         ptx::tc_fence_before();
