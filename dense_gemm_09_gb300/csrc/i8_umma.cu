@@ -550,6 +550,36 @@ __device__ __forceinline__ uint32_t pack_bits(T a, T b)
            static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(&b)) << 16;
 }
 
+// Sixteen accumulator columns from `col` of this lane's row, times the row's
+// scale sa and the columns' (in shared memory at `scale`), plus their biases.
+// The scales' loads are in flight beside the accumulator's.
+__device__ __forceinline__ void load_scaled(const Params &p, uint32_t taddr, uint32_t scale, uint32_t bias, int col,
+                                            float sa, float (&v)[16])
+{
+    uint32_t r[16];
+    float4 s[4];
+    tmem_ld_32x32b_x16(taddr + col, r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = ptx::ld_shared_v4f(scale + static_cast<uint32_t>(col + 4 * i) * 4u);
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[4 * i] = __uint_as_float(r[4 * i]) * sa * s[i].x;
+        v[4 * i + 1] = __uint_as_float(r[4 * i + 1]) * sa * s[i].y;
+        v[4 * i + 2] = __uint_as_float(r[4 * i + 2]) * sa * s[i].z;
+        v[4 * i + 3] = __uint_as_float(r[4 * i + 3]) * sa * s[i].w;
+    }
+    if (!p.c.bias) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 o = ptx::ld_shared_v4f(bias + static_cast<uint32_t>(col + 4 * i) * 4u);
+        v[4 * i] += o.x;
+        v[4 * i + 1] += o.y;
+        v[4 * i + 2] += o.z;
+        v[4 * i + 3] += o.w;
+    }
+}
+
 // Rows = tokens: the warp's 32 rows x bn columns from (row0, c0), by boxes of
 // 128 bytes of columns staged in shared memory (128-byte swizzle) and stored
 // by TMA, or, where TMA cannot describe C, by rows of 32 columns.
@@ -573,42 +603,29 @@ __device__ __forceinline__ void drain_tokens(const Params &p, const CUtensorMap 
             if (lane == 0 && nbox >= 2) ptx::bulk_wait_read<1>();  // this box's last store has read it
             __syncwarp();
             const uint32_t dst = buf + static_cast<uint32_t>(lane) * 128u;
+#pragma unroll 1
+            for (int part = 0; part < kCols / 16; ++part) {  // (rolled: its code is fetched cold)
+                float v[16];
+                load_scaled(p, taddr, scale, bias, b * kCols + part * 16, sa, v);
+                if (beta != 0.f && row < p.rows) {
 #pragma unroll
-            for (int part = 0; part < kCols / 16; ++part) {
-                uint32_t r[16];
-                tmem_ld_32x32b_x16(taddr + b * kCols + part * 16, r);
-                ptx::tmem_ld_wait();
+                    for (int e = 0; e < 16; ++e)
+                        if (col0 + part * 16 + e < p.cols) v[e] = fmaf(beta, i8_to_f32(crow[col0 + part * 16 + e]), v[e]);
+                }
                 constexpr int kPer = 16 / sizeof(T);  // values of a 16-byte word
 #pragma unroll
-                for (int j = 0; j < 16 / kPer; ++j) {
-                    const int c = part * 16 + j * kPer;
-                    float v[kPer];
-#pragma unroll
-                    for (int e = 0; e < kPer; e += 4) {
-                        const uint32_t at = static_cast<uint32_t>(b * kCols + c + e) * 4u;
-                        const float4 s = ptx::ld_shared_v4f(scale + at), o = ptx::ld_shared_v4f(bias + at);
-                        const uint32_t *a = r + j * kPer + e;
-                        v[e] = fmaf(__uint_as_float(a[0]) * sa, s.x, o.x);
-                        v[e + 1] = fmaf(__uint_as_float(a[1]) * sa, s.y, o.y);
-                        v[e + 2] = fmaf(__uint_as_float(a[2]) * sa, s.z, o.z);
-                        v[e + 3] = fmaf(__uint_as_float(a[3]) * sa, s.w, o.w);
-                    }
-                    if (beta != 0.f && row < p.rows) {
-#pragma unroll
-                        for (int e = 0; e < kPer; ++e)
-                            if (col0 + c + e < p.cols) v[e] = fmaf(beta, i8_to_f32(crow[col0 + c + e]), v[e]);
-                    }
+                for (int j = 0; j < 16; j += kPer) {
                     uint4 q;
                     if constexpr (sizeof(T) == 2)
-                        q = make_uint4(pack_bits(i8_from_f32<T>(v[0]), i8_from_f32<T>(v[1])),
-                                       pack_bits(i8_from_f32<T>(v[2]), i8_from_f32<T>(v[3])),
-                                       pack_bits(i8_from_f32<T>(v[4]), i8_from_f32<T>(v[5])),
-                                       pack_bits(i8_from_f32<T>(v[6]), i8_from_f32<T>(v[7])));
+                        q = make_uint4(pack_bits(i8_from_f32<T>(v[j]), i8_from_f32<T>(v[j + 1])),
+                                       pack_bits(i8_from_f32<T>(v[j + 2]), i8_from_f32<T>(v[j + 3])),
+                                       pack_bits(i8_from_f32<T>(v[j + 4]), i8_from_f32<T>(v[j + 5])),
+                                       pack_bits(i8_from_f32<T>(v[j + 6]), i8_from_f32<T>(v[j + 7])));
                     else
-                        q = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                       __float_as_uint(v[3]));
-                    ptx::st_shared_v4(dst + ((static_cast<uint32_t>(c / kPer) ^ (static_cast<uint32_t>(lane) & 7u)) << 4),
-                                      q);
+                        q = make_uint4(__float_as_uint(v[j]), __float_as_uint(v[j + 1]), __float_as_uint(v[j + 2]),
+                                       __float_as_uint(v[j + 3]));
+                    const uint32_t word = static_cast<uint32_t>((part * 16 + j) / kPer);
+                    ptx::st_shared_v4(dst + ((word ^ (static_cast<uint32_t>(lane) & 7u)) << 4), q);
                 }
             }
             ptx::fence_proxy_async_smem();  // the TMA store reads through the async proxy
@@ -627,17 +644,13 @@ __device__ __forceinline__ void drain_tokens(const Params &p, const CUtensorMap 
     for (int b = 0; b < p.bn / 32; ++b) {
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
-            uint32_t r[16];
+            float v[16];
             __syncwarp();
-            tmem_ld_32x32b_x16(taddr + b * 32 + part * 16, r);
-            ptx::tmem_ld_wait();
+            load_scaled(p, taddr, scale, bias, b * 32 + part * 16, sa, v);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int e = part * 16 + i;
-                const float v = fmaf(__uint_as_float(r[i]) * sa, ctrl->scale[b * 32 + e], ctrl->bias[b * 32 + e]);
-                ptx::st_shared_f32(box + (static_cast<uint32_t>(lane) * 32u + (static_cast<uint32_t>(e) ^ lane)) * 4u,
-                                   v);
-            }
+            for (int i = 0; i < 16; ++i)
+                ptx::st_shared_f32(box + (static_cast<uint32_t>(lane) * 32u + (static_cast<uint32_t>(part * 16 + i) ^ lane)) * 4u,
+                                   v[i]);
         }
         __syncwarp();
         const int64_t col = c0 + b * 32 + lane;
@@ -659,24 +672,29 @@ __device__ __forceinline__ void drain_tokens(const Params &p, const CUtensorMap 
 // m0 + j, whose scale is at sa[j]; for each token the warp's lanes store
 // consecutive channels.
 template <typename T, int kCount>
-__device__ __forceinline__ void store_channels(const Params &p, int64_t n, int64_t m0, const float *sa, float sb,
+__device__ __forceinline__ void store_channels(const Params &p, int64_t n, int64_t m0, uint32_t sa, float sb,
                                                float bias, const float (&v)[kCount])
 {
     const int64_t left = p.cols - m0;
+    if (n >= p.rows || !DGEMM_CHECK(m0 >= 0 && n >= 0)) return;
     T *dst = static_cast<T *>(p.c.C) + m0 * p.c.ldc + n;
-    const bool in = n < p.rows && DGEMM_CHECK(m0 >= 0 && n >= 0);
+    float x[kCount];
+#pragma unroll
+    for (int j = 0; j < kCount; j += 4) {
+        const float4 s = ptx::ld_shared_v4f(sa + 4u * static_cast<uint32_t>(j));
+        x[j] = fmaf(v[j] * s.x, sb, bias);
+        x[j + 1] = fmaf(v[j + 1] * s.y, sb, bias);
+        x[j + 2] = fmaf(v[j + 2] * s.z, sb, bias);
+        x[j + 3] = fmaf(v[j + 3] * s.w, sb, bias);
+    }
     if (p.c.beta != 0.f) {
 #pragma unroll
         for (int j = 0; j < kCount; ++j)
-            if (in && j < left) {
-                T *d = dst + j * p.c.ldc;
-                *d = i8_from_f32<T>(fmaf(p.c.beta, i8_to_f32(*d), fmaf(v[j] * sa[j], sb, bias)));
-            }
-        return;
+            if (j < left) x[j] = fmaf(p.c.beta, i8_to_f32(dst[j * p.c.ldc]), x[j]);
     }
 #pragma unroll
     for (int j = 0; j < kCount; ++j)
-        if (in && j < left) dst[j * p.c.ldc] = i8_from_f32<T>(fmaf(v[j] * sa[j], sb, bias));
+        if (j < left) dst[j * p.c.ldc] = i8_from_f32<T>(x[j]);
 }
 
 // The scales (and biases) of the tile's columns, by the 128 epilogue threads;
@@ -736,7 +754,7 @@ __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap 
                 float v[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j >> 3][j & 7]);
-                store_channels<T>(p, row, c0 + b, ctrl->scale + b, rs, rb, v);
+                store_channels<T>(p, row, c0 + b, ptx::smem_addr(ctrl->scale + b), rs, rb, v);
             }
         }
         ptx::tc_fence_before();
@@ -828,7 +846,7 @@ __device__ __forceinline__ void splitk_reduce(const Params &p, const Ctrl *ctrl,
                 v[4 * q + 3] += f.w;
             }
         }
-        store_channels<T>(p, n, c0 + g * 8, ctrl->scale + g * 8, sb, bias, v);
+        store_channels<T>(p, n, c0 + g * 8, ptx::smem_addr(ctrl->scale + g * 8), sb, bias, v);
     }
 }
 
