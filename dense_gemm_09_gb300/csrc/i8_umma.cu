@@ -192,6 +192,13 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr)
     return v;
 }
 
+// Meet the other CTA of the cluster without ordering memory: nothing is handed
+// over.  (A releasing arrival waits for all earlier stores, ~1 us.)
+__device__ __forceinline__ void cluster_leave()
+{
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ void named_barrier(uint32_t id, uint32_t threads)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -300,30 +307,59 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, WaitCtl
     return probe<kCtas == 2>(bar, parity) || warp_wait_slow<kCtas == 2>(bar, parity, wc);
 }
 
+// One raw stage: K block kb of 128 rows from rr and of this CTA's columns from
+// cc (by one thread).
+__device__ __forceinline__ void load_stage(const CUtensorMap *tmap_r, const CUtensorMap *tmap_c, const Params &p,
+                                           uint32_t raw, Ctrl *ctrl, uint32_t stage, int kb, int32_t rr, int32_t cc)
+{
+    const uint32_t full = ptx::smem_addr(&ctrl->raw_full[stage]);
+    const uint32_t dst = raw + stage * static_cast<uint32_t>(p.raw_bytes);
+    ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(p.raw_bytes));
+    // the innermost coordinate is a multiple of 128 bytes
+    ptx::tma_load_2d(dst, tmap_r, full, kb * kRowBytes, rr);
+    ptx::tma_load_2d(dst + kRawRowsBytes, tmap_c, full, kb * kRowBytes, cc);
+}
+
+// The first loads of the CTA, into the empty ring, by the thread that has set
+// the ring's barriers up: they are in flight while the rest of the CTA (and
+// its pair) starts, ~0.5 us.  Two of them, because the start waits for this
+// thread and each takes it ~200 clocks.  Returns their number.
+template <int kCtas>
+__device__ __forceinline__ int prefill(const CUtensorMap *tmap_r, const CUtensorMap *tmap_c, const Params &p,
+                                       uint32_t raw, Ctrl *ctrl, uint32_t rank)
+{
+    const Sched sc = schedule<kCtas>(p);
+    int64_t r0, c0;
+    tile_origin(p, sc.t0, kRows * kCtas, r0, c0);
+    const int n = min(2, sc.kb1 - sc.kb0);
+    for (int i = 0; i < n; ++i)
+        load_stage(tmap_r, tmap_c, p, raw, ctrl, i, sc.kb0 + i, static_cast<int32_t>(r0 + rank * kRows),
+                   static_cast<int32_t>(c0 + rank * (p.bn / kCtas)));
+    return n;
+}
+
+// The rest of the loads, after the `done` of prefill.
 template <int kCtas>
 __device__ __forceinline__ void run_producer(const CUtensorMap *tmap_r, const CUtensorMap *tmap_c, const Params &p,
-                                             uint32_t raw, Ctrl *ctrl, uint32_t rank, WaitCtl *wc)
+                                             uint32_t raw, Ctrl *ctrl, uint32_t rank, int done, WaitCtl *wc)
 {
     const Sched sc = schedule<kCtas>(p);
     const int64_t tiles = p.tiles_r * p.tiles_c;
     const int cols = p.bn / kCtas;  // columns this CTA converts
-    uint32_t stage = 0, phase = 0;
+    uint32_t stage = static_cast<uint32_t>(done), phase = 0;
+    if (stage == static_cast<uint32_t>(p.raw_stages)) {
+        stage = 0;
+        phase = 1;
+    }
     bool ok = true;
     for (int64_t t = sc.t0; ok && t < tiles; t += sc.dt) {
         int64_t r0, c0;
         tile_origin(p, t, kRows * kCtas, r0, c0);
         const int32_t rr = static_cast<int32_t>(r0 + rank * kRows), cc = static_cast<int32_t>(c0 + rank * cols);
-        for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
+        for (int kb = t == sc.t0 ? sc.kb0 + done : sc.kb0; kb < sc.kb1; ++kb) {
             ok = warp_wait<1>(ptx::smem_addr(&ctrl->raw_empty[stage]), phase ^ 1u, wc);
             if (!ok) break;
-            if (elect_one()) {
-                const uint32_t full = ptx::smem_addr(&ctrl->raw_full[stage]);
-                const uint32_t dst = raw + stage * static_cast<uint32_t>(p.raw_bytes);
-                ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(p.raw_bytes));
-                // the innermost coordinate is a multiple of 128 bytes
-                ptx::tma_load_2d(dst, tmap_r, full, kb * kRowBytes, rr);
-                ptx::tma_load_2d(dst + kRawRowsBytes, tmap_c, full, kb * kRowBytes, cc);
-            }
+            if (elect_one()) load_stage(tmap_r, tmap_c, p, raw, ctrl, stage, kb, rr, cc);
             __syncwarp();
             if (++stage == static_cast<uint32_t>(p.raw_stages)) {
                 stage = 0;
@@ -580,12 +616,20 @@ __device__ __forceinline__ void load_scaled(const Params &p, uint32_t taddr, uin
     }
 }
 
-// Rows = tokens: the warp's 32 rows x bn columns from (row0, c0), by boxes of
+// A warp's share of a tile's columns: every step-th piece from `first`, staged
+// in `boxes` boxes at `box`.
+struct Share {
+    int first, step;
+    uint32_t box;
+    int boxes;
+};
+
+// Rows = tokens: the warp's 32 rows x its share of the bn columns from (row0, c0), by boxes of
 // 128 bytes of columns staged in shared memory (128-byte swizzle) and stored
 // by TMA, or, where TMA cannot describe C, by rows of 32 columns.
 template <typename T>
 __device__ __forceinline__ void drain_tokens(const Params &p, const CUtensorMap *tmap_o, const Ctrl *ctrl,
-                                             uint32_t taddr, int64_t row0, int64_t c0, float sa, uint32_t box,
+                                             uint32_t taddr, int64_t row0, int64_t c0, float sa, const Share &sh,
                                              int lane, uint32_t &nbox)
 {
     constexpr int kCols = 128 / sizeof(T);  // columns of a box
@@ -596,11 +640,16 @@ __device__ __forceinline__ void drain_tokens(const Params &p, const CUtensorMap 
     if (!DGEMM_CHECK((taddr & 0xFFFFu) + static_cast<uint32_t>(p.bn) <= 2u * static_cast<uint32_t>(p.bn))) return;
     if (p.tma_store) {
 #pragma unroll 1
-        for (int b = 0; b < p.bn / kCols; ++b) {
+        for (int b = sh.first; b < p.bn / kCols; b += sh.step) {
             const int64_t col0 = c0 + b * kCols;
-            const uint32_t buf = box + (nbox & 1u) * kBoxBytes;
+            const uint32_t buf = sh.box + (sh.boxes == 2 ? (nbox & 1u) * kBoxBytes : 0u);
             if (row0 >= p.rows || col0 >= p.cols) break;  // warp-uniform: nothing of C here
-            if (lane == 0 && nbox >= 2) ptx::bulk_wait_read<1>();  // this box's last store has read it
+            if (lane == 0) {  // this box's last store has read it
+                if (sh.boxes == 2)
+                    ptx::bulk_wait_read<1>();
+                else
+                    ptx::bulk_wait_read<0>();
+            }
             __syncwarp();
             const uint32_t dst = buf + static_cast<uint32_t>(lane) * 128u;
 #pragma unroll 1
@@ -641,7 +690,8 @@ __device__ __forceinline__ void drain_tokens(const Params &p, const CUtensorMap 
     // value e of row t sits at word e ^ t of the staged row, so both the
     // row-wise writes and the column-wise reads hit 32 different banks
 #pragma unroll 1
-    for (int b = 0; b < p.bn / 32; ++b) {
+    for (int b = sh.first; b < p.bn / 32; b += sh.step) {
+        const uint32_t box = sh.box;
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
             float v[16];
@@ -711,6 +761,40 @@ __device__ __forceinline__ void load_column_values(const Params &p, Ctrl *ctrl, 
     named_barrier(kEpiBarrier, 32 * kEpiWarps);
 }
 
+// One tile's accumulator at taddr (this warp's TMEM lanes) to C.
+template <bool kSwap, typename T>
+__device__ __forceinline__ void drain(const Params &p, const CUtensorMap *tmap_o, const Ctrl *ctrl, uint32_t taddr,
+                                      int64_t row0, int64_t c0, float rs, float rb, const Share &sh, int lane,
+                                      uint32_t &nbox)
+{
+    if constexpr (!kSwap) {
+        drain_tokens<T>(p, tmap_o, ctrl, taddr, row0, c0, rs, sh, lane, nbox);
+    } else {
+#pragma unroll 1
+        for (int b = 16 * sh.first; b < p.bn; b += 16 * sh.step) {
+            uint32_t r[16];
+            __syncwarp();
+            tmem_ld_32x32b_x16(taddr + b, r);
+            ptx::tmem_ld_wait();
+            float v[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+            store_channels<T>(p, row0 + lane, c0 + b, ptx::smem_addr(ctrl->scale + b), rs, rb, v);
+        }
+    }
+}
+
+// This lane's row of the accumulator: a token's scale, or a channel's scale
+// and bias.
+template <bool kSwap>
+__device__ __forceinline__ void load_row_values(const Params &p, int64_t row, float &rs, float &rb)
+{
+    rs = row < p.rows ? __ldg((kSwap ? p.c.scale_b : p.c.scale_a) + row) : 0.f;
+    rb = kSwap && p.c.bias && row < p.rows ? __ldg(p.c.bias + row) : 0.f;
+}
+
+// The CTA's tiles but the last, while the MMAs of the next one run; then the
+// column values of the last and the wait for its accumulator.
 template <int kCtas, bool kSwap, typename T>
 __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap *tmap_o, Ctrl *ctrl,
                                              uint32_t tmem_base, uint32_t box, uint32_t rank, int warp, int lane,
@@ -719,7 +803,7 @@ __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap 
     const Sched sc = schedule<kCtas>(p);
     const int64_t tiles = p.tiles_r * p.tiles_c;
     const uint32_t quarter = static_cast<uint32_t>(warp & 3);  // the TMEM lanes this warp may read
-    box += quarter * 2 * kBoxBytes;
+    const Share sh{0, 1, box + quarter * 2 * kBoxBytes, 2};
     uint32_t acc = 0, acc_phase = 0, nbox = 0;
     for (int64_t t = sc.t0; t < tiles; t += sc.dt) {
         int64_t r0, c0;
@@ -728,41 +812,51 @@ __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap 
         __syncwarp();
         named_barrier(kEpiBarrier, 32 * kEpiWarps);  // the last tile's values have been read
         load_column_values<kSwap>(p, ctrl, c0, quarter * 32 + lane);
-        // this lane's row, loaded while the MMAs run: a token's scale, or a
-        // channel's scale and bias
-        const int64_t row = row0 + lane;
-        const float rs = row < p.rows ? __ldg((kSwap ? p.c.scale_b : p.c.scale_a) + row) : 0.f;
-        const float rb = kSwap && p.c.bias && row < p.rows ? __ldg(p.c.bias + row) : 0.f;
+        float rs, rb;  // loaded while the MMAs run
+        load_row_values<kSwap>(p, row0 + lane, rs, rb);
         bool ok = warp_wait<kCtas>(ptx::smem_addr(&ctrl->acc_full[acc]), acc_phase, wc);
+        if (t + sc.dt >= tiles) break;  // drain_last's, whether it came or not
         // every epilogue warp leaves together, so none waits for another at
         // the named barrier
         __syncwarp();
         ok = !ptx::bar_red_or(kEpiBarrier, 32 * kEpiWarps, !ok);
         if (!ok) break;
         ptx::tc_fence_after();
-        const uint32_t taddr = tmem_base + ((quarter * 32u) << 16) + acc * static_cast<uint32_t>(p.bn);
-        if constexpr (!kSwap) {
-            drain_tokens<T>(p, tmap_o, ctrl, taddr, row0, c0, rs, box, lane, nbox);
-        } else {
-#pragma unroll 1
-            for (int b = 0; b < p.bn; b += 16) {
-                uint32_t r[2][8];
-                __syncwarp();
-                tmem_ld_32x32b_x8(taddr + b, r[0]);
-                tmem_ld_32x32b_x8(taddr + b + 8, r[1]);
-                ptx::tmem_ld_wait();
-                float v[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j >> 3][j & 7]);
-                store_channels<T>(p, row, c0 + b, ptx::smem_addr(ctrl->scale + b), rs, rb, v);
-            }
-        }
+        drain<kSwap, T>(p, tmap_o, ctrl, tmem_base + ((quarter * 32u) << 16) + acc * static_cast<uint32_t>(p.bn), row0, c0,
+                        rs, rb, sh, lane, nbox);
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_leader<kCtas>(ptx::smem_addr(&ctrl->acc_empty[acc]));
         acc ^= 1u;
         if (acc == 0) acc_phase ^= 1u;
     }
+}
+
+// The last tile of the CTA, after a barrier of all its warps: no MMAs are left
+// to hide the drain behind, so 16 warps share it (the epilogue's and the row
+// converters', group g of four taking every fourth piece of columns).  The
+// converters' warps stage in the raw ring, which is idle now.
+template <int kCtas, bool kSwap, typename T>
+__device__ __forceinline__ void drain_last(const Params &p, const CUtensorMap *tmap_o, const Ctrl *ctrl,
+                                           uint32_t tmem_base, uint32_t box, uint32_t raw, uint32_t rank, int warp,
+                                           int lane, WaitCtl *wc)
+{
+    if (__any_sync(0xFFFFFFFFu, aborted(wc))) return;
+    ptx::tc_fence_after();
+    const Sched sc = schedule<kCtas>(p);
+    const int64_t n = (p.tiles_r * p.tiles_c - sc.t0 + sc.dt - 1) / sc.dt;
+    const int group = (warp - 4) >> 2;
+    const uint32_t quarter = static_cast<uint32_t>(warp & 3);
+    int64_t r0, c0;
+    tile_origin(p, sc.t0 + (n - 1) * sc.dt, kRows * kCtas, r0, c0);
+    const int64_t row0 = r0 + rank * kRows + quarter * 32;
+    float rs, rb;
+    load_row_values<kSwap>(p, row0 + lane, rs, rb);
+    const Share sh{group, 1 + kConvGroups,
+                   group == 0 ? box + quarter * 2 * kBoxBytes : raw + ((group - 1) * 4 + quarter) * kBoxBytes, 1};
+    uint32_t nbox = 0;
+    drain<kSwap, T>(p, tmap_o, ctrl, tmem_base + ((quarter * 32u) << 16) + static_cast<uint32_t>((n - 1) & 1) * p.bn, row0,
+                    c0, rs, rb, sh, lane, nbox);
     if (lane == 0) ptx::bulk_wait<0>();  // stores done before the CTA leaves
 }
 
@@ -790,7 +884,7 @@ __device__ __forceinline__ void splitk_push(const Params &p, uint32_t tmem_base,
     const uint32_t groups = static_cast<uint32_t>(p.bn) / 8;
     const int row = static_cast<int>(quarter * 32 + lane);
 #pragma unroll 1
-    for (uint32_t g = 0; g < groups; ++g) {
+    for (uint32_t g = static_cast<uint32_t>(warp - 4) >> 2; g < groups; g += 1 + kConvGroups) {  // shared as in drain_last
         const uint32_t owner = g % S;
         if (owner == rank) continue;
         uint32_t r[8];
@@ -823,7 +917,7 @@ __device__ __forceinline__ void splitk_reduce(const Params &p, const Ctrl *ctrl,
     const float sb = n < p.rows ? __ldg(p.c.scale_b + n) : 0.f;
     const float bias = p.c.bias && n < p.rows ? __ldg(p.c.bias + n) : 0.f;
 #pragma unroll 1
-    for (uint32_t g = rank; g < groups; g += S) {
+    for (uint32_t g = rank + S * (static_cast<uint32_t>(warp - 4) >> 2); g < groups; g += S * (1 + kConvGroups)) {
         uint32_t own[8];
         __syncwarp();
         tmem_ld_32x32b_x8(tmem_base + ((quarter * 32u) << 16) + g * 8, own);
@@ -866,12 +960,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = kCtas == 2 ? (ptx::cluster_ctarank() & 1u) : 0u;
     const bool leader = rank == 0;
+    int loaded = 0;  // raw stages already under way (warp 0)
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kMaxRaw; ++s) {
-            ptx::mbar_init(ptx::smem_addr(&ctrl->raw_full[s]), 1);
-            ptx::mbar_init(ptx::smem_addr(&ctrl->raw_empty[s]), 16);
+    if (warp == 0) {
+        if (elect_one()) {
+            for (int s = 0; s < kMaxRaw; ++s) {
+                ptx::mbar_init(ptx::smem_addr(&ctrl->raw_full[s]), 1);
+                ptx::mbar_init(ptx::smem_addr(&ctrl->raw_empty[s]), 16);
+            }
+            ptx::fence_mbarrier_init();
+            loaded = prefill<kCtas>(&tmap_r, &tmap_c, p, raw, ctrl, rank);
         }
+        loaded = __reduce_max_sync(0xFFFFFFFFu, loaded);
+    } else if (warp == 1) {
+        if constexpr (kCtas == 2) {
+            ptx::tmem_alloc_pair(ptx::smem_addr(&ctrl->tmem_base), kTmemCols);
+            ptx::tmem_relinquish_pair();
+        } else {
+            ptx::tmem_alloc(ptx::smem_addr(&ctrl->tmem_base), kTmemCols);
+            ptx::tmem_relinquish();
+        }
+    } else if (warp == 2 && elect_one()) {
         for (int s = 0; s < kMaxConv; ++s) ptx::mbar_init(ptx::smem_addr(&ctrl->conv_full[s]), 16 * kCtas);
         for (int s = 0; s < 2 * kMaxConv; ++s) ptx::mbar_init(ptx::smem_addr(&ctrl->conv_empty[s]), 1);
         for (int a = 0; a < 2; ++a) {
@@ -883,21 +992,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ctrl->wait.abort = 0;
         ctrl->wait.limit_ns = p.wait_limit_ns;
         ptx::fence_mbarrier_init();
-    }
-    if (warp == 0 && lane == 0) {
-        ptx::prefetch_tmap(&tmap_r);
-        ptx::prefetch_tmap(&tmap_c);
         if (p.tma_store) ptx::prefetch_tmap(&tmap_o);
     }
-    if (warp == 1) {
-        if constexpr (kCtas == 2) {
-            ptx::tmem_alloc_pair(ptx::smem_addr(&ctrl->tmem_base), kTmemCols);
-            ptx::tmem_relinquish_pair();
-        } else {
-            ptx::tmem_alloc(ptx::smem_addr(&ctrl->tmem_base), kTmemCols);
-            ptx::tmem_relinquish();
-        }
-    }
+    __syncwarp();
     ptx::tc_fence_before();
     if constexpr (kCtas == 2)
         ptx::cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
@@ -908,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     WaitCtl *wc = &ctrl->wait;
 
     if (warp == 0) {
-        run_producer<kCtas>(&tmap_r, &tmap_c, p, raw, ctrl, rank, wc);
+        run_producer<kCtas>(&tmap_r, &tmap_c, p, raw, ctrl, rank, loaded, wc);
     } else if (warp == 1) {
         if (leader) run_mma<kCtas>(p, conv, ctrl, tmem_base, wc);
     } else if (warp >= 8 + 4 * kConvGroups) {
@@ -932,23 +1029,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             run_epilogue<kCtas, kSwap, T>(p, &tmap_o, ctrl, tmem_base, box, rank, warp, lane, wc);
     }
 
-    if constexpr (kCtas == 1 && kSwap) {
-        if (p.splitk > 1) {  // uniform over the cluster
-            __syncwarp();
-            ptx::tc_fence_before();
-            ptx::cluster_sync();  // every CTA's sums are complete: the raw rings are idle
-            if (warp >= 4 && warp < 8) splitk_push(p, tmem_base, raw, warp, lane, wc);
-            __syncwarp();
-            ptx::tc_fence_before();
-            ptx::cluster_sync();  // every partial has landed in its owner
-            if (warp >= 4 && warp < 8) splitk_reduce<T>(p, ctrl, tmem_base, raw, warp, lane, wc);
-        }
+    const bool drains = warp >= 4 && warp < 8 + 4 * kConvGroups;  // (warp-uniform)
+    __syncwarp();  // the barriers below are warp-aligned: reconverge the single-lane roles
+    ptx::tc_fence_before();
+    if (kCtas == 1 && kSwap && p.splitk > 1) {  // uniform over the cluster
+        ptx::cluster_sync();  // every CTA's sums are complete: the raw rings are idle
+        if (drains) splitk_push(p, tmem_base, raw, warp, lane, wc);
+        __syncwarp();
+        ptx::tc_fence_before();
+        ptx::cluster_sync();  // every partial has landed in its owner
+        if (drains) splitk_reduce<T>(p, ctrl, tmem_base, raw, warp, lane, wc);
+    } else {
+        __syncthreads();  // every role of this CTA is done
+        if (drains) drain_last<kCtas, kSwap, T>(p, &tmap_o, ctrl, tmem_base, box, raw, rank, warp, lane, wc);
     }
-
-    __syncwarp();  // the barrier below is warp-aligned: reconverge the single-lane roles
+    __syncwarp();
     ptx::tc_fence_before();
     if constexpr (kCtas == 2)
-        ptx::cluster_sync();  // no CTA leaves while the other may still signal or read it
+        cluster_leave();  // no CTA leaves while the other may still signal or read it
     else
         __syncthreads();
     if (warp == 1) {
