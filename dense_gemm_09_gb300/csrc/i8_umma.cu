@@ -99,7 +99,7 @@ struct Ctrl {
 struct Params {
     I8Params c;
     int64_t rows, cols;            // of the accumulator matrix: (M, N), or (N, M) with kSwap
-    int64_t tiles_r, tiles_c;
+    uint32_t tiles_r, tiles_c;     // their product is below 2^31
     int bn;                        // tile columns; a CTA of a pair converts half of them
     int num_kb;                    // K blocks of 128
     int raw_stages, raw_bytes;
@@ -192,9 +192,9 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr)
     return v;
 }
 
-// Meet the other CTA of the cluster without ordering memory: nothing is handed
-// over.  (A releasing arrival waits for all earlier stores, ~1 us.)
-__device__ __forceinline__ void cluster_leave()
+// Meet the other CTA of the cluster without ordering memory.  (A releasing
+// arrival waits for all earlier stores, up to ~1 us.)
+__device__ __forceinline__ void cluster_meet()
 {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
@@ -235,7 +235,7 @@ __device__ __forceinline__ void widen16(const uint4 &c, uint32_t *out)
 // blocks [kb0, kb1) (all of them, or with split-K the r-th of S near-equal
 // ranges for rank r of the cluster).
 struct Sched {
-    int64_t t0, dt;
+    uint32_t t0, dt;
     int kb0, kb1;
 };
 
@@ -243,31 +243,36 @@ template <int kCtas>
 __device__ __forceinline__ Sched schedule(const Params &p)
 {
     Sched s;
-    const int S = kCtas == 1 ? p.splitk : 1;
-    const int64_t per = kCtas == 2 ? 2 : S;  // CTAs that share a tile
-    s.t0 = blockIdx.x / per;
-    s.dt = gridDim.x / per;
+    const uint32_t S = kCtas == 1 ? static_cast<uint32_t>(p.splitk) : 1u;
+    s.t0 = blockIdx.x;
+    s.dt = gridDim.x;
     s.kb0 = 0;
     s.kb1 = p.num_kb;
-    if (S > 1) {
-        const int64_t r = ptx::cluster_ctarank();
-        s.kb0 = static_cast<int>(r * p.num_kb / S);
-        s.kb1 = static_cast<int>((r + 1) * p.num_kb / S);
+    if constexpr (kCtas == 2) {
+        s.t0 >>= 1;
+        s.dt >>= 1;
+    } else if (S > 1) {
+        const uint32_t r = ptx::cluster_ctarank();
+        s.t0 /= S;
+        s.dt /= S;
+        s.kb0 = static_cast<int>(r * static_cast<uint32_t>(p.num_kb) / S);
+        s.kb1 = static_cast<int>((r + 1) * static_cast<uint32_t>(p.num_kb) / S);
     }
     return s;
 }
 
 // Tile t in groups of 8 tile columns: tiles in flight together share a few
 // bands of either operand.
-__device__ __forceinline__ void tile_origin(const Params &p, int64_t t, int tile_rows, int64_t &r0, int64_t &c0)
+__device__ __forceinline__ void tile_origin(const Params &p, uint32_t t, int tile_rows, int64_t &r0, int64_t &c0)
 {
-    constexpr int64_t kGroup = 8;
-    const int64_t per_group = kGroup * p.tiles_r;
-    const int64_t g = t / per_group, r = t % per_group;
-    const int64_t left = p.tiles_c - g * kGroup;
-    const int64_t gc = left < kGroup ? left : kGroup;
-    c0 = (g * kGroup + r % gc) * p.bn;
-    r0 = (r / gc) * tile_rows;
+    constexpr uint32_t kGroup = 8;
+    const uint32_t per_group = kGroup * p.tiles_r;
+    const uint32_t g = t / per_group, r = t - g * per_group;
+    const uint32_t left = p.tiles_c - g * kGroup;
+    const uint32_t gc = left < kGroup ? left : kGroup;
+    const uint32_t row = r / gc;
+    c0 = static_cast<int64_t>(g * kGroup + r - row * gc) * p.bn;
+    r0 = static_cast<int64_t>(row) * tile_rows;
 }
 
 // ---- roles
@@ -344,7 +349,7 @@ __device__ __forceinline__ void run_producer(const CUtensorMap *tmap_r, const CU
                                              uint32_t raw, Ctrl *ctrl, uint32_t rank, int done, WaitCtl *wc)
 {
     const Sched sc = schedule<kCtas>(p);
-    const int64_t tiles = p.tiles_r * p.tiles_c;
+    const uint32_t tiles = p.tiles_r * p.tiles_c;
     const int cols = p.bn / kCtas;  // columns this CTA converts
     uint32_t stage = static_cast<uint32_t>(done), phase = 0;
     if (stage == static_cast<uint32_t>(p.raw_stages)) {
@@ -352,7 +357,7 @@ __device__ __forceinline__ void run_producer(const CUtensorMap *tmap_r, const CU
         phase = 1;
     }
     bool ok = true;
-    for (int64_t t = sc.t0; ok && t < tiles; t += sc.dt) {
+    for (uint32_t t = sc.t0; ok && t < tiles; t += sc.dt) {
         int64_t r0, c0;
         tile_origin(p, t, kRows * kCtas, r0, c0);
         const int32_t rr = static_cast<int32_t>(r0 + rank * kRows), cc = static_cast<int32_t>(c0 + rank * cols);
@@ -388,6 +393,12 @@ __device__ __forceinline__ void arrive_leader(uint32_t bar)
         ptx::mbar_arrive(bar);
 }
 
+// Tiles of this CTA (at least one: the grid has no more CTAs than tiles).
+__device__ __forceinline__ uint32_t my_tiles(const Params &p, const Sched &sc)
+{
+    return (p.tiles_r * p.tiles_c - sc.t0 + sc.dt - 1) / sc.dt;
+}
+
 // A converter group's walk over the halves of the CTA's raw stages, in the order
 // the producer fills them, and the converted stages they go to: group g takes
 // halves g, g + 3, ... (two a stage).
@@ -400,9 +411,7 @@ struct HalfIter {
 
     __device__ __forceinline__ HalfIter(const Params &p, const Sched &sc, uint32_t group)
     {
-        const int64_t tiles = p.tiles_r * p.tiles_c;
-        const int64_t mine = sc.t0 < tiles ? (tiles - sc.t0 + sc.dt - 1) / sc.dt : 0;
-        left = static_cast<int32_t>(mine * (sc.kb1 - sc.kb0));
+        left = static_cast<int32_t>(my_tiles(p, sc)) * (sc.kb1 - sc.kb0);
         stages = static_cast<uint32_t>(p.raw_stages);
         conv_stages = static_cast<uint32_t>(p.conv_stages);
         stage = phase = conv = conv_phase = 0;
@@ -519,7 +528,7 @@ template <int kCtas>
 __device__ __forceinline__ void run_mma(const Params &p, uint32_t conv, Ctrl *ctrl, uint32_t tmem_base, WaitCtl *wc)
 {
     const Sched sc = schedule<kCtas>(p);
-    const int64_t tiles = p.tiles_r * p.tiles_c;
+    const uint32_t tiles = p.tiles_r * p.tiles_c;
     const uint32_t half_bytes = static_cast<uint32_t>(p.bn / kCtas) * 128u;
     // D f32, A and B f16 and K-major, N = bn, M = 128 rows a CTA
     const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(p.bn >> 3) << 17) |
@@ -532,7 +541,7 @@ __device__ __forceinline__ void run_mma(const Params &p, uint32_t conv, Ctrl *ct
     uint32_t cs = 0, cphase = 0, acc = 0, acc_phase = 0;
     // test hook: wait on a barrier nothing arrives at, so the wait runs out
     bool ok = !p.inject_stall || warp_wait<1>(ptx::smem_addr(&ctrl->never), 0, wc);
-    for (int64_t t = sc.t0; ok && t < tiles; t += sc.dt) {
+    for (uint32_t t = sc.t0; ok && t < tiles; t += sc.dt) {
         ok = warp_wait<kCtas>(ptx::smem_addr(&ctrl->acc_empty[acc]), acc_phase ^ 1u, wc);
         if (!ok) break;
         const uint32_t d = tmem_base + acc * static_cast<uint32_t>(p.bn);
@@ -564,9 +573,10 @@ __device__ __forceinline__ void run_mma(const Params &p, uint32_t conv, Ctrl *ct
         if (acc == 0) acc_phase ^= 1u;
     }
     __syncwarp();
-    // every MMA this thread issued has finished before TMEM can be released
-    // (the elected thread is the same one each time)
-    if (elect_one()) {
+    // The epilogue's wait for the last accumulator covers every MMA and commit;
+    // after an abort, wait here for what was issued before TMEM is released
+    // (the elected thread is the same one each time).
+    if (!ok && elect_one()) {
         if constexpr (kCtas == 2)
             ptx::umma_commit_pair_multicast(ptx::smem_addr(&ctrl->mma_done), 0x1);
         else
@@ -801,11 +811,11 @@ __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap 
                                              WaitCtl *wc)
 {
     const Sched sc = schedule<kCtas>(p);
-    const int64_t tiles = p.tiles_r * p.tiles_c;
+    const uint32_t tiles = p.tiles_r * p.tiles_c;
     const uint32_t quarter = static_cast<uint32_t>(warp & 3);  // the TMEM lanes this warp may read
     const Share sh{0, 1, box + quarter * 2 * kBoxBytes, 2};
     uint32_t acc = 0, acc_phase = 0, nbox = 0;
-    for (int64_t t = sc.t0; t < tiles; t += sc.dt) {
+    for (uint32_t t = sc.t0; t < tiles; t += sc.dt) {
         int64_t r0, c0;
         tile_origin(p, t, kRows * kCtas, r0, c0);
         const int64_t row0 = r0 + rank * kRows + quarter * 32;
@@ -832,31 +842,45 @@ __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap 
     }
 }
 
+// The last (with split-K: the only) tile of the CTA as a draining warp sees it.
+struct LastTile {
+    int64_t row0, c0;   // first row of the warp's 32, first column of the tile
+    float rs, rb;       // this lane's row values
+    uint32_t acc;       // accumulator
+};
+
+template <int kCtas, bool kSwap>
+__device__ __forceinline__ LastTile last_tile(const Params &p, uint32_t rank, int warp, int lane)
+{
+    const Sched sc = schedule<kCtas>(p);
+    const uint32_t n = my_tiles(p, sc);
+    LastTile l;
+    int64_t r0;
+    tile_origin(p, sc.t0 + (n - 1) * sc.dt, kRows * kCtas, r0, l.c0);
+    l.row0 = r0 + rank * kRows + static_cast<uint32_t>(warp & 3) * 32;
+    l.acc = (n - 1) & 1u;
+    load_row_values<kSwap>(p, l.row0 + lane, l.rs, l.rb);
+    return l;
+}
+
 // The last tile of the CTA, after a barrier of all its warps: no MMAs are left
 // to hide the drain behind, so 16 warps share it (the epilogue's and the row
 // converters', group g of four taking every fourth piece of columns).  The
 // converters' warps stage in the raw ring, which is idle now.
-template <int kCtas, bool kSwap, typename T>
+template <bool kSwap, typename T>
 __device__ __forceinline__ void drain_last(const Params &p, const CUtensorMap *tmap_o, const Ctrl *ctrl,
-                                           uint32_t tmem_base, uint32_t box, uint32_t raw, uint32_t rank, int warp,
+                                           const LastTile &l, uint32_t tmem_base, uint32_t box, uint32_t raw, int warp,
                                            int lane, WaitCtl *wc)
 {
     if (__any_sync(0xFFFFFFFFu, aborted(wc))) return;
     ptx::tc_fence_after();
-    const Sched sc = schedule<kCtas>(p);
-    const int64_t n = (p.tiles_r * p.tiles_c - sc.t0 + sc.dt - 1) / sc.dt;
     const int group = (warp - 4) >> 2;
     const uint32_t quarter = static_cast<uint32_t>(warp & 3);
-    int64_t r0, c0;
-    tile_origin(p, sc.t0 + (n - 1) * sc.dt, kRows * kCtas, r0, c0);
-    const int64_t row0 = r0 + rank * kRows + quarter * 32;
-    float rs, rb;
-    load_row_values<kSwap>(p, row0 + lane, rs, rb);
     const Share sh{group, 1 + kConvGroups,
                    group == 0 ? box + quarter * 2 * kBoxBytes : raw + ((group - 1) * 4 + quarter) * kBoxBytes, 1};
     uint32_t nbox = 0;
-    drain<kSwap, T>(p, tmap_o, ctrl, tmem_base + ((quarter * 32u) << 16) + static_cast<uint32_t>((n - 1) & 1) * p.bn, row0,
-                    c0, rs, rb, sh, lane, nbox);
+    drain<kSwap, T>(p, tmap_o, ctrl, tmem_base + ((quarter * 32u) << 16) + l.acc * static_cast<uint32_t>(p.bn), l.row0,
+                    l.c0, l.rs, l.rb, sh, lane, nbox);
     if (lane == 0) ptx::bulk_wait<0>();  // stores done before the CTA leaves
 }
 
@@ -902,8 +926,8 @@ __device__ __forceinline__ void splitk_push(const Params &p, uint32_t tmem_base,
 }
 
 template <typename T>
-__device__ __forceinline__ void splitk_reduce(const Params &p, const Ctrl *ctrl, uint32_t tmem_base, uint32_t raw, int warp, int lane,
-                                              WaitCtl *wc)
+__device__ __forceinline__ void splitk_reduce(const Params &p, const Ctrl *ctrl, const LastTile &l, uint32_t tmem_base,
+                                              uint32_t raw, int warp, int lane, WaitCtl *wc)
 {
     if (__any_sync(0xFFFFFFFFu, aborted(wc))) return;
     ptx::tc_fence_after();
@@ -911,11 +935,6 @@ __device__ __forceinline__ void splitk_reduce(const Params &p, const Ctrl *ctrl,
     const uint32_t S = static_cast<uint32_t>(p.splitk), rank = ptx::cluster_ctarank();
     const uint32_t groups = static_cast<uint32_t>(p.bn) / 8;
     const int row = static_cast<int>(quarter * 32 + lane);
-    int64_t r0, c0;
-    tile_origin(p, blockIdx.x / S, kRows, r0, c0);
-    const int64_t n = r0 + row;
-    const float sb = n < p.rows ? __ldg(p.c.scale_b + n) : 0.f;
-    const float bias = p.c.bias && n < p.rows ? __ldg(p.c.bias + n) : 0.f;
 #pragma unroll 1
     for (uint32_t g = rank + S * (static_cast<uint32_t>(warp - 4) >> 2); g < groups; g += S * (1 + kConvGroups)) {
         uint32_t own[8];
@@ -940,7 +959,7 @@ __device__ __forceinline__ void splitk_reduce(const Params &p, const Ctrl *ctrl,
                 v[4 * q + 3] += f.w;
             }
         }
-        store_channels<T>(p, n, c0 + g * 8, ptx::smem_addr(ctrl->scale + g * 8), sb, bias, v);
+        store_channels<T>(p, l.row0 + lane, l.c0 + g * 8, ptx::smem_addr(ctrl->scale + g * 8), l.rs, l.rb, v);
     }
 }
 
@@ -996,10 +1015,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     ptx::tc_fence_before();
-    if constexpr (kCtas == 2)
-        ptx::cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
-    else
-        __syncthreads();
+    __syncthreads();
+    // both CTAs' barriers exist (fence_mbarrier_init above) before any
+    // cross-CTA signal
+    if constexpr (kCtas == 2) cluster_meet();
     ptx::tc_fence_after();
     const uint32_t tmem_base = ctrl->tmem_base;
     WaitCtl *wc = &ctrl->wait;
@@ -1030,6 +1049,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     const bool drains = warp >= 4 && warp < 8 + 4 * kConvGroups;  // (warp-uniform)
+    LastTile last{};
+    if (drains) last = last_tile<kCtas, kSwap>(p, rank, warp, lane);  // its loads are in flight across the barrier
     __syncwarp();  // the barriers below are warp-aligned: reconverge the single-lane roles
     ptx::tc_fence_before();
     if (kCtas == 1 && kSwap && p.splitk > 1) {  // uniform over the cluster
@@ -1038,15 +1059,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         ptx::tc_fence_before();
         ptx::cluster_sync();  // every partial has landed in its owner
-        if (drains) splitk_reduce<T>(p, ctrl, tmem_base, raw, warp, lane, wc);
+        if (drains) splitk_reduce<T>(p, ctrl, last, tmem_base, raw, warp, lane, wc);
     } else {
         __syncthreads();  // every role of this CTA is done
-        if (drains) drain_last<kCtas, kSwap, T>(p, &tmap_o, ctrl, tmem_base, box, raw, rank, warp, lane, wc);
+        if (drains) drain_last<kSwap, T>(p, &tmap_o, ctrl, last, tmem_base, box, raw, warp, lane, wc);
     }
     __syncwarp();
     ptx::tc_fence_before();
     if constexpr (kCtas == 2)
-        cluster_leave();  // no CTA leaves while the other may still signal or read it
+        cluster_meet();  // no CTA leaves while the other may still signal or read it
     else
         __syncthreads();
     if (warp == 1) {
@@ -1121,14 +1142,16 @@ bool launch(const I8Params &c, int bn, int splitk, cudaStream_t stream)
     p.rows = kSwap ? c.N : c.M;
     p.cols = kSwap ? c.M : c.N;
     p.bn = bn;
-    p.tiles_r = (p.rows + kRows * kCtas - 1) / (kRows * kCtas);
-    p.tiles_c = (p.cols + bn - 1) / bn;
+    const int64_t tiles_r = (p.rows + kRows * kCtas - 1) / (kRows * kCtas), tiles_c = (p.cols + bn - 1) / bn;
+    const int64_t tiles = tiles_r * tiles_c;
+    if (tiles > INT32_MAX / 16) return false;  // (32-bit tile arithmetic, with room for a group of tile columns)
+    p.tiles_r = static_cast<uint32_t>(tiles_r);
+    p.tiles_c = static_cast<uint32_t>(tiles_c);
     p.num_kb = static_cast<int>((c.K + kRowBytes - 1) / kRowBytes);
     p.splitk = std::min(splitk, p.num_kb);
     const int smem = set_rings(p, kCtas, kSwap);
     const int cluster = kCtas == 2 ? 2 : p.splitk;
     const int fit = capacity<kCtas, kSwap, T>(cluster);
-    const int64_t tiles = p.tiles_r * p.tiles_c;
     if (fit < 1 || p.raw_stages < 2 || p.conv_stages < 2 || (p.splitk > 1 && tiles > fit)) return false;
     CUtensorMap mr{}, mc{}, mo{};
     const void *pr = kSwap ? c.B : c.A, *pc = kSwap ? c.A : c.B;
