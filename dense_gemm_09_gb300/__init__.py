@@ -424,7 +424,7 @@ def gemm_i8_tn(A, B, C, scale_a, scale_b, bias=None, beta: float = 0.0, stream=N
 
 
 # Kernels for tune_i8_next (see dgemm_tune_i8_next in include/dgemm.h)
-TUNE_I8_MMA, TUNE_I8_PAIR_TOKENS, TUNE_I8_PAIR_CHANNELS, TUNE_I8_SPLIT, TUNE_I8_DECODE = 1, 2, 3, 4, 5
+TUNE_I8_MMA, TUNE_I8_PAIR_TOKENS, TUNE_I8_PAIR_CHANNELS, TUNE_I8_SPLIT, TUNE_I8_DECODE, TUNE_I8_DOT = 1, 2, 3, 4, 5, 6
 
 
 def tune_i8_next(variant: int, bn: int = 0, split: int = 1) -> None:

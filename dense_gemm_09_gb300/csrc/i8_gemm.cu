@@ -8,6 +8,7 @@
 // of 64 bytes staged in shared memory through registers (the next chunk's
 // loads are in flight while a chunk is multiplied); mma.sync m16n8k32 on
 // int8 with exact int32 sums.
+#include <algorithm>
 #include <cstdint>
 #include <mutex>
 #include <string>
@@ -188,23 +189,105 @@ bool tma_ok(const I8Params &p)
            p.N <= kMax && p.K <= kMax;
 }
 
-I8Config choose_config(const I8Params &p, int sm_count)
+// ---- automatic choice, for operands that TMA can describe
+//
+// Estimated times in us, fitted to GB300 sweeps of every kernel over 8 shapes
+// of B x 19 numbers of tokens (1 .. 4096); the smallest estimate runs.
+//
+// 1 to 4 tokens take the dot-product kernel, whose split gives it ~2000 warps
+// (4000 from 3 tokens on, which have fewer loads in flight each) of at most
+// 4096 K values.  5 to 8 tokens take the mma.sync kernel, which nothing else
+// came near.
+struct Candidate {
+    double us;
+    I8Config cfg;
+};
+
+constexpr double kHbm = 6.4e6;  // bytes a us
+
+// Time of one K block of 128, by tile width; between the points, linear.
+double stage_us(bool pair, int bn)
 {
-    if (p.M > 128) return {kI8PairTokens, 192, 1};
-    const int bn = static_cast<int>((p.M + 15) / 16 * 16);
-    const int64_t tiles = (p.N + 127) / 128, kb = (p.K + 127) / 128;
+    struct Point {
+        int bn;
+        double us;
+    };
+    static constexpr Point kPair[] = {{32, 0.33}, {64, 0.337}, {96, 0.352}, {128, 0.37}, {192, 0.445}, {256, 0.575}};
+    static constexpr Point kSingle[] = {{16, 0.345}, {64, 0.385}, {128, 0.54}};
+    const Point *p = pair ? kPair : kSingle;
+    while (bn > p[1].bn) ++p;
+    return p[0].us + (p[1].us - p[0].us) * (bn - p[0].bn) / (p[1].bn - p[0].bn);
+}
+
+I8Config dot_config(const I8Params &p)
+{
+    const int64_t groups = (p.N + 3) / 4, want = p.M > 2 ? 4096 : 2048;
     int split = 1;
-    while (split < 8 && tiles * (split + 1) <= sm_count && kb >= 4 * (split + 1)) ++split;
-    return {kI8Split, bn, split};
+    while (split < 8 && (groups * split < want || p.K > 4096 * split)) split *= 2;
+    return {kI8Dot, 0, split};
+}
+
+// mma.sync: ~20 clocks of an SM for each product of 16 channels x 8 tokens x
+// 32, or ~0.2 + 0.6 us a turn of 128 K values and group of 8 tokens where
+// there are few warps.
+Candidate decode_candidate(const I8Params &p)
+{
+    const int warps = p.N < 4096 ? 16 : 8;
+    const double groups = static_cast<double>(p.M <= 8 ? 1 : p.M <= 16 ? 2 : 4);
+    const double turns = static_cast<double>((p.K + 127) / 128 + warps - 1) / warps;
+    const double nk = static_cast<double>(p.N) * static_cast<double>(p.K);
+    return {2.2 + std::max({1.6e-7 * groups * nk, turns * (0.2 + 0.6 * groups), nk / kHbm}), {kI8Decode, 0, warps}};
+}
+
+I8Config choose_config(const I8Params &p, int sm_count, bool (*fits)(const I8Params &, const I8Config &))
+{
+    if (p.K < (1 << 17)) {
+        if (p.M <= 4) return dot_config(p);
+        if (p.M <= 8) return decode_candidate(p).cfg;
+    }
+    const int64_t kb = (p.K + 127) / 128;
+    const double hbm = static_cast<double>(p.M + p.N) * static_cast<double>(p.K) / kHbm;
+    Candidate best{1e30, {kI8PairTokens, 192, 1}};
+    auto take = [&](const Candidate &c) {
+        if (c.us < best.us && fits(p, c.cfg)) best = c;
+    };
+    if (p.M <= 32 && p.K < (1 << 17)) take(decode_candidate(p));
+    // one CTA per 128 channels x bn tokens: at most two widths, every split
+    // that keeps all CTAs resident.  Its tail, 128 columns of one accumulator
+    // stored token by token, grows with bn; a split costs an exchange.
+    const int64_t m16 = (p.M + 15) / 16 * 16;
+    for (int bn : {static_cast<int>(std::min<int64_t>(m16, 128)), 64}) {
+        if (bn > m16) continue;
+        const int64_t tiles = (p.N + 127) / 128 * ((p.M + bn - 1) / bn);
+        for (int S = 1; S <= 8 && tiles * S <= sm_count && S <= kb; ++S)
+            take({4.8 + 0.022 * bn + (S > 1 ? 1.6 : 0.0) +
+                      std::max(static_cast<double>((kb + S - 1) / S) * stage_us(false, bn), hbm),
+                  {kI8Split, bn, S}});
+    }
+    // CTA pairs of 256 x bn, in waves: rows are the channels (for few tokens)
+    // or the tokens, whose tiles drain faster into C
+    const int64_t pairs = sm_count / 2;
+    auto pair = [&](int variant, int bn, int64_t rows, int64_t cols, double drain) {
+        const int64_t tiles = (rows + 255) / 256 * ((cols + bn - 1) / bn), waves = (tiles + pairs - 1) / pairs;
+        if (bn > 192 && waves > 1) return;
+        take({5.2 + 0.014 * bn + drain * static_cast<double>(waves - 1) +
+                  std::max(static_cast<double>(waves * kb) * stage_us(true, bn), hbm),
+              {variant, bn, 1}});
+    };
+    for (int bn : {64, 128, 192, 256}) pair(kI8PairTokens, bn, p.M, p.N, 0.8);
+    const int64_t m32 = (p.M + 31) / 32 * 32;
+    for (int bn : {64, 96, 128, 192, 256})
+        if (bn <= m32) pair(kI8PairChannels, bn, p.N, p.M, 3.0);
+    return best.cfg;
 }
 
 // Kernel names by configuration, built once.
 const char *config_name(const I8Config &c)
 {
-    static std::string names[13][9][2];
+    static std::string names[17][9][2];
     static std::once_flag once;
     std::call_once(once, [] {
-        for (int w = 1; w <= 12; ++w) {
+        for (int w = 1; w <= 16; ++w) {
             const std::string bn = std::to_string(16 * w);
             names[w][0][0] = "i8_umma_pair_256x" + bn + "_tokens";
             names[w][0][1] = "i8_umma_pair_256x" + bn + "_channels";
@@ -212,14 +295,19 @@ const char *config_name(const I8Config &c)
         }
     });
     if (c.variant == kI8Decode) return c.split == 8 ? "i8_decode_16_channels_8_warps" : "i8_decode_16_channels_16_warps";
+    if (c.variant == kI8Dot)
+        return c.split == 1   ? "i8_dot_4_channels_split1"
+               : c.split == 2 ? "i8_dot_4_channels_split2"
+               : c.split == 4 ? "i8_dot_4_channels_split4"
+                              : "i8_dot_4_channels_split8";
     if (c.variant == kI8Split) return names[c.bn / 16][c.split][0].c_str();
     return names[c.bn / 16][0][c.variant == kI8PairChannels ? 1 : 0].c_str();
 }
 
+// (A launch that cannot be prepared falls back to the kernel for every case.)
 bool launch_config(const I8Params &p, int c_type, const I8Config &cfg, cudaStream_t stream)
 {
-    return cfg.variant == kI8Decode ? launch_i8_decode(p, c_type, cfg.split, stream)
-                                    : launch_i8_umma(p, c_type, cfg, stream);
+    return cfg.variant >= kI8Decode ? launch_i8_decode(p, c_type, cfg, stream) : launch_i8_umma(p, c_type, cfg, stream);
 }
 
 }  // namespace
@@ -234,7 +322,7 @@ const char *launch_gemm_i8(const I8Params &q, int c_type, cudaStream_t stream, c
     t_tune = {kI8Auto, 0, 1};
     if (tma_ok(p) && cfg.variant != kI8Mma) {
         if (cfg.variant != kI8Auto && launch_config(p, c_type, cfg, stream)) return config_name(cfg);
-        cfg = choose_config(p, dev.sm_count);
+        cfg = choose_config(p, dev.sm_count, i8_umma_fits);
         if (launch_config(p, c_type, cfg, stream)) return config_name(cfg);
     }
     switch (c_type) {
@@ -248,9 +336,8 @@ const char *launch_gemm_i8(const I8Params &q, int c_type, cudaStream_t stream, c
 int i8_tune_next(int variant, int bn, int split)
 {
     const I8Config cfg{variant, bn, split};
-    const bool ok = variant == kI8Auto || variant == kI8Mma || i8_umma_config_ok(cfg) ||
-                    (variant == kI8Decode && (split == 8 || split == 16));
-    if (!ok) return DGEMM_ERR_INVALID_ARG;
+    if (variant != kI8Auto && variant != kI8Mma && !i8_umma_config_ok(cfg) && !i8_decode_config_ok(cfg))
+        return DGEMM_ERR_INVALID_ARG;
     t_tune = cfg;
     return DGEMM_OK;
 }

@@ -22,22 +22,26 @@ struct I8Params {
 
 // Kernel of one call: variant, tile width and split (as dgemm_tune_i8_next
 // numbers them).
-enum { kI8Auto = 0, kI8Mma = 1, kI8PairTokens = 2, kI8PairChannels = 3, kI8Split = 4, kI8Decode = 5 };
+enum { kI8Auto = 0, kI8Mma = 1, kI8PairTokens = 2, kI8PairChannels = 3, kI8Split = 4, kI8Decode = 5, kI8Dot = 6 };
 struct I8Config {
     int variant;
     int bn;     // tile columns: channels (kI8PairTokens) or tokens
-    int split;  // kI8Split: CTAs that share a tile along K; kI8Decode: warps of a block
+    int split;  // kI8Split: CTAs that share a tile along K; kI8Dot: warps that do;
+                // kI8Decode: warps of a block
 };
 
 // The tensor-core kernels (i8_umma.cu), for operands TMA can describe: false,
 // and nothing launched, where the configuration cannot run.
 bool i8_umma_config_ok(const I8Config &cfg);
 bool launch_i8_umma(const I8Params &c, int c_type, const I8Config &cfg, cudaStream_t stream);
+// Whether the configuration's CTAs can be resident together where they have to
+// (split-K, wide tiles); true without a GPU and for the other kernels.
+bool i8_umma_fits(const I8Params &c, const I8Config &cfg);
 
-// The kernel for at most 16 tokens (i8_decode.cu), `warps` (8 or 16) to a
-// block; operands with 16-byte aligned rows.
-bool i8_decode_ok(const I8Params &p);
-bool launch_i8_decode(const I8Params &p, int c_type, int warps, cudaStream_t stream);
+// The kernels for few tokens (i8_decode.cu), for operands with 16-byte aligned
+// rows: as above.
+bool i8_decode_config_ok(const I8Config &cfg);
+bool launch_i8_decode(const I8Params &p, int c_type, const I8Config &cfg, cudaStream_t stream);
 
 __device__ __forceinline__ float i8_to_f32(float v) { return v; }
 __device__ __forceinline__ float i8_to_f32(__half v) { return __half2float(v); }

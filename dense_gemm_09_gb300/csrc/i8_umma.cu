@@ -67,13 +67,15 @@ constexpr int kRows = 128;                      // accumulator rows of a CTA: TM
 constexpr int kRowBytes = 128;                  // K values of a raw stage, one byte each
 constexpr int kRawRowsBytes = kRows * kRowBytes;
 constexpr int kHalfK = 64;                      // K values of a converted half
-constexpr int kMaxBn = 192;                     // tile columns
+constexpr int kMaxBn = 256;                     // tile columns
+constexpr int kMaxBn2 = 192;                    // with a second accumulator, for CTAs of several tiles
 constexpr int kMaxSplitBn = 128;                // of a single CTA's tile
 constexpr int kMaxRaw = 8;                      // raw stages
 constexpr int kMaxConv = 4;                     // converted stages, of two halves each
 constexpr int kConvCols = kHalfK / 2;           // TMEM columns of a half's rows: two FP16 values a column
-constexpr int kTmemCols = 512;                  // two accumulators of bn columns, then the converted rows
-static_assert(2 * kMaxBn + 2 * 2 * kConvCols <= kTmemCols, "two converted stages fit beside any accumulators");
+constexpr int kTmemCols = 512;                  // one or two accumulators of bn columns, then the converted rows
+static_assert(kMaxBn + 2 * 2 * kConvCols <= kTmemCols && 2 * kMaxBn2 + 2 * 2 * kConvCols <= kTmemCols,
+              "two converted stages fit beside any accumulators");
 constexpr int kBoxBytes = 4096;                 // epilogue staging: 32 rows x 128 bytes
 constexpr int kEpiWarps = 4;
 constexpr int kConvGroups = 3;                  // converter groups of four warps, of either kind
@@ -104,6 +106,7 @@ struct Params {
     int num_kb;                    // K blocks of 128
     int raw_stages, raw_bytes;
     int conv_stages;               // 2 .. kMaxConv
+    int conv_col;                  // first TMEM column of the converted rows: the accumulators' columns
     int splitk;                    // CTAs of a cluster that share a tile (single CTAs)
     int tma_store;
     uint64_t wait_limit_ns;
@@ -450,7 +453,7 @@ __device__ __forceinline__ void run_row_converter(const Params &p, uint32_t raw,
 {
     const uint32_t quarter = static_cast<uint32_t>(warp & 3);
     const uint32_t row = quarter * 32 + lane;
-    const uint32_t lanes = tmem_base + ((quarter * 32u) << 16) + 2 * static_cast<uint32_t>(p.bn);
+    const uint32_t lanes = tmem_base + ((quarter * 32u) << 16) + static_cast<uint32_t>(p.conv_col);
     for (HalfIter it(p, schedule<kCtas>(p), group); it.more(); it.next()) {
         if (!warp_wait<1>(ptx::smem_addr(&ctrl->raw_full[it.stage]), it.phase, wc)) return;
         const uint32_t src = raw + it.stage * static_cast<uint32_t>(p.raw_bytes) + row * kRowBytes;
@@ -537,7 +540,7 @@ __device__ __forceinline__ void run_mma(const Params &p, uint32_t conv, Ctrl *ct
     // an MMA's K step 2, in its address field
     const uint64_t b_desc = ptx::smem_desc(conv, 16, 1024, ptx::kSw128);
     tmem_base = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);  // a uniform value for the compiler
-    const uint32_t a_base = tmem_base + 2 * static_cast<uint32_t>(p.bn);
+    const uint32_t a_base = tmem_base + static_cast<uint32_t>(p.conv_col);
     uint32_t cs = 0, cphase = 0, acc = 0, acc_phase = 0;
     // test hook: wait on a barrier nothing arrives at, so the wait runs out
     bool ok = !p.inject_stall || warp_wait<1>(ptx::smem_addr(&ctrl->never), 0, wc);
@@ -647,7 +650,7 @@ __device__ __forceinline__ void drain_tokens(const Params &p, const CUtensorMap 
     const float beta = p.c.beta;
     const uint32_t scale = ptx::smem_addr(ctrl->scale), bias = ptx::smem_addr(ctrl->bias);
     T *crow = static_cast<T *>(p.c.C) + row * p.c.ldc;
-    if (!DGEMM_CHECK((taddr & 0xFFFFu) + static_cast<uint32_t>(p.bn) <= 2u * static_cast<uint32_t>(p.bn))) return;
+    if (!DGEMM_CHECK((taddr & 0xFFFFu) + static_cast<uint32_t>(p.bn) <= static_cast<uint32_t>(p.conv_col))) return;
     if (p.tma_store) {
 #pragma unroll 1
         for (int b = sh.first; b < p.bn / kCols; b += sh.step) {
@@ -1028,13 +1031,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         if (leader) run_mma<kCtas>(p, conv, ctrl, tmem_base, wc);
     } else if (warp >= 8 + 4 * kConvGroups) {
-        const int tid = threadIdx.x & 127, half = (warp - 8 - 4 * kConvGroups) >> 2;
+        const int tid = threadIdx.x & 127, group = (warp - 8 - 4 * kConvGroups) >> 2;
         switch ((p.bn / kCtas + 31) / 32) {  // chunks a thread takes; uniform
-        case 1: run_col_converter<kCtas, 1>(p, raw, conv, ctrl, tid, half, lane, wc); break;
-        case 2: run_col_converter<kCtas, 2>(p, raw, conv, ctrl, tid, half, lane, wc); break;
-        case 3: run_col_converter<kCtas, 3>(p, raw, conv, ctrl, tid, half, lane, wc); break;
-        default:
-            if constexpr (kCtas == 1) run_col_converter<kCtas, 4>(p, raw, conv, ctrl, tid, half, lane, wc);
+        case 1: run_col_converter<kCtas, 1>(p, raw, conv, ctrl, tid, group, lane, wc); break;
+        case 2: run_col_converter<kCtas, 2>(p, raw, conv, ctrl, tid, group, lane, wc); break;
+        case 3: run_col_converter<kCtas, 3>(p, raw, conv, ctrl, tid, group, lane, wc); break;
+        default: run_col_converter<kCtas, 4>(p, raw, conv, ctrl, tid, group, lane, wc);
         }
     } else if (warp >= 8) {
         run_row_converter<kCtas>(p, raw, ctrl, tmem_base, warp, (warp - 8) >> 2, lane, wc);
@@ -1091,7 +1093,7 @@ int set_rings(Params &p, int ctas, bool swap)
     const int conv_bytes = 2 * (p.bn / ctas) * 128;
     p.raw_bytes = kRawRowsBytes + p.bn / ctas * kRowBytes;
     const int space = kSmemLimit - (swap ? 0 : kEpiWarps * 2 * kBoxBytes) - 1024 - static_cast<int>(sizeof(Ctrl));
-    p.conv_stages = std::min({kMaxConv, (kTmemCols - 2 * p.bn) / (2 * kConvCols), (space - 3 * p.raw_bytes) / conv_bytes});
+    p.conv_stages = std::min({kMaxConv, (kTmemCols - p.conv_col) / (2 * kConvCols), (space - 3 * p.raw_bytes) / conv_bytes});
     p.raw_stages = std::min(kMaxRaw, (space - p.conv_stages * conv_bytes) / p.raw_bytes);
     return kSmemLimit - space + p.conv_stages * conv_bytes + p.raw_stages * p.raw_bytes;
 }
@@ -1149,9 +1151,12 @@ bool launch(const I8Params &c, int bn, int splitk, cudaStream_t stream)
     p.tiles_c = static_cast<uint32_t>(tiles_c);
     p.num_kb = static_cast<int>((c.K + kRowBytes - 1) / kRowBytes);
     p.splitk = std::min(splitk, p.num_kb);
-    const int smem = set_rings(p, kCtas, kSwap);
     const int cluster = kCtas == 2 ? 2 : p.splitk;
     const int fit = capacity<kCtas, kSwap, T>(cluster);
+    // CTAs of one tile need one accumulator
+    if (tiles > fit && bn > kMaxBn2) return false;
+    p.conv_col = tiles > fit ? 2 * bn : bn;
+    const int smem = set_rings(p, kCtas, kSwap);
     if (fit < 1 || p.raw_stages < 2 || p.conv_stages < 2 || (p.splitk > 1 && tiles > fit)) return false;
     CUtensorMap mr{}, mc{}, mo{};
     const void *pr = kSwap ? c.B : c.A, *pc = kSwap ? c.A : c.B;
@@ -1208,7 +1213,7 @@ bool launch_typed(const I8Params &c, const I8Config &cfg, cudaStream_t stream)
 bool i8_umma_config_ok(const I8Config &cfg)
 {
     switch (cfg.variant) {
-    case kI8PairTokens: return cfg.bn == 64 || cfg.bn == 128 || cfg.bn == 192;
+    case kI8PairTokens: return cfg.bn == 64 || cfg.bn == 128 || cfg.bn == 192 || cfg.bn == 256;
     case kI8PairChannels: return cfg.bn >= 32 && cfg.bn <= kMaxBn && cfg.bn % 32 == 0;
     case kI8Split: return cfg.bn >= 16 && cfg.bn <= kMaxSplitBn && cfg.bn % 16 == 0 && cfg.split >= 1 && cfg.split <= 8;
     default: return false;
@@ -1224,6 +1229,23 @@ bool launch_i8_umma(const I8Params &c, int c_type, const I8Config &cfg, cudaStre
     case DGEMM_TYPE_BF16: return launch_typed<__nv_bfloat16>(c, cfg, stream);
     default: return false;
     }
+}
+
+bool i8_umma_fits(const I8Params &c, const I8Config &cfg)
+{
+    if (cfg.variant == kI8Split && cfg.split > 1) {
+        const int64_t tiles = (c.N + kRows - 1) / kRows * ((c.M + cfg.bn - 1) / cfg.bn);
+        const int fit = capacity<1, true, float>(cfg.split);
+        return fit == 0 || tiles <= fit;
+    }
+    if ((cfg.variant == kI8PairTokens || cfg.variant == kI8PairChannels) && cfg.bn > kMaxBn2) {
+        const bool tokens = cfg.variant == kI8PairTokens;
+        const int64_t tiles = ((tokens ? c.M : c.N) + 2 * kRows - 1) / (2 * kRows) *
+                              (((tokens ? c.N : c.M) + cfg.bn - 1) / cfg.bn);
+        const int fit = capacity<2, false, float>(2);
+        return fit == 0 || tiles <= fit;
+    }
+    return true;
 }
 
 int i8_read_status(int clear)

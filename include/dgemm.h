@@ -485,12 +485,16 @@ int dgemm_tune_next(int variant, int bn, int split);
  * gemm_i8_tn call made by the calling host thread.
  *   variant 0: automatic (the default);
  *           1: the mma.sync kernel for operands of any alignment;
- *           2: CTA pair, 256 tokens x bn channels (bn 64, 128 or 192);
- *           3: CTA pair, 256 channels x bn tokens (bn 32..192 in steps of 32);
+ *           2: CTA pair, 256 tokens x bn channels (bn 64, 128, 192 or, if every
+ *              pair has at most one tile, 256);
+ *           3: CTA pair, 256 channels x bn tokens (bn 32..192, or 256 as above,
+ *              in steps of 32);
  *           4: one CTA per 128 channels x bn tokens (bn 16..128 in steps of
  *              16), `split` (1..8) CTAs of a cluster sharing it along K;
- *           5: at most 16 tokens, blocks of 16 channels and `split` (8 or 16)
- *              warps.
+ *           5: at most 32 tokens, mma.sync, blocks of 16 channels and `split` (8
+ *              or 16) warps;
+ *           6: at most 4 tokens, dot products, `split` (1, 2, 4 or 8) warps to 4
+ *              channels.
  * Returns DGEMM_ERR_INVALID_ARG (and records nothing) for values outside
  * these ranges, else DGEMM_OK.  A configuration the next call cannot take is
  * ignored; dgemm_last_kernel() names what ran.  Source: as dgemm_tune_next.

@@ -52,11 +52,17 @@ def _check(M, N, K, ty="f32", bias=False, beta=0.0, pad=(0, 0), offset=(0, 0), c
 
 # every kernel and tile width on request: (variant, bn, split), name
 KERNELS = [((1, 0, 1), "i8_mma_"), ((2, 64, 1), "pair_256x64_tokens"), ((2, 128, 1), "pair_256x128_tokens"),
-           ((2, 192, 1), "pair_256x192_tokens"), ((3, 32, 1), "pair_256x32_channels"),
+           ((2, 192, 1), "pair_256x192_tokens"), ((2, 256, 1), "pair_256x256_tokens"),
+           ((3, 32, 1), "pair_256x32_channels"), ((3, 160, 1), "pair_256x160_channels"),
            ((3, 96, 1), "pair_256x96_channels"), ((3, 128, 1), "pair_256x128_channels"),
-           ((3, 192, 1), "pair_256x192_channels"), ((4, 16, 1), "128x16_channels_split1"),
+           ((3, 192, 1), "pair_256x192_channels"), ((3, 256, 1), "pair_256x256_channels"),
+           ((4, 16, 1), "128x16_channels_split1"),
            ((4, 48, 3), "128x48_channels_split3"), ((4, 64, 8), "128x64_channels_split8"),
-           ((4, 112, 5), "128x112_channels_split5"), ((4, 128, 2), "128x128_channels_split2")]
+           ((4, 112, 5), "128x112_channels_split5"), ((4, 128, 2), "128x128_channels_split2"),
+           ((5, 0, 8), "decode_16_channels_8"), ((5, 0, 16), "decode_16_channels_16"), ((6, 0, 1), "dot_4_channels_split1"),
+           ((6, 0, 2), "dot_4_channels_split2"), ((6, 0, 4), "dot_4_channels_split4"),
+           ((6, 0, 8), "dot_4_channels_split8")]
+MOST_TOKENS = {5: 32, 6: 4}  # of the kernels for few
 
 
 @pytest.mark.parametrize("tune,name", KERNELS, ids=[n for _, n in KERNELS])
@@ -70,7 +76,10 @@ def test_every_kernel(tune, name):
     # one K block (whole, half, a tail in either half), many; one tile, ragged
     # edges both ways, several tiles
     for M, N, K in ((128, 128, 128), (1, 1, 16), (16, 128, 64), (30, 500, 48), (130, 129, 80), (256, 192, 1024),
-                    (100, 300, 2064), (257, 513, 1000), (300, 700, 4096)):
+                    (100, 300, 2064), (257, 513, 1000), (300, 700, 4096), (2, 37, 4100), (3, 300, 9000), (4, 70, 513),
+                    (7, 33, 3000), (9, 17, 130), (24, 300, 2500)):
+        if M > MOST_TOKENS.get(tune[0], M):
+            continue
         for ty, bias, beta in (("f32", True, 0.5), ("bf16", False, 0.0)):
             got = _check(M, N, K, ty, bias, beta, pad=((-K) % 16, (-K) % 16), call=call)
             split = tune[2]
@@ -89,8 +98,27 @@ def test_every_kernel_stores_any_pitch(tune, name, c_pad, c_offset):
         dg.tune_i8_next(*tune)
         return dg.gemm_i8_tn(*a, **k)
 
+    M = min(70, MOST_TOKENS.get(tune[0], 70))
     for ty in ref.TYPES:
-        _check(70, 333, 256, ty, True, 0.5, c_pad=c_pad, c_offset=c_offset, call=call)
+        assert name in _check(M, 333, 256, ty, True, 0.5, c_pad=c_pad, c_offset=c_offset, call=call)
+
+
+def test_tune_refusals():
+    import dense_gemm_09_gb300 as dg
+    for bad in ((-1, 0, 1), (7, 0, 1), (2, 32, 1), (2, 320, 1), (3, 16, 1), (3, 288, 1), (4, 8, 1), (4, 144, 1), (4, 64, 0),
+                (4, 64, 9), (5, 0, 4), (6, 0, 3), (6, 0, 16)):
+        with pytest.raises(dg.DgemmError):
+            dg.tune_i8_next(*bad)
+    # what the next call cannot take is ignored
+    A, B, sa, sb, _, _ = _operands(100, 300, 256, 3)
+    C = torch.empty((100, 300), device="cuda")
+    dg.tune_i8_next(6, 0, 1)
+    dg.gemm_i8_tn(A, B, C, sa, sb)
+    assert "dot" not in dg.last_kernel()
+    dg.tune_i8_next(1)
+    dg.tune_i8_next(0)
+    dg.gemm_i8_tn(A, B, C, sa, sb)
+    assert "mma" not in dg.last_kernel().replace("umma", "")
 
 
 SMALL = [(1, 1, 1), (1, 1, 64), (2, 3, 5), (7, 9, 33), (16, 16, 16), (17, 65, 129), (64, 64, 64), (65, 63, 127),
