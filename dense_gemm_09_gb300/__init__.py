@@ -185,8 +185,14 @@ def _mat(t: torch.Tensor, name: str, dtype: torch.dtype):
     return t.data_ptr(), max(ld, cols)
 
 
+# the current stream's handle without a Stream object around it (~3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
@@ -316,49 +322,72 @@ def gemm_bf16_nn(A, B, C, alpha: float = 1.0, beta: float = 0.0, stream=None):
 
 
 # ---- linear layers in 8-bit integers
+#
+# These calls are small (a few microseconds of GPU time for one token), so
+# their checks are written to be cheap: one look at each attribute.
 
 _TYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # dgemm_type
+_I8, _F32 = torch.int8, torch.float32
 
 
-def _type(t: torch.Tensor, name: str) -> int:
-    code = _TYPE.get(t.dtype) if isinstance(t, torch.Tensor) else None
+def _rows(t, name: str, dtype):
+    """(address, pitch, shape) of a matrix of dtype."""
+    try:
+        shape, (ld, step) = t.shape, t.stride()
+        rows, cols = shape
+    except (AttributeError, TypeError, ValueError):
+        raise ValueError("%s must be a 2-D tensor" % name) from None
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if step != 1 and cols > 1:
+        raise ValueError("%s must have unit column stride" % name)
+    if ld < cols:
+        if rows > 1:
+            raise ValueError("%s has overlapping rows" % name)
+        ld = cols  # the pitch of a single row is never used
+    return t.data_ptr(), ld, shape
+
+
+def _rows_float(t, name: str):
+    """_rows of a float matrix, its dtype and dgemm_type."""
+    dtype = getattr(t, "dtype", None)
+    code = _TYPE.get(dtype)
     if code is None:
         raise TypeError("%s must be a float32, float16 or bfloat16 tensor" % name)
-    return code
+    p, ld, shape = _rows(t, name, dtype)
+    return p, ld, shape, dtype, code
 
 
-def _vec(t, name: str, dtype: torch.dtype, n: int) -> int:
+def _rows_like(t, name: str, dtype, shape):
+    p, ld, got = _rows(t, name, dtype)
+    if got != shape:
+        raise ValueError("shape mismatch: %s %s, expected %s" % (name, tuple(got), tuple(shape)))
+    return p, ld
+
+
+def _vec(t, name: str, dtype, n: int) -> int:
     if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.shape[0] != n:
         raise ValueError("%s must be a 1-D tensor of %d" % (name, n))
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if not t.is_cuda or (n > 1 and t.stride(0) != 1):
         raise ValueError("%s must be a contiguous CUDA tensor" % name)
     return t.data_ptr()
 
 
-def _like(t, name: str, dtype: torch.dtype, shape):
-    r = _mat(t, name, dtype)
-    if t.shape != shape:
-        raise ValueError("shape mismatch: %s %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    return r
-
-
-def _status(st: int, name: str) -> None:
-    if st != OK:
-        raise DgemmError(st, name)
-
-
 def quantize_i8(X, Q, scale, stream=None):
     """Each row of X (float32, float16 or bfloat16) as int8 with one FP32 scale:
     scale = max|x| / 127, Q = rint(x / scale).  Writes and returns (Q, scale);
     a row of zeros gets scale 0, a row with a NaN or an infinity scale NaN."""
-    ty = _type(X, "X")
-    px, ldx = _mat(X, "X", X.dtype)
-    pq, ldq = _like(Q, "Q", torch.int8, X.shape)
-    rows, cols = X.shape
-    _status(lib().quantize_i8(rows, cols, px, ldx, ty, pq, ldq, _vec(scale, "scale", torch.float32, rows),
-                              _stream(stream)), "quantize_i8")
+    px, ldx, shape, _, ty = _rows_float(X, "X")
+    pq, ldq = _rows_like(Q, "Q", _I8, shape)
+    rows, cols = shape
+    st = (_lib or lib()).quantize_i8(rows, cols, px, ldx, ty, pq, ldq, _vec(scale, "scale", _F32, rows),
+                                     _stream(stream))
+    if st:
+        raise DgemmError(st, "quantize_i8")
     return Q, scale
 
 
@@ -367,40 +396,43 @@ def rmsnorm_i8(X, gamma, Q, scale, residual=None, H=None, eps: float = 1e-6, str
     int8 in Q with their FP32 scales.  H, if given, receives h in X's type (it
     may be X or residual itself).  gamma has X's type or float32.  Returns
     (Q, scale)."""
-    ty = _type(X, "X")
-    px, ldx = _mat(X, "X", X.dtype)
-    rows, cols = X.shape
-    pq, ldq = _like(Q, "Q", torch.int8, X.shape)
-    pr, ldr = _like(residual, "residual", X.dtype, X.shape) if residual is not None else (None, 0)
-    ph, ldh = _like(H, "H", X.dtype, X.shape) if H is not None else (None, 0)
-    tg = _type(gamma, "gamma")
-    pg = _vec(gamma, "gamma", torch.float32 if tg == 0 else X.dtype, cols)
-    _status(lib().rmsnorm_i8(rows, cols, px, ldx, pr, ldr, pg, tg, eps, ty, ph, ldh, pq, ldq,
-                             _vec(scale, "scale", torch.float32, rows), _stream(stream)), "rmsnorm_i8")
+    px, ldx, shape, dtype, ty = _rows_float(X, "X")
+    rows, cols = shape
+    pq, ldq = _rows_like(Q, "Q", _I8, shape)
+    pr, ldr = (None, 0) if residual is None else _rows_like(residual, "residual", dtype, shape)
+    ph, ldh = (None, 0) if H is None else _rows_like(H, "H", dtype, shape)
+    tg = _TYPE.get(getattr(gamma, "dtype", None), -1)
+    pg = _vec(gamma, "gamma", _F32 if tg == 0 else dtype, cols)
+    st = (_lib or lib()).rmsnorm_i8(rows, cols, px, ldx, pr, ldr, pg, tg, eps, ty, ph, ldh, pq, ldq,
+                                    _vec(scale, "scale", _F32, rows), _stream(stream))
+    if st:
+        raise DgemmError(st, "rmsnorm_i8")
     return Q, scale
 
 
 def swiglu_i8(G, U, Q, scale, stream=None):
     """y = G / (1 + exp(-G)) * U; the rows of y as int8 in Q with their FP32
     scales.  G and U may be column slices of one tensor.  Returns (Q, scale)."""
-    ty = _type(G, "G")
-    pg, ldg = _mat(G, "G", G.dtype)
-    pu, ldu = _like(U, "U", G.dtype, G.shape)
-    pq, ldq = _like(Q, "Q", torch.int8, G.shape)
-    rows, cols = G.shape
-    _status(lib().swiglu_i8(rows, cols, pg, ldg, pu, ldu, ty, pq, ldq, _vec(scale, "scale", torch.float32, rows),
-                            _stream(stream)), "swiglu_i8")
+    pg, ldg, shape, dtype, ty = _rows_float(G, "G")
+    pu, ldu = _rows_like(U, "U", dtype, shape)
+    pq, ldq = _rows_like(Q, "Q", _I8, shape)
+    rows, cols = shape
+    st = (_lib or lib()).swiglu_i8(rows, cols, pg, ldg, pu, ldu, ty, pq, ldq, _vec(scale, "scale", _F32, rows),
+                                   _stream(stream))
+    if st:
+        raise DgemmError(st, "swiglu_i8")
     return Q, scale
 
 
 def dequantize_i8(Q, scale, X, stream=None):
     """X = Q * scale (a scale for each row), rounded once to X's type."""
-    ty = _type(X, "X")
-    px, ldx = _mat(X, "X", X.dtype)
-    pq, ldq = _like(Q, "Q", torch.int8, X.shape)
-    rows, cols = X.shape
-    _status(lib().dequantize_i8(rows, cols, pq, ldq, _vec(scale, "scale", torch.float32, rows), px, ldx, ty,
-                                _stream(stream)), "dequantize_i8")
+    px, ldx, shape, _, ty = _rows_float(X, "X")
+    pq, ldq = _rows_like(Q, "Q", _I8, shape)
+    rows, cols = shape
+    st = (_lib or lib()).dequantize_i8(rows, cols, pq, ldq, _vec(scale, "scale", _F32, rows), px, ldx, ty,
+                                       _stream(stream))
+    if st:
+        raise DgemmError(st, "dequantize_i8")
     return X
 
 
@@ -408,18 +440,17 @@ def gemm_i8_tn(A, B, C, scale_a, scale_b, bias=None, beta: float = 0.0, stream=N
     """C[m, n] = scale_a[m] * scale_b[n] * (A @ B.T)[m, n] + bias[n] + beta * C[m, n];
     A: M x K and B: N x K int8, C: M x N float32, float16 or bfloat16; scales
     and bias float32."""
-    ty = _type(C, "C")
-    pa, lda = _mat(A, "A", torch.int8)
-    pb, ldb = _mat(B, "B", torch.int8)
-    pc, ldc = _mat(C, "C", C.dtype)
-    M, K = A.shape
-    N, K2 = B.shape
-    if K2 != K or tuple(C.shape) != (M, N):
+    pc, ldc, (M, N), _, ty = _rows_float(C, "C")
+    pa, lda, (Ma, K) = _rows(A, "A", _I8)
+    pb, ldb, (Nb, Kb) = _rows(B, "B", _I8)
+    if Ma != M or Nb != N or Kb != K:
         raise ValueError("shape mismatch: A %s, B %s, C %s" % (tuple(A.shape), tuple(B.shape), tuple(C.shape)))
-    _status(lib().gemm_i8_tn(M, N, K, pa, lda, _vec(scale_a, "scale_a", torch.float32, M), pb, ldb,
-                             _vec(scale_b, "scale_b", torch.float32, N),
-                             None if bias is None else _vec(bias, "bias", torch.float32, N), beta, pc, ldc, ty,
-                             _stream(stream)), "gemm_i8_tn")
+    st = (_lib or lib()).gemm_i8_tn(M, N, K, pa, lda, _vec(scale_a, "scale_a", _F32, M), pb, ldb,
+                                    _vec(scale_b, "scale_b", _F32, N),
+                                    None if bias is None else _vec(bias, "bias", _F32, N), beta, pc, ldc, ty,
+                                    _stream(stream))
+    if st:
+        raise DgemmError(st, "gemm_i8_tn")
     return C
 
 
@@ -430,4 +461,6 @@ TUNE_I8_MMA, TUNE_I8_PAIR_TOKENS, TUNE_I8_PAIR_CHANNELS, TUNE_I8_SPLIT, TUNE_I8_
 def tune_i8_next(variant: int, bn: int = 0, split: int = 1) -> None:
     """Tuning hook: fix the kernel of the next gemm_i8_tn call on this thread
     (variant TUNE_I8_* or TUNE_AUTO, tile width bn, CTAs sharing a tile)."""
-    _status(lib().dgemm_tune_i8_next(int(variant), int(bn), int(split)), "dgemm_tune_i8_next")
+    st = lib().dgemm_tune_i8_next(int(variant), int(bn), int(split))
+    if st != OK:
+        raise DgemmError(st, "dgemm_tune_i8_next")

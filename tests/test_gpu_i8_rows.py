@@ -279,3 +279,11 @@ def test_refusals():
         dg.swiglu_i8(x, x.half(), q, s)
     with pytest.raises(ValueError):
         dg.dequantize_i8(q, s, x[:, :4])
+    with pytest.raises(ValueError, match="overlapping"):
+        dg.quantize_i8(x[:1].expand(4, 8), q, s)
+    with pytest.raises(ValueError):
+        dg.quantize_i8(x[0], q[0], s)
+    with pytest.raises(TypeError):
+        dg.quantize_i8(None, q, s)
+    with pytest.raises(ValueError):
+        dg.quantize_i8(x, None, s)
