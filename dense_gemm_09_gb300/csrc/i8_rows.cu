@@ -12,13 +12,16 @@
 // happens once, where q or H is stored (the norm uses the unrounded h).
 //
 // The bound is HBM: every input byte is read once and every output byte
-// written once, with a few operations a byte.  A row needs two results over
-// all of its elements before the first q can be written (the norm's sum of
-// squares, then the maximum), so the row's values stay in registers between:
-// a group of kThreads threads holds a row, kVecs vectors of 8 elements a
-// thread.  Rows longer than the registers of one block (32768 elements) are
-// read again from memory for each pass.
+// written once.  A row needs two results over all of its elements before the
+// first q can be written (the norm's sum of squares, then the maximum), so the
+// row's values stay in registers between: a group of kThreads threads holds a
+// row, kVecs vectors of 8 elements a thread.  Rows longer than the registers
+// of one block (32768 elements) are read again from memory for each pass.
+// At 3 to 7 bytes an element the instructions count too (an SM has ~8 of them
+// for each of its threads' elements at HBM speed), hence the packed
+// conversions, the three-input maximum and the rounding by one FMA below.
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -34,6 +37,7 @@ namespace dgemm {
 namespace {
 
 constexpr int kVec = 8;  // elements of one vector: 16 bytes of a 16-bit type, 8 bytes of q
+constexpr int64_t kFewRows = 304;  // two blocks an SM
 
 enum { kOpQuantize = 0, kOpNorm = 1, kOpSwiglu = 2 };
 
@@ -68,36 +72,77 @@ __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2hal
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// kAligned: the vector starts on a 16-byte boundary (sizeof(T) == 2) or two
-// (FP32); n < kVec, or an unaligned operand, takes element loads.  Elements
-// past n are 0.
+// A vector as it lies in memory.
+template <typename T>
+struct Raw {
+    static constexpr int kWords = kVec * sizeof(T) / 16;
+    uint4 w[kWords];
+};
+
+// kAligned: the vector starts on a 16-byte boundary; n < kVec, or an unaligned
+// operand, takes element loads.  Elements past n are 0.
 template <typename T, bool kAligned>
-__device__ __forceinline__ void load_vec(const T *p, int n, float (&v)[kVec])
+__device__ __forceinline__ Raw<T> load_raw(const T *p, int n)
 {
+    Raw<T> r;
     if (kAligned && n == kVec) {
-        constexpr int kWords = kVec * sizeof(T) / 16;
-        uint4 w[kWords];
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) w[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
-        const T *e = reinterpret_cast<const T *>(w);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) v[i] = to_f32(e[i]);
-        return;
+        for (int i = 0; i < Raw<T>::kWords; ++i) r.w[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+        return r;
     }
+    alignas(16) T e[kVec];
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) v[i] = i < n ? to_f32(p[i]) : 0.f;
+    for (int i = 0; i < kVec; ++i) e[i] = i < n ? p[i] : from_f32<T>(0.f);
+#pragma unroll
+    for (int i = 0; i < Raw<T>::kWords; ++i) r.w[i] = reinterpret_cast<const uint4 *>(e)[i];
+    return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack(const Raw<T> &r, float (&v)[kVec])
+{
+    if constexpr (sizeof(T) == 4) {
+        const float *e = reinterpret_cast<const float *>(r.w);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) v[i] = e[i];
+    } else {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(r.w);
+#pragma unroll
+        for (int i = 0; i < kVec / 2; ++i) {
+            float2 f;
+            if constexpr (std::is_same<T, __half>::value)
+                f = __half22float2(*reinterpret_cast<const __half2 *>(w + i));
+            else
+                f = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    }
 }
 
 template <typename T, bool kAligned>
 __device__ __forceinline__ void store_vec(T *p, int n, const float (&v)[kVec])
 {
     if (kAligned && n == kVec && DGEMM_CHECK((reinterpret_cast<uintptr_t>(p) & 15u) == 0)) {
-        alignas(16) T e[kVec];
+        Raw<T> r;
+        uint32_t *w = reinterpret_cast<uint32_t *>(r.w);
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) e[i] = from_f32<T>(v[i]);
+            for (int i = 0; i < kVec; ++i) w[i] = __float_as_uint(v[i]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(kVec * sizeof(T) / 16); ++i)
-            reinterpret_cast<uint4 *>(p)[i] = reinterpret_cast<const uint4 *>(e)[i];
+            for (int i = 0; i < kVec / 2; ++i) {
+                if constexpr (std::is_same<T, __half>::value) {
+                    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                } else {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < Raw<T>::kWords; ++i) reinterpret_cast<uint4 *>(p)[i] = r.w[i];
         return;
     }
 #pragma unroll
@@ -107,18 +152,28 @@ __device__ __forceinline__ void store_vec(T *p, int n, const float (&v)[kVec])
 
 // ---- the quantisation's scale and steps
 
-// A row's largest |y| as the bits of a non-negative float: unsigned order is
-// the order of the values, with infinities and then NaNs above every finite
-// value, so one integer maximum also finds a row that is not finite.
-__device__ __forceinline__ uint32_t abs_bits(float v)
+// max(|a|, |b|, |c|), NaN if one of them is.
+__device__ __forceinline__ float max3_abs(float a, float b, float c)
 {
-    return __float_as_uint(v) & 0x7FFFFFFFu;
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+__device__ __forceinline__ float max_abs(float amax, const float (&v)[kVec])
+{
+#pragma unroll
+    for (int i = 0; i < kVec; i += 2) amax = max3_abs(amax, v[i], v[i + 1]);
+    return amax;
 }
 
 struct Quantiser {
-    float scale, pre, inv;
-    bool finite;
+    float scale, inv;
+    bool finite, tiny;
 
+    // The row's largest |y| as its bits: for non-negative floats unsigned order
+    // is the order of the values, infinities and then NaNs above every finite
+    // one, so the threads' maxima meet in an integer maximum.
     __device__ __forceinline__ explicit Quantiser(uint32_t amax_bits)
     {
         const float a = __uint_as_float(amax_bits);
@@ -126,33 +181,48 @@ struct Quantiser {
         scale = finite ? a / 127.f : __uint_as_float(0x7FC00000u);
         // 127 / a leaves FP32's range below a = 2^-121; such rows are first
         // multiplied by a power of two, which is exact
-        pre = a < 0x1p-100f ? 0x1p100f : 1.f;
-        inv = finite && a > 0.f ? 127.f / (a * pre) : 0.f;
+        tiny = a < 0x1p-100f;
+        inv = a > 0.f ? 127.f / (tiny ? a * 0x1p100f : a) : 0.f;
     }
 
-    // rint(y * 127 / a), ties to even; within [-127, 127] because |y| <= a,
-    // and a product that rounds up past 127 still rounds to 127
-    __device__ __forceinline__ int32_t step(float y) const
+    // rint(y * 127 / a), ties to even, in the low byte: added to 1.5 * 2^23,
+    // whose unit in the last place is 1, the product is rounded to a whole
+    // number within the FMA.  |y| <= a, and a product that rounds up past
+    // 127 still rounds to 127.
+    __device__ __forceinline__ uint32_t step(float y) const { return __float_as_uint(fmaf(y, inv, 12582912.f)); }
+
+    // the steps of eight values, a byte each
+    __device__ __forceinline__ uint2 steps(const float (&y)[kVec]) const
     {
-        return finite ? __float2int_rn(y * pre * inv) : 0;
+        if (!finite) return make_uint2(0u, 0u);
+        float z[kVec];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) z[i] = y[i];
+        if (tiny) {
+            asm volatile("");  // a branch, not eight predicated products for every row
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) z[i] *= 0x1p100f;
+        }
+        uint32_t b[kVec];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) b[i] = step(z[i]);
+        const uint32_t p0 = __byte_perm(b[0], b[1], 0x0040), p1 = __byte_perm(b[2], b[3], 0x0040);
+        const uint32_t p2 = __byte_perm(b[4], b[5], 0x0040), p3 = __byte_perm(b[6], b[7], 0x0040);
+        return make_uint2(__byte_perm(p0, p1, 0x5410), __byte_perm(p2, p3, 0x5410));
     }
 };
 
 template <bool kAligned>
 __device__ __forceinline__ void store_q(int8_t *p, int n, const float (&y)[kVec], const Quantiser &qz)
 {
-    uint32_t b[kVec];
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) b[i] = static_cast<uint32_t>(qz.step(y[i])) & 0xFFu;
+    const uint2 b = qz.steps(y);
     if (kAligned && n == kVec && DGEMM_CHECK((reinterpret_cast<uintptr_t>(p) & 7u) == 0)) {
-        const uint32_t lo = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
-        const uint32_t hi = b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24;
-        *reinterpret_cast<uint2 *>(p) = make_uint2(lo, hi);
+        *reinterpret_cast<uint2 *>(p) = b;
         return;
     }
 #pragma unroll
     for (int i = 0; i < kVec; ++i)
-        if (i < n) p[i] = static_cast<int8_t>(b[i]);
+        if (i < n) p[i] = static_cast<int8_t>((i < 4 ? b.x : b.y) >> (8 * (i & 3)));
 }
 
 // ---- reductions over the threads of a row
@@ -191,35 +261,43 @@ __device__ __forceinline__ float silu(float g)
     return __fdividef(g, 1.f + __expf(-g));
 }
 
-// The values before the norm / quantisation of the vector at column c: x, the
-// residual's sum, or the gated product.
-template <int kOp, typename T, bool kAligned>
-__device__ __forceinline__ void load_row_vec(const RowParams &p, int64_t row, int64_t c, int n, float (&v)[kVec])
+// The values before the norm / quantisation: x, the residual's sum, or the
+// gated product.
+template <int kOp, typename T>
+__device__ __forceinline__ void combine(const RowParams &p, const Raw<T> &x, const Raw<T> &y, float (&v)[kVec])
 {
-    load_vec<T, kAligned>(static_cast<const T *>(p.x) + row * p.ldx + c, n, v);
-    if constexpr (kOp == kOpNorm) {
-        if (p.y) {
-            float r[kVec];
-            load_vec<T, kAligned>(static_cast<const T *>(p.y) + row * p.ldy + c, n, r);
+    unpack(x, v);
+    if constexpr (kOp == kOpQuantize) return;
+    float u[kVec];
+    unpack(y, u);  // (zeros where there is no residual)
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) v[i] += r[i];
-        }
-    }
-    if constexpr (kOp == kOpSwiglu) {
-        float u[kVec];
-        load_vec<T, kAligned>(static_cast<const T *>(p.y) + row * p.ldy + c, n, u);
+    for (int i = 0; i < kVec; ++i) v[i] = kOp == kOpNorm ? v[i] + u[i] : silu(v[i]) * u[i];
+}
+
+template <typename T>
+__device__ __forceinline__ Raw<T> zero_raw()
+{
+    Raw<T> r;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) v[i] = silu(v[i]) * u[i];
-    }
+    for (int i = 0; i < Raw<T>::kWords; ++i) r.w[i] = make_uint4(0, 0, 0, 0);
+    return r;
+}
+
+template <int kOp, typename T, bool kAligned>
+__device__ __forceinline__ Raw<T> load_second(const RowParams &p, int64_t row, int64_t c, int n)
+{
+    if constexpr (kOp == kOpQuantize) return zero_raw<T>();
+    if (kOp == kOpNorm && !p.y) return zero_raw<T>();
+    return load_raw<T, kAligned>(static_cast<const T *>(p.y) + row * p.ldy + c, n);
 }
 
 template <typename T, bool kAligned>
 __device__ __forceinline__ void load_gamma(const RowParams &p, int64_t c, int n, float (&g)[kVec])
 {
     if (p.gamma_f32)
-        load_vec<float, kAligned>(static_cast<const float *>(p.gamma) + c, n, g);
+        unpack(load_raw<float, kAligned>(static_cast<const float *>(p.gamma) + c, n), g);
     else
-        load_vec<T, kAligned>(static_cast<const T *>(p.gamma) + c, n, g);
+        unpack(load_raw<T, kAligned>(static_cast<const T *>(p.gamma) + c, n), g);
 }
 
 __device__ __forceinline__ int vec_len(int64_t cols, int64_t c)
@@ -239,47 +317,55 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) rows_kernel(c
     const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsPerBlock + threadIdx.x / kThreads;
     if (row >= p.rows) return;  // (whole warps; a block of one row never leaves here)
     const int t = static_cast<int>(threadIdx.x % kThreads);
-    float v[kVecs][kVec];
+    const int cols = static_cast<int>(p.cols);
+    int n[kVecs];  // this thread's elements of each vector, from column (j * kThreads + t) * kVec
+    Raw<T> x[kVecs], y[kVecs];
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-        const int64_t c = static_cast<int64_t>(j * kThreads + t) * kVec;
-        load_row_vec<kOp, T, kAligned>(p, row, c, vec_len(p.cols, c), v[j]);
+        const int c = (j * kThreads + t) * kVec;
+        n[j] = max(0, min(kVec, cols - c));
+        x[j] = load_raw<T, kAligned>(static_cast<const T *>(p.x) + row * p.ldx + c, n[j]);
+        y[j] = load_second<kOp, T, kAligned>(p, row, c, n[j]);
     }
-    uint32_t amax = 0;
+    float v[kVecs][kVec];
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) combine<kOp>(p, x[j], y[j], v[j]);
+    float amax = 0.f;
     if constexpr (kOp == kOpNorm) {
         float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            const int64_t c = static_cast<int64_t>(j * kThreads + t) * kVec;
-            if (p.h) store_vec<T, kAligned>(static_cast<T *>(p.h) + row * p.ldh + c, vec_len(p.cols, c), v[j]);
+            const int c = (j * kThreads + t) * kVec;
+            if (p.h) store_vec<T, kAligned>(static_cast<T *>(p.h) + row * p.ldh + c, n[j], v[j]);
 #pragma unroll
             for (int i = 0; i < kVec; ++i) ss = fmaf(v[j][i], v[j][i], ss);
         }
-        ss = row_sum<kThreads>(ss, s_sum);
-        // a sum of squares past FP32's range marks the row like a NaN in it
-        if (!(ss < __uint_as_float(0x7F800000u))) amax = 0x7FC00000u;
-        const float rstd = rsqrtf(ss / static_cast<float>(p.cols) + p.eps);
+        // the weights do not wait for the sum
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            const int64_t c = static_cast<int64_t>(j * kThreads + t) * kVec;
             float g[kVec];
-            load_gamma<T, kAligned>(p, c, vec_len(p.cols, c), g);
+            load_gamma<T, kAligned>(p, (j * kThreads + t) * kVec, n[j], g);
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) v[j][i] *= rstd * g[i];
+            for (int i = 0; i < kVec; ++i) v[j][i] *= g[i];
         }
+        ss = row_sum<kThreads>(ss, s_sum);
+        // a sum of squares past FP32's range marks the row like a NaN in it
+        if (!(ss < __uint_as_float(0x7F800000u))) amax = __uint_as_float(0x7FC00000u);
+        const float rstd = rsqrtf(ss / static_cast<float>(cols) + p.eps);
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) v[j][i] *= rstd;
     }
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j)
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) amax = max(amax, abs_bits(v[j][i]));
-    const Quantiser qz(row_max<kThreads>(amax, s_max));
+    for (int j = 0; j < kVecs; ++j) amax = max_abs(amax, v[j]);
+    const Quantiser qz(row_max<kThreads>(__float_as_uint(amax) & 0x7FFFFFFFu, s_max));
     if (t == 0) p.scale[row] = qz.scale;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-        const int64_t c = static_cast<int64_t>(j * kThreads + t) * kVec;
-        const int n = vec_len(p.cols, c);
-        if (DGEMM_CHECK(n == 0 || (row >= 0 && row < p.rows && c + n <= p.cols)))
-            store_q<kAligned>(p.q + row * p.ldq + c, n, v[j], qz);
+        const int c = (j * kThreads + t) * kVec;
+        if (DGEMM_CHECK(n[j] == 0 || (row >= 0 && row < p.rows && c + n[j] <= cols)))
+            store_q<kAligned>(p.q + row * p.ldq + c, n[j], v[j], qz);
     }
 }
 
@@ -293,28 +379,29 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(const RowParams p)
     __shared__ float s_sum[32];
     __shared__ uint32_t s_max[32];
     const int64_t row = blockIdx.x;
-    float ss = 0.f, rstd = 1.f;
-    uint32_t amax = 0;
+    auto value = [&](int64_t c, int n, float (&v)[kVec]) {
+        combine<kOp>(p, load_raw<T, kAligned>(static_cast<const T *>(p.x) + row * p.ldx + c, n),
+                     load_second<kOp, T, kAligned>(p, row, c, n), v);
+    };
+    float rstd = 1.f, amax = 0.f;
     if constexpr (kOp == kOpNorm) {
+        float ss = 0.f;
         for (int64_t c = static_cast<int64_t>(threadIdx.x) * kVec; c < p.cols; c += kThreads * kVec) {
             float v[kVec];
-            load_row_vec<kOp, T, kAligned>(p, row, c, vec_len(p.cols, c), v);
+            value(c, vec_len(p.cols, c), v);
 #pragma unroll
             for (int i = 0; i < kVec; ++i) ss = fmaf(v[i], v[i], ss);
         }
         ss = row_sum<kThreads>(ss, s_sum);
-        if (!(ss < __uint_as_float(0x7F800000u))) amax = 0x7FC00000u;
+        if (!(ss < __uint_as_float(0x7F800000u))) amax = __uint_as_float(0x7FC00000u);
         rstd = rsqrtf(ss / static_cast<float>(p.cols) + p.eps);
     }
-    auto value = [&](int64_t c, int n, float (&v)[kVec]) {
-        load_row_vec<kOp, T, kAligned>(p, row, c, n, v);
-    };
     auto norm = [&](int64_t c, int n, float (&v)[kVec]) {
         if constexpr (kOp == kOpNorm) {
             float g[kVec];
             load_gamma<T, kAligned>(p, c, n, g);
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) v[i] *= rstd * g[i];
+            for (int i = 0; i < kVec; ++i) v[i] = v[i] * g[i] * rstd;
         }
     };
     for (int64_t c = static_cast<int64_t>(threadIdx.x) * kVec; c < p.cols; c += kThreads * kVec) {
@@ -322,10 +409,9 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(const RowParams p)
         const int n = vec_len(p.cols, c);
         value(c, n, v);
         norm(c, n, v);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) amax = max(amax, abs_bits(v[i]));
+        amax = max_abs(amax, v);
     }
-    const Quantiser qz(row_max<kThreads>(amax, s_max));
+    const Quantiser qz(row_max<kThreads>(__float_as_uint(amax) & 0x7FFFFFFFu, s_max));
     if (threadIdx.x == 0) p.scale[row] = qz.scale;
     for (int64_t c = static_cast<int64_t>(threadIdx.x) * kVec; c < p.cols; c += kThreads * kVec) {
         float v[kVec];
@@ -339,29 +425,39 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(const RowParams p)
     }
 }
 
+// A thread's piece: two vectors of one row, 16 bytes of q.
+constexpr int kPiece = 2 * kVec;
+
+// `pieces` to a row; rows * pieces is below 2^31.
 template <typename T, bool kAligned>
 __global__ void __launch_bounds__(256)
-    dequantize_kernel(int64_t rows, int64_t cols, const int8_t *__restrict__ q, int64_t ldq,
-                      const float *__restrict__ scale, T *__restrict__ x, int64_t ldx, int64_t vecs)
+    dequantize_kernel(uint32_t rows, int64_t cols, const int8_t *__restrict__ q, int64_t ldq,
+                      const float *__restrict__ scale, T *__restrict__ x, int64_t ldx, uint32_t pieces)
 {
-    const int64_t total = rows * vecs;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t row = i / vecs, c = (i - row * vecs) * kVec;
-        const int n = vec_len(cols, c);
+    const uint32_t total = rows * pieces;
+    for (uint32_t i = blockIdx.x * 256u + threadIdx.x; i < total; i += gridDim.x * 256u) {
+        const uint32_t row = i / pieces;
+        const int64_t c = static_cast<int64_t>(i - row * pieces) * kPiece;
+        const int64_t left = cols - c;
         const int8_t *src = q + row * ldq + c;
-        const float s = scale[row];
-        float v[kVec];
-        if (kAligned && n == kVec) {
-            const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(src));
-            const int8_t *e = reinterpret_cast<const int8_t *>(&w);
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) v[k] = static_cast<float>(e[k]) * s;
+        T *dst = x + row * ldx + c;
+        const float s = __ldg(scale + row);
+        alignas(16) int8_t e[kPiece];
+        if (kAligned && left >= kPiece) {
+            *reinterpret_cast<uint4 *>(e) = __ldcs(reinterpret_cast<const uint4 *>(src));
         } else {
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) v[k] = k < n ? static_cast<float>(src[k]) * s : 0.f;
+            for (int k = 0; k < kPiece; ++k) e[k] = k < left ? src[k] : static_cast<int8_t>(0);
         }
-        if (DGEMM_CHECK(row < rows && c + n <= cols)) store_vec<T, kAligned>(x + row * ldx + c, n, v);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float v[kVec];
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) v[k] = static_cast<float>(e[h * kVec + k]) * s;
+            const int64_t l = left - h * kVec;
+            const int n = l >= kVec ? kVec : l > 0 ? static_cast<int>(l) : 0;
+            if (DGEMM_CHECK(row < rows && c + h * kVec + n <= cols || n == 0)) store_vec<T, kAligned>(dst + h * kVec, n, v);
+        }
     }
 }
 
@@ -376,20 +472,25 @@ void launch_rows(const RowParams &p, cudaStream_t stream)
         <<<static_cast<unsigned>(grid), kThreads < 128 ? 128 : kThreads, 0, stream>>>(p);
 }
 
+// Threads by the row's length, four vectors each where there are rows enough to
+// fill the SMs; few rows are spread over more threads instead, one vector
+// each (one row of 4096 through the norm: 4.7 us with 128 threads, see the
+// launch table for the other).
 template <int kOp, typename T, bool kAligned>
 const char *launch_rows_by_length(const RowParams &p, cudaStream_t stream)
 {
     const int64_t vecs = (p.cols + kVec - 1) / kVec;
+    const bool few = p.rows <= kFewRows;
     if (vecs <= 32)
         launch_rows<kOp, T, kAligned, 32, 1>(p, stream);
     else if (vecs <= 128)
-        launch_rows<kOp, T, kAligned, 32, 4>(p, stream);
+        few ? launch_rows<kOp, T, kAligned, 128, 1>(p, stream) : launch_rows<kOp, T, kAligned, 32, 4>(p, stream);
     else if (vecs <= 512)
-        launch_rows<kOp, T, kAligned, 128, 4>(p, stream);
+        few ? launch_rows<kOp, T, kAligned, 512, 1>(p, stream) : launch_rows<kOp, T, kAligned, 128, 4>(p, stream);
     else if (vecs <= 1024)
-        launch_rows<kOp, T, kAligned, 256, 4>(p, stream);
+        few ? launch_rows<kOp, T, kAligned, 1024, 1>(p, stream) : launch_rows<kOp, T, kAligned, 256, 4>(p, stream);
     else if (vecs <= 2048)
-        launch_rows<kOp, T, kAligned, 512, 4>(p, stream);
+        few ? launch_rows<kOp, T, kAligned, 1024, 2>(p, stream) : launch_rows<kOp, T, kAligned, 512, 4>(p, stream);
     else if (vecs <= 4096)
         launch_rows<kOp, T, kAligned, 1024, 4>(p, stream);
     else {
@@ -431,15 +532,19 @@ template <typename T>
 const char *launch_dequantize_typed(int64_t rows, int64_t cols, const int8_t *q, int64_t ldq, const float *scale,
                                     void *x, int64_t ldx, cudaStream_t stream, const DeviceInfo &dev)
 {
-    const int64_t vecs = (cols + kVec - 1) / kVec;
-    const int64_t cap = static_cast<int64_t>(dev.sm_count) * 16;
-    const int64_t want = (rows * vecs + 255) / 256;
-    const unsigned grid = static_cast<unsigned>(want < cap ? want : cap);
-    T *out = static_cast<T *>(x);
-    if (aligned(q, ldq, 1, 8) && aligned(x, ldx, sizeof(T), 16))
-        dequantize_kernel<T, true><<<grid, 256, 0, stream>>>(rows, cols, q, ldq, scale, out, ldx, vecs);
-    else
-        dequantize_kernel<T, false><<<grid, 256, 0, stream>>>(rows, cols, q, ldq, scale, out, ldx, vecs);
+    const int64_t pieces = (cols + kPiece - 1) / kPiece;
+    if (pieces > INT32_MAX) return nullptr;
+    const int64_t cap = static_cast<int64_t>(dev.sm_count) * 32;
+    const int64_t most = INT32_MAX / pieces;  // rows of one launch: 32-bit piece numbers
+    const bool vec = aligned(q, ldq, 1, 16) && aligned(x, ldx, sizeof(T), 16);
+    for (int64_t r = 0; r < rows; r += most) {
+        const int64_t n = rows - r < most ? rows - r : most;
+        const int64_t want = (n * pieces + 255) / 256;
+        const unsigned grid = static_cast<unsigned>(want < cap ? want : cap);
+        auto kernel = vec ? dequantize_kernel<T, true> : dequantize_kernel<T, false>;
+        kernel<<<grid, 256, 0, stream>>>(static_cast<uint32_t>(n), cols, q + r * ldq, ldq, scale + r,
+                                         static_cast<T *>(x) + r * ldx, ldx, static_cast<uint32_t>(pieces));
+    }
     return "i8_dequantize";
 }
 
