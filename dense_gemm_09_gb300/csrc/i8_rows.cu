@@ -14,8 +14,8 @@
 // The bound is HBM: every input byte is read once and every output byte
 // written once.  A row needs two results over all of its elements before the
 // first q can be written (the norm's sum of squares, then the maximum), so the
-// row's values stay in registers between: a group of kThreads threads holds a
-// row, kVecs vectors of 8 elements a thread.  Rows longer than the registers
+// row's values stay in registers between: a warp or a block holds a row, kVecs
+// vectors of 8 elements a thread.  Rows longer than the registers
 // of one block (32768 elements) are read again from memory for each pass.
 // At 3 to 7 bytes an element the instructions count too (an SM has ~8 of them
 // for each of its threads' elements at HBM speed), hence the packed
@@ -39,13 +39,24 @@ namespace {
 constexpr int kVec = 8;  // elements of one vector: 16 bytes of a 16-bit type, 8 bytes of q
 constexpr int64_t kFewRows = 304;  // two blocks an SM
 
-enum { kOpQuantize = 0, kOpNorm = 1, kOpSwiglu = 2 };
+// kOpNorm with a residual, kOpNormAlone without
+enum { kOpQuantize = 0, kOpNorm = 1, kOpSwiglu = 2, kOpNormAlone = 3 };
+
+constexpr bool is_norm(int op)
+{
+    return op == kOpNorm || op == kOpNormAlone;
+}
+
+constexpr bool has_second(int op)
+{
+    return op == kOpNorm || op == kOpSwiglu;
+}
 
 struct RowParams {
     int64_t rows, cols;
     const void *x;  // the row to quantise / norm; the gate of swiglu
     int64_t ldx;
-    const void *y;  // residual (norm; may be null) or the up rows (swiglu)
+    const void *y;  // residual (kOpNorm) or the up rows (swiglu)
     int64_t ldy;
     const void *gamma;
     int gamma_f32;  // gamma is FP32 whatever the rows' type
@@ -81,13 +92,15 @@ struct Raw {
 
 // kAligned: the vector starts on a 16-byte boundary; n < kVec, or an unaligned
 // operand, takes element loads.  Elements past n are 0.
-template <typename T, bool kAligned>
+// kKeep: the vector is read again by other rows (else it streams through).
+template <typename T, bool kAligned, bool kKeep = false>
 __device__ __forceinline__ Raw<T> load_raw(const T *p, int n)
 {
     Raw<T> r;
     if (kAligned && n == kVec) {
 #pragma unroll
-        for (int i = 0; i < Raw<T>::kWords; ++i) r.w[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+        for (int i = 0; i < Raw<T>::kWords; ++i)
+            r.w[i] = kKeep ? __ldg(reinterpret_cast<const uint4 *>(p) + i) : __ldcs(reinterpret_cast<const uint4 *>(p) + i);
         return r;
     }
     alignas(16) T e[kVec];
@@ -227,30 +240,29 @@ __device__ __forceinline__ void store_q(int8_t *p, int n, const float (&y)[kVec]
 
 // ---- reductions over the threads of a row
 
-template <int kThreads>
+// over a warp (kWarp) or the whole block
+template <bool kWarp>
 __device__ __forceinline__ float row_sum(float v, float *shared)
 {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    if constexpr (kThreads == 32) return v;
-    constexpr int kWarps = kThreads / 32;
+    if constexpr (kWarp) return v;
     if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = static_cast<int>(threadIdx.x & 31) < kWarps ? shared[threadIdx.x & 31] : 0.f;
+    v = (threadIdx.x & 31) < (blockDim.x >> 5) ? shared[threadIdx.x & 31] : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
 
-template <int kThreads>
+template <bool kWarp>
 __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t *shared)
 {
     v = __reduce_max_sync(0xFFFFFFFFu, v);
-    if constexpr (kThreads == 32) return v;
-    constexpr int kWarps = kThreads / 32;
+    if constexpr (kWarp) return v;
     if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = static_cast<int>(threadIdx.x & 31) < kWarps ? shared[threadIdx.x & 31] : 0u;
+    v = (threadIdx.x & 31) < (blockDim.x >> 5) ? shared[threadIdx.x & 31] : 0u;
     return __reduce_max_sync(0xFFFFFFFFu, v);
 }
 
@@ -267,37 +279,27 @@ template <int kOp, typename T>
 __device__ __forceinline__ void combine(const RowParams &p, const Raw<T> &x, const Raw<T> &y, float (&v)[kVec])
 {
     unpack(x, v);
-    if constexpr (kOp == kOpQuantize) return;
+    if constexpr (!has_second(kOp)) return;
     float u[kVec];
-    unpack(y, u);  // (zeros where there is no residual)
+    unpack(y, u);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) v[i] = kOp == kOpNorm ? v[i] + u[i] : silu(v[i]) * u[i];
-}
-
-template <typename T>
-__device__ __forceinline__ Raw<T> zero_raw()
-{
-    Raw<T> r;
-#pragma unroll
-    for (int i = 0; i < Raw<T>::kWords; ++i) r.w[i] = make_uint4(0, 0, 0, 0);
-    return r;
 }
 
 template <int kOp, typename T, bool kAligned>
 __device__ __forceinline__ Raw<T> load_second(const RowParams &p, int64_t row, int64_t c, int n)
 {
-    if constexpr (kOp == kOpQuantize) return zero_raw<T>();
-    if (kOp == kOpNorm && !p.y) return zero_raw<T>();
-    return load_raw<T, kAligned>(static_cast<const T *>(p.y) + row * p.ldy + c, n);
+    if constexpr (has_second(kOp)) return load_raw<T, kAligned>(static_cast<const T *>(p.y) + row * p.ldy + c, n);
+    return Raw<T>{};
 }
 
 template <typename T, bool kAligned>
 __device__ __forceinline__ void load_gamma(const RowParams &p, int64_t c, int n, float (&g)[kVec])
 {
     if (p.gamma_f32)
-        unpack(load_raw<float, kAligned>(static_cast<const float *>(p.gamma) + c, n), g);
+        unpack(load_raw<float, kAligned, true>(static_cast<const float *>(p.gamma) + c, n), g);
     else
-        unpack(load_raw<T, kAligned>(static_cast<const T *>(p.gamma) + c, n), g);
+        unpack(load_raw<T, kAligned, true>(static_cast<const T *>(p.gamma) + c, n), g);
 }
 
 __device__ __forceinline__ int vec_len(int64_t cols, int64_t c)
@@ -306,23 +308,24 @@ __device__ __forceinline__ int vec_len(int64_t cols, int64_t c)
     return left >= kVec ? kVec : left > 0 ? static_cast<int>(left) : 0;
 }
 
-// One row a block (kThreads > 32) or a warp (kThreads == 32, four rows a
-// block): the row's values stay in registers, kVecs vectors a thread.
-template <int kOp, typename T, bool kAligned, int kThreads, int kVecs>
-__global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) rows_kernel(const RowParams p)
+// One row a block of at most kMost threads, or (kMost == 32) a warp, four rows
+// a block: the row's values stay in registers, kVecs vectors a thread.
+template <int kOp, typename T, bool kAligned, int kMost, int kVecs>
+__global__ void __launch_bounds__(kMost < 128 ? 128 : kMost, kMost < 128 ? 8 : 1024 / kMost) rows_kernel(const RowParams p)
 {
-    constexpr int kRowsPerBlock = kThreads < 128 ? 128 / kThreads : 1;
+    constexpr bool kWarp = kMost == 32;
+    const int threads = kWarp ? 32 : static_cast<int>(blockDim.x);
     __shared__ float s_sum[32];
     __shared__ uint32_t s_max[32];
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsPerBlock + threadIdx.x / kThreads;
+    const int64_t row = kWarp ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5) : blockIdx.x;
     if (row >= p.rows) return;  // (whole warps; a block of one row never leaves here)
-    const int t = static_cast<int>(threadIdx.x % kThreads);
+    const int t = static_cast<int>(kWarp ? threadIdx.x & 31 : threadIdx.x);
     const int cols = static_cast<int>(p.cols);
-    int n[kVecs];  // this thread's elements of each vector, from column (j * kThreads + t) * kVec
+    int n[kVecs];  // this thread's elements of each vector, from column (j * threads + t) * kVec
     Raw<T> x[kVecs], y[kVecs];
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-        const int c = (j * kThreads + t) * kVec;
+        const int c = (j * threads + t) * kVec;
         n[j] = max(0, min(kVec, cols - c));
         x[j] = load_raw<T, kAligned>(static_cast<const T *>(p.x) + row * p.ldx + c, n[j]);
         y[j] = load_second<kOp, T, kAligned>(p, row, c, n[j]);
@@ -331,11 +334,11 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) rows_kernel(c
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) combine<kOp>(p, x[j], y[j], v[j]);
     float amax = 0.f;
-    if constexpr (kOp == kOpNorm) {
+    if constexpr (is_norm(kOp)) {
         float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            const int c = (j * kThreads + t) * kVec;
+            const int c = (j * threads + t) * kVec;
             if (p.h) store_vec<T, kAligned>(static_cast<T *>(p.h) + row * p.ldh + c, n[j], v[j]);
 #pragma unroll
             for (int i = 0; i < kVec; ++i) ss = fmaf(v[j][i], v[j][i], ss);
@@ -344,11 +347,11 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) rows_kernel(c
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
             float g[kVec];
-            load_gamma<T, kAligned>(p, (j * kThreads + t) * kVec, n[j], g);
+            load_gamma<T, kAligned>(p, (j * threads + t) * kVec, n[j], g);
 #pragma unroll
             for (int i = 0; i < kVec; ++i) v[j][i] *= g[i];
         }
-        ss = row_sum<kThreads>(ss, s_sum);
+        ss = row_sum<kWarp>(ss, s_sum);
         // a sum of squares past FP32's range marks the row like a NaN in it
         if (!(ss < __uint_as_float(0x7F800000u))) amax = __uint_as_float(0x7FC00000u);
         const float rstd = rsqrtf(ss / static_cast<float>(cols) + p.eps);
@@ -359,11 +362,11 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) rows_kernel(c
     }
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) amax = max_abs(amax, v[j]);
-    const Quantiser qz(row_max<kThreads>(__float_as_uint(amax) & 0x7FFFFFFFu, s_max));
+    const Quantiser qz(row_max<kWarp>(__float_as_uint(amax) & 0x7FFFFFFFu, s_max));
     if (t == 0) p.scale[row] = qz.scale;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-        const int c = (j * kThreads + t) * kVec;
+        const int c = (j * threads + t) * kVec;
         if (DGEMM_CHECK(n[j] == 0 || (row >= 0 && row < p.rows && c + n[j] <= cols)))
             store_q<kAligned>(p.q + row * p.ldq + c, n[j], v[j], qz);
     }
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(const RowParams p)
                      load_second<kOp, T, kAligned>(p, row, c, n), v);
     };
     float rstd = 1.f, amax = 0.f;
-    if constexpr (kOp == kOpNorm) {
+    if constexpr (is_norm(kOp)) {
         float ss = 0.f;
         for (int64_t c = static_cast<int64_t>(threadIdx.x) * kVec; c < p.cols; c += kThreads * kVec) {
             float v[kVec];
@@ -392,12 +395,12 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(const RowParams p)
 #pragma unroll
             for (int i = 0; i < kVec; ++i) ss = fmaf(v[i], v[i], ss);
         }
-        ss = row_sum<kThreads>(ss, s_sum);
+        ss = row_sum<false>(ss, s_sum);
         if (!(ss < __uint_as_float(0x7F800000u))) amax = __uint_as_float(0x7FC00000u);
         rstd = rsqrtf(ss / static_cast<float>(p.cols) + p.eps);
     }
     auto norm = [&](int64_t c, int n, float (&v)[kVec]) {
-        if constexpr (kOp == kOpNorm) {
+        if constexpr (is_norm(kOp)) {
             float g[kVec];
             load_gamma<T, kAligned>(p, c, n, g);
 #pragma unroll
@@ -411,18 +414,26 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(const RowParams p)
         norm(c, n, v);
         amax = max_abs(amax, v);
     }
-    const Quantiser qz(row_max<kThreads>(__float_as_uint(amax) & 0x7FFFFFFFu, s_max));
+    const Quantiser qz(row_max<false>(__float_as_uint(amax) & 0x7FFFFFFFu, s_max));
     if (threadIdx.x == 0) p.scale[row] = qz.scale;
     for (int64_t c = static_cast<int64_t>(threadIdx.x) * kVec; c < p.cols; c += kThreads * kVec) {
         float v[kVec];
         const int n = vec_len(p.cols, c);
         value(c, n, v);
         // the last read of this thread's elements: H may now overwrite an input
-        if constexpr (kOp == kOpNorm)
+        if constexpr (is_norm(kOp))
             if (p.h) store_vec<T, kAligned>(static_cast<T *>(p.h) + row * p.ldh + c, n, v);
         norm(c, n, v);
         if (DGEMM_CHECK(c + n <= p.cols)) store_q<kAligned>(p.q + row * p.ldq + c, n, v, qz);
     }
+}
+
+// The int8 value whose byte (with the sign bit flipped, so that it is v + 128)
+// is the k-th of u: under the exponent of 2^23 the byte is the number 2^23 +
+// v + 128, exactly.
+__device__ __forceinline__ float byte_to_f32(uint32_t u, int k)
+{
+    return __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + k)) - 8388736.f;
 }
 
 // A thread's piece: two vectors of one row, 16 bytes of q.
@@ -449,11 +460,12 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
             for (int k = 0; k < kPiece; ++k) e[k] = k < left ? src[k] : static_cast<int8_t>(0);
         }
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(e);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float v[kVec];
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) v[k] = static_cast<float>(e[h * kVec + k]) * s;
+            for (int k = 0; k < kVec; ++k) v[k] = byte_to_f32(w[h * 2 + k / 4] ^ 0x80808080u, k & 3) * s;
             const int64_t l = left - h * kVec;
             const int n = l >= kVec ? kVec : l > 0 ? static_cast<int>(l) : 0;
             if (DGEMM_CHECK(row < rows && c + h * kVec + n <= cols || n == 0)) store_vec<T, kAligned>(dst + h * kVec, n, v);
@@ -463,41 +475,45 @@ __global__ void __launch_bounds__(256)
 
 // ---- host side
 
-template <int kOp, typename T, bool kAligned, int kThreads, int kVecs>
+template <int kOp, typename T, bool kAligned, int kMost, int kVecs>
 void launch_rows(const RowParams &p, cudaStream_t stream)
 {
-    constexpr int kRowsPerBlock = kThreads < 128 ? 128 / kThreads : 1;
-    const int64_t grid = (p.rows + kRowsPerBlock - 1) / kRowsPerBlock;
-    rows_kernel<kOp, T, kAligned, kThreads, kVecs>
-        <<<static_cast<unsigned>(grid), kThreads < 128 ? 128 : kThreads, 0, stream>>>(p);
+    const int64_t vecs = (p.cols + kVec - 1) / kVec;
+    // threads: a warp for each 32 * kVecs vectors
+    const unsigned threads = kMost == 32 ? 128u : static_cast<unsigned>((vecs + 32 * kVecs - 1) / (32 * kVecs) * 32);
+    const unsigned grid = static_cast<unsigned>(kMost == 32 ? (p.rows + 3) / 4 : p.rows);
+    rows_kernel<kOp, T, kAligned, kMost, kVecs><<<grid, threads, 0, stream>>>(p);
 }
 
-// Threads by the row's length, four vectors each where there are rows enough to
-// fill the SMs; few rows are spread over more threads instead, one vector
-// each (one row of 4096 through the norm: 4.7 us with 128 threads, see the
-// launch table for the other).
+// Four vectors a thread where there are rows enough to fill the SMs; few rows
+// are spread over more threads instead, one vector each (one row of 4096
+// bf16 through the norm: 2.4 us with 512 threads, 4.7 with 128).
 template <int kOp, typename T, bool kAligned>
 const char *launch_rows_by_length(const RowParams &p, cudaStream_t stream)
 {
     const int64_t vecs = (p.cols + kVec - 1) / kVec;
     const bool few = p.rows <= kFewRows;
-    if (vecs <= 32)
-        launch_rows<kOp, T, kAligned, 32, 1>(p, stream);
-    else if (vecs <= 128)
-        few ? launch_rows<kOp, T, kAligned, 128, 1>(p, stream) : launch_rows<kOp, T, kAligned, 32, 4>(p, stream);
-    else if (vecs <= 512)
-        few ? launch_rows<kOp, T, kAligned, 512, 1>(p, stream) : launch_rows<kOp, T, kAligned, 128, 4>(p, stream);
-    else if (vecs <= 1024)
-        few ? launch_rows<kOp, T, kAligned, 1024, 1>(p, stream) : launch_rows<kOp, T, kAligned, 256, 4>(p, stream);
-    else if (vecs <= 2048)
-        few ? launch_rows<kOp, T, kAligned, 1024, 2>(p, stream) : launch_rows<kOp, T, kAligned, 512, 4>(p, stream);
-    else if (vecs <= 4096)
-        launch_rows<kOp, T, kAligned, 1024, 4>(p, stream);
-    else {
+    if (vecs > 4096) {
         long_rows_kernel<kOp, T, kAligned><<<static_cast<unsigned>(p.rows), 1024, 0, stream>>>(p);
         return "i8_long_rows";
     }
-    return kOp == kOpNorm ? "i8_rmsnorm_rows" : kOp == kOpSwiglu ? "i8_swiglu_rows" : "i8_quantize_rows";
+    if (few && vecs > 32 && vecs <= 1024)
+        launch_rows<kOp, T, kAligned, 1024, 1>(p, stream);
+    else if (few && vecs > 1024 && vecs <= 2048)
+        launch_rows<kOp, T, kAligned, 1024, 2>(p, stream);
+    else if (vecs <= 32)
+        launch_rows<kOp, T, kAligned, 32, 1>(p, stream);
+    else if (vecs <= 64)
+        launch_rows<kOp, T, kAligned, 32, 2>(p, stream);
+    else if (vecs <= 128)
+        launch_rows<kOp, T, kAligned, 32, 4>(p, stream);
+    else if (vecs <= 1024)
+        launch_rows<kOp, T, kAligned, 256, 4>(p, stream);
+    else if (vecs <= 2048)
+        launch_rows<kOp, T, kAligned, 512, 4>(p, stream);
+    else
+        launch_rows<kOp, T, kAligned, 1024, 4>(p, stream);
+    return is_norm(kOp) ? "i8_rmsnorm_rows" : kOp == kOpSwiglu ? "i8_swiglu_rows" : "i8_quantize_rows";
 }
 
 bool aligned(const void *p, int64_t ld, int64_t elem, int64_t to)
@@ -583,7 +599,7 @@ const char *launch_rmsnorm_i8(int64_t rows, int64_t cols, const void *x, int64_t
     p.q = q;
     p.ldq = ldq;
     p.scale = scale;
-    return launch_rows_op<kOpNorm>(type, p, stream);
+    return residual ? launch_rows_op<kOpNorm>(type, p, stream) : launch_rows_op<kOpNormAlone>(type, p, stream);
 }
 
 const char *launch_swiglu_i8(int64_t rows, int64_t cols, const void *g, int64_t ldg, const void *u, int64_t ldu,
