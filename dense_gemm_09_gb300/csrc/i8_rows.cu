@@ -37,7 +37,7 @@ namespace dgemm {
 namespace {
 
 constexpr int kVec = 8;  // elements of one vector: 16 bytes of a 16-bit type, 8 bytes of q
-constexpr int64_t kFewRows = 304;  // two blocks an SM
+constexpr int64_t kResident = 152 * 2048;  // threads that run at once
 
 // kOpNorm with a residual, kOpNormAlone without
 enum { kOpQuantize = 0, kOpNorm = 1, kOpSwiglu = 2, kOpNormAlone = 3 };
@@ -311,7 +311,7 @@ __device__ __forceinline__ int vec_len(int64_t cols, int64_t c)
 // One row a block of at most kMost threads, or (kMost == 32) a warp, four rows
 // a block: the row's values stay in registers, kVecs vectors a thread.
 template <int kOp, typename T, bool kAligned, int kMost, int kVecs>
-__global__ void __launch_bounds__(kMost < 128 ? 128 : kMost, kMost < 128 ? 8 : 1024 / kMost) rows_kernel(const RowParams p)
+__global__ void __launch_bounds__(kMost < 128 ? 128 : kMost, kMost < 128 ? 6 : 1024 / kMost) rows_kernel(const RowParams p)
 {
     constexpr bool kWarp = kMost == 32;
     const int threads = kWarp ? 32 : static_cast<int>(blockDim.x);
@@ -485,14 +485,17 @@ void launch_rows(const RowParams &p, cudaStream_t stream)
     rows_kernel<kOp, T, kAligned, kMost, kVecs><<<grid, threads, 0, stream>>>(p);
 }
 
-// Four vectors a thread where there are rows enough to fill the SMs; few rows
-// are spread over more threads instead, one vector each (one row of 4096
-// bf16 through the norm: 2.4 us with 512 threads, 4.7 with 128).
+// Four vectors a thread where there are rows enough to fill the SMs; work that
+// is resident at once with one vector a thread (two, for rows of more than
+// 8192) is spread that wide instead.  Through the norm with residual, bf16,
+// wide against four vectors: one row of 4096 2.4 and 4.7 us, 333 rows of 4096
+// 3.3 and 3.8, 333 rows of 8192 (not resident) 5.7 and 4.9.
 template <int kOp, typename T, bool kAligned>
 const char *launch_rows_by_length(const RowParams &p, cudaStream_t stream)
 {
     const int64_t vecs = (p.cols + kVec - 1) / kVec;
-    const bool few = p.rows <= kFewRows;
+    const int64_t wide = p.rows * (vecs <= 1024 ? vecs : (vecs + 1) / 2);  // threads
+    const bool few = wide <= kResident;
     if (vecs > 4096) {
         long_rows_kernel<kOp, T, kAligned><<<static_cast<unsigned>(p.rows), 1024, 0, stream>>>(p);
         return "i8_long_rows";
