@@ -24,6 +24,7 @@
 
 #include <cuda_runtime.h>
 
+#include "chained.cuh"
 #include "dgemm.h"
 #include "i8_gemm.h"
 #include "internal.h"
@@ -90,6 +91,8 @@ template <typename T, int kTokens, int kUnroll>
 __global__ void __launch_bounds__(kDotWarps * 32) i8_dot_kernel(const I8Params p, int split)
 {
     __shared__ int32_t sums[kDotWarps][kDotRows * kTokens];
+    chain_wait();
+    chain_next();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int groups = kDotWarps / split;  // of kDotRows channels, in this block
     const int64_t n0 = (static_cast<int64_t>(blockIdx.x) * groups + warp / split) * kDotRows;
@@ -142,6 +145,8 @@ template <typename T, int kTiles, int kWarps>
 __global__ void __launch_bounds__(kWarps * 32) i8_decode_kernel(const I8Params p)
 {
     __shared__ int32_t sums[kWarps][kTiles * 8][kChannels];
+    chain_wait();
+    chain_next();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kChannels;
     // this thread's two channels and its tokens
@@ -191,8 +196,8 @@ template <typename T, int kTokens, int kUnroll>
 void launch_dot(const I8Params &p, int split, cudaStream_t stream)
 {
     const int64_t rows = kDotRows * (kDotWarps / split);
-    i8_dot_kernel<T, kTokens, kUnroll>
-        <<<static_cast<unsigned>((p.N + rows - 1) / rows), kDotWarps * 32, 0, stream>>>(p, split);
+    launch_chained(i8_dot_kernel<T, kTokens, kUnroll>, static_cast<unsigned>((p.N + rows - 1) / rows), kDotWarps * 32, 0,
+                   stream, 1, p, split);
 }
 
 template <typename T>
@@ -213,9 +218,9 @@ void launch_decode_tiles(const I8Params &p, int warps, cudaStream_t stream)
 {
     const unsigned grid = static_cast<unsigned>((p.N + kChannels - 1) / kChannels);
     if (warps == 8)
-        i8_decode_kernel<T, kTiles, 8><<<grid, 256, 0, stream>>>(p);
+        launch_chained(i8_decode_kernel<T, kTiles, 8>, grid, 256, 0, stream, 1, p);
     else
-        i8_decode_kernel<T, kTiles, 16><<<grid, 512, 0, stream>>>(p);
+        launch_chained(i8_decode_kernel<T, kTiles, 16>, grid, 512, 0, stream, 1, p);
 }
 
 template <typename T>

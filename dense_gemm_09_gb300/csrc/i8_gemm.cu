@@ -17,6 +17,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "chained.cuh"
 #include "dgemm.h"
 #include "i8_gemm.h"
 #include "internal.h"
@@ -86,6 +87,8 @@ template <typename T, int kW>
 __global__ void __launch_bounds__(kThreads) i8_mma_kernel(const I8Params p, int64_t tiles_n)
 {
     __shared__ __align__(16) uint8_t sa[kTile * kPitch], sb[kTile * kPitch];
+    chain_wait();
+    chain_next();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int64_t m0 = blockIdx.x / tiles_n * kTile, n0 = blockIdx.x % tiles_n * kTile;
     const int wm = (warp & 1) * 32, wn = (warp >> 1) * 32;
@@ -167,14 +170,14 @@ const char *launch_mma(const I8Params &p, cudaStream_t stream)
                p.lda % to == 0 && p.ldb % to == 0;
     };
     if (on(16)) {
-        i8_mma_kernel<T, 16><<<grid, kThreads, 0, stream>>>(p, tiles_n);
+        launch_chained(i8_mma_kernel<T, 16>, grid, kThreads, 0, stream, 1, p, tiles_n);
         return "i8_mma_64x64x64_ld16";
     }
     if (on(4)) {
-        i8_mma_kernel<T, 4><<<grid, kThreads, 0, stream>>>(p, tiles_n);
+        launch_chained(i8_mma_kernel<T, 4>, grid, kThreads, 0, stream, 1, p, tiles_n);
         return "i8_mma_64x64x64_ld4";
     }
-    i8_mma_kernel<T, 1><<<grid, kThreads, 0, stream>>>(p, tiles_n);
+    launch_chained(i8_mma_kernel<T, 1>, grid, kThreads, 0, stream, 1, p, tiles_n);
     return "i8_mma_64x64x64_ld1";
 }
 

@@ -27,6 +27,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "chained.cuh"
 #include "dgemm.h"
 #include "internal.h"
 
@@ -317,6 +318,8 @@ __global__ void __launch_bounds__(kMost < 128 ? 128 : kMost, kMost < 128 ? 6 : 1
     const int threads = kWarp ? 32 : static_cast<int>(blockDim.x);
     __shared__ float s_sum[32];
     __shared__ uint32_t s_max[32];
+    chain_wait();
+    chain_next();
     const int64_t row = kWarp ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5) : blockIdx.x;
     if (row >= p.rows) return;  // (whole warps; a block of one row never leaves here)
     const int t = static_cast<int>(kWarp ? threadIdx.x & 31 : threadIdx.x);
@@ -381,6 +384,8 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(const RowParams p)
     constexpr int kThreads = 1024;
     __shared__ float s_sum[32];
     __shared__ uint32_t s_max[32];
+    chain_wait();
+    chain_next();
     const int64_t row = blockIdx.x;
     auto value = [&](int64_t c, int n, float (&v)[kVec]) {
         combine<kOp>(p, load_raw<T, kAligned>(static_cast<const T *>(p.x) + row * p.ldx + c, n),
@@ -445,6 +450,8 @@ __global__ void __launch_bounds__(256)
     dequantize_kernel(uint32_t rows, int64_t cols, const int8_t *__restrict__ q, int64_t ldq,
                       const float *__restrict__ scale, T *__restrict__ x, int64_t ldx, uint32_t pieces)
 {
+    chain_wait();
+    chain_next();
     const uint32_t total = rows * pieces;
     for (uint32_t i = blockIdx.x * 256u + threadIdx.x; i < total; i += gridDim.x * 256u) {
         const uint32_t row = i / pieces;
@@ -482,7 +489,7 @@ void launch_rows(const RowParams &p, cudaStream_t stream)
     // threads: a warp for each 32 * kVecs vectors
     const unsigned threads = kMost == 32 ? 128u : static_cast<unsigned>((vecs + 32 * kVecs - 1) / (32 * kVecs) * 32);
     const unsigned grid = static_cast<unsigned>(kMost == 32 ? (p.rows + 3) / 4 : p.rows);
-    rows_kernel<kOp, T, kAligned, kMost, kVecs><<<grid, threads, 0, stream>>>(p);
+    launch_chained(rows_kernel<kOp, T, kAligned, kMost, kVecs>, grid, threads, 0, stream, 1, p);
 }
 
 // Four vectors a thread where there are rows enough to fill the SMs; work that
@@ -497,7 +504,7 @@ const char *launch_rows_by_length(const RowParams &p, cudaStream_t stream)
     const int64_t wide = p.rows * (vecs <= 1024 ? vecs : (vecs + 1) / 2);  // threads
     const bool few = wide <= kResident;
     if (vecs > 4096) {
-        long_rows_kernel<kOp, T, kAligned><<<static_cast<unsigned>(p.rows), 1024, 0, stream>>>(p);
+        launch_chained(long_rows_kernel<kOp, T, kAligned>, static_cast<unsigned>(p.rows), 1024, 0, stream, 1, p);
         return "i8_long_rows";
     }
     if (few && vecs > 32 && vecs <= 1024)
@@ -561,8 +568,8 @@ const char *launch_dequantize_typed(int64_t rows, int64_t cols, const int8_t *q,
         const int64_t want = (n * pieces + 255) / 256;
         const unsigned grid = static_cast<unsigned>(want < cap ? want : cap);
         auto kernel = vec ? dequantize_kernel<T, true> : dequantize_kernel<T, false>;
-        kernel<<<grid, 256, 0, stream>>>(static_cast<uint32_t>(n), cols, q + r * ldq, ldq, scale + r,
-                                         static_cast<T *>(x) + r * ldx, ldx, static_cast<uint32_t>(pieces));
+        launch_chained(kernel, grid, 256, 0, stream, 1, static_cast<uint32_t>(n), cols, q + r * ldq, ldq, scale + r,
+                       static_cast<T *>(x) + r * ldx, ldx, static_cast<uint32_t>(pieces));
     }
     return "i8_dequantize";
 }

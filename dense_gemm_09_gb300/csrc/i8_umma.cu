@@ -52,6 +52,7 @@
 #include <cuda_runtime.h>
 
 #include "bounded_wait.cuh"
+#include "chained.cuh"
 #include "dgemm.h"
 #include "i8_gemm.h"
 #include "internal.h"
@@ -991,6 +992,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::mbar_init(ptx::smem_addr(&ctrl->raw_empty[s]), 16);
             }
             ptx::fence_mbarrier_init();
+            chain_wait();  // (everything below reads or writes the call's operands)
             loaded = prefill<kCtas>(&tmap_r, &tmap_c, p, raw, ctrl, rank);
         }
         loaded = __reduce_max_sync(0xFFFFFFFFu, loaded);
@@ -1023,6 +1025,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // cross-CTA signal
     if constexpr (kCtas == 2) cluster_meet();
     ptx::tc_fence_after();
+    chain_wait();
+    chain_next();
     const uint32_t tmem_base = ctrl->tmem_base;
     WaitCtl *wc = &ctrl->wait;
 
@@ -1178,19 +1182,8 @@ bool launch(const I8Params &c, int bn, int splitk, cudaStream_t stream)
     const uint64_t stall = take_injected_stall();
     p.inject_stall = stall ? 1 : 0;
     p.wait_limit_ns = stall ? stall : kWaitLimitNs;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(cluster * std::min<int64_t>(tiles, fit)));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, i8_umma_kernel<kCtas, kSwap, T>, mr, mc, mo, p) != cudaSuccess) {
+    if (launch_chained(i8_umma_kernel<kCtas, kSwap, T>, static_cast<unsigned>(cluster * std::min<int64_t>(tiles, fit)), kThreads,
+                       smem, stream, static_cast<unsigned>(cluster), mr, mc, mo, p) != cudaSuccess) {
         cudaGetLastError();
         return false;
     }
