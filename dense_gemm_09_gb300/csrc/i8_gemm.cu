@@ -9,6 +9,7 @@
 // loads are in flight while a chunk is multiplied); mma.sync m16n8k32 on
 // int8 with exact int32 sums.
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 #include <string>
@@ -197,9 +198,7 @@ bool tma_ok(const I8Params &p)
 // Estimated times in us, fitted to GB300 sweeps of every kernel over 8 shapes
 // of B x 19 numbers of tokens (1 .. 4096); the smallest estimate runs.
 //
-// 1 to 4 tokens take the dot-product kernel, whose split gives it ~2000 warps
-// (4000 from 3 tokens on, which have fewer loads in flight each) of at most
-// 4096 K values.  5 to 8 tokens take the mma.sync kernel, which nothing else
+// 1 to 4 tokens take the dot-product kernel.  5 to 8 tokens take the mma.sync kernel, which nothing else
 // came near.
 struct Candidate {
     double us;
@@ -222,12 +221,24 @@ double stage_us(bool pair, int bn)
     return p[0].us + (p[1].us - p[0].us) * (bn - p[0].bn) / (p[1].bn - p[0].bn);
 }
 
-I8Config dot_config(const I8Params &p)
+// Blocks of 32 / split channels in whole waves of three an SM: a launch of 0.6
+// or of 1.1 waves leaves memory idle at its end (8192 x 4096: split 1 and 4,
+// 256 and 1024 blocks, 7.9 and 6.8 us; 16384 x 4096: 1 and 2, 14.5 and 13.1).
+I8Config dot_config(const I8Params &p, int sm_count)
 {
-    const int64_t groups = (p.N + 3) / 4, want = p.M > 2 ? 4096 : 2048;
-    int split = 1;
-    while (split < 8 && (groups * split < want || p.K > 4096 * split)) split *= 2;
-    return {kI8Dot, 0, split};
+    if (p.N <= 1024) return {kI8Dot, 0, 8};
+    int best = 1;
+    double best_score = -1.0;
+    for (int split = 1, bits = 0; split <= 4; split *= 2, ++bits) {
+        if (split > 1 && p.K < 512 * split) break;  // a turn for every warp
+        const double waves = static_cast<double>((p.N * split + 31) / 32) / (3.0 * sm_count);
+        const double score = waves / std::ceil(waves) - 0.08 * bits;
+        if (score > best_score) {
+            best_score = score;
+            best = split;
+        }
+    }
+    return {kI8Dot, 0, best};
 }
 
 // mma.sync: ~20 clocks of an SM for each product of 16 channels x 8 tokens x
@@ -245,7 +256,7 @@ Candidate decode_candidate(const I8Params &p)
 I8Config choose_config(const I8Params &p, int sm_count, bool (*fits)(const I8Params &, const I8Config &))
 {
     if (p.K < (1 << 17)) {
-        if (p.M <= 4) return dot_config(p);
+        if (p.M <= 4) return dot_config(p, sm_count);
         if (p.M <= 8) return decode_candidate(p).cfg;
     }
     const int64_t kb = (p.K + 127) / 128;
