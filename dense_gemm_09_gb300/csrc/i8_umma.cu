@@ -630,6 +630,27 @@ __device__ __forceinline__ void load_scaled(const Params &p, uint32_t taddr, uin
     }
 }
 
+// v += beta * old for sixteen columns of a row of C (`left` of them in C), whose
+// rows start on 16-byte boundaries.
+template <typename T>
+__device__ __forceinline__ void add_old(const T *c, int64_t left, float beta, float (&v)[16])
+{
+    if (left >= 16 && DGEMM_CHECK((reinterpret_cast<uintptr_t>(c) & 15u) == 0)) {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) {
+            constexpr int kPer = 16 / sizeof(T);
+            const uint4 w = reinterpret_cast<const uint4 *>(c)[i];
+            const T *e = reinterpret_cast<const T *>(&w);
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) v[i * kPer + j] = fmaf(beta, i8_to_f32(e[j]), v[i * kPer + j]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        if (e < left) v[e] = fmaf(beta, i8_to_f32(c[e]), v[e]);
+}
+
 // A warp's share of a tile's columns: every step-th piece from `first`, staged
 // in `boxes` boxes at `box`.
 struct Share {
@@ -670,11 +691,7 @@ __device__ __forceinline__ void drain_tokens(const Params &p, const CUtensorMap 
             for (int part = 0; part < kCols / 16; ++part) {  // (rolled: its code is fetched cold)
                 float v[16];
                 load_scaled(p, taddr, scale, bias, b * kCols + part * 16, sa, v);
-                if (beta != 0.f && row < p.rows) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (col0 + part * 16 + e < p.cols) v[e] = fmaf(beta, i8_to_f32(crow[col0 + part * 16 + e]), v[e]);
-                }
+                if (beta != 0.f && row < p.rows) add_old(crow + col0 + part * 16, p.cols - col0 - part * 16, beta, v);
                 constexpr int kPer = 16 / sizeof(T);  // values of a 16-byte word
 #pragma unroll
                 for (int j = 0; j < 16; j += kPer) {
