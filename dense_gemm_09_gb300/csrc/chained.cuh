@@ -26,14 +26,21 @@ __device__ __forceinline__ void chain_next()
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+inline cudaLaunchAttribute chained_attribute()
+{
+    cudaLaunchAttribute a = {};
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    return a;
+}
+
 // `cluster` CTAs to a cluster (1: none).
 template <typename... Params, typename... Args>
 cudaError_t launch_chained(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
                            unsigned cluster, Args &&...args)
 {
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[0] = chained_attribute();
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = cluster;
     attr[1].val.clusterDim.y = 1;

@@ -49,8 +49,10 @@ __device__ __forceinline__ void store_one(const I8Params &p, int64_t row, int64_
     *dst = i8_from_f32<T>(v);
 }
 
-// The 32 bytes of one thread's half row of a chunk, as kW-byte loads; bytes
-// past the row's end (left) or of rows outside the matrix are zeros.
+// The 32 bytes of one thread's half row of a chunk, as kW-byte loads (1: as the
+// aligned words around them, shifted into place: every word holds a byte of
+// the matrix); bytes past the row's end (left) or of rows outside the matrix
+// are zeros.
 template <int kW>
 __device__ __forceinline__ void load_half_row(const int8_t *p, bool row_ok, int64_t left, uint32_t (&w)[8])
 {
@@ -63,6 +65,19 @@ __device__ __forceinline__ void load_half_row(const int8_t *p, bool row_ok, int6
     if (row_ok && left >= 32 && kW == 4) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
+        return;
+    }
+    if (row_ok && left >= 32 && kW == 1) {
+        const uint32_t shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u) * 8u;
+        const uint32_t *a = reinterpret_cast<const uint32_t *>(p - shift / 8);
+        uint32_t lo = __ldg(a);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            // the last word only if the 32 bytes reach into it
+            const uint32_t hi = i < 7 || shift ? __ldg(a + i + 1) : 0u;
+            w[i] = __funnelshift_r(lo, hi, shift);
+            lo = hi;
+        }
         return;
     }
 #pragma unroll

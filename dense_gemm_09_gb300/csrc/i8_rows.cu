@@ -444,8 +444,8 @@ __device__ __forceinline__ float byte_to_f32(uint32_t u, int k)
 // A thread's piece: two vectors of one row, 16 bytes of q.
 constexpr int kPiece = 2 * kVec;
 
-// `pieces` to a row; rows * pieces is below 2^31.
-template <typename T, bool kAligned>
+// `pieces` to a row; rows * pieces is below 2^31.  q and x on 16-byte rows.
+template <typename T>
 __global__ void __launch_bounds__(256)
     dequantize_kernel(uint32_t rows, int64_t cols, const int8_t *__restrict__ q, int64_t ldq,
                       const float *__restrict__ scale, T *__restrict__ x, int64_t ldx, uint32_t pieces)
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(256)
         T *dst = x + row * ldx + c;
         const float s = __ldg(scale + row);
         alignas(16) int8_t e[kPiece];
-        if (kAligned && left >= kPiece) {
+        if (left >= kPiece) {
             *reinterpret_cast<uint4 *>(e) = __ldcs(reinterpret_cast<const uint4 *>(src));
         } else {
 #pragma unroll
@@ -475,7 +475,31 @@ __global__ void __launch_bounds__(256)
             for (int k = 0; k < kVec; ++k) v[k] = byte_to_f32(w[h * 2 + k / 4] ^ 0x80808080u, k & 3) * s;
             const int64_t l = left - h * kVec;
             const int n = l >= kVec ? kVec : l > 0 ? static_cast<int>(l) : 0;
-            if (DGEMM_CHECK(row < rows && c + h * kVec + n <= cols || n == 0)) store_vec<T, kAligned>(dst + h * kVec, n, v);
+            if (DGEMM_CHECK((row < rows && c + h * kVec + n <= cols) || n == 0))
+                store_vec<T, true>(dst + h * kVec, n, v);
+        }
+    }
+}
+
+// Rows of any alignment: element by element, consecutive threads on
+// consecutive columns; blocks of 1024 columns, rows over the grid's other
+// dimension.
+constexpr int kAnyCols = 1024;
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+    dequantize_any_kernel(int64_t rows, int64_t cols, const int8_t *__restrict__ q, int64_t ldq,
+                          const float *__restrict__ scale, T *__restrict__ x, int64_t ldx)
+{
+    chain_wait();
+    chain_next();
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kAnyCols + threadIdx.x;
+    for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+        const float s = __ldg(scale + row);
+#pragma unroll
+        for (int k = 0; k < kAnyCols / 256; ++k) {
+            const int64_t c = c0 + k * 256;
+            if (c < cols && DGEMM_CHECK(row >= 0)) x[row * ldx + c] = from_f32<T>(static_cast<float>(q[row * ldq + c]) * s);
         }
     }
 }
@@ -558,18 +582,30 @@ template <typename T>
 const char *launch_dequantize_typed(int64_t rows, int64_t cols, const int8_t *q, int64_t ldq, const float *scale,
                                     void *x, int64_t ldx, cudaStream_t stream, const DeviceInfo &dev)
 {
+    T *out = static_cast<T *>(x);
+    if (!aligned(q, ldq, 1, 16) || !aligned(x, ldx, sizeof(T), 16)) {
+        const int64_t across = (cols + kAnyCols - 1) / kAnyCols;
+        if (across > INT32_MAX) return nullptr;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(across), static_cast<unsigned>(rows < 65535 ? rows : 65535));
+        cfg.blockDim = dim3(256);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr = chained_attribute();
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        cudaLaunchKernelEx(&cfg, dequantize_any_kernel<T>, rows, cols, q, ldq, scale, out, ldx);
+        return "i8_dequantize_any";
+    }
     const int64_t pieces = (cols + kPiece - 1) / kPiece;
     if (pieces > INT32_MAX) return nullptr;
     const int64_t cap = static_cast<int64_t>(dev.sm_count) * 32;
     const int64_t most = INT32_MAX / pieces;  // rows of one launch: 32-bit piece numbers
-    const bool vec = aligned(q, ldq, 1, 16) && aligned(x, ldx, sizeof(T), 16);
     for (int64_t r = 0; r < rows; r += most) {
         const int64_t n = rows - r < most ? rows - r : most;
         const int64_t want = (n * pieces + 255) / 256;
         const unsigned grid = static_cast<unsigned>(want < cap ? want : cap);
-        auto kernel = vec ? dequantize_kernel<T, true> : dequantize_kernel<T, false>;
-        launch_chained(kernel, grid, 256, 0, stream, 1, static_cast<uint32_t>(n), cols, q + r * ldq, ldq, scale + r,
-                       static_cast<T *>(x) + r * ldx, ldx, static_cast<uint32_t>(pieces));
+        launch_chained(dequantize_kernel<T>, grid, 256, 0, stream, 1, static_cast<uint32_t>(n), cols, q + r * ldq, ldq,
+                       scale + r, out + r * ldx, ldx, static_cast<uint32_t>(pieces));
     }
     return "i8_dequantize";
 }
