@@ -113,8 +113,9 @@ def _load(path: str):
     L.rmsnorm_i8.argtypes = [i64, i64, vp, i64, vp, i64, vp, ci, f32, ci, vp, i64, vp, i64, vp, vp]
     L.swiglu_i8.argtypes = [i64, i64, vp, i64, vp, i64, ci, vp, i64, vp, vp]
     L.dequantize_i8.argtypes = [i64, i64, vp, i64, vp, vp, i64, ci, vp]
-    for name in ("gemm_i8_tn", "quantize_i8", "rmsnorm_i8", "swiglu_i8", "dequantize_i8"):
+    for name in _I8_CALLS:
         getattr(L, name).restype = ci
+    L.i8_entry = {name: ctypes.cast(getattr(L, name), vp).value for name in _I8_CALLS}
     L.dgemm_test_pair_units.argtypes = [i64, i64, i64, i64, i64, vp, i64]
     L.dgemm_test_pair_units.restype = i64
     L.dgemm_test_stream_k_tiles.argtypes = [i64, i64, i64, ci, ci]
@@ -185,15 +186,18 @@ def _mat(t: torch.Tensor, name: str, dtype: torch.dtype):
     return t.data_ptr(), max(ld, cols)
 
 
-# the current stream's handle without a Stream object around it (~3 us a call)
+# a device's current stream as a handle, without a Stream object around it
+# (which costs ~3 us a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current_stream(device: int) -> int:
+    return _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 def _stream(stream) -> int:
     if stream is None:
-        if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
-        stream = torch.cuda.current_stream()
+        return _current_stream(torch.cuda.current_device())
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
@@ -324,71 +328,41 @@ def gemm_bf16_nn(A, B, C, alpha: float = 1.0, beta: float = 0.0, stream=None):
 # ---- linear layers in 8-bit integers
 #
 # These calls are small (a few microseconds of GPU time for one token), so
-# their checks are written to be cheap: one look at each attribute.
+# their tensors are read and checked in C (binding/i8_calls.c, built beside the
+# library); each function here names its arguments and passes them on with
+# the library's entry point.
 
-_TYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # dgemm_type
-_I8, _F32 = torch.int8, torch.float32
-
-
-def _rows(t, name: str, dtype):
-    """(address, pitch, shape) of a matrix of dtype."""
-    try:
-        shape, (ld, step) = t.shape, t.stride()
-        rows, cols = shape
-    except (AttributeError, TypeError, ValueError):
-        raise ValueError("%s must be a 2-D tensor" % name) from None
-    if t.dtype is not dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    if step != 1 and cols > 1:
-        raise ValueError("%s must have unit column stride" % name)
-    if ld < cols:
-        if rows > 1:
-            raise ValueError("%s has overlapping rows" % name)
-        ld = cols  # the pitch of a single row is never used
-    return t.data_ptr(), ld, shape
+_I8_CALLS = ("gemm_i8_tn", "quantize_i8", "rmsnorm_i8", "swiglu_i8", "dequantize_i8")
+_calls_module = None
 
 
-def _rows_float(t, name: str):
-    """_rows of a float matrix, its dtype and dgemm_type."""
-    dtype = getattr(t, "dtype", None)
-    code = _TYPE.get(dtype)
-    if code is None:
-        raise TypeError("%s must be a float32, float16 or bfloat16 tensor" % name)
-    p, ld, shape = _rows(t, name, dtype)
-    return p, ld, shape, dtype, code
+def _calls():
+    """The marshalling module, set up with this binding's types."""
+    global _calls_module
+    with _lock:
+        if _calls_module is None:
+            from importlib import import_module
+            try:
+                m = import_module("." + "_i8_calls", __name__)
+            except ImportError as e:
+                raise RuntimeError("_i8_calls is not built; run dense_gemm_09_gb300.build()") from e
+            m.setup(torch.float32, torch.float16, torch.bfloat16, torch.int8, getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device), _raw_stream or _current_stream,
+                    DgemmError)
+            _calls_module = m
+        return _calls_module
 
 
-def _rows_like(t, name: str, dtype, shape):
-    p, ld, got = _rows(t, name, dtype)
-    if got != shape:
-        raise ValueError("shape mismatch: %s %s, expected %s" % (name, tuple(got), tuple(shape)))
-    return p, ld
-
-
-def _vec(t, name: str, dtype, n: int) -> int:
-    if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.shape[0] != n:
-        raise ValueError("%s must be a 1-D tensor of %d" % (name, n))
-    if t.dtype is not dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if not t.is_cuda or (n > 1 and t.stride(0) != 1):
-        raise ValueError("%s must be a contiguous CUDA tensor" % name)
-    return t.data_ptr()
+def _i8(name: str):
+    """The module and the address of an entry point of the loaded library."""
+    return _calls_module or _calls(), (_lib or lib()).i8_entry[name]
 
 
 def quantize_i8(X, Q, scale, stream=None):
     """Each row of X (float32, float16 or bfloat16) as int8 with one FP32 scale:
     scale = max|x| / 127, Q = rint(x / scale).  Writes and returns (Q, scale);
     a row of zeros gets scale 0, a row with a NaN or an infinity scale NaN."""
-    px, ldx, shape, _, ty = _rows_float(X, "X")
-    pq, ldq = _rows_like(Q, "Q", _I8, shape)
-    rows, cols = shape
-    st = (_lib or lib()).quantize_i8(rows, cols, px, ldx, ty, pq, ldq, _vec(scale, "scale", _F32, rows),
-                                     _stream(stream))
-    if st:
-        raise DgemmError(st, "quantize_i8")
-    return Q, scale
+    m, entry = _i8("quantize_i8")
+    return m.quantize_i8(entry, X, Q, scale, stream)
 
 
 def rmsnorm_i8(X, gamma, Q, scale, residual=None, H=None, eps: float = 1e-6, stream=None):
@@ -396,62 +370,30 @@ def rmsnorm_i8(X, gamma, Q, scale, residual=None, H=None, eps: float = 1e-6, str
     int8 in Q with their FP32 scales.  H, if given, receives h in X's type (it
     may be X or residual itself).  gamma has X's type or float32.  Returns
     (Q, scale)."""
-    px, ldx, shape, dtype, ty = _rows_float(X, "X")
-    rows, cols = shape
-    pq, ldq = _rows_like(Q, "Q", _I8, shape)
-    pr, ldr = (None, 0) if residual is None else _rows_like(residual, "residual", dtype, shape)
-    ph, ldh = (None, 0) if H is None else _rows_like(H, "H", dtype, shape)
-    tg = _TYPE.get(getattr(gamma, "dtype", None), -1)
-    pg = _vec(gamma, "gamma", _F32 if tg == 0 else dtype, cols)
-    st = (_lib or lib()).rmsnorm_i8(rows, cols, px, ldx, pr, ldr, pg, tg, eps, ty, ph, ldh, pq, ldq,
-                                    _vec(scale, "scale", _F32, rows), _stream(stream))
-    if st:
-        raise DgemmError(st, "rmsnorm_i8")
-    return Q, scale
+    m, entry = _i8("rmsnorm_i8")
+    return m.rmsnorm_i8(entry, X, gamma, Q, scale, residual, H, eps, stream)
 
 
 def swiglu_i8(G, U, Q, scale, stream=None):
     """y = G / (1 + exp(-G)) * U; the rows of y as int8 in Q with their FP32
     scales.  G and U may be column slices of one tensor.  Returns (Q, scale)."""
-    pg, ldg, shape, dtype, ty = _rows_float(G, "G")
-    pu, ldu = _rows_like(U, "U", dtype, shape)
-    pq, ldq = _rows_like(Q, "Q", _I8, shape)
-    rows, cols = shape
-    st = (_lib or lib()).swiglu_i8(rows, cols, pg, ldg, pu, ldu, ty, pq, ldq, _vec(scale, "scale", _F32, rows),
-                                   _stream(stream))
-    if st:
-        raise DgemmError(st, "swiglu_i8")
-    return Q, scale
+    m, entry = _i8("swiglu_i8")
+    return m.swiglu_i8(entry, G, U, Q, scale, stream)
 
 
 def dequantize_i8(Q, scale, X, stream=None):
     """X = Q * scale (a scale for each row), rounded once to X's type."""
-    px, ldx, shape, _, ty = _rows_float(X, "X")
-    pq, ldq = _rows_like(Q, "Q", _I8, shape)
-    rows, cols = shape
-    st = (_lib or lib()).dequantize_i8(rows, cols, pq, ldq, _vec(scale, "scale", _F32, rows), px, ldx, ty,
-                                       _stream(stream))
-    if st:
-        raise DgemmError(st, "dequantize_i8")
-    return X
+    m, entry = _i8("dequantize_i8")
+    return m.dequantize_i8(entry, Q, scale, X, stream)
 
 
 def gemm_i8_tn(A, B, C, scale_a, scale_b, bias=None, beta: float = 0.0, stream=None):
     """C[m, n] = scale_a[m] * scale_b[n] * (A @ B.T)[m, n] + bias[n] + beta * C[m, n];
     A: M x K and B: N x K int8, C: M x N float32, float16 or bfloat16; scales
-    and bias float32."""
-    pc, ldc, (M, N), _, ty = _rows_float(C, "C")
-    pa, lda, (Ma, K) = _rows(A, "A", _I8)
-    pb, ldb, (Nb, Kb) = _rows(B, "B", _I8)
-    if Ma != M or Nb != N or Kb != K:
-        raise ValueError("shape mismatch: A %s, B %s, C %s" % (tuple(A.shape), tuple(B.shape), tuple(C.shape)))
-    st = (_lib or lib()).gemm_i8_tn(M, N, K, pa, lda, _vec(scale_a, "scale_a", _F32, M), pb, ldb,
-                                    _vec(scale_b, "scale_b", _F32, N),
-                                    None if bias is None else _vec(bias, "bias", _F32, N), beta, pc, ldc, ty,
-                                    _stream(stream))
-    if st:
-        raise DgemmError(st, "gemm_i8_tn")
-    return C
+    and bias float32.  Rows on 16-byte boundaries (any length K; pad the
+    pitch) take the fast kernels."""
+    m, entry = _i8("gemm_i8_tn")
+    return m.gemm_i8_tn(entry, A, B, C, scale_a, scale_b, bias, beta, stream)
 
 
 # Kernels for tune_i8_next (see dgemm_tune_i8_next in include/dgemm.h)

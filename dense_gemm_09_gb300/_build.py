@@ -8,7 +8,8 @@ device, primary context -- of the process that loads it).
 The checked build (libdgemm_checked.so, objects under _build/checked/) is
 the same sources compiled with -DDGEMM_CHECKED: device-side bounds checks on
 the indices the kernels compute (see csrc/checked.cuh).  build_all() compiles
-both libraries' units at once.
+both libraries' units at once, and the CPython module that marshals the 8-bit
+calls (binding/i8_calls.c -> _i8_calls.so, by gcc).
 """
 from __future__ import annotations
 
@@ -17,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,6 +27,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdgemm.so")
 LIB_CHECKED = os.path.join(PKG, "libdgemm_checked.so")
+CALLS_SRC = os.path.join(PKG, "binding", "i8_calls.c")
+CALLS = os.path.join(PKG, "_i8_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
@@ -63,6 +67,17 @@ def _variant(checked: bool):
     return LIB, BUILD, []
 
 
+def build_calls(force: bool = False) -> str:
+    """Compile the CPython module of the 8-bit calls against this interpreter's
+    headers."""
+    if force or not os.path.exists(CALLS) or os.path.getmtime(CALLS) < os.path.getmtime(CALLS_SRC):
+        tmp = CALLS + ".tmp%d" % os.getpid()
+        subprocess.check_call(["gcc", "-O2", "-std=c11", "-Wall", "-fPIC", "-shared",
+                               "-I" + sysconfig.get_paths()["include"], "-o", tmp, CALLS_SRC])
+        os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build_all(variants=(False, True), force: bool = False, verbose: bool = False,
               extra_flags: list[str] | None = None) -> list[str]:
     """Compile the requested builds (False: libdgemm.so, True: the checked
@@ -95,6 +110,7 @@ def build_all(variants=(False, True), force: bool = False, verbose: bool = False
                 print(out, file=sys.stderr)
     if failed:
         raise RuntimeError("nvcc failed:\n" + "\n".join(failed))
+    build_calls(force)
     for lib, objs, _ in jobs:
         tmp = lib + ".tmp%d" % os.getpid()
         subprocess.check_call([cc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs])

@@ -68,5 +68,35 @@ def test_optional_pointers(L):
 
 def test_types_are_what_the_header_says(L):
     import dense_gemm_09_gb300 as dg
-    assert dg._TYPE == {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
     assert L.gemm_i8_tn.restype is ctypes.c_int
+    assert all(dg.lib().i8_entry[n] for n in CALLS)
+
+
+def test_binding_checks_tensors_before_the_device(L):
+    # CPU tensors reach the checks of the marshalling module, not the library
+    import dense_gemm_09_gb300 as dg
+    x, q, s = torch.ones((2, 8)), torch.zeros((2, 8), dtype=torch.int8), torch.zeros(2)
+    with pytest.raises(ValueError, match="X must be a CUDA tensor"):
+        dg.quantize_i8(x, q, s)
+    with pytest.raises(ValueError, match="X must be a 2-D tensor"):
+        dg.quantize_i8(x[0], q, s)
+    with pytest.raises(TypeError, match="X must be a float32, float16 or bfloat16 tensor"):
+        dg.quantize_i8(q, q, s)
+    with pytest.raises(TypeError, match="X must be a float32"):
+        dg.dequantize_i8(q, s, None)
+    with pytest.raises(TypeError, match="X must be"):
+        dg.rmsnorm_i8([1.0], s, q, s)
+    with pytest.raises(TypeError, match="C must be"):
+        dg.gemm_i8_tn(q, q, q, s, s)
+    with pytest.raises(TypeError):
+        dg._calls().quantize_i8(1, x)  # too few arguments
+
+
+def test_binding_fails_loudly_without_the_marshalling_module(monkeypatch):
+    import sys
+
+    import dense_gemm_09_gb300 as dg
+    monkeypatch.setattr(dg, "_calls_module", None)
+    monkeypatch.setitem(sys.modules, "dense_gemm_09_gb300._i8_calls", None)
+    with pytest.raises(RuntimeError, match="not built"):
+        dg.quantize_i8(None, None, None)
