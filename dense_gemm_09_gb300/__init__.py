@@ -343,11 +343,12 @@ def _calls():
         if _calls_module is None:
             from importlib import import_module
             try:
-                m = import_module("." + "_i8_calls", __name__)
+                m = import_module("._i8_calls", __name__)
             except ImportError as e:
                 raise RuntimeError("_i8_calls is not built; run dense_gemm_09_gb300.build()") from e
-            m.setup(torch.float32, torch.float16, torch.bfloat16, torch.int8, getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device), _raw_stream or _current_stream,
-                    DgemmError)
+            m.setup(torch.float32, torch.float16, torch.bfloat16, torch.int8,
+                    getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+                    _raw_stream or _current_stream, DgemmError)
             _calls_module = m
         return _calls_module
 

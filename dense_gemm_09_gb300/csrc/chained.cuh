@@ -8,8 +8,14 @@
 // ever; only the launch itself, and what a kernel sets up before the call
 // (barriers, tensor memory), lie beside the previous kernel.  chain_next()
 // lets the next such launch begin as soon as all blocks of this one run.
+//
+// So an operand of such a kernel may be written while the kernel already runs,
+// and the non-coherent loads (ld.global.nc, __ldg, const __restrict__
+// parameters), which may count on read-only data and move across the wait, do
+// not fit: the kernels load through the functions here, which stay behind it.
 #pragma once
 
+#include <cstdint>
 #include <utility>
 
 #include <cuda_runtime.h>
@@ -24,6 +30,36 @@ __device__ __forceinline__ void chain_wait()
 __device__ __forceinline__ void chain_next()
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+__device__ __forceinline__ float load_f32(const float *p)
+{
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t load_u32(const uint32_t *p)
+{
+    uint32_t v;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
+// kOnce: the bytes are not read again (not kept in L1).
+template <bool kOnce = false>
+__device__ __forceinline__ uint4 load_v4(const void *p)
+{
+    uint4 v;
+    if constexpr (kOnce)
+        asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(p));
+    else
+        asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(p));
+    return v;
 }
 
 inline cudaLaunchAttribute chained_attribute()

@@ -20,6 +20,7 @@
 // At 3 to 7 bytes an element the instructions count too (an SM has ~8 of them
 // for each of its threads' elements at HBM speed), hence the packed
 // conversions, the three-input maximum and the rounding by one FMA below.
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
@@ -101,7 +102,7 @@ __device__ __forceinline__ Raw<T> load_raw(const T *p, int n)
     if (kAligned && n == kVec) {
 #pragma unroll
         for (int i = 0; i < Raw<T>::kWords; ++i)
-            r.w[i] = kKeep ? __ldg(reinterpret_cast<const uint4 *>(p) + i) : __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+            r.w[i] = kKeep ? load_v4(reinterpret_cast<const uint4 *>(p) + i) : __ldcs(reinterpret_cast<const uint4 *>(p) + i);
         return r;
     }
     alignas(16) T e[kVec];
@@ -267,6 +268,26 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t *shared)
     return __reduce_max_sync(0xFFFFFFFFu, v);
 }
 
+// Both at once: one meeting of the row's threads instead of two.
+template <bool kWarp>
+__device__ __forceinline__ void row_sum_max(float &sum, uint32_t &most, float *s_sum, uint32_t *s_max)
+{
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if constexpr (kWarp) return;
+    if ((threadIdx.x & 31) == 0) {
+        s_sum[threadIdx.x >> 5] = sum;
+        s_max[threadIdx.x >> 5] = most;
+    }
+    __syncthreads();
+    const bool in = (threadIdx.x & 31) < (blockDim.x >> 5);
+    sum = in ? s_sum[threadIdx.x & 31] : 0.f;
+    most = __reduce_max_sync(0xFFFFFFFFu, in ? s_max[threadIdx.x & 31] : 0u);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+}
+
 // g / (1 + exp(-g)).  The fast division is within 2 ulp up to 2^126 and gives
 // 0 above, where the quotient is below 1e-35 anyway.
 __device__ __forceinline__ float silu(float g)
@@ -309,6 +330,57 @@ __device__ __forceinline__ int vec_len(int64_t cols, int64_t c)
     return left >= kVec ? kVec : left > 0 ? static_cast<int>(left) : 0;
 }
 
+// A row held by its threads, from its values before the norm / quantisation to
+// H, the scale and q.  weights(j, g) gives the norm's weights of vector j.
+template <int kOp, typename T, bool kAligned, bool kWarp, int kVecs, typename W>
+__device__ __forceinline__ void finish_row(const RowParams &p, int64_t row, int t, int threads, const int (&n)[kVecs],
+                                           float (&v)[kVecs][kVec], const W &weights, float *s_sum, uint32_t *s_max)
+{
+    const int cols = static_cast<int>(p.cols);
+    float amax = 0.f;
+    if constexpr (is_norm(kOp)) {
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            const int c = (j * threads + t) * kVec;
+            if (p.h) store_vec<T, kAligned>(static_cast<T *>(p.h) + row * p.ldh + c, n[j], v[j]);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) ss = fmaf(v[j][i], v[j][i], ss);
+        }
+        // neither the weights nor the maximum wait for the sum: rounding is
+        // monotone, so the largest |v g rstd| is the largest |v g| times rstd
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            float g[kVec];
+            weights(j, g);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) v[j][i] *= g[i];
+            amax = max_abs(amax, v[j]);
+        }
+        uint32_t most = __float_as_uint(amax) & 0x7FFFFFFFu;
+        row_sum_max<kWarp>(ss, most, s_sum, s_max);
+        const float rstd = rsqrtf(ss / static_cast<float>(cols) + p.eps);
+        // a sum of squares past FP32's range marks the row like a NaN in it
+        amax = ss < __uint_as_float(0x7F800000u) ? __uint_as_float(most) * rstd : __uint_as_float(0x7FC00000u);
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) v[j][i] *= rstd;
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) amax = max_abs(amax, v[j]);
+        amax = __uint_as_float(row_max<kWarp>(__float_as_uint(amax) & 0x7FFFFFFFu, s_max));
+    }
+    const Quantiser qz(__float_as_uint(amax) & 0x7FFFFFFFu);
+    if (t == 0) p.scale[row] = qz.scale;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+        const int c = (j * threads + t) * kVec;
+        if (DGEMM_CHECK(n[j] == 0 || (row >= 0 && row < p.rows && c + n[j] <= cols)))
+            store_q<kAligned>(p.q + row * p.ldq + c, n[j], v[j], qz);
+    }
+}
+
 // One row a block of at most kMost threads, or (kMost == 32) a warp, four rows
 // a block: the row's values stay in registers, kVecs vectors a thread.
 template <int kOp, typename T, bool kAligned, int kMost, int kVecs>
@@ -325,7 +397,10 @@ __global__ void __launch_bounds__(kMost < 128 ? 128 : kMost, kMost < 128 ? 6 : 1
     const int t = static_cast<int>(kWarp ? threadIdx.x & 31 : threadIdx.x);
     const int cols = static_cast<int>(p.cols);
     int n[kVecs];  // this thread's elements of each vector, from column (j * threads + t) * kVec
-    Raw<T> x[kVecs], y[kVecs];
+    Raw<T> x[kVecs], y[kVecs], w[kVecs];
+    // the norm's weights in the rows' type come beside the row where registers
+    // are left for them
+    const bool early = is_norm(kOp) && kVecs <= 2 && (sizeof(T) == 4 || !p.gamma_f32);
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
         const int c = (j * threads + t) * kVec;
@@ -333,45 +408,110 @@ __global__ void __launch_bounds__(kMost < 128 ? 128 : kMost, kMost < 128 ? 6 : 1
         x[j] = load_raw<T, kAligned>(static_cast<const T *>(p.x) + row * p.ldx + c, n[j]);
         y[j] = load_second<kOp, T, kAligned>(p, row, c, n[j]);
     }
+    if (early) {
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j)
+            w[j] = load_raw<T, kAligned, true>(static_cast<const T *>(p.gamma) + (j * threads + t) * kVec, n[j]);
+    }
     float v[kVecs][kVec];
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) combine<kOp>(p, x[j], y[j], v[j]);
-    float amax = 0.f;
-    if constexpr (is_norm(kOp)) {
-        float ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-            const int c = (j * threads + t) * kVec;
-            if (p.h) store_vec<T, kAligned>(static_cast<T *>(p.h) + row * p.ldh + c, n[j], v[j]);
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) ss = fmaf(v[j][i], v[j][i], ss);
-        }
-        // the weights do not wait for the sum
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-            float g[kVec];
-            load_gamma<T, kAligned>(p, (j * threads + t) * kVec, n[j], g);
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) v[j][i] *= g[i];
-        }
-        ss = row_sum<kWarp>(ss, s_sum);
-        // a sum of squares past FP32's range marks the row like a NaN in it
-        if (!(ss < __uint_as_float(0x7F800000u))) amax = __uint_as_float(0x7FC00000u);
-        const float rstd = rsqrtf(ss / static_cast<float>(cols) + p.eps);
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j)
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) v[j][i] *= rstd;
-    }
-#pragma unroll
-    for (int j = 0; j < kVecs; ++j) amax = max_abs(amax, v[j]);
-    const Quantiser qz(row_max<kWarp>(__float_as_uint(amax) & 0x7FFFFFFFu, s_max));
-    if (t == 0) p.scale[row] = qz.scale;
+    finish_row<kOp, T, kAligned, kWarp, kVecs>(
+        p, row, t, threads, n, v,
+        [&](int j, float(&g)[kVec]) {
+            if (early)
+                unpack(w[j], g);
+            else
+                load_gamma<T, kAligned>(p, (j * threads + t) * kVec, n[j], g);
+        },
+        s_sum, s_max);
+}
+
+// 16 bytes from global to shared memory, of which `bytes` are read and the rest
+// are zeros, without a register in between.
+__device__ __forceinline__ void copy_async16(uint4 *dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(bytes)
+                 : "memory");
+}
+
+// As rows_kernel for many rows of a 16-bit type: a block (warp) takes one row
+// after another, and while it works on one, the next is on its way to shared
+// memory.  Each thread fetches the vectors that it will use itself, so that no
+// thread waits for another's; a slot is free again as soon as its thread has
+// read it.  The norm's weights (in the rows' type) stay in shared memory too.
+// 8192 rows of bf16, rows_kernel and this one: quantize of 8192 33.0 and 30.7
+// us, of 12288 58.9 and 46.1; swiglu of 8192 52.7 and 50.5, of 12288 85.4 and
+// 74.4; norm of 8192 43.6 and 39.4, of 12288 78.3 and 59.6.  The norm with
+// residual, which stores H too, does not gain (71.3 and 85.8).
+constexpr bool is_piped(int op)
+{
+    return op != kOpNorm;
+}
+
+template <int kOp, typename T, int kMost, int kVecs>
+__global__ void __launch_bounds__(kMost < 128 ? 128 : kMost, kMost < 128 ? 6 : 1024 / kMost)
+    piped_rows_kernel(const RowParams p)
+{
+    static_assert(sizeof(T) == 2, "a vector is one 16-byte word");
+    constexpr bool kWarp = kMost == 32;
+    constexpr int kInputs = has_second(kOp) ? 2 : 1;
+    extern __shared__ uint4 slots[];  // [input, then weights][vector][thread of the block]
+    const int threads = kWarp ? 32 : static_cast<int>(blockDim.x);
+    __shared__ float s_sum[2][32];  // by turns, so that one barrier a row is enough
+    __shared__ uint32_t s_max[2][32];
+    chain_wait();
+    chain_next();
+    const int64_t first = kWarp ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5) : blockIdx.x;
+    const int64_t step = kWarp ? static_cast<int64_t>(gridDim.x) * 4 : gridDim.x;
+    const int t = static_cast<int>(kWarp ? threadIdx.x & 31 : threadIdx.x);
+    const int cols = static_cast<int>(p.cols);
+    int n[kVecs];
+    auto slot = [&](int input, int j) { return slots + (input * kVecs + j) * static_cast<int>(blockDim.x) + threadIdx.x; };
+    const bool keep = is_norm(kOp) && !p.gamma_f32;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
         const int c = (j * threads + t) * kVec;
-        if (DGEMM_CHECK(n[j] == 0 || (row >= 0 && row < p.rows && c + n[j] <= cols)))
-            store_q<kAligned>(p.q + row * p.ldq + c, n[j], v[j], qz);
+        n[j] = max(0, min(kVec, cols - c));
+        if (keep) copy_async16(slot(kInputs, j), static_cast<const T *>(p.gamma) + (n[j] ? c : 0), n[j] * 2);
+    }
+    auto fetch = [&](int64_t row) {
+        if (row >= p.rows) return;
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            const int c = n[j] ? (j * threads + t) * kVec : 0, bytes = n[j] * 2;
+            copy_async16(slot(0, j), static_cast<const T *>(p.x) + row * p.ldx + c, bytes);
+            if constexpr (kInputs == 2) copy_async16(slot(1, j), static_cast<const T *>(p.y) + row * p.ldy + c, bytes);
+        }
+    };
+    fetch(first);
+    int turn = 0;
+    for (int64_t row = first; row < p.rows; row += step) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        float v[kVecs][kVec];
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            Raw<T> x, y{};
+            x.w[0] = *slot(0, j);
+            if constexpr (kInputs == 2) y.w[0] = *slot(1, j);
+            combine<kOp>(p, x, y, v[j]);
+        }
+        fetch(row + step);
+        finish_row<kOp, T, true, kWarp, kVecs>(
+            p, row, t, threads, n, v,
+            [&](int j, float(&g)[kVec]) {
+                if (keep) {
+                    Raw<T> w;
+                    w.w[0] = *slot(kInputs, j);
+                    unpack(w, g);
+                } else {
+                    load_gamma<T, true>(p, (j * threads + t) * kVec, n[j], g);
+                }
+            },
+            s_sum[turn], s_max[turn]);
+        turn ^= 1;
     }
 }
 
@@ -447,8 +587,8 @@ constexpr int kPiece = 2 * kVec;
 // `pieces` to a row; rows * pieces is below 2^31.  q and x on 16-byte rows.
 template <typename T>
 __global__ void __launch_bounds__(256)
-    dequantize_kernel(uint32_t rows, int64_t cols, const int8_t *__restrict__ q, int64_t ldq,
-                      const float *__restrict__ scale, T *__restrict__ x, int64_t ldx, uint32_t pieces)
+    dequantize_kernel(uint32_t rows, int64_t cols, const int8_t *q, int64_t ldq,
+                      const float *scale, T *x, int64_t ldx, uint32_t pieces)
 {
     chain_wait();
     chain_next();
@@ -459,7 +599,7 @@ __global__ void __launch_bounds__(256)
         const int64_t left = cols - c;
         const int8_t *src = q + row * ldq + c;
         T *dst = x + row * ldx + c;
-        const float s = __ldg(scale + row);
+        const float s = load_f32(scale + row);
         alignas(16) int8_t e[kPiece];
         if (left >= kPiece) {
             *reinterpret_cast<uint4 *>(e) = __ldcs(reinterpret_cast<const uint4 *>(src));
@@ -488,14 +628,14 @@ constexpr int kAnyCols = 1024;
 
 template <typename T>
 __global__ void __launch_bounds__(256)
-    dequantize_any_kernel(int64_t rows, int64_t cols, const int8_t *__restrict__ q, int64_t ldq,
-                          const float *__restrict__ scale, T *__restrict__ x, int64_t ldx)
+    dequantize_any_kernel(int64_t rows, int64_t cols, const int8_t *q, int64_t ldq,
+                          const float *scale, T *x, int64_t ldx)
 {
     chain_wait();
     chain_next();
     const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kAnyCols + threadIdx.x;
     for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
-        const float s = __ldg(scale + row);
+        const float s = load_f32(scale + row);
 #pragma unroll
         for (int k = 0; k < kAnyCols / 256; ++k) {
             const int64_t c = c0 + k * 256;
@@ -506,6 +646,37 @@ __global__ void __launch_bounds__(256)
 
 // ---- host side
 
+template <int kOp, int kVecs>
+constexpr size_t piped_smem(unsigned threads)
+{
+    return static_cast<size_t>((has_second(kOp) ? 2 : 1) + (is_norm(kOp) ? 1 : 0)) * kVecs * threads * 16;
+}
+
+// Blocks of this many threads of piped_rows_kernel that the current device runs at
+// once, cached; 0 if it cannot run.
+template <int kOp, typename T, int kMost, int kVecs>
+int piped_blocks(unsigned threads)
+{
+    constexpr int kMaxDevices = 64;
+    static std::atomic<int> cached[kMaxDevices][33];  // blocks + 1, by warps
+    int dev = 0;
+    if (threads > 1024 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+    std::atomic<int> &c = cached[dev][threads / 32];
+    int blocks = c.load(std::memory_order_relaxed) - 1;
+    if (blocks >= 0) return blocks;
+    auto kernel = piped_rows_kernel<kOp, T, kMost, kVecs>;
+    int sms = 0, per_sm = 0;
+    const bool ok = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(piped_smem<kOp, kVecs>(kMost < 128 ? 128 : kMost))) == cudaSuccess &&
+                    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
+                    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, static_cast<int>(threads),
+                                                                  piped_smem<kOp, kVecs>(threads)) == cudaSuccess;
+    blocks = ok ? sms * per_sm : 0;
+    cudaGetLastError();  // a failed query leaves no sticky error behind
+    c.store(blocks + 1, std::memory_order_relaxed);
+    return blocks;
+}
+
 template <int kOp, typename T, bool kAligned, int kMost, int kVecs>
 void launch_rows(const RowParams &p, cudaStream_t stream)
 {
@@ -513,6 +684,14 @@ void launch_rows(const RowParams &p, cudaStream_t stream)
     // threads: a warp for each 32 * kVecs vectors
     const unsigned threads = kMost == 32 ? 128u : static_cast<unsigned>((vecs + 32 * kVecs - 1) / (32 * kVecs) * 32);
     const unsigned grid = static_cast<unsigned>(kMost == 32 ? (p.rows + 3) / 4 : p.rows);
+    if constexpr (is_piped(kOp) && kAligned && sizeof(T) == 2 && kVecs == 4) {
+        const int resident = piped_blocks<kOp, T, kMost, kVecs>(threads);
+        if (resident > 0 && grid > static_cast<unsigned>(resident)) {
+            launch_chained(piped_rows_kernel<kOp, T, kMost, kVecs>, static_cast<unsigned>(resident), threads,
+                           piped_smem<kOp, kVecs>(threads), stream, 1, p);
+            return;
+        }
+    }
     launch_chained(rows_kernel<kOp, T, kAligned, kMost, kVecs>, grid, threads, 0, stream, 1, p);
 }
 
@@ -520,7 +699,8 @@ void launch_rows(const RowParams &p, cudaStream_t stream)
 // is resident at once with one vector a thread (two, for rows of more than
 // 8192) is spread that wide instead.  Through the norm with residual, bf16,
 // wide against four vectors: one row of 4096 2.4 and 4.7 us, 333 rows of 4096
-// 3.3 and 3.8, 333 rows of 8192 (not resident) 5.7 and 4.9.
+// 3.3 and 3.8, 333 rows of 8192 (not resident) 5.7 and 4.9.  More rows of four
+// vectors than run at once go to piped_rows_kernel.
 template <int kOp, typename T, bool kAligned>
 const char *launch_rows_by_length(const RowParams &p, cudaStream_t stream)
 {

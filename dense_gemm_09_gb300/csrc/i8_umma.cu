@@ -10,14 +10,19 @@
 // integer one.  Operands stay int8 in HBM and L2 and on their way into the
 // SM; they are widened to FP16 inside it.
 //
-// What bounds it.  Shared memory: each SM moves 128 bytes a clock through it,
-// and a K step of 64 costs a CTA of a pair (256 x 192 tiles) 14 KB written by
-// TMA, 14 KB read by the converters, 12 KB of widened columns written and
-// 12 KB read by the MMAs, against 384 clocks of MMA.  So the operand that
-// supplies the MMA's rows never goes back to shared memory: its converter
-// warps store it to tensor memory (tcgen05.st) and the MMAs take A from there.
-// That leaves 52 KB, 416 clocks; with both operands widened in shared memory
-// it would be 84 KB, 672 clocks.
+// What bounds it.  The tensor pipe, once shared memory is kept out of the way:
+// each SM moves 128 bytes a clock through it, and a K step of 64 costs a CTA of
+// a pair (256 x 192 tiles) 14 KB written by TMA, 14 KB read by the
+// converters, 12 KB of widened columns written and 12 KB read by the MMAs,
+// against 384 clocks of MMA.  So the operand that supplies the MMA's rows
+// never goes back to shared memory: its converter warps store it to tensor
+// memory (tcgen05.st) and the MMAs take A from there.  That leaves 52 KB, 416
+// clocks; with both operands widened in shared memory it would be 84 KB, 672
+// clocks.  Measured with operands in place, an MMA of K = 16 takes N / 2 + 10
+// clocks with A in tensor memory (N / 2 + 43 with A in shared memory): 848
+// clocks for 128 K values at N = 192, and the kernel takes 850.  8192 x 8192 x
+// 4096 to bf16: 295 us, 1865 TFLOP/s, 98 % of the measured bf16 GEMM rate
+// (321 us in a long run, where the power limit sets the clock).
 //
 // Roles (32 warps, one CTA an SM):
 //   warp 0       TMA producer: 128-byte rows (128 K values) of both operands
@@ -41,7 +46,9 @@
 // leader's barrier.
 //
 // "Rows" are A's tokens (kSwap = false) or B's channels (kSwap = true: the
-// accumulator holds C^T, for few tokens).
+// accumulator holds C^T, for few tokens).  Tiles that all run at once have one
+// accumulator of up to 256 columns; a CTA of several tiles has two of up to
+// 192, so that one drains while the next fills.
 #include <algorithm>
 #include <climits>
 #include <cstdint>
@@ -785,8 +792,8 @@ __device__ __forceinline__ void load_column_values(const Params &p, Ctrl *ctrl, 
 {
     for (int c = tid; c < p.bn; c += 32 * kEpiWarps) {
         const bool in = c0 + c < p.cols && c < kMaxBn;
-        ctrl->scale[c] = in ? __ldg((kSwap ? p.c.scale_a : p.c.scale_b) + c0 + c) : 0.f;
-        if constexpr (!kSwap) ctrl->bias[c] = in && p.c.bias ? __ldg(p.c.bias + c0 + c) : 0.f;
+        ctrl->scale[c] = in ? load_f32((kSwap ? p.c.scale_a : p.c.scale_b) + c0 + c) : 0.f;
+        if constexpr (!kSwap) ctrl->bias[c] = in && p.c.bias ? load_f32(p.c.bias + c0 + c) : 0.f;
     }
     __syncwarp();
     named_barrier(kEpiBarrier, 32 * kEpiWarps);
@@ -820,8 +827,8 @@ __device__ __forceinline__ void drain(const Params &p, const CUtensorMap *tmap_o
 template <bool kSwap>
 __device__ __forceinline__ void load_row_values(const Params &p, int64_t row, float &rs, float &rb)
 {
-    rs = row < p.rows ? __ldg((kSwap ? p.c.scale_b : p.c.scale_a) + row) : 0.f;
-    rb = kSwap && p.c.bias && row < p.rows ? __ldg(p.c.bias + row) : 0.f;
+    rs = row < p.rows ? load_f32((kSwap ? p.c.scale_b : p.c.scale_a) + row) : 0.f;
+    rb = kSwap && p.c.bias && row < p.rows ? load_f32(p.c.bias + row) : 0.f;
 }
 
 // The CTA's tiles but the last, while the MMAs of the next one run; then the
@@ -893,7 +900,10 @@ __device__ __forceinline__ void drain_last(const Params &p, const CUtensorMap *t
                                            const LastTile &l, uint32_t tmem_base, uint32_t box, uint32_t raw, int warp,
                                            int lane, WaitCtl *wc)
 {
-    if (__any_sync(0xFFFFFFFFu, aborted(wc))) return;
+    if (__any_sync(0xFFFFFFFFu, aborted(wc))) {
+        if (lane == 0) ptx::bulk_wait<0>();  // earlier tiles' stores
+        return;
+    }
     ptx::tc_fence_after();
     const int group = (warp - 4) >> 2;
     const uint32_t quarter = static_cast<uint32_t>(warp & 3);
