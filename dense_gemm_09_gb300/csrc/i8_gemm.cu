@@ -3,11 +3,18 @@
 //
 //   C[m, n] = scale_a[m] * scale_b[n] * sum_k A[m, k] B[n, k] + bias[n] + beta * C[m, n].
 //
+// The choice of the kernel (choose_config below), and the one for every case.
+// Operands that TMA can describe (rows on 16-byte boundaries) go to the
+// tensor-core kernel (i8_umma.cu) or, for few tokens, to the dot-product and
+// mma.sync kernels (i8_decode.cu).
+//
 // i8_mma_kernel is the kernel for every case: operands of any alignment and
 // pitch, any sizes.  64 x 64 output tiles, four warps of 32 x 32; K in chunks
 // of 64 bytes staged in shared memory through registers (the next chunk's
 // loads are in flight while a chunk is multiplied); mma.sync m16n8k32 on
-// int8 with exact int32 sums.
+// int8 with exact int32 sums.  Bound by the integer tensor rate: 149 Top/s
+// at 16-byte alignment, 125 at 4, 109 at any (1023 x 8193 x 4095 at a pitch of
+// 4095: 631 us, against 53 us at a pitch of 4096 by the tensor-core kernel).
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -57,24 +64,24 @@ template <int kW>
 __device__ __forceinline__ void load_half_row(const int8_t *p, bool row_ok, int64_t left, uint32_t (&w)[8])
 {
     if (row_ok && left >= 32 && kW == 16) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p)), b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+        const uint4 a = load_v4(p), b = load_v4(p + 16);
         w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
         w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
         return;
     }
     if (row_ok && left >= 32 && kW == 4) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
+        for (int i = 0; i < 8; ++i) w[i] = load_u32(reinterpret_cast<const uint32_t *>(p) + i);
         return;
     }
     if (row_ok && left >= 32 && kW == 1) {
         const uint32_t shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u) * 8u;
         const uint32_t *a = reinterpret_cast<const uint32_t *>(p - shift / 8);
-        uint32_t lo = __ldg(a);
+        uint32_t lo = load_u32(a);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             // the last word only if the 32 bytes reach into it
-            const uint32_t hi = i < 7 || shift ? __ldg(a + i + 1) : 0u;
+            const uint32_t hi = i < 7 || shift ? load_u32(a + i + 1) : 0u;
             w[i] = __funnelshift_r(lo, hi, shift);
             lo = hi;
         }
@@ -213,8 +220,8 @@ bool tma_ok(const I8Params &p)
 // Estimated times in us, fitted to GB300 sweeps of every kernel over 8 shapes
 // of B x 19 numbers of tokens (1 .. 4096); the smallest estimate runs.
 //
-// 1 to 4 tokens take the dot-product kernel.  5 to 8 tokens take the mma.sync kernel, which nothing else
-// came near.
+// 1 and 2 tokens take the dot-product kernel, 3 to 8 the mma.sync kernel; no
+// other came near.
 struct Candidate {
     double us;
     I8Config cfg;
@@ -236,32 +243,15 @@ double stage_us(bool pair, int bn)
     return p[0].us + (p[1].us - p[0].us) * (bn - p[0].bn) / (p[1].bn - p[0].bn);
 }
 
-// Blocks of 32 / split channels in whole waves of three an SM: a launch of 0.6
-// or of 1.1 waves leaves memory idle at its end (8192 x 4096: split 1 and 4,
-// 256 and 1024 blocks, 7.9 and 6.8 us; 16384 x 4096: 1 and 2, 14.5 and 13.1).
-I8Config dot_config(const I8Params &p, int sm_count)
-{
-    if (p.N <= 1024) return {kI8Dot, 0, 8};
-    int best = 1;
-    double best_score = -1.0;
-    for (int split = 1, bits = 0; split <= 4; split *= 2, ++bits) {
-        if (split > 1 && p.K < 512 * split) break;  // a turn for every warp
-        const double waves = static_cast<double>((p.N * split + 31) / 32) / (3.0 * sm_count);
-        const double score = waves / std::ceil(waves) - 0.08 * bits;
-        if (score > best_score) {
-            best_score = score;
-            best = split;
-        }
-    }
-    return {kI8Dot, 0, best};
-}
-
 // mma.sync: ~20 clocks of an SM for each product of 16 channels x 8 tokens x
 // 32, or ~0.2 + 0.6 us a turn of 128 K values and group of 8 tokens where
-// there are few warps.
+// there are few warps.  Blocks of 16 warps where each has a turn, of 8 where
+// there are many blocks anyway (8 tokens, 16 and 8 warps: 4096 x 14336 13.4
+// and 17.5 us, 8192 x 4096 8.3 and 9.5; 28672 x 4096 25.4 and 23.3, 16384 x
+// 2048 9.2 and 7.8).
 Candidate decode_candidate(const I8Params &p)
 {
-    const int warps = p.N < 4096 ? 16 : 8;
+    const int warps = p.N <= 12288 && p.K >= 2048 ? 16 : 8;
     const double groups = static_cast<double>(p.M <= 8 ? 1 : p.M <= 16 ? 2 : 4);
     const double turns = static_cast<double>((p.K + 127) / 128 + warps - 1) / warps;
     const double nk = static_cast<double>(p.N) * static_cast<double>(p.K);
@@ -271,7 +261,7 @@ Candidate decode_candidate(const I8Params &p)
 I8Config choose_config(const I8Params &p, int sm_count, bool (*fits)(const I8Params &, const I8Config &))
 {
     if (p.K < (1 << 17)) {
-        if (p.M <= 4) return dot_config(p, sm_count);
+        if (p.M <= 2) return {kI8Dot, 0, 1};
         if (p.M <= 8) return decode_candidate(p).cfg;
     }
     const int64_t kb = (p.K + 127) / 128;
@@ -324,19 +314,15 @@ const char *config_name(const I8Config &c)
         }
     });
     if (c.variant == kI8Decode) return c.split == 8 ? "i8_decode_16_channels_8_warps" : "i8_decode_16_channels_16_warps";
-    if (c.variant == kI8Dot)
-        return c.split == 1   ? "i8_dot_4_channels_split1"
-               : c.split == 2 ? "i8_dot_4_channels_split2"
-               : c.split == 4 ? "i8_dot_4_channels_split4"
-                              : "i8_dot_4_channels_split8";
+    if (c.variant == kI8Dot) return "i8_dot_4_channels";
     if (c.variant == kI8Split) return names[c.bn / 16][c.split][0].c_str();
     return names[c.bn / 16][0][c.variant == kI8PairChannels ? 1 : 0].c_str();
 }
 
 // (A launch that cannot be prepared falls back to the kernel for every case.)
-bool launch_config(const I8Params &p, int c_type, const I8Config &cfg, cudaStream_t stream)
+bool launch_config(const I8Params &p, int c_type, const I8Config &cfg, int sm_count, cudaStream_t stream)
 {
-    return cfg.variant >= kI8Decode ? launch_i8_decode(p, c_type, cfg, stream) : launch_i8_umma(p, c_type, cfg, stream);
+    return cfg.variant >= kI8Decode ? launch_i8_decode(p, c_type, cfg, sm_count, stream) : launch_i8_umma(p, c_type, cfg, stream);
 }
 
 }  // namespace
@@ -350,9 +336,9 @@ const char *launch_gemm_i8(const I8Params &q, int c_type, cudaStream_t stream, c
     I8Config cfg = t_tune;
     t_tune = {kI8Auto, 0, 1};
     if (tma_ok(p) && cfg.variant != kI8Mma) {
-        if (cfg.variant != kI8Auto && launch_config(p, c_type, cfg, stream)) return config_name(cfg);
+        if (cfg.variant != kI8Auto && launch_config(p, c_type, cfg, dev.sm_count, stream)) return config_name(cfg);
         cfg = choose_config(p, dev.sm_count, i8_umma_fits);
-        if (launch_config(p, c_type, cfg, stream)) return config_name(cfg);
+        if (launch_config(p, c_type, cfg, dev.sm_count, stream)) return config_name(cfg);
     }
     switch (c_type) {
     case DGEMM_TYPE_F32: return launch_mma<float>(p, stream);

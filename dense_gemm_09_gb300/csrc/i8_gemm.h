@@ -26,8 +26,7 @@ enum { kI8Auto = 0, kI8Mma = 1, kI8PairTokens = 2, kI8PairChannels = 3, kI8Split
 struct I8Config {
     int variant;
     int bn;     // tile columns: channels (kI8PairTokens) or tokens
-    int split;  // kI8Split: CTAs that share a tile along K; kI8Dot: warps that do;
-                // kI8Decode: warps of a block
+    int split;  // kI8Split: CTAs that share a tile along K
 };
 
 // The tensor-core kernels (i8_umma.cu), for operands TMA can describe: false,
@@ -41,7 +40,7 @@ bool i8_umma_fits(const I8Params &c, const I8Config &cfg);
 // The kernels for few tokens (i8_decode.cu), for operands with 16-byte aligned
 // rows: as above.
 bool i8_decode_config_ok(const I8Config &cfg);
-bool launch_i8_decode(const I8Params &p, int c_type, const I8Config &cfg, cudaStream_t stream);
+bool launch_i8_decode(const I8Params &p, int c_type, const I8Config &cfg, int sm_count, cudaStream_t stream);
 
 __device__ __forceinline__ float i8_to_f32(float v) { return v; }
 __device__ __forceinline__ float i8_to_f32(__half v) { return __half2float(v); }

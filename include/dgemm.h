@@ -493,8 +493,7 @@ int dgemm_tune_next(int variant, int bn, int split);
  *              16), `split` (1..8) CTAs of a cluster sharing it along K;
  *           5: at most 32 tokens, mma.sync, blocks of 16 channels and `split` (8
  *              or 16) warps;
- *           6: at most 4 tokens, dot products, `split` (1, 2, 4 or 8) warps to 4
- *              channels.
+ *           6: at most 2 tokens, dot products (split 1).
  * Returns DGEMM_ERR_INVALID_ARG (and records nothing) for values outside
  * these ranges, else DGEMM_OK.  A configuration the next call cannot take is
  * ignored; dgemm_last_kernel() names what ran.  Source: as dgemm_tune_next.
