@@ -6,20 +6,23 @@
 // built to have many of their bytes in flight.  Sums are exact int32; they
 // cannot overflow for K < 2^17.
 //
-// i8_dot_kernel, 1 to 4 tokens: four-way dot products on the integer pipes.
-//   A warp reads 512 contiguous bytes of each of four channels at a time, so
-//   every line that leaves L2 is used whole: 8192 x 4096 weights in 7.0 us
-//   against 8.9 us for i8_decode_kernel, 16384 x 16384 in 38.7 against 48 us.
-//   One dot product of four bytes per token and weight word: ~1/4 of the
-//   memory time for each token.
+// i8_dot_kernel, 1 and 2 tokens: four-way dot products on the integer pipes.  A
+//   warp reads 512 contiguous bytes of each of four channels at a time, so
+//   every line that leaves L2 is used whole, and the work is dealt evenly
+//   over all warps.  One token: 8192 x 4096 weights in 5.6 us (6.0 TB/s), 28672
+//   x 4096 in 19.8 (5.9 TB/s); a tail of blocks, dealt by whole rows, took 7.0
+//   and 19.9.
 // i8_decode_kernel, up to 32 tokens: mma.sync m16n8k32 on int8, its 16 rows the
 //   channels, its 8 columns the tokens.  A fragment wants four 4-byte pieces
 //   of a row, 16 bytes apart; since any order of K will do as long as both
 //   operands follow it, each thread instead loads 16 contiguous bytes and
 //   uses them as the pieces of two products.  The integer tensor rate (a
 //   product takes ~20 clocks of an SM) keeps pace with memory for one group
-//   of 8 tokens; more groups pay where a tensor-core launch's fixed cost is
-//   larger.
+//   of 8 tokens (8192 x 4096: 8.2 us); more groups pay where a tensor-core
+//   launch's fixed cost is larger (32 tokens, 2048 x 2048: 4.2 against 6.8 us).
+//   The warps of a block read neighbouring pieces of its rows; dealt in even
+//   ranges like the dot products', a warp walking along K by itself, they
+//   took longer (8 tokens, 8192 x 4096 9.9, 1024 x 8192 9.1 against 4.0 us).
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
@@ -90,8 +93,10 @@ constexpr int kDotGroups = 64;  // groups a block may have
 // The work is cut into units of a group of four channels x 512 K values, and
 // spread evenly: every block takes an equal range of groups, every warp an
 // equal range of its block's units, whatever N and K are.  A group's sum that
-// two warps share meets in shared memory; it is an integer, so the order does not
-// matter.  kUnroll units are loaded before the first product.
+// two warps share meets in shared memory; it is an integer, so the order does
+// not matter.  kUnroll units are loaded before the first product.  What lies past
+// a row's end within the 16 bytes that hold its last value is read (rows start on
+// 16-byte boundaries) and cut off.
 template <typename T, int kTokens, int kUnroll, int kBlocks>
 __global__ void __launch_bounds__(kDotWarps * 32, kBlocks)
     i8_dot_kernel(const I8Params p, int groups_each, int groups_more, int turns)

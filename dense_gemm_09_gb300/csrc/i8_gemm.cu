@@ -245,17 +245,19 @@ double stage_us(bool pair, int bn)
 
 // mma.sync: ~20 clocks of an SM for each product of 16 channels x 8 tokens x
 // 32, or ~0.2 + 0.6 us a turn of 128 K values and group of 8 tokens where
-// there are few warps.  Blocks of 16 warps where each has a turn, of 8 where
-// there are many blocks anyway (8 tokens, 16 and 8 warps: 4096 x 14336 13.4
-// and 17.5 us, 8192 x 4096 8.3 and 9.5; 28672 x 4096 25.4 and 23.3, 16384 x
-// 2048 9.2 and 7.8).
+// there are few warps; and the warps' sums, for every channel and group.
+// Blocks of 16 warps where each has a turn, of 8 where there are many blocks
+// anyway (8 tokens, 16 and 8 warps: 4096 x 14336 13.4 and 17.5 us, 8192 x 4096
+// 8.3 and 9.5; 28672 x 4096 25.4 and 23.3, 16384 x 2048 9.2 and 7.8).
 Candidate decode_candidate(const I8Params &p)
 {
     const int warps = p.N <= 12288 && p.K >= 2048 ? 16 : 8;
-    const double groups = static_cast<double>(p.M <= 8 ? 1 : p.M <= 16 ? 2 : 4);
+    const double groups = p.M <= 8 ? 1.0 : p.M <= 16 ? 2.0 : 4.0;
     const double turns = static_cast<double>((p.K + 127) / 128 + warps - 1) / warps;
     const double nk = static_cast<double>(p.N) * static_cast<double>(p.K);
-    return {2.2 + std::max({1.6e-7 * groups * nk, turns * (0.2 + 0.6 * groups), nk / kHbm}), {kI8Decode, 0, warps}};
+    return {2.2 + 0.8e-4 * groups * static_cast<double>(p.N) +
+                std::max({1.6e-7 * groups * nk, turns * (0.2 + 0.6 * groups), nk / kHbm}),
+            {kI8Decode, 0, warps}};
 }
 
 I8Config choose_config(const I8Params &p, int sm_count, bool (*fits)(const I8Params &, const I8Config &))
@@ -271,16 +273,18 @@ I8Config choose_config(const I8Params &p, int sm_count, bool (*fits)(const I8Par
         if (c.us < best.us && fits(p, c.cfg)) best = c;
     };
     if (p.M <= 32 && p.K < (1 << 17)) take(decode_candidate(p));
-    // one CTA per 128 channels x bn tokens: at most two widths, every split
-    // that keeps all CTAs resident.  Its tail, 128 columns of one accumulator
-    // stored token by token, grows with bn; a split costs an exchange.
+    // one CTA per 128 channels x bn tokens: at most two widths, without a split
+    // in waves, or every split that keeps all CTAs resident.  Its tail, 128
+    // columns of one accumulator stored token by token, grows with bn; a split
+    // costs an exchange.
     const int64_t m16 = (p.M + 15) / 16 * 16;
     for (int bn : {static_cast<int>(std::min<int64_t>(m16, 128)), 64}) {
         if (bn > m16) continue;
         const int64_t tiles = (p.N + 127) / 128 * ((p.M + bn - 1) / bn);
-        for (int S = 1; S <= 8 && tiles * S <= sm_count && S <= kb; ++S)
-            take({4.8 + 0.022 * bn + (S > 1 ? 1.6 : 0.0) +
-                      std::max(static_cast<double>((kb + S - 1) / S) * stage_us(false, bn), hbm),
+        const int64_t waves = (tiles + sm_count - 1) / sm_count;
+        for (int S = 1; S <= 8 && (S == 1 || tiles * S <= sm_count) && S <= kb; ++S)
+            take({4.8 + 0.022 * bn + (S > 1 ? 1.6 : static_cast<double>(waves - 1)) +
+                      std::max(static_cast<double>(waves * ((kb + S - 1) / S)) * stage_us(false, bn), hbm),
                   {kI8Split, bn, S}});
     }
     // CTA pairs of 256 x bn, in waves: rows are the channels (for few tokens)

@@ -445,10 +445,12 @@ __device__ __forceinline__ void copy_async16(uint4 *dst, const void *src, int by
 // 8192 rows of bf16, rows_kernel and this one: quantize of 8192 33.0 and 30.7
 // us, of 12288 58.9 and 46.1; swiglu of 8192 52.7 and 50.5, of 12288 85.4 and
 // 74.4; norm of 8192 43.6 and 39.4, of 12288 78.3 and 59.6.  The norm with
-// residual, which stores H too, does not gain (71.3 and 85.8).
-constexpr bool is_piped(int op)
+// residual, which stores H too, loses (of 8192 71.3 and 85.8) except where an SM
+// holds one row at a time (4096 rows of 20000 106.5 and 88.4, 2048 of 32768
+// 81.3 and 83.9).
+constexpr bool is_piped(int op, int most_threads)
 {
-    return op != kOpNorm;
+    return op != kOpNorm || most_threads == 1024;
 }
 
 template <int kOp, typename T, int kMost, int kVecs>
@@ -684,7 +686,7 @@ void launch_rows(const RowParams &p, cudaStream_t stream)
     // threads: a warp for each 32 * kVecs vectors
     const unsigned threads = kMost == 32 ? 128u : static_cast<unsigned>((vecs + 32 * kVecs - 1) / (32 * kVecs) * 32);
     const unsigned grid = static_cast<unsigned>(kMost == 32 ? (p.rows + 3) / 4 : p.rows);
-    if constexpr (is_piped(kOp) && kAligned && sizeof(T) == 2 && kVecs == 4) {
+    if constexpr (is_piped(kOp, kMost) && kAligned && sizeof(T) == 2 && kVecs == 4) {
         const int resident = piped_blocks<kOp, T, kMost, kVecs>(threads);
         if (resident > 0 && grid > static_cast<unsigned>(resident)) {
             launch_chained(piped_rows_kernel<kOp, T, kMost, kVecs>, static_cast<unsigned>(resident), threads,

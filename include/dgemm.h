@@ -282,6 +282,8 @@ int gemm_bf16_nn(int64_t M, int64_t N, int64_t K, float alpha,
  *   the row length, an unknown type or a NULL pointer that is not said to be
  *   optional.  Pointers are aligned to their element type; rows that start
  *   on 16-byte boundaries (int8 outputs: 8-byte) take the fastest kernels.
+ *   An aligned word of up to 16 bytes that holds part of an int8 row may be read
+ *   whole (what is past the row has no effect); writes stay within the rows.
  *   Outputs must not overlap inputs, except where a call allows it.
  * Source: none on the pages (their products are floating-point).
  */

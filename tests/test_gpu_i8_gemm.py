@@ -338,3 +338,13 @@ def test_refusals():
         dg.gemm_i8_tn(A.cpu(), B, C, sa, sb)
     with pytest.raises(ValueError):
         dg.gemm_i8_tn(A, B, torch.empty((6, 4), device="cuda").t(), sa, sb)
+
+
+@pytest.mark.parametrize("ty", ref.TYPES)
+@pytest.mark.parametrize("M", [12, 16, 31])
+def test_more_channels_than_one_wave(M, ty):
+    # a CTA an SM holds 128 channels: several tiles a CTA, the last wave ragged
+    import dense_gemm_09_gb300 as dg
+    for N in (19456, 19457, 20481, 24576, 29312, 39001):
+        _check(M, N, 1024, ty, True, 0.5)
+    assert dg.device_status() == dg.OK
