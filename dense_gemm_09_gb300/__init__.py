@@ -360,8 +360,9 @@ def _i8(name: str):
 
 def quantize_i8(X, Q, scale, stream=None):
     """Each row of X (float32, float16 or bfloat16) as int8 with one FP32 scale:
-    scale = max|x| / 127, Q = rint(x / scale).  Writes and returns (Q, scale);
-    a row of zeros gets scale 0, a row with a NaN or an infinity scale NaN."""
+    a = max|x|, scale = a / 127, Q = rint(127 x / a), ties to even.  Writes and
+    returns (Q, scale); a row of zeros gets scale 0, a row with a NaN or an
+    infinity scale NaN."""
     m, entry = _i8("quantize_i8")
     return m.quantize_i8(entry, X, Q, scale, stream)
 

@@ -19,7 +19,7 @@
 // of one block (32768 elements) are read again from memory for each pass.
 // At 3 to 7 bytes an element the instructions count too (an SM has ~8 of them
 // for each of its threads' elements at HBM speed), hence the packed
-// conversions, the three-input maximum and the rounding by one FMA below.
+// conversions, the three-input maximum and the rounding by one addition below.
 #include <atomic>
 #include <cstdint>
 #include <type_traits>
@@ -182,53 +182,159 @@ __device__ __forceinline__ float max_abs(float amax, const float (&v)[kVec])
     return amax;
 }
 
-struct Quantiser {
-    float scale, inv;
-    bool finite, tiny;
+// Two FP32 operations at a time.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi)
+{
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 
-    // The row's largest |y| as its bits: for non-negative floats unsigned order
-    // is the order of the values, infinities and then NaNs above every finite
-    // one, so the threads' maxima meet in an integer maximum.
-    __device__ __forceinline__ explicit Quantiser(uint32_t amax_bits)
+// How a row's quotients 127 y / a are formed.  A product with the rounded 127 / a
+// leans to one side, and half of all ties (a whole number and a half) go to the
+// wrong step.  y (hi + lo), with hi + lo = 127 / a to ~2^-46 and the sum rounded
+// once, makes a tie of every quotient that is one.
+//   kOneProduct   for y with several FP32 roundings in them, ties there being
+//                 chance;
+//   kTies         ties are right.  Quotients of 16-bit y that are no ties are at
+//                 least 2^-20 (relative) away from all ties and cannot come out
+//                 as one;
+//   kTiesAndNear  those of FP32 y may be as near as 2^-33: what comes out as a
+//                 tie is looked at again.
+// 8192 x 8192, one product and the form in use: quantize bf16 30.2 and 30.5 us, FP32
+// 48.2 and 49.1; norm of bf16 40.1 and 39.0 (its quotients do without 1 / sqrt).
+enum { kOneProduct, kTies, kTiesAndNear };
+
+template <int kOp, typename T>
+constexpr int quotient_form()
+{
+    if (kOp == kOpSwiglu) return kOneProduct;
+    return kOp == kOpQuantize && sizeof(T) == 4 ? kTiesAndNear : kTies;
+}
+
+// The steps rint(127 y / a), ties to even, of a row whose largest |y| is a.
+// Rounding to a whole number is the addition of 1.5 * 2^23, whose unit in the last
+// place is 1: the step is the sum's low byte.  |y| <= a, and a quotient that
+// rounds up past 127 still rounds to 127.
+template <int kForm>
+struct Quantiser {
+    float scale, hi, lo, factor;
+    bool finite;
+
+    static constexpr float kWhole = 12582912.f;
+
+    // For y = values * times: the largest |value| as its bits, and times.  (For
+    // non-negative floats unsigned order is the order of the values, infinities
+    // and then NaNs above every finite one, so the threads' maxima meet in an
+    // integer maximum.)  The steps do not depend on `times`.
+    __device__ __forceinline__ explicit Quantiser(uint32_t most_bits, float times = 1.f)
     {
-        const float a = __uint_as_float(amax_bits);
-        finite = amax_bits < 0x7F800000u;
+        float most = __uint_as_float(most_bits);
+        const float a = most * times;
+        finite = a < __uint_as_float(0x7F800000u);
         scale = finite ? a / 127.f : __uint_as_float(0x7FC00000u);
-        // 127 / a leaves FP32's range below a = 2^-121; such rows are first
-        // multiplied by a power of two, which is exact
-        tiny = a < 0x1p-100f;
-        inv = a > 0.f ? 127.f / (tiny ? a * 0x1p100f : a) : 0.f;
+        // far from 1, hi or lo would leave FP32's range: such rows are first
+        // multiplied by a power of two.  (That is exact upwards; downwards it
+        // may round values below 2^-26 of the largest, whose steps are 0.)
+        factor = most < 0x1p-100f ? 0x1p100f : most > 0x1p100f ? 0x1p-100f : 1.f;
+        most *= factor;
+        hi = a > 0.f ? 127.f / most : 0.f;
+        lo = fmaf(-hi, most, 127.f) * (hi * (1.f / 127.f));  // what hi is short of, over `most`
     }
 
-    // rint(y * 127 / a), ties to even, in the low byte: added to 1.5 * 2^23,
-    // whose unit in the last place is 1, the product is rounded to a whole
-    // number within the FMA.  |y| <= a, and a product that rounds up past
-    // 127 still rounds to 127.
-    __device__ __forceinline__ uint32_t step(float y) const { return __float_as_uint(fmaf(y, inv, 12582912.f)); }
+    // kWhole + the step, where t = y hi + y lo, rounded, is a tie; rest: what
+    // the rounding took.
+    __device__ __forceinline__ float past_tie(float y, float t, float sum) const
+    {
+        const float side = t - (sum - kWhole), rest = fmaf(y, lo, fmaf(y, hi, -t));
+        if (fabsf(side) == 0.5f && fabsf(rest) > 0x1p-38f * fabsf(t)) {
+            if (side > 0.f && rest > 0.f) return sum + 1.f;
+            if (side < 0.f && rest < 0.f) return sum - 1.f;
+        }
+        return sum;
+    }
 
     // the steps of eight values, a byte each
     __device__ __forceinline__ uint2 steps(const float (&y)[kVec]) const
     {
         if (!finite) return make_uint2(0u, 0u);
-        float z[kVec];
+        float z[kVec], sum[kVec];
 #pragma unroll
         for (int i = 0; i < kVec; ++i) z[i] = y[i];
-        if (tiny) {
+        if (factor != 1.f) {
             asm volatile("");  // a branch, not eight predicated products for every row
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) z[i] *= 0x1p100f;
+            for (int i = 0; i < kVec; ++i) z[i] *= factor;
+        }
+        if constexpr (kForm == kOneProduct) {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) sum[i] = fmaf(z[i], hi, kWhole);
+        } else {
+            const uint64_t hi2 = pack2(hi, hi), lo2 = pack2(lo, lo), whole2 = pack2(kWhole, kWhole);
+            float off = 0.f;  // the largest distance from a whole number
+            uint64_t t2[kVec / 2];
+#pragma unroll
+            for (int i = 0; i < kVec / 2; ++i) {
+                const uint64_t y2 = pack2(z[2 * i], z[2 * i + 1]);
+                t2[i] = fma2(y2, hi2, mul2(y2, lo2));
+                const uint64_t sum2 = add2(t2[i], whole2);
+                unpack2(sum2, sum[2 * i], sum[2 * i + 1]);
+                if constexpr (kForm == kTiesAndNear) {
+                    const uint64_t step2 = add2(sum2, pack2(-kWhole, -kWhole));
+                    float d[2];
+                    unpack2(fma2(step2, pack2(-1.f, -1.f), t2[i]), d[0], d[1]);
+                    off = max3_abs(off, d[0], d[1]);
+                }
+            }
+            if constexpr (kForm == kTiesAndNear) {
+                if (off == 0.5f) {
+                    asm volatile("");
+#pragma unroll
+                    for (int i = 0; i < kVec / 2; ++i) {
+                        float t[2];
+                        unpack2(t2[i], t[0], t[1]);
+                        sum[2 * i] = past_tie(z[2 * i], t[0], sum[2 * i]);
+                        sum[2 * i + 1] = past_tie(z[2 * i + 1], t[1], sum[2 * i + 1]);
+                    }
+                }
+            }
         }
         uint32_t b[kVec];
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) b[i] = step(z[i]);
+        for (int i = 0; i < kVec; ++i) b[i] = __float_as_uint(sum[i]);
         const uint32_t p0 = __byte_perm(b[0], b[1], 0x0040), p1 = __byte_perm(b[2], b[3], 0x0040);
         const uint32_t p2 = __byte_perm(b[4], b[5], 0x0040), p3 = __byte_perm(b[6], b[7], 0x0040);
         return make_uint2(__byte_perm(p0, p1, 0x5410), __byte_perm(p2, p3, 0x5410));
     }
 };
 
-template <bool kAligned>
-__device__ __forceinline__ void store_q(int8_t *p, int n, const float (&y)[kVec], const Quantiser &qz)
+template <int kOp, typename T>
+using RowQuantiser = Quantiser<quotient_form<kOp, T>()>;
+
+template <bool kAligned, int kForm>
+__device__ __forceinline__ void store_q(int8_t *p, int n, const float (&y)[kVec], const Quantiser<kForm> &qz)
 {
     const uint2 b = qz.steps(y);
     if (kAligned && n == kVec && DGEMM_CHECK((reinterpret_cast<uintptr_t>(p) & 7u) == 0)) {
@@ -337,7 +443,8 @@ __device__ __forceinline__ void finish_row(const RowParams &p, int64_t row, int 
                                            float (&v)[kVecs][kVec], const W &weights, float *s_sum, uint32_t *s_max)
 {
     const int cols = static_cast<int>(p.cols);
-    float amax = 0.f;
+    float amax = 0.f, rstd = 1.f;
+    uint32_t most;
     if constexpr (is_norm(kOp)) {
         float ss = 0.f;
 #pragma unroll
@@ -347,8 +454,8 @@ __device__ __forceinline__ void finish_row(const RowParams &p, int64_t row, int 
 #pragma unroll
             for (int i = 0; i < kVec; ++i) ss = fmaf(v[j][i], v[j][i], ss);
         }
-        // neither the weights nor the maximum wait for the sum: rounding is
-        // monotone, so the largest |v g rstd| is the largest |v g| times rstd
+        // neither the weights nor the maximum wait for the sum, and the steps
+        // need no 1 / sqrt at all: it cancels in y / a
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
             float g[kVec];
@@ -357,21 +464,16 @@ __device__ __forceinline__ void finish_row(const RowParams &p, int64_t row, int 
             for (int i = 0; i < kVec; ++i) v[j][i] *= g[i];
             amax = max_abs(amax, v[j]);
         }
-        uint32_t most = __float_as_uint(amax) & 0x7FFFFFFFu;
+        most = __float_as_uint(amax) & 0x7FFFFFFFu;
         row_sum_max<kWarp>(ss, most, s_sum, s_max);
-        const float rstd = rsqrtf(ss / static_cast<float>(cols) + p.eps);
         // a sum of squares past FP32's range marks the row like a NaN in it
-        amax = ss < __uint_as_float(0x7F800000u) ? __uint_as_float(most) * rstd : __uint_as_float(0x7FC00000u);
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j)
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) v[j][i] *= rstd;
+        rstd = ss < __uint_as_float(0x7F800000u) ? rsqrtf(ss / static_cast<float>(cols) + p.eps) : __uint_as_float(0x7FC00000u);
     } else {
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) amax = max_abs(amax, v[j]);
-        amax = __uint_as_float(row_max<kWarp>(__float_as_uint(amax) & 0x7FFFFFFFu, s_max));
+        most = row_max<kWarp>(__float_as_uint(amax) & 0x7FFFFFFFu, s_max);
     }
-    const Quantiser qz(__float_as_uint(amax) & 0x7FFFFFFFu);
+    const RowQuantiser<kOp, T> qz(most, rstd);
     if (t == 0) p.scale[row] = qz.scale;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
@@ -543,25 +645,24 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(const RowParams p)
             for (int i = 0; i < kVec; ++i) ss = fmaf(v[i], v[i], ss);
         }
         ss = row_sum<false>(ss, s_sum);
-        if (!(ss < __uint_as_float(0x7F800000u))) amax = __uint_as_float(0x7FC00000u);
-        rstd = rsqrtf(ss / static_cast<float>(p.cols) + p.eps);
+        rstd = ss < __uint_as_float(0x7F800000u) ? rsqrtf(ss / static_cast<float>(p.cols) + p.eps) : __uint_as_float(0x7FC00000u);
     }
-    auto norm = [&](int64_t c, int n, float (&v)[kVec]) {
+    auto weigh = [&](int64_t c, int n, float (&v)[kVec]) {
         if constexpr (is_norm(kOp)) {
             float g[kVec];
             load_gamma<T, kAligned>(p, c, n, g);
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) v[i] = v[i] * g[i] * rstd;
+            for (int i = 0; i < kVec; ++i) v[i] *= g[i];
         }
     };
     for (int64_t c = static_cast<int64_t>(threadIdx.x) * kVec; c < p.cols; c += kThreads * kVec) {
         float v[kVec];
         const int n = vec_len(p.cols, c);
         value(c, n, v);
-        norm(c, n, v);
+        weigh(c, n, v);
         amax = max_abs(amax, v);
     }
-    const Quantiser qz(row_max<false>(__float_as_uint(amax) & 0x7FFFFFFFu, s_max));
+    const RowQuantiser<kOp, T> qz(row_max<false>(__float_as_uint(amax) & 0x7FFFFFFFu, s_max), rstd);
     if (threadIdx.x == 0) p.scale[row] = qz.scale;
     for (int64_t c = static_cast<int64_t>(threadIdx.x) * kVec; c < p.cols; c += kThreads * kVec) {
         float v[kVec];
@@ -570,7 +671,7 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(const RowParams p)
         // the last read of this thread's elements: H may now overwrite an input
         if constexpr (is_norm(kOp))
             if (p.h) store_vec<T, kAligned>(static_cast<T *>(p.h) + row * p.ldh + c, n, v);
-        norm(c, n, v);
+        weigh(c, n, v);
         if (DGEMM_CHECK(c + n <= p.cols)) store_q<kAligned>(p.q + row * p.ldq + c, n, v, qz);
     }
 }

@@ -272,6 +272,10 @@ int gemm_bf16_nn(int64_t M, int64_t N, int64_t K, float alpha,
  *
  *     a = max |y|,   scale = a / 127,   q = rint(y * 127 / a)   (ties to even)
  *
+ * quantize_i8's steps are exactly these of the values it is given.  The y of
+ * rmsnorm_i8 and swiglu_i8 carry a few FP32 roundings, so one that close to a tie
+ * may take either step (in rmsnorm_i8, equal or halved h * gamma keep equal or
+ * halved y).
  * A row of zeros gets scale 0 and zeros.  A row with a NaN or an infinity in
  * it (or, in rmsnorm_i8, a sum of squares past FP32's range) gets the scale
  * NaN and zeros, so everything that is made from it is NaN.
