@@ -6,8 +6,8 @@
  * ctypes a call spent 5 to 7 us on the host, most of it on reading and checking
  * tensors' attributes in Python; here it spends 3 to 4, of which the launch
  * itself is ~2.  The module does what the ctypes binding does for the other
- * calls: reads pointers, pitches and the current stream, checks shapes and
- * types, calls the C ABI and raises.  It links neither torch nor the library:
+ * calls: reads pointers, pitches and the current stream, checks shapes, types
+ * and devices, calls the C ABI and raises.  It links neither torch nor the library:
  * tensors are read through their Python attributes, and the entry points'
  * addresses come with each call.
  */
@@ -21,7 +21,7 @@
 enum { F32 = 0, F16 = 1, BF16 = 2, I8 = 3, kTypes = 4 }; /* 0..2: dgemm_type */
 static PyObject *g_dtype[kTypes];
 static PyObject *g_get_device, *g_raw_stream, *g_error;
-static PyObject *s_shape, *s_stride, *s_dtype, *s_is_cuda, *s_data_ptr, *s_cuda_stream;
+static PyObject *s_shape, *s_stride, *s_dtype, *s_is_cuda, *s_get_device, *s_data_ptr, *s_cuda_stream;
 
 static PyObject *setup(PyObject *self, PyObject *args)
 {
@@ -73,6 +73,22 @@ static int wrong_type(PyObject *t, const char *name, int want)
     return -1;
 }
 
+/* Whether t is on the GPU of the call's tensors before it (*device; -1: none so
+ * far).  The kernels run on one GPU, where another's addresses mean nothing. */
+static int same_device(PyObject *t, const char *name, int64_t *device)
+{
+    PyObject *d = PyObject_CallMethodNoArgs(t, s_get_device);
+    if (!d) return -1;
+    const int64_t on = PyLong_AsLongLong(d);
+    Py_DECREF(d);
+    if (on == -1 && PyErr_Occurred()) return -1;
+    if (*device < 0) *device = on;
+    if (on == *device) return 0;
+    PyErr_Format(PyExc_ValueError, "%s is on cuda:%lld, another tensor of the call on cuda:%lld", name, (long long)on,
+                 (long long)*device);
+    return -1;
+}
+
 static int on_gpu(PyObject *t)
 {
     PyObject *c = PyObject_GetAttr(t, s_is_cuda);
@@ -121,7 +137,7 @@ static int address(PyObject *t, void **ptr)
 }
 
 /* A matrix of type `want`, or with want < 0 of any float type. */
-static int matrix(PyObject *t, const char *name, int want, Mat *m)
+static int matrix(PyObject *t, const char *name, int want, Mat *m, int64_t *device)
 {
     int64_t shape[2], stride[2];
     m->type = type_of(t);
@@ -152,12 +168,13 @@ static int matrix(PyObject *t, const char *name, int want, Mat *m)
         }
         m->ld = m->cols; /* the pitch of a single row is never used */
     }
+    if (same_device(t, name, device) != 0) return -1;
     return address(t, &m->ptr);
 }
 
-static int matrix_like(PyObject *t, const char *name, int want, const Mat *like, Mat *m)
+static int matrix_like(PyObject *t, const char *name, int want, const Mat *like, Mat *m, int64_t *device)
 {
-    if (matrix(t, name, want, m) != 0) return -1;
+    if (matrix(t, name, want, m, device) != 0) return -1;
     if (m->rows != like->rows || m->cols != like->cols) {
         PyErr_Format(PyExc_ValueError, "shape mismatch: %s (%lld, %lld), expected (%lld, %lld)", name,
                      (long long)m->rows, (long long)m->cols, (long long)like->rows, (long long)like->cols);
@@ -166,7 +183,7 @@ static int matrix_like(PyObject *t, const char *name, int want, const Mat *like,
     return 0;
 }
 
-static int vector(PyObject *t, const char *name, int want, int64_t n, void **ptr)
+static int vector(PyObject *t, const char *name, int want, int64_t n, void **ptr, int64_t *device)
 {
     int64_t shape, stride;
     if (layout(t, 1, &shape, &stride) != 0 || shape != n) {
@@ -178,26 +195,35 @@ static int vector(PyObject *t, const char *name, int want, int64_t n, void **ptr
         PyErr_Format(PyExc_ValueError, "%s must be a contiguous CUDA tensor", name);
         return -1;
     }
+    if (same_device(t, name, device) != 0) return -1;
     return address(t, ptr);
 }
 
 /* ---- the stream, entry points and results */
 
-/* None: the current device's current stream; a Stream; or a handle. */
-static int stream_of(PyObject *s, void **out)
+/* None: the current device's current stream; a Stream; or a handle.  The
+ * tensors have to be on the current device, which is where kernels are launched. */
+static int stream_of(PyObject *s, int64_t device, void **out)
 {
-    PyObject *h;
-    if (s == Py_None) {
-        PyObject *dev = PyObject_CallNoArgs(g_get_device);
-        if (!dev) return -1;
-        h = PyObject_CallOneArg(g_raw_stream, dev);
+    PyObject *h, *dev = PyObject_CallNoArgs(g_get_device);
+    if (!dev) return -1;
+    const int64_t current = PyLong_AsLongLong(dev);
+    if (current != device) {
+        if (!PyErr_Occurred())
+            PyErr_Format(PyExc_ValueError, "the tensors are on cuda:%lld, the current device is cuda:%lld",
+                         (long long)device, (long long)current);
         Py_DECREF(dev);
+        return -1;
+    }
+    if (s == Py_None) {
+        h = PyObject_CallOneArg(g_raw_stream, dev);
     } else if (PyLong_Check(s)) {
         Py_INCREF(s);
         h = s;
     } else {
         h = PyObject_GetAttr(s, s_cuda_stream);
     }
+    Py_DECREF(dev);
     if (!h) return -1;
     *out = PyLong_AsVoidPtr(h);
     Py_DECREF(h);
@@ -246,10 +272,12 @@ static PyObject *quantize_i8(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
     Mat x, q;
     void *fn, *scale, *stream;
+    int64_t device = -1;
     int st;
     (void)self;
-    if (arity("quantize_i8", n, 5) || entry(a[0], &fn) || matrix(a[1], "X", -1, &x) ||
-        matrix_like(a[2], "Q", I8, &x, &q) || vector(a[3], "scale", F32, x.rows, &scale) || stream_of(a[4], &stream))
+    if (arity("quantize_i8", n, 5) || entry(a[0], &fn) || matrix(a[1], "X", -1, &x, &device) ||
+        matrix_like(a[2], "Q", I8, &x, &q, &device) || vector(a[3], "scale", F32, x.rows, &scale, &device) ||
+        stream_of(a[4], device, &stream))
         return NULL;
     Py_BEGIN_ALLOW_THREADS
     st = ((quantize_fn)fn)(x.rows, x.cols, x.ptr, x.ld, x.type, q.ptr, q.ld, scale, stream);
@@ -261,17 +289,19 @@ static PyObject *rmsnorm_i8(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
     Mat x, q, r = {0}, h = {0};
     void *fn, *gamma, *scale, *stream;
+    int64_t device = -1;
     int st;
     (void)self;
-    if (arity("rmsnorm_i8", n, 9) || entry(a[0], &fn) || matrix(a[1], "X", -1, &x) ||
-        matrix_like(a[3], "Q", I8, &x, &q) || (a[5] != Py_None && matrix_like(a[5], "residual", x.type, &x, &r)) ||
-        (a[6] != Py_None && matrix_like(a[6], "H", x.type, &x, &h)))
+    if (arity("rmsnorm_i8", n, 9) || entry(a[0], &fn) || matrix(a[1], "X", -1, &x, &device) ||
+        matrix_like(a[3], "Q", I8, &x, &q, &device) ||
+        (a[5] != Py_None && matrix_like(a[5], "residual", x.type, &x, &r, &device)) ||
+        (a[6] != Py_None && matrix_like(a[6], "H", x.type, &x, &h, &device)))
         return NULL;
     /* the weights: FP32, or the rows' type */
     const int gtype = type_of(a[2]) == F32 ? F32 : x.type;
     const double eps = PyFloat_AsDouble(a[7]);
-    if ((eps == -1.0 && PyErr_Occurred()) || vector(a[2], "gamma", gtype, x.cols, &gamma) ||
-        vector(a[4], "scale", F32, x.rows, &scale) || stream_of(a[8], &stream))
+    if ((eps == -1.0 && PyErr_Occurred()) || vector(a[2], "gamma", gtype, x.cols, &gamma, &device) ||
+        vector(a[4], "scale", F32, x.rows, &scale, &device) || stream_of(a[8], device, &stream))
         return NULL;
     Py_BEGIN_ALLOW_THREADS
     st = ((rmsnorm_fn)fn)(x.rows, x.cols, x.ptr, x.ld, r.ptr, r.ld, gamma, gtype, (float)eps, x.type, h.ptr, h.ld, q.ptr,
@@ -284,11 +314,12 @@ static PyObject *swiglu_i8(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
     Mat g, u, q;
     void *fn, *scale, *stream;
+    int64_t device = -1;
     int st;
     (void)self;
-    if (arity("swiglu_i8", n, 6) || entry(a[0], &fn) || matrix(a[1], "G", -1, &g) ||
-        matrix_like(a[2], "U", g.type, &g, &u) || matrix_like(a[3], "Q", I8, &g, &q) ||
-        vector(a[4], "scale", F32, g.rows, &scale) || stream_of(a[5], &stream))
+    if (arity("swiglu_i8", n, 6) || entry(a[0], &fn) || matrix(a[1], "G", -1, &g, &device) ||
+        matrix_like(a[2], "U", g.type, &g, &u, &device) || matrix_like(a[3], "Q", I8, &g, &q, &device) ||
+        vector(a[4], "scale", F32, g.rows, &scale, &device) || stream_of(a[5], device, &stream))
         return NULL;
     Py_BEGIN_ALLOW_THREADS
     st = ((swiglu_fn)fn)(g.rows, g.cols, g.ptr, g.ld, u.ptr, u.ld, g.type, q.ptr, q.ld, scale, stream);
@@ -300,10 +331,12 @@ static PyObject *dequantize_i8(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
     Mat x, q;
     void *fn, *scale, *stream;
+    int64_t device = -1;
     int st;
     (void)self;
-    if (arity("dequantize_i8", n, 5) || entry(a[0], &fn) || matrix(a[3], "X", -1, &x) ||
-        matrix_like(a[1], "Q", I8, &x, &q) || vector(a[2], "scale", F32, x.rows, &scale) || stream_of(a[4], &stream))
+    if (arity("dequantize_i8", n, 5) || entry(a[0], &fn) || matrix(a[3], "X", -1, &x, &device) ||
+        matrix_like(a[1], "Q", I8, &x, &q, &device) || vector(a[2], "scale", F32, x.rows, &scale, &device) ||
+        stream_of(a[4], device, &stream))
         return NULL;
     Py_BEGIN_ALLOW_THREADS
     st = ((dequantize_fn)fn)(x.rows, x.cols, q.ptr, q.ld, scale, x.ptr, x.ld, x.type, stream);
@@ -317,10 +350,11 @@ static PyObject *gemm_i8_tn(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
     Mat A, B, C;
     void *fn, *sa, *sb, *bias = NULL, *stream;
+    int64_t device = -1;
     int st;
     (void)self;
-    if (arity("gemm_i8_tn", n, 9) || entry(a[0], &fn) || matrix(a[3], "C", -1, &C) || matrix(a[1], "A", I8, &A) ||
-        matrix(a[2], "B", I8, &B))
+    if (arity("gemm_i8_tn", n, 9) || entry(a[0], &fn) || matrix(a[3], "C", -1, &C, &device) ||
+        matrix(a[1], "A", I8, &A, &device) || matrix(a[2], "B", I8, &B, &device))
         return NULL;
     if (A.rows != C.rows || B.rows != C.cols || A.cols != B.cols) {
         PyErr_Format(PyExc_ValueError, "shape mismatch: A (%lld, %lld), B (%lld, %lld), C (%lld, %lld)",
@@ -329,9 +363,9 @@ static PyObject *gemm_i8_tn(PyObject *self, PyObject *const *a, Py_ssize_t n)
         return NULL;
     }
     const double beta = PyFloat_AsDouble(a[7]);
-    if ((beta == -1.0 && PyErr_Occurred()) || vector(a[4], "scale_a", F32, C.rows, &sa) ||
-        vector(a[5], "scale_b", F32, C.cols, &sb) || (a[6] != Py_None && vector(a[6], "bias", F32, C.cols, &bias)) ||
-        stream_of(a[8], &stream))
+    if ((beta == -1.0 && PyErr_Occurred()) || vector(a[4], "scale_a", F32, C.rows, &sa, &device) ||
+        vector(a[5], "scale_b", F32, C.cols, &sb, &device) ||
+        (a[6] != Py_None && vector(a[6], "bias", F32, C.cols, &bias, &device)) || stream_of(a[8], device, &stream))
         return NULL;
     Py_BEGIN_ALLOW_THREADS
     st = ((gemm_fn)fn)(C.rows, C.cols, A.cols, A.ptr, A.ld, sa, B.ptr, B.ld, sb, bias, (float)beta, C.ptr, C.ld, C.type,
@@ -362,8 +396,9 @@ PyMODINIT_FUNC PyInit__i8_calls(void)
     s_stride = PyUnicode_InternFromString("stride");
     s_dtype = PyUnicode_InternFromString("dtype");
     s_is_cuda = PyUnicode_InternFromString("is_cuda");
+    s_get_device = PyUnicode_InternFromString("get_device");
     s_data_ptr = PyUnicode_InternFromString("data_ptr");
     s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
-    if (!s_shape || !s_stride || !s_dtype || !s_is_cuda || !s_data_ptr || !s_cuda_stream) return NULL;
+    if (!s_shape || !s_stride || !s_dtype || !s_is_cuda || !s_get_device || !s_data_ptr || !s_cuda_stream) return NULL;
     return PyModule_Create(&module);
 }
