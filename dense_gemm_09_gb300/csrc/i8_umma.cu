@@ -210,6 +210,11 @@ __device__ __forceinline__ void cluster_meet()
     asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ void fence_cluster()
+{
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
+
 __device__ __forceinline__ void named_barrier(uint32_t id, uint32_t threads)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -383,14 +388,13 @@ __device__ __forceinline__ void run_producer(const CUtensorMap *tmap_r, const CU
             }
         }
     }
-    if (!ok && elect_one()) {
-        // Do not leave while TMA may still be writing into this CTA's memory:
-        // stages before `stage` were last filled in this phase, the others (if
-        // at all: a barrier's phase 1 counts as over before its first) in the one
-        // before.
+    // Do not leave while TMA may still be writing into this CTA's memory (after an
+    // abort, whoever raised it; else these loads are waited for anyway): stages
+    // before `stage` were last filled in this phase, the others (if at all: a
+    // barrier's phase 1 counts as over before its first) in the one before.
+    if (elect_one())
         for (uint32_t s = 0; s < static_cast<uint32_t>(p.raw_stages); ++s)
             drain_wait(ptx::smem_addr(&ctrl->raw_full[s]), s < stage ? phase : phase ^ 1u);
-    }
     __syncwarp();
 }
 
@@ -584,10 +588,9 @@ __device__ __forceinline__ void run_mma(const Params &p, uint32_t conv, Ctrl *ct
         if (acc == 0) acc_phase ^= 1u;
     }
     __syncwarp();
-    // The epilogue's wait for the last accumulator covers every MMA and commit;
-    // after an abort, wait here for what was issued before TMEM is released
-    // (the elected thread is the same one each time).
-    if (!ok && elect_one()) {
+    // Whatever the epilogue's waits came to, every MMA issued has finished before
+    // TMEM is released (the elected thread is the same one each time).
+    if (elect_one()) {
         if constexpr (kCtas == 2)
             ptx::umma_commit_pair_multicast(ptx::smem_addr(&ctrl->mma_done), 0x1);
         else
@@ -864,7 +867,9 @@ __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap 
                         rs, rb, sh, lane, nbox);
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_leader<kCtas>(ptx::smem_addr(&ctrl->acc_empty[acc]));
+        // (the accumulator's next tile; an arrival that nothing waits for could
+        // reach a CTA that has left)
+        if (lane == 0 && t + 2 * sc.dt < tiles) arrive_leader<kCtas>(ptx::smem_addr(&ctrl->acc_empty[acc]));
         acc ^= 1u;
         if (acc == 0) acc_phase ^= 1u;
     }
@@ -895,13 +900,14 @@ __device__ __forceinline__ LastTile last_tile(const Params &p, uint32_t rank, in
 // to hide the drain behind, so 16 warps share it (the epilogue's and the row
 // converters', group g of four taking every fourth piece of columns).  The
 // converters' warps stage in the raw ring, which is idle now.
-template <bool kSwap, typename T>
+template <int kCtas, bool kSwap, typename T>
 __device__ __forceinline__ void drain_last(const Params &p, const CUtensorMap *tmap_o, const Ctrl *ctrl,
                                            const LastTile &l, uint32_t tmem_base, uint32_t box, uint32_t raw, int warp,
                                            int lane, WaitCtl *wc)
 {
     if (__any_sync(0xFFFFFFFFu, aborted(wc))) {
         if (lane == 0) ptx::bulk_wait<0>();  // earlier tiles' stores
+        if (kCtas == 2) fence_cluster();     // and arrivals (see the call)
         return;
     }
     ptx::tc_fence_after();
@@ -1095,7 +1101,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (drains) splitk_reduce<T>(p, ctrl, last, tmem_base, raw, warp, lane, wc);
     } else {
         __syncthreads();  // every role of this CTA is done
-        if (drains) drain_last<kSwap, T>(p, &tmap_o, ctrl, last, tmem_base, box, raw, warp, lane, wc);
+        // after an abort, arrivals on the leader's barriers that nothing has waited
+        // for may be under way: they come before this CTA's part in the meeting below
+        if (kCtas == 2 && !drains && __any_sync(0xFFFFFFFFu, aborted(wc))) fence_cluster();
+        if (drains) drain_last<kCtas, kSwap, T>(p, &tmap_o, ctrl, last, tmem_base, box, raw, warp, lane, wc);
     }
     __syncwarp();
     ptx::tc_fence_before();
