@@ -24,20 +24,29 @@ import dense_gemm_09_gb300 as dg
 
 def _rows(n: int, cols: int, dtype, device) -> torch.Tensor:
     """n x cols with rows on 16-byte boundaries (the fast kernels' condition)."""
-    step = 16 // torch.empty((), dtype=dtype).element_size()
+    step = 16 // dtype.itemsize
+    if cols % step == 0:
+        return torch.empty((n, cols), dtype=dtype, device=device)
     return torch.empty((n, -(-cols // step) * step), dtype=dtype, device=device)[:, :cols]
 
 
 def quantize_weights(w: torch.Tensor):
     """Int8 rows and scales of a weight matrix (a row for each output channel)."""
     q = _rows(w.shape[0], w.shape[1], torch.int8, w.device)
-    return dg.quantize_i8(w, q, torch.empty(w.shape[0], device=w.device))
+    return dg.quantize_i8(w, q, torch.empty(w.shape[0], dtype=torch.float32, device=w.device))
 
 
 class GatedMlp:
     """The layer, for up to `most` tokens at a time.  gamma: the norm's weights;
     w_gate, w_up: ffn x hidden; w_down: hidden x ffn (float32, float16 or
-    bfloat16, as nn.Linear stores them)."""
+    bfloat16, as nn.Linear stores them).
+
+    A layer may be called from several streams and threads at once, and replayed
+    in graphs beside them: each call's rows are its own, allocated on the
+    current stream (in a capture, in the graph's memory) as torch allocates any
+    tensor.  q1, t1, gu, q2, t2 are the last call's, to look at."""
+
+    q1 = t1 = gu = q2 = t2 = None
 
     def __init__(self, gamma, w_gate, w_up, w_down, most: int, dtype=torch.bfloat16, eps: float = 1e-6):
         dev, (ffn, hidden) = w_gate.device, w_gate.shape
@@ -45,18 +54,22 @@ class GatedMlp:
         # the two projections of the same rows are one product
         self.w1, self.s1 = quantize_weights(torch.cat([w_gate, w_up]))
         self.w2, self.s2 = quantize_weights(w_down)
-        self.q1, self.q2 = _rows(most, hidden, torch.int8, dev), _rows(most, ffn, torch.int8, dev)
-        self.t1, self.t2 = torch.empty(most, device=dev), torch.empty(most, device=dev)
-        self.gu = _rows(most, 2 * ffn, dtype, dev)
+        self.hidden, self.dtype, self.most = hidden, dtype, most
 
     def __call__(self, h: torch.Tensor) -> torch.Tensor:
         """h (tokens x hidden, the residual stream) is updated and returned."""
-        m = h.shape[0]
-        q1, t1, gu, q2, t2 = self.q1[:m], self.t1[:m], self.gu[:m], self.q2[:m], self.t2[:m]
+        m, ffn, dev = h.shape[0], self.ffn, h.device
+        if m > self.most:
+            raise ValueError("%d tokens, the layer was made for %d" % (m, self.most))
+        q1, t1 = _rows(m, self.hidden, torch.int8, dev), torch.empty(m, dtype=torch.float32, device=dev)
         dg.rmsnorm_i8(h, self.gamma, q1, t1, eps=self.eps)
+        gu = _rows(m, 2 * ffn, self.dtype, dev)
         dg.gemm_i8_tn(q1, self.w1, gu, t1, self.s1)
-        dg.swiglu_i8(gu[:, :self.ffn], gu[:, self.ffn:], q2, t2)
-        return dg.gemm_i8_tn(q2, self.w2, h, t2, self.s2, beta=1.0)
+        q2, t2 = _rows(m, ffn, torch.int8, dev), torch.empty(m, dtype=torch.float32, device=dev)
+        dg.swiglu_i8(gu[:, :ffn], gu[:, ffn:], q2, t2)
+        dg.gemm_i8_tn(q2, self.w2, h, t2, self.s2, beta=1.0)
+        self.q1, self.t1, self.gu, self.q2, self.t2 = q1, t1, gu, q2, t2
+        return h
 
 
 def plain(h, gamma, w_gate, w_up, w_down, eps: float = 1e-6):
