@@ -436,6 +436,13 @@ __device__ __forceinline__ int vec_len(int64_t cols, int64_t c)
     return left >= kVec ? kVec : left > 0 ? static_cast<int>(left) : 0;
 }
 
+// 1 / sqrt(mean + eps) from the sum of a row's squares.  A sum past FP32's range
+// marks the row like a NaN in it.
+__device__ __forceinline__ float norm_factor(float ss, int64_t cols, float eps)
+{
+    return ss < __uint_as_float(0x7F800000u) ? rsqrtf(ss / static_cast<float>(cols) + eps) : __uint_as_float(0x7FC00000u);
+}
+
 // A row held by its threads, from its values before the norm / quantisation to
 // H, the scale and q.  weights(j, g) gives the norm's weights of vector j.
 template <int kOp, typename T, bool kAligned, bool kWarp, int kVecs, typename W>
@@ -466,8 +473,7 @@ __device__ __forceinline__ void finish_row(const RowParams &p, int64_t row, int 
         }
         most = __float_as_uint(amax) & 0x7FFFFFFFu;
         row_sum_max<kWarp>(ss, most, s_sum, s_max);
-        // a sum of squares past FP32's range marks the row like a NaN in it
-        rstd = ss < __uint_as_float(0x7F800000u) ? rsqrtf(ss / static_cast<float>(cols) + p.eps) : __uint_as_float(0x7FC00000u);
+        rstd = norm_factor(ss, cols, p.eps);
     } else {
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) amax = max_abs(amax, v[j]);
@@ -619,13 +625,25 @@ __global__ void __launch_bounds__(kMost < 128 ? 128 : kMost, kMost < 128 ? 6 : 1
     }
 }
 
+// The norm with an eps below this comes here whatever the row's length.  The squares
+// of a row of small values leave FP32's range; from 2^-100 on, what is lost of them
+// is nothing beside eps.  Without, a row of values below 2^-40, some of whose squares
+// would be lost, is multiplied by 2^90, exactly, and eps by its square.  (The
+// squares of 2^-149 and 2^-40 become 2^-118 and 2^100.)  A row of zeros stays one,
+// even with an eps of 0.
+// It costs passes over the row (norm with residual, bf16, eps of 1e-6 and of 0: 8192
+// rows of 1024 9.4 and 17.3 us, of 8192 71 and 210); in the kernels above the branch
+// alone would cost every norm its registers (32 values a thread in 64 of them: up
+// to 152 bytes spilled).
+constexpr float kSmallEps = 0x1p-100f, kSmallRow = 0x1p-40f, kSmallFactor = 0x1p90f;
+
 // Rows longer than one block's registers: the same three steps, each reading
 // the row again (the second and third mostly from L2).  H is stored in the
 // last pass, so it may be the buffer of X or of the residual here too.
 template <int kOp, typename T, bool kAligned>
 __global__ void __launch_bounds__(1024) long_rows_kernel(const RowParams p)
 {
-    constexpr int kThreads = 1024;
+    const int step = static_cast<int>(blockDim.x) * kVec;
     __shared__ float s_sum[32];
     __shared__ uint32_t s_max[32];
     chain_wait();
@@ -635,27 +653,42 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(const RowParams p)
         combine<kOp>(p, load_raw<T, kAligned>(static_cast<const T *>(p.x) + row * p.ldx + c, n),
                      load_second<kOp, T, kAligned>(p, row, c, n), v);
     };
-    float rstd = 1.f, amax = 0.f;
+    float rstd = 1.f, amax = 0.f, factor = 1.f;
     if constexpr (is_norm(kOp)) {
-        float ss = 0.f;
-        for (int64_t c = static_cast<int64_t>(threadIdx.x) * kVec; c < p.cols; c += kThreads * kVec) {
+        float ss = 0.f, eps = p.eps;
+        bool zeros = false;
+        if (eps < kSmallEps) {
+            float largest = 0.f;
+            for (int64_t c = static_cast<int64_t>(threadIdx.x) * kVec; c < p.cols; c += step) {
+                float v[kVec];
+                value(c, vec_len(p.cols, c), v);
+                largest = max_abs(largest, v);
+            }
+            largest = __uint_as_float(row_max<false>(__float_as_uint(largest) & 0x7FFFFFFFu, s_max));
+            zeros = largest == 0.f;
+            if (largest < kSmallRow) {
+                factor = kSmallFactor;
+                eps = eps * kSmallFactor * kSmallFactor;  // (the factors' own product is past FP32)
+            }
+        }
+        for (int64_t c = static_cast<int64_t>(threadIdx.x) * kVec; c < p.cols; c += step) {
             float v[kVec];
             value(c, vec_len(p.cols, c), v);
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) ss = fmaf(v[i], v[i], ss);
+            for (int i = 0; i < kVec; ++i) ss = fmaf(v[i] * factor, v[i] * factor, ss);
         }
         ss = row_sum<false>(ss, s_sum);
-        rstd = ss < __uint_as_float(0x7F800000u) ? rsqrtf(ss / static_cast<float>(p.cols) + p.eps) : __uint_as_float(0x7FC00000u);
+        rstd = zeros ? 0.f : norm_factor(ss, p.cols, eps);
     }
     auto weigh = [&](int64_t c, int n, float (&v)[kVec]) {
         if constexpr (is_norm(kOp)) {
             float g[kVec];
             load_gamma<T, kAligned>(p, c, n, g);
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) v[i] *= g[i];
+            for (int i = 0; i < kVec; ++i) v[i] *= factor * g[i];
         }
     };
-    for (int64_t c = static_cast<int64_t>(threadIdx.x) * kVec; c < p.cols; c += kThreads * kVec) {
+    for (int64_t c = static_cast<int64_t>(threadIdx.x) * kVec; c < p.cols; c += step) {
         float v[kVec];
         const int n = vec_len(p.cols, c);
         value(c, n, v);
@@ -664,7 +697,7 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(const RowParams p)
     }
     const RowQuantiser<kOp, T> qz(row_max<false>(__float_as_uint(amax) & 0x7FFFFFFFu, s_max), rstd);
     if (threadIdx.x == 0) p.scale[row] = qz.scale;
-    for (int64_t c = static_cast<int64_t>(threadIdx.x) * kVec; c < p.cols; c += kThreads * kVec) {
+    for (int64_t c = static_cast<int64_t>(threadIdx.x) * kVec; c < p.cols; c += step) {
         float v[kVec];
         const int n = vec_len(p.cols, c);
         value(c, n, v);
@@ -810,8 +843,10 @@ const char *launch_rows_by_length(const RowParams &p, cudaStream_t stream)
     const int64_t vecs = (p.cols + kVec - 1) / kVec;
     const int64_t wide = p.rows * (vecs <= 1024 ? vecs : (vecs + 1) / 2);  // threads
     const bool few = wide <= kResident;
-    if (vecs > 4096) {
-        launch_chained(long_rows_kernel<kOp, T, kAligned>, static_cast<unsigned>(p.rows), 1024, 0, stream, 1, p);
+    if (vecs > 4096 || (is_norm(kOp) && p.eps < kSmallEps)) {
+        // (shorter rows, there for their eps: four vectors a thread)
+        const unsigned threads = vecs > 4096 ? 1024u : static_cast<unsigned>((vecs + 127) / 128 * 32);
+        launch_chained(long_rows_kernel<kOp, T, kAligned>, static_cast<unsigned>(p.rows), threads, 0, stream, 1, p);
         return "i8_long_rows";
     }
     if (few && vecs > 32 && vecs <= 1024)

@@ -306,7 +306,9 @@ int quantize_i8(int64_t rows, int64_t cols, const void *X, int64_t ldx, int type
  *     h = X + residual,   y = h * gamma / sqrt(mean(h^2) + eps)
  *   residual : same type as X; NULL for none.
  *   gamma    : `cols` weights of gamma_type, which is `type` or DGEMM_TYPE_F32.
- *   eps      : >= 0 (DGEMM_ERR_INVALID_ARG otherwise, NaN too).
+ *   eps      : >= 0 (DGEMM_ERR_INVALID_ARG otherwise, NaN too).  With eps == 0, h
+ *              of any size down to FP32's smallest has its norm, and a row of
+ *              zeros gives zeros; an eps below 2^-100 takes a slower kernel.
  *   H        : if not NULL, receives h rounded to `type`; may be X's or the
  *              residual's own buffer (with the same leading dimension).  The
  *              norm is taken of the unrounded h.
