@@ -394,11 +394,17 @@ __device__ __forceinline__ void row_sum_max(float &sum, uint32_t &most, float *s
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
 }
 
-// g / (1 + exp(-g)).  The fast division is within 2 ulp up to 2^126 and gives
-// 0 above, where the quotient is below 1e-35 anyway.
+// g / (1 + exp(-g)).  1 + exp(-g) is formed as 4 (1/4 + 2^(-g log2 e - 2)), whose
+// second factor's reciprocal is a normal number up to the largest finite sum (2^128,
+// at g = -88.7, where the quotient is 2^-121: a large u makes an ordinary value of
+// it), so that the plain approximations do, flushing what is below (ex2 within
+// 2^-22, rcp within 2^-23).  Past it the quotient is 0, as in FP32 arithmetic.
 __device__ __forceinline__ float silu(float g)
 {
-    return __fdividef(g, 1.f + __expf(-g));
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(g, -1.4426950408889634f, -2.f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(0.25f + e));
+    return g * (0.25f * r);
 }
 
 // The values before the norm / quantisation: x, the residual's sum, or the
