@@ -395,7 +395,11 @@ def gemm_i8_tn(A, B, C, scale_a, scale_b, bias=None, beta: float = 0.0, stream=N
     and bias float32.  Rows on 16-byte boundaries (any length K; pad the
     pitch) take the fast kernels."""
     m, entry = _i8("gemm_i8_tn")
-    return m.gemm_i8_tn(entry, A, B, C, scale_a, scale_b, bias, beta, stream)
+    try:
+        return m.gemm_i8_tn(entry, A, B, C, scale_a, scale_b, bias, beta, stream)
+    except BaseException:
+        lib().dgemm_tune_i8_next(0, 0, 1)  # a request of tune_i8_next was for this call
+        raise
 
 
 # Kernels for tune_i8_next (see dgemm_tune_i8_next in include/dgemm.h)

@@ -308,6 +308,7 @@ extern "C" int gemm_i8_tn(int64_t M, int64_t N, int64_t K, const int8_t *A, int6
                           const int8_t *B, int64_t ldb, const float *scale_b, const float *bias, float beta, void *C,
                           int64_t ldc, int c_type, cudaStream_t stream)
 {
+    const I8Config tune = i8_take_tune();  // (before any return: it is for this call only)
     int st = validate(M, N, K, 1.f, A, lda, B, ldb, K, C, ldc);
     if (st != DGEMM_OK) return st;
     if (!known_type(c_type)) return DGEMM_ERR_INVALID_ARG;
@@ -317,7 +318,7 @@ extern "C" int gemm_i8_tn(int64_t M, int64_t N, int64_t K, const int8_t *A, int6
     DeviceInfo dev;
     if ((st = check_device(dev)) != DGEMM_OK) return st;
     const I8Params p{M, N, K, A, B, lda, ldb, scale_a, scale_b, bias, beta, C, ldc};
-    return finish(launch_gemm_i8(p, c_type, stream, dev));
+    return finish(launch_gemm_i8(p, c_type, tune, stream, dev));
 }
 
 extern "C" int quantize_i8(int64_t rows, int64_t cols, const void *X, int64_t ldx, int type, int8_t *Q, int64_t ldq,

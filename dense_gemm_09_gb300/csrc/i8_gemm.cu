@@ -304,22 +304,26 @@ I8Config choose_config(const I8Params &p, int sm_count, bool (*fits)(const I8Par
     return best.cfg;
 }
 
-// Kernel names by configuration, built once.
-const char *config_name(const I8Config &c)
+// Kernel names by configuration, built once.  A tile with fewer K blocks than the
+// split asked for has one CTA a block.
+const char *config_name(const I8Config &c, int64_t K)
 {
-    static std::string names[17][9][2];
+    static std::string names[17][9][9];  // by width, split (0: pairs) and CTAs that ran (0, 1: pairs' rows)
     static std::once_flag once;
     std::call_once(once, [] {
         for (int w = 1; w <= 16; ++w) {
             const std::string bn = std::to_string(16 * w);
             names[w][0][0] = "i8_umma_pair_256x" + bn + "_tokens";
             names[w][0][1] = "i8_umma_pair_256x" + bn + "_channels";
-            for (int S = 1; S <= 8; ++S) names[w][S][0] = "i8_umma_128x" + bn + "_channels_split" + std::to_string(S);
+            for (int S = 1; S <= 8; ++S)
+                for (int ran = 1; ran <= S; ++ran)
+                    names[w][S][ran] = "i8_umma_128x" + bn + "_channels_split" + std::to_string(S) +
+                                       (ran < S ? "_ran_" + std::to_string(ran) : "");
         }
     });
     if (c.variant == kI8Decode) return c.split == 8 ? "i8_decode_16_channels_8_warps" : "i8_decode_16_channels_16_warps";
     if (c.variant == kI8Dot) return "i8_dot_4_channels";
-    if (c.variant == kI8Split) return names[c.bn / 16][c.split][0].c_str();
+    if (c.variant == kI8Split) return names[c.bn / 16][c.split][std::min<int64_t>(c.split, (K + 127) / 128)].c_str();
     return names[c.bn / 16][0][c.variant == kI8PairChannels ? 1 : 0].c_str();
 }
 
@@ -331,18 +335,17 @@ bool launch_config(const I8Params &p, int c_type, const I8Config &cfg, int sm_co
 
 }  // namespace
 
-const char *launch_gemm_i8(const I8Params &q, int c_type, cudaStream_t stream, const DeviceInfo &dev)
+const char *launch_gemm_i8(const I8Params &q, int c_type, const I8Config &tune, cudaStream_t stream,
+                           const DeviceInfo &dev)
 {
     I8Params p = q;
     // the pitch of a single row is never used
     if (p.M == 1) p.lda = (p.K + 15) / 16 * 16;
     if (p.N == 1) p.ldb = (p.K + 15) / 16 * 16;
-    I8Config cfg = t_tune;
-    t_tune = {kI8Auto, 0, 1};
-    if (tma_ok(p) && cfg.variant != kI8Mma) {
-        if (cfg.variant != kI8Auto && launch_config(p, c_type, cfg, dev.sm_count, stream)) return config_name(cfg);
-        cfg = choose_config(p, dev.sm_count, i8_umma_fits);
-        if (launch_config(p, c_type, cfg, dev.sm_count, stream)) return config_name(cfg);
+    if (tma_ok(p) && tune.variant != kI8Mma) {
+        if (tune.variant != kI8Auto && launch_config(p, c_type, tune, dev.sm_count, stream)) return config_name(tune, p.K);
+        const I8Config cfg = choose_config(p, dev.sm_count, i8_umma_fits);
+        if (launch_config(p, c_type, cfg, dev.sm_count, stream)) return config_name(cfg, p.K);
     }
     switch (c_type) {
     case DGEMM_TYPE_F32: return launch_mma<float>(p, stream);
@@ -359,6 +362,13 @@ int i8_tune_next(int variant, int bn, int split)
         return DGEMM_ERR_INVALID_ARG;
     t_tune = cfg;
     return DGEMM_OK;
+}
+
+I8Config i8_take_tune()
+{
+    const I8Config cfg = t_tune;
+    t_tune = {kI8Auto, 0, 1};
+    return cfg;
 }
 
 }  // namespace dgemm

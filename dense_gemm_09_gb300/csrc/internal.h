@@ -114,10 +114,14 @@ const char *launch_dequantize_i8(int64_t rows, int64_t cols, const int8_t *q, in
 
 // The 8-bit product (i8_gemm.cu); c_type is a dgemm_type.
 struct I8Params;
-const char *launch_gemm_i8(const I8Params &p, int c_type, cudaStream_t stream, const DeviceInfo &dev);
+struct I8Config;
+const char *launch_gemm_i8(const I8Params &p, int c_type, const I8Config &tune, cudaStream_t stream,
+                           const DeviceInfo &dev);
 
-// Tuning hook behind dgemm_tune_i8_next.
+// Tuning hook behind dgemm_tune_i8_next: the request of this host thread, and its
+// taking (by every gemm_i8_tn call, whatever becomes of it).
 int i8_tune_next(int variant, int bn, int split);
+I8Config i8_take_tune();
 
 // Device status word of the 8-bit tensor-core kernels.
 int i8_read_status(int clear);

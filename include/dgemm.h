@@ -490,7 +490,8 @@ int dgemm_tune_next(int variant, int bn, int split);
 
 /*
  * dgemm_tune_i8_next -- TUNING HOOK: as dgemm_tune_next, for the next
- * gemm_i8_tn call made by the calling host thread.
+ * gemm_i8_tn call made by the calling host thread, whether it launches
+ * anything or not.
  *   variant 0: automatic (the default);
  *           1: the mma.sync kernel for operands of any alignment;
  *           2: CTA pair, 256 tokens x bn channels (bn 64, 128, 192 or, if every
@@ -504,7 +505,8 @@ int dgemm_tune_next(int variant, int bn, int split);
  *           6: at most 2 tokens, dot products (split 1).
  * Returns DGEMM_ERR_INVALID_ARG (and records nothing) for values outside
  * these ranges, else DGEMM_OK.  A configuration the next call cannot take is
- * ignored; dgemm_last_kernel() names what ran.  Source: as dgemm_tune_next.
+ * ignored; dgemm_last_kernel() names what ran ("..._split8_ran_3": three CTAs,
+ * since K has no more blocks of 128).  Source: as dgemm_tune_next.
  */
 int dgemm_tune_i8_next(int variant, int bn, int split);
 
