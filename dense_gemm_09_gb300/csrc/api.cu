@@ -314,7 +314,8 @@ extern "C" int gemm_i8_tn(int64_t M, int64_t N, int64_t K, const int8_t *A, int6
     if (!known_type(c_type)) return DGEMM_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return DGEMM_OK;
     if (!scale_a || !scale_b) return DGEMM_ERR_INVALID_ARG;
-    if ((M + 63) / 64 > INT32_MAX / ((N + 63) / 64)) return DGEMM_ERR_INVALID_ARG;
+    // (no sum that could pass 2^63)
+    if ((M - 1) / 64 + 1 > INT32_MAX / ((N - 1) / 64 + 1)) return DGEMM_ERR_INVALID_ARG;
     DeviceInfo dev;
     if ((st = check_device(dev)) != DGEMM_OK) return st;
     const I8Params p{M, N, K, A, B, lda, ldb, scale_a, scale_b, bias, beta, C, ldc};

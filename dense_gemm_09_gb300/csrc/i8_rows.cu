@@ -822,7 +822,7 @@ int piped_blocks(unsigned threads)
 template <int kOp, typename T, bool kAligned, int kMost, int kVecs>
 void launch_rows(const RowParams &p, cudaStream_t stream)
 {
-    const int64_t vecs = (p.cols + kVec - 1) / kVec;
+    const int64_t vecs = (p.cols - 1) / kVec + 1;
     // threads: a warp for each 32 * kVecs vectors
     const unsigned threads = kMost == 32 ? 128u : static_cast<unsigned>((vecs + 32 * kVecs - 1) / (32 * kVecs) * 32);
     const unsigned grid = static_cast<unsigned>(kMost == 32 ? (p.rows + 3) / 4 : p.rows);
@@ -846,7 +846,7 @@ void launch_rows(const RowParams &p, cudaStream_t stream)
 template <int kOp, typename T, bool kAligned>
 const char *launch_rows_by_length(const RowParams &p, cudaStream_t stream)
 {
-    const int64_t vecs = (p.cols + kVec - 1) / kVec;
+    const int64_t vecs = (p.cols - 1) / kVec + 1;
     const int64_t wide = p.rows * (vecs <= 1024 ? vecs : (vecs + 1) / 2);  // threads
     const bool few = wide <= kResident;
     if (vecs > 4096 || (is_norm(kOp) && p.eps < kSmallEps)) {
@@ -908,7 +908,7 @@ const char *launch_dequantize_typed(int64_t rows, int64_t cols, const int8_t *q,
 {
     T *out = static_cast<T *>(x);
     if (!aligned(q, ldq, 1, 16) || !aligned(x, ldx, sizeof(T), 16)) {
-        const int64_t across = (cols + kAnyCols - 1) / kAnyCols;
+        const int64_t across = (cols - 1) / kAnyCols + 1;
         if (across > INT32_MAX) return nullptr;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(across), static_cast<unsigned>(rows < 65535 ? rows : 65535));
@@ -920,7 +920,7 @@ const char *launch_dequantize_typed(int64_t rows, int64_t cols, const int8_t *q,
         cudaLaunchKernelEx(&cfg, dequantize_any_kernel<T>, rows, cols, q, ldq, scale, out, ldx);
         return "i8_dequantize_any";
     }
-    const int64_t pieces = (cols + kPiece - 1) / kPiece;
+    const int64_t pieces = (cols - 1) / kPiece + 1;
     if (pieces > INT32_MAX) return nullptr;
     const int64_t cap = static_cast<int64_t>(dev.sm_count) * 32;
     const int64_t most = INT32_MAX / pieces;  // rows of one launch: 32-bit piece numbers
