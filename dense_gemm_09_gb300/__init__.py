@@ -341,7 +341,11 @@ def _calls():
     global _calls_module
     with _lock:
         if _calls_module is None:
-            from importlib import import_module
+            from importlib import import_module, machinery, util
+            spec = util.find_spec("._i8_calls", __name__)
+            if spec is not None and not str(spec.origin).endswith(machinery.EXTENSION_SUFFIXES[0]):
+                # it reads Python objects by the layout it was compiled with
+                raise RuntimeError("%s may be another interpreter's; run dense_gemm_09_gb300.build()" % spec.origin)
             try:
                 m = import_module("._i8_calls", __name__)
             except ImportError as e:

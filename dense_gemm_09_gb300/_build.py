@@ -9,7 +9,8 @@ The checked build (libdgemm_checked.so, objects under _build/checked/) is
 the same sources compiled with -DDGEMM_CHECKED: device-side bounds checks on
 the indices the kernels compute (see csrc/checked.cuh).  build_all() compiles
 both libraries' units at once, and the CPython module that marshals the 8-bit
-calls (binding/i8_calls.c -> _i8_calls.so, by gcc).
+calls (binding/i8_calls.c, by gcc), whose file name carries the interpreter's tag:
+another interpreter looks for another file.
 """
 from __future__ import annotations
 
@@ -19,6 +20,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+from importlib.machinery import EXTENSION_SUFFIXES
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -28,7 +30,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdgemm.so")
 LIB_CHECKED = os.path.join(PKG, "libdgemm_checked.so")
 CALLS_SRC = os.path.join(PKG, "binding", "i8_calls.c")
-CALLS = os.path.join(PKG, "_i8_calls.so")
+CALLS = os.path.join(PKG, "_i8_calls" + EXTENSION_SUFFIXES[0])
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
@@ -67,13 +69,21 @@ def _variant(checked: bool):
     return LIB, BUILD, []
 
 
-def build_calls(force: bool = False) -> str:
+def build_calls(force: bool = False) -> str | None:
     """Compile the CPython module of the 8-bit calls against this interpreter's
-    headers."""
+    headers.  Without them it is left out, with a line on stderr: the 8-bit calls
+    of the Python package then raise, the C ABI and the other calls do without."""
+    untagged = os.path.join(PKG, "_i8_calls.so")  # any interpreter would take it
+    if os.path.exists(untagged):
+        os.remove(untagged)
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        print("no Python.h in %s: the Python package's 8-bit calls are not built" % include, file=sys.stderr)
+        return None
     if force or not os.path.exists(CALLS) or os.path.getmtime(CALLS) < os.path.getmtime(CALLS_SRC):
         tmp = CALLS + ".tmp%d" % os.getpid()
-        subprocess.check_call(["gcc", "-O2", "-std=c11", "-Wall", "-fPIC", "-shared",
-                               "-I" + sysconfig.get_paths()["include"], "-o", tmp, CALLS_SRC])
+        subprocess.check_call(["gcc", "-O2", "-std=c11", "-Wall", "-fPIC", "-shared", "-I" + include,
+                               "-o", tmp, CALLS_SRC])
         os.replace(tmp, CALLS)
     return CALLS
 
