@@ -6,9 +6,11 @@
 // FP16 rate, but every int8 value is exact in FP16, a product of two is exact
 // in FP32, and sums of such products are exact while they stay below 2^24
 // (K <= 1024 always; real data far longer), so the product runs on
-// kind::f16 with FP32 accumulators in tensor memory and loses nothing to an
-// integer one.  Operands stay int8 in HBM and L2 and on their way into the
-// SM; they are widened to FP16 inside it.
+// kind::f16 with FP32 accumulators in tensor memory and up to there loses nothing
+// to an integer one.  Past 2^24 the accumulator truncates at every MMA (16384
+// products of one sign: 4.8e-5 of the sum on average, always towards zero).
+// Operands stay int8 in HBM and L2 and on their way into the SM; they are
+// widened to FP16 inside it.
 //
 // What bounds it.  The tensor pipe, once shared memory is kept out of the way:
 // each SM moves 128 bytes a clock through it, and a K step of 64 costs a CTA of

@@ -337,9 +337,14 @@ int dequantize_i8(int64_t rows, int64_t cols, const int8_t *Q, int64_t ldq, cons
  *   bias    : N floats, or NULL for none.
  *   beta    : scale of the old C, which is not read when beta == 0.
  *   C, ldc  : device, c_type (a dgemm_type), M x N row-major (ldc >= N).
- * The sum is exact wherever its partial sums stay below 2^24 (always for K
- * <= 1024), and within FP32 rounding of each partial sum beyond; the rest is
- * formed in FP32 and rounded once to c_type.
+ * The sum is exact wherever sum_k |A[m, k] B[n, k]| < 2^24 (always for K <= 1024;
+ * normally distributed rows that fill the 8 bits, up to K ~ 20000).  Beyond, it depends on the
+ * kernel, and so on M: for few tokens, and for rows off 16 bytes, it is a whole
+ * number rounded once to FP32; otherwise it is kept in FP32 in the tensor cores,
+ * which truncate: each step of 16 products may lose up to a unit in the last place
+ * of the running sum, towards zero (5e-5 of a sum of 16384 products of one sign).
+ * So a row of A may give other bits in a larger batch there.  The rest is formed
+ * in FP32 and rounded once to c_type.
  * K == 0 gives bias + beta * C (A and B are not read; the scales are).
  * DGEMM_ERR_INVALID_ARG as above, and for more than 2^31 - 1 tiles of 64 x 64
  * of C.
