@@ -778,10 +778,18 @@ __global__ void __launch_bounds__(256)
     const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kAnyCols + threadIdx.x;
     for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
         const float s = load_f32(scale + row);
+        // all of them loaded before the first store, which the compiler has to take
+        // for a store into q
+        int8_t v[kAnyCols / 256];
 #pragma unroll
         for (int k = 0; k < kAnyCols / 256; ++k) {
             const int64_t c = c0 + k * 256;
-            if (c < cols && DGEMM_CHECK(row >= 0)) x[row * ldx + c] = from_f32<T>(static_cast<float>(q[row * ldq + c]) * s);
+            v[k] = c < cols ? q[row * ldq + c] : static_cast<int8_t>(0);
+        }
+#pragma unroll
+        for (int k = 0; k < kAnyCols / 256; ++k) {
+            const int64_t c = c0 + k * 256;
+            if (c < cols && DGEMM_CHECK(row >= 0)) x[row * ldx + c] = from_f32<T>(static_cast<float>(v[k]) * s);
         }
     }
 }
