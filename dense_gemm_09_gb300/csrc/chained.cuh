@@ -12,7 +12,10 @@
 // So an operand of such a kernel may be written while the kernel already runs,
 // and the non-coherent loads (ld.global.nc, __ldg, const __restrict__
 // parameters), which may count on read-only data and move across the wait, do
-// not fit: the kernels load through the functions here, which stay behind it.
+// not fit.  Vectors and scales are loaded through the functions here, whose
+// assembly is volatile like chain_wait()'s and stays behind it.  Single elements
+// are plain loads through pointers without restrict: chain_wait() says that it
+// writes memory, so the compiler keeps them behind it too.
 #pragma once
 
 #include <cstdint>
@@ -59,6 +62,16 @@ __device__ __forceinline__ uint4 load_v4(const void *p)
         asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                      : "l"(p));
+    return v;
+}
+
+// The bytes are read once and may leave the caches first.
+__device__ __forceinline__ uint4 load_v4_stream(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.cs.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
     return v;
 }
 

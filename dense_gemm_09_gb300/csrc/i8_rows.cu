@@ -102,7 +102,8 @@ __device__ __forceinline__ Raw<T> load_raw(const T *p, int n)
     if (kAligned && n == kVec) {
 #pragma unroll
         for (int i = 0; i < Raw<T>::kWords; ++i)
-            r.w[i] = kKeep ? load_v4(reinterpret_cast<const uint4 *>(p) + i) : __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+            r.w[i] = kKeep ? load_v4(reinterpret_cast<const uint4 *>(p) + i)
+                           : load_v4_stream(reinterpret_cast<const uint4 *>(p) + i);
         return r;
     }
     alignas(16) T e[kVec];
@@ -743,7 +744,7 @@ __global__ void __launch_bounds__(256)
         const float s = load_f32(scale + row);
         alignas(16) int8_t e[kPiece];
         if (left >= kPiece) {
-            *reinterpret_cast<uint4 *>(e) = __ldcs(reinterpret_cast<const uint4 *>(src));
+            *reinterpret_cast<uint4 *>(e) = load_v4_stream(src);
         } else {
 #pragma unroll
             for (int k = 0; k < kPiece; ++k) e[k] = k < left ? src[k] : static_cast<int8_t>(0);
