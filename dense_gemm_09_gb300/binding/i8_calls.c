@@ -4,7 +4,7 @@
  *
  * These calls take a few microseconds of GPU time for one token, and through
  * ctypes a call spent 5 to 7 us on the host, most of it on reading and checking
- * tensors' attributes in Python; here it spends 3 to 4, of which the launch
+ * tensors' attributes in Python; here it spends 3.5 to 4.6, of which the launch
  * itself is ~2.  The module does what the ctypes binding does for the other
  * calls: reads pointers, pitches and the current stream, checks shapes, types
  * and devices, calls the C ABI and raises.  It links neither torch nor the library:

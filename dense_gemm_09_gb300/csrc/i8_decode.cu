@@ -9,17 +9,19 @@
 // i8_dot_kernel, 1 and 2 tokens: four-way dot products on the integer pipes.  A
 //   warp reads 512 contiguous bytes of each of four channels at a time, so
 //   every line that leaves L2 is used whole, and the work is dealt evenly
-//   over all warps.  One token: 8192 x 4096 weights in 5.6 us (6.0 TB/s), 28672
-//   x 4096 in 19.8 (5.9 TB/s); a tail of blocks, dealt by whole rows, took 7.0
-//   and 19.9.
+//   over all warps.  One token, weights cycled past the L2: 8192 x 4096 in 7.3 us
+//   (4.6 TB/s: start and end of the launch show), 28672 x 4096 in 19.8 (5.9 TB/s),
+//   16384 x 16384 in 42.7 (6.3 TB/s).  The same 8192 x 4096 weights every time
+//   stay in L2: 5.6 us, and 7.0 for a tail of blocks dealt by whole rows.
 // i8_decode_kernel, up to 32 tokens: mma.sync m16n8k32 on int8, its 16 rows the
 //   channels, its 8 columns the tokens.  A fragment wants four 4-byte pieces
 //   of a row, 16 bytes apart; since any order of K will do as long as both
 //   operands follow it, each thread instead loads 16 contiguous bytes and
 //   uses them as the pieces of two products.  The integer tensor rate (a
 //   product takes ~20 clocks of an SM) keeps pace with memory for one group
-//   of 8 tokens (8192 x 4096: 8.2 us); more groups pay where a tensor-core
-//   launch's fixed cost is larger (32 tokens, 2048 x 2048: 4.2 against 6.8 us).
+//   of 8 tokens (8192 x 4096: 9.6 us with cold weights, 6.7 from L2); more groups
+//   pay where a tensor-core launch's fixed cost is larger (32 tokens, 2048 x
+//   2048: 4.2 against 6.8 us).
 //   The warps of a block read neighbouring pieces of its rows; dealt in even
 //   ranges like the dot products', a warp walking along K by itself, they
 //   took longer (8 tokens, 8192 x 4096 9.9, 1024 x 8192 9.1 against 4.0 us).
@@ -259,8 +261,8 @@ void launch_dot(const I8Params &p, int sm_count, cudaStream_t stream)
 }
 
 // Two units of a warp in flight where blocks have few groups, else one and a
-// block more an SM (1 token: 4096 x 4096 3.2 and 3.6 us, 8192 x 4096 5.9 and
-// 5.6, 28672 x 4096 20.3 and 19.8).
+// block more an SM (1 token, the same weights every time: 4096 x 4096 3.2 and 3.6
+// us, 8192 x 4096 5.9 and 5.6, 28672 x 4096 20.3 and 19.8).
 template <typename T>
 void launch_dot_tokens(const I8Params &p, int sm_count, cudaStream_t stream)
 {

@@ -555,8 +555,9 @@ __device__ __forceinline__ void copy_async16(uint4 *dst, const void *src, int by
 // us, of 12288 58.9 and 46.1; swiglu of 8192 52.7 and 50.5, of 12288 85.4 and
 // 74.4; norm of 8192 43.6 and 39.4, of 12288 78.3 and 59.6.  The norm with
 // residual, which stores H too, loses (of 8192 71.3 and 85.8) except where an SM
-// holds one row at a time (4096 rows of 20000 106.5 and 88.4, 2048 of 32768
-// 81.3 and 83.9).
+// holds one row at a time, from 16385 columns on: 4096 rows of 16400 97.2 and 80.7,
+// of 20000 105.3 and 89.4, of 24576 119.7 and 116.7, 700 of 28672 29.6 and 24.9;
+// the end of that range is even (2048 of 32768 81.8 and 83.3).
 constexpr bool is_piped(int op, int most_threads)
 {
     return op != kOpNorm || most_threads == 1024;

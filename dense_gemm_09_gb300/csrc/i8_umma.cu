@@ -23,8 +23,9 @@
 // clocks.  Measured with operands in place, an MMA of K = 16 takes N / 2 + 10
 // clocks with A in tensor memory (N / 2 + 43 with A in shared memory): 848
 // clocks for 128 K values at N = 192, and the kernel takes 850.  8192 x 8192 x
-// 4096 to bf16: 295 us, 1865 TFLOP/s, 98 % of the measured bf16 GEMM rate
-// (321 us in a long run, where the power limit sets the clock).
+// 4096 to bf16: 295 us, 1865 TFLOP/s, 96 % of the measured bf16 GEMM rate
+// (up to 327 us in a long run, where the power limit sets the clock: 98 % of
+// the rate that is sustained there).
 //
 // Roles (32 warps, one CTA an SM):
 //   warp 0       TMA producer: 128-byte rows (128 K values) of both operands
