@@ -317,12 +317,10 @@ __device__ __forceinline__ void run_producer(const CUtensorMap *tmap_a, const CU
             }
         }
     }
-    if (!ok) {
-        // Do not leave while TMA may still be writing into this CTA's smem.
-        for (int s = 0; s < p.stages; ++s)
-            if ((issued >> s) & 1u)
-                drain_wait(ptx::smem_addr(&ctrl->full[s]), (issued_phase >> s) & 1u);
-    }
+    // Do not leave while TMA may still be writing into this CTA's smem, whichever
+    // role's wait has run out (if none has, these loads are waited for anyway).
+    for (int s = 0; s < p.stages; ++s)
+        if ((issued >> s) & 1u) drain_wait(ptx::smem_addr(&ctrl->full[s]), (issued_phase >> s) & 1u);
 }
 
 // Byte offset of (row r, byte b of the row) in a K-major tile of 128-byte
@@ -1433,9 +1431,10 @@ __device__ __forceinline__ void pair_producer(const CUtensorMap *tmap_a, const C
             }
         }
     }
-    if (!ok && half == 0) {
+    if (half == 0) {
         // The leader's barrier counts both CTAs' bytes: wait (bounded) for
-        // the loads in flight before the pair leaves.
+        // the loads in flight before the pair leaves, whichever role's wait has
+        // run out (if none has, they are waited for anyway).
         for (int s = 0; s < S::kStages; ++s)
             if ((issued >> s) & 1u)
                 drain_wait(ptx::smem_addr(&ctrl->full[s]), (issued_phase >> s) & 1u);
@@ -1735,12 +1734,8 @@ __device__ __forceinline__ void p128_producer(const CUtensorMap *tmap_a, const C
     const int64_t mh = m0 + rank * 64, nb = n0 + rank * (p.bn / 2);  // this CTA's rows of A, of B
     const uint32_t half = p128_half_bytes(p.bn);
     uint32_t stage = 0, phase = 0, issued = 0, issued_phase = 0;
-    bool ok = true;
     for (int64_t kb = 0; kb < p.num_kb; kb += 2) {
-        if (!wait_bounded_cluster(ptx::smem_addr(&ctrl->empty[stage]), phase ^ 1u, wc)) {
-            ok = false;
-            break;
-        }
+        if (!wait_bounded_cluster(ptx::smem_addr(&ctrl->empty[stage]), phase ^ 1u, wc)) break;
         const bool second = kb + 1 < p.num_kb;
         const uint32_t full_local = ptx::smem_addr(&ctrl->full[stage]);
         const uint32_t full = ptx::mapa(full_local, 0);  // the leader's barrier
@@ -1771,9 +1766,8 @@ __device__ __forceinline__ void p128_producer(const CUtensorMap *tmap_a, const C
             phase ^= 1u;
         }
     }
-    if (!ok && rank == 0) {
-        // the leader's barriers count both CTAs' bytes: wait (bounded) for
-        // the loads in flight before the pair leaves
+    if (rank == 0) {
+        // as pair_producer: the loads in flight, before the pair leaves
         for (int s = 0; s < p.stages; ++s)
             if ((issued >> s) & 1u) drain_wait(ptx::smem_addr(&ctrl->full[s]), (issued_phase >> s) & 1u);
     }
