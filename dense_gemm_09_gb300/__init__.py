@@ -22,6 +22,24 @@ Linear layers in 8-bit integers (int8 rows with one FP32 scale a row):
                                                  C = scale_a scale_b A@B.T + bias + beta*C
     dequantize_i8(Q, scale, X)                   X = scale * Q
 
+Linear layers in 8-bit floating point (an FP32 scale for each block of 128), and tokens
+by expert:
+
+    quantize_f8(X, Q, scale, transposed)         X in 8 bits, by rows, columns or 128 x 128
+    swiglu_f8(G, U, Q, scale)                    silu(G) * U in 8 bits
+    dequantize_f8(Q, scale, X)                   X = scale * Q
+    gemm_f8_tn(A, B, C, scale_a, scale_b, bias, beta)
+                                                 C = A@B.T + bias + beta*C, scaled block by block
+    gemm_f8_tn_experts(A, B, C, scale_a, scale_b, offsets)
+                                                 the same for each expert's rows and weights
+    sort_by_expert(experts, offsets, position)   where each (token, choice) goes
+    gather_by_expert(X, position, Y)             tokens to expert order
+    gather_by_expert_f8(X, position, Q, scale)   the same, in 8 bits
+    combine_experts(Y, position, weights, X, beta)
+                                                 and back: X = sum of weights * Y + beta*X
+    combine_experts_grad(dX, Y, position, weights, dY, dweights)
+                                                 its gradients
+
 Matrices are 2-D tensors with unit column stride; a row stride larger than
 the width is passed on as the leading dimension.  C is updated in place and
 returned.
@@ -49,6 +67,12 @@ class DgemmError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
         super().__init__("%s: %s" % (where, status_string(status)))
+
+
+class F8Matrix(ctypes.Structure):
+    """dgemm_f8 of include/dgemm.h, for callers of the C ABI through ctypes."""
+    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64), ("type", ctypes.c_int), ("block", ctypes.c_int),
+                ("scale", ctypes.c_void_p), ("scale_row", ctypes.c_int64), ("scale_blk", ctypes.c_int64)]
 
 
 def build(force: bool = False) -> str:
@@ -113,9 +137,22 @@ def _load(path: str):
     L.rmsnorm_i8.argtypes = [i64, i64, vp, i64, vp, i64, vp, ci, f32, ci, vp, i64, vp, i64, vp, vp]
     L.swiglu_i8.argtypes = [i64, i64, vp, i64, vp, i64, ci, vp, i64, vp, vp]
     L.dequantize_i8.argtypes = [i64, i64, vp, i64, vp, vp, i64, ci, vp]
-    for name in _I8_CALLS:
+    f8 = ctypes.POINTER(F8Matrix)
+    L.quantize_f8.argtypes = [i64, i64, vp, i64, ci, ci, f8, vp]
+    L.swiglu_f8.argtypes = [i64, i64, vp, i64, vp, i64, ci, f8, vp]
+    L.dequantize_f8.argtypes = [i64, i64, f8, vp, i64, ci, vp]
+    L.gemm_f8_tn.argtypes = [i64, i64, i64, f8, f8, vp, f32, vp, i64, ci, vp]
+    L.gemm_f8_tn_experts.argtypes = [i64, i64, i64, ci, vp, f8, f8, i64, i64, vp, i64, ci, vp]
+    L.sort_by_expert.argtypes = [i64, i64, ci, vp, ci, vp, vp, vp]
+    L.gather_by_expert.argtypes = [i64, i64, i64, vp, i64, ci, vp, i64, vp, i64, vp]
+    L.gather_by_expert_f8.argtypes = [i64, i64, i64, vp, i64, ci, vp, i64, f8, vp]
+    L.combine_experts.argtypes = [i64, i64, i64, vp, i64, i64, ci, vp, vp, f32, vp, i64, vp]
+    L.combine_experts_grad.argtypes = [i64, i64, i64, vp, i64, vp, i64, i64, ci, vp, vp, vp, i64, vp, vp]
+    L.dgemm_tune_f8_next.argtypes = [ci, ci, ci]
+    L.dgemm_tune_f8_next.restype = ci
+    for name in _I8_CALLS + _F8_CALLS:
         getattr(L, name).restype = ci
-    L.i8_entry = {name: ctypes.cast(getattr(L, name), vp).value for name in _I8_CALLS}
+    L.i8_entry = {name: ctypes.cast(getattr(L, name), vp).value for name in _I8_CALLS + _F8_CALLS}
     L.dgemm_test_pair_units.argtypes = [i64, i64, i64, i64, i64, vp, i64]
     L.dgemm_test_pair_units.restype = i64
     L.dgemm_test_stream_k_tiles.argtypes = [i64, i64, i64, ci, ci]
@@ -333,6 +370,8 @@ def gemm_bf16_nn(A, B, C, alpha: float = 1.0, beta: float = 0.0, stream=None):
 # the library's entry point.
 
 _I8_CALLS = ("gemm_i8_tn", "quantize_i8", "rmsnorm_i8", "swiglu_i8", "dequantize_i8")
+_F8_CALLS = ("quantize_f8", "swiglu_f8", "dequantize_f8", "gemm_f8_tn", "gemm_f8_tn_experts", "sort_by_expert",
+             "gather_by_expert", "gather_by_expert_f8", "combine_experts", "combine_experts_grad")
 _calls_module = None
 
 
@@ -352,7 +391,8 @@ def _calls():
                 raise RuntimeError("_i8_calls is not built; run dense_gemm_09_gb300.build()") from e
             m.setup(torch.float32, torch.float16, torch.bfloat16, torch.int8,
                     getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
-                    _raw_stream or _current_stream, DgemmError)
+                    _raw_stream or _current_stream, DgemmError,
+                    torch.float8_e4m3fn, torch.float8_e5m2, torch.int32, torch.int64)
             _calls_module = m
         return _calls_module
 
@@ -416,3 +456,112 @@ def tune_i8_next(variant: int, bn: int = 0, split: int = 1) -> None:
     st = lib().dgemm_tune_i8_next(int(variant), int(bn), int(split))
     if st != OK:
         raise DgemmError(st, "dgemm_tune_i8_next")
+
+
+# ---- linear layers in 8-bit floating point, and tokens by expert
+#
+# A matrix is float8_e4m3fn or float8_e5m2 with a float32 tensor of scales beside
+# it, one for each 128 columns: (rows, ceil(cols / 128)) where each row has its
+# own, (ceil(rows / 128), ceil(cols / 128)) where bands of 128 rows share them.
+# Scales may have any strides (a transposed view serves as it is).
+
+
+def quantize_f8(X, Q, scale, transposed: bool = False, stream=None):
+    """X (float32, float16 or bfloat16) in 8 bits: for each block, a = max|x|, scale
+    = a / 448 and Q = x * (448 / a) to nearest, ties to even (57344 for
+    float8_e5m2).  A block is 128 columns of a row, or 128 x 128 values, by the
+    shape of `scale`; with transposed, Q is X.T and a block 128 rows of a column of X.
+    Writes and returns (Q, scale); a block of zeros gets scale 0, one with a NaN or
+    an infinity scale NaN."""
+    m, entry = _i8("quantize_f8")
+    return m.quantize_f8(entry, X, Q, scale, transposed, stream)
+
+
+def swiglu_f8(G, U, Q, scale, stream=None):
+    """y = G / (1 + exp(-G)) * U in 8 bits, a scale for each 128 columns of a row.  G and
+    U may be column slices of one tensor.  Returns (Q, scale)."""
+    m, entry = _i8("swiglu_f8")
+    return m.swiglu_f8(entry, G, U, Q, scale, stream)
+
+
+def dequantize_f8(Q, scale, X, stream=None):
+    """X = Q * scale, block by block, rounded once to X's type."""
+    m, entry = _i8("dequantize_f8")
+    return m.dequantize_f8(entry, Q, scale, X, stream)
+
+
+def _f8_product(name, *args):
+    m, entry = _i8(name)
+    try:
+        return getattr(m, name)(entry, *args)
+    except BaseException:
+        lib().dgemm_tune_f8_next(0, 0, 1)  # a request of tune_f8_next was for this call
+        raise
+
+
+def gemm_f8_tn(A, B, C, scale_a, scale_b, bias=None, beta: float = 0.0, stream=None):
+    """C[m, n] = sum over blocks b of 128 along K of scale_a[m, b] * scale_b[n, b] *
+    (A_b @ B_b.T)[m, n], + bias[n] + beta * C[m, n]; A: M x K and B: N x K in 8 bits
+    (scales a row, or a band of 128 rows), C: M x N float32, float16 or bfloat16.
+    Rows on 16-byte boundaries (any length K; pad the pitch) take the fast kernels."""
+    return _f8_product("gemm_f8_tn", A, B, C, scale_a, scale_b, bias, beta, stream)
+
+
+def gemm_f8_tn_experts(A, B, C, scale_a, scale_b, offsets, stream=None):
+    """C[m] = A[m] @ B[e].T for offsets[e] <= m < offsets[e + 1]: rows sorted by expert
+    (M x K, a scale for each 128 columns of a row) times each expert's weights (experts x
+    N x K; scale_b with a leading dimension of experts too).  offsets: int32, experts + 1.
+    Rows that belong to no expert are left as they were."""
+    return _f8_product("gemm_f8_tn_experts", A, B, C, scale_a, scale_b, offsets, stream)
+
+
+def sort_by_expert(experts, offsets, position, stream=None):
+    """Sorts the pairs (token, choice) of `experts` (tokens x top, int32 or int64) by
+    expert, in their own order within one.  offsets (int32, number of experts + 1)
+    receives each expert's first row, position (int32, tokens x top) each pair's row; a
+    pair whose expert is not in 0 .. number - 1 has none (-1).  Returns (offsets,
+    position)."""
+    m, entry = _i8("sort_by_expert")
+    return m.sort_by_expert(entry, experts, offsets, position, stream)
+
+
+def gather_by_expert(X, position, Y, stream=None):
+    """Y[position[t, j]] = X[t]; the other rows of Y are left as they were.  Its gradient
+    is combine_experts(dY, position, None, dX)."""
+    m, entry = _i8("gather_by_expert")
+    return m.gather_by_expert(entry, X, position, Y, stream)
+
+
+def gather_by_expert_f8(X, position, Q, scale, stream=None):
+    """gather_by_expert of quantize_f8's rows: each token is read and quantised once.
+    Returns (Q, scale)."""
+    m, entry = _i8("gather_by_expert_f8")
+    return m.gather_by_expert_f8(entry, X, position, Q, scale, stream)
+
+
+def combine_experts(Y, position, weights, X, beta: float = 0.0, stream=None):
+    """X[t] = sum_j weights[t, j] * Y[position[t, j]] + beta * X[t], in FP32, rounded
+    once.  weights: float32, tokens x top, or None for ones.  Pairs without a row
+    add nothing."""
+    m, entry = _i8("combine_experts")
+    return m.combine_experts(entry, Y, position, weights, X, beta, stream)
+
+
+def combine_experts_grad(dX, Y, position, weights, dY, dweights, stream=None):
+    """The gradients of combine_experts: dY[position[t, j]] = weights[t, j] * dX[t] and
+    dweights[t, j] = <dX[t], Y[position[t, j]]> (0 without a row).  Returns (dY,
+    dweights)."""
+    m, entry = _i8("combine_experts_grad")
+    return m.combine_experts_grad(entry, dX, Y, position, weights, dY, dweights, stream)
+
+
+# Kernels for tune_f8_next (see dgemm_tune_f8_next in include/dgemm.h)
+TUNE_F8_ANY, TUNE_F8_PAIR, TUNE_F8_CHANNELS = 1, 2, 3
+
+
+def tune_f8_next(variant: int, bn: int = 0, split: int = 1) -> None:
+    """Tuning hook: fix the kernel of the next gemm_f8_tn or gemm_f8_tn_experts call on
+    this thread (variant TUNE_F8_* or TUNE_AUTO, tile width bn, CTAs sharing a tile)."""
+    st = lib().dgemm_tune_f8_next(int(variant), int(bn), int(split))
+    if st != OK:
+        raise DgemmError(st, "dgemm_tune_f8_next")

@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include "dgemm.h"
+#include "f8.cuh"
 #include "i8_gemm.h"
 #include "internal.h"
 
@@ -71,7 +72,8 @@ int checks_failed(int clear, int *site)
 {
     int (*const readers[])(int, int *) = {check_status_simt, check_status_tma, check_status_umma,
                                           check_status_scale, check_status_repack, check_status_i8_rows,
-                                          check_status_i8_gemm, check_status_i8_umma, check_status_i8_decode};
+                                          check_status_i8_gemm, check_status_i8_umma, check_status_i8_decode,
+                                          check_status_f8_rows, check_status_f8_gemm, check_status_experts};
     int status = DGEMM_OK, where = 0;
     for (auto rd : readers) {
         int s = 0;
@@ -374,6 +376,179 @@ extern "C" int dequantize_i8(int64_t rows, int64_t cols, const int8_t *Q, int64_
     return finish(launch_dequantize_i8(rows, cols, Q, ldq, scale, X, ldx, type, stream, dev));
 }
 
+namespace {
+
+// A matrix in 8-bit floating point, read or written.
+bool f8_ok(const dgemm_f8 *q, int64_t rows, int64_t cols, bool written)
+{
+    if (!q || q->ld < cols || (q->type != DGEMM_F8_E4M3 && q->type != DGEMM_F8_E5M2) || (q->block != 1 && q->block != kF8Block) ||
+        q->scale_row < 0 || q->scale_blk < 0)
+        return false;
+    if (rows == 0 || cols == 0) return true;
+    return !written || ((q->scale_row > 0 || rows <= q->block) && (q->scale_blk > 0 || cols <= kF8Block));
+}
+
+bool f8_given(const dgemm_f8 *q)
+{
+    return q->data && q->scale;
+}
+
+// Sizes of the calls on tokens by expert.
+bool moves_ok(int64_t tokens, int64_t top, int64_t cols, int64_t rows, int type)
+{
+    return tokens >= 0 && top >= 0 && cols >= 0 && rows >= 0 && tokens <= INT32_MAX && cols <= INT32_MAX && rows <= INT32_MAX &&
+           (tokens == 0 || top <= INT32_MAX / tokens) && known_type(type);
+}
+
+}  // namespace
+
+extern "C" int quantize_f8(int64_t rows, int64_t cols, const void *X, int64_t ldx, int type, int transposed,
+                           const dgemm_f8 *Q, cudaStream_t stream)
+{
+    bool empty;
+    if (!rows_ok(rows, cols, type, &empty) || cols > INT32_MAX || ldx < cols ||
+        !f8_ok(Q, transposed ? cols : rows, transposed ? rows : cols, true) || (transposed && Q->block != 1))
+        return DGEMM_ERR_INVALID_ARG;
+    if (empty) return DGEMM_OK;
+    if (!X || !f8_given(Q)) return DGEMM_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int st = check_device(dev); st != DGEMM_OK) return st;
+    return finish(launch_quantize_f8(rows, cols, X, ldx, type, transposed != 0, *Q, stream));
+}
+
+extern "C" int swiglu_f8(int64_t rows, int64_t cols, const void *G, int64_t ldg, const void *U, int64_t ldu, int type,
+                         const dgemm_f8 *Q, cudaStream_t stream)
+{
+    bool empty;
+    if (!rows_ok(rows, cols, type, &empty) || cols > INT32_MAX || ldg < cols || ldu < cols || !f8_ok(Q, rows, cols, true) ||
+        Q->block != 1)
+        return DGEMM_ERR_INVALID_ARG;
+    if (empty) return DGEMM_OK;
+    if (!G || !U || !f8_given(Q)) return DGEMM_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int st = check_device(dev); st != DGEMM_OK) return st;
+    return finish(launch_swiglu_f8(rows, cols, G, ldg, U, ldu, type, *Q, stream));
+}
+
+extern "C" int dequantize_f8(int64_t rows, int64_t cols, const dgemm_f8 *Q, void *X, int64_t ldx, int type, cudaStream_t stream)
+{
+    bool empty;
+    if (!rows_ok(rows, cols, type, &empty) || cols > INT32_MAX || ldx < cols || !f8_ok(Q, rows, cols, false))
+        return DGEMM_ERR_INVALID_ARG;
+    if (empty) return DGEMM_OK;
+    if (!X || !f8_given(Q)) return DGEMM_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int st = check_device(dev); st != DGEMM_OK) return st;
+    return finish(launch_dequantize_f8(rows, cols, *Q, X, ldx, type, stream));
+}
+
+namespace {
+
+// What the two products check alike; *done: there is nothing to compute.
+int validate_f8(int64_t M, int64_t N, int64_t K, const dgemm_f8 *A, const dgemm_f8 *B, const void *C, int64_t ldc, int c_type,
+                int64_t more_tiles, bool *done)
+{
+    *done = true;
+    if (M < 0 || N < 0 || K < 0 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX || ldc < N || !known_type(c_type) ||
+        !f8_ok(A, M, K, false) || !f8_ok(B, N, K, false))
+        return DGEMM_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return DGEMM_OK;
+    if (!C || (K > 0 && (!f8_given(A) || !f8_given(B)))) return DGEMM_ERR_INVALID_ARG;
+    if ((M - 1) / 16 + 1 + more_tiles > INT32_MAX / ((N - 1) / 64 + 1)) return DGEMM_ERR_INVALID_ARG;
+    *done = false;
+    return DGEMM_OK;
+}
+
+}  // namespace
+
+extern "C" int gemm_f8_tn(int64_t M, int64_t N, int64_t K, const dgemm_f8 *A, const dgemm_f8 *B, const float *bias, float beta,
+                          void *C, int64_t ldc, int c_type, cudaStream_t stream)
+{
+    const F8Config tune = f8_take_tune();  // (before any return: it is for this call only)
+    bool done;
+    int st = validate_f8(M, N, K, A, B, C, ldc, c_type, 0, &done);
+    if (st != DGEMM_OK || done) return st;
+    DeviceInfo dev;
+    if ((st = check_device(dev)) != DGEMM_OK) return st;
+    const F8Params p{M, N, K, f8_operand(*A), f8_operand(*B), 1, nullptr, 0, 0, bias, beta, C, ldc, c_type};
+    return finish(launch_gemm_f8(p, tune, stream, dev));
+}
+
+extern "C" int gemm_f8_tn_experts(int64_t M, int64_t N, int64_t K, int experts, const int32_t *offsets, const dgemm_f8 *A,
+                                  const dgemm_f8 *B, int64_t b_stride, int64_t scale_stride, void *C, int64_t ldc, int c_type,
+                                  cudaStream_t stream)
+{
+    const F8Config tune = f8_take_tune();
+    bool done;
+    if (experts < 1 || experts > kMaxExperts || b_stride < 0 || scale_stride < 0) return DGEMM_ERR_INVALID_ARG;
+    int st = validate_f8(M, N, K, A, B, C, ldc, c_type, experts, &done);
+    if (st == DGEMM_OK && A->block != 1) st = DGEMM_ERR_INVALID_ARG;
+    if (st != DGEMM_OK || done) return st;
+    if (!offsets) return DGEMM_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if ((st = check_device(dev)) != DGEMM_OK) return st;
+    const F8Params p{M, N, K, f8_operand(*A), f8_operand(*B), experts, offsets, b_stride, scale_stride, nullptr, 0.f, C, ldc, c_type};
+    return finish(launch_gemm_f8(p, tune, stream, dev));
+}
+
+extern "C" int sort_by_expert(int64_t tokens, int64_t top, int experts, const void *ids, int id_bytes, int32_t *offsets,
+                              int32_t *position, cudaStream_t stream)
+{
+    if (!moves_ok(tokens, top, 0, 0, DGEMM_TYPE_F32) || experts < 1 || experts > kMaxExperts || (id_bytes != 4 && id_bytes != 8) ||
+        !offsets || (tokens * top > 0 && (!ids || !position)))
+        return DGEMM_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int st = check_device(dev); st != DGEMM_OK) return st;
+    return finish(launch_sort_by_expert(tokens * top, experts, ids, id_bytes, offsets, position, stream));
+}
+
+extern "C" int gather_by_expert(int64_t tokens, int64_t top, int64_t cols, const void *X, int64_t ldx, int type,
+                                const int32_t *position, int64_t rows, void *Y, int64_t ldy, cudaStream_t stream)
+{
+    if (!moves_ok(tokens, top, cols, rows, type) || ldx < cols || ldy < cols) return DGEMM_ERR_INVALID_ARG;
+    if (tokens == 0 || top == 0 || cols == 0 || rows == 0) return DGEMM_OK;
+    if (!X || !position || !Y) return DGEMM_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int st = check_device(dev); st != DGEMM_OK) return st;
+    return finish(launch_gather(tokens, top, cols, X, ldx, type, position, rows, Y, ldy, stream));
+}
+
+extern "C" int gather_by_expert_f8(int64_t tokens, int64_t top, int64_t cols, const void *X, int64_t ldx, int type,
+                                   const int32_t *position, int64_t rows, const dgemm_f8 *Q, cudaStream_t stream)
+{
+    if (!moves_ok(tokens, top, cols, rows, type) || ldx < cols || !f8_ok(Q, rows, cols, true) || Q->block != 1)
+        return DGEMM_ERR_INVALID_ARG;
+    if (tokens == 0 || top == 0 || cols == 0 || rows == 0) return DGEMM_OK;
+    if (!X || !position || !f8_given(Q)) return DGEMM_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int st = check_device(dev); st != DGEMM_OK) return st;
+    return finish(launch_gather_f8(tokens, top, cols, X, ldx, type, position, rows, *Q, stream));
+}
+
+extern "C" int combine_experts(int64_t tokens, int64_t top, int64_t cols, const void *Y, int64_t ldy, int64_t rows, int type,
+                               const int32_t *position, const float *weights, float beta, void *X, int64_t ldx, cudaStream_t stream)
+{
+    if (!moves_ok(tokens, top, cols, rows, type) || ldx < cols || ldy < cols) return DGEMM_ERR_INVALID_ARG;
+    if (tokens == 0 || cols == 0) return DGEMM_OK;
+    if (!X || (top > 0 && !position) || (top > 0 && rows > 0 && !Y)) return DGEMM_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int st = check_device(dev); st != DGEMM_OK) return st;
+    return finish(launch_combine(tokens, top, cols, Y, ldy, rows, type, position, weights, beta, X, ldx, stream));
+}
+
+extern "C" int combine_experts_grad(int64_t tokens, int64_t top, int64_t cols, const void *dX, int64_t lddx, const void *Y,
+                                    int64_t ldy, int64_t rows, int type, const int32_t *position, const float *weights, void *dY,
+                                    int64_t lddy, float *dweights, cudaStream_t stream)
+{
+    if (!moves_ok(tokens, top, cols, rows, type) || lddx < cols || ldy < cols || lddy < cols || (dY == Y && dY && lddy != ldy))
+        return DGEMM_ERR_INVALID_ARG;
+    if (tokens == 0 || top == 0) return DGEMM_OK;
+    if (!position || !weights || !dweights || (cols > 0 && (!dX || (rows > 0 && (!Y || !dY))))) return DGEMM_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int st = check_device(dev); st != DGEMM_OK) return st;
+    return finish(launch_combine_grad(tokens, top, cols, dX, lddx, Y, ldy, rows, type, position, weights, dY, lddy, dweights, stream));
+}
+
 extern "C" const char *dgemm_status_string(int status)
 {
     switch (status) {
@@ -434,6 +609,11 @@ extern "C" int dgemm_tune_next(int variant, int bn, int split)
 extern "C" int dgemm_tune_i8_next(int variant, int bn, int split)
 {
     return i8_tune_next(variant, bn, split);
+}
+
+extern "C" int dgemm_tune_f8_next(int variant, int bn, int split)
+{
+    return f8_tune_next(variant, bn, split);
 }
 
 extern "C" int64_t dgemm_test_pair_units(int64_t tiles, int64_t pairs, int64_t num_kb, int64_t sk_tiles,

@@ -1,0 +1,198 @@
+// f8_gemm.cu -- gemm_f8_tn and gemm_f8_tn_experts: the choice of a kernel, and the
+// kernel for operands of any alignment.
+//
+//   C[m, n] = sum_b sa(m, b) sb(n, b) sum_(k in b) A[m, k] B[n, k] + bias[n] + beta C[m, n]
+//
+// f8_any_kernel: tiles of 64 tokens x 64 channels.  A block of 128 K values of both
+// operands is widened to FP16 (exact for either 8-bit type) into shared memory,
+// multiplied by mma.sync with FP32 accumulators, and the block's sums are scaled and
+// added to FP32 sums in registers.  It takes what TMA cannot: rows off 16-byte
+// boundaries, whose bytes it loads one by one, and is bound by those loads.
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "chained.cuh"
+#include "dgemm.h"
+#include "f8.cuh"
+#include "internal.h"
+
+#define DGEMM_UNIT 11
+#include "checked.cuh"
+#include "f8_tiles.cuh"
+#include "rows.cuh"
+
+namespace dgemm {
+namespace {
+
+constexpr int kTile = 64;
+constexpr int kPitch = kF8Block + 8;  // halves: rows 4 banks apart
+constexpr int kThreads = 128;
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2])
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+// 64 rows x 128 K values of an operand from `row` (rows up to row_end) and k0, as
+// FP16; zeros outside.
+__device__ __forceinline__ void load_tile(__half *s, const F8Operand &o, const uint8_t *base, int64_t row, int64_t row_end,
+                                          int64_t k0, int64_t K)
+{
+    for (int i = threadIdx.x; i < kTile * kF8Block / 4; i += kThreads) {
+        const int r = i / (kF8Block / 4), c = i % (kF8Block / 4) * 4;
+        uint32_t w = 0;
+        if (row + r < row_end) {
+            const uint8_t *src = base + (row + r) * o.ld + k0 + c;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k0 + c + k < K) w |= static_cast<uint32_t>(src[k]) << (8 * k);
+        }
+        uint32_t *dst = reinterpret_cast<uint32_t *>(s + r * kPitch + c);
+        if (!DGEMM_CHECK(r < kTile && c + 4 <= kF8Block)) continue;
+        if (o.type == DGEMM_F8_E5M2) {
+            dst[0] = f8x2_to_f16x2<true>(w & 0xFFFFu);
+            dst[1] = f8x2_to_f16x2<true>(w >> 16);
+        } else {
+            dst[0] = f8x2_to_f16x2<false>(w & 0xFFFFu);
+            dst[1] = f8x2_to_f16x2<false>(w >> 16);
+        }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) f8_any_kernel(const F8Params p, uint32_t tiles_n)
+{
+    __shared__ __align__(16) __half s_a[kTile * kPitch], s_b[kTile * kPitch];
+    extern __shared__ uint32_t s_table[];
+    const F8Table table{s_table, reinterpret_cast<int32_t *>(s_table + p.experts + 1)};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    chain_wait();
+    chain_next();
+    if (warp == 0) fill_table(p, kTile, table, lane);
+    __syncthreads();
+    const uint32_t tiles = table.first[p.experts] * tiles_n;
+    const int wr = (warp >> 1) * 32, wc = (warp & 1) * 32;
+    for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const F8Tile tile = find_tile(table, p.experts, tiles_n, kTile, kTile, t);
+        const uint8_t *B = p.b.p + tile.expert * p.b_stride;
+        const float *sb = p.b.scale + tile.expert * p.sb_stride;
+        float acc[2][4][4] = {};
+        for (int64_t k0 = 0; k0 < p.K; k0 += kF8Block) {
+            __syncthreads();  // the last block has been read
+            load_tile(s_a, p.a, p.a.p, tile.t0, tile.t_end, k0, p.K);
+            load_tile(s_b, p.b, B, tile.n0, p.N, k0, p.K);
+            __syncthreads();
+            float part[2][4][4] = {};
+#pragma unroll
+            for (int k = 0; k < kF8Block; k += 16) {
+                uint32_t a[2][4], b[4][2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const __half *src = s_a + (wr + i * 16 + g) * kPitch + k + 2 * q;
+                    a[i][0] = *reinterpret_cast<const uint32_t *>(src);
+                    a[i][1] = *reinterpret_cast<const uint32_t *>(src + 8 * kPitch);
+                    a[i][2] = *reinterpret_cast<const uint32_t *>(src + 8);
+                    a[i][3] = *reinterpret_cast<const uint32_t *>(src + 8 * kPitch + 8);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const __half *src = s_b + (wc + j * 8 + g) * kPitch + k + 2 * q;
+                    b[j][0] = *reinterpret_cast<const uint32_t *>(src);
+                    b[j][1] = *reinterpret_cast<const uint32_t *>(src + 8);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mma16816(part[i][j], a[i], b[j]);
+            }
+            const int64_t kb = k0 / kF8Block;
+            float ra[2][2], cb[4][2];  // scales of this thread's rows and columns (clamped to ones that exist)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t m = min(static_cast<int64_t>(tile.t0 + wr + i * 16 + h * 8 + g), static_cast<int64_t>(tile.t_end - 1));
+                    ra[i][h] = p.a.scale[m / p.a.block * p.a.s_row + kb * p.a.s_blk];
+                }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t n = min(tile.n0 + wc + j * 8 + 2 * q + h, p.N - 1);
+                    cb[j][h] = sb[n / p.b.block * p.b.s_row + kb * p.b.s_blk];
+                }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        acc[i][j][v] = fmaf(part[i][j][v] * cb[j][v & 1], ra[i][v >> 1], acc[i][j][v]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int64_t m = tile.t0 + wr + i * 16 + (v >> 1) * 8 + g, n = tile.n0 + wc + j * 8 + 2 * q + (v & 1);
+                    if (m >= tile.t_end || n >= p.N || !DGEMM_CHECK(m < p.M)) continue;
+                    T *dst = static_cast<T *>(p.C) + m * p.ldc + n;
+                    float x = acc[i][j][v];
+                    if (p.bias) x += p.bias[n];
+                    if (p.beta != 0.f) x = fmaf(p.beta, to_f32(*dst), x);
+                    *dst = from_f32<T>(x);
+                }
+    }
+}
+
+thread_local F8Config t_tune = {kF8Auto, 0, 1};
+
+const char *launch_any(const F8Params &p, cudaStream_t stream, const DeviceInfo &dev)
+{
+    const int64_t tiles_n = (p.N - 1) / kTile + 1, bound = token_tiles_bound(p, kTile);
+    const int64_t tiles = tiles_n * bound;
+    if (tiles > INT32_MAX) return nullptr;
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, static_cast<int64_t>(dev.sm_count) * 8));
+    auto kernel = p.c_type == DGEMM_TYPE_F32 ? f8_any_kernel<float>
+                  : p.c_type == DGEMM_TYPE_F16 ? f8_any_kernel<__half>
+                                               : f8_any_kernel<__nv_bfloat16>;
+    const size_t smem = static_cast<size_t>(p.experts + 1) * 8;
+    if (launch_chained(kernel, grid, kThreads, smem, stream, 1, p, static_cast<uint32_t>(tiles_n)) != cudaSuccess) return nullptr;
+    return "f8_any_64x64";
+}
+
+}  // namespace
+
+int f8_tune_next(int variant, int bn, int split)
+{
+    const F8Config cfg{variant, bn, split};
+    if (variant != kF8Auto && variant != kF8Any && !f8_umma_config_ok(cfg)) return DGEMM_ERR_INVALID_ARG;
+    t_tune = cfg;
+    return DGEMM_OK;
+}
+
+F8Config f8_take_tune()
+{
+    const F8Config cfg = t_tune;
+    t_tune = {kF8Auto, 0, 1};
+    return cfg;
+}
+
+const char *launch_gemm_f8(const F8Params &p, const F8Config &tune, cudaStream_t stream, const DeviceInfo &dev)
+{
+    (void)tune;
+    return launch_any(p, stream, dev);
+}
+
+}  // namespace dgemm
+
+DGEMM_DEFINE_CHECK_READER(check_status_f8_gemm)

@@ -7,6 +7,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "dgemm.h"
+
 namespace dgemm {
 
 inline bool aligned16(const void *p)
@@ -75,6 +77,9 @@ int check_status_i8_rows(int clear, int *site);
 int check_status_i8_gemm(int clear, int *site);
 int check_status_i8_umma(int clear, int *site);
 int check_status_i8_decode(int clear, int *site);
+int check_status_f8_rows(int clear, int *site);
+int check_status_f8_gemm(int clear, int *site);
+int check_status_experts(int clear, int *site);
 
 // Rows taken off M for the C-store checks of the next TMA-fed SIMT launch
 // on this host thread (dgemm_test_shrink_bounds); taking it clears it.
@@ -122,6 +127,30 @@ const char *launch_gemm_i8(const I8Params &p, int c_type, const I8Config &tune, 
 // taking (by every gemm_i8_tn call, whatever becomes of it).
 int i8_tune_next(int variant, int bn, int split);
 I8Config i8_take_tune();
+
+// 8-bit floating point: the rows (f8_rows.cu) and the product (f8_gemm.cu).
+const char *launch_quantize_f8(int64_t rows, int64_t cols, const void *x, int64_t ldx, int type, bool transposed,
+                               const dgemm_f8 &q, cudaStream_t stream);
+const char *launch_swiglu_f8(int64_t rows, int64_t cols, const void *g, int64_t ldg, const void *u, int64_t ldu, int type,
+                             const dgemm_f8 &q, cudaStream_t stream);
+const char *launch_gather_f8(int64_t tokens, int64_t top, int64_t cols, const void *x, int64_t ldx, int type,
+                             const int32_t *position, int64_t rows, const dgemm_f8 &q, cudaStream_t stream);
+const char *launch_dequantize_f8(int64_t rows, int64_t cols, const dgemm_f8 &q, void *x, int64_t ldx, int type,
+                                 cudaStream_t stream);
+struct F8Params;
+struct F8Config;
+const char *launch_gemm_f8(const F8Params &p, const F8Config &tune, cudaStream_t stream, const DeviceInfo &dev);
+
+// Tokens by expert (experts.cu); types are dgemm_types.
+const char *launch_sort_by_expert(int64_t pairs, int experts, const void *ids, int id_bytes, int32_t *offsets,
+                                  int32_t *position, cudaStream_t stream);
+const char *launch_gather(int64_t tokens, int64_t top, int64_t cols, const void *x, int64_t ldx, int type,
+                          const int32_t *position, int64_t rows, void *y, int64_t ldy, cudaStream_t stream);
+const char *launch_combine(int64_t tokens, int64_t top, int64_t cols, const void *y, int64_t ldy, int64_t rows, int type,
+                           const int32_t *position, const float *weights, float beta, void *x, int64_t ldx, cudaStream_t stream);
+const char *launch_combine_grad(int64_t tokens, int64_t top, int64_t cols, const void *dx, int64_t lddx, const void *y,
+                                int64_t ldy, int64_t rows, int type, const int32_t *position, const float *weights, void *dy,
+                                int64_t lddy, float *dw, cudaStream_t stream);
 
 // Device status word of the 8-bit tensor-core kernels.
 int i8_read_status(int clear);

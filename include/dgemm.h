@@ -353,6 +353,151 @@ int gemm_i8_tn(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, co
                const int8_t *B, int64_t ldb, const float *scale_b, const float *bias, float beta,
                void *C, int64_t ldc, int c_type, cudaStream_t stream);
 
+/*
+ * Linear layers in 8-bit floating point, and tokens by expert
+ * -----------------------------------------------------------
+ * A matrix of rows x cols values is held as 8-bit floating-point numbers Q with
+ * one float scale for each block: 128 columns of one row (block == 1), or of a
+ * band of 128 rows (block == 128; the last blocks may be smaller).  Element
+ * (i, j) stands for scale(i / block, j / 128) * Q[i, j], and scale(r, b) lies at
+ * scale[r * scale_row + b * scale_blk].
+ * The calls that write such matrices form, in FP32, values y, and for each block
+ *
+ *     a = max |y|,   scale = a / 448,   Q = (y * (448 / a))  rounded to 8 bits
+ *
+ * (e5m2: 57344 in the place of 448), with the quotients and the product rounded
+ * to FP32 and Q to nearest, ties to even: Q is these operations' result to the
+ * bit for quantize_f8 and gather_by_expert_f8, whose y are given values.  (Blocks
+ * with a < 2^-100 are multiplied by 2^100 first.)  A block of zeros gets
+ * scale 0 and zeros.  A block with a NaN or an infinity in it gets scale NaN and
+ * zeros, so everything that is made from it is NaN.
+ * Conventions, beyond those at the top: row-major, leading dimensions in
+ *   elements, at least the row length; sizes of 0 return DGEMM_OK and write
+ *   nothing; DGEMM_ERR_INVALID_ARG for negative sizes, more than 2^31 - 1 rows or
+ *   columns, leading dimensions below the row length, negative scale strides
+ *   (where the scales are written: also 0, if there are several along it), an unknown type or block, or a
+ *   NULL pointer that is not said to be optional.  Pointers are aligned to their
+ *   element type; rows on 16-byte boundaries take the fastest kernels.  Writes
+ *   stay within the rows.  Outputs must not overlap inputs, except where a call allows it.
+ * Source: none on the pages (their products take 16- and 32-bit operands).
+ */
+typedef enum {
+    DGEMM_F8_E4M3 = 0, /* largest value 448, no infinities */
+    DGEMM_F8_E5M2 = 1  /* largest value 57344 */
+} dgemm_f8_type;
+
+typedef struct {
+    void *data;        /* device, one byte an element */
+    int64_t ld;        /* elements from one row to the next */
+    int type;          /* a dgemm_f8_type */
+    int block;         /* rows that share a scale: 1 or 128 */
+    float *scale;      /* device */
+    int64_t scale_row; /* floats from one row (band) of scales to the next */
+    int64_t scale_blk; /* floats from one block of 128 columns to the next */
+} dgemm_f8;
+
+/*
+ * quantize_f8 -- y = X (rows x cols of `type`, a dgemm_type), written to Q of the
+ * same shape; with transposed != 0, y = X^T and Q is cols x rows (Q->block 1:
+ * a scale for each 128 rows of X down a column, which is the form that the
+ * product over those rows takes).
+ */
+int quantize_f8(int64_t rows, int64_t cols, const void *X, int64_t ldx, int type, int transposed,
+                const dgemm_f8 *Q, cudaStream_t stream);
+
+/*
+ * swiglu_f8 -- y = G / (1 + exp(-G)) * U, elementwise; Q->block 1.  G and U may be
+ * column ranges of one wider matrix.  (y carries a few FP32 roundings, so a value that
+ * close to a tie may take either step.)
+ */
+int swiglu_f8(int64_t rows, int64_t cols, const void *G, int64_t ldg, const void *U, int64_t ldu, int type,
+              const dgemm_f8 *Q, cudaStream_t stream);
+
+/* dequantize_f8 -- X = scale * Q, formed in FP32 and rounded once to `type`. */
+int dequantize_f8(int64_t rows, int64_t cols, const dgemm_f8 *Q, void *X, int64_t ldx, int type,
+                  cudaStream_t stream);
+
+/*
+ * gemm_f8_tn -- product of two such matrices, A (M x K) and B (stored N x K):
+ *     C[m, n] = sum_b scale_a(m, b) scale_b(n, b) sum_(k in block b) A[m, k] B[n, k]
+ *               + bias[n] + beta * C[m, n]
+ *   bias : N floats, or NULL for none.   beta: the old C is not read when it is 0.
+ *   C    : M x N of c_type (a dgemm_type), ldc >= N.
+ * Either operand may have either block and either 8-bit type, so with W held in
+ * 128 x 128 blocks the products of a linear layer's training are: X W^T as it
+ * stands, dY W on W's transposed data and scales, and dY^T X on quantize_f8's
+ * transposed form of both (block 1, beta = 1 to add to a gradient).
+ * Sums within a block of 128 are formed by the tensor cores from exact products,
+ * in FP32 arithmetic that truncates; sums over blocks in FP32.  One row of A
+ * gives the same bits in any batch that takes the same kernel (dgemm_last_kernel).
+ * K == 0 gives bias + beta * C.  DGEMM_ERR_INVALID_ARG as above, and for more
+ * than 2^31 - 1 tiles of 16 x 64 of C.
+ */
+int gemm_f8_tn(int64_t M, int64_t N, int64_t K, const dgemm_f8 *A, const dgemm_f8 *B, const float *bias,
+               float beta, void *C, int64_t ldc, int c_type, cudaStream_t stream);
+
+/*
+ * gemm_f8_tn_experts -- the product of each expert's rows with its own weights:
+ *     C[m, :] = A[m, :] * B_e^T   for offsets[e] <= m < offsets[e + 1]
+ *   experts : number of weight matrices, 1 .. 1024.
+ *   offsets : device, experts + 1 integers, ascending, from 0 to at most M; read when the
+ *             call runs on the stream.  Values out of order are raised to the one before
+ *             them and values past M lowered to M, so that nothing outside the operands is touched.
+ *   A       : M x K rows sorted by expert, block 1.
+ *   B       : the first expert's weights (N x K); the others' data b_stride
+ *             elements and scales scale_stride floats further on each.
+ * Rows of C from offsets[experts] on (and before offsets[0]) are left as they were.
+ */
+int gemm_f8_tn_experts(int64_t M, int64_t N, int64_t K, int experts, const int32_t *offsets, const dgemm_f8 *A,
+                       const dgemm_f8 *B, int64_t b_stride, int64_t scale_stride, void *C, int64_t ldc, int c_type,
+                       cudaStream_t stream);
+
+/*
+ * sort_by_expert -- where each pair (token, choice) goes when the pairs are sorted by
+ * expert: position[t * top + j] is the row of pair (t, j), pairs of one expert in
+ * the order of t * top + j; offsets[e] is the first row of expert e, offsets[experts]
+ * the number of rows.  A pair whose expert is not in 0 .. experts - 1 (padding) has
+ * no row: position -1.
+ *   ids   : device, tokens * top expert numbers, of id_bytes (4 or 8) bytes each.
+ *   experts: 1 .. 1024.   tokens * top < 2^31.
+ */
+int sort_by_expert(int64_t tokens, int64_t top, int experts, const void *ids, int id_bytes, int32_t *offsets,
+                   int32_t *position, cudaStream_t stream);
+
+/*
+ * gather_by_expert -- Y[position[t, j]] = X[t] (rows of `type`).  X: tokens x cols; Y:
+ * `rows` x cols.  Positions outside 0 .. rows - 1 are skipped; rows that no
+ * position names are left as they were.  Positions within 0 .. rows - 1 must differ.
+ * gather_by_expert_f8 -- the same with quantize_f8's form of X in Q (rows x cols, block 1).
+ * Their gradient is combine_experts of Y's, without weights.
+ */
+int gather_by_expert(int64_t tokens, int64_t top, int64_t cols, const void *X, int64_t ldx, int type,
+                     const int32_t *position, int64_t rows, void *Y, int64_t ldy, cudaStream_t stream);
+int gather_by_expert_f8(int64_t tokens, int64_t top, int64_t cols, const void *X, int64_t ldx, int type,
+                        const int32_t *position, int64_t rows, const dgemm_f8 *Q, cudaStream_t stream);
+
+/*
+ * combine_experts -- X[t] = sum_j weights[t, j] * Y[position[t, j]] + beta * X[t], added
+ * up in FP32 in the order of j and rounded once to `type`.
+ *   weights : device, tokens * top floats; NULL for ones.
+ *   beta    : the old X is not read when it is 0.
+ * Positions outside 0 .. rows - 1 add nothing, whatever their weight.
+ */
+int combine_experts(int64_t tokens, int64_t top, int64_t cols, const void *Y, int64_t ldy, int64_t rows, int type,
+                    const int32_t *position, const float *weights, float beta, void *X, int64_t ldx,
+                    cudaStream_t stream);
+
+/*
+ * combine_experts_grad -- combine_experts' gradients, from dX:
+ *     dY[position[t, j]] = weights[t, j] * dX[t],   dweights[t, j] = sum_c dX[t, c] Y[position[t, j], c]
+ * Sums in FP32, in an order that depends on the sizes alone.  Positions outside 0 ..
+ * rows - 1: dweights is 0; rows of dY that no position names are left as they were.
+ * dY may be Y's own buffer (with the same leading dimension).
+ */
+int combine_experts_grad(int64_t tokens, int64_t top, int64_t cols, const void *dX, int64_t lddx, const void *Y,
+                         int64_t ldy, int64_t rows, int type, const int32_t *position, const float *weights,
+                         void *dY, int64_t lddy, float *dweights, cudaStream_t stream);
+
 /* A static, NUL-terminated description of a dgemm_status value. */
 const char *dgemm_status_string(int status);
 
@@ -383,7 +528,8 @@ int dgemm_device_status(int clear);
  * clear of the device status: (translation unit x 100000 + source line) of
  * the library's sources, units 1 sgemm_simt.cu, 2 sgemm_tma.cu,
  * 3 umma_gemm.cu, 4 scale_c.cu, 5 repack.cu, 6 i8_rows.cu, 7 i8_gemm.cu,
- * 8 i8_umma.cu, 9 i8_decode.cu; 0 if none failed, and always 0 in libdgemm.so.  Synchronises the device.  Source: none on the pages.
+ * 8 i8_umma.cu, 9 i8_decode.cu, 10 f8_rows.cu, 11 f8_gemm.cu, 12 f8_umma.cu,
+ * 13 experts.cu; 0 if none failed, and always 0 in libdgemm.so.  Synchronises the device.  Source: none on the pages.
  */
 int dgemm_check_site(void);
 
@@ -514,6 +660,18 @@ int dgemm_tune_next(int variant, int bn, int split);
  * since K has no more blocks of 128).  Source: as dgemm_tune_next.
  */
 int dgemm_tune_i8_next(int variant, int bn, int split);
+
+/*
+ * dgemm_tune_f8_next -- TUNING HOOK: as dgemm_tune_i8_next, for the next gemm_f8_tn or
+ * gemm_f8_tn_experts call made by the calling host thread.
+ *   variant 0: automatic (the default);
+ *           1: the mma.sync kernel for operands of any alignment;
+ *           2: CTA pair, 256 tokens x bn channels (bn 128 or 256);
+ *           3: one CTA per 128 channels x bn tokens (bn 16, 32, 64 or 128), `split`
+ *              (1..8; 1 for gemm_f8_tn_experts) CTAs of a cluster sharing it along K.
+ * Source: as dgemm_tune_next.
+ */
+int dgemm_tune_f8_next(int variant, int bn, int split);
 
 /*
  * dgemm_last_kernel -- name of the kernel variant the last successful call
