@@ -73,7 +73,7 @@ int checks_failed(int clear, int *site)
     int (*const readers[])(int, int *) = {check_status_simt, check_status_tma, check_status_umma,
                                           check_status_scale, check_status_repack, check_status_i8_rows,
                                           check_status_i8_gemm, check_status_i8_umma, check_status_i8_decode,
-                                          check_status_f8_rows, check_status_f8_gemm, check_status_experts};
+                                          check_status_f8_rows, check_status_f8_gemm, check_status_f8_umma, check_status_experts};
     int status = DGEMM_OK, where = 0;
     for (auto rd : readers) {
         int s = 0;
@@ -571,9 +571,11 @@ extern "C" int dgemm_device_status(int clear)
     const int a = umma_read_status(clear);
     const int b = simt_read_status(clear);
     const int c = i8_read_status(clear);
+    const int d = f8_read_status(clear);
     if (a != DGEMM_OK) return a;
     if (b != DGEMM_OK) return b;
     if (c != DGEMM_OK) return c;
+    if (d != DGEMM_OK) return d;
     return checks_failed(clear, nullptr);
 }
 

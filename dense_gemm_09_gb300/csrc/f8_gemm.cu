@@ -170,6 +170,30 @@ const char *launch_any(const F8Params &p, cudaStream_t stream, const DeviceInfo 
     return "f8_any_64x64";
 }
 
+// Rows of tokens a tile would have on average, and the kernel for them.
+F8Config choose(const F8Params &p, const DeviceInfo &dev)
+{
+    const int64_t tokens = p.offsets ? (p.M + p.experts - 1) / p.experts : p.M;
+    if (tokens > 128) return {kF8Pair, 256, 1};
+    const int bn = tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : 128;
+    int split = 1;
+    if (!p.offsets)
+        while (split < 8 && (p.N + 127) / 128 * split * 2 <= dev.sm_count) split *= 2;
+    return {kF8Channels, bn, split};
+}
+
+const char *kernel_name(const F8Config &cfg)
+{
+    if (cfg.variant == kF8Pair) return cfg.bn == 256 ? "f8_pair_256x256" : "f8_pair_256x128";
+    static const char *const names[4][4] = {
+        {"f8_channels_128x16", "f8_channels_128x16_split2", "f8_channels_128x16_split4", "f8_channels_128x16_split8"},
+        {"f8_channels_128x32", "f8_channels_128x32_split2", "f8_channels_128x32_split4", "f8_channels_128x32_split8"},
+        {"f8_channels_128x64", "f8_channels_128x64_split2", "f8_channels_128x64_split4", "f8_channels_128x64_split8"},
+        {"f8_channels_128x128", "f8_channels_128x128_split2", "f8_channels_128x128_split4", "f8_channels_128x128_split8"}};
+    return names[cfg.bn == 16 ? 0 : cfg.bn == 32 ? 1 : cfg.bn == 64 ? 2 : 3]
+                [cfg.split == 1 ? 0 : cfg.split <= 2 ? 1 : cfg.split <= 4 ? 2 : 3];
+}
+
 }  // namespace
 
 int f8_tune_next(int variant, int bn, int split)
@@ -189,7 +213,17 @@ F8Config f8_take_tune()
 
 const char *launch_gemm_f8(const F8Params &p, const F8Config &tune, cudaStream_t stream, const DeviceInfo &dev)
 {
-    (void)tune;
+    // TMA's conditions, but for C's
+    const bool tma = p.K > 0 && aligned(p.a.p, p.a.ld, 1, 16) && aligned(p.b.p, p.b.ld, 1, 16) &&
+                     (p.experts == 1 || (p.b_stride % 16 == 0 && p.b_stride > 0));
+    if (tma && tune.variant != kF8Any) {
+        F8Config cfg = tune;
+        if (cfg.variant == kF8Auto || !launch_f8_umma(p, cfg, stream)) {
+            cfg = choose(p, dev);
+            if (!launch_f8_umma(p, cfg, stream)) return launch_any(p, stream, dev);
+        }
+        return kernel_name(cfg);
+    }
     return launch_any(p, stream, dev);
 }
 

@@ -1,5 +1,907 @@
+// f8_umma.cu -- gemm_f8_tn and gemm_f8_tn_experts on the tensor cores (tcgen05).
+//
+//   C[m, n] = sum_b sa(m, b) sb(n, b) sum_(k in b) A[m, k] B[n, k] + bias[n] + beta C[m, n]
+//
+// The mathematics.  A block b is 128 K values, one 128-byte swizzled row of either
+// operand: four MMAs of kind::f8f6f4 (K = 32) sum it into an accumulator in tensor
+// memory, from zero.  The scales are any FP32 numbers, so they cannot join the MMA;
+// the accumulator is read back block by block, multiplied by its row's and column's
+// scales and added to sums in registers, in FP32, while the MMAs fill the next one.
+//
+// What bounds it.  For many tokens the tensor pipe: a block of a 256 x 256 tile takes a
+// CTA pair 512 clocks of MMA (8192 products a clock and SM), and each CTA 256 clocks of
+// tensor-memory reads and 128 to 256 of packed FMAs beside them.  For few tokens the
+// weights' bytes: there the channels are the MMA's rows and the tokens its columns
+// (kSwap), so that no row of the tensor cores' work is padding that is loaded.
+//
+// Roles (12 warps):
+//   warp 0      TMA producer: 128 bytes of K of both operands a stage;
+//   warp 1      MMA issuer (in a pair's other CTA it tells the leader which of its own
+//               stages have landed);
+//   warp 2      the blocks' scales, by 4-byte asynchronous copies into a ring;
+//   warp 3      the table of tiles, at the start;
+//   warps 4-11  two groups of four: group g has columns g bn / 2 .. of the tile, warp w
+//               of it the accumulator's rows 32 w ..: sums in registers, then C.
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+#include <mutex>
+#include <type_traits>
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "bounded_wait.cuh"
+#include "chained.cuh"
+#include "dgemm.h"
 #include "f8.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+#include "umma_warp.cuh"
+
+#define DGEMM_UNIT 12
+#include "checked.cuh"
+#include "f8_tiles.cuh"
+#include "rows.cuh"
+
 namespace dgemm {
-bool f8_umma_config_ok(const F8Config &) { return false; }
-bool launch_f8_umma(const F8Params &, const F8Config &, cudaStream_t) { return false; }
+namespace {
+
+constexpr int kRows = 128;                     // accumulator rows of a CTA: TMEM lanes
+constexpr int kRowBytes = kF8Block;            // a block of K, one byte a value
+constexpr int kRowsBytes = kRows * kRowBytes;
+constexpr int kMaxStages = 12;
+constexpr int kMaxAccs = 8;
+constexpr int kScaleSlots = 4;
+constexpr int kBoxBytes = 4096;                // epilogue staging: 32 rows x 128 bytes
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (4 + kEpiWarps);
+constexpr int kSmemLimit = 227 * 1024;
+
+struct Ctrl {
+    uint64_t full[kMaxStages];       // a stage of this CTA has landed
+    uint64_t peer_full[kMaxStages];  // leader: the other CTA's has
+    uint64_t empty[kMaxStages];      // the MMAs have read it
+    uint64_t acc_full[kMaxAccs];     // the MMAs of a block are done
+    uint64_t acc_empty[kMaxAccs];    // leader: every epilogue warp of the pair has read them
+    uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
+    uint64_t mma_done;
+    uint64_t never;                  // test hook: a barrier nothing arrives at
+    WaitCtl wait;
+    uint32_t tmem_base;
+};
+
+struct Params {
+    F8Params c;
+    uint32_t tiles_n;      // tiles of channels
+    int num_kb;            // blocks of K
+    int stages;
+    int boxes;             // staging boxes of an epilogue warp
+    int splitk;            // CTAs of a cluster that share a tile (kSwap)
+    int tma_store;
+    uint32_t idesc;
+    uint64_t wait_limit_ns;
+    int inject_stall;
+};
+
+// One kernel: kCtas CTAs share an MMA; kSwap: the rows are channels and the columns
+// tokens; kBn columns to a tile; kUniform: the scales of a group's columns are one number
+// (bands of 128 channels).
+template <int kCtas_, bool kSwap_, int kBn_, bool kUniform_>
+struct Shape {
+    static constexpr int kCtas = kCtas_, kBn = kBn_;
+    static constexpr bool kSwap = kSwap_, kUniform = kUniform_;
+    static constexpr int kWgCols = kBn / 2;                     // columns of an epilogue group
+    static constexpr int kTileRows = kRows * kCtas;
+    static constexpr int kTokens = kSwap ? kBn : kTileRows, kChannels = kSwap ? kRows : kBn;  // of a tile
+    static constexpr int kStageBytes = kRowsBytes + kBn / kCtas * kRowBytes;
+    static constexpr int kAccs = 512 / kBn < kMaxAccs ? 512 / kBn : kMaxAccs;
+    static constexpr int kTmemCols = kAccs * kBn;
+    static constexpr int kScaleCols = kUniform ? 4 : kBn;       // floats of a slot beside the rows'
+    static constexpr int kScaleBytes = kScaleSlots * (kRows + kScaleCols) * 4;
+    static constexpr int kPerSm = kBn <= 32 ? 2 : 1;            // CTAs an SM
+    static_assert(kTmemCols >= 32 && (kTmemCols & (kTmemCols - 1)) == 0 && kPerSm * kTmemCols <= 512, "TMEM");
+};
+
+// ---- PTX
+
+template <int kCtas>
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+{
+    if constexpr (kCtas == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
 }
+
+// kChunk columns of this lane's row; the values are there after tmem_wait.
+template <int kChunk>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[kChunk])
+{
+    if constexpr (kChunk == 32)
+        ptx::tmem_ld_32x32b_x32(taddr, r);
+    else if constexpr (kChunk == 16)
+        tmem_ld_32x32b_x16(taddr, r);
+    else
+        tmem_ld_32x32b_x8(taddr, r);
+}
+
+// Wait for the loads of r; its values pass through the assembly, so that no use of them
+// moves before the wait.
+template <int kChunk>
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[kChunk])
+{
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < kChunk; i += 8)
+        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                     "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+
+__device__ __forceinline__ void copy_async4(uint32_t dst, const float *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// warp_wait for the epilogue, in line: a call would have to save the sums, up to 128
+// registers, around itself.
+template <int kCtas>
+__device__ __forceinline__ bool epi_wait(uint32_t bar, uint32_t parity, WaitCtl *wc)
+{
+    if (probe<kCtas == 2>(bar, parity)) return true;
+    uint64_t t0 = 0;
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (probe<kCtas == 2>(bar, parity)) return true;
+        if (__any_sync(0xFFFFFFFFu, aborted(wc))) return false;
+        const uint64_t now = ptx::globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (__any_sync(0xFFFFFFFFu, now - t0 > wc->limit_ns)) {
+            raise_abort(wc);
+            return false;
+        }
+    }
+}
+
+// ---- schedule
+
+// The work of one CTA (pair, or cluster that splits K): tiles t0, t0 + dt, ... below
+// `tiles`, and of each the blocks [kb0, kb1).
+struct Sched {
+    uint32_t t0, dt, tiles;
+    int kb0, kb1;
+    // blocks this CTA works on in all
+    __device__ __forceinline__ uint32_t blocks() const
+    {
+        return t0 < tiles ? ((tiles - t0 + dt - 1) / dt) * static_cast<uint32_t>(kb1 - kb0) : 0u;
+    }
+};
+
+template <typename S>
+__device__ __forceinline__ Sched schedule(const Params &p, const F8Table &table)
+{
+    Sched s;
+    const uint32_t n = S::kCtas == 2 ? 2u : static_cast<uint32_t>(p.splitk);
+    s.t0 = blockIdx.x / n;
+    s.dt = gridDim.x / n;
+    s.tiles = table.first[p.c.experts] * p.tiles_n;
+    s.kb0 = 0;
+    s.kb1 = p.num_kb;
+    if (S::kCtas == 1 && n > 1) {
+        const uint32_t r = ptx::cluster_ctarank();
+        s.kb0 = static_cast<int>(r * static_cast<uint32_t>(p.num_kb) / n);
+        s.kb1 = static_cast<int>((r + 1) * static_cast<uint32_t>(p.num_kb) / n);
+    }
+    return s;
+}
+
+template <typename S>
+__device__ __forceinline__ F8Tile tile_at(const Params &p, const F8Table &table, uint32_t t)
+{
+    return find_tile(table, p.c.experts, p.tiles_n, S::kTokens, S::kChannels, t);
+}
+
+// A ring's position: slot and the parity of its turn.
+struct Ring {
+    uint32_t slot = 0, phase = 0;
+    __device__ __forceinline__ void next(uint32_t slots)
+    {
+        if (++slot == slots) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+// ---- roles
+
+template <typename S>
+__device__ __forceinline__ void run_producer(const CUtensorMap *tmap_t, const CUtensorMap *tmap_w, const Params &p,
+                                             const F8Table &table, uint32_t ring, Ctrl *ctrl, uint32_t rank, WaitCtl *wc)
+{
+    const Sched sc = schedule<S>(p, table);
+    const uint32_t stages = static_cast<uint32_t>(p.stages);
+    Ring st;
+    bool ok = true;
+    for (uint32_t t = sc.t0; ok && t < sc.tiles; t += sc.dt) {
+        const F8Tile tile = tile_at<S>(p, table, t);
+        // this CTA's part of the pair's tile: 128 of its rows, half of its columns
+        const int32_t tok = tile.t0 + static_cast<int32_t>(rank) * (S::kSwap ? S::kBn / S::kCtas : kRows);
+        const int32_t chan = static_cast<int32_t>(tile.n0) + static_cast<int32_t>(rank) * (S::kSwap ? kRows : S::kBn / S::kCtas);
+        for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
+            ok = warp_wait<1>(ptx::smem_addr(&ctrl->empty[st.slot]), st.phase ^ 1u, wc);
+            if (!ok) break;
+            if (elect_one()) {
+                const uint32_t full = ptx::smem_addr(&ctrl->full[st.slot]);
+                const uint32_t dst = ring + st.slot * S::kStageBytes;
+                ptx::mbar_arrive_expect_tx(full, S::kStageBytes);
+                // the innermost coordinate is a multiple of 128 bytes
+                ptx::tma_load_3d(dst + (S::kSwap ? kRowsBytes : 0), tmap_t, full, kb * kRowBytes, tok, 0);
+                ptx::tma_load_3d(dst + (S::kSwap ? 0 : kRowsBytes), tmap_w, full, kb * kRowBytes, chan, tile.expert);
+            }
+            __syncwarp();
+            st.next(stages);
+        }
+    }
+    // Do not leave while TMA may still be writing into this CTA's memory, or the MMAs'
+    // commits may still arrive here: stages before the current one were last filled in
+    // this phase, the others (if at all: a barrier's phase 1 counts as over before its
+    // first) in the one before.
+    if (elect_one())
+        for (uint32_t s = 0; s < stages; ++s) {
+            drain_wait(ptx::smem_addr(&ctrl->full[s]), s < st.slot ? st.phase : st.phase ^ 1u);
+            if (ok) ok = drain_wait(ptx::smem_addr(&ctrl->empty[s]), s < st.slot ? st.phase : st.phase ^ 1u);
+        }
+    __syncwarp();
+}
+
+// The other CTA of a pair: each stage that has landed here is the leader's to use.
+template <typename S>
+__device__ __forceinline__ void run_forwarder(const Params &p, const F8Table &table, Ctrl *ctrl, int lane, WaitCtl *wc)
+{
+    Ring st;
+    for (uint32_t n = schedule<S>(p, table).blocks(); n > 0; --n) {
+        if (!warp_wait<1>(ptx::smem_addr(&ctrl->full[st.slot]), st.phase, wc)) return;
+        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(ptx::smem_addr(&ctrl->peer_full[st.slot]), 0));
+        __syncwarp();
+        st.next(static_cast<uint32_t>(p.stages));
+    }
+}
+
+template <typename S>
+__device__ __forceinline__ void run_mma(const Params &p, const F8Table &table, uint32_t ring, Ctrl *ctrl, uint32_t tmem_base,
+                                        WaitCtl *wc)
+{
+    tmem_base = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);  // a uniform value for the compiler
+    // descriptors of the first stage; a stage on is kStageBytes / 16, an MMA's K step 2, in
+    // their address fields
+    const uint64_t row_desc = ptx::smem_desc(ring, 16, 1024, ptx::kSw128);
+    const uint64_t col_desc = ptx::smem_desc(ring + kRowsBytes, 16, 1024, ptx::kSw128);
+    const uint32_t idesc = p.idesc;
+    Ring st, acc;
+    // test hook: wait on a barrier nothing arrives at, so the wait runs out
+    bool ok = !p.inject_stall || warp_wait<1>(ptx::smem_addr(&ctrl->never), 0, wc);
+    for (uint32_t n = schedule<S>(p, table).blocks(); ok && n > 0; --n) {
+        ok = warp_wait<S::kCtas>(ptx::smem_addr(&ctrl->acc_empty[acc.slot]), acc.phase ^ 1u, wc) &&
+             warp_wait<1>(ptx::smem_addr(&ctrl->full[st.slot]), st.phase, wc) &&
+             (S::kCtas == 1 || warp_wait<2>(ptx::smem_addr(&ctrl->peer_full[st.slot]), st.phase, wc));
+        if (!ok) break;
+        ptx::tc_fence_after();
+        if (elect_one()) {
+            const uint32_t d = tmem_base + acc.slot * S::kBn;
+            const uint64_t a = row_desc + st.slot * (S::kStageBytes >> 4), b = col_desc + st.slot * (S::kStageBytes >> 4);
+#pragma unroll
+            for (int k = 0; k < kRowBytes / 32; ++k) umma_f8<S::kCtas>(d, a + k * 2, b + k * 2, idesc, k == 0 ? 0u : 1u);
+            commit_all<S::kCtas>(ptx::smem_addr(&ctrl->empty[st.slot]));
+            commit_all<S::kCtas>(ptx::smem_addr(&ctrl->acc_full[acc.slot]));
+        }
+        __syncwarp();
+        st.next(static_cast<uint32_t>(p.stages));
+        acc.next(S::kAccs);
+    }
+    // Whatever the epilogue's waits came to, every MMA issued has finished before TMEM is
+    // released (the elected thread is the same one each time).
+    if (elect_one()) {
+        if constexpr (S::kCtas == 2)
+            ptx::umma_commit_pair_multicast(ptx::smem_addr(&ctrl->mma_done), 0x1);
+        else
+            ptx::umma_commit(ptx::smem_addr(&ctrl->mma_done));
+        drain_wait(ptx::smem_addr(&ctrl->mma_done), 0);
+    }
+    __syncwarp();
+}
+
+// A block's scales: the CTA's 128 rows', then the tile's columns' (kUniform: one for each
+// group of columns).  Rows past the operand take its last one's, for sums that are not
+// stored.
+template <typename S>
+__device__ __forceinline__ void run_scales(const Params &p, const F8Table &table, uint32_t scales, Ctrl *ctrl, uint32_t rank,
+                                           int lane, WaitCtl *wc)
+{
+    constexpr int kR = kRows / 32, kC = S::kUniform ? 1 : (S::kBn + 31) / 32;
+    const Sched sc = schedule<S>(p, table);
+    Ring st;
+    bool ok = true;
+    for (uint32_t t = sc.t0; ok && t < sc.tiles; t += sc.dt) {
+        const F8Tile tile = tile_at<S>(p, table, t);
+        const float *weights = p.c.b.scale + tile.expert * p.c.sb_stride;
+        auto place = [&](bool token, int64_t i) {
+            const F8Operand &o = token ? p.c.a : p.c.b;
+            const int64_t at = token ? min(tile.t0 + i, p.c.M - 1) : min(tile.n0 + i, p.c.N - 1);
+            return (token ? o.scale : weights) + at / o.block * o.s_row;
+        };
+        const float *row[kR], *col[kC];
+#pragma unroll
+        for (int i = 0; i < kR; ++i) row[i] = place(!S::kSwap, rank * kRows + i * 32 + lane);
+#pragma unroll
+        for (int i = 0; i < kC; ++i) col[i] = place(S::kSwap, S::kUniform ? (lane & 1) * S::kWgCols : i * 32 + lane);
+        const int64_t row_blk = (S::kSwap ? p.c.b : p.c.a).s_blk, col_blk = (S::kSwap ? p.c.a : p.c.b).s_blk;
+        for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
+            ok = warp_wait<1>(ptx::smem_addr(&ctrl->sc_empty[st.slot]), st.phase ^ 1u, wc);
+            if (!ok) break;
+            const uint32_t dst = scales + st.slot * (kRows + S::kScaleCols) * 4;
+#pragma unroll
+            for (int i = 0; i < kR; ++i) copy_async4(dst + (i * 32 + lane) * 4, row[i] + kb * row_blk);
+#pragma unroll
+            for (int i = 0; i < kC; ++i)
+                if (i * 32 + lane < (S::kUniform ? 2 : S::kBn)) copy_async4(dst + (kRows + i * 32 + lane) * 4, col[i] + kb * col_blk);
+            ptx::cp_async_mbar_arrive_noinc(ptx::smem_addr(&ctrl->sc_full[st.slot]));
+            st.next(kScaleSlots);
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// ---- epilogue
+
+// What one epilogue warp keeps from tile to tile.
+struct Epi {
+    Ring acc, sc;
+    uint32_t left;  // blocks to go
+    uint32_t nbox;
+};
+
+// The sums of one tile (or of this CTA's blocks of it), two columns a word.
+template <typename S>
+__device__ __forceinline__ bool sum_blocks(const Params &p, Ctrl *ctrl, uint32_t scales, uint32_t taddr, int row, int group,
+                                           int blocks, int lane, Epi &e, uint64_t (&sum)[S::kWgCols / 2], WaitCtl *wc)
+{
+    constexpr int kChunk = S::kWgCols == 64 ? 32 : S::kWgCols < 16 ? S::kWgCols : 16, kChunks = S::kWgCols / kChunk;
+#pragma unroll
+    for (int i = 0; i < S::kWgCols / 2; ++i) sum[i] = 0ull;
+    for (int kb = 0; kb < blocks; ++kb) {
+        if (!epi_wait<1>(ptx::smem_addr(&ctrl->sc_full[e.sc.slot]), e.sc.phase, wc)) return false;
+        const uint32_t sc = scales + e.sc.slot * (kRows + S::kScaleCols) * 4;
+        float r = ptx::ld_shared_f32(sc + row * 4);
+        if constexpr (S::kUniform) r *= ptx::ld_shared_f32(sc + (kRows + group) * 4);
+        const uint64_t r2 = pack2(r, r);
+        if (!epi_wait<S::kCtas>(ptx::smem_addr(&ctrl->acc_full[e.acc.slot]), e.acc.phase, wc)) return false;
+        ptx::tc_fence_after();
+        const uint32_t src = taddr + e.acc.slot * S::kBn;
+        uint32_t d[kChunks > 1 ? 2 : 1][kChunk];
+        tmem_load<kChunk>(src, d[0]);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            uint32_t(&v)[kChunk] = d[c & 1];
+            tmem_wait<kChunk>(v);
+            if (c + 1 < kChunks) {
+                tmem_load<kChunk>(src + (c + 1) * kChunk, d[(c + 1) & 1]);
+            } else {
+                ptx::tc_fence_before();
+                __syncwarp();
+                // (an arrival that nothing waits for could reach a CTA that has left)
+                if (lane == 0 && e.left > S::kAccs) {
+                    if constexpr (S::kCtas == 2)
+                        arrive_remote(ptx::mapa(ptx::smem_addr(&ctrl->acc_empty[e.acc.slot]), 0));
+                    else
+                        ptx::mbar_arrive(ptx::smem_addr(&ctrl->acc_empty[e.acc.slot]));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kChunk; i += 4) {
+                uint64_t x = pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                uint64_t y = pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+                if constexpr (!S::kUniform) {
+                    const float4 s = ptx::ld_shared_v4f(sc + (kRows + group * S::kWgCols + c * kChunk + i) * 4);
+                    x = mul2(x, pack2(s.x, s.y));
+                    y = mul2(y, pack2(s.z, s.w));
+                }
+                const int at = (c * kChunk + i) / 2;
+                sum[at] = fma2(x, r2, sum[at]);
+                sum[at + 1] = fma2(y, r2, sum[at + 1]);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctrl->sc_empty[e.sc.slot]));
+        --e.left;
+        e.acc.next(S::kAccs);
+        e.sc.next(kScaleSlots);
+    }
+    return true;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack_bits(float a, float b)
+{
+    if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+
+// Rows = tokens: a warp's 32 rows from `row0` (up to row_end) x kCols columns from col0.  Boxes
+// of 128 bytes of columns are staged in shared memory (128-byte swizzle: word w of row r at
+// w ^ (r mod 8)) and stored by TMA, or, where the box holds rows that are not the expert's
+// or TMA cannot describe C, word by word, 8 lanes a row.
+template <typename T, int kCols>
+__device__ __forceinline__ void store_tokens(const Params &p, const CUtensorMap *tmap_o, const uint64_t (&sum)[kCols / 2],
+                                             int64_t row0, int64_t row_end, int64_t col0, uint32_t box, int lane, uint32_t &nbox)
+{
+    constexpr int kPer = 16 / sizeof(T), kBoxCols = 128 / sizeof(T);  // values of a word, of a row of the box
+    if (row0 >= row_end) return;  // warp-uniform
+    const int64_t row = row0 + lane;
+    const float beta = p.c.beta;
+    T *const C = static_cast<T *>(p.c.C);
+    const bool whole = p.tma_store && (!p.c.offsets || row0 + 32 <= row_end);
+    const bool words = (reinterpret_cast<uintptr_t>(C) & 15u) == 0 && p.c.ldc % kPer == 0;
+#pragma unroll
+    for (int b = 0; b < kCols / kBoxCols; ++b) {
+        const int64_t c = col0 + b * kBoxCols;
+        if (c >= p.c.N) return;
+        const uint32_t buf = box + (p.boxes == 2 ? (nbox & 1u) * kBoxBytes : 0u);
+        if (lane == 0) {  // this box's last store has read it
+            if (p.boxes == 2)
+                ptx::bulk_wait_read<1>();
+            else
+                ptx::bulk_wait_read<0>();
+        }
+        __syncwarp();
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            float v[kPer];
+#pragma unroll
+            for (int i = 0; i < kPer; i += 2) unpack2(sum[(b * kBoxCols + w * kPer + i) / 2], v[i], v[i + 1]);
+            const int64_t cw = c + w * kPer;
+            if (p.c.bias) {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    if (cw + i < p.c.N) v[i] += p.c.bias[cw + i];
+            }
+            if (beta != 0.f && row < row_end) {
+                const T *old = C + row * p.c.ldc + cw;
+                if (words && cw + kPer <= p.c.N) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(old);
+                    const T *o = reinterpret_cast<const T *>(&q);
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) v[i] = fmaf(beta, to_f32(o[i]), v[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i)
+                        if (cw + i < p.c.N) v[i] = fmaf(beta, to_f32(old[i]), v[i]);
+                }
+            }
+            uint4 q;
+            if constexpr (sizeof(T) == 2)
+                q = make_uint4(pack_bits<T>(v[0], v[1]), pack_bits<T>(v[2], v[3]), pack_bits<T>(v[4], v[5]), pack_bits<T>(v[6], v[7]));
+            else
+                q = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+            ptx::st_shared_v4(buf + lane * 128u + ((w ^ (lane & 7u)) << 4), q);
+        }
+        if (whole) {
+            ptx::fence_proxy_async_smem();  // the TMA store reads through the async proxy
+            __syncwarp();
+            if (lane == 0 && DGEMM_CHECK(row0 >= 0 && c >= 0 && row0 < p.c.M && c < p.c.N)) {
+                ptx::tma_store_2d(tmap_o, buf, static_cast<int32_t>(c), static_cast<int32_t>(row0));
+                ptx::bulk_commit();
+            }
+            ++nbox;
+            continue;
+        }
+        __syncwarp();
+#pragma unroll 1
+        for (int i = 0; i < 32; i += 4) {
+            const uint32_t r = i + (lane >> 3), w = lane & 7u;
+            const int64_t m = row0 + r, cw = c + w * kPer;
+            if (m >= row_end || cw >= p.c.N || !DGEMM_CHECK(m < p.c.M)) continue;
+            const uint4 q = ld_shared_v4(buf + r * 128u + ((w ^ (r & 7u)) << 4));
+            T *dst = C + m * p.c.ldc + cw;
+            if (words && cw + kPer <= p.c.N) {
+                *reinterpret_cast<uint4 *>(dst) = q;
+            } else {
+                const T *v = reinterpret_cast<const T *>(&q);
+#pragma unroll
+                for (int k = 0; k < kPer; ++k)
+                    if (cw + k < p.c.N) dst[k] = v[k];
+            }
+        }
+        __syncwarp();  // the box is written again
+    }
+}
+
+// Rows = channels: this lane's channel n of tokens m0 .. m_end; the warp's lanes store
+// consecutive channels.
+template <typename T, int kCols>
+__device__ __forceinline__ void store_channels(const Params &p, const uint64_t (&sum)[kCols / 2], int64_t n, int64_t m0, int64_t m_end)
+{
+    if (n >= p.c.N) return;
+    const float bias = p.c.bias ? p.c.bias[n] : 0.f;
+    T *dst = static_cast<T *>(p.c.C) + m0 * p.c.ldc + n;
+#pragma unroll
+    for (int j = 0; j < kCols; j += 2) {
+        float v[2];
+        unpack2(sum[j / 2], v[0], v[1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (m0 + j + i >= m_end || !DGEMM_CHECK(m0 + j + i < p.c.M)) continue;
+            T *d = dst + (j + i) * p.c.ldc;
+            float x = v[i] + bias;
+            if (p.c.beta != 0.f) x = fmaf(p.c.beta, to_f32(*d), x);
+            *d = from_f32<T>(x);
+        }
+    }
+}
+
+template <typename S, int kCols>
+__device__ __forceinline__ void store_channels_any(const Params &p, const uint64_t (&sum)[kCols / 2], int64_t n, int64_t m0, int64_t m_end)
+{
+    switch (p.c.c_type) {
+    case DGEMM_TYPE_F32: return store_channels<float, kCols>(p, sum, n, m0, m_end);
+    case DGEMM_TYPE_F16: return store_channels<__half, kCols>(p, sum, n, m0, m_end);
+    default: return store_channels<__nv_bfloat16, kCols>(p, sum, n, m0, m_end);
+    }
+}
+
+// Split-K: the S CTAs of a cluster have each summed a range of one tile's blocks.  Groups of
+// 8 columns are owned round-robin by the ranks; each CTA pushes the groups it does not own
+// into the owner's idle stage ring, [sender slot][owned group][column quad][row] in 16-byte
+// units, and the owner adds the partials in rank order, so the sum does not depend on timing.
+__device__ __forceinline__ uint32_t recv_offset(uint32_t groups, uint32_t slot, uint32_t idx, uint32_t S, int q, int row)
+{
+    const uint32_t owned = (groups + S - 1) / S;
+    return (((slot * owned + idx) * 2u + static_cast<uint32_t>(q)) * kRows + static_cast<uint32_t>(row)) * 16u;
+}
+
+template <typename S>
+__device__ __forceinline__ void join_split(const Params &p, const F8Tile &tile, uint32_t ring, int row, int group, int64_t n,
+                                           const uint64_t (&sum)[S::kWgCols / 2], WaitCtl *wc)
+{
+    constexpr uint32_t kGroups = S::kBn / 8, kMine = S::kWgCols / 8;  // of the tile, of this thread
+    const uint32_t N = static_cast<uint32_t>(p.splitk), rank = ptx::cluster_ctarank();
+    const uint32_t bytes = static_cast<uint32_t>(p.stages) * S::kStageBytes;
+    ptx::cluster_sync();  // every CTA's sums are complete: the rings are idle
+    const bool stop = __any_sync(0xFFFFFFFFu, aborted(wc));
+    if (!stop) {
+#pragma unroll
+        for (uint32_t i = 0; i < kMine; ++i) {
+            const uint32_t g = group * kMine + i, owner = g % N;
+            if (owner == rank) continue;
+            const uint32_t slot = rank < owner ? rank : rank - 1;
+            if (!DGEMM_CHECK(recv_offset(kGroups, slot, g / N, N, 1, row) + 16 <= bytes)) continue;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float4 f;
+                unpack2(sum[i * 4 + q * 2], f.x, f.y);
+                unpack2(sum[i * 4 + q * 2 + 1], f.z, f.w);
+                ptx::st_shared_cluster_v4(ptx::mapa(ring + recv_offset(kGroups, slot, g / N, N, q, row), owner), f);
+            }
+        }
+    }
+    __syncwarp();
+    ptx::cluster_sync();  // every partial has landed in its owner
+    if (stop) return;
+#pragma unroll
+    for (uint32_t i = 0; i < kMine; ++i) {
+        const uint32_t g = group * kMine + i;
+        if (g % N != rank) continue;
+        uint64_t total[4] = {};
+        for (uint32_t s = 0; s < N; ++s) {
+            const uint32_t slot = s < rank ? s : s - 1;
+            if (s != rank && !DGEMM_CHECK(recv_offset(kGroups, slot, g / N, N, 1, row) + 16 <= bytes)) continue;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint64_t a = sum[i * 4 + q * 2], b = sum[i * 4 + q * 2 + 1];
+                if (s != rank) {
+                    const float4 f = ptx::ld_shared_v4f(ring + recv_offset(kGroups, slot, g / N, N, q, row));
+                    a = pack2(f.x, f.y);
+                    b = pack2(f.z, f.w);
+                }
+                total[q * 2] = add2(total[q * 2], a);
+                total[q * 2 + 1] = add2(total[q * 2 + 1], b);
+            }
+        }
+        store_channels_any<S, 8>(p, total, n, tile.t0 + g * 8, tile.t_end);
+    }
+}
+
+template <typename S>
+__device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap *tmap_o, const F8Table &table, uint32_t ring,
+                                             uint32_t box, uint32_t scales, Ctrl *ctrl, uint32_t tmem_base, uint32_t rank,
+                                             int warp, int lane, WaitCtl *wc)
+{
+    const Sched sc = schedule<S>(p, table);
+    const int quarter = warp & 3, group = (warp - 4) >> 2, row = quarter * 32 + lane;
+    const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + group * S::kWgCols;
+    const uint32_t my_box = box + static_cast<uint32_t>(warp - 4) * p.boxes * kBoxBytes;
+    Epi e{{}, {}, sc.blocks(), 0};
+    uint64_t sum[S::kWgCols / 2];
+    if (S::kSwap && p.splitk > 1) {  // one tile, uniform over the cluster
+        const F8Tile tile = tile_at<S>(p, table, sc.t0);
+        sum_blocks<S>(p, ctrl, scales, taddr, row, group, sc.kb1 - sc.kb0, lane, e, sum, wc);  // (a time-out raises the abort flag)
+        __syncwarp();
+        if constexpr (S::kSwap) join_split<S>(p, tile, ring, row, group, tile.n0 + row, sum, wc);
+        return;
+    }
+    for (uint32_t t = sc.t0; t < sc.tiles; t += sc.dt) {
+        const F8Tile tile = tile_at<S>(p, table, t);
+        if (!sum_blocks<S>(p, ctrl, scales, taddr, row, group, sc.kb1 - sc.kb0, lane, e, sum, wc)) break;
+        if constexpr (S::kSwap) {
+            store_channels_any<S, S::kWgCols>(p, sum, tile.n0 + rank * kRows + row, tile.t0 + group * S::kWgCols, tile.t_end);
+        } else {
+            const int64_t row0 = tile.t0 + rank * kRows + quarter * 32, col0 = tile.n0 + group * S::kWgCols;
+            switch (p.c.c_type) {
+            case DGEMM_TYPE_F32: store_tokens<float, S::kWgCols>(p, tmap_o, sum, row0, tile.t_end, col0, my_box, lane, e.nbox); break;
+            case DGEMM_TYPE_F16: store_tokens<__half, S::kWgCols>(p, tmap_o, sum, row0, tile.t_end, col0, my_box, lane, e.nbox); break;
+            default: store_tokens<__nv_bfloat16, S::kWgCols>(p, tmap_o, sum, row0, tile.t_end, col0, my_box, lane, e.nbox);
+            }
+        }
+        __syncwarp();
+    }
+    if (!S::kSwap && lane == 0) ptx::bulk_wait<0>();  // stores done before the CTA leaves
+}
+
+template <typename S>
+__global__ void __launch_bounds__(kThreads, S::kPerSm)
+    f8_umma_kernel(const __grid_constant__ CUtensorMap tmap_t, const __grid_constant__ CUtensorMap tmap_w,
+                   const __grid_constant__ CUtensorMap tmap_o, const Params p)
+{
+    // stage ring | staging boxes | scales | control | table of tiles
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t ring = ptx::smem_addr(smem);
+    const uint32_t box = ring + static_cast<uint32_t>(p.stages) * S::kStageBytes;
+    const uint32_t scales = box + (S::kSwap ? 0u : static_cast<uint32_t>(kEpiWarps * p.boxes) * kBoxBytes);
+    Ctrl *ctrl = reinterpret_cast<Ctrl *>(smem + (scales - ring) + S::kScaleBytes);
+    uint32_t *words = reinterpret_cast<uint32_t *>(ctrl + 1);
+    const F8Table table{words, reinterpret_cast<int32_t *>(words + p.c.experts + 1)};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = S::kCtas == 2 ? (ptx::cluster_ctarank() & 1u) : 0u;
+
+    if (warp == 0 && elect_one()) {
+        for (int s = 0; s < kMaxStages; ++s) {
+            ptx::mbar_init(ptx::smem_addr(&ctrl->full[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&ctrl->peer_full[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&ctrl->empty[s]), 1);
+        }
+        for (int a = 0; a < kMaxAccs; ++a) {
+            ptx::mbar_init(ptx::smem_addr(&ctrl->acc_full[a]), 1);
+            ptx::mbar_init(ptx::smem_addr(&ctrl->acc_empty[a]), kEpiWarps * S::kCtas);
+        }
+        for (int s = 0; s < kScaleSlots; ++s) {
+            ptx::mbar_init(ptx::smem_addr(&ctrl->sc_full[s]), 32);
+            ptx::mbar_init(ptx::smem_addr(&ctrl->sc_empty[s]), kEpiWarps);
+        }
+        ptx::mbar_init(ptx::smem_addr(&ctrl->mma_done), 1);
+        ptx::mbar_init(ptx::smem_addr(&ctrl->never), 1);
+        ctrl->wait.abort = 0;
+        ctrl->wait.limit_ns = p.wait_limit_ns;
+        ptx::fence_mbarrier_init();
+    } else if (warp == 1) {
+        if constexpr (S::kCtas == 2) {
+            ptx::tmem_alloc_pair(ptx::smem_addr(&ctrl->tmem_base), S::kTmemCols);
+            ptx::tmem_relinquish_pair();
+        } else {
+            ptx::tmem_alloc(ptx::smem_addr(&ctrl->tmem_base), S::kTmemCols);
+            ptx::tmem_relinquish();
+        }
+    } else if (warp == 2 && elect_one()) {
+        ptx::prefetch_tmap(&tmap_t);
+        ptx::prefetch_tmap(&tmap_w);
+        if (p.tma_store) ptx::prefetch_tmap(&tmap_o);
+    }
+    __syncwarp();
+    chain_wait();  // (everything below reads or writes the call's operands)
+    chain_next();
+    if (warp == 3) fill_table(p.c, S::kTokens, table, lane);
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    // both CTAs' barriers exist (fence_mbarrier_init above) before any cross-CTA signal
+    if constexpr (S::kCtas == 2) cluster_meet();
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = ctrl->tmem_base;
+    WaitCtl *wc = &ctrl->wait;
+
+    if (warp < 4) {
+        if (warp == 0) {
+            run_producer<S>(&tmap_t, &tmap_w, p, table, ring, ctrl, rank, wc);
+        } else if (warp == 1) {
+            if (rank == 0)
+                run_mma<S>(p, table, ring, ctrl, tmem_base, wc);
+            else
+                run_forwarder<S>(p, table, ctrl, lane, wc);
+        } else if (warp == 2) {
+            run_scales<S>(p, table, scales, ctrl, rank, lane, wc);
+        }
+        __syncwarp();
+        if (S::kSwap && p.splitk > 1) {  // (join_split's barriers)
+            ptx::cluster_sync();
+            ptx::cluster_sync();
+        }
+    } else {
+        run_epilogue<S>(p, &tmap_o, table, ring, box, scales, ctrl, tmem_base, rank, warp, lane, wc);
+    }
+
+    __syncwarp();  // the barriers below are warp-aligned: reconverge the single-lane roles
+    ptx::tc_fence_before();
+    __syncthreads();  // every role of this CTA is done
+    if constexpr (S::kCtas == 2) {
+        // after an abort, arrivals on the leader's barriers that nothing has waited for may be
+        // under way: they come before this CTA's part in the meeting
+        if (__any_sync(0xFFFFFFFFu, aborted(wc))) fence_cluster();
+        cluster_meet();  // no CTA leaves while the other may still signal or read it
+    }
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        if constexpr (S::kCtas == 2)
+            ptx::tmem_dealloc_pair(tmem_base, S::kTmemCols);
+        else
+            ptx::tmem_dealloc(tmem_base, S::kTmemCols);
+    }
+}
+
+// ---- host side
+
+// Dynamic shared memory of a launch, and its rings: two boxes a warp if that leaves five
+// stages, else one.
+template <typename S>
+int set_rings(Params &p)
+{
+    const int fixed = S::kScaleBytes + static_cast<int>(sizeof(Ctrl)) + 8 * (p.c.experts + 1);
+    const int limit = S::kPerSm == 2 ? 113 * 1024 : kSmemLimit;  // (an SM's 228 KB, less 1 KB a CTA)
+    p.boxes = 0;
+    if (!S::kSwap) p.boxes = (limit - fixed - 2 * kEpiWarps * kBoxBytes) / S::kStageBytes >= 5 ? 2 : 1;
+    const int boxes = kEpiWarps * p.boxes * kBoxBytes;
+    p.stages = std::min(kMaxStages, (limit - fixed - boxes) / S::kStageBytes);
+    return fixed + boxes + p.stages * S::kStageBytes;
+}
+
+// CTAs (or clusters of `cluster`) of the kernel that can be resident at once on the
+// current device, cached; 0 if it cannot run.
+template <typename S>
+int capacity(int cluster)
+{
+    constexpr int kMaxDevices = 64;
+    static int cached[kMaxDevices][9];
+    static std::once_flag once[kMaxDevices];
+    int dev = 0;
+    if (cluster < 1 || cluster > 8 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+    std::call_once(once[dev], [dev] {
+        auto kernel = f8_umma_kernel<S>;
+        const int smem = S::kPerSm == 2 ? 113 * 1024 : kSmemLimit;
+        int sms = 0;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess &&
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) {
+            cached[dev][1] = sms * S::kPerSm;
+            for (int s = 2; s <= (S::kCtas == 2 ? 2 : 8); ++s) {
+                cudaLaunchConfig_t cfg = {};
+                cudaLaunchAttribute attr[1];
+                attr[0].id = cudaLaunchAttributeClusterDimension;
+                attr[0].val.clusterDim.x = static_cast<unsigned>(s);
+                attr[0].val.clusterDim.y = 1;
+                attr[0].val.clusterDim.z = 1;
+                cfg.gridDim = dim3(static_cast<unsigned>(sms - sms % s));
+                cfg.blockDim = dim3(kThreads);
+                cfg.dynamicSmemBytes = smem;
+                cfg.attrs = attr;
+                cfg.numAttrs = 1;
+                int n = 0;
+                if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
+                cached[dev][s] = n;
+            }
+        }
+        cudaGetLastError();  // a failed query leaves no sticky error behind
+    });
+    return cached[dev][cluster];
+}
+
+template <typename S>
+bool launch(const F8Params &c, int splitk, cudaStream_t stream)
+{
+    Params p{};
+    p.c = c;
+    const int64_t tiles_n = (c.N + S::kChannels - 1) / S::kChannels, tiles = tiles_n * token_tiles_bound(c, S::kTokens);
+    if (tiles > INT32_MAX / 16) return false;  // (32-bit tile arithmetic, with room for a group of tile columns)
+    p.tiles_n = static_cast<uint32_t>(tiles_n);
+    p.num_kb = static_cast<int>((c.K + kRowBytes - 1) / kRowBytes);
+    p.splitk = S::kSwap && !c.offsets ? std::min(splitk, p.num_kb) : 1;
+    if (tiles / 76 * p.num_kb > INT32_MAX) return false;  // blocks of one CTA
+    const int cluster = S::kCtas == 2 ? 2 : p.splitk;
+    const int fit = capacity<S>(cluster);
+    const int smem = set_rings<S>(p);
+    if (fit < 1 || p.stages < 3 || (p.splitk > 1 && tiles > fit)) return false;
+    constexpr int kTokBox = S::kSwap ? S::kBn / S::kCtas : kRows, kChanBox = S::kSwap ? kRows : S::kBn / S::kCtas;
+    const uint64_t k = static_cast<uint64_t>(c.K), m = static_cast<uint64_t>(c.M), n = static_cast<uint64_t>(c.N);
+    CUtensorMap mt{}, mw{}, mo{};
+    if (!encode_tiled_3d(&mt, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.a.p, {k, m, 1}, {static_cast<uint64_t>(c.a.ld), m * c.a.ld},
+                         {kRowBytes, kTokBox, 1}, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tiled_3d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.b.p, {k, n, static_cast<uint64_t>(c.experts)},
+                         {static_cast<uint64_t>(c.b.ld), c.experts > 1 ? static_cast<uint64_t>(c.b_stride) : n * c.b.ld},
+                         {kRowBytes, kChanBox, 1}, CU_TENSOR_MAP_SWIZZLE_128B))
+        return false;
+    if (!S::kSwap) {
+        const int e = c.c_type == DGEMM_TYPE_F32 ? 4 : 2;
+        const CUtensorMapDataType dt = c.c_type == DGEMM_TYPE_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                       : c.c_type == DGEMM_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        p.tma_store = aligned16(c.C) && c.ldc * e % 16 == 0 &&
+                      encode_tiled_2d(&mo, dt, c.C, n, m, static_cast<uint64_t>(c.ldc) * e, static_cast<uint32_t>(128 / e), 32,
+                                      CU_TENSOR_MAP_SWIZZLE_128B);
+    }
+    // D f32; the types of the rows' and the columns' operand; both K-major; N = kBn, M = 128 rows a CTA
+    const uint32_t rows_type = static_cast<uint32_t>((S::kSwap ? c.b : c.a).type), cols_type = static_cast<uint32_t>((S::kSwap ? c.a : c.b).type);
+    p.idesc = (1u << 4) | (rows_type << 7) | (cols_type << 10) | (static_cast<uint32_t>(S::kBn >> 3) << 17) |
+              (static_cast<uint32_t>(S::kTileRows >> 4) << 24);
+    const uint64_t stall = take_injected_stall();
+    p.inject_stall = stall ? 1 : 0;
+    p.wait_limit_ns = stall ? stall : kWaitLimitNs;
+    if (launch_chained(f8_umma_kernel<S>, static_cast<unsigned>(cluster * std::min<int64_t>(tiles, fit)), kThreads, smem, stream,
+                       static_cast<unsigned>(cluster), mt, mw, mo, p) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return true;
+}
+
+}  // namespace
+
+bool f8_umma_config_ok(const F8Config &cfg)
+{
+    switch (cfg.variant) {
+    case kF8Pair: return cfg.bn == 128 || cfg.bn == 256;
+    case kF8Channels:
+        return (cfg.bn == 16 || cfg.bn == 32 || cfg.bn == 64 || cfg.bn == 128) && cfg.split >= 1 && cfg.split <= 8;
+    default: return false;
+    }
+}
+
+bool launch_f8_umma(const F8Params &c, const F8Config &cfg, cudaStream_t stream)
+{
+    if (!f8_umma_config_ok(cfg)) return false;
+    if (cfg.variant == kF8Pair) {
+        const bool uniform = c.b.block == kF8Block;
+        if (cfg.bn == 256)
+            return uniform ? launch<Shape<2, false, 256, true>>(c, 1, stream) : launch<Shape<2, false, 256, false>>(c, 1, stream);
+        return uniform ? launch<Shape<2, false, 128, true>>(c, 1, stream) : launch<Shape<2, false, 128, false>>(c, 1, stream);
+    }
+    switch (cfg.bn) {
+    case 16: return launch<Shape<1, true, 16, false>>(c, cfg.split, stream);
+    case 32: return launch<Shape<1, true, 32, false>>(c, cfg.split, stream);
+    case 64: return launch<Shape<1, true, 64, false>>(c, cfg.split, stream);
+    default: return launch<Shape<1, true, 128, false>>(c, cfg.split, stream);
+    }
+}
+
+int f8_read_status(int clear)
+{
+    return read_wait_status(clear);
+}
+
+}  // namespace dgemm
+
+DGEMM_DEFINE_CHECK_READER(check_status_f8_umma)

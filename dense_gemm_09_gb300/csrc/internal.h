@@ -60,6 +60,10 @@ int simt_read_status(int clear);
 bool encode_tiled_2d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t outer,
                      uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle);
 
+// The same with three dimensions (innermost first; byte strides of the outer two).
+bool encode_tiled_3d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, const uint64_t (&dims)[3],
+                     const uint64_t (&strides)[2], const uint32_t (&box)[3], CUtensorMapSwizzle swizzle);
+
 // The stall requested by dgemm_test_inject_stall for the next launch of a
 // kernel with bounded waits on this host thread (its wait limit in ns, 0 if
 // none); taking it clears the request.
@@ -79,6 +83,7 @@ int check_status_i8_umma(int clear, int *site);
 int check_status_i8_decode(int clear, int *site);
 int check_status_f8_rows(int clear, int *site);
 int check_status_f8_gemm(int clear, int *site);
+int check_status_f8_umma(int clear, int *site);
 int check_status_experts(int clear, int *site);
 
 // Rows taken off M for the C-store checks of the next TMA-fed SIMT launch
@@ -154,6 +159,7 @@ const char *launch_combine_grad(int64_t tokens, int64_t top, int64_t cols, const
 
 // Device status word of the 8-bit tensor-core kernels.
 int i8_read_status(int clear);
+int f8_read_status(int clear);
 
 // Test hook behind dgemm_test_inject_stall.
 void umma_inject_stall(uint64_t wait_limit_ns);

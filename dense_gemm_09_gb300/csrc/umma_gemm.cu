@@ -2826,6 +2826,12 @@ bool encode_tiled_2d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, u
     return make_map(m, dt, base, inner, outer, row_bytes, box_inner, box_outer, swizzle);
 }
 
+bool encode_tiled_3d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, const uint64_t (&dims)[3],
+                     const uint64_t (&strides)[2], const uint32_t (&box)[3], CUtensorMapSwizzle swizzle)
+{
+    return make_map_3d(m, dt, base, dims, strides, box, swizzle);
+}
+
 int umma_read_status(int clear)
 {
     return read_wait_status(clear);
