@@ -275,7 +275,7 @@ __device__ __forceinline__ void run_forwarder(const Params &p, const F8Table &ta
     Ring st;
     for (uint32_t n = schedule<S>(p, table).blocks(); n > 0; --n) {
         if (!warp_wait<1>(ptx::smem_addr(&ctrl->full[st.slot]), st.phase, wc)) return;
-        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(ptx::smem_addr(&ctrl->peer_full[st.slot]), 0));
+        if (lane == 0) arrive_remote(ptx::mapa(ptx::smem_addr(&ctrl->peer_full[st.slot]), 0));
         __syncwarp();
         st.next(static_cast<uint32_t>(p.stages));
     }
