@@ -54,7 +54,8 @@ constexpr int kRowBytes = kF8Block;            // a block of K, one byte a value
 constexpr int kRowsBytes = kRows * kRowBytes;
 constexpr int kMaxStages = 12;
 constexpr int kMaxAccs = 8;
-constexpr int kScaleSlots = 4;
+constexpr int kSpan = 4;                        // blocks whose scales go together: a wait costs ~150 clocks
+constexpr int kScaleSlots = 2;
 constexpr int kBoxBytes = 4096;                // epilogue staging: 32 rows x 128 bytes
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (4 + kEpiWarps);
@@ -64,12 +65,12 @@ struct Ctrl {
     uint64_t full[kMaxStages];       // a stage of this CTA has landed
     uint64_t peer_full[kMaxStages];  // leader: the other CTA's has
     uint64_t empty[kMaxStages];      // the MMAs have read it
-    uint64_t acc_full[kMaxAccs];     // the MMAs of a block are done
-    uint64_t acc_empty[kMaxAccs];    // leader: every epilogue warp of the pair has read them
+    uint64_t acc_full[kMaxAccs];     // the MMAs of a block (a half of it: [half][slot]) are done
+    uint64_t acc_empty[kMaxAccs];    // leader: every epilogue warp of the pair that reads them has
     uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
     uint64_t mma_done;
     uint64_t never;                  // test hook: a barrier nothing arrives at
-    WaitCtl wait;
+    uint32_t stop, limit_us;         // a wait ran out; a wait's limit, in 1024 ns (adjacent, see role_wait)
     uint32_t tmem_base;
 };
 
@@ -82,7 +83,7 @@ struct Params {
     int splitk;            // CTAs of a cluster that share a tile (kSwap)
     int tma_store;
     uint32_t idesc;
-    uint64_t wait_limit_ns;
+    uint32_t wait_limit_us;
     int inject_stall;
 };
 
@@ -97,11 +98,19 @@ struct Shape {
     static constexpr int kTileRows = kRows * kCtas;
     static constexpr int kTokens = kSwap ? kBn : kTileRows, kChannels = kSwap ? kRows : kBn;  // of a tile
     static constexpr int kStageBytes = kRowsBytes + kBn / kCtas * kRowBytes;
-    static constexpr int kAccs = 512 / kBn < kMaxAccs ? 512 / kBn : kMaxAccs;
+    // tiles of 256 columns: an MMA for each epilogue group's half, with accumulators and
+    // barriers of its own, so that one group reads while the other's half is multiplied
+    static constexpr int kHalves = kBn == 256 ? 2 : 1;
+    static constexpr int kAccs = 512 / kBn < kMaxAccs ? 512 / kBn : kMaxAccs;  // of either half
     static constexpr int kTmemCols = kAccs * kBn;
-    static constexpr int kScaleCols = kUniform ? 4 : kBn;       // floats of a slot beside the rows'
-    static constexpr int kScaleBytes = kScaleSlots * (kRows + kScaleCols) * 4;
+    // a slot of scales: [row][block], then [group][block] or [block][column]
+    static constexpr int kSlotBytes = kSpan * (kRows + (kUniform ? 2 : kBn)) * 4;
+    static constexpr int kScaleBytes = kScaleSlots * kSlotBytes;
     static constexpr int kPerSm = kBn <= 32 ? 2 : 1;            // CTAs an SM
+    // sums of 128 columns and 64 more on their way do not fit the 168 registers a thread that
+    // 384 threads share alike: the four other warps give 112 each of theirs
+    static constexpr bool kMoveRegs = kWgCols >= 128;
+    static_assert(!kMoveRegs || 128 * 56 + 256 * 224 <= 384 * 168, "what is taken was given");
     static_assert(kTmemCols >= 32 && (kTmemCols & (kTmemCols - 1)) == 0 && kPerSm * kTmemCols <= 512, "TMEM");
 };
 
@@ -155,25 +164,62 @@ __device__ __forceinline__ void copy_async4(uint32_t dst, const float *src)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// warp_wait for the epilogue, in line: a call would have to save the sums, up to 128
-// registers, around itself.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const float *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Whether the phase of this parity is over, without waiting.
+__device__ __forceinline__ bool test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// warp_wait, in line (a call would have to save the epilogue's sums around itself, and
+// functions do not go with setmaxnreg), with the wait control at a shared-memory address.
+__device__ __forceinline__ bool stopped(uint32_t wc)
+{
+    uint32_t v;
+    asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(v) : "r"(wc) : "memory");
+    return v != 0;
+}
+
 template <int kCtas>
-__device__ __forceinline__ bool epi_wait(uint32_t bar, uint32_t parity, WaitCtl *wc)
+__device__ __forceinline__ bool role_wait(uint32_t bar, uint32_t parity, uint32_t wc)
 {
     if (probe<kCtas == 2>(bar, parity)) return true;
-    uint64_t t0 = 0;
+    uint32_t began = 0;  // in microseconds
     for (;;) {
 #pragma unroll 1
         for (int i = 0; i < 32; ++i)
             if (probe<kCtas == 2>(bar, parity)) return true;
-        if (__any_sync(0xFFFFFFFFu, aborted(wc))) return false;
-        const uint64_t now = ptx::globaltimer_ns();
-        if (t0 == 0) t0 = now;
-        if (__any_sync(0xFFFFFFFFu, now - t0 > wc->limit_ns)) {
-            raise_abort(wc);
+        if (__any_sync(0xFFFFFFFFu, stopped(wc))) return false;
+        const uint32_t now = static_cast<uint32_t>(ptx::globaltimer_ns() >> 10) | 1u;
+        if (began == 0) began = now;
+        uint32_t limit;
+        asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(limit) : "r"(wc + 4u) : "memory");
+        if (__any_sync(0xFFFFFFFFu, now - began > limit)) {
+            atomicExch(&g_wait_status, DGEMM_ERR_TIMEOUT);
+            asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(wc), "r"(1u) : "memory");
             return false;
         }
     }
+}
+
+__device__ __forceinline__ bool role_drain(uint32_t bar, uint32_t parity)
+{
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (!ptx::mbar_try_wait(bar, parity))
+        if (ptx::globaltimer_ns() - t0 > kDrainLimitNs) return false;
+    return true;
 }
 
 // ---- schedule
@@ -230,7 +276,7 @@ struct Ring {
 
 template <typename S>
 __device__ __forceinline__ void run_producer(const CUtensorMap *tmap_t, const CUtensorMap *tmap_w, const Params &p,
-                                             const F8Table &table, uint32_t ring, Ctrl *ctrl, uint32_t rank, WaitCtl *wc)
+                                             const F8Table &table, uint32_t ring, Ctrl *ctrl, uint32_t rank, uint32_t wc)
 {
     const Sched sc = schedule<S>(p, table);
     const uint32_t stages = static_cast<uint32_t>(p.stages);
@@ -242,7 +288,7 @@ __device__ __forceinline__ void run_producer(const CUtensorMap *tmap_t, const CU
         const int32_t tok = tile.t0 + static_cast<int32_t>(rank) * (S::kSwap ? S::kBn / S::kCtas : kRows);
         const int32_t chan = static_cast<int32_t>(tile.n0) + static_cast<int32_t>(rank) * (S::kSwap ? kRows : S::kBn / S::kCtas);
         for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
-            ok = warp_wait<1>(ptx::smem_addr(&ctrl->empty[st.slot]), st.phase ^ 1u, wc);
+            ok = role_wait<1>(ptx::smem_addr(&ctrl->empty[st.slot]), st.phase ^ 1u, wc);
             if (!ok) break;
             if (elect_one()) {
                 const uint32_t full = ptx::smem_addr(&ctrl->full[st.slot]);
@@ -250,7 +296,14 @@ __device__ __forceinline__ void run_producer(const CUtensorMap *tmap_t, const CU
                 ptx::mbar_arrive_expect_tx(full, S::kStageBytes);
                 // the innermost coordinate is a multiple of 128 bytes
                 ptx::tma_load_3d(dst + (S::kSwap ? kRowsBytes : 0), tmap_t, full, kb * kRowBytes, tok, 0);
-                ptx::tma_load_3d(dst + (S::kSwap ? 0 : kRowsBytes), tmap_w, full, kb * kRowBytes, chan, tile.expert);
+                if constexpr (S::kHalves == 1) {
+                    ptx::tma_load_3d(dst + (S::kSwap ? 0 : kRowsBytes), tmap_w, full, kb * kRowBytes, chan, tile.expert);
+                } else {  // of each half's 128 columns, this CTA's 64
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        ptx::tma_load_3d(dst + kRowsBytes + h * 64 * kRowBytes, tmap_w, full, kb * kRowBytes,
+                                         static_cast<int32_t>(tile.n0) + h * 128 + static_cast<int32_t>(rank) * 64, tile.expert);
+                }
             }
             __syncwarp();
             st.next(stages);
@@ -262,19 +315,19 @@ __device__ __forceinline__ void run_producer(const CUtensorMap *tmap_t, const CU
     // first) in the one before.
     if (elect_one())
         for (uint32_t s = 0; s < stages; ++s) {
-            drain_wait(ptx::smem_addr(&ctrl->full[s]), s < st.slot ? st.phase : st.phase ^ 1u);
-            if (ok) ok = drain_wait(ptx::smem_addr(&ctrl->empty[s]), s < st.slot ? st.phase : st.phase ^ 1u);
+            role_drain(ptx::smem_addr(&ctrl->full[s]), s < st.slot ? st.phase : st.phase ^ 1u);
+            if (ok) ok = role_drain(ptx::smem_addr(&ctrl->empty[s]), s < st.slot ? st.phase : st.phase ^ 1u);
         }
     __syncwarp();
 }
 
 // The other CTA of a pair: each stage that has landed here is the leader's to use.
 template <typename S>
-__device__ __forceinline__ void run_forwarder(const Params &p, const F8Table &table, Ctrl *ctrl, int lane, WaitCtl *wc)
+__device__ __forceinline__ void run_forwarder(const Params &p, const F8Table &table, Ctrl *ctrl, int lane, uint32_t wc)
 {
     Ring st;
     for (uint32_t n = schedule<S>(p, table).blocks(); n > 0; --n) {
-        if (!warp_wait<1>(ptx::smem_addr(&ctrl->full[st.slot]), st.phase, wc)) return;
+        if (!role_wait<1>(ptx::smem_addr(&ctrl->full[st.slot]), st.phase, wc)) return;
         if (lane == 0) arrive_remote(ptx::mapa(ptx::smem_addr(&ctrl->peer_full[st.slot]), 0));
         __syncwarp();
         st.next(static_cast<uint32_t>(p.stages));
@@ -283,7 +336,7 @@ __device__ __forceinline__ void run_forwarder(const Params &p, const F8Table &ta
 
 template <typename S>
 __device__ __forceinline__ void run_mma(const Params &p, const F8Table &table, uint32_t ring, Ctrl *ctrl, uint32_t tmem_base,
-                                        WaitCtl *wc)
+                                        uint32_t wc)
 {
     tmem_base = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);  // a uniform value for the compiler
     // descriptors of the first stage; a stage on is kStageBytes / 16, an MMA's K step 2, in
@@ -293,22 +346,31 @@ __device__ __forceinline__ void run_mma(const Params &p, const F8Table &table, u
     const uint32_t idesc = p.idesc;
     Ring st, acc;
     // test hook: wait on a barrier nothing arrives at, so the wait runs out
-    bool ok = !p.inject_stall || warp_wait<1>(ptx::smem_addr(&ctrl->never), 0, wc);
+    bool ok = !p.inject_stall || role_wait<1>(ptx::smem_addr(&ctrl->never), 0, wc);
     for (uint32_t n = schedule<S>(p, table).blocks(); ok && n > 0; --n) {
-        ok = warp_wait<S::kCtas>(ptx::smem_addr(&ctrl->acc_empty[acc.slot]), acc.phase ^ 1u, wc) &&
-             warp_wait<1>(ptx::smem_addr(&ctrl->full[st.slot]), st.phase, wc) &&
-             (S::kCtas == 1 || warp_wait<2>(ptx::smem_addr(&ctrl->peer_full[st.slot]), st.phase, wc));
-        if (!ok) break;
-        ptx::tc_fence_after();
-        if (elect_one()) {
-            const uint32_t d = tmem_base + acc.slot * S::kBn;
-            const uint64_t a = row_desc + st.slot * (S::kStageBytes >> 4), b = col_desc + st.slot * (S::kStageBytes >> 4);
+        // (one look at all the barriers costs what one at a single one does)
+        bool there = test(ptx::smem_addr(&ctrl->full[st.slot]), st.phase);
+        if (S::kCtas == 2) there = there & test(ptx::smem_addr(&ctrl->peer_full[st.slot]), st.phase);
+        ok = __all_sync(0xFFFFFFFFu, there) ||
+             (role_wait<1>(ptx::smem_addr(&ctrl->full[st.slot]), st.phase, wc) &&
+              (S::kCtas == 1 || role_wait<2>(ptx::smem_addr(&ctrl->peer_full[st.slot]), st.phase, wc)));
+        const uint64_t a = row_desc + st.slot * (S::kStageBytes >> 4);
 #pragma unroll
-            for (int k = 0; k < kRowBytes / 32; ++k) umma_f8<S::kCtas>(d, a + k * 2, b + k * 2, idesc, k == 0 ? 0u : 1u);
-            commit_all<S::kCtas>(ptx::smem_addr(&ctrl->empty[st.slot]));
-            commit_all<S::kCtas>(ptx::smem_addr(&ctrl->acc_full[acc.slot]));
+        for (uint32_t h = 0; h < S::kHalves; ++h) {
+            if (ok) ok = role_wait<S::kCtas>(ptx::smem_addr(&ctrl->acc_empty[h * S::kAccs + acc.slot]), acc.phase ^ 1u, wc);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            if (elect_one()) {
+                const uint32_t d = tmem_base + acc.slot * S::kBn + h * (S::kBn / 2);
+                const uint64_t b = col_desc + (st.slot * S::kStageBytes + h * (S::kBn / S::kCtas / 2) * kRowBytes) / 16;
+#pragma unroll
+                for (int k = 0; k < kRowBytes / 32; ++k) umma_f8<S::kCtas>(d, a + k * 2, b + k * 2, idesc, k == 0 ? 0u : 1u);
+                if (h == S::kHalves - 1) commit_all<S::kCtas>(ptx::smem_addr(&ctrl->empty[st.slot]));
+                commit_all<S::kCtas>(ptx::smem_addr(&ctrl->acc_full[h * S::kAccs + acc.slot]));
+            }
+            __syncwarp();
         }
-        __syncwarp();
+        if (!ok) break;
         st.next(static_cast<uint32_t>(p.stages));
         acc.next(S::kAccs);
     }
@@ -319,20 +381,24 @@ __device__ __forceinline__ void run_mma(const Params &p, const F8Table &table, u
             ptx::umma_commit_pair_multicast(ptx::smem_addr(&ctrl->mma_done), 0x1);
         else
             ptx::umma_commit(ptx::smem_addr(&ctrl->mma_done));
-        drain_wait(ptx::smem_addr(&ctrl->mma_done), 0);
+        role_drain(ptx::smem_addr(&ctrl->mma_done), 0);
     }
     __syncwarp();
 }
 
-// A block's scales: the CTA's 128 rows', then the tile's columns' (kUniform: one for each
-// group of columns).  Rows past the operand take its last one's, for sums that are not
-// stored.
+// The scales of kSpan blocks at a time: the CTA's 128 rows', then the tile's columns'
+// (kUniform: one for each group of columns).  Rows past the operand take its last one's,
+// for sums that are not stored.
 template <typename S>
 __device__ __forceinline__ void run_scales(const Params &p, const F8Table &table, uint32_t scales, Ctrl *ctrl, uint32_t rank,
-                                           int lane, WaitCtl *wc)
+                                           int lane, uint32_t wc)
 {
     constexpr int kR = kRows / 32, kC = S::kUniform ? 1 : (S::kBn + 31) / 32;
     const Sched sc = schedule<S>(p, table);
+    const F8Operand &ro = S::kSwap ? p.c.b : p.c.a, &co = S::kSwap ? p.c.a : p.c.b;
+    // a row's scales of a span as one 16-byte word, where they lie so
+    const bool words = ro.s_blk == 1 && ro.s_row % 4 == 0 && sc.kb0 % 4 == 0 && p.c.sb_stride % 4 == 0 &&
+                       (reinterpret_cast<uintptr_t>(ro.scale) & 15u) == 0;
     Ring st;
     bool ok = true;
     for (uint32_t t = sc.t0; ok && t < sc.tiles; t += sc.dt) {
@@ -348,16 +414,28 @@ __device__ __forceinline__ void run_scales(const Params &p, const F8Table &table
         for (int i = 0; i < kR; ++i) row[i] = place(!S::kSwap, rank * kRows + i * 32 + lane);
 #pragma unroll
         for (int i = 0; i < kC; ++i) col[i] = place(S::kSwap, S::kUniform ? (lane & 1) * S::kWgCols : i * 32 + lane);
-        const int64_t row_blk = (S::kSwap ? p.c.b : p.c.a).s_blk, col_blk = (S::kSwap ? p.c.a : p.c.b).s_blk;
-        for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
-            ok = warp_wait<1>(ptx::smem_addr(&ctrl->sc_empty[st.slot]), st.phase ^ 1u, wc);
+        for (int kb = sc.kb0; kb < sc.kb1; kb += kSpan) {
+            ok = role_wait<1>(ptx::smem_addr(&ctrl->sc_empty[st.slot]), st.phase ^ 1u, wc);
             if (!ok) break;
-            const uint32_t dst = scales + st.slot * (kRows + S::kScaleCols) * 4;
+            const uint32_t dst = scales + st.slot * S::kSlotBytes, cols = dst + kRows * kSpan * 4;
+            const int n = min(kSpan, sc.kb1 - kb);
+            if (words && n == kSpan) {
 #pragma unroll
-            for (int i = 0; i < kR; ++i) copy_async4(dst + (i * 32 + lane) * 4, row[i] + kb * row_blk);
+                for (int i = 0; i < kR; ++i) copy_async16(dst + (i * 32 + lane) * 16, row[i] + kb);
+            } else {
+                for (int j = 0; j < n; ++j)
 #pragma unroll
-            for (int i = 0; i < kC; ++i)
-                if (i * 32 + lane < (S::kUniform ? 2 : S::kBn)) copy_async4(dst + (kRows + i * 32 + lane) * 4, col[i] + kb * col_blk);
+                    for (int i = 0; i < kR; ++i) copy_async4(dst + ((i * 32 + lane) * kSpan + j) * 4, row[i] + (kb + j) * ro.s_blk);
+            }
+            for (int j = 0; j < n; ++j) {
+                if constexpr (S::kUniform) {
+                    if (lane < 2) copy_async4(cols + (lane * kSpan + j) * 4, col[0] + (kb + j) * co.s_blk);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kC; ++i)
+                        if (i * 32 + lane < S::kBn) copy_async4(cols + (j * S::kBn + i * 32 + lane) * 4, col[i] + (kb + j) * co.s_blk);
+                }
+            }
             ptx::cp_async_mbar_arrive_noinc(ptx::smem_addr(&ctrl->sc_full[st.slot]));
             st.next(kScaleSlots);
         }
@@ -377,18 +455,37 @@ struct Epi {
 // The sums of one tile (or of this CTA's blocks of it), two columns a word.
 template <typename S>
 __device__ __forceinline__ bool sum_blocks(const Params &p, Ctrl *ctrl, uint32_t scales, uint32_t taddr, int row, int group,
-                                           int blocks, int lane, Epi &e, uint64_t (&sum)[S::kWgCols / 2], WaitCtl *wc)
+                                           int blocks, int lane, Epi &e, uint64_t (&sum)[S::kWgCols / 2], uint32_t wc)
 {
-    constexpr int kChunk = S::kWgCols == 64 ? 32 : S::kWgCols < 16 ? S::kWgCols : 16, kChunks = S::kWgCols / kChunk;
+    constexpr int kChunk = S::kWgCols < 32 ? S::kWgCols : 32, kChunks = S::kWgCols / kChunk;
 #pragma unroll
     for (int i = 0; i < S::kWgCols / 2; ++i) sum[i] = 0ull;
+    float4 r4 = {};
+    uint32_t cols = 0;
+    auto acc_bar = [&]() { return ptx::smem_addr(&ctrl->acc_full[(S::kHalves == 2 ? group * S::kAccs : 0) + e.acc.slot]); };
+    bool ready = false;  // the block's accumulator, as a look ahead saw it
     for (int kb = 0; kb < blocks; ++kb) {
-        if (!epi_wait<1>(ptx::smem_addr(&ctrl->sc_full[e.sc.slot]), e.sc.phase, wc)) return false;
-        const uint32_t sc = scales + e.sc.slot * (kRows + S::kScaleCols) * 4;
-        float r = ptx::ld_shared_f32(sc + row * 4);
-        if constexpr (S::kUniform) r *= ptx::ld_shared_f32(sc + (kRows + group) * 4);
+        const int j = kb % kSpan;
+        if (j == 0) {
+            if (!role_wait<1>(ptx::smem_addr(&ctrl->sc_full[e.sc.slot]), e.sc.phase, wc)) return false;
+            const uint32_t slot = scales + e.sc.slot * S::kSlotBytes;
+            cols = slot + kRows * kSpan * 4;
+            r4 = ptx::ld_shared_v4f(slot + row * (kSpan * 4));
+            if constexpr (S::kUniform) {
+                const float4 c4 = ptx::ld_shared_v4f(cols + group * (kSpan * 4));
+                r4.x *= c4.x;
+                r4.y *= c4.y;
+                r4.z *= c4.z;
+                r4.w *= c4.w;
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctrl->sc_empty[e.sc.slot]));
+                e.sc.next(kScaleSlots);
+            }
+        }
+        const float r = j == 0 ? r4.x : j == 1 ? r4.y : j == 2 ? r4.z : r4.w;
         const uint64_t r2 = pack2(r, r);
-        if (!epi_wait<S::kCtas>(ptx::smem_addr(&ctrl->acc_full[e.acc.slot]), e.acc.phase, wc)) return false;
+        const uint32_t slot = (S::kHalves == 2 ? group * S::kAccs : 0) + e.acc.slot;
+        if (!__all_sync(0xFFFFFFFFu, ready) && !role_wait<1>(acc_bar(), e.acc.phase, wc)) return false;
         ptx::tc_fence_after();
         const uint32_t src = taddr + e.acc.slot * S::kBn;
         uint32_t d[kChunks > 1 ? 2 : 1][kChunk];
@@ -405,17 +502,20 @@ __device__ __forceinline__ bool sum_blocks(const Params &p, Ctrl *ctrl, uint32_t
                 // (an arrival that nothing waits for could reach a CTA that has left)
                 if (lane == 0 && e.left > S::kAccs) {
                     if constexpr (S::kCtas == 2)
-                        arrive_remote(ptx::mapa(ptx::smem_addr(&ctrl->acc_empty[e.acc.slot]), 0));
+                        arrive_remote(ptx::mapa(ptx::smem_addr(&ctrl->acc_empty[slot]), 0));
                     else
-                        ptx::mbar_arrive(ptx::smem_addr(&ctrl->acc_empty[e.acc.slot]));
+                        ptx::mbar_arrive(ptx::smem_addr(&ctrl->acc_empty[slot]));
                 }
+                --e.left;
+                e.acc.next(S::kAccs);
+                ready = test(acc_bar(), e.acc.phase);  // (its latency lies beside the last sums)
             }
 #pragma unroll
             for (int i = 0; i < kChunk; i += 4) {
                 uint64_t x = pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
                 uint64_t y = pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
                 if constexpr (!S::kUniform) {
-                    const float4 s = ptx::ld_shared_v4f(sc + (kRows + group * S::kWgCols + c * kChunk + i) * 4);
+                    const float4 s = ptx::ld_shared_v4f(cols + (j * S::kBn + group * S::kWgCols + c * kChunk + i) * 4);
                     x = mul2(x, pack2(s.x, s.y));
                     y = mul2(y, pack2(s.z, s.w));
                 }
@@ -424,11 +524,11 @@ __device__ __forceinline__ bool sum_blocks(const Params &p, Ctrl *ctrl, uint32_t
                 sum[at + 1] = fma2(y, r2, sum[at + 1]);
             }
         }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctrl->sc_empty[e.sc.slot]));
-        --e.left;
-        e.acc.next(S::kAccs);
-        e.sc.next(kScaleSlots);
+        if (!S::kUniform && (j == kSpan - 1 || kb + 1 == blocks)) {
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctrl->sc_empty[e.sc.slot]));
+            e.sc.next(kScaleSlots);
+        }
     }
     return true;
 }
@@ -445,18 +545,55 @@ __device__ __forceinline__ uint32_t pack_bits(float a, float b)
     }
 }
 
+// Rows = tokens: the bias and the old C added to this lane's sums, if the call has them.  (Apart
+// from the stores, whose code, fetched anew for each tile, is a tenth of this.)
+template <typename T, int kCols>
+__device__ __forceinline__ void add_bias_and_old(const Params &p, uint64_t (&sum)[kCols / 2], int64_t row, int64_t row_end, int64_t col0)
+{
+    constexpr int kPer = 16 / sizeof(T);  // values of a 16-byte word
+    const float beta = p.c.beta;
+    if (!p.c.bias && beta == 0.f) return;
+    const T *const C = static_cast<const T *>(p.c.C) + row * p.c.ldc;
+    const bool words = (reinterpret_cast<uintptr_t>(p.c.C) & 15u) == 0 && p.c.ldc % kPer == 0;
+#pragma unroll
+    for (int w = 0; w < kCols; w += kPer) {
+        const int64_t c = col0 + w;
+        float v[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; i += 2) unpack2(sum[(w + i) / 2], v[i], v[i + 1]);
+        if (p.c.bias) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (c + i < p.c.N) v[i] += p.c.bias[c + i];
+        }
+        if (beta != 0.f && row < row_end) {
+            if (words && c + kPer <= p.c.N) {
+                const uint4 q = *reinterpret_cast<const uint4 *>(C + c);
+                const T *o = reinterpret_cast<const T *>(&q);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) v[i] = fmaf(beta, to_f32(o[i]), v[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    if (c + i < p.c.N) v[i] = fmaf(beta, to_f32(C[c + i]), v[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; i += 2) sum[(w + i) / 2] = pack2(v[i], v[i + 1]);
+    }
+}
+
 // Rows = tokens: a warp's 32 rows from `row0` (up to row_end) x kCols columns from col0.  Boxes
 // of 128 bytes of columns are staged in shared memory (128-byte swizzle: word w of row r at
 // w ^ (r mod 8)) and stored by TMA, or, where the box holds rows that are not the expert's
 // or TMA cannot describe C, word by word, 8 lanes a row.
 template <typename T, int kCols>
-__device__ __forceinline__ void store_tokens(const Params &p, const CUtensorMap *tmap_o, const uint64_t (&sum)[kCols / 2],
-                                             int64_t row0, int64_t row_end, int64_t col0, uint32_t box, int lane, uint32_t &nbox)
+__device__ __forceinline__ void store_tokens(const Params &p, const CUtensorMap *tmap_o, uint64_t (&sum)[kCols / 2], int64_t row0,
+                                             int64_t row_end, int64_t col0, uint32_t box, int lane, uint32_t &nbox)
 {
     constexpr int kPer = 16 / sizeof(T), kBoxCols = 128 / sizeof(T);  // values of a word, of a row of the box
     if (row0 >= row_end) return;  // warp-uniform
-    const int64_t row = row0 + lane;
-    const float beta = p.c.beta;
+    add_bias_and_old<T, kCols>(p, sum, row0 + lane, row_end, col0);
     T *const C = static_cast<T *>(p.c.C);
     const bool whole = p.tma_store && (!p.c.offsets || row0 + 32 <= row_end);
     const bool words = (reinterpret_cast<uintptr_t>(C) & 15u) == 0 && p.c.ldc % kPer == 0;
@@ -477,25 +614,6 @@ __device__ __forceinline__ void store_tokens(const Params &p, const CUtensorMap 
             float v[kPer];
 #pragma unroll
             for (int i = 0; i < kPer; i += 2) unpack2(sum[(b * kBoxCols + w * kPer + i) / 2], v[i], v[i + 1]);
-            const int64_t cw = c + w * kPer;
-            if (p.c.bias) {
-#pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    if (cw + i < p.c.N) v[i] += p.c.bias[cw + i];
-            }
-            if (beta != 0.f && row < row_end) {
-                const T *old = C + row * p.c.ldc + cw;
-                if (words && cw + kPer <= p.c.N) {
-                    const uint4 q = *reinterpret_cast<const uint4 *>(old);
-                    const T *o = reinterpret_cast<const T *>(&q);
-#pragma unroll
-                    for (int i = 0; i < kPer; ++i) v[i] = fmaf(beta, to_f32(o[i]), v[i]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kPer; ++i)
-                        if (cw + i < p.c.N) v[i] = fmaf(beta, to_f32(old[i]), v[i]);
-                }
-            }
             uint4 q;
             if constexpr (sizeof(T) == 2)
                 q = make_uint4(pack_bits<T>(v[0], v[1]), pack_bits<T>(v[2], v[3]), pack_bits<T>(v[4], v[5]), pack_bits<T>(v[6], v[7]));
@@ -579,13 +697,13 @@ __device__ __forceinline__ uint32_t recv_offset(uint32_t groups, uint32_t slot, 
 
 template <typename S>
 __device__ __forceinline__ void join_split(const Params &p, const F8Tile &tile, uint32_t ring, int row, int group, int64_t n,
-                                           const uint64_t (&sum)[S::kWgCols / 2], WaitCtl *wc)
+                                           const uint64_t (&sum)[S::kWgCols / 2], uint32_t wc)
 {
     constexpr uint32_t kGroups = S::kBn / 8, kMine = S::kWgCols / 8;  // of the tile, of this thread
     const uint32_t N = static_cast<uint32_t>(p.splitk), rank = ptx::cluster_ctarank();
     const uint32_t bytes = static_cast<uint32_t>(p.stages) * S::kStageBytes;
     ptx::cluster_sync();  // every CTA's sums are complete: the rings are idle
-    const bool stop = __any_sync(0xFFFFFFFFu, aborted(wc));
+    const bool stop = __any_sync(0xFFFFFFFFu, stopped(wc));
     if (!stop) {
 #pragma unroll
         for (uint32_t i = 0; i < kMine; ++i) {
@@ -632,7 +750,7 @@ __device__ __forceinline__ void join_split(const Params &p, const F8Tile &tile, 
 template <typename S>
 __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap *tmap_o, const F8Table &table, uint32_t ring,
                                              uint32_t box, uint32_t scales, Ctrl *ctrl, uint32_t tmem_base, uint32_t rank,
-                                             int warp, int lane, WaitCtl *wc)
+                                             int warp, int lane, uint32_t wc)
 {
     const Sched sc = schedule<S>(p, table);
     const int quarter = warp & 3, group = (warp - 4) >> 2, row = quarter * 32 + lane;
@@ -648,8 +766,8 @@ __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap 
         return;
     }
     for (uint32_t t = sc.t0; t < sc.tiles; t += sc.dt) {
-        const F8Tile tile = tile_at<S>(p, table, t);
         if (!sum_blocks<S>(p, ctrl, scales, taddr, row, group, sc.kb1 - sc.kb0, lane, e, sum, wc)) break;
+        const F8Tile tile = tile_at<S>(p, table, t);
         if constexpr (S::kSwap) {
             store_channels_any<S, S::kWgCols>(p, sum, tile.n0 + rank * kRows + row, tile.t0 + group * S::kWgCols, tile.t_end);
         } else {
@@ -689,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, S::kPerSm)
         }
         for (int a = 0; a < kMaxAccs; ++a) {
             ptx::mbar_init(ptx::smem_addr(&ctrl->acc_full[a]), 1);
-            ptx::mbar_init(ptx::smem_addr(&ctrl->acc_empty[a]), kEpiWarps * S::kCtas);
+            ptx::mbar_init(ptx::smem_addr(&ctrl->acc_empty[a]), kEpiWarps / S::kHalves * S::kCtas);
         }
         for (int s = 0; s < kScaleSlots; ++s) {
             ptx::mbar_init(ptx::smem_addr(&ctrl->sc_full[s]), 32);
@@ -697,8 +815,8 @@ __global__ void __launch_bounds__(kThreads, S::kPerSm)
         }
         ptx::mbar_init(ptx::smem_addr(&ctrl->mma_done), 1);
         ptx::mbar_init(ptx::smem_addr(&ctrl->never), 1);
-        ctrl->wait.abort = 0;
-        ctrl->wait.limit_ns = p.wait_limit_ns;
+        ctrl->stop = 0u;
+        ctrl->limit_us = p.wait_limit_us;
         ptx::fence_mbarrier_init();
     } else if (warp == 1) {
         if constexpr (S::kCtas == 2) {
@@ -724,9 +842,10 @@ __global__ void __launch_bounds__(kThreads, S::kPerSm)
     if constexpr (S::kCtas == 2) cluster_meet();
     ptx::tc_fence_after();
     const uint32_t tmem_base = ctrl->tmem_base;
-    WaitCtl *wc = &ctrl->wait;
+    const uint32_t wc = ptx::smem_addr(&ctrl->stop);
 
     if (warp < 4) {
+        if constexpr (S::kMoveRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 0) {
             run_producer<S>(&tmap_t, &tmap_w, p, table, ring, ctrl, rank, wc);
         } else if (warp == 1) {
@@ -743,6 +862,7 @@ __global__ void __launch_bounds__(kThreads, S::kPerSm)
             ptx::cluster_sync();
         }
     } else {
+        if constexpr (S::kMoveRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         run_epilogue<S>(p, &tmap_o, table, ring, box, scales, ctrl, tmem_base, rank, warp, lane, wc);
     }
 
@@ -752,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, S::kPerSm)
     if constexpr (S::kCtas == 2) {
         // after an abort, arrivals on the leader's barriers that nothing has waited for may be
         // under way: they come before this CTA's part in the meeting
-        if (__any_sync(0xFFFFFFFFu, aborted(wc))) fence_cluster();
+        if (__any_sync(0xFFFFFFFFu, stopped(wc))) fence_cluster();
         cluster_meet();  // no CTA leaves while the other may still signal or read it
     }
     if (warp == 1) {
@@ -835,7 +955,7 @@ bool launch(const F8Params &c, int splitk, cudaStream_t stream)
     const int fit = capacity<S>(cluster);
     const int smem = set_rings<S>(p);
     if (fit < 1 || p.stages < 3 || (p.splitk > 1 && tiles > fit)) return false;
-    constexpr int kTokBox = S::kSwap ? S::kBn / S::kCtas : kRows, kChanBox = S::kSwap ? kRows : S::kBn / S::kCtas;
+    constexpr int kTokBox = S::kSwap ? S::kBn / S::kCtas : kRows, kChanBox = S::kSwap ? kRows : S::kBn / S::kCtas / S::kHalves;
     const uint64_t k = static_cast<uint64_t>(c.K), m = static_cast<uint64_t>(c.M), n = static_cast<uint64_t>(c.N);
     CUtensorMap mt{}, mw{}, mo{};
     if (!encode_tiled_3d(&mt, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.a.p, {k, m, 1}, {static_cast<uint64_t>(c.a.ld), m * c.a.ld},
@@ -853,13 +973,13 @@ bool launch(const F8Params &c, int splitk, cudaStream_t stream)
                       encode_tiled_2d(&mo, dt, c.C, n, m, static_cast<uint64_t>(c.ldc) * e, static_cast<uint32_t>(128 / e), 32,
                                       CU_TENSOR_MAP_SWIZZLE_128B);
     }
-    // D f32; the types of the rows' and the columns' operand; both K-major; N = kBn, M = 128 rows a CTA
+    // D f32; the types of the rows' and the columns' operand; both K-major; N = kBn (or a half), M = 128 rows a CTA
     const uint32_t rows_type = static_cast<uint32_t>((S::kSwap ? c.b : c.a).type), cols_type = static_cast<uint32_t>((S::kSwap ? c.a : c.b).type);
-    p.idesc = (1u << 4) | (rows_type << 7) | (cols_type << 10) | (static_cast<uint32_t>(S::kBn >> 3) << 17) |
+    p.idesc = (1u << 4) | (rows_type << 7) | (cols_type << 10) | (static_cast<uint32_t>(S::kBn / S::kHalves >> 3) << 17) |
               (static_cast<uint32_t>(S::kTileRows >> 4) << 24);
     const uint64_t stall = take_injected_stall();
     p.inject_stall = stall ? 1 : 0;
-    p.wait_limit_ns = stall ? stall : kWaitLimitNs;
+    p.wait_limit_us = static_cast<uint32_t>(std::min<uint64_t>((stall ? stall : kWaitLimitNs) >> 10, UINT32_MAX / 2));
     if (launch_chained(f8_umma_kernel<S>, static_cast<unsigned>(cluster * std::min<int64_t>(tiles, fit)), kThreads, smem, stream,
                        static_cast<unsigned>(cluster), mt, mw, mo, p) != cudaSuccess) {
         cudaGetLastError();
