@@ -54,8 +54,9 @@ constexpr int kRowBytes = kF8Block;            // a block of K, one byte a value
 constexpr int kRowsBytes = kRows * kRowBytes;
 constexpr int kMaxStages = 12;
 constexpr int kMaxAccs = 8;
-constexpr int kSpan = 4;                        // blocks whose scales go together: a wait costs ~150 clocks
+constexpr int kSpan = 8;                        // blocks whose scales go together (a wait costs ~100 clocks)
 constexpr int kScaleSlots = 2;
+constexpr int kRowPitch = kSpan + 4;            // floats: 16-byte words, the rows of eight lanes on distinct banks
 constexpr int kBoxBytes = 4096;                // epilogue staging: 32 rows x 128 bytes
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (4 + kEpiWarps);
@@ -104,7 +105,7 @@ struct Shape {
     static constexpr int kAccs = 512 / kBn < kMaxAccs ? 512 / kBn : kMaxAccs;  // of either half
     static constexpr int kTmemCols = kAccs * kBn;
     // a slot of scales: [row][block], then [group][block] or [block][column]
-    static constexpr int kSlotBytes = kSpan * (kRows + (kUniform ? 2 : kBn)) * 4;
+    static constexpr int kSlotBytes = (kRowPitch * kRows + kSpan * (kUniform ? 2 : kBn)) * 4;
     static constexpr int kScaleBytes = kScaleSlots * kSlotBytes;
     static constexpr int kPerSm = kBn <= 32 ? 2 : 1;            // CTAs an SM
     // sums of 128 columns and 64 more on their way do not fit the 168 registers a thread that
@@ -167,6 +168,24 @@ __device__ __forceinline__ void copy_async4(uint32_t dst, const float *src)
 __device__ __forceinline__ void copy_async16(uint32_t dst, const float *src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// One lane's arrival, without a branch around it.
+__device__ __forceinline__ void arrive_if(bool yes, uint32_t bar)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+                 "r"(static_cast<uint32_t>(yes))
+                 : "memory");
+}
+
+// The same on the barrier of a cluster's CTA (as arrive_remote).
+__device__ __forceinline__ void arrive_remote_if(bool yes, uint32_t cluster_addr)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t@q mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];\n\t}" ::"r"(
+            cluster_addr),
+        "r"(static_cast<uint32_t>(yes))
+        : "memory");
 }
 
 // Whether the phase of this parity is over, without waiting.
@@ -347,17 +366,20 @@ __device__ __forceinline__ void run_mma(const Params &p, const F8Table &table, u
     Ring st, acc;
     // test hook: wait on a barrier nothing arrives at, so the wait runs out
     bool ok = !p.inject_stall || role_wait<1>(ptx::smem_addr(&ctrl->never), 0, wc);
+    const uint32_t full = ptx::smem_addr(ctrl->full), peer = ptx::smem_addr(ctrl->peer_full), empty = ptx::smem_addr(ctrl->empty);
+    const uint32_t acc_full = ptx::smem_addr(ctrl->acc_full), acc_empty = ptx::smem_addr(ctrl->acc_empty);
     for (uint32_t n = schedule<S>(p, table).blocks(); ok && n > 0; --n) {
-        // (one look at all the barriers costs what one at a single one does)
-        bool there = test(ptx::smem_addr(&ctrl->full[st.slot]), st.phase);
-        if (S::kCtas == 2) there = there & test(ptx::smem_addr(&ctrl->peer_full[st.slot]), st.phase);
-        ok = __all_sync(0xFFFFFFFFu, there) ||
-             (role_wait<1>(ptx::smem_addr(&ctrl->full[st.slot]), st.phase, wc) &&
-              (S::kCtas == 1 || role_wait<2>(ptx::smem_addr(&ctrl->peer_full[st.slot]), st.phase, wc)));
+        // a look at all the barriers of the block costs what one at a single one does
+        bool there[4] = {test(full + st.slot * 8, st.phase), true, test(acc_empty + acc.slot * 8, acc.phase ^ 1u), true};
+        if (S::kCtas == 2) there[1] = test(peer + st.slot * 8, st.phase);
+        if (S::kHalves == 2) there[3] = test(acc_empty + (S::kAccs + acc.slot) * 8, acc.phase ^ 1u);
+        ok = (__all_sync(0xFFFFFFFFu, there[0]) || role_wait<1>(full + st.slot * 8, st.phase, wc)) &&
+             (__all_sync(0xFFFFFFFFu, there[1]) || role_wait<2>(peer + st.slot * 8, st.phase, wc));
         const uint64_t a = row_desc + st.slot * (S::kStageBytes >> 4);
 #pragma unroll
         for (uint32_t h = 0; h < S::kHalves; ++h) {
-            if (ok) ok = role_wait<S::kCtas>(ptx::smem_addr(&ctrl->acc_empty[h * S::kAccs + acc.slot]), acc.phase ^ 1u, wc);
+            const uint32_t at = (h * S::kAccs + acc.slot) * 8;
+            if (ok) ok = __all_sync(0xFFFFFFFFu, there[2 + h]) || role_wait<S::kCtas>(acc_empty + at, acc.phase ^ 1u, wc);
             if (!ok) break;
             ptx::tc_fence_after();
             if (elect_one()) {
@@ -365,8 +387,8 @@ __device__ __forceinline__ void run_mma(const Params &p, const F8Table &table, u
                 const uint64_t b = col_desc + (st.slot * S::kStageBytes + h * (S::kBn / S::kCtas / 2) * kRowBytes) / 16;
 #pragma unroll
                 for (int k = 0; k < kRowBytes / 32; ++k) umma_f8<S::kCtas>(d, a + k * 2, b + k * 2, idesc, k == 0 ? 0u : 1u);
-                if (h == S::kHalves - 1) commit_all<S::kCtas>(ptx::smem_addr(&ctrl->empty[st.slot]));
-                commit_all<S::kCtas>(ptx::smem_addr(&ctrl->acc_full[h * S::kAccs + acc.slot]));
+                if (h == S::kHalves - 1) commit_all<S::kCtas>(empty + st.slot * 8);
+                commit_all<S::kCtas>(acc_full + at);
             }
             __syncwarp();
         }
@@ -396,7 +418,7 @@ __device__ __forceinline__ void run_scales(const Params &p, const F8Table &table
     constexpr int kR = kRows / 32, kC = S::kUniform ? 1 : (S::kBn + 31) / 32;
     const Sched sc = schedule<S>(p, table);
     const F8Operand &ro = S::kSwap ? p.c.b : p.c.a, &co = S::kSwap ? p.c.a : p.c.b;
-    // a row's scales of a span as one 16-byte word, where they lie so
+    // a row's scales of a span as 16-byte words, where they lie so
     const bool words = ro.s_blk == 1 && ro.s_row % 4 == 0 && sc.kb0 % 4 == 0 && p.c.sb_stride % 4 == 0 &&
                        (reinterpret_cast<uintptr_t>(ro.scale) & 15u) == 0;
     Ring st;
@@ -417,16 +439,20 @@ __device__ __forceinline__ void run_scales(const Params &p, const F8Table &table
         for (int kb = sc.kb0; kb < sc.kb1; kb += kSpan) {
             ok = role_wait<1>(ptx::smem_addr(&ctrl->sc_empty[st.slot]), st.phase ^ 1u, wc);
             if (!ok) break;
-            const uint32_t dst = scales + st.slot * S::kSlotBytes, cols = dst + kRows * kSpan * 4;
+            const uint32_t dst = scales + st.slot * S::kSlotBytes, cols = dst + kRows * kRowPitch * 4;
             const int n = min(kSpan, sc.kb1 - kb);
             if (words && n == kSpan) {
 #pragma unroll
-                for (int i = 0; i < kR; ++i) copy_async16(dst + (i * 32 + lane) * 16, row[i] + kb);
+                for (int i = 0; i < kR; ++i)
+#pragma unroll
+                    for (int j = 0; j < kSpan; j += 4) copy_async16(dst + ((i * 32 + lane) * kRowPitch + j) * 4, row[i] + kb + j);
             } else {
+#pragma unroll 1
                 for (int j = 0; j < n; ++j)
 #pragma unroll
-                    for (int i = 0; i < kR; ++i) copy_async4(dst + ((i * 32 + lane) * kSpan + j) * 4, row[i] + (kb + j) * ro.s_blk);
+                    for (int i = 0; i < kR; ++i) copy_async4(dst + ((i * 32 + lane) * kRowPitch + j) * 4, row[i] + (kb + j) * ro.s_blk);
             }
+#pragma unroll 1
             for (int j = 0; j < n; ++j) {
                 if constexpr (S::kUniform) {
                     if (lane < 2) copy_async4(cols + (lane * kSpan + j) * 4, col[0] + (kb + j) * co.s_blk);
@@ -452,82 +478,88 @@ struct Epi {
     uint32_t nbox;
 };
 
-// The sums of one tile (or of this CTA's blocks of it), two columns a word.
+// The sums of one tile (or of this CTA's blocks of it), two columns a word.  A look at a
+// barrier takes ~100 clocks to come back, so those of the next block are taken, and its
+// scales fetched, beside the sums of this one.
 template <typename S>
 __device__ __forceinline__ bool sum_blocks(const Params &p, Ctrl *ctrl, uint32_t scales, uint32_t taddr, int row, int group,
                                            int blocks, int lane, Epi &e, uint64_t (&sum)[S::kWgCols / 2], uint32_t wc)
 {
-    constexpr int kChunk = S::kWgCols < 32 ? S::kWgCols : 32, kChunks = S::kWgCols / kChunk;
+    constexpr int kChunk = S::kWgCols >= 128 ? 16 : S::kWgCols < 32 ? S::kWgCols : 32, kChunks = S::kWgCols / kChunk;
 #pragma unroll
     for (int i = 0; i < S::kWgCols / 2; ++i) sum[i] = 0ull;
-    float4 r4 = {};
-    uint32_t cols = 0;
-    auto acc_bar = [&]() { return ptx::smem_addr(&ctrl->acc_full[(S::kHalves == 2 ? group * S::kAccs : 0) + e.acc.slot]); };
-    bool ready = false;  // the block's accumulator, as a look ahead saw it
-    for (int kb = 0; kb < blocks; ++kb) {
-        const int j = kb % kSpan;
-        if (j == 0) {
-            if (!role_wait<1>(ptx::smem_addr(&ctrl->sc_full[e.sc.slot]), e.sc.phase, wc)) return false;
-            const uint32_t slot = scales + e.sc.slot * S::kSlotBytes;
-            cols = slot + kRows * kSpan * 4;
-            r4 = ptx::ld_shared_v4f(slot + row * (kSpan * 4));
-            if constexpr (S::kUniform) {
-                const float4 c4 = ptx::ld_shared_v4f(cols + group * (kSpan * 4));
-                r4.x *= c4.x;
-                r4.y *= c4.y;
-                r4.z *= c4.z;
-                r4.w *= c4.w;
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctrl->sc_empty[e.sc.slot]));
-                e.sc.next(kScaleSlots);
-            }
-        }
-        const float r = j == 0 ? r4.x : j == 1 ? r4.y : j == 2 ? r4.z : r4.w;
-        const uint64_t r2 = pack2(r, r);
-        const uint32_t slot = (S::kHalves == 2 ? group * S::kAccs : 0) + e.acc.slot;
-        if (!__all_sync(0xFFFFFFFFu, ready) && !role_wait<1>(acc_bar(), e.acc.phase, wc)) return false;
+    const uint32_t acc_full = ptx::smem_addr(ctrl->acc_full) + (S::kHalves == 2 ? group * S::kAccs : 0) * 8;
+    uint32_t acc_empty = ptx::smem_addr(ctrl->acc_empty) + (S::kHalves == 2 ? group * S::kAccs : 0) * 8;
+    if constexpr (S::kCtas == 2) acc_empty = ptx::mapa(acc_empty, 0);
+    const uint32_t sc_full = ptx::smem_addr(ctrl->sc_full), sc_empty = ptx::smem_addr(ctrl->sc_empty);
+    if (!role_wait<1>(sc_full + e.sc.slot * 8, e.sc.phase, wc)) return false;
+    uint32_t slot = scales + e.sc.slot * S::kSlotBytes;  // of this block's scales
+    float r = ptx::ld_shared_f32(slot + row * (kRowPitch * 4)), c = 1.f;
+    if constexpr (S::kUniform) c = ptx::ld_shared_f32(slot + kRows * kRowPitch * 4 + group * (kSpan * 4));
+    bool ready = false;  // the block's accumulator, as the look ahead saw it
+    int j = 0;           // the block's place in its span
+    for (int left = blocks; left > 0; --left) {
+        if (!__all_sync(0xFFFFFFFFu, ready) && !role_wait<1>(acc_full + e.acc.slot * 8, e.acc.phase, wc)) return false;
         ptx::tc_fence_after();
-        const uint32_t src = taddr + e.acc.slot * S::kBn;
+        const uint32_t src = taddr + e.acc.slot * S::kBn, release = acc_empty + e.acc.slot * 8;
         uint32_t d[kChunks > 1 ? 2 : 1][kChunk];
         tmem_load<kChunk>(src, d[0]);
+        e.acc.next(S::kAccs);
+        ready = test(acc_full + e.acc.slot * 8, e.acc.phase);
+        const float rc = S::kUniform ? r * c : r;
+        const uint64_t r2 = pack2(rc, rc);
+        const uint32_t cols = slot + (kRows * kRowPitch + j * S::kBn + group * S::kWgCols) * 4;
+        const bool last = j == kSpan - 1 || left == 1;  // of its span
+        bool more = false;
+        if (!last) {
+            r = ptx::ld_shared_f32(slot + (row * kRowPitch + j + 1) * 4);
+            if constexpr (S::kUniform) c = ptx::ld_shared_f32(slot + (kRows * kRowPitch + group * kSpan + j + 1) * 4);
+        } else if (left > 1) {
+            const uint32_t n = e.sc.slot + 1 == kScaleSlots ? 0u : e.sc.slot + 1;
+            more = test(sc_full + n * 8, e.sc.phase ^ (n == 0 ? 1u : 0u));
+        }
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            uint32_t(&v)[kChunk] = d[c & 1];
-            tmem_wait<kChunk>(v);
-            if (c + 1 < kChunks) {
-                tmem_load<kChunk>(src + (c + 1) * kChunk, d[(c + 1) & 1]);
+        for (int k = 0; k < kChunks; ++k) {
+            uint32_t(&v)[kChunk] = d[k & 1];
+            tmem_wait<kChunk>(v);  // (of the whole warp)
+            if (k + 1 < kChunks) {
+                tmem_load<kChunk>(src + (k + 1) * kChunk, d[(k + 1) & 1]);
             } else {
                 ptx::tc_fence_before();
-                __syncwarp();
                 // (an arrival that nothing waits for could reach a CTA that has left)
-                if (lane == 0 && e.left > S::kAccs) {
-                    if constexpr (S::kCtas == 2)
-                        arrive_remote(ptx::mapa(ptx::smem_addr(&ctrl->acc_empty[slot]), 0));
-                    else
-                        ptx::mbar_arrive(ptx::smem_addr(&ctrl->acc_empty[slot]));
-                }
+                const bool yes = lane == 0 && e.left > S::kAccs;
+                if constexpr (S::kCtas == 2)
+                    arrive_remote_if(yes, release);
+                else
+                    arrive_if(yes, release);
                 --e.left;
-                e.acc.next(S::kAccs);
-                ready = test(acc_bar(), e.acc.phase);  // (its latency lies beside the last sums)
             }
 #pragma unroll
             for (int i = 0; i < kChunk; i += 4) {
                 uint64_t x = pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
                 uint64_t y = pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
                 if constexpr (!S::kUniform) {
-                    const float4 s = ptx::ld_shared_v4f(cols + (j * S::kBn + group * S::kWgCols + c * kChunk + i) * 4);
-                    x = mul2(x, pack2(s.x, s.y));
-                    y = mul2(y, pack2(s.z, s.w));
+                    const float4 f = ptx::ld_shared_v4f(cols + (k * kChunk + i) * 4);
+                    x = mul2(x, pack2(f.x, f.y));
+                    y = mul2(y, pack2(f.z, f.w));
                 }
-                const int at = (c * kChunk + i) / 2;
+                const int at = (k * kChunk + i) / 2;
                 sum[at] = fma2(x, r2, sum[at]);
                 sum[at + 1] = fma2(y, r2, sum[at + 1]);
             }
         }
-        if (!S::kUniform && (j == kSpan - 1 || kb + 1 == blocks)) {
+        ++j;
+        if (last) {
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctrl->sc_empty[e.sc.slot]));
+            arrive_if(lane == 0, sc_empty + e.sc.slot * 8);
             e.sc.next(kScaleSlots);
+            if (left > 1) {
+                if (!__all_sync(0xFFFFFFFFu, more) && !role_wait<1>(sc_full + e.sc.slot * 8, e.sc.phase, wc)) return false;
+                slot = scales + e.sc.slot * S::kSlotBytes;
+                r = ptx::ld_shared_f32(slot + row * (kRowPitch * 4));
+                if constexpr (S::kUniform) c = ptx::ld_shared_f32(slot + (kRows * kRowPitch + group * kSpan) * 4);
+                j = 0;
+            }
         }
     }
     return true;
