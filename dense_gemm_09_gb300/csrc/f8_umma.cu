@@ -18,8 +18,9 @@
 //   warp 0      TMA producer: 128 bytes of K of both operands a stage;
 //   warp 1      MMA issuer (in a pair's other CTA it tells the leader which of its own
 //               stages have landed);
-//   warp 2      the blocks' scales, by 4-byte asynchronous copies into a ring;
-//   warp 3      the table of tiles, at the start;
+//   warp 2      the blocks' scales, by asynchronous copies into a ring;
+//   warp 3      the table of tiles, at the start; then MMA issuer of the second half of
+//               tiles of 256 columns;
 //   warps 4-11  two groups of four: group g has columns g bn / 2 .. of the tile, warp w
 //               of it the accumulator's rows 32 w ..: sums in registers, then C.
 #include <algorithm>
@@ -69,7 +70,7 @@ struct Ctrl {
     uint64_t acc_full[kMaxAccs];     // the MMAs of a block (a half of it: [half][slot]) are done
     uint64_t acc_empty[kMaxAccs];    // leader: every epilogue warp of the pair that reads them has
     uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
-    uint64_t mma_done;
+    uint64_t mma_done[2];
     uint64_t never;                  // test hook: a barrier nothing arrives at
     uint32_t stop, limit_us;         // a wait ran out; a wait's limit, in 1024 ns (adjacent, see role_wait)
     uint32_t tmem_base;
@@ -353,57 +354,51 @@ __device__ __forceinline__ void run_forwarder(const Params &p, const F8Table &ta
     }
 }
 
+// The MMAs of a block, or with kHalves == 2 those of the half that this warp issues.
 template <typename S>
 __device__ __forceinline__ void run_mma(const Params &p, const F8Table &table, uint32_t ring, Ctrl *ctrl, uint32_t tmem_base,
-                                        uint32_t wc)
+                                        uint32_t half, uint32_t wc)
 {
-    tmem_base = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);  // a uniform value for the compiler
+    tmem_base = __shfl_sync(0xFFFFFFFFu, tmem_base, 0) + half * (S::kBn / 2);  // a uniform value for the compiler
     // descriptors of the first stage; a stage on is kStageBytes / 16, an MMA's K step 2, in
     // their address fields
     const uint64_t row_desc = ptx::smem_desc(ring, 16, 1024, ptx::kSw128);
-    const uint64_t col_desc = ptx::smem_desc(ring + kRowsBytes, 16, 1024, ptx::kSw128);
+    const uint64_t col_desc = ptx::smem_desc(ring + kRowsBytes + half * (S::kBn / S::kCtas / 2) * kRowBytes, 16, 1024, ptx::kSw128);
     const uint32_t idesc = p.idesc;
+    const uint32_t full = ptx::smem_addr(ctrl->full), peer = ptx::smem_addr(ctrl->peer_full), empty = ptx::smem_addr(ctrl->empty);
+    const uint32_t acc_full = ptx::smem_addr(ctrl->acc_full) + half * S::kAccs * 8, acc_empty = ptx::smem_addr(ctrl->acc_empty) + half * S::kAccs * 8;
     Ring st, acc;
+    bool landed = false, both = S::kCtas == 1;  // this CTA's and the other's stage, as a look ahead saw them
     // test hook: wait on a barrier nothing arrives at, so the wait runs out
     bool ok = !p.inject_stall || role_wait<1>(ptx::smem_addr(&ctrl->never), 0, wc);
-    const uint32_t full = ptx::smem_addr(ctrl->full), peer = ptx::smem_addr(ctrl->peer_full), empty = ptx::smem_addr(ctrl->empty);
-    const uint32_t acc_full = ptx::smem_addr(ctrl->acc_full), acc_empty = ptx::smem_addr(ctrl->acc_empty);
     for (uint32_t n = schedule<S>(p, table).blocks(); ok && n > 0; --n) {
-        // a look at all the barriers of the block costs what one at a single one does
-        bool there[4] = {test(full + st.slot * 8, st.phase), true, test(acc_empty + acc.slot * 8, acc.phase ^ 1u), true};
-        if (S::kCtas == 2) there[1] = test(peer + st.slot * 8, st.phase);
-        if (S::kHalves == 2) there[3] = test(acc_empty + (S::kAccs + acc.slot) * 8, acc.phase ^ 1u);
-        ok = (__all_sync(0xFFFFFFFFu, there[0]) || role_wait<1>(full + st.slot * 8, st.phase, wc)) &&
-             (__all_sync(0xFFFFFFFFu, there[1]) || role_wait<2>(peer + st.slot * 8, st.phase, wc));
-        const uint64_t a = row_desc + st.slot * (S::kStageBytes >> 4);
-#pragma unroll
-        for (uint32_t h = 0; h < S::kHalves; ++h) {
-            const uint32_t at = (h * S::kAccs + acc.slot) * 8;
-            if (ok) ok = __all_sync(0xFFFFFFFFu, there[2 + h]) || role_wait<S::kCtas>(acc_empty + at, acc.phase ^ 1u, wc);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            if (elect_one()) {
-                const uint32_t d = tmem_base + acc.slot * S::kBn + h * (S::kBn / 2);
-                const uint64_t b = col_desc + (st.slot * S::kStageBytes + h * (S::kBn / S::kCtas / 2) * kRowBytes) / 16;
-#pragma unroll
-                for (int k = 0; k < kRowBytes / 32; ++k) umma_f8<S::kCtas>(d, a + k * 2, b + k * 2, idesc, k == 0 ? 0u : 1u);
-                if (h == S::kHalves - 1) commit_all<S::kCtas>(empty + st.slot * 8);
-                commit_all<S::kCtas>(acc_full + at);
-            }
-            __syncwarp();
-        }
+        ok = (__all_sync(0xFFFFFFFFu, landed) || role_wait<1>(full + st.slot * 8, st.phase, wc)) &&
+             (__all_sync(0xFFFFFFFFu, both) || role_wait<2>(peer + st.slot * 8, st.phase, wc)) &&
+             role_wait<S::kCtas>(acc_empty + acc.slot * 8, acc.phase ^ 1u, wc);
         if (!ok) break;
+        ptx::tc_fence_after();
+        if (elect_one()) {
+            const uint32_t d = tmem_base + acc.slot * S::kBn;
+            const uint64_t a = row_desc + st.slot * (S::kStageBytes >> 4), b = col_desc + st.slot * (S::kStageBytes >> 4);
+#pragma unroll
+            for (int k = 0; k < kRowBytes / 32; ++k) umma_f8<S::kCtas>(d, a + k * 2, b + k * 2, idesc, k == 0 ? 0u : 1u);
+            commit_all<S::kCtas>(acc_full + acc.slot * 8);
+            commit_all<S::kCtas>(empty + st.slot * 8);
+        }
+        __syncwarp();
         st.next(static_cast<uint32_t>(p.stages));
         acc.next(S::kAccs);
+        landed = test(full + st.slot * 8, st.phase);
+        if constexpr (S::kCtas == 2) both = test(peer + st.slot * 8, st.phase);
     }
     // Whatever the epilogue's waits came to, every MMA issued has finished before TMEM is
     // released (the elected thread is the same one each time).
     if (elect_one()) {
         if constexpr (S::kCtas == 2)
-            ptx::umma_commit_pair_multicast(ptx::smem_addr(&ctrl->mma_done), 0x1);
+            ptx::umma_commit_pair_multicast(ptx::smem_addr(&ctrl->mma_done[half]), 0x1);
         else
-            ptx::umma_commit(ptx::smem_addr(&ctrl->mma_done));
-        role_drain(ptx::smem_addr(&ctrl->mma_done), 0);
+            ptx::umma_commit(ptx::smem_addr(&ctrl->mma_done[half]));
+        role_drain(ptx::smem_addr(&ctrl->mma_done[half]), 0);
     }
     __syncwarp();
 }
@@ -835,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, S::kPerSm)
         for (int s = 0; s < kMaxStages; ++s) {
             ptx::mbar_init(ptx::smem_addr(&ctrl->full[s]), 1);
             ptx::mbar_init(ptx::smem_addr(&ctrl->peer_full[s]), 1);
-            ptx::mbar_init(ptx::smem_addr(&ctrl->empty[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&ctrl->empty[s]), S::kHalves);
         }
         for (int a = 0; a < kMaxAccs; ++a) {
             ptx::mbar_init(ptx::smem_addr(&ctrl->acc_full[a]), 1);
@@ -845,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, S::kPerSm)
             ptx::mbar_init(ptx::smem_addr(&ctrl->sc_full[s]), 32);
             ptx::mbar_init(ptx::smem_addr(&ctrl->sc_empty[s]), kEpiWarps);
         }
-        ptx::mbar_init(ptx::smem_addr(&ctrl->mma_done), 1);
+        for (int h = 0; h < 2; ++h) ptx::mbar_init(ptx::smem_addr(&ctrl->mma_done[h]), 1);
         ptx::mbar_init(ptx::smem_addr(&ctrl->never), 1);
         ctrl->stop = 0u;
         ctrl->limit_us = p.wait_limit_us;
@@ -880,10 +875,10 @@ __global__ void __launch_bounds__(kThreads, S::kPerSm)
         if constexpr (S::kMoveRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 0) {
             run_producer<S>(&tmap_t, &tmap_w, p, table, ring, ctrl, rank, wc);
-        } else if (warp == 1) {
+        } else if (warp == 1 || (S::kHalves == 2 && warp == 3)) {
             if (rank == 0)
-                run_mma<S>(p, table, ring, ctrl, tmem_base, wc);
-            else
+                run_mma<S>(p, table, ring, ctrl, tmem_base, warp >> 1, wc);
+            else if (warp == 1)
                 run_forwarder<S>(p, table, ctrl, lane, wc);
         } else if (warp == 2) {
             run_scales<S>(p, table, scales, ctrl, rank, lane, wc);
