@@ -76,12 +76,13 @@ __global__ void __launch_bounds__(kThreads) f8_any_kernel(const F8Params p, uint
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     chain_wait();
     chain_next();
-    if (warp == 0) fill_table(p, kTile, table, lane);
+    if (p.offsets && warp == 0) fill_table(p, kTile, table, lane);
     __syncthreads();
-    const uint32_t tiles = table.first[p.experts] * tiles_n;
+    const uint32_t tiles_t = static_cast<uint32_t>((p.M + kTile - 1) / kTile);  // (of one matrix)
+    const uint32_t tiles = (p.offsets ? table.first[p.experts] : tiles_t) * tiles_n;
     const int wr = (warp >> 1) * 32, wc = (warp & 1) * 32;
     for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const F8Tile tile = find_tile(table, p.experts, tiles_n, kTile, kTile, t);
+        const F8Tile tile = find_tile(p, table, tiles_t, tiles_n, kTile, kTile, t);
         const uint8_t *B = p.b.p + tile.expert * p.b_stride;
         const float *sb = p.b.scale + tile.expert * p.sb_stride;
         float acc[2][4][4] = {};

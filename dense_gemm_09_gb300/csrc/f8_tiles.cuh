@@ -4,7 +4,7 @@
 // A tile is `tile` tokens of one expert (from the expert's first row on) times a
 // number of channels.  How many tokens an expert has is known on the GPU alone, so
 // every CTA forms the table of the experts' first tiles for itself, in shared
-// memory; one matrix is one expert with all the rows.
+// memory; one matrix is one expert with all the rows, without a table.
 #pragma once
 
 #include <cstdint>
@@ -27,15 +27,6 @@ struct F8Table {
 // all are kept within 0 .. M.
 __device__ __forceinline__ void fill_table(const F8Params &p, int tile, const F8Table &table, int lane)
 {
-    if (!p.offsets) {
-        if (lane == 0) {
-            table.first[0] = 0u;
-            table.first[1] = static_cast<uint32_t>((p.M + tile - 1) / tile);
-            table.start[0] = 0;
-            table.start[1] = static_cast<int32_t>(p.M);
-        }
-        return;
-    }
     const int32_t most = static_cast<int32_t>(p.M);
     int32_t before = 0;   // the offset before this batch, in order
     uint32_t tiles = 0;   // of the experts before this batch
@@ -82,28 +73,37 @@ struct F8Tile {
 
 // Tile t, in groups of 8 tile columns (of channels) over all of the expert's tokens,
 // so that tiles in flight together share a few bands of either operand.
-__device__ __forceinline__ F8Tile find_tile(const F8Table &table, int experts, uint32_t tiles_n, int tile, int bn, uint32_t t)
+__device__ __forceinline__ F8Tile find_tile(const F8Params &p, const F8Table &table, uint32_t all_tiles_t, uint32_t tiles_n,
+                                            int tile, int bn, uint32_t t)
 {
     F8Tile r;
-    const uint32_t of_tokens = t / tiles_n;
-    int lo = 0, hi = experts;  // the last expert whose first tile is not past it (so it has tiles)
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (table.first[mid] <= of_tokens)
-            lo = mid;
-        else
-            hi = mid;
+    uint32_t first = 0, tiles_t = all_tiles_t;
+    int32_t begin = 0;
+    r.expert = 0;
+    r.t_end = static_cast<int32_t>(p.M);
+    if (p.offsets) {
+        const uint32_t of_tokens = t / tiles_n;
+        int lo = 0, hi = p.experts;  // the last expert whose first tile is not past it (so it has tiles)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (table.first[mid] <= of_tokens)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        r.expert = lo;
+        first = table.first[lo];
+        tiles_t = table.first[lo + 1] - first;
+        begin = table.start[lo];
+        r.t_end = table.start[lo + 1];
     }
-    r.expert = lo;
-    const uint32_t first = table.first[lo], tiles_t = table.first[lo + 1] - first;
     constexpr uint32_t kGroup = 8;
     const uint32_t local = t - first * tiles_n, per_group = kGroup * tiles_t;
     const uint32_t g = local / per_group, in = local - g * per_group;
     const uint32_t left = tiles_n - g * kGroup, gc = left < kGroup ? left : kGroup;
     const uint32_t band = in / gc;
     r.n0 = static_cast<int64_t>(g * kGroup + in - band * gc) * bn;
-    r.t0 = table.start[lo] + static_cast<int32_t>(band) * tile;
-    r.t_end = table.start[lo + 1];
+    r.t0 = begin + static_cast<int32_t>(band) * tile;
     return r;
 }
 

@@ -79,6 +79,7 @@ struct Ctrl {
 struct Params {
     F8Params c;
     uint32_t tiles_n;      // tiles of channels
+    uint32_t tiles_t;      // tiles of tokens, of one matrix (experts: in the table)
     int num_kb;            // blocks of K
     int stages;
     int boxes;             // staging boxes of an epilogue warp
@@ -99,21 +100,26 @@ struct Shape {
     static constexpr int kWgCols = kBn / 2;                     // columns of an epilogue group
     static constexpr int kTileRows = kRows * kCtas;
     static constexpr int kTokens = kSwap ? kBn : kTileRows, kChannels = kSwap ? kRows : kBn;  // of a tile
-    static constexpr int kStageBytes = kRowsBytes + kBn / kCtas * kRowBytes;
+    // blocks that go from role to role together: a hand-over costs a role some hundred clocks,
+    // which a block of few columns does not take
+    static constexpr int kGroup = !kSwap || kBn == 128 ? 1 : kBn == 16 ? 4 : 2;
+    static constexpr int kBlockBytes = kRowsBytes + kBn / kCtas * kRowBytes;
+    static constexpr int kStageBytes = kGroup * kBlockBytes;
     // tiles of 256 columns: an MMA for each epilogue group's half, with accumulators and
     // barriers of its own, so that one group reads while the other's half is multiplied
     static constexpr int kHalves = kBn == 256 ? 2 : 1;
-    static constexpr int kAccs = 512 / kBn < kMaxAccs ? 512 / kBn : kMaxAccs;  // of either half
-    static constexpr int kTmemCols = kAccs * kBn;
+    static constexpr int kAccCols = kGroup * kBn;
+    static constexpr int kAccs = 512 / kAccCols < kMaxAccs ? 512 / kAccCols : kMaxAccs;  // of either half
+    static constexpr int kTmemCols = kAccs * kAccCols;
     // a slot of scales: [row][block], then [group][block] or [block][column]
     static constexpr int kSlotBytes = (kRowPitch * kRows + kSpan * (kUniform ? 2 : kBn)) * 4;
     static constexpr int kScaleBytes = kScaleSlots * kSlotBytes;
-    static constexpr int kPerSm = kBn <= 32 ? 2 : 1;            // CTAs an SM
     // sums of 128 columns and 64 more on their way do not fit the 168 registers a thread that
     // 384 threads share alike: the four other warps give 112 each of theirs
     static constexpr bool kMoveRegs = kWgCols >= 128;
     static_assert(!kMoveRegs || 128 * 56 + 256 * 224 <= 384 * 168, "what is taken was given");
-    static_assert(kTmemCols >= 32 && (kTmemCols & (kTmemCols - 1)) == 0 && kPerSm * kTmemCols <= 512, "TMEM");
+    static_assert(kTmemCols >= 32 && (kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols <= 512, "TMEM");
+    static_assert(kSpan % kGroup == 0, "a group's scales are in one slot");
 };
 
 // ---- PTX
@@ -249,10 +255,10 @@ __device__ __forceinline__ bool role_drain(uint32_t bar, uint32_t parity)
 struct Sched {
     uint32_t t0, dt, tiles;
     int kb0, kb1;
-    // blocks this CTA works on in all
-    __device__ __forceinline__ uint32_t blocks() const
+    // groups of blocks this CTA works on in all
+    __device__ __forceinline__ uint32_t groups(int of) const
     {
-        return t0 < tiles ? ((tiles - t0 + dt - 1) / dt) * static_cast<uint32_t>(kb1 - kb0) : 0u;
+        return t0 < tiles ? ((tiles - t0 + dt - 1) / dt) * static_cast<uint32_t>((kb1 - kb0 + of - 1) / of) : 0u;
     }
 };
 
@@ -263,7 +269,7 @@ __device__ __forceinline__ Sched schedule(const Params &p, const F8Table &table)
     const uint32_t n = S::kCtas == 2 ? 2u : static_cast<uint32_t>(p.splitk);
     s.t0 = blockIdx.x / n;
     s.dt = gridDim.x / n;
-    s.tiles = table.first[p.c.experts] * p.tiles_n;
+    s.tiles = (p.c.offsets ? table.first[p.c.experts] : p.tiles_t) * p.tiles_n;
     s.kb0 = 0;
     s.kb1 = p.num_kb;
     if (S::kCtas == 1 && n > 1) {
@@ -277,7 +283,7 @@ __device__ __forceinline__ Sched schedule(const Params &p, const F8Table &table)
 template <typename S>
 __device__ __forceinline__ F8Tile tile_at(const Params &p, const F8Table &table, uint32_t t)
 {
-    return find_tile(table, p.c.experts, p.tiles_n, S::kTokens, S::kChannels, t);
+    return find_tile(p.c, table, p.tiles_t, p.tiles_n, S::kTokens, S::kChannels, t);
 }
 
 // A ring's position: slot and the parity of its turn.
@@ -294,37 +300,61 @@ struct Ring {
 
 // ---- roles
 
+// One stage: blocks kb .. kb_end (a group at most) of this CTA's part of the pair's tile, 128
+// of its rows and half of its columns (by one thread).
+template <typename S>
+__device__ __forceinline__ void load_stage(const CUtensorMap *tmap_t, const CUtensorMap *tmap_w, uint32_t ring, Ctrl *ctrl,
+                                           uint32_t slot, const F8Tile &tile, uint32_t rank, int kb, int kb_end)
+{
+    const int32_t tok = tile.t0 + static_cast<int32_t>(rank) * (S::kSwap ? S::kBn / S::kCtas : kRows);
+    const int32_t chan = static_cast<int32_t>(tile.n0) + static_cast<int32_t>(rank) * (S::kSwap ? kRows : S::kBn / S::kCtas / S::kHalves);
+    const uint32_t full = ptx::smem_addr(&ctrl->full[slot]);
+    const int n = min(S::kGroup, kb_end - kb);
+    ptx::mbar_arrive_expect_tx(full, n * S::kBlockBytes);
+#pragma unroll
+    for (int g = 0; g < S::kGroup; ++g) {
+        if (g >= n) break;
+        const uint32_t dst = ring + slot * S::kStageBytes + g * S::kBlockBytes;
+        const int32_t k = (kb + g) * kRowBytes;  // (the innermost coordinate, a multiple of 128 bytes)
+        ptx::tma_load_3d(dst + (S::kSwap ? kRowsBytes : 0), tmap_t, full, k, tok, 0);
+        // (with halves: of each half's 128 columns, this CTA's 64)
+#pragma unroll
+        for (int h = 0; h < S::kHalves; ++h)
+            ptx::tma_load_3d(dst + (S::kSwap ? 0 : kRowsBytes) + h * 64 * kRowBytes, tmap_w, full, k, chan + h * 128, tile.expert);
+    }
+}
+
+// The first loads of the CTA, into the empty ring, by the thread that has set the ring's
+// barriers up: they are in flight while the rest of the CTA (and its pair) starts.  Of one
+// matrix only (the tiles of experts take the table).  Returns the number of stages.
+template <typename S>
+__device__ __forceinline__ int prefill(const CUtensorMap *tmap_t, const CUtensorMap *tmap_w, const Params &p, const F8Table &table,
+                                       uint32_t ring, Ctrl *ctrl, uint32_t rank)
+{
+    const Sched sc = schedule<S>(p, table);
+    const F8Tile tile = tile_at<S>(p, table, sc.t0);
+    int n = 0;
+    for (int kb = sc.kb0; kb < sc.kb1 && n < p.stages; kb += S::kGroup, ++n)
+        load_stage<S>(tmap_t, tmap_w, ring, ctrl, n, tile, rank, kb, sc.kb1);
+    return n;
+}
+
+// The rest of the loads, after the `done` stages of prefill.
 template <typename S>
 __device__ __forceinline__ void run_producer(const CUtensorMap *tmap_t, const CUtensorMap *tmap_w, const Params &p,
-                                             const F8Table &table, uint32_t ring, Ctrl *ctrl, uint32_t rank, uint32_t wc)
+                                             const F8Table &table, uint32_t ring, Ctrl *ctrl, uint32_t rank, int done, uint32_t wc)
 {
     const Sched sc = schedule<S>(p, table);
     const uint32_t stages = static_cast<uint32_t>(p.stages);
     Ring st;
+    for (int i = 0; i < done; ++i) st.next(stages);
     bool ok = true;
     for (uint32_t t = sc.t0; ok && t < sc.tiles; t += sc.dt) {
         const F8Tile tile = tile_at<S>(p, table, t);
-        // this CTA's part of the pair's tile: 128 of its rows, half of its columns
-        const int32_t tok = tile.t0 + static_cast<int32_t>(rank) * (S::kSwap ? S::kBn / S::kCtas : kRows);
-        const int32_t chan = static_cast<int32_t>(tile.n0) + static_cast<int32_t>(rank) * (S::kSwap ? kRows : S::kBn / S::kCtas);
-        for (int kb = sc.kb0; kb < sc.kb1; ++kb) {
+        for (int kb = sc.kb0 + (t == sc.t0 ? done * S::kGroup : 0); kb < sc.kb1; kb += S::kGroup) {
             ok = role_wait<1>(ptx::smem_addr(&ctrl->empty[st.slot]), st.phase ^ 1u, wc);
             if (!ok) break;
-            if (elect_one()) {
-                const uint32_t full = ptx::smem_addr(&ctrl->full[st.slot]);
-                const uint32_t dst = ring + st.slot * S::kStageBytes;
-                ptx::mbar_arrive_expect_tx(full, S::kStageBytes);
-                // the innermost coordinate is a multiple of 128 bytes
-                ptx::tma_load_3d(dst + (S::kSwap ? kRowsBytes : 0), tmap_t, full, kb * kRowBytes, tok, 0);
-                if constexpr (S::kHalves == 1) {
-                    ptx::tma_load_3d(dst + (S::kSwap ? 0 : kRowsBytes), tmap_w, full, kb * kRowBytes, chan, tile.expert);
-                } else {  // of each half's 128 columns, this CTA's 64
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        ptx::tma_load_3d(dst + kRowsBytes + h * 64 * kRowBytes, tmap_w, full, kb * kRowBytes,
-                                         static_cast<int32_t>(tile.n0) + h * 128 + static_cast<int32_t>(rank) * 64, tile.expert);
-                }
-            }
+            if (elect_one()) load_stage<S>(tmap_t, tmap_w, ring, ctrl, st.slot, tile, rank, kb, sc.kb1);
             __syncwarp();
             st.next(stages);
         }
@@ -346,7 +376,7 @@ template <typename S>
 __device__ __forceinline__ void run_forwarder(const Params &p, const F8Table &table, Ctrl *ctrl, int lane, uint32_t wc)
 {
     Ring st;
-    for (uint32_t n = schedule<S>(p, table).blocks(); n > 0; --n) {
+    for (uint32_t n = schedule<S>(p, table).groups(S::kGroup); n > 0; --n) {
         if (!role_wait<1>(ptx::smem_addr(&ctrl->full[st.slot]), st.phase, wc)) return;
         if (lane == 0) arrive_remote(ptx::mapa(ptx::smem_addr(&ctrl->peer_full[st.slot]), 0));
         __syncwarp();
@@ -371,21 +401,29 @@ __device__ __forceinline__ void run_mma(const Params &p, const F8Table &table, u
     bool landed = false, both = S::kCtas == 1;  // this CTA's and the other's stage, as a look ahead saw them
     // test hook: wait on a barrier nothing arrives at, so the wait runs out
     bool ok = !p.inject_stall || role_wait<1>(ptx::smem_addr(&ctrl->never), 0, wc);
-    for (uint32_t n = schedule<S>(p, table).blocks(); ok && n > 0; --n) {
+    const Sched sc = schedule<S>(p, table);
+    int left = sc.kb1 - sc.kb0;  // blocks of the tile
+    for (uint32_t n = sc.groups(S::kGroup); ok && n > 0; --n) {
         ok = (__all_sync(0xFFFFFFFFu, landed) || role_wait<1>(full + st.slot * 8, st.phase, wc)) &&
              (__all_sync(0xFFFFFFFFu, both) || role_wait<2>(peer + st.slot * 8, st.phase, wc)) &&
              role_wait<S::kCtas>(acc_empty + acc.slot * 8, acc.phase ^ 1u, wc);
         if (!ok) break;
         ptx::tc_fence_after();
         if (elect_one()) {
-            const uint32_t d = tmem_base + acc.slot * S::kBn;
-            const uint64_t a = row_desc + st.slot * (S::kStageBytes >> 4), b = col_desc + st.slot * (S::kStageBytes >> 4);
 #pragma unroll
-            for (int k = 0; k < kRowBytes / 32; ++k) umma_f8<S::kCtas>(d, a + k * 2, b + k * 2, idesc, k == 0 ? 0u : 1u);
+            for (int g = 0; g < S::kGroup; ++g) {
+                if (g >= left) break;
+                const uint32_t d = tmem_base + acc.slot * S::kAccCols + g * S::kBn, at = (st.slot * S::kStageBytes + g * S::kBlockBytes) / 16;
+#pragma unroll
+                for (int k = 0; k < kRowBytes / 32; ++k)
+                    umma_f8<S::kCtas>(d, row_desc + at + k * 2, col_desc + at + k * 2, idesc, k == 0 ? 0u : 1u);
+            }
             commit_all<S::kCtas>(acc_full + acc.slot * 8);
             commit_all<S::kCtas>(empty + st.slot * 8);
         }
         __syncwarp();
+        left -= S::kGroup;
+        if (left <= 0) left = sc.kb1 - sc.kb0;
         st.next(static_cast<uint32_t>(p.stages));
         acc.next(S::kAccs);
         landed = test(full + st.slot * 8, st.phase);
@@ -496,7 +534,7 @@ __device__ __forceinline__ bool sum_blocks(const Params &p, Ctrl *ctrl, uint32_t
     for (int left = blocks; left > 0; --left) {
         if (!__all_sync(0xFFFFFFFFu, ready) && !role_wait<1>(acc_full + e.acc.slot * 8, e.acc.phase, wc)) return false;
         ptx::tc_fence_after();
-        const uint32_t src = taddr + e.acc.slot * S::kBn, release = acc_empty + e.acc.slot * 8;
+        const uint32_t src = taddr + e.acc.slot * S::kAccCols, release = acc_empty + e.acc.slot * 8;
         uint32_t d[kChunks > 1 ? 2 : 1][kChunk];
         tmem_load<kChunk>(src, d[0]);
         e.acc.next(S::kAccs);
@@ -558,6 +596,72 @@ __device__ __forceinline__ bool sum_blocks(const Params &p, Ctrl *ctrl, uint32_t
         }
     }
     return true;
+}
+
+// The same by groups of blocks: a group's accumulators are read together.
+template <typename S>
+__device__ __forceinline__ bool sum_groups(const Params &p, Ctrl *ctrl, uint32_t scales, uint32_t taddr, int row, int group,
+                                           int blocks, int lane, Epi &e, uint64_t (&sum)[S::kWgCols / 2], uint32_t wc)
+{
+    constexpr int kChunk = S::kWgCols < 32 ? S::kWgCols : 32;
+    static_assert(S::kWgCols <= 32 && !S::kUniform && S::kCtas == 1, "narrow tiles of single CTAs");
+#pragma unroll
+    for (int i = 0; i < S::kWgCols / 2; ++i) sum[i] = 0ull;
+    const uint32_t acc_full = ptx::smem_addr(ctrl->acc_full), acc_empty = ptx::smem_addr(ctrl->acc_empty);
+    const uint32_t sc_full = ptx::smem_addr(ctrl->sc_full), sc_empty = ptx::smem_addr(ctrl->sc_empty);
+    int j = 0;  // the group's place in its span of scales
+    for (int left = blocks; left > 0; left -= S::kGroup) {
+        if (j == 0 && !role_wait<1>(sc_full + e.sc.slot * 8, e.sc.phase, wc)) return false;
+        const uint32_t slot = scales + e.sc.slot * S::kSlotBytes;
+        float r[S::kGroup];
+#pragma unroll
+        for (int g = 0; g < S::kGroup; ++g) r[g] = ptx::ld_shared_f32(slot + (row * kRowPitch + j + g) * 4);
+        if (!role_wait<1>(acc_full + e.acc.slot * 8, e.acc.phase, wc)) return false;
+        ptx::tc_fence_after();
+        uint32_t d[S::kGroup][kChunk];
+#pragma unroll
+        for (int g = 0; g < S::kGroup; ++g)  // (past the last block: what an earlier one left, not used)
+            tmem_load<kChunk>(taddr + e.acc.slot * S::kAccCols + g * S::kBn, d[g]);
+#pragma unroll
+        for (int g = 0; g < S::kGroup; ++g) tmem_wait<kChunk>(d[g]);
+        ptx::tc_fence_before();
+        // (an arrival that nothing waits for could reach a CTA that has left)
+        arrive_if(lane == 0 && e.left > S::kAccs, acc_empty + e.acc.slot * 8);
+#pragma unroll
+        for (int g = 0; g < S::kGroup; ++g) {
+            if (g >= left) break;  // uniform
+            const uint64_t r2 = pack2(r[g], r[g]);
+            const uint32_t cols = slot + (kRows * kRowPitch + (j + g) * S::kBn + group * S::kWgCols) * 4;
+#pragma unroll
+            for (int i = 0; i < kChunk; i += 4) {
+                const float4 f = ptx::ld_shared_v4f(cols + i * 4);
+                const uint64_t x = pack2(__uint_as_float(d[g][i]), __uint_as_float(d[g][i + 1]));
+                const uint64_t y = pack2(__uint_as_float(d[g][i + 2]), __uint_as_float(d[g][i + 3]));
+                sum[i / 2] = fma2(mul2(x, pack2(f.x, f.y)), r2, sum[i / 2]);
+                sum[i / 2 + 1] = fma2(mul2(y, pack2(f.z, f.w)), r2, sum[i / 2 + 1]);
+            }
+        }
+        --e.left;
+        e.acc.next(S::kAccs);
+        j += S::kGroup;
+        if (j == kSpan || left <= S::kGroup) {
+            __syncwarp();
+            arrive_if(lane == 0, sc_empty + e.sc.slot * 8);
+            e.sc.next(kScaleSlots);
+            j = 0;
+        }
+    }
+    return true;
+}
+
+template <typename S>
+__device__ __forceinline__ bool sum_tile(const Params &p, Ctrl *ctrl, uint32_t scales, uint32_t taddr, int row, int group,
+                                         int blocks, int lane, Epi &e, uint64_t (&sum)[S::kWgCols / 2], uint32_t wc)
+{
+    if constexpr (S::kGroup > 1)
+        return sum_groups<S>(p, ctrl, scales, taddr, row, group, blocks, lane, e, sum, wc);
+    else
+        return sum_blocks<S>(p, ctrl, scales, taddr, row, group, blocks, lane, e, sum, wc);
 }
 
 template <typename T>
@@ -783,17 +887,17 @@ __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap 
     const int quarter = warp & 3, group = (warp - 4) >> 2, row = quarter * 32 + lane;
     const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + group * S::kWgCols;
     const uint32_t my_box = box + static_cast<uint32_t>(warp - 4) * p.boxes * kBoxBytes;
-    Epi e{{}, {}, sc.blocks(), 0};
+    Epi e{{}, {}, sc.groups(S::kGroup), 0};
     uint64_t sum[S::kWgCols / 2];
     if (S::kSwap && p.splitk > 1) {  // one tile, uniform over the cluster
         const F8Tile tile = tile_at<S>(p, table, sc.t0);
-        sum_blocks<S>(p, ctrl, scales, taddr, row, group, sc.kb1 - sc.kb0, lane, e, sum, wc);  // (a time-out raises the abort flag)
+        sum_tile<S>(p, ctrl, scales, taddr, row, group, sc.kb1 - sc.kb0, lane, e, sum, wc);  // (a time-out raises the abort flag)
         __syncwarp();
         if constexpr (S::kSwap) join_split<S>(p, tile, ring, row, group, tile.n0 + row, sum, wc);
         return;
     }
     for (uint32_t t = sc.t0; t < sc.tiles; t += sc.dt) {
-        if (!sum_blocks<S>(p, ctrl, scales, taddr, row, group, sc.kb1 - sc.kb0, lane, e, sum, wc)) break;
+        if (!sum_tile<S>(p, ctrl, scales, taddr, row, group, sc.kb1 - sc.kb0, lane, e, sum, wc)) break;
         const F8Tile tile = tile_at<S>(p, table, t);
         if constexpr (S::kSwap) {
             store_channels_any<S, S::kWgCols>(p, sum, tile.n0 + rank * kRows + row, tile.t0 + group * S::kWgCols, tile.t_end);
@@ -811,7 +915,7 @@ __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap 
 }
 
 template <typename S>
-__global__ void __launch_bounds__(kThreads, S::kPerSm)
+__global__ void __launch_bounds__(kThreads, 1)
     f8_umma_kernel(const __grid_constant__ CUtensorMap tmap_t, const __grid_constant__ CUtensorMap tmap_w,
                    const __grid_constant__ CUtensorMap tmap_o, const Params p)
 {
@@ -826,12 +930,28 @@ __global__ void __launch_bounds__(kThreads, S::kPerSm)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = S::kCtas == 2 ? (ptx::cluster_ctarank() & 1u) : 0u;
 
-    if (warp == 0 && elect_one()) {
-        for (int s = 0; s < kMaxStages; ++s) {
-            ptx::mbar_init(ptx::smem_addr(&ctrl->full[s]), 1);
-            ptx::mbar_init(ptx::smem_addr(&ctrl->peer_full[s]), 1);
-            ptx::mbar_init(ptx::smem_addr(&ctrl->empty[s]), S::kHalves);
+    int loaded = 0;  // stages already under way (warp 0)
+    if (warp == 0) {
+        if (elect_one()) {
+            for (int s = 0; s < kMaxStages; ++s) {
+                ptx::mbar_init(ptx::smem_addr(&ctrl->full[s]), 1);
+                ptx::mbar_init(ptx::smem_addr(&ctrl->empty[s]), S::kHalves);
+            }
+            ptx::fence_mbarrier_init();
+            chain_wait();  // (what follows reads the call's operands)
+            if (!p.c.offsets) loaded = prefill<S>(&tmap_t, &tmap_w, p, table, ring, ctrl, rank);
         }
+        loaded = __reduce_max_sync(0xFFFFFFFFu, loaded);
+    } else if (warp == 1) {
+        if constexpr (S::kCtas == 2) {
+            ptx::tmem_alloc_pair(ptx::smem_addr(&ctrl->tmem_base), S::kTmemCols);
+            ptx::tmem_relinquish_pair();
+        } else {
+            ptx::tmem_alloc(ptx::smem_addr(&ctrl->tmem_base), S::kTmemCols);
+            ptx::tmem_relinquish();
+        }
+    } else if (warp == 2 && elect_one()) {
+        for (int s = 0; s < kMaxStages; ++s) ptx::mbar_init(ptx::smem_addr(&ctrl->peer_full[s]), 1);
         for (int a = 0; a < kMaxAccs; ++a) {
             ptx::mbar_init(ptx::smem_addr(&ctrl->acc_full[a]), 1);
             ptx::mbar_init(ptx::smem_addr(&ctrl->acc_empty[a]), kEpiWarps / S::kHalves * S::kCtas);
@@ -845,23 +965,13 @@ __global__ void __launch_bounds__(kThreads, S::kPerSm)
         ctrl->stop = 0u;
         ctrl->limit_us = p.wait_limit_us;
         ptx::fence_mbarrier_init();
-    } else if (warp == 1) {
-        if constexpr (S::kCtas == 2) {
-            ptx::tmem_alloc_pair(ptx::smem_addr(&ctrl->tmem_base), S::kTmemCols);
-            ptx::tmem_relinquish_pair();
-        } else {
-            ptx::tmem_alloc(ptx::smem_addr(&ctrl->tmem_base), S::kTmemCols);
-            ptx::tmem_relinquish();
-        }
-    } else if (warp == 2 && elect_one()) {
-        ptx::prefetch_tmap(&tmap_t);
-        ptx::prefetch_tmap(&tmap_w);
         if (p.tma_store) ptx::prefetch_tmap(&tmap_o);
     }
     __syncwarp();
+    const uint32_t wc = ptx::smem_addr(&ctrl->stop);
     chain_wait();  // (everything below reads or writes the call's operands)
     chain_next();
-    if (warp == 3) fill_table(p.c, S::kTokens, table, lane);
+    if (warp == 3 && p.c.offsets) fill_table(p.c, S::kTokens, table, lane);
     __syncwarp();
     ptx::tc_fence_before();
     __syncthreads();
@@ -869,12 +979,11 @@ __global__ void __launch_bounds__(kThreads, S::kPerSm)
     if constexpr (S::kCtas == 2) cluster_meet();
     ptx::tc_fence_after();
     const uint32_t tmem_base = ctrl->tmem_base;
-    const uint32_t wc = ptx::smem_addr(&ctrl->stop);
 
     if (warp < 4) {
         if constexpr (S::kMoveRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 0) {
-            run_producer<S>(&tmap_t, &tmap_w, p, table, ring, ctrl, rank, wc);
+            run_producer<S>(&tmap_t, &tmap_w, p, table, ring, ctrl, rank, loaded, wc);
         } else if (warp == 1 || (S::kHalves == 2 && warp == 3)) {
             if (rank == 0)
                 run_mma<S>(p, table, ring, ctrl, tmem_base, warp >> 1, wc);
@@ -920,11 +1029,10 @@ template <typename S>
 int set_rings(Params &p)
 {
     const int fixed = S::kScaleBytes + static_cast<int>(sizeof(Ctrl)) + 8 * (p.c.experts + 1);
-    const int limit = S::kPerSm == 2 ? 113 * 1024 : kSmemLimit;  // (an SM's 228 KB, less 1 KB a CTA)
-    p.boxes = 0;
-    if (!S::kSwap) p.boxes = (limit - fixed - 2 * kEpiWarps * kBoxBytes) / S::kStageBytes >= 5 ? 2 : 1;
+        p.boxes = 0;
+    if (!S::kSwap) p.boxes = (kSmemLimit - fixed - 2 * kEpiWarps * kBoxBytes) / S::kStageBytes >= 5 ? 2 : 1;
     const int boxes = kEpiWarps * p.boxes * kBoxBytes;
-    p.stages = std::min(kMaxStages, (limit - fixed - boxes) / S::kStageBytes);
+    p.stages = std::min(kMaxStages, (kSmemLimit - fixed - boxes) / S::kStageBytes);
     return fixed + boxes + p.stages * S::kStageBytes;
 }
 
@@ -940,11 +1048,10 @@ int capacity(int cluster)
     if (cluster < 1 || cluster > 8 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
     std::call_once(once[dev], [dev] {
         auto kernel = f8_umma_kernel<S>;
-        const int smem = S::kPerSm == 2 ? 113 * 1024 : kSmemLimit;
         int sms = 0;
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess &&
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) == cudaSuccess &&
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) {
-            cached[dev][1] = sms * S::kPerSm;
+            cached[dev][1] = sms;
             for (int s = 2; s <= (S::kCtas == 2 ? 2 : 8); ++s) {
                 cudaLaunchConfig_t cfg = {};
                 cudaLaunchAttribute attr[1];
@@ -954,7 +1061,7 @@ int capacity(int cluster)
                 attr[0].val.clusterDim.z = 1;
                 cfg.gridDim = dim3(static_cast<unsigned>(sms - sms % s));
                 cfg.blockDim = dim3(kThreads);
-                cfg.dynamicSmemBytes = smem;
+                cfg.dynamicSmemBytes = kSmemLimit;
                 cfg.attrs = attr;
                 cfg.numAttrs = 1;
                 int n = 0;
@@ -975,13 +1082,14 @@ bool launch(const F8Params &c, int splitk, cudaStream_t stream)
     const int64_t tiles_n = (c.N + S::kChannels - 1) / S::kChannels, tiles = tiles_n * token_tiles_bound(c, S::kTokens);
     if (tiles > INT32_MAX / 16) return false;  // (32-bit tile arithmetic, with room for a group of tile columns)
     p.tiles_n = static_cast<uint32_t>(tiles_n);
+    p.tiles_t = static_cast<uint32_t>((c.M + S::kTokens - 1) / S::kTokens);
     p.num_kb = static_cast<int>((c.K + kRowBytes - 1) / kRowBytes);
     p.splitk = S::kSwap && !c.offsets ? std::min(splitk, p.num_kb) : 1;
     if (tiles / 76 * p.num_kb > INT32_MAX) return false;  // blocks of one CTA
     const int cluster = S::kCtas == 2 ? 2 : p.splitk;
     const int fit = capacity<S>(cluster);
     const int smem = set_rings<S>(p);
-    if (fit < 1 || p.stages < 3 || (p.splitk > 1 && tiles > fit)) return false;
+    if (fit < 1 || p.stages < 2 || (p.splitk > 1 && tiles > fit)) return false;
     constexpr int kTokBox = S::kSwap ? S::kBn / S::kCtas : kRows, kChanBox = S::kSwap ? kRows : S::kBn / S::kCtas / S::kHalves;
     const uint64_t k = static_cast<uint64_t>(c.K), m = static_cast<uint64_t>(c.M), n = static_cast<uint64_t>(c.N);
     CUtensorMap mt{}, mw{}, mo{};
