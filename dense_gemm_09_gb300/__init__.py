@@ -556,7 +556,7 @@ def combine_experts_grad(dX, Y, position, weights, dY, dweights, stream=None):
 
 
 # Kernels for tune_f8_next (see dgemm_tune_f8_next in include/dgemm.h)
-TUNE_F8_ANY, TUNE_F8_PAIR, TUNE_F8_CHANNELS = 1, 2, 3
+TUNE_F8_ANY, TUNE_F8_PAIR, TUNE_F8_CHANNELS, TUNE_F8_DECODE = 1, 2, 3, 4
 
 
 def tune_f8_next(variant: int, bn: int = 0, split: int = 1) -> None:

@@ -73,7 +73,8 @@ int checks_failed(int clear, int *site)
     int (*const readers[])(int, int *) = {check_status_simt, check_status_tma, check_status_umma,
                                           check_status_scale, check_status_repack, check_status_i8_rows,
                                           check_status_i8_gemm, check_status_i8_umma, check_status_i8_decode,
-                                          check_status_f8_rows, check_status_f8_gemm, check_status_f8_umma, check_status_experts};
+                                          check_status_f8_rows, check_status_f8_gemm, check_status_f8_umma, check_status_f8_decode,
+                                          check_status_experts};
     int status = DGEMM_OK, where = 0;
     for (auto rd : readers) {
         int s = 0;

@@ -20,6 +20,9 @@ struct F8Operand {
     const float *scale;
     int64_t s_row, s_blk;
     int type, block;
+
+    // the row of scales of a row
+    __host__ __device__ int64_t band(int64_t row) const { return block == 1 ? row : row / kF8Block; }
 };
 
 inline F8Operand f8_operand(const dgemm_f8 &m)
@@ -43,17 +46,22 @@ struct F8Params {
 constexpr int kMaxExperts = 1024;
 
 // Kernel of one call: variant, tile width and split (as dgemm_tune_f8_next numbers them).
-enum { kF8Auto = 0, kF8Any = 1, kF8Pair = 2, kF8Channels = 3 };
+enum { kF8Auto = 0, kF8Any = 1, kF8Pair = 2, kF8Channels = 3, kF8Decode = 4 };
 struct F8Config {
     int variant;
     int bn;     // tile columns: channels (kF8Pair) or tokens (kF8Channels)
-    int split;  // kF8Channels: CTAs that share a tile along K
+    int split;  // kF8Channels: CTAs that share a tile along K; kF8Decode: warps of a thread block
 };
 
 // The tensor-core kernels (f8_umma.cu): false, and nothing launched, where the
 // configuration cannot run.
 bool f8_umma_config_ok(const F8Config &cfg);
 bool launch_f8_umma(const F8Params &c, const F8Config &cfg, cudaStream_t stream);
+
+// The kernel for a few tokens (f8_decode.cu), for operands with 16-byte aligned rows: as above.
+constexpr int kF8DecodeTokens = 8;
+bool f8_decode_config_ok(const F8Config &cfg);
+bool launch_f8_decode(const F8Params &p, const F8Config &cfg, cudaStream_t stream);
 
 // Tuning hook behind dgemm_tune_f8_next: the request of this host thread, and its
 // taking (by every gemm_f8_tn and gemm_f8_tn_experts call, whatever becomes of it).

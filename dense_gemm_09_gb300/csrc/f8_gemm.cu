@@ -121,14 +121,14 @@ __global__ void __launch_bounds__(kThreads) f8_any_kernel(const F8Params p, uint
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int64_t m = min(static_cast<int64_t>(tile.t0 + wr + i * 16 + h * 8 + g), static_cast<int64_t>(tile.t_end - 1));
-                    ra[i][h] = p.a.scale[m / p.a.block * p.a.s_row + kb * p.a.s_blk];
+                    ra[i][h] = p.a.scale[p.a.band(m) * p.a.s_row + kb * p.a.s_blk];
                 }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int64_t n = min(tile.n0 + wc + j * 8 + 2 * q + h, p.N - 1);
-                    cb[j][h] = sb[n / p.b.block * p.b.s_row + kb * p.b.s_blk];
+                    cb[j][h] = sb[p.b.band(n) * p.b.s_row + kb * p.b.s_blk];
                 }
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -175,6 +175,8 @@ const char *launch_any(const F8Params &p, cudaStream_t stream, const DeviceInfo 
 F8Config choose(const F8Params &p, const DeviceInfo &dev)
 {
     const int64_t tokens = p.offsets ? (p.M + p.experts - 1) / p.experts : p.M;
+    // (weights of more than ~100 MB: even, then the tensor-core kernel)
+    if (!p.offsets && tokens <= kF8DecodeTokens && p.N * p.K <= (int64_t{100} << 20)) return {kF8Decode, 0, 8};
     if (tokens > 128) return {kF8Pair, 256, 1};
     const int bn = tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : 128;
     int split = 1;
@@ -185,6 +187,7 @@ F8Config choose(const F8Params &p, const DeviceInfo &dev)
 
 const char *kernel_name(const F8Config &cfg)
 {
+    if (cfg.variant == kF8Decode) return cfg.split == 4 ? "f8_decode_4_warps" : "f8_decode_8_warps";
     if (cfg.variant == kF8Pair) return cfg.bn == 256 ? "f8_pair_256x256" : "f8_pair_256x128";
     static const char *const names[4][4] = {
         {"f8_channels_128x16", "f8_channels_128x16_split2", "f8_channels_128x16_split4", "f8_channels_128x16_split8"},
@@ -200,7 +203,8 @@ const char *kernel_name(const F8Config &cfg)
 int f8_tune_next(int variant, int bn, int split)
 {
     const F8Config cfg{variant, bn, split};
-    if (variant != kF8Auto && variant != kF8Any && !f8_umma_config_ok(cfg)) return DGEMM_ERR_INVALID_ARG;
+    if (variant != kF8Auto && variant != kF8Any && !f8_umma_config_ok(cfg) && !f8_decode_config_ok(cfg))
+        return DGEMM_ERR_INVALID_ARG;
     t_tune = cfg;
     return DGEMM_OK;
 }
@@ -218,10 +222,13 @@ const char *launch_gemm_f8(const F8Params &p, const F8Config &tune, cudaStream_t
     const bool tma = p.K > 0 && aligned(p.a.p, p.a.ld, 1, 16) && aligned(p.b.p, p.b.ld, 1, 16) &&
                      (p.experts == 1 || (p.b_stride % 16 == 0 && p.b_stride > 0));
     if (tma && tune.variant != kF8Any) {
+        auto run = [&](const F8Config &cfg) {
+            return cfg.variant == kF8Decode ? launch_f8_decode(p, cfg, stream) : launch_f8_umma(p, cfg, stream);
+        };
         F8Config cfg = tune;
-        if (cfg.variant == kF8Auto || !launch_f8_umma(p, cfg, stream)) {
+        if (cfg.variant == kF8Auto || !run(cfg)) {
             cfg = choose(p, dev);
-            if (!launch_f8_umma(p, cfg, stream)) return launch_any(p, stream, dev);
+            if (!run(cfg)) return launch_any(p, stream, dev);
         }
         return kernel_name(cfg);
     }

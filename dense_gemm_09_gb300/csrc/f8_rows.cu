@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads)
                     b[i].y |= v;
             }
         }
-        s[i] = q.scale[r / q.block * q.s_row + (col[i] / kF8Block) * q.s_blk];
+        s[i] = q.scale[q.band(r) * q.s_row + (col[i] / kF8Block) * q.s_blk];
     }
 #pragma unroll
     for (int i = 0; i < kMany; ++i) {

@@ -462,7 +462,7 @@ __device__ __forceinline__ void run_scales(const Params &p, const F8Table &table
         auto place = [&](bool token, int64_t i) {
             const F8Operand &o = token ? p.c.a : p.c.b;
             const int64_t at = token ? min(tile.t0 + i, p.c.M - 1) : min(tile.n0 + i, p.c.N - 1);
-            return (token ? o.scale : weights) + at / o.block * o.s_row;
+            return (token ? o.scale : weights) + o.band(at) * o.s_row;
         };
         const float *row[kR], *col[kC];
 #pragma unroll

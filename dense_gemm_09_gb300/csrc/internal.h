@@ -84,6 +84,7 @@ int check_status_i8_decode(int clear, int *site);
 int check_status_f8_rows(int clear, int *site);
 int check_status_f8_gemm(int clear, int *site);
 int check_status_f8_umma(int clear, int *site);
+int check_status_f8_decode(int clear, int *site);
 int check_status_experts(int clear, int *site);
 
 // Rows taken off M for the C-store checks of the next TMA-fed SIMT launch

@@ -529,7 +529,7 @@ int dgemm_device_status(int clear);
  * the library's sources, units 1 sgemm_simt.cu, 2 sgemm_tma.cu,
  * 3 umma_gemm.cu, 4 scale_c.cu, 5 repack.cu, 6 i8_rows.cu, 7 i8_gemm.cu,
  * 8 i8_umma.cu, 9 i8_decode.cu, 10 f8_rows.cu, 11 f8_gemm.cu, 12 f8_umma.cu,
- * 13 experts.cu; 0 if none failed, and always 0 in libdgemm.so.  Synchronises the device.  Source: none on the pages.
+ * 13 experts.cu, 14 f8_decode.cu; 0 if none failed, and always 0 in libdgemm.so.  Synchronises the device.  Source: none on the pages.
  */
 int dgemm_check_site(void);
 
@@ -668,7 +668,9 @@ int dgemm_tune_i8_next(int variant, int bn, int split);
  *           1: the mma.sync kernel for operands of any alignment;
  *           2: CTA pair, 256 tokens x bn channels (bn 128 or 256);
  *           3: one CTA per 128 channels x bn tokens (bn 16, 32, 64 or 128), `split`
- *              (1..8; 1 for gemm_f8_tn_experts) CTAs of a cluster sharing it along K.
+ *              (1..8; 1 for gemm_f8_tn_experts) CTAs of a cluster sharing it along K;
+ *           4: gemm_f8_tn of at most 8 tokens, mma.sync, blocks of 16 channels and `split`
+ *              (4 or 8) warps.
  * Source: as dgemm_tune_next.
  */
 int dgemm_tune_f8_next(int variant, int bn, int split);
