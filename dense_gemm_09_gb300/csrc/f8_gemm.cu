@@ -10,6 +10,7 @@
 // boundaries, whose bytes it loads one by one, and is bound by those loads.
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -171,30 +172,69 @@ const char *launch_any(const F8Params &p, cudaStream_t stream, const DeviceInfo 
     return "f8_any_64x64";
 }
 
-// Rows of tokens a tile would have on average, and the kernel for them.
+// The kernels' times, fitted to GB300 sweeps: a start, then waves of tiles, each of which takes
+// a CTA (pair) `block` for every 128 of K and `tile` besides; never less than the operands'
+// bytes.  In microseconds, K = 4096, measured and as estimated here: pair 256 x 256 for 8192 x
+// 8192 237 (238), for 512 x 4096 20.9 (20.9); pair 256 x 128 for 512 x 4096 14.4 (14.3), for
+// 256 x 8192 14.7 (14.3); 128 channels x 64 tokens for 128 x 8192 13.4 (13.1), for 256 x 8192
+// 22.0 (21.7); x 32 for 20 x 8192 10.6 (10.6); x 16 for 16 x 8192 11.4 (11.1), split in two
+// 10.3 (10.5); dot products for one token, 8192 channels 8.9 (8.9), 4096 channels 6.4 (6.2).
+struct Kernel {
+    F8Config cfg;
+    int tokens, channels, ctas;  // of a tile
+    double block, block_rows;    // with weights in bands of 128 rows, and with a scale a row
+    double tile;
+};
+constexpr Kernel kKernels[] = {{{kF8Pair, 256, 1}, 256, 256, 2, 0.5, 0.97, 0.4},
+                               {{kF8Pair, 128, 1}, 256, 128, 2, 0.29, 0.42, 0.5},
+                               {{kF8Channels, 64, 1}, 64, 128, 1, 0.25, 0.25, 0.6},
+                               {{kF8Channels, 32, 1}, 32, 128, 1, 0.175, 0.175, 0.5},
+                               {{kF8Channels, 16, 1}, 16, 128, 1, 0.19, 0.19, 0.5}};
+constexpr double kStart = 4.5, kJoin = 2.4, kBytesUs = 6.2e6;
+
 F8Config choose(const F8Params &p, const DeviceInfo &dev)
 {
-    const int64_t tokens = p.offsets ? (p.M + p.experts - 1) / p.experts : p.M;
-    // (weights of more than ~100 MB: even, then the tensor-core kernel)
-    if (!p.offsets && tokens <= kF8DecodeTokens && p.N * p.K <= (int64_t{100} << 20)) return {kF8Decode, 0, 8};
-    if (tokens > 128) return {kF8Pair, 256, 1};
-    const int bn = tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : 128;
-    int split = 1;
-    if (!p.offsets)
-        while (split < 8 && (p.N + 127) / 128 * split * 2 <= dev.sm_count) split *= 2;
-    return {kF8Channels, bn, split};
+    const double nb = static_cast<double>((p.K + kF8Block - 1) / kF8Block);
+    // experts that have rows, at most; rows of each of them, on average
+    const double experts = static_cast<double>(p.offsets ? std::min<int64_t>(p.M, p.experts) : 1), rows = static_cast<double>(p.M) / experts;
+    const double bytes = (experts * static_cast<double>(p.N) + static_cast<double>(p.M)) * static_cast<double>(p.K);
+    F8Config best{};
+    double least = 1e300;
+    auto offer = [&](const F8Config &cfg, double us) {
+        if (us < least) {
+            least = us;
+            best = cfg;
+        }
+    };
+    for (const Kernel &k : kKernels) {
+        // (an expert's last tile is half full on average, if it has more than one)
+        const double tiles_t = p.offsets ? experts * (rows <= k.tokens ? 1.0 : rows / k.tokens + 0.5)
+                                         : static_cast<double>((p.M + k.tokens - 1) / k.tokens);
+        const double tiles = tiles_t * static_cast<double>((p.N + k.channels - 1) / k.channels);
+        const double slots = dev.sm_count / k.ctas, block = p.b.block == kF8Block ? k.block : k.block_rows;
+        for (int split = 1; split <= 8; split *= 2) {
+            if (split > 1 && (k.cfg.variant != kF8Channels || k.tokens > 32 || p.offsets || tiles * split > slots || nb < 2 * split)) break;
+            const double waves = p.offsets ? std::max(1.0, tiles / slots) : std::ceil(tiles * split / slots);
+            const double run = waves * (std::ceil(nb / split) * block + k.tile) + (split > 1 ? kJoin : 0.0);
+            offer({k.cfg.variant, k.cfg.bn, split}, kStart + std::max(run, bytes / kBytesUs));
+        }
+    }
+    if (!p.offsets && p.M <= kF8DecodeTokens) {
+        const double waves = std::ceil(static_cast<double>((p.N + 15) / 16) / (dev.sm_count * 4));
+        offer({kF8Decode, 0, 8}, 3.5 + std::max(waves * std::ceil(nb / 8) * 1.1, bytes / kBytesUs));
+    }
+    return best;
 }
 
 const char *kernel_name(const F8Config &cfg)
 {
     if (cfg.variant == kF8Decode) return cfg.split == 4 ? "f8_decode_4_warps" : "f8_decode_8_warps";
     if (cfg.variant == kF8Pair) return cfg.bn == 256 ? "f8_pair_256x256" : "f8_pair_256x128";
-    static const char *const names[4][4] = {
+    static const char *const names[3][4] = {
         {"f8_channels_128x16", "f8_channels_128x16_split2", "f8_channels_128x16_split4", "f8_channels_128x16_split8"},
         {"f8_channels_128x32", "f8_channels_128x32_split2", "f8_channels_128x32_split4", "f8_channels_128x32_split8"},
-        {"f8_channels_128x64", "f8_channels_128x64_split2", "f8_channels_128x64_split4", "f8_channels_128x64_split8"},
-        {"f8_channels_128x128", "f8_channels_128x128_split2", "f8_channels_128x128_split4", "f8_channels_128x128_split8"}};
-    return names[cfg.bn == 16 ? 0 : cfg.bn == 32 ? 1 : cfg.bn == 64 ? 2 : 3]
+        {"f8_channels_128x64", "f8_channels_128x64_split2", "f8_channels_128x64_split4", "f8_channels_128x64_split8"}};
+    return names[cfg.bn == 16 ? 0 : cfg.bn == 32 ? 1 : 2]
                 [cfg.split == 1 ? 0 : cfg.split <= 2 ? 1 : cfg.split <= 4 ? 2 : 3];
 }
 

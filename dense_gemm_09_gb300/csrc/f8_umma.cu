@@ -18,7 +18,7 @@
 //   warp 0      TMA producer: 128 bytes of K of both operands a stage;
 //   warp 1      MMA issuer (in a pair's other CTA it tells the leader which of its own
 //               stages have landed);
-//   warp 2      the blocks' scales, by asynchronous copies into a ring;
+//   warp 2      the blocks' scales, into a ring;
 //   warp 3      the table of tiles, at the start; then MMA issuer of the second half of
 //               tiles of 256 columns;
 //   warps 4-11  two groups of four: group g has columns g bn / 2 .. of the tile, warp w
@@ -84,7 +84,10 @@ struct Params {
     int stages;
     int boxes;             // staging boxes of an epilogue warp
     int splitk;            // CTAs of a cluster that share a tile (kSwap)
+    int one_row;           // the tile's rows share their scales
+    int a_words, b_words;  // an operand's scales along K lie in 16-byte words
     int tma_store;
+    int tok_rows, chan_rows;  // of a load's box: no more than the operand has
     uint32_t idesc;
     uint32_t wait_limit_us;
     int inject_stall;
@@ -102,7 +105,7 @@ struct Shape {
     static constexpr int kTokens = kSwap ? kBn : kTileRows, kChannels = kSwap ? kRows : kBn;  // of a tile
     // blocks that go from role to role together: a hand-over costs a role some hundred clocks,
     // which a block of few columns does not take
-    static constexpr int kGroup = !kSwap || kBn == 128 ? 1 : kBn == 16 ? 4 : 2;
+    static constexpr int kGroup = !kSwap ? 1 : kBn == 16 ? 4 : 2;
     static constexpr int kBlockBytes = kRowsBytes + kBn / kCtas * kRowBytes;
     static constexpr int kStageBytes = kGroup * kBlockBytes;
     // tiles of 256 columns: an MMA for each epilogue group's half, with accumulators and
@@ -167,6 +170,7 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[kChunk])
                      "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 
+// 4 or 16 bytes from global to shared memory, without a register in between.
 __device__ __forceinline__ void copy_async4(uint32_t dst, const float *src)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -301,26 +305,31 @@ struct Ring {
 // ---- roles
 
 // One stage: blocks kb .. kb_end (a group at most) of this CTA's part of the pair's tile, 128
-// of its rows and half of its columns (by one thread).
+// of its rows and half of its columns (by one thread).  Boxes that hold no row of the operand
+// are left out (loads out of range cost TMA more than loads; what the stage holds in their
+// place meets sums that are not stored).
 template <typename S>
-__device__ __forceinline__ void load_stage(const CUtensorMap *tmap_t, const CUtensorMap *tmap_w, uint32_t ring, Ctrl *ctrl,
-                                           uint32_t slot, const F8Tile &tile, uint32_t rank, int kb, int kb_end)
+__device__ __forceinline__ void load_stage(const CUtensorMap *tmap_t, const CUtensorMap *tmap_w, const Params &p, uint32_t ring,
+                                           Ctrl *ctrl, uint32_t slot, const F8Tile &tile, uint32_t rank, int kb, int kb_end)
 {
     const int32_t tok = tile.t0 + static_cast<int32_t>(rank) * (S::kSwap ? S::kBn / S::kCtas : kRows);
     const int32_t chan = static_cast<int32_t>(tile.n0) + static_cast<int32_t>(rank) * (S::kSwap ? kRows : S::kBn / S::kCtas / S::kHalves);
+    const bool toks = tok < p.c.M, chans[2] = {chan < p.c.N, S::kHalves == 2 && chan + 128 < p.c.N};
     const uint32_t full = ptx::smem_addr(&ctrl->full[slot]);
     const int n = min(S::kGroup, kb_end - kb);
-    ptx::mbar_arrive_expect_tx(full, n * S::kBlockBytes);
+    const int rows = (toks ? p.tok_rows : 0) + (chans[0] ? p.chan_rows : 0) + (chans[1] ? p.chan_rows : 0);
+    ptx::mbar_arrive_expect_tx(full, n * rows * kRowBytes);
 #pragma unroll
     for (int g = 0; g < S::kGroup; ++g) {
         if (g >= n) break;
         const uint32_t dst = ring + slot * S::kStageBytes + g * S::kBlockBytes;
         const int32_t k = (kb + g) * kRowBytes;  // (the innermost coordinate, a multiple of 128 bytes)
-        ptx::tma_load_3d(dst + (S::kSwap ? kRowsBytes : 0), tmap_t, full, k, tok, 0);
+        if (toks) ptx::tma_load_3d(dst + (S::kSwap ? kRowsBytes : 0), tmap_t, full, k, tok, 0);
         // (with halves: of each half's 128 columns, this CTA's 64)
 #pragma unroll
         for (int h = 0; h < S::kHalves; ++h)
-            ptx::tma_load_3d(dst + (S::kSwap ? 0 : kRowsBytes) + h * 64 * kRowBytes, tmap_w, full, k, chan + h * 128, tile.expert);
+            if (chans[h])
+                ptx::tma_load_3d(dst + (S::kSwap ? 0 : kRowsBytes) + h * 64 * kRowBytes, tmap_w, full, k, chan + h * 128, tile.expert);
     }
 }
 
@@ -335,7 +344,7 @@ __device__ __forceinline__ int prefill(const CUtensorMap *tmap_t, const CUtensor
     const F8Tile tile = tile_at<S>(p, table, sc.t0);
     int n = 0;
     for (int kb = sc.kb0; kb < sc.kb1 && n < p.stages; kb += S::kGroup, ++n)
-        load_stage<S>(tmap_t, tmap_w, ring, ctrl, n, tile, rank, kb, sc.kb1);
+        load_stage<S>(tmap_t, tmap_w, p, ring, ctrl, n, tile, rank, kb, sc.kb1);
     return n;
 }
 
@@ -354,7 +363,7 @@ __device__ __forceinline__ void run_producer(const CUtensorMap *tmap_t, const CU
         for (int kb = sc.kb0 + (t == sc.t0 ? done * S::kGroup : 0); kb < sc.kb1; kb += S::kGroup) {
             ok = role_wait<1>(ptx::smem_addr(&ctrl->empty[st.slot]), st.phase ^ 1u, wc);
             if (!ok) break;
-            if (elect_one()) load_stage<S>(tmap_t, tmap_w, ring, ctrl, st.slot, tile, rank, kb, sc.kb1);
+            if (elect_one()) load_stage<S>(tmap_t, tmap_w, p, ring, ctrl, st.slot, tile, rank, kb, sc.kb1);
             __syncwarp();
             st.next(stages);
         }
@@ -441,60 +450,99 @@ __device__ __forceinline__ void run_mma(const Params &p, const F8Table &table, u
     __syncwarp();
 }
 
-// The scales of kSpan blocks at a time: the CTA's 128 rows', then the tile's columns'
-// (kUniform: one for each group of columns).  Rows past the operand take its last one's,
-// for sums that are not stored.
+// A row's scales of n blocks (kSpan at most) from p on; `words`: they lie in 16-byte words.
+__device__ __forceinline__ void load_span(const float *p, int64_t blk, bool words, int n, float (&v)[kSpan])
+{
+    if (words && n == kSpan) {
+#pragma unroll
+        for (int j = 0; j < kSpan; j += 4) {
+            const uint4 w = load_v4(p + j);
+            v[j] = __uint_as_float(w.x);
+            v[j + 1] = __uint_as_float(w.y);
+            v[j + 2] = __uint_as_float(w.z);
+            v[j + 3] = __uint_as_float(w.w);
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < kSpan; ++j) v[j] = j < n ? load_f32(p + j * blk) : 0.f;
+}
+
+// The scales of kSpan blocks at a time: the CTA's 128 rows' (or the one number that they
+// share: channels in bands of 128), then the tile's columns' (kUniform: one for each group
+// of columns).  By asynchronous copies, each of which takes ~6 clocks a lane, also where all
+// lanes read one address: so what rows share is copied once, and the columns of narrow tiles
+// go through registers.  Rows past the operand have none, for sums that are not stored.
 template <typename S>
 __device__ __forceinline__ void run_scales(const Params &p, const F8Table &table, uint32_t scales, Ctrl *ctrl, uint32_t rank,
                                            int lane, uint32_t wc)
 {
-    constexpr int kR = kRows / 32, kC = S::kUniform ? 1 : (S::kBn + 31) / 32;
     const Sched sc = schedule<S>(p, table);
     const F8Operand &ro = S::kSwap ? p.c.b : p.c.a, &co = S::kSwap ? p.c.a : p.c.b;
-    // a row's scales of a span as 16-byte words, where they lie so
-    const bool words = ro.s_blk == 1 && ro.s_row % 4 == 0 && sc.kb0 % 4 == 0 && p.c.sb_stride % 4 == 0 &&
-                       (reinterpret_cast<uintptr_t>(ro.scale) & 15u) == 0;
+    const bool in_words = sc.kb0 % 4 == 0;
+    const bool row_words = in_words && (S::kSwap ? p.b_words : p.a_words), col_words = in_words && (S::kSwap ? p.a_words : p.b_words);
     Ring st;
     bool ok = true;
     for (uint32_t t = sc.t0; ok && t < sc.tiles; t += sc.dt) {
         const F8Tile tile = tile_at<S>(p, table, t);
-        const float *weights = p.c.b.scale + tile.expert * p.c.sb_stride;
-        auto place = [&](bool token, int64_t i) {
-            const F8Operand &o = token ? p.c.a : p.c.b;
-            const int64_t at = token ? min(tile.t0 + i, p.c.M - 1) : min(tile.n0 + i, p.c.N - 1);
-            return (token ? o.scale : weights) + o.band(at) * o.s_row;
+        // of row (column) i of the tile: its scales from block kb on, or null
+        auto place = [&](const F8Operand &o, bool token, int i, int kb) -> const float * {
+            const int64_t at = token ? static_cast<int64_t>(tile.t0) + i : tile.n0 + i;
+            if (at >= (token ? p.c.M : p.c.N)) return nullptr;
+            return o.scale + (token ? 0 : tile.expert * p.c.sb_stride) + o.band(at) * o.s_row + kb * o.s_blk;
         };
-        const float *row[kR], *col[kC];
-#pragma unroll
-        for (int i = 0; i < kR; ++i) row[i] = place(!S::kSwap, rank * kRows + i * 32 + lane);
-#pragma unroll
-        for (int i = 0; i < kC; ++i) col[i] = place(S::kSwap, S::kUniform ? (lane & 1) * S::kWgCols : i * 32 + lane);
         for (int kb = sc.kb0; kb < sc.kb1; kb += kSpan) {
             ok = role_wait<1>(ptx::smem_addr(&ctrl->sc_empty[st.slot]), st.phase ^ 1u, wc);
             if (!ok) break;
             const uint32_t dst = scales + st.slot * S::kSlotBytes, cols = dst + kRows * kRowPitch * 4;
             const int n = min(kSpan, sc.kb1 - kb);
-            if (words && n == kSpan) {
-#pragma unroll
-                for (int i = 0; i < kR; ++i)
-#pragma unroll
-                    for (int j = 0; j < kSpan; j += 4) copy_async16(dst + ((i * 32 + lane) * kRowPitch + j) * 4, row[i] + kb + j);
+            if (p.one_row) {
+                if (lane < n) copy_async4(dst + lane * 4, place(ro, !S::kSwap, 0, kb + lane));
             } else {
 #pragma unroll 1
-                for (int j = 0; j < n; ++j)
+                for (int i = 0; i < kRows; i += 32) {
+                    const float *src = place(ro, !S::kSwap, static_cast<int>(rank) * kRows + i + lane, kb);
+                    const uint32_t to = dst + (i + lane) * kRowPitch * 4;
+                    if (!src) continue;
+                    if (row_words && n == kSpan) {
 #pragma unroll
-                    for (int i = 0; i < kR; ++i) copy_async4(dst + ((i * 32 + lane) * kRowPitch + j) * 4, row[i] + (kb + j) * ro.s_blk);
+                        for (int j = 0; j < kSpan; j += 4) copy_async16(to + j * 4, src + j);
+                    } else {
+                        for (int j = 0; j < n; ++j) copy_async4(to + j * 4, src + j * ro.s_blk);
+                    }
+                }
+                __syncwarp();
             }
+            if constexpr (S::kUniform) {
+                const int j = lane % kSpan, group = lane / kSpan;
+                if (group < 2 && j < n)
+                    if (const float *src = place(co, S::kSwap, group * S::kWgCols, kb + j))
+                        copy_async4(cols + (group * kSpan + j) * 4, src);
+            } else if constexpr (!S::kSwap) {
 #pragma unroll 1
-            for (int j = 0; j < n; ++j) {
-                if constexpr (S::kUniform) {
-                    if (lane < 2) copy_async4(cols + (lane * kSpan + j) * 4, col[0] + (kb + j) * co.s_blk);
-                } else {
+                for (int i = 0; i < S::kBn; i += 32)
+                    if (const float *src = place(co, S::kSwap, i + lane, kb))
+                        for (int j = 0; j < n; ++j) copy_async4(cols + (j * S::kBn + i + lane) * 4, src + j * co.s_blk);
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < S::kBn; i += 64) {
+                    float v[2][kSpan];
 #pragma unroll
-                    for (int i = 0; i < kC; ++i)
-                        if (i * 32 + lane < S::kBn) copy_async4(cols + (j * S::kBn + i * 32 + lane) * 4, col[i] + (kb + j) * co.s_blk);
+                    for (int h = 0; h < 2; ++h) {
+                        const int c = i + h * 32 + lane;
+                        if (c < S::kBn)
+                            if (const float *src = place(co, S::kSwap, c, kb)) load_span(src, co.s_blk, col_words, n, v[h]);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int c = i + h * 32 + lane;
+                        if (c >= S::kBn) continue;
+#pragma unroll
+                        for (int j = 0; j < kSpan; ++j) ptx::st_shared_f32(cols + (j * S::kBn + c) * 4, v[h][j]);
+                    }
                 }
             }
+            __syncwarp();
             ptx::cp_async_mbar_arrive_noinc(ptx::smem_addr(&ctrl->sc_full[st.slot]));
             st.next(kScaleSlots);
         }
@@ -885,19 +933,20 @@ __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap 
 {
     const Sched sc = schedule<S>(p, table);
     const int quarter = warp & 3, group = (warp - 4) >> 2, row = quarter * 32 + lane;
+    const int sc_row = S::kSwap && p.one_row ? 0 : row;
     const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + group * S::kWgCols;
     const uint32_t my_box = box + static_cast<uint32_t>(warp - 4) * p.boxes * kBoxBytes;
     Epi e{{}, {}, sc.groups(S::kGroup), 0};
     uint64_t sum[S::kWgCols / 2];
     if (S::kSwap && p.splitk > 1) {  // one tile, uniform over the cluster
         const F8Tile tile = tile_at<S>(p, table, sc.t0);
-        sum_tile<S>(p, ctrl, scales, taddr, row, group, sc.kb1 - sc.kb0, lane, e, sum, wc);  // (a time-out raises the abort flag)
+        sum_tile<S>(p, ctrl, scales, taddr, sc_row, group, sc.kb1 - sc.kb0, lane, e, sum, wc);  // (a time-out raises the abort flag)
         __syncwarp();
         if constexpr (S::kSwap) join_split<S>(p, tile, ring, row, group, tile.n0 + row, sum, wc);
         return;
     }
     for (uint32_t t = sc.t0; t < sc.tiles; t += sc.dt) {
-        if (!sum_tile<S>(p, ctrl, scales, taddr, row, group, sc.kb1 - sc.kb0, lane, e, sum, wc)) break;
+        if (!sum_tile<S>(p, ctrl, scales, taddr, sc_row, group, sc.kb1 - sc.kb0, lane, e, sum, wc)) break;
         const F8Tile tile = tile_at<S>(p, table, t);
         if constexpr (S::kSwap) {
             store_channels_any<S, S::kWgCols>(p, sum, tile.n0 + rank * kRows + row, tile.t0 + group * S::kWgCols, tile.t_end);
@@ -1091,13 +1140,18 @@ bool launch(const F8Params &c, int splitk, cudaStream_t stream)
     const int smem = set_rings<S>(p);
     if (fit < 1 || p.stages < 2 || (p.splitk > 1 && tiles > fit)) return false;
     constexpr int kTokBox = S::kSwap ? S::kBn / S::kCtas : kRows, kChanBox = S::kSwap ? kRows : S::kBn / S::kCtas / S::kHalves;
+    p.one_row = S::kSwap && c.b.block == kF8Block;
+    p.a_words = c.a.s_blk == 1 && c.a.s_row % 4 == 0 && aligned16(c.a.scale);
+    p.b_words = c.b.s_blk == 1 && c.b.s_row % 4 == 0 && c.sb_stride % 4 == 0 && aligned16(c.b.scale);
     const uint64_t k = static_cast<uint64_t>(c.K), m = static_cast<uint64_t>(c.M), n = static_cast<uint64_t>(c.N);
+    p.tok_rows = static_cast<int>(std::min<int64_t>(kTokBox, c.M));
+    p.chan_rows = static_cast<int>(std::min<int64_t>(kChanBox, c.N));
     CUtensorMap mt{}, mw{}, mo{};
     if (!encode_tiled_3d(&mt, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.a.p, {k, m, 1}, {static_cast<uint64_t>(c.a.ld), m * c.a.ld},
-                         {kRowBytes, kTokBox, 1}, CU_TENSOR_MAP_SWIZZLE_128B) ||
+                         {kRowBytes, static_cast<uint32_t>(p.tok_rows), 1}, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_tiled_3d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.b.p, {k, n, static_cast<uint64_t>(c.experts)},
                          {static_cast<uint64_t>(c.b.ld), c.experts > 1 ? static_cast<uint64_t>(c.b_stride) : n * c.b.ld},
-                         {kRowBytes, kChanBox, 1}, CU_TENSOR_MAP_SWIZZLE_128B))
+                         {kRowBytes, static_cast<uint32_t>(p.chan_rows), 1}, CU_TENSOR_MAP_SWIZZLE_128B))
         return false;
     if (!S::kSwap) {
         const int e = c.c_type == DGEMM_TYPE_F32 ? 4 : 2;
@@ -1130,7 +1184,7 @@ bool f8_umma_config_ok(const F8Config &cfg)
     switch (cfg.variant) {
     case kF8Pair: return cfg.bn == 128 || cfg.bn == 256;
     case kF8Channels:
-        return (cfg.bn == 16 || cfg.bn == 32 || cfg.bn == 64 || cfg.bn == 128) && cfg.split >= 1 && cfg.split <= 8;
+        return (cfg.bn == 16 || cfg.bn == 32 || cfg.bn == 64) && cfg.split >= 1 && cfg.split <= 8;
     default: return false;
     }
 }
@@ -1147,8 +1201,7 @@ bool launch_f8_umma(const F8Params &c, const F8Config &cfg, cudaStream_t stream)
     switch (cfg.bn) {
     case 16: return launch<Shape<1, true, 16, false>>(c, cfg.split, stream);
     case 32: return launch<Shape<1, true, 32, false>>(c, cfg.split, stream);
-    case 64: return launch<Shape<1, true, 64, false>>(c, cfg.split, stream);
-    default: return launch<Shape<1, true, 128, false>>(c, cfg.split, stream);
+    default: return launch<Shape<1, true, 64, false>>(c, cfg.split, stream);
     }
 }
 

@@ -667,7 +667,7 @@ int dgemm_tune_i8_next(int variant, int bn, int split);
  *   variant 0: automatic (the default);
  *           1: the mma.sync kernel for operands of any alignment;
  *           2: CTA pair, 256 tokens x bn channels (bn 128 or 256);
- *           3: one CTA per 128 channels x bn tokens (bn 16, 32, 64 or 128), `split`
+ *           3: one CTA per 128 channels x bn tokens (bn 16, 32 or 64), `split`
  *              (1..8; 1 for gemm_f8_tn_experts) CTAs of a cluster sharing it along K;
  *           4: gemm_f8_tn of at most 8 tokens, mma.sync, blocks of 16 channels and `split`
  *              (4 or 8) warps.

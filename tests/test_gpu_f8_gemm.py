@@ -17,8 +17,8 @@ def dg():
 
 
 # (variant, bn, split) of tune_f8_next; None: the library's choice
-KERNELS = [None, (1, 0, 1), (2, 128, 1), (2, 256, 1), (3, 16, 1), (3, 16, 4), (3, 32, 2), (3, 64, 1), (3, 64, 8), (3, 128, 1),
-           (3, 128, 3), (4, 0, 4), (4, 0, 8)]
+KERNELS = [None, (1, 0, 1), (2, 128, 1), (2, 256, 1), (3, 16, 1), (3, 16, 4), (3, 32, 2), (3, 64, 1), (3, 64, 8), (3, 64, 3),
+           (4, 0, 4), (4, 0, 8)]
 
 
 def tune(dg, kernel):
