@@ -95,11 +95,13 @@ struct Params {
 
 // One kernel: kCtas CTAs share an MMA; kSwap: the rows are channels and the columns
 // tokens; kBn columns to a tile; kUniform: the scales of a group's columns are one number
-// (bands of 128 channels).
-template <int kCtas_, bool kSwap_, int kBn_, bool kUniform_>
+// (bands of 128 channels); kExtra: the call may have a bias or a beta (a kernel of their own
+// for the CTA pairs: without, the sums of 256 columns just fit the registers, and 8 bytes a
+// thread that do not cost 8192 x 8192 x 4096 20 of 237 us).
+template <int kCtas_, bool kSwap_, int kBn_, bool kUniform_, bool kExtra_>
 struct Shape {
     static constexpr int kCtas = kCtas_, kBn = kBn_;
-    static constexpr bool kSwap = kSwap_, kUniform = kUniform_;
+    static constexpr bool kSwap = kSwap_, kUniform = kUniform_, kExtra = kExtra_;
     static constexpr int kWgCols = kBn / 2;                     // columns of an epilogue group
     static constexpr int kTileRows = kRows * kCtas;
     static constexpr int kTokens = kSwap ? kBn : kTileRows, kChannels = kSwap ? kRows : kBn;  // of a tile
@@ -724,55 +726,107 @@ __device__ __forceinline__ uint32_t pack_bits(float a, float b)
     }
 }
 
-// Rows = tokens: the bias and the old C added to this lane's sums, if the call has them.  (Apart
-// from the stores, whose code, fetched anew for each tile, is a tenth of this.)
-template <typename T, int kCols>
-__device__ __forceinline__ void add_bias_and_old(const Params &p, uint64_t (&sum)[kCols / 2], int64_t row, int64_t row_end, int64_t col0)
+// Rows = tokens: the bias added to this lane's sums, if the call has one.  (Apart from the
+// stores, whose code, fetched anew for each tile, is a tenth of this.)
+template <int kCols>
+__device__ __forceinline__ void add_bias(const Params &p, uint64_t (&sum)[kCols / 2], int64_t col0)
 {
-    constexpr int kPer = 16 / sizeof(T);  // values of a 16-byte word
-    const float beta = p.c.beta;
-    if (!p.c.bias && beta == 0.f) return;
-    const T *const C = static_cast<const T *>(p.c.C) + row * p.c.ldc;
-    const bool words = (reinterpret_cast<uintptr_t>(p.c.C) & 15u) == 0 && p.c.ldc % kPer == 0;
+    if (!p.c.bias) return;
 #pragma unroll
-    for (int w = 0; w < kCols; w += kPer) {
-        const int64_t c = col0 + w;
-        float v[kPer];
+    for (int i = 0; i < kCols; i += 2) {
+        const int64_t c = col0 + i;
+        sum[i / 2] = add2(sum[i / 2], pack2(c < p.c.N ? p.c.bias[c] : 0.f, c + 1 < p.c.N ? p.c.bias[c + 1] : 0.f));
+    }
+}
+
+// Brings the old C of a warp's 32 rows x kCols columns into L2, ahead of their sums.
+template <int kCols>
+__device__ __forceinline__ void prefetch_old(const Params &p, int64_t row, int64_t row_end, int64_t col0)
+{
+    const int e = p.c.c_type == DGEMM_TYPE_F32 ? 4 : 2;
+    if (row >= row_end) return;
+    const char *src = static_cast<const char *>(p.c.C) + (row * p.c.ldc + col0) * e;
+    for (int b = 0; b < kCols * e && col0 + b / e < p.c.N; b += 128) ptx::prefetch_l2(src + b);
+}
+
+// The old C of a box (32 rows of 128 bytes from row0 and column c) into it, 8 lanes a row.
+template <typename T>
+__device__ __forceinline__ void load_old_box(const Params &p, uint32_t buf, int64_t row0, int64_t row_end, int64_t c, bool words, int lane)
+{
+    constexpr int kPer = 16 / sizeof(T);
+    const T *const C = static_cast<const T *>(p.c.C);
+    const uint32_t w = lane & 7u;
+    const int64_t cw = c + w * kPer;
+#pragma unroll 1
+    for (int i = 0; i < 32; i += 16) {
+        uint4 q[4];
 #pragma unroll
-        for (int i = 0; i < kPer; i += 2) unpack2(sum[(w + i) / 2], v[i], v[i + 1]);
-        if (p.c.bias) {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (c + i < p.c.N) v[i] += p.c.bias[c + i];
-        }
-        if (beta != 0.f && row < row_end) {
-            if (words && c + kPer <= p.c.N) {
-                const uint4 q = *reinterpret_cast<const uint4 *>(C + c);
-                const T *o = reinterpret_cast<const T *>(&q);
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) v[i] = fmaf(beta, to_f32(o[i]), v[i]);
+        for (int h = 0; h < 4; ++h) {
+            const int64_t m = row0 + i + h * 4 + (lane >> 3);
+            const T *src = C + m * p.c.ldc + cw;
+            if (m < row_end && words && cw + kPer <= p.c.N) {
+                q[h] = *reinterpret_cast<const uint4 *>(src);
             } else {
+                alignas(16) T v[kPer];
 #pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    if (c + i < p.c.N) v[i] = fmaf(beta, to_f32(C[c + i]), v[i]);
+                for (int k = 0; k < kPer; ++k) v[k] = m < row_end && cw + k < p.c.N ? src[k] : from_f32<T>(0.f);
+                q[h] = *reinterpret_cast<const uint4 *>(v);
             }
         }
 #pragma unroll
-        for (int i = 0; i < kPer; i += 2) sum[(w + i) / 2] = pack2(v[i], v[i + 1]);
+        for (int h = 0; h < 4; ++h) {
+            const uint32_t r = i + h * 4 + (lane >> 3);
+            ptx::st_shared_v4(buf + r * 128u + ((w ^ (r & 7u)) << 4), q[h]);
+        }
     }
+    __syncwarp();
+}
+
+// Rows = tokens: beta times the old C added to a warp's sums, box by box through shared
+// memory (the stores' box, whose last store has to have read it).
+template <typename T, int kCols>
+__device__ __forceinline__ void add_old(const Params &p, uint64_t (&sum)[kCols / 2], int64_t row0, int64_t row_end, int64_t col0,
+                                        uint32_t box, int lane)
+{
+    constexpr int kPer = 16 / sizeof(T), kBoxCols = 128 / sizeof(T);
+    const float beta = p.c.beta;
+    if (beta == 0.f) return;
+    const bool words = (reinterpret_cast<uintptr_t>(p.c.C) & 15u) == 0 && p.c.ldc % kPer == 0;
+    if (lane == 0) ptx::bulk_wait_read<0>();
+#pragma unroll
+    for (int b = 0; b < kCols / kBoxCols; ++b) {
+        const int64_t c = col0 + b * kBoxCols;
+        if (c >= p.c.N) return;
+        __syncwarp();
+        load_old_box<T>(p, box, row0, row_end, c, words, lane);
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            const uint4 q = ld_shared_v4(box + lane * 128u + ((w ^ (lane & 7u)) << 4));
+            const T *o = reinterpret_cast<const T *>(&q);
+#pragma unroll
+            for (int i = 0; i < kPer; i += 2) {
+                uint64_t &s = sum[(b * kBoxCols + w * kPer + i) / 2];
+                s = fma2(pack2(to_f32(o[i]), to_f32(o[i + 1])), pack2(beta, beta), s);
+            }
+        }
+    }
+    __syncwarp();
 }
 
 // Rows = tokens: a warp's 32 rows from `row0` (up to row_end) x kCols columns from col0.  Boxes
 // of 128 bytes of columns are staged in shared memory (128-byte swizzle: word w of row r at
 // w ^ (r mod 8)) and stored by TMA, or, where the box holds rows that are not the expert's
 // or TMA cannot describe C, word by word, 8 lanes a row.
-template <typename T, int kCols>
+template <typename T, int kCols, bool kExtra>
 __device__ __forceinline__ void store_tokens(const Params &p, const CUtensorMap *tmap_o, uint64_t (&sum)[kCols / 2], int64_t row0,
                                              int64_t row_end, int64_t col0, uint32_t box, int lane, uint32_t &nbox)
 {
     constexpr int kPer = 16 / sizeof(T), kBoxCols = 128 / sizeof(T);  // values of a word, of a row of the box
     if (row0 >= row_end) return;  // warp-uniform
-    add_bias_and_old<T, kCols>(p, sum, row0 + lane, row_end, col0);
+    if constexpr (kExtra) {
+        add_bias<kCols>(p, sum, col0);
+        add_old<T, kCols>(p, sum, row0, row_end, col0, box, lane);
+    }
     T *const C = static_cast<T *>(p.c.C);
     const bool whole = p.tma_store && (!p.c.offsets || row0 + 32 <= row_end);
     const bool words = (reinterpret_cast<uintptr_t>(C) & 15u) == 0 && p.c.ldc % kPer == 0;
@@ -793,12 +847,13 @@ __device__ __forceinline__ void store_tokens(const Params &p, const CUtensorMap 
             float v[kPer];
 #pragma unroll
             for (int i = 0; i < kPer; i += 2) unpack2(sum[(b * kBoxCols + w * kPer + i) / 2], v[i], v[i + 1]);
+            const uint32_t word = buf + lane * 128u + ((w ^ (lane & 7u)) << 4);
             uint4 q;
             if constexpr (sizeof(T) == 2)
                 q = make_uint4(pack_bits<T>(v[0], v[1]), pack_bits<T>(v[2], v[3]), pack_bits<T>(v[4], v[5]), pack_bits<T>(v[6], v[7]));
             else
                 q = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-            ptx::st_shared_v4(buf + lane * 128u + ((w ^ (lane & 7u)) << 4), q);
+            ptx::st_shared_v4(word, q);
         }
         if (whole) {
             ptx::fence_proxy_async_smem();  // the TMA store reads through the async proxy
@@ -946,6 +1001,10 @@ __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap 
         return;
     }
     for (uint32_t t = sc.t0; t < sc.tiles; t += sc.dt) {
+        if (!S::kSwap && S::kExtra && p.c.beta != 0.f) {
+            const F8Tile tile = tile_at<S>(p, table, t);
+            prefetch_old<S::kWgCols>(p, static_cast<int64_t>(tile.t0) + rank * kRows + row, tile.t_end, tile.n0 + group * S::kWgCols);
+        }
         if (!sum_tile<S>(p, ctrl, scales, taddr, sc_row, group, sc.kb1 - sc.kb0, lane, e, sum, wc)) break;
         const F8Tile tile = tile_at<S>(p, table, t);
         if constexpr (S::kSwap) {
@@ -953,9 +1012,9 @@ __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap 
         } else {
             const int64_t row0 = tile.t0 + rank * kRows + quarter * 32, col0 = tile.n0 + group * S::kWgCols;
             switch (p.c.c_type) {
-            case DGEMM_TYPE_F32: store_tokens<float, S::kWgCols>(p, tmap_o, sum, row0, tile.t_end, col0, my_box, lane, e.nbox); break;
-            case DGEMM_TYPE_F16: store_tokens<__half, S::kWgCols>(p, tmap_o, sum, row0, tile.t_end, col0, my_box, lane, e.nbox); break;
-            default: store_tokens<__nv_bfloat16, S::kWgCols>(p, tmap_o, sum, row0, tile.t_end, col0, my_box, lane, e.nbox);
+            case DGEMM_TYPE_F32: store_tokens<float, S::kWgCols, S::kExtra>(p, tmap_o, sum, row0, tile.t_end, col0, my_box, lane, e.nbox); break;
+            case DGEMM_TYPE_F16: store_tokens<__half, S::kWgCols, S::kExtra>(p, tmap_o, sum, row0, tile.t_end, col0, my_box, lane, e.nbox); break;
+            default: store_tokens<__nv_bfloat16, S::kWgCols, S::kExtra>(p, tmap_o, sum, row0, tile.t_end, col0, my_box, lane, e.nbox);
             }
         }
         __syncwarp();
@@ -1177,6 +1236,15 @@ bool launch(const F8Params &c, int splitk, cudaStream_t stream)
     return true;
 }
 
+template <int kBn>
+bool launch_pair(const F8Params &c, cudaStream_t stream)
+{
+    const bool uniform = c.b.block == kF8Block, extra = c.bias || c.beta != 0.f;
+    if (uniform)
+        return extra ? launch<Shape<2, false, kBn, true, true>>(c, 1, stream) : launch<Shape<2, false, kBn, true, false>>(c, 1, stream);
+    return extra ? launch<Shape<2, false, kBn, false, true>>(c, 1, stream) : launch<Shape<2, false, kBn, false, false>>(c, 1, stream);
+}
+
 }  // namespace
 
 bool f8_umma_config_ok(const F8Config &cfg)
@@ -1192,16 +1260,11 @@ bool f8_umma_config_ok(const F8Config &cfg)
 bool launch_f8_umma(const F8Params &c, const F8Config &cfg, cudaStream_t stream)
 {
     if (!f8_umma_config_ok(cfg)) return false;
-    if (cfg.variant == kF8Pair) {
-        const bool uniform = c.b.block == kF8Block;
-        if (cfg.bn == 256)
-            return uniform ? launch<Shape<2, false, 256, true>>(c, 1, stream) : launch<Shape<2, false, 256, false>>(c, 1, stream);
-        return uniform ? launch<Shape<2, false, 128, true>>(c, 1, stream) : launch<Shape<2, false, 128, false>>(c, 1, stream);
-    }
+    if (cfg.variant == kF8Pair) return cfg.bn == 256 ? launch_pair<256>(c, stream) : launch_pair<128>(c, stream);
     switch (cfg.bn) {
-    case 16: return launch<Shape<1, true, 16, false>>(c, cfg.split, stream);
-    case 32: return launch<Shape<1, true, 32, false>>(c, cfg.split, stream);
-    default: return launch<Shape<1, true, 64, false>>(c, cfg.split, stream);
+    case 16: return launch<Shape<1, true, 16, false, true>>(c, cfg.split, stream);
+    case 32: return launch<Shape<1, true, 32, false, true>>(c, cfg.split, stream);
+    default: return launch<Shape<1, true, 64, false, true>>(c, cfg.split, stream);
     }
 }
 
