@@ -99,7 +99,8 @@ __device__ __forceinline__ uint32_t f32x2_to_f8x2(float lo, float hi)
 // unsigned order is the order of the values, infinities and then NaNs last).
 template <bool kE5>
 struct F8Block {
-    float scale, inv, factor;
+    float scale, inv;  // inv: 0 of zeros, and of a block that is not finite
+    bool tiny;         // y is multiplied by 2^100 before inv
 
     __device__ __forceinline__ explicit F8Block(uint32_t most_bits)
     {
@@ -107,28 +108,31 @@ struct F8Block {
         const float a = __uint_as_float(most_bits);
         const bool finite = most_bits < 0x7F800000u;
         scale = finite ? a / kTop : __uint_as_float(0x7FC00000u);
-        factor = a < 0x1p-100f ? 0x1p100f : 1.f;
-        inv = finite && a > 0.f ? kTop / (a * factor) : 0.f;
-    }
-
-    // eight values; a block that is not finite gives zeros (its products with inv = 0
-    // may be NaN)
-    __device__ __forceinline__ uint2 eight(const float (&y)[8]) const
-    {
-        if (inv == 0.f) return make_uint2(0u, 0u);
-        uint32_t h[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float lo = y[2 * i], hi = y[2 * i + 1];
-            if (factor != 1.f) {
-                lo *= factor;
-                hi *= factor;
-            }
-            h[i] = f32x2_to_f8x2<kE5>(lo * inv, hi * inv);
-        }
-        return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+        tiny = a < 0x1p-100f && a > 0.f;
+        inv = finite && a > 0.f ? kTop / (tiny ? a * 0x1p100f : a) : 0.f;
     }
 };
+
+// Eight values of one block, or (inv[i]) of eight.  Without a factor they give zeros (their
+// product with 0 may be NaN).
+template <bool kE5>
+__device__ __forceinline__ uint2 f8_eight(const float (&y)[8], float inv)
+{
+    uint32_t h[4];
+    uint64_t inv2;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(inv2) : "f"(inv));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint64_t v;
+        float lo, hi;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(y[2 * i]), "f"(y[2 * i + 1]));
+        asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(inv2));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+        h[i] = f32x2_to_f8x2<kE5>(lo, hi);
+    }
+    if (inv == 0.f) return make_uint2(0u, 0u);
+    return make_uint2(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410));
+}
 
 }  // namespace
 #endif

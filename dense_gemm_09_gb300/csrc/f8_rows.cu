@@ -57,49 +57,68 @@ __device__ __forceinline__ void store_bytes(uint8_t *p, int n, uint2 b)
         if (i < n) p[i] = static_cast<uint8_t>((i < 4 ? b.x : b.y) >> (8 * (i & 3)));
 }
 
-// A warp takes 2 * kMany consecutive blocks, two at a time, all of them loaded
-// before the first is worked on.
+// A warp takes 2 * kMany consecutive blocks, two at a time, all of them loaded before the
+// first is worked on.  Their maxima meet in one lane each, which forms the block's scale and
+// factor: one division of either kind for all of them.
 template <int kOp, typename T, bool kAligned, bool kE5, int kMany>
 __global__ void __launch_bounds__(kThreads) f8_rows_kernel(const RowParams p)
 {
     chain_wait();
     chain_next();
-    const int lane = threadIdx.x & (kLanes - 1);
-    const uint32_t half = (threadIdx.x >> 4) & 1u, warp = threadIdx.x >> 5;
-    const uint32_t total = p.rows * p.blocks;
+    const int lane = threadIdx.x & (kLanes - 1), half = (threadIdx.x >> 4) & 1;
+    const uint32_t warp = threadIdx.x >> 5, total = p.rows * p.blocks;
     const uint32_t first = (blockIdx.x * (kThreads / 32) + warp) * (2 * kMany) + half;
     uint32_t row[kMany], col[kMany];
     int n[kMany];
     Raw<T> x[kMany], u[kMany];
+    uint32_t r = first / p.blocks, b = first - r * p.blocks;
 #pragma unroll
     for (int i = 0; i < kMany; ++i) {
-        const uint32_t g = first + 2 * i;
-        row[i] = g / p.blocks;
-        col[i] = (g - row[i] * p.blocks) * kF8Block + lane * kVec;
-        n[i] = g < total && col[i] < p.cols ? static_cast<int>(min(p.cols - col[i], static_cast<uint32_t>(kVec))) : 0;
+        row[i] = r;
+        col[i] = b * kF8Block + lane * kVec;
+        n[i] = r < p.rows && col[i] < p.cols ? static_cast<int>(min(p.cols - col[i], static_cast<uint32_t>(kVec))) : 0;
         x[i] = load_raw<T, kAligned>(static_cast<const T *>(p.x) + static_cast<int64_t>(row[i]) * p.ldx + col[i], n[i]);
         if constexpr (kOp == kOpSwiglu)
             u[i] = load_raw<T, kAligned>(static_cast<const T *>(p.u) + static_cast<int64_t>(row[i]) * p.ldu + col[i], n[i]);
+        b += 2;
+        while (b >= p.blocks) {
+            b -= p.blocks;
+            ++r;
+        }
     }
+    float v[kMany][kVec];
+    uint32_t mine = 0;  // of block `lane`
 #pragma unroll
     for (int i = 0; i < kMany; ++i) {
-        float v[kVec];
-        unpack(x[i], v);
+        unpack(x[i], v[i]);
         if constexpr (kOp == kOpSwiglu) {
             float w[kVec];
             unpack(u[i], w);
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) v[k] = silu(v[k]) * w[k];
+            for (int k = 0; k < kVec; ++k) v[i][k] = silu(v[i][k]) * w[k];
         }
-        uint32_t most = __float_as_uint(max_abs(0.f, v)) & 0x7FFFFFFFu;
+        uint32_t most = __float_as_uint(max_abs(0.f, v[i])) & 0x7FFFFFFFu;
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-        const F8Block<kE5> block(most);
-        const uint2 b = block.eight(v);
+        if (lane == i) mine = most;
+    }
+    const F8Block<kE5> block(mine);
+    if (__any_sync(0xFFFFFFFFu, lane < kMany && block.tiny)) {
+#pragma unroll
+        for (int i = 0; i < kMany; ++i) {
+            const float times = __shfl_sync(0xFFFFFFFFu, block.tiny ? 0x1p100f : 1.f, half * kLanes + i);
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) v[i][k] *= times;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kMany; ++i) {
+        const float inv = __shfl_sync(0xFFFFFFFFu, block.inv, half * kLanes + i);
+        const uint2 bytes = f8_eight<kE5>(v[i], inv);
         const bool in = first + 2 * i < total;
-        auto put = [&](int64_t r) {
-            if (DGEMM_CHECK(col[i] + n[i] <= p.cols || n[i] == 0)) store_bytes<kAligned>(p.q + r * p.ldq + col[i], n[i], b);
-            if (lane == 0) p.scale[r * p.s_row + (col[i] / kF8Block) * p.s_blk] = block.scale;
+        auto put = [&](int64_t to) {
+            if (DGEMM_CHECK(col[i] + n[i] <= p.cols || n[i] == 0)) store_bytes<kAligned>(p.q + to * p.ldq + col[i], n[i], bytes);
+            if (lane == i) p.scale[to * p.s_row + (col[i] / kF8Block) * p.s_blk] = block.scale;
         };
         if constexpr (kOp != kOpGather) {
             if (in) put(row[i]);
@@ -122,93 +141,171 @@ struct TileParams {
     int64_t ldq;
     float *scale;
     int64_t s_row, s_blk;
-    uint32_t tiles_c;
+    uint32_t tiles, tiles_c;
 };
 
-// A thread block holds a tile of 128 x 128 values, 8 rows of a vector a thread.
-// kTransposed: thread t has rows 8 (t / 16) .. and columns 8 (t mod 16) .., so that
-// each of its columns is one 8-byte word of a row of Q^T; the words meet in shared
-// memory, word w of row c at w ^ (c / 8), which keeps both the columns' stores and
-// the rows' loads on distinct banks.
-template <typename T, bool kAligned, bool kAlignedQ, bool kE5, bool kTransposed>
-__global__ void __launch_bounds__(kThreads) f8_tile_kernel(const TileParams p)
+// 16 bytes from global to shared memory, of which `bytes` are read and the rest are zeros.
+__device__ __forceinline__ void copy_async16(uint4 *dst, const void *src, int bytes)
 {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(bytes)
+                 : "memory");
+}
+
+constexpr int kTileSlots = 3;  // tiles of a thread block in shared memory: one worked on, two on their way
+
+template <typename T>
+constexpr size_t tile_smem()
+{
+    return static_cast<size_t>(kTileSlots) * kF8Block * kF8Block * sizeof(T);
+}
+
+// A thread block takes one tile of 128 x 128 values after another, 8 vectors of it a thread,
+// while the next two are on their way to shared memory (each thread fetches the vectors that
+// it will use itself; rows off 16 bytes are loaded when their turn comes).
+// kTransposed: thread t has rows 8 (t / 16) .. and columns 8 (t mod 16) .., so that each of its
+// columns is one 8-byte word of a row of Q^T; the words meet in shared memory, word w of row c
+// at w ^ (c / 8), which keeps both the columns' stores and the rows' loads on distinct banks.
+template <typename T, bool kAligned, bool kAlignedQ, bool kE5, bool kTransposed>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) f8_tile_kernel(const TileParams p)
+{
+    extern __shared__ uint4 slots[];  // [slot][vector][word][thread]
+    constexpr int kWords = Raw<T>::kWords, kPer = 16 / sizeof(T);
     __shared__ uint32_t s_most[kF8Block];
+    __shared__ float s_inv[kF8Block];
     __shared__ uint2 s_word[kTransposed ? kF8Block * kLanes : 1];
     const int t = threadIdx.x, lane = t & (kLanes - 1), group = t / kLanes;
-    if (t < kF8Block) s_most[t] = 0u;
+    auto row_of = [&](int i) { return kTransposed ? group * 8 + i : i * (kThreads / kLanes) + group; };
+    auto origin = [&](uint32_t tile, int64_t &r0, int64_t &c0) {
+        r0 = static_cast<int64_t>(tile / p.tiles_c) * kF8Block;
+        c0 = static_cast<int64_t>(tile % p.tiles_c) * kF8Block;
+    };
+    auto slot_of = [&](int slot, int i, int w) { return slots + ((slot * 8 + i) * kWords + w) * kThreads + t; };
+    auto fetch = [&](uint32_t tile, int slot) {
+        if (kAligned && tile < p.tiles) {
+            int64_t r0, c0;
+            origin(tile, r0, c0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int64_t row = r0 + row_of(i), col = c0 + lane * kVec;
+                const int n = row < p.rows ? vec_len(p.cols, col) : 0;
+                const T *src = static_cast<const T *>(p.x) + (n > 0 ? row * p.ldx + col : 0);
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) {
+                    const int in = max(0, min(kPer, n - w * kPer));
+                    copy_async16(slot_of(slot, i, w), in > 0 ? src + w * kPer : src, in * static_cast<int>(sizeof(T)));
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
     chain_wait();
     chain_next();
-    const int64_t r0 = static_cast<int64_t>(blockIdx.x / p.tiles_c) * kF8Block;
-    const int64_t c0 = static_cast<int64_t>(blockIdx.x % p.tiles_c) * kF8Block;
-    const int64_t col = c0 + lane * kVec;
-    const int n = vec_len(p.cols, col);
-    Raw<T> x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int64_t row = r0 + (kTransposed ? group * 8 + i : i * (kThreads / kLanes) + group);
-        x[i] = load_raw<T, kAligned>(static_cast<const T *>(p.x) + (row < p.rows ? row * p.ldx + col : 0),
-                                     row < p.rows ? n : 0);
-    }
-    __syncthreads();
-    if constexpr (!kTransposed) {
-        float amax = 0.f;
+    int slot = 0;
+    fetch(blockIdx.x, 0);
+    fetch(blockIdx.x + gridDim.x, 1);
+    for (uint32_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+        int64_t r0, c0;
+        origin(tile, r0, c0);
+        const int64_t col = c0 + lane * kVec;
+        const int n = vec_len(p.cols, col);
+        if (t < kF8Block) s_most[t] = 0u;
+        fetch(tile + 2 * gridDim.x, slot >= 1 ? slot - 1 : kTileSlots - 1);  // (the slot of the tile before)
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+        Raw<T> x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float v[kVec];
-            unpack(x[i], v);
-            amax = max_abs(amax, v);
+            if constexpr (kAligned) {
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) x[i].w[w] = *slot_of(slot, i, w);
+            } else {
+                const int64_t row = r0 + row_of(i);
+                x[i] = load_raw<T, false>(static_cast<const T *>(p.x) + (row < p.rows ? row * p.ldx + col : 0), row < p.rows ? n : 0);
+            }
         }
-        const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax) & 0x7FFFFFFFu);
-        if ((t & 31) == 0) atomicMax(&s_most[0], most);
+        slot = slot + 1 == kTileSlots ? 0 : slot + 1;
         __syncthreads();
-        const F8Block<kE5> block(s_most[0]);
-        if (t == 0) p.scale[(r0 / kF8Block) * p.s_row + (c0 / kF8Block) * p.s_blk] = block.scale;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t row = r0 + i * (kThreads / kLanes) + group;
-            float v[kVec];
-            unpack(x[i], v);
-            if (row < p.rows && DGEMM_CHECK(col + n <= p.cols || n == 0))
-                store_bytes<kAlignedQ>(p.q + row * p.ldq + col, n, block.eight(v));
-        }
-    } else {
-        float most[kVec] = {};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float v[kVec];
-            unpack(x[i], v);
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) most[k] = max3_abs(most[k], v[k], 0.f);
-        }
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) {
-            uint32_t m = __float_as_uint(most[k]) & 0x7FFFFFFFu;
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));  // the warp's other eight rows
-            if ((t & 16) == 0) atomicMax(&s_most[lane * kVec + k], m);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) {
-            const int c = lane * kVec + k;
-            const F8Block<kE5> block(s_most[c]);
-            if (group == 0 && k < n) p.scale[(c0 + c) * p.s_row + (r0 / kF8Block) * p.s_blk] = block.scale;
-            float y[kVec];  // the column's eight rows
+        // the largest magnitude of the tile, or of each of this thread's columns
+        if constexpr (!kTransposed) {
+            float amax = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 float v[kVec];
                 unpack(x[i], v);
-                y[i] = v[k];
+                amax = max_abs(amax, v);
             }
-            s_word[c * kLanes + (group ^ lane)] = block.eight(y);
+            const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax) & 0x7FFFFFFFu);
+            if ((t & 31) == 0) atomicMax(&s_most[0], most);
+        } else {
+            float most[kVec] = {};
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                float v[kVec], w[kVec];
+                unpack(x[i], v);
+                unpack(x[i + 1], w);
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) most[k] = max3_abs(most[k], v[k], w[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) {
+                uint32_t m = __float_as_uint(most[k]) & 0x7FFFFFFFu;
+                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));  // the warp's other eight rows
+                if ((t & 16) == 0) atomicMax(&s_most[lane * kVec + k], m);
+            }
         }
         __syncthreads();
-        const int left = vec_len(p.rows, r0 + lane * kVec);  // of this thread's word of each row of Q
+        if constexpr (!kTransposed) {
+            const F8Block<kE5> block(s_most[0]);
+            if (t == 0) p.scale[(r0 / kF8Block) * p.s_row + (c0 / kF8Block) * p.s_blk] = block.scale;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = i * (kThreads / kLanes) + group;
-            if (c0 + c < p.cols)
-                store_bytes<kAlignedQ>(p.q + (c0 + c) * p.ldq + r0 + lane * kVec, left, s_word[c * kLanes + (lane ^ (c / 8))]);
+            for (int i = 0; i < 8; ++i) {
+                const int64_t row = r0 + row_of(i);
+                float v[kVec];
+                unpack(x[i], v);
+                if (block.tiny) {
+#pragma unroll
+                    for (int k = 0; k < kVec; ++k) v[k] *= 0x1p100f;
+                }
+                if (row < p.rows && DGEMM_CHECK(col + n <= p.cols || n == 0))
+                    store_bytes<kAlignedQ>(p.q + row * p.ldq + col, n, f8_eight<kE5>(v, block.inv));
+            }
+            __syncthreads();  // s_most has been read
+        } else {
+            bool tiny = false;
+            if (t < kF8Block) {  // one thread a column: its scale and factor
+                const F8Block<kE5> block(s_most[t]);
+                s_inv[t] = block.inv;
+                tiny = block.tiny;
+                if (c0 + t < p.cols) p.scale[(c0 + t) * p.s_row + (r0 / kF8Block) * p.s_blk] = block.scale;
+            }
+            const bool some_tiny = __syncthreads_or(tiny) != 0;
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) {
+                const int c = lane * kVec + k;
+                float y[kVec];  // the column's eight rows
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float v[kVec];
+                    unpack(x[i], v);
+                    y[i] = v[k];
+                }
+                if (some_tiny && __uint_as_float(s_most[c]) < 0x1p-100f) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] *= 0x1p100f;
+                }
+                s_word[c * kLanes + (group ^ lane)] = f8_eight<kE5>(y, s_inv[c]);
+            }
+            __syncthreads();
+            const int left = vec_len(p.rows, r0 + lane * kVec);  // of this thread's word of each row of Q
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = i * (kThreads / kLanes) + group;
+                if (c0 + c < p.cols)
+                    store_bytes<kAlignedQ>(p.q + (c0 + c) * p.ldq + r0 + lane * kVec, left, s_word[c * kLanes + (lane ^ (c / 8))]);
+            }
+            // (s_most is written again behind the barrier that the words are written behind; the
+            // words behind the next tile's)
         }
     }
 }
@@ -329,13 +426,24 @@ const char *launch_rows_op(int type, int64_t rows, int64_t cols, const void *x, 
     }
 }
 
+template <typename T, bool kAligned, bool kAlignedQ, bool kE5, bool kTransposed>
+bool launch_tile_kernel(const TileParams &p, cudaStream_t stream)
+{
+    auto kernel = f8_tile_kernel<T, kAligned, kAlignedQ, kE5, kTransposed>;
+    constexpr size_t smem = kAligned ? tile_smem<T>() : 0;
+    constexpr uint32_t most = 152 * (sizeof(T) == 2 ? 2 : 1);  // thread blocks that run at once
+    if (smem > 0 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+        return false;
+    return launch_chained(kernel, p.tiles < most ? p.tiles : most, kThreads, smem, stream, 1, p) == cudaSuccess;
+}
+
 template <typename T, bool kE5, bool kTransposed>
-cudaError_t launch_tiles_aligned(const TileParams &p, unsigned grid, cudaStream_t stream)
+bool launch_tiles_aligned(const TileParams &p, cudaStream_t stream)
 {
     const bool x = aligned(p.x, p.ldx, sizeof(T), 16), q = aligned(p.q, p.ldq, 1, 8);
-    if (x && q) return launch_chained(f8_tile_kernel<T, true, true, kE5, kTransposed>, grid, kThreads, 0, stream, 1, p);
-    if (x) return launch_chained(f8_tile_kernel<T, true, false, kE5, kTransposed>, grid, kThreads, 0, stream, 1, p);
-    return launch_chained(f8_tile_kernel<T, false, false, kE5, kTransposed>, grid, kThreads, 0, stream, 1, p);
+    if (x && q) return launch_tile_kernel<T, true, true, kE5, kTransposed>(p, stream);
+    if (x) return launch_tile_kernel<T, true, false, kE5, kTransposed>(p, stream);
+    return launch_tile_kernel<T, false, false, kE5, kTransposed>(p, stream);
 }
 
 template <typename T>
@@ -343,7 +451,7 @@ const char *launch_tiles(int64_t rows, int64_t cols, const void *x, int64_t ldx,
                          cudaStream_t stream)
 {
     const int64_t tiles_c = (cols - 1) / kF8Block + 1, tiles_r = (rows - 1) / kF8Block + 1;
-    const int64_t most = INT32_MAX / tiles_c;  // bands of one launch
+    const int64_t most = kMostUnits / tiles_c;  // bands of one launch
     const bool e5 = q.type == DGEMM_F8_E5M2;
     for (int64_t b = 0; b < tiles_r; b += most) {
         const int64_t bands = tiles_r - b < most ? tiles_r - b : most, r = b * kF8Block;
@@ -358,12 +466,10 @@ const char *launch_tiles(int64_t rows, int64_t cols, const void *x, int64_t ldx,
         p.s_row = q.scale_row;
         p.s_blk = q.scale_blk;
         p.tiles_c = static_cast<uint32_t>(tiles_c);
-        const unsigned grid = static_cast<unsigned>(bands * tiles_c);
-        const cudaError_t st = transposed ? (e5 ? launch_tiles_aligned<T, true, true>(p, grid, stream)
-                                                : launch_tiles_aligned<T, false, true>(p, grid, stream))
-                                          : (e5 ? launch_tiles_aligned<T, true, false>(p, grid, stream)
-                                                : launch_tiles_aligned<T, false, false>(p, grid, stream));
-        if (st != cudaSuccess) return nullptr;
+        p.tiles = static_cast<uint32_t>(bands * tiles_c);
+        const bool done = transposed ? (e5 ? launch_tiles_aligned<T, true, true>(p, stream) : launch_tiles_aligned<T, false, true>(p, stream))
+                                     : (e5 ? launch_tiles_aligned<T, true, false>(p, stream) : launch_tiles_aligned<T, false, false>(p, stream));
+        if (!done) return nullptr;
     }
     return transposed ? "f8_quantize_transposed" : "f8_quantize_blocks";
 }
