@@ -161,16 +161,50 @@ constexpr size_t tile_smem()
     return static_cast<size_t>(kTileSlots) * kF8Block * kF8Block * sizeof(T);
 }
 
+// The columns that a thread has of a tile: eight in a row, or (FP32) four and, 64 on, four more,
+// so that the 16-byte words of neighbouring threads lie side by side: copies of every other
+// word read each sector of L2 twice (16384 x 8192 in blocks 169 us).
+template <typename T>
+struct TileCols {
+    static constexpr bool kSplit = sizeof(T) == 4;
+    static __device__ __forceinline__ int at(int lane, int k) { return kSplit ? (k >> 2) * 64 + lane * 4 + (k & 3) : lane * kVec + k; }
+    static __device__ __forceinline__ int lane_of(int c) { return kSplit ? (c & 63) >> 2 : c / kVec; }
+};
+
+// A thread's eight bytes of a row at q (column c0 of the tile on, `left` columns there).
+template <typename T, bool kAligned>
+__device__ __forceinline__ void store_tile_bytes(uint8_t *q, int lane, int left, uint2 b)
+{
+    if constexpr (!TileCols<T>::kSplit) {
+        store_bytes<kAligned>(q + lane * kVec, max(0, min(kVec, left - lane * kVec)), b);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = TileCols<T>::at(lane, 4 * h), n = left - c;
+            const uint32_t w = h ? b.y : b.x;
+            if (kAligned && n >= 4 && DGEMM_CHECK((reinterpret_cast<uintptr_t>(q + c) & 3u) == 0)) {
+                *reinterpret_cast<uint32_t *>(q + c) = w;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k < n) q[c + k] = static_cast<uint8_t>(w >> (8 * k));
+            }
+        }
+    }
+}
+
 // A thread block takes one tile of 128 x 128 values after another, 8 vectors of it a thread,
 // while the next two are on their way to shared memory (each thread fetches the vectors that
 // it will use itself; rows off 16 bytes are loaded when their turn comes).
-// kTransposed: thread t has rows 8 (t / 16) .. and columns 8 (t mod 16) .., so that each of its
-// columns is one 8-byte word of a row of Q^T; the words meet in shared memory, word w of row c
-// at w ^ (c / 8), which keeps both the columns' stores and the rows' loads on distinct banks.
+// kTransposed: thread t has rows 8 (t / 16) .. and the columns of t mod 16, so that each of
+// its columns is one 8-byte word of a row of Q^T; the words meet in shared memory, word w of
+// row c at w ^ (the thread that has it, mod 16), which keeps both the columns' stores and the
+// rows' loads on distinct banks.
 template <typename T, bool kAligned, bool kAlignedQ, bool kE5, bool kTransposed>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) f8_tile_kernel(const TileParams p)
 {
     extern __shared__ uint4 slots[];  // [slot][vector][word][thread]
+    using Cols = TileCols<T>;
     constexpr int kWords = Raw<T>::kWords, kPer = 16 / sizeof(T);
     __shared__ uint32_t s_most[kF8Block];
     __shared__ float s_inv[kF8Block];
@@ -188,13 +222,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) f8_tile_kern
             origin(tile, r0, c0);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int64_t row = r0 + row_of(i), col = c0 + lane * kVec;
-                const int n = row < p.rows ? vec_len(p.cols, col) : 0;
-                const T *src = static_cast<const T *>(p.x) + (n > 0 ? row * p.ldx + col : 0);
+                const int64_t row = r0 + row_of(i);
+                const T *src = static_cast<const T *>(p.x) + (row < p.rows ? row * p.ldx : 0);
 #pragma unroll
                 for (int w = 0; w < kWords; ++w) {
-                    const int in = max(0, min(kPer, n - w * kPer));
-                    copy_async16(slot_of(slot, i, w), in > 0 ? src + w * kPer : src, in * static_cast<int>(sizeof(T)));
+                    const int64_t col = c0 + Cols::at(lane, w * kPer), left = row < p.rows ? p.cols - col : 0;
+                    const int in = left >= kPer ? kPer : left > 0 ? static_cast<int>(left) : 0;
+                    copy_async16(slot_of(slot, i, w), in > 0 ? src + col : src, in * static_cast<int>(sizeof(T)));
                 }
             }
         }
@@ -208,8 +242,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) f8_tile_kern
     for (uint32_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
         int64_t r0, c0;
         origin(tile, r0, c0);
-        const int64_t col = c0 + lane * kVec;
-        const int n = vec_len(p.cols, col);
+        const int cols = static_cast<int>(min(p.cols - c0, static_cast<int64_t>(kF8Block)));  // of the tile
         if (t < kF8Block) s_most[t] = 0u;
         fetch(tile + 2 * gridDim.x, slot >= 1 ? slot - 1 : kTileSlots - 1);  // (the slot of the tile before)
         asm volatile("cp.async.wait_group 2;" ::: "memory");
@@ -221,7 +254,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) f8_tile_kern
                 for (int w = 0; w < kWords; ++w) x[i].w[w] = *slot_of(slot, i, w);
             } else {
                 const int64_t row = r0 + row_of(i);
-                x[i] = load_raw<T, false>(static_cast<const T *>(p.x) + (row < p.rows ? row * p.ldx + col : 0), row < p.rows ? n : 0);
+                const T *src = static_cast<const T *>(p.x) + (row < p.rows ? row * p.ldx + c0 : 0);
+                alignas(16) T e[kVec];
+#pragma unroll
+                for (int k = 0; k < kVec; ++k)
+                    e[k] = row < p.rows && Cols::at(lane, k) < cols ? src[Cols::at(lane, k)] : from_f32<T>(0.f);
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) x[i].w[w] = reinterpret_cast<const uint4 *>(e)[w];
             }
         }
         slot = slot + 1 == kTileSlots ? 0 : slot + 1;
@@ -251,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) f8_tile_kern
             for (int k = 0; k < kVec; ++k) {
                 uint32_t m = __float_as_uint(most[k]) & 0x7FFFFFFFu;
                 m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));  // the warp's other eight rows
-                if ((t & 16) == 0) atomicMax(&s_most[lane * kVec + k], m);
+                if ((t & 16) == 0) atomicMax(&s_most[Cols::at(lane, k)], m);
             }
         }
         __syncthreads();
@@ -267,8 +306,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) f8_tile_kern
 #pragma unroll
                     for (int k = 0; k < kVec; ++k) v[k] *= 0x1p100f;
                 }
-                if (row < p.rows && DGEMM_CHECK(col + n <= p.cols || n == 0))
-                    store_bytes<kAlignedQ>(p.q + row * p.ldq + col, n, f8_eight<kE5>(v, block.inv));
+                if (row < p.rows && DGEMM_CHECK(c0 + cols <= p.cols))
+                    store_tile_bytes<T, kAlignedQ>(p.q + row * p.ldq + c0, lane, cols, f8_eight<kE5>(v, block.inv));
             }
             __syncthreads();  // s_most has been read
         } else {
@@ -282,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) f8_tile_kern
             const bool some_tiny = __syncthreads_or(tiny) != 0;
 #pragma unroll
             for (int k = 0; k < kVec; ++k) {
-                const int c = lane * kVec + k;
+                const int c = Cols::at(lane, k);
                 float y[kVec];  // the column's eight rows
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -302,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) f8_tile_kern
             for (int i = 0; i < 8; ++i) {
                 const int c = i * (kThreads / kLanes) + group;
                 if (c0 + c < p.cols)
-                    store_bytes<kAlignedQ>(p.q + (c0 + c) * p.ldq + r0 + lane * kVec, left, s_word[c * kLanes + (lane ^ (c / 8))]);
+                    store_bytes<kAlignedQ>(p.q + (c0 + c) * p.ldq + r0 + lane * kVec, left, s_word[c * kLanes + (lane ^ Cols::lane_of(c))]);
             }
             // (s_most is written again behind the barrier that the words are written behind; the
             // words behind the next tile's)
