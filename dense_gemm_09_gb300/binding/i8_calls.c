@@ -426,7 +426,7 @@ static int f8_scale(PyObject *t, const char *name, int64_t rows, int64_t cols, i
     q->scale_blk = shape[1] > 1 ? stride[1] : 1;
     if (written && shape[0] > 1 && shape[1] > 1) {
         const int64_t a = q->scale_row, b = q->scale_blk;
-        if (!(a >= b * shape[1] || b >= a * shape[0])) {
+        if (a < 1 || b < 1 || !(a >= b * shape[1] || b >= a * shape[0])) {
             PyErr_Format(PyExc_ValueError, "%s has overlapping elements", name);
             return -1;
         }
