@@ -230,12 +230,11 @@ const char *kernel_name(const F8Config &cfg)
 {
     if (cfg.variant == kF8Decode) return cfg.split == 4 ? "f8_decode_4_warps" : "f8_decode_8_warps";
     if (cfg.variant == kF8Pair) return cfg.bn == 256 ? "f8_pair_256x256" : "f8_pair_256x128";
-    static const char *const names[3][4] = {
-        {"f8_channels_128x16", "f8_channels_128x16_split2", "f8_channels_128x16_split4", "f8_channels_128x16_split8"},
-        {"f8_channels_128x32", "f8_channels_128x32_split2", "f8_channels_128x32_split4", "f8_channels_128x32_split8"},
-        {"f8_channels_128x64", "f8_channels_128x64_split2", "f8_channels_128x64_split4", "f8_channels_128x64_split8"}};
-    return names[cfg.bn == 16 ? 0 : cfg.bn == 32 ? 1 : 2]
-                [cfg.split == 1 ? 0 : cfg.split <= 2 ? 1 : cfg.split <= 4 ? 2 : 3];
+#define DGEMM_F8_SPLITS(name) {name, name "_split2", name "_split3", name "_split4", name "_split5", name "_split6", name "_split7", name "_split8"}
+    static const char *const names[3][8] = {DGEMM_F8_SPLITS("f8_channels_128x16"), DGEMM_F8_SPLITS("f8_channels_128x32"),
+                                            DGEMM_F8_SPLITS("f8_channels_128x64")};
+#undef DGEMM_F8_SPLITS
+    return names[cfg.bn == 16 ? 0 : cfg.bn == 32 ? 1 : 2][cfg.split - 1];
 }
 
 }  // namespace
@@ -266,6 +265,7 @@ const char *launch_gemm_f8(const F8Params &p, const F8Config &tune, cudaStream_t
             return cfg.variant == kF8Decode ? launch_f8_decode(p, cfg, stream) : launch_f8_umma(p, cfg, stream);
         };
         F8Config cfg = tune;
+        cfg.split = static_cast<int>(std::min<int64_t>(cfg.split, cfg.variant == kF8Channels ? (p.K - 1) / kF8Block + 1 : 8));
         if (cfg.variant == kF8Auto || !run(cfg)) {
             cfg = choose(p, dev);
             if (!run(cfg)) return launch_any(p, stream, dev);

@@ -750,18 +750,19 @@ __device__ __forceinline__ void prefetch_old(const Params &p, int64_t row, int64
 }
 
 // The old C of a box (32 rows of 128 bytes from row0 and column c) into it, 8 lanes a row.
-template <typename T>
+template <typename T, int kCols>
 __device__ __forceinline__ void load_old_box(const Params &p, uint32_t buf, int64_t row0, int64_t row_end, int64_t c, bool words, int lane)
 {
     constexpr int kPer = 16 / sizeof(T);
     const T *const C = static_cast<const T *>(p.c.C);
     const uint32_t w = lane & 7u;
     const int64_t cw = c + w * kPer;
+    constexpr int kMany = kCols <= 64 ? 8 : 4;  // words of a lane on their way (as the sums leave registers)
 #pragma unroll 1
-    for (int i = 0; i < 32; i += 16) {
-        uint4 q[4];
+    for (int i = 0; i < 32; i += 4 * kMany) {
+        uint4 q[kMany];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
+        for (int h = 0; h < kMany; ++h) {
             const int64_t m = row0 + i + h * 4 + (lane >> 3);
             const T *src = C + m * p.c.ldc + cw;
             if (m < row_end && words && cw + kPer <= p.c.N) {
@@ -774,7 +775,7 @@ __device__ __forceinline__ void load_old_box(const Params &p, uint32_t buf, int6
             }
         }
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
+        for (int h = 0; h < kMany; ++h) {
             const uint32_t r = i + h * 4 + (lane >> 3);
             ptx::st_shared_v4(buf + r * 128u + ((w ^ (r & 7u)) << 4), q[h]);
         }
@@ -798,7 +799,7 @@ __device__ __forceinline__ void add_old(const Params &p, uint64_t (&sum)[kCols /
         const int64_t c = col0 + b * kBoxCols;
         if (c >= p.c.N) return;
         __syncwarp();
-        load_old_box<T>(p, box, row0, row_end, c, words, lane);
+        load_old_box<T, kCols>(p, box, row0, row_end, c, words, lane);
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
             const uint4 q = ld_shared_v4(box + lane * 128u + ((w ^ (lane & 7u)) << 4));
@@ -1192,7 +1193,7 @@ bool launch(const F8Params &c, int splitk, cudaStream_t stream)
     p.tiles_n = static_cast<uint32_t>(tiles_n);
     p.tiles_t = static_cast<uint32_t>((c.M + S::kTokens - 1) / S::kTokens);
     p.num_kb = static_cast<int>((c.K + kRowBytes - 1) / kRowBytes);
-    p.splitk = S::kSwap && !c.offsets ? std::min(splitk, p.num_kb) : 1;
+    p.splitk = splitk;
     if (tiles / 76 * p.num_kb > INT32_MAX) return false;  // blocks of one CTA
     const int cluster = S::kCtas == 2 ? 2 : p.splitk;
     const int fit = capacity<S>(cluster);
@@ -1259,7 +1260,7 @@ bool f8_umma_config_ok(const F8Config &cfg)
 
 bool launch_f8_umma(const F8Params &c, const F8Config &cfg, cudaStream_t stream)
 {
-    if (!f8_umma_config_ok(cfg)) return false;
+    if (!f8_umma_config_ok(cfg) || (cfg.split > 1 && (c.offsets || cfg.split > (c.K - 1) / kF8Block + 1))) return false;
     if (cfg.variant == kF8Pair) return cfg.bn == 256 ? launch_pair<256>(c, stream) : launch_pair<128>(c, stream);
     switch (cfg.bn) {
     case 16: return launch<Shape<1, true, 16, false, true>>(c, cfg.split, stream);
