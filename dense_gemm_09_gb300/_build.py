@@ -9,7 +9,7 @@ The checked build (libdgemm_checked.so, objects under _build/checked/) is
 the same sources compiled with -DDGEMM_CHECKED: device-side bounds checks on
 the indices the kernels compute (see csrc/checked.cuh).  build_all() compiles
 both libraries' units at once, and the CPython module that marshals the 8-bit
-calls (binding/i8_calls.c, by gcc), whose file name carries the interpreter's tag:
+calls and those on tokens by expert (binding/i8_calls.c, by gcc), whose file name carries the interpreter's tag:
 another interpreter looks for another file.
 """
 from __future__ import annotations
