@@ -177,20 +177,24 @@ const char *launch_any(const F8Params &p, cudaStream_t stream, const DeviceInfo 
 // bytes.  In microseconds, K = 4096, measured and as estimated here: pair 256 x 256 for 8192 x
 // 8192 237 (238), for 512 x 4096 20.9 (20.9); pair 256 x 128 for 512 x 4096 14.4 (14.3), for
 // 256 x 8192 14.7 (14.3); 128 channels x 64 tokens for 128 x 8192 13.4 (13.1), for 256 x 8192
-// 22.0 (21.7); x 32 for 20 x 8192 10.6 (10.6); x 16 for 16 x 8192 11.4 (11.1), split in two
-// 10.3 (10.5); dot products for one token, 8192 channels 8.9 (8.9), 4096 channels 6.4 (6.2).
+// 22.0 (21.7); x 32 for 20 x 8192 10.6 (11.1); x 16 for 16 x 8192 11.4 (11.1),
+// for 9 x 512, K = 1664, split in four 5.3 (6.9); dot products for one token, 8192 channels
+// 8.9 (8.9), 4096 channels 6.4 (7.9).
 struct Kernel {
     F8Config cfg;
     int tokens, channels, ctas;  // of a tile
     double block, block_rows;    // with weights in bands of 128 rows, and with a scale a row
     double tile;
+    double join;                 // of split sums, for every doubling of the CTAs
 };
-constexpr Kernel kKernels[] = {{{kF8Pair, 256, 1}, 256, 256, 2, 0.5, 0.97, 0.4},
-                               {{kF8Pair, 128, 1}, 256, 128, 2, 0.29, 0.42, 0.5},
-                               {{kF8Channels, 64, 1}, 64, 128, 1, 0.25, 0.25, 0.6},
-                               {{kF8Channels, 32, 1}, 32, 128, 1, 0.175, 0.175, 0.5},
-                               {{kF8Channels, 16, 1}, 16, 128, 1, 0.19, 0.19, 0.5}};
-constexpr double kStart = 4.5, kJoin = 2.4, kBytesUs = 6.2e6;
+// (Narrow tiles first: of kernels that the bytes bound they do best, one token, 8 of 64 experts
+// of 4096 x 2048, x 16 11.3 us, x 32 12.6, x 64 15.1.)
+constexpr Kernel kKernels[] = {{{kF8Channels, 16, 1}, 16, 128, 1, 0.19, 0.19, 0.5, 0.8},
+                               {{kF8Channels, 32, 1}, 32, 128, 1, 0.19, 0.19, 0.5, 1.2},
+                               {{kF8Channels, 64, 1}, 64, 128, 1, 0.25, 0.25, 0.6, 0.0},
+                               {{kF8Pair, 128, 1}, 256, 128, 2, 0.29, 0.42, 0.5, 0.0},
+                               {{kF8Pair, 256, 1}, 256, 256, 2, 0.5, 0.97, 0.4, 0.0}};
+constexpr double kStart = 4.5, kBytesUs = 6.2e6;
 
 F8Config choose(const F8Params &p, const DeviceInfo &dev)
 {
@@ -213,14 +217,14 @@ F8Config choose(const F8Params &p, const DeviceInfo &dev)
         const double tiles = tiles_t * static_cast<double>((p.N + k.channels - 1) / k.channels);
         const double slots = dev.sm_count / k.ctas, block = p.b.block == kF8Block ? k.block : k.block_rows;
         for (int split = 1; split <= 8; split *= 2) {
-            if (split > 1 && (k.cfg.variant != kF8Channels || k.tokens > 32 || p.offsets || tiles * split > slots || nb < 2 * split)) break;
+            if (split > 1 && (k.join == 0.0 || p.offsets || tiles * split > slots || nb < 2 * split)) break;
             const double waves = p.offsets ? std::max(1.0, tiles / slots) : std::ceil(tiles * split / slots);
-            const double run = waves * (std::ceil(nb / split) * block + k.tile) + (split > 1 ? kJoin : 0.0);
+            const double run = waves * (std::ceil(nb / split) * block + k.tile) + k.join * std::log2(split);
             offer({k.cfg.variant, k.cfg.bn, split}, kStart + std::max(run, bytes / kBytesUs));
         }
     }
     if (!p.offsets && p.M <= kF8DecodeTokens) {
-        const double waves = std::ceil(static_cast<double>((p.N + 15) / 16) / (dev.sm_count * 4));
+        const double waves = std::max(1.0, static_cast<double>((p.N + 15) / 16) / (dev.sm_count * 4));
         offer({kF8Decode, 0, 8}, 3.5 + std::max(waves * std::ceil(nb / 8) * 1.1, bytes / kBytesUs));
     }
     return best;
@@ -267,8 +271,9 @@ const char *launch_gemm_f8(const F8Params &p, const F8Config &tune, cudaStream_t
         F8Config cfg = tune;
         cfg.split = static_cast<int>(std::min<int64_t>(cfg.split, cfg.variant == kF8Channels ? (p.K - 1) / kF8Block + 1 : 8));
         if (cfg.variant == kF8Auto || !run(cfg)) {
-            cfg = choose(p, dev);
-            if (!run(cfg)) return launch_any(p, stream, dev);
+            // (clusters that do not fit the GPU all at once are made smaller)
+            for (cfg = choose(p, dev); !run(cfg); cfg.split /= 2)
+                if (cfg.split == 1) return launch_any(p, stream, dev);
         }
         return kernel_name(cfg);
     }

@@ -94,6 +94,13 @@ def test_larger(dg, m, n, k):
         check(dg, m, n, k, out=out, rb=rb)
 
 
+# (clusters of eight, of as many tiles as there are groups of eight SMs, don't all fit the GPU)
+@pytest.mark.parametrize("m,n,k", [(3, 2176, 7040), (9, 2304, 7040), (17, 2432, 4096), (20, 2304, 16384), (40, 1152, 4096)])
+def test_few_rows_and_a_long_k_run_on_the_tensor_cores(dg, m, n, k):
+    assert "any" not in check(dg, m, n, k)
+    assert "any" not in check(dg, m, n, k, kernel=(3, 32, 8))
+
+
 def test_no_k(dg):
     a, b = (torch.empty(r, 0, dtype=torch.float8_e4m3fn, device="cuda") for r in (5, 9))
     sa, sb = torch.empty(5, 0, device="cuda"), torch.empty(9, 0, device="cuda")
