@@ -1138,7 +1138,7 @@ template <typename S>
 int set_rings(Params &p)
 {
     const int fixed = S::kScaleBytes + static_cast<int>(sizeof(Ctrl)) + 8 * (p.c.experts + 1);
-        p.boxes = 0;
+    p.boxes = 0;
     if (!S::kSwap) p.boxes = (kSmemLimit - fixed - 2 * kEpiWarps * kBoxBytes) / S::kStageBytes >= 5 ? 2 : 1;
     const int boxes = kEpiWarps * p.boxes * kBoxBytes;
     p.stages = std::min(kMaxStages, (kSmemLimit - fixed - boxes) / S::kStageBytes);

@@ -375,8 +375,8 @@ int gemm_i8_tn(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, co
  *   elements, at least the row length; sizes of 0 return DGEMM_OK and write
  *   nothing; DGEMM_ERR_INVALID_ARG for negative sizes, more than 2^31 - 1 rows or
  *   columns, leading dimensions below the row length, negative scale strides
- *   (where the scales are written: also 0, if there are several along it), an unknown type or block, or a
- *   NULL pointer that is not said to be optional.  Pointers are aligned to their
+ *   (where the scales are written: also 0, if there are several along it), an
+ *   unknown type or block, or a NULL pointer that is not said to be optional.  Pointers are aligned to their
  *   element type; rows on 16-byte boundaries take the fastest kernels.  Writes
  *   stay within the rows.  Outputs must not overlap inputs, except where a call allows it.
  * Source: none on the pages (their products take 16- and 32-bit operands).
@@ -428,7 +428,9 @@ int dequantize_f8(int64_t rows, int64_t cols, const dgemm_f8 *Q, void *X, int64_
  * stands, dY W on W's transposed data and scales, and dY^T X on quantize_f8's
  * transposed form of both (block 1, beta = 1 to add to a gradient).
  * Sums within a block of 128 are formed by the tensor cores from exact products,
- * in FP32 arithmetic that truncates; sums over blocks in FP32.  One row of A
+ * in FP32 arithmetic that truncates; sums over blocks in FP32.  Two blocks' scales
+ * may be multiplied with each other first: their product has to be in FP32's normal
+ * range (or 0).  One row of A
  * gives the same bits in any batch that takes the same kernel (dgemm_last_kernel).
  * K == 0 gives bias + beta * C.  DGEMM_ERR_INVALID_ARG as above, and for more
  * than 2^31 - 1 tiles of 16 x 64 of C.
