@@ -66,6 +66,19 @@ def test_sort_of_nothing(dg):
         assert offsets.tolist() == [0] * 6
 
 
+@pytest.mark.parametrize("tokens", [20, 257])
+@pytest.mark.parametrize("e", [1, 2, 3, 31, 32, 127, 128, 129, 1023])
+def test_padding_is_no_expert(dg, tokens, e):
+    """Numbers next to the range, and of every bit, among those of each expert."""
+    g = torch.Generator().manual_seed(e)
+    ids = torch.randint(0, e, (tokens, 8), generator=g, dtype=torch.int32)
+    ids[:, ::3] = torch.tensor([-1, e, 2 * e, 2 ** 31 - 1, -2 ** 31], dtype=torch.int64)[
+        torch.randint(0, 5, ids[:, ::3].shape, generator=g)].to(torch.int32)
+    wo, wp = sorted_plain(ids.cuda(), e)
+    offsets, position = sort(dg, ids.cuda(), e)
+    assert torch.equal(offsets.cpu(), wo) and torch.equal(position.cpu(), wp)
+
+
 def test_sort_of_one_expert(dg):
     """Every pair goes to the last expert: the longest run of equal numbers."""
     ids = torch.full((5000, 4), 63, dtype=torch.int32, device="cuda")
