@@ -139,6 +139,12 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 4) f8_decode_kernel(const F8Pa
     const int64_t n = static_cast<int64_t>(blockIdx.x) * kChannels;
     chain_wait();
     chain_next();
+    // the value of C that this thread stores, and its old one, on its way beside the sums
+    static_assert(kChannels * kF8DecodeTokens <= 4 * 32, "a thread for each, of four warps");
+    const int c = static_cast<int>(threadIdx.x) % kChannels, m = static_cast<int>(threadIdx.x) / kChannels;
+    const bool mine = m < p.M && n + c < p.N;
+    T *const dst = static_cast<T *>(p.C) + m * p.ldc + n + c;
+    const float old = mine && p.beta != 0.f ? to_f32(*dst) : 0.f;
     const Places places(p, n, g, q);
     const int whole = static_cast<int>(p.K / kF8Block);  // blocks
     float sum[4] = {};
@@ -165,14 +171,11 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 4) f8_decode_kernel(const F8Pa
 #pragma unroll
     for (int v = 0; v < 4; ++v) s_sum[warp][g + 8 * (v >> 1)][2 * q + (v & 1)] = sum[v];
     __syncthreads();
-    for (int i = threadIdx.x; i < kChannels * static_cast<int>(p.M); i += blockDim.x) {
-        const int c = i % kChannels, m = i / kChannels;
-        if (n + c >= p.N || !DGEMM_CHECK(m < kF8DecodeTokens)) continue;
+    if (mine && DGEMM_CHECK(m < kF8DecodeTokens)) {
         float x = 0.f;
         for (int w = 0; w < warps; ++w) x += s_sum[w][c][m];
         if (p.bias) x += load_f32(p.bias + n + c);
-        T *dst = static_cast<T *>(p.C) + m * p.ldc + n + c;
-        if (p.beta != 0.f) x = fmaf(p.beta, to_f32(*dst), x);
+        if (p.beta != 0.f) x = fmaf(p.beta, old, x);
         *dst = from_f32<T>(x);
     }
 }

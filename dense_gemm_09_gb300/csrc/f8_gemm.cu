@@ -175,25 +175,26 @@ const char *launch_any(const F8Params &p, cudaStream_t stream, const DeviceInfo 
 // The kernels' times, fitted to GB300 sweeps: a start, then waves of tiles, each of which takes
 // a CTA (pair) `block` for every 128 of K and `tile` besides; never less than the operands'
 // bytes.  In microseconds, K = 4096, measured and as estimated here: pair 256 x 256 for 8192 x
-// 8192 237 (238), for 512 x 4096 20.9 (20.9); pair 256 x 128 for 512 x 4096 14.4 (14.3), for
-// 256 x 8192 14.7 (14.3); 128 channels x 64 tokens for 128 x 8192 13.4 (13.1), for 256 x 8192
-// 22.0 (21.7); x 32 for 20 x 8192 10.6 (11.1); x 16 for 16 x 8192 11.4 (11.1),
-// for 9 x 512, K = 1664, split in four 5.3 (6.9); dot products for one token, 8192 channels
-// 8.9 (8.9), 4096 channels 6.4 (7.9).
+// 8192 235 (236), and with a scale a row 354 (357); pair 256 x 128 for 512 x 4096 14.4 (14.4),
+// for 2048 x 4096 of 512 values with the old C, to FP32, 23.7 (23.8), where 256 x 256 takes
+// 29.8 (28.5); 128 channels x 64 tokens for 128 x 8192 13.4 (13.1), for 256 x 8192 22.0 (21.7);
+// x 32 for 20 x 8192 10.6 (11.1); x 16 for 16 x 8192 11.4 (11.1), for 9 x 512, K = 1664, split
+// in four 5.3 (6.9); dot products for one token, 8192 channels 8.9 (8.9), 4096 channels 6.4
+// (7.9).
 struct Kernel {
     F8Config cfg;
     int tokens, channels, ctas;  // of a tile
     double block, block_rows;    // with weights in bands of 128 rows, and with a scale a row
-    double tile;
+    double tile[2][2];           // the stores: [with the old C read][to FP32]
     double join;                 // of split sums, for every doubling of the CTAs
 };
 // (Narrow tiles first: of kernels that the bytes bound they do best, one token, 8 of 64 experts
 // of 4096 x 2048, x 16 11.3 us, x 32 12.6, x 64 15.1.)
-constexpr Kernel kKernels[] = {{{kF8Channels, 16, 1}, 16, 128, 1, 0.19, 0.19, 0.5, 0.8},
-                               {{kF8Channels, 32, 1}, 32, 128, 1, 0.19, 0.19, 0.5, 1.2},
-                               {{kF8Channels, 64, 1}, 64, 128, 1, 0.25, 0.25, 0.6, 0.0},
-                               {{kF8Pair, 128, 1}, 256, 128, 2, 0.29, 0.42, 0.5, 0.0},
-                               {{kF8Pair, 256, 1}, 256, 256, 2, 0.5, 0.97, 0.4, 0.0}};
+constexpr Kernel kKernels[] = {{{kF8Channels, 16, 1}, 16, 128, 1, 0.19, 0.19, {{0.5, 0.5}, {0.9, 0.9}}, 0.8},
+                               {{kF8Channels, 32, 1}, 32, 128, 1, 0.19, 0.19, {{0.5, 0.5}, {1.0, 1.0}}, 1.2},
+                               {{kF8Channels, 64, 1}, 64, 128, 1, 0.25, 0.25, {{0.6, 0.6}, {2.2, 2.2}}, 0.0},
+                               {{kF8Pair, 128, 1}, 256, 128, 2, 0.28, 0.38, {{0.9, 1.1}, {2.4, 3.7}}, 0.0},
+                               {{kF8Pair, 256, 1}, 256, 256, 2, 0.47, 0.74, {{1.5, 2.5}, {5.6, 10.1}}, 0.0}};
 constexpr double kStart = 4.5, kBytesUs = 6.2e6;
 
 F8Config choose(const F8Params &p, const DeviceInfo &dev)
@@ -216,10 +217,11 @@ F8Config choose(const F8Params &p, const DeviceInfo &dev)
                                          : static_cast<double>((p.M + k.tokens - 1) / k.tokens);
         const double tiles = tiles_t * static_cast<double>((p.N + k.channels - 1) / k.channels);
         const double slots = dev.sm_count / k.ctas, block = p.b.block == kF8Block ? k.block : k.block_rows;
+        const double tile = k.tile[p.beta != 0.f][p.c_type == DGEMM_TYPE_F32];
         for (int split = 1; split <= 8; split *= 2) {
             if (split > 1 && (k.join == 0.0 || p.offsets || tiles * split > slots || nb < 2 * split)) break;
             const double waves = p.offsets ? std::max(1.0, tiles / slots) : std::ceil(tiles * split / slots);
-            const double run = waves * (std::ceil(nb / split) * block + k.tile) + k.join * std::log2(split);
+            const double run = waves * (std::ceil(nb / split) * block + tile) + k.join * std::log2(split);
             offer({k.cfg.variant, k.cfg.bn, split}, kStart + std::max(run, bytes / kBytesUs));
         }
     }

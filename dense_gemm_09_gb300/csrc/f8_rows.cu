@@ -11,6 +11,11 @@
 // block's values stay in registers between its maximum and its bytes.  A block of
 // a row is 16 lanes of 8 elements: loads of 16 bytes a lane, the maximum in four
 // shuffles, stores of 8 bytes a lane, without shared memory or barriers.
+//
+// 8192 x 8192, and the time of its bytes at the measured copy rate: bf16 rows 38.1 us
+// (30.1), FP32 50.1 (50), gated bf16 59.7 (50), blocks of 128 x 128 bf16 33.6 (29.8) and FP32
+// 56 (49.6), transposed bf16 42.1 (30.1), back to bf16 32.3 (30.1).  Of the 16-bit forms the
+// instructions bound the rest: the conversion to 8 bits takes 21 values a clock and SM.
 #include <cstdint>
 #include <type_traits>
 
@@ -196,7 +201,7 @@ constexpr size_t tile_smem()
 
 // The columns that a thread has of a tile: eight in a row, or (FP32) four and, 64 on, four more,
 // so that the 16-byte words of neighbouring threads lie side by side: copies of every other
-// word read each sector of L2 twice (16384 x 8192 in blocks 169 us).
+// word read each sector of L2 twice (16384 x 8192 in blocks 169 us, and 110).
 template <typename T>
 struct TileCols {
     static constexpr bool kSplit = sizeof(T) == 4;

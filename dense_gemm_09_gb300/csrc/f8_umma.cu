@@ -8,11 +8,16 @@
 // the accumulator is read back block by block, multiplied by its row's and column's
 // scales and added to sums in registers, in FP32, while the MMAs fill the next one.
 //
-// What bounds it.  For many tokens the tensor pipe: a block of a 256 x 256 tile takes a
-// CTA pair 512 clocks of MMA (8192 products a clock and SM), and each CTA 256 clocks of
-// tensor-memory reads and 128 to 256 of packed FMAs beside them.  For few tokens the
-// weights' bytes: there the channels are the MMA's rows and the tokens its columns
-// (kSwap), so that no row of the tensor cores' work is padding that is loaded.
+// What bounds it.  For many tokens the card's power.  8192 x 8192 x 4096 takes 235 to 247
+// us (2230 to 2340 TFLOP/s) at 1390 of 1400 W and 1950 MHz: ~1000 clocks a block of a 256 x
+// 256 tile, where the MMAs alone take 512 (8192 products a clock and SM) and the packed FMAs
+// of a CTA 256 beside them.  Operands of zeros run in the same number of clocks, at 2070 MHz.
+// Of 137 us for 4864 x 8192 x 4096, 32 go without the FMAs and another 2 without reading the
+// accumulators; fewer clocks a block were not less time (larger pieces of the accumulator
+// read at once, or the next block's first piece ahead: 145 to 159 us, with spilled sums).
+// For few tokens the weights' bytes: there the channels are the MMA's rows and the tokens its
+// columns (kSwap), so that no row of the tensor cores' work is padding that is loaded: 16
+// tokens, 8 of 64 experts of 4096 x 2048 take 66 us, 7.2 TB/s (reads alone go faster than copies).
 //
 // Roles (12 warps):
 //   warp 0      TMA producer: 128 bytes of K of both operands a stage;
@@ -119,7 +124,7 @@ struct Shape {
     // a slot of scales: [row][block], then [group][block] or [block][column]
     static constexpr int kSlotBytes = (kRowPitch * kRows + kSpan * (kUniform ? 2 : kBn)) * 4;
     static constexpr int kScaleBytes = kScaleSlots * kSlotBytes;
-    // sums of 128 columns and 64 more on their way do not fit the 168 registers a thread that
+    // sums of 128 columns and 32 more on their way do not fit the 168 registers a thread that
     // 384 threads share alike: the four other warps give 112 each of theirs
     static constexpr bool kMoveRegs = kWgCols >= 128;
     static_assert(!kMoveRegs || 128 * 56 + 256 * 224 <= 384 * 168, "what is taken was given");
@@ -893,21 +898,39 @@ template <typename T, int kCols>
 __device__ __forceinline__ void store_channels(const Params &p, const uint64_t (&sum)[kCols / 2], int64_t n, int64_t m0, int64_t m_end)
 {
     if (n >= p.c.N) return;
+    constexpr int kMany = kCols == 16 ? 16 : 8;  // old values on their way together
     const float bias = p.c.bias ? p.c.bias[n] : 0.f;
     T *dst = static_cast<T *>(p.c.C) + m0 * p.c.ldc + n;
 #pragma unroll
-    for (int j = 0; j < kCols; j += 2) {
-        float v[2];
-        unpack2(sum[j / 2], v[0], v[1]);
+    for (int j0 = 0; j0 < kCols; j0 += kMany) {
+        T old[kMany];
+        if (p.c.beta != 0.f) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (m0 + j + i >= m_end || !DGEMM_CHECK(m0 + j + i < p.c.M)) continue;
-            T *d = dst + (j + i) * p.c.ldc;
-            float x = v[i] + bias;
-            if (p.c.beta != 0.f) x = fmaf(p.c.beta, to_f32(*d), x);
-            *d = from_f32<T>(x);
+            for (int j = 0; j < kMany; ++j)
+                if (m0 + j0 + j < m_end) old[j] = dst[(j0 + j) * p.c.ldc];
+        }
+#pragma unroll
+        for (int j = 0; j < kMany; j += 2) {
+            float v[2];
+            unpack2(sum[(j0 + j) / 2], v[0], v[1]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (m0 + j0 + j + i >= m_end || !DGEMM_CHECK(m0 + j0 + j + i < p.c.M)) continue;
+                float x = v[i] + bias;
+                if (p.c.beta != 0.f) x = fmaf(p.c.beta, to_f32(old[j + i]), x);
+                dst[(j0 + j + i) * p.c.ldc] = from_f32<T>(x);
+            }
         }
     }
+}
+
+// Brings a warp's old C (32 channels of kCols tokens) into L2, ahead of the sums.
+template <int kCols>
+__device__ __forceinline__ void prefetch_channels(const Params &p, int64_t n, int64_t m0, int64_t m_end, int lane)
+{
+    const int e = p.c.c_type == DGEMM_TYPE_F32 ? 4 : 2;
+    if (n < p.c.N && lane < kCols && m0 + lane < m_end)
+        ptx::prefetch_l2(static_cast<const char *>(p.c.C) + ((m0 + lane) * p.c.ldc + n) * e);
 }
 
 template <typename S, int kCols>
@@ -996,15 +1019,20 @@ __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap 
     uint64_t sum[S::kWgCols / 2];
     if (S::kSwap && p.splitk > 1) {  // one tile, uniform over the cluster
         const F8Tile tile = tile_at<S>(p, table, sc.t0);
+        if (p.c.beta != 0.f)
+            prefetch_channels<S::kWgCols>(p, tile.n0 + quarter * 32, tile.t0 + group * S::kWgCols, tile.t_end, lane);
         sum_tile<S>(p, ctrl, scales, taddr, sc_row, group, sc.kb1 - sc.kb0, lane, e, sum, wc);  // (a time-out raises the abort flag)
         __syncwarp();
         if constexpr (S::kSwap) join_split<S>(p, tile, ring, row, group, tile.n0 + row, sum, wc);
         return;
     }
     for (uint32_t t = sc.t0; t < sc.tiles; t += sc.dt) {
-        if (!S::kSwap && S::kExtra && p.c.beta != 0.f) {
+        if (S::kExtra && p.c.beta != 0.f) {
             const F8Tile tile = tile_at<S>(p, table, t);
-            prefetch_old<S::kWgCols>(p, static_cast<int64_t>(tile.t0) + rank * kRows + row, tile.t_end, tile.n0 + group * S::kWgCols);
+            if constexpr (S::kSwap)
+                prefetch_channels<S::kWgCols>(p, tile.n0 + quarter * 32, tile.t0 + group * S::kWgCols, tile.t_end, lane);
+            else
+                prefetch_old<S::kWgCols>(p, static_cast<int64_t>(tile.t0) + rank * kRows + row, tile.t_end, tile.n0 + group * S::kWgCols);
         }
         if (!sum_tile<S>(p, ctrl, scales, taddr, sc_row, group, sc.kb1 - sc.kb0, lane, e, sum, wc)) break;
         const F8Tile tile = tile_at<S>(p, table, t);
