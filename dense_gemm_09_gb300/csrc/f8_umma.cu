@@ -40,6 +40,7 @@
 #include <cuda_runtime.h>
 
 #include "bounded_wait.cuh"
+#include "box_edge.cuh"
 #include "chained.cuh"
 #include "dgemm.h"
 #include "f8.cuh"
@@ -76,6 +77,7 @@ struct Ctrl {
     uint64_t acc_empty[kMaxAccs];    // leader: every epilogue warp of the pair that reads them has
     uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
     uint64_t mma_done[2];
+    uint64_t old_full[kEpiWarps];    // an epilogue warp's old C has landed in its boxes
     uint64_t never;                  // test hook: a barrier nothing arrives at
     uint32_t stop, limit_us;         // a wait ran out; a wait's limit, in 1024 ns (adjacent, see role_wait)
     uint32_t tmem_base;
@@ -92,6 +94,7 @@ struct Params {
     int one_row;           // the tile's rows share their scales
     int a_words, b_words;  // an operand's scales along K lie in 16-byte words
     int tma_store;
+    int tma_old;           // tiles of 128 columns: the old C comes by TMA too, into the two boxes
     int tok_rows, chan_rows;  // of a load's box: no more than the operand has
     uint32_t idesc;
     uint32_t wait_limit_us;
@@ -564,6 +567,8 @@ struct Epi {
     Ring acc, sc;
     uint32_t left;  // blocks to go
     uint32_t nbox;
+    uint32_t old_phase;  // of the old C's barrier
+    bool old_coming;     // loads of it that nothing has waited for
 };
 
 // The sums of one tile (or of this CTA's blocks of it), two columns a word.  A look at a
@@ -788,6 +793,25 @@ __device__ __forceinline__ void load_old_box(const Params &p, uint32_t buf, int6
     __syncwarp();
 }
 
+// Rows = tokens, tiles of 128 columns: the old C of a warp's 32 rows x kCols columns on its way
+// into the boxes that the sums will be stored from (what lies past C's edges arrives as zeros).
+template <int kCols>
+__device__ __forceinline__ void load_old(const Params &p, const CUtensorMap *tmap_o, int64_t row0, int64_t row_end, int64_t col0,
+                                         uint32_t box, uint32_t bar, int lane, Epi &e)
+{
+    if (row0 >= row_end || col0 >= p.c.N || !DGEMM_CHECK(row0 >= 0 && col0 >= 0 && row0 < p.c.M)) return;  // warp-uniform
+    e.old_coming = true;
+    if (lane == 0) {
+        const int cols = p.c.c_type == DGEMM_TYPE_F32 ? 32 : 64, n = col0 + cols < p.c.N ? kCols / cols : 1;
+        ptx::bulk_wait_read<0>();  // the boxes' last stores have read them
+        ptx::mbar_arrive_expect_tx(bar, n * kBoxBytes);
+        for (int b = 0; b < n; ++b)
+            ptx::tma_load_2d(box + ((e.nbox + b) & 1u) * kBoxBytes, tmap_o, bar, static_cast<int32_t>(col0) + b * cols,
+                             static_cast<int32_t>(row0));
+    }
+    __syncwarp();
+}
+
 // Rows = tokens: beta times the old C added to a warp's sums, box by box through shared
 // memory (the stores' box, whose last store has to have read it).
 template <typename T, int kCols>
@@ -825,13 +849,21 @@ __device__ __forceinline__ void add_old(const Params &p, uint64_t (&sum)[kCols /
 // or TMA cannot describe C, word by word, 8 lanes a row.
 template <typename T, int kCols, bool kExtra>
 __device__ __forceinline__ void store_tokens(const Params &p, const CUtensorMap *tmap_o, uint64_t (&sum)[kCols / 2], int64_t row0,
-                                             int64_t row_end, int64_t col0, uint32_t box, int lane, uint32_t &nbox)
+                                             int64_t row_end, int64_t col0, uint32_t box, int lane, uint32_t bar, uint32_t wc, Epi &e)
 {
     constexpr int kPer = 16 / sizeof(T), kBoxCols = 128 / sizeof(T);  // values of a word, of a row of the box
+    uint32_t &nbox = e.nbox;
     if (row0 >= row_end) return;  // warp-uniform
+    const bool in_box = kExtra && kCols == 64 && e.old_coming;  // the old C is where the sums go
     if constexpr (kExtra) {
         add_bias<kCols>(p, sum, col0);
-        add_old<T, kCols>(p, sum, row0, row_end, col0, box, lane);
+        if (in_box) {
+            if (!role_wait<1>(bar, e.old_phase, wc)) return;
+            e.old_coming = false;
+            e.old_phase ^= 1u;
+        } else {
+            add_old<T, kCols>(p, sum, row0, row_end, col0, box, lane);
+        }
     }
     T *const C = static_cast<T *>(p.c.C);
     const bool whole = p.tma_store && (!p.c.offsets || row0 + 32 <= row_end);
@@ -855,13 +887,19 @@ __device__ __forceinline__ void store_tokens(const Params &p, const CUtensorMap 
             for (int i = 0; i < kPer; i += 2) unpack2(sum[(b * kBoxCols + w * kPer + i) / 2], v[i], v[i + 1]);
             const uint32_t word = buf + lane * 128u + ((w ^ (lane & 7u)) << 4);
             uint4 q;
+            if (in_box) {
+                q = ld_shared_v4(word);
+                const T *o = reinterpret_cast<const T *>(&q);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) v[i] = fmaf(p.c.beta, to_f32(o[i]), v[i]);
+            }
             if constexpr (sizeof(T) == 2)
                 q = make_uint4(pack_bits<T>(v[0], v[1]), pack_bits<T>(v[2], v[3]), pack_bits<T>(v[4], v[5]), pack_bits<T>(v[6], v[7]));
             else
                 q = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
             ptx::st_shared_v4(word, q);
         }
-        if (whole) {
+        if (whole && !box_edge(c, kBoxCols, p.c.N, sizeof(T))) {
             ptx::fence_proxy_async_smem();  // the TMA store reads through the async proxy
             __syncwarp();
             if (lane == 0 && DGEMM_CHECK(row0 >= 0 && c >= 0 && row0 < p.c.M && c < p.c.N)) {
@@ -871,24 +909,7 @@ __device__ __forceinline__ void store_tokens(const Params &p, const CUtensorMap 
             ++nbox;
             continue;
         }
-        __syncwarp();
-#pragma unroll 1
-        for (int i = 0; i < 32; i += 4) {
-            const uint32_t r = i + (lane >> 3), w = lane & 7u;
-            const int64_t m = row0 + r, cw = c + w * kPer;
-            if (m >= row_end || cw >= p.c.N || !DGEMM_CHECK(m < p.c.M)) continue;
-            const uint4 q = ld_shared_v4(buf + r * 128u + ((w ^ (r & 7u)) << 4));
-            T *dst = C + m * p.c.ldc + cw;
-            if (words && cw + kPer <= p.c.N) {
-                *reinterpret_cast<uint4 *>(dst) = q;
-            } else {
-                const T *v = reinterpret_cast<const T *>(&q);
-#pragma unroll
-                for (int k = 0; k < kPer; ++k)
-                    if (cw + k < p.c.N) dst[k] = v[k];
-            }
-        }
-        __syncwarp();  // the box is written again
+        if (DGEMM_CHECK(row_end <= p.c.M)) store_box(C, p.c.ldc, row_end, p.c.N, row0, c, words, buf, lane);
     }
 }
 
@@ -1014,8 +1035,8 @@ __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap 
     const int quarter = warp & 3, group = (warp - 4) >> 2, row = quarter * 32 + lane;
     const int sc_row = S::kSwap && p.one_row ? 0 : row;
     const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + group * S::kWgCols;
-    const uint32_t my_box = box + static_cast<uint32_t>(warp - 4) * p.boxes * kBoxBytes;
-    Epi e{{}, {}, sc.groups(S::kGroup), 0};
+    const uint32_t my_box = box + static_cast<uint32_t>(warp - 4) * p.boxes * kBoxBytes, bar = ptx::smem_addr(&ctrl->old_full[warp - 4]);
+    Epi e{{}, {}, sc.groups(S::kGroup), 0, 0, false};
     uint64_t sum[S::kWgCols / 2];
     if (S::kSwap && p.splitk > 1) {  // one tile, uniform over the cluster
         const F8Tile tile = tile_at<S>(p, table, sc.t0);
@@ -1031,6 +1052,9 @@ __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap 
             const F8Tile tile = tile_at<S>(p, table, t);
             if constexpr (S::kSwap)
                 prefetch_channels<S::kWgCols>(p, tile.n0 + quarter * 32, tile.t0 + group * S::kWgCols, tile.t_end, lane);
+            else if (S::kBn == 128 && p.tma_old)
+                load_old<S::kWgCols>(p, tmap_o, static_cast<int64_t>(tile.t0) + rank * kRows + quarter * 32, tile.t_end,
+                                     tile.n0 + group * S::kWgCols, my_box, bar, lane, e);
             else
                 prefetch_old<S::kWgCols>(p, static_cast<int64_t>(tile.t0) + rank * kRows + row, tile.t_end, tile.n0 + group * S::kWgCols);
         }
@@ -1041,14 +1065,18 @@ __device__ __forceinline__ void run_epilogue(const Params &p, const CUtensorMap 
         } else {
             const int64_t row0 = tile.t0 + rank * kRows + quarter * 32, col0 = tile.n0 + group * S::kWgCols;
             switch (p.c.c_type) {
-            case DGEMM_TYPE_F32: store_tokens<float, S::kWgCols, S::kExtra>(p, tmap_o, sum, row0, tile.t_end, col0, my_box, lane, e.nbox); break;
-            case DGEMM_TYPE_F16: store_tokens<__half, S::kWgCols, S::kExtra>(p, tmap_o, sum, row0, tile.t_end, col0, my_box, lane, e.nbox); break;
-            default: store_tokens<__nv_bfloat16, S::kWgCols, S::kExtra>(p, tmap_o, sum, row0, tile.t_end, col0, my_box, lane, e.nbox);
+            case DGEMM_TYPE_F32: store_tokens<float, S::kWgCols, S::kExtra>(p, tmap_o, sum, row0, tile.t_end, col0, my_box, lane, bar, wc, e); break;
+            case DGEMM_TYPE_F16: store_tokens<__half, S::kWgCols, S::kExtra>(p, tmap_o, sum, row0, tile.t_end, col0, my_box, lane, bar, wc, e); break;
+            default: store_tokens<__nv_bfloat16, S::kWgCols, S::kExtra>(p, tmap_o, sum, row0, tile.t_end, col0, my_box, lane, bar, wc, e);
             }
+            if (e.old_coming) break;  // its wait ran out
         }
         __syncwarp();
     }
-    if (!S::kSwap && lane == 0) ptx::bulk_wait<0>();  // stores done before the CTA leaves
+    if (!S::kSwap && lane == 0) {
+        if (e.old_coming) role_drain(bar, e.old_phase);  // (after an abort)
+        ptx::bulk_wait<0>();                             // loads and stores done before the CTA leaves
+    }
 }
 
 template <typename S>
@@ -1098,6 +1126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(ptx::smem_addr(&ctrl->sc_empty[s]), kEpiWarps);
         }
         for (int h = 0; h < 2; ++h) ptx::mbar_init(ptx::smem_addr(&ctrl->mma_done[h]), 1);
+        for (int w = 0; w < kEpiWarps; ++w) ptx::mbar_init(ptx::smem_addr(&ctrl->old_full[w]), 1);
         ptx::mbar_init(ptx::smem_addr(&ctrl->never), 1);
         ctrl->stop = 0u;
         ctrl->limit_us = p.wait_limit_us;
@@ -1250,6 +1279,7 @@ bool launch(const F8Params &c, int splitk, cudaStream_t stream)
                       encode_tiled_2d(&mo, dt, c.C, n, m, static_cast<uint64_t>(c.ldc) * e, static_cast<uint32_t>(128 / e), 32,
                                       CU_TENSOR_MAP_SWIZZLE_128B);
     }
+    p.tma_old = p.tma_store && p.boxes == 2;
     // D f32; the types of the rows' and the columns' operand; both K-major; N = kBn (or a half), M = 128 rows a CTA
     const uint32_t rows_type = static_cast<uint32_t>((S::kSwap ? c.b : c.a).type), cols_type = static_cast<uint32_t>((S::kSwap ? c.a : c.b).type);
     p.idesc = (1u << 4) | (rows_type << 7) | (cols_type << 10) | (static_cast<uint32_t>(S::kBn / S::kHalves >> 3) << 17) |

@@ -62,6 +62,7 @@
 #include <cuda_runtime.h>
 
 #include "bounded_wait.cuh"
+#include "box_edge.cuh"
 #include "chained.cuh"
 #include "dgemm.h"
 #include "i8_gemm.h"
@@ -610,6 +611,11 @@ __device__ __forceinline__ void drain_tokens(const Params &p, const CUtensorMap 
                     const uint32_t word = static_cast<uint32_t>((part * 16 + j) / kPer);
                     ptx::st_shared_v4(dst + ((word ^ (static_cast<uint32_t>(lane) & 7u)) << 4), q);
                 }
+            }
+            if (box_edge(col0, kCols, p.cols, sizeof(T))) {
+                if (DGEMM_CHECK(row0 >= 0 && col0 >= 0))
+                    store_box(static_cast<T *>(p.c.C), p.c.ldc, p.rows, p.cols, row0, col0, true, buf, lane);
+                continue;
             }
             ptx::fence_proxy_async_smem();  // the TMA store reads through the async proxy
             __syncwarp();

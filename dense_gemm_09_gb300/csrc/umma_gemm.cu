@@ -53,6 +53,7 @@
 #include <cuda_runtime.h>
 
 #include "bounded_wait.cuh"
+#include "box_edge.cuh"
 #include "dgemm.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -651,8 +652,8 @@ __device__ __forceinline__ void store_chunk(const Params &p, int64_t row, int64_
 // f16 or 32 f32 columns), written with the 128-byte swizzle (16-byte chunk j
 // of row r at chunk position j ^ (r mod 8): the 8 rows a wavefront touches
 // fall in distinct banks).  One lane stores a full box with a TMA tensor
-// store, which writes whole lines and clips rows / columns outside C; the
-// next box goes to the other buffer while the first is read out.
+// store, which writes whole lines and clips rows / columns outside C (a box in
+// which N ends inside a 16-byte word is stored by the warp); the next box goes to the other buffer while the first is read out.
 constexpr int EPI_BOX_BYTES = 4096;
 constexpr int EPI_BYTES = 4 * 2 * EPI_BOX_BYTES;  // four warps, two boxes each
 
@@ -817,6 +818,12 @@ __device__ __forceinline__ void drain_rows(const Params &p, const CUtensorMap *t
                                __float_as_uint(v[j * 4 + 2]), __float_as_uint(v[j * 4 + 3]));
             }
             ptx::st_shared_v4(rowbase + ((static_cast<uint32_t>(j) ^ (static_cast<uint32_t>(lane) & 7u)) << 4), q);
+        }
+        if (box_edge(col0, COLS, p.N, Traits<kKind>::kElem)) {
+            using E = std::conditional_t<Traits<kKind>::kElem == 2, uint16_t, float>;
+            if (DGEMM_CHECK(row0 >= 0 && col0 >= 0))
+                store_box(reinterpret_cast<E *>(p.C), p.ldc, p.M, p.N, row0, col0, true, buf, lane);
+            continue;
         }
         ptx::fence_proxy_async_smem();  // make the box visible to the TMA engine
         __syncwarp();

@@ -45,6 +45,27 @@ def test_waits_that_run_out_at_once(tune, m, n, k):
         assert torch.equal(c, want)
 
 
+@pytest.mark.parametrize("m,n", [(300, 700), (2048, 8192)])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_waits_that_run_out_with_the_old_c_on_its_way(m, n, out):
+    import dense_gemm_09_gb300 as dg
+    a, b, sa, sb = operands(m, n, 384)
+    c0 = torch.randn(m, n, device="cuda").to(out)
+    want = c0.clone()
+    dg.tune_f8_next(2, 128, 1)
+    dg.gemm_f8_tn(a, b, want, sa, sb, beta=-1.5)
+    assert dg.device_status(clear=True) == dg.OK
+    for limit in (0, 1, 1000, 3000, 20000):
+        dg.tune_f8_next(2, 128, 1)
+        dg.test_inject_stall(limit)
+        dg.gemm_f8_tn(a, b, c0.clone(), sa, sb, beta=-1.5)
+        assert dg.device_status(clear=True) == dg.ERR_TIMEOUT
+        c = c0.clone()
+        dg.tune_f8_next(2, 128, 1)
+        dg.gemm_f8_tn(a, b, c, sa, sb, beta=-1.5)
+        assert dg.device_status(clear=True) == dg.OK and torch.equal(c, want)
+
+
 def test_a_stalled_launch_by_expert():
     import dense_gemm_09_gb300 as dg
     a, _, sa, _ = operands(600, 1, 512)

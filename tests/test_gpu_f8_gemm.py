@@ -94,6 +94,15 @@ def test_larger(dg, m, n, k):
         check(dg, m, n, k, out=out, rb=rb)
 
 
+@pytest.mark.parametrize("kernel", [(2, 128, 1), (2, 256, 1), (3, 16, 4), (3, 64, 1)], ids=str)
+@pytest.mark.parametrize("out", ref.TYPES)
+@pytest.mark.parametrize("m,n,k,cpad", [(1, 33, 128, 7), (257, 1000, 200, 0), (130, 132, 640, 0), (1100, 2100, 300, 12), (2100, 4160, 400, 0),
+                                        (300, 513, 256, 0)])
+def test_the_old_c(dg, m, n, k, cpad, out, kernel):
+    """Several tiles a CTA, edges inside a box, rows of C on 16 bytes and off them."""
+    check(dg, m, n, k, kernel, 1, 1, "e5m2", "e4m3", out, True, 0.75, cpad=cpad)
+
+
 # (clusters of eight, of as many tiles as there are groups of eight SMs, don't all fit the GPU)
 @pytest.mark.parametrize("m,n,k", [(3, 2176, 7040), (9, 2304, 7040), (17, 2432, 4096), (20, 2304, 16384), (40, 1152, 4096)])
 def test_few_rows_and_a_long_k_run_on_the_tensor_cores(dg, m, n, k):
