@@ -176,8 +176,8 @@ const char *launch_any(const F8Params &p, cudaStream_t stream, const DeviceInfo 
 // a CTA (pair) `block` for every 128 of K and `tile` besides; never less than the operands'
 // bytes.  In microseconds, K = 4096, measured and as estimated here: pair 256 x 256 for 8192 x
 // 8192 235 (236), and with a scale a row 354 (357); pair 256 x 128 for 512 x 4096 14.4 (14.4),
-// for 2048 x 4096 of 512 values with the old C, to FP32, 23.7 (23.8), where 256 x 256 takes
-// 29.8 (28.5); 128 channels x 64 tokens for 128 x 8192 13.4 (13.1), for 256 x 8192 22.0 (21.7);
+// for 2048 x 4096 of 512 values with the old C, to FP32, 20.1 (19.4), where 256 x 256 takes
+// 29.9 (28.5); 128 channels x 64 tokens for 128 x 8192 13.4 (13.1), for 256 x 8192 22.0 (21.7);
 // x 32 for 20 x 8192 10.6 (11.1); x 16 for 16 x 8192 11.4 (11.1), for 9 x 512, K = 1664, split
 // in four 5.3 (6.9); dot products for one token, 8192 channels 8.9 (8.9), 4096 channels 6.4
 // (7.9).
@@ -193,7 +193,7 @@ struct Kernel {
 constexpr Kernel kKernels[] = {{{kF8Channels, 16, 1}, 16, 128, 1, 0.19, 0.19, {{0.5, 0.5}, {0.9, 0.9}}, 0.8},
                                {{kF8Channels, 32, 1}, 32, 128, 1, 0.19, 0.19, {{0.5, 0.5}, {1.0, 1.0}}, 1.2},
                                {{kF8Channels, 64, 1}, 64, 128, 1, 0.25, 0.25, {{0.6, 0.6}, {2.2, 2.2}}, 0.0},
-                               {{kF8Pair, 128, 1}, 256, 128, 2, 0.28, 0.38, {{0.9, 1.1}, {2.4, 3.7}}, 0.0},
+                               {{kF8Pair, 128, 1}, 256, 128, 2, 0.28, 0.38, {{0.9, 1.1}, {1.8, 2.6}}, 0.0},
                                {{kF8Pair, 256, 1}, 256, 256, 2, 0.47, 0.74, {{1.5, 2.5}, {5.6, 10.1}}, 0.0}};
 constexpr double kStart = 4.5, kBytesUs = 6.2e6;
 
