@@ -127,6 +127,9 @@ struct Shape {
     // a slot of scales: [row][block], then [group][block] or [block][column]
     static constexpr int kSlotBytes = (kRowPitch * kRows + kSpan * (kUniform ? 2 : kBn)) * 4;
     static constexpr int kScaleBytes = kScaleSlots * kSlotBytes;
+    // arrivals that a slot of scales takes: one for each lane's asynchronous copies, and where the
+    // columns go through registers one that releases their stores
+    static constexpr uint32_t kScaleArrivals = 32 + (kSwap ? 1 : 0);
     // sums of 128 columns and 32 more on their way do not fit the 168 registers a thread that
     // 384 threads share alike: the four other warps give 112 each of theirs
     static constexpr bool kMoveRegs = kWgCols >= 128;
@@ -553,7 +556,10 @@ __device__ __forceinline__ void run_scales(const Params &p, const F8Table &table
                 }
             }
             __syncwarp();
+            // (announces the lane's asynchronous copies and nothing else that it wrote)
             ptx::cp_async_mbar_arrive_noinc(ptx::smem_addr(&ctrl->sc_full[st.slot]));
+            // the lanes' own stores are behind the __syncwarp, and one arrival releases them
+            if constexpr (S::kSwap) arrive_if(lane == 0, ptx::smem_addr(&ctrl->sc_full[st.slot]));
             st.next(kScaleSlots);
         }
     }
@@ -1122,7 +1128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(ptx::smem_addr(&ctrl->acc_empty[a]), kEpiWarps / S::kHalves * S::kCtas);
         }
         for (int s = 0; s < kScaleSlots; ++s) {
-            ptx::mbar_init(ptx::smem_addr(&ctrl->sc_full[s]), 32);
+            ptx::mbar_init(ptx::smem_addr(&ctrl->sc_full[s]), S::kScaleArrivals);
             ptx::mbar_init(ptx::smem_addr(&ctrl->sc_empty[s]), kEpiWarps);
         }
         for (int h = 0; h < 2; ++h) ptx::mbar_init(ptx::smem_addr(&ctrl->mma_done[h]), 1);
