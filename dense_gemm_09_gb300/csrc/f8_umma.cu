@@ -916,6 +916,11 @@ __device__ __forceinline__ void store_tokens(const Params &p, const CUtensorMap 
             continue;
         }
         if (DGEMM_CHECK(row_end <= p.c.M)) store_box(C, p.c.ldc, row_end, p.c.N, row0, c, words, buf, lane);
+        if (kExtra && kCols == 64 && p.tma_old) {
+            // a later tile's old C comes into this box by TMA, behind what the lanes wrote and read here
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+        }
     }
 }
 

@@ -45,3 +45,25 @@ def test_scales_of_many_turns(dg, k, rb, kernel):
             dg.gemm_f8_tn(a8, b8, c.fill_(float("nan")), sa, sb)
             assert torch.equal(c, want), dg.last_kernel()
     assert dg.device_status() == dg.OK
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n", [129, 1030, 1097])
+def test_the_old_c_behind_an_edge(dg, n, out):
+    """Several tiles a CTA of which some end inside a 16-byte word: their box is stored by the
+    warp, and takes the old C of a later tile by TMA."""
+    m, k = 20000, 256
+    a, b = ints(m, k), ints(n, k)
+    c0 = ints(m, n, most=200)
+    want = (a.double() @ b.double().t() - 2 * c0.double()).to(out)
+    store = torch.full((m, n + 16 - n % 16), 77.0, device="cuda").to(out)
+    c = store[:, :n]
+    a8, b8 = a.to(torch.float8_e4m3fn), b.to(torch.float8_e4m3fn)
+    ones = [torch.ones(m, 2, device="cuda"), torch.ones(n, 2, device="cuda")]
+    for rb in (1, 128):
+        for _ in range(5):
+            c.copy_(c0)
+            dg.tune_f8_next(2, 128, 1)
+            dg.gemm_f8_tn(a8, b8, c, ones[0], ones[1][:-(-n // rb)], beta=-2.0)
+            assert torch.equal(c, want), dg.last_kernel()
+    assert bool((store[:, n:] == 77).all()) and dg.device_status() == dg.OK
