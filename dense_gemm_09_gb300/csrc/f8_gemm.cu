@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) f8_any_kernel(const F8Params p, uint
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int64_t m = min(static_cast<int64_t>(tile.t0 + wr + i * 16 + h * 8 + g), static_cast<int64_t>(tile.t_end - 1));
+                    const int64_t m = min(static_cast<int64_t>(tile.t0) + wr + i * 16 + h * 8 + g, static_cast<int64_t>(tile.t_end - 1));
                     ra[i][h] = p.a.scale[p.a.band(m) * p.a.s_row + kb * p.a.s_blk];
                 }
 #pragma unroll
@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(kThreads) f8_any_kernel(const F8Params p, uint
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    const int64_t m = tile.t0 + wr + i * 16 + (v >> 1) * 8 + g, n = tile.n0 + wc + j * 8 + 2 * q + (v & 1);
+                    // (a tile of an expert that begins anywhere may end past 2^31)
+                    const int64_t m = static_cast<int64_t>(tile.t0) + wr + i * 16 + (v >> 1) * 8 + g, n = tile.n0 + wc + j * 8 + 2 * q + (v & 1);
                     if (m >= tile.t_end || n >= p.N || !DGEMM_CHECK(m < p.M)) continue;
                     T *dst = static_cast<T *>(p.C) + m * p.ldc + n;
                     float x = acc[i][j][v];
@@ -263,8 +264,9 @@ F8Config f8_take_tune()
 
 const char *launch_gemm_f8(const F8Params &p, const F8Config &tune, cudaStream_t stream, const DeviceInfo &dev)
 {
-    // TMA's conditions, but for C's
-    const bool tma = p.K > 0 && aligned(p.a.p, p.a.ld, 1, 16) && aligned(p.b.p, p.b.ld, 1, 16) &&
+    // TMA's conditions, but for C's; the kernels that use it count rows in 32 bits, to the end of a tile
+    constexpr int64_t kMost = INT32_MAX - 512;
+    const bool tma = p.K > 0 && p.M <= kMost && p.N <= kMost && p.K <= kMost && aligned(p.a.p, p.a.ld, 1, 16) && aligned(p.b.p, p.b.ld, 1, 16) &&
                      (p.experts == 1 || (p.b_stride % 16 == 0 && p.b_stride > 0));
     if (tma && tune.variant != kF8Any) {
         auto run = [&](const F8Config &cfg) {

@@ -42,7 +42,7 @@ __device__ __forceinline__ void fill_table(const F8Params &p, int tile, const F8
         // this lane's expert begins at `at` and the expert before it began at `prev`
         int32_t prev = __shfl_up_sync(0xFFFFFFFFu, at, 1);
         if (lane == 0) prev = e0 == 0 ? at : before;
-        uint32_t up = static_cast<uint32_t>(at - prev + tile - 1) / static_cast<uint32_t>(tile);
+        uint32_t up = (static_cast<uint32_t>(at - prev) + static_cast<uint32_t>(tile - 1)) / static_cast<uint32_t>(tile);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, up, o);
