@@ -20,7 +20,7 @@ import argparse
 import torch
 
 import dense_gemm_09_gb300 as dg
-from dense_gemm_09_gb300.w8a8 import _rows, _time
+from dense_gemm_09_gb300.w8a8 import _rows, _settle, _time
 
 F8 = torch.float8_e4m3fn
 
@@ -44,7 +44,9 @@ class ExpertMlp:
     float16 or bfloat16).
 
     Like GatedMlp it may be called from several streams and threads at once, and replayed in
-    graphs beside them: each call's rows are its own, allocated on the current stream."""
+    graphs beside them: each call's rows are its own, allocated on the current stream.  The
+    weights are laid out when the constructor returns (made in a capture, the layer belongs to
+    that graph's stream)."""
 
     def __init__(self, w_gate, w_up, w_down, dtype=torch.bfloat16):
         self.experts, self.ffn, self.hidden = w_gate.shape
@@ -52,6 +54,7 @@ class ExpertMlp:
         self.w1, self.s1 = quantize_experts(torch.cat([w_gate, w_up], 1))
         self.w2, self.s2 = quantize_experts(w_down)
         self.dtype = dtype
+        _settle(w_gate.device)  # the first call may come on any stream
 
     def __call__(self, x: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, h: torch.Tensor) -> torch.Tensor:
         """h (tokens x hidden, the residual stream) is updated and returned.  x: the tokens, normed;

@@ -30,6 +30,13 @@ def _rows(n: int, cols: int, dtype, device) -> torch.Tensor:
     return torch.empty((n, -(-cols // step) * step), dtype=dtype, device=device)[:, :cols]
 
 
+def _settle(device: torch.device) -> None:
+    """Waits for the current stream (unless it is being captured): what was laid out on it may
+    then be used on any other."""
+    if device.type == "cuda" and not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(device).synchronize()
+
+
 def quantize_weights(w: torch.Tensor):
     """Int8 rows and scales of a weight matrix (a row for each output channel)."""
     q = _rows(w.shape[0], w.shape[1], torch.int8, w.device)
