@@ -51,7 +51,8 @@ class GatedMlp:
     A layer may be called from several streams and threads at once, and replayed
     in graphs beside them: each call's rows are its own, allocated on the
     current stream (in a capture, in the graph's memory) as torch allocates any
-    tensor.  q1, t1, gu, q2, t2 are the last call's, to look at."""
+    tensor.  The weights are laid out when the constructor returns (made in a
+    capture, the layer belongs to that graph's stream).  q1, t1, gu, q2, t2 are the last call's, to look at."""
 
     q1 = t1 = gu = q2 = t2 = None
 
@@ -62,6 +63,7 @@ class GatedMlp:
         self.w1, self.s1 = quantize_weights(torch.cat([w_gate, w_up]))
         self.w2, self.s2 = quantize_weights(w_down)
         self.hidden, self.dtype, self.most = hidden, dtype, most
+        _settle(dev)  # the first call may come on any stream
 
     def __call__(self, h: torch.Tensor) -> torch.Tensor:
         """h (tokens x hidden, the residual stream) is updated and returned."""

@@ -33,3 +33,11 @@ def test_a_mixture_of_experts(dg):
     ids, share = torch.arange(100, device="cuda").view(50, 2) % 4, torch.full((50, 2), 0.5, device="cuda")
     got, want = first_call(lambda: ExpertMlp(*w), lambda layer: layer(x, ids, share, torch.zeros_like(x)))
     assert torch.equal(got, want) and bool(want.isfinite().all()) and bool((want != 0).any())
+
+
+def test_a_gated_layer(dg):
+    from dense_gemm_09_gb300.w8a8 import GatedMlp
+    w = [torch.randn(*s, device="cuda") / 16 for s in ((256, 384), (256, 384), (384, 256))]
+    h, gamma = torch.randn(50, 384, device="cuda").bfloat16(), torch.ones(384, device="cuda")
+    got, want = first_call(lambda: GatedMlp(gamma, *w, most=50), lambda layer: layer(h.clone()))
+    assert torch.equal(got, want) and bool(want.isfinite().all()) and bool((want != h).any())

@@ -46,3 +46,9 @@ def test_a_mixture_of_experts(calls):
     from dense_gemm_09_gb300.moe import ExpertMlp
     ExpertMlp(weights(3, 40, 24), weights(3, 40, 24), weights(3, 24, 40))
     assert calls == 6 * ["quantize_f8"] + ["settle cpu"]
+
+
+def test_a_gated_layer(calls):
+    from dense_gemm_09_gb300.w8a8 import GatedMlp
+    GatedMlp(torch.ones(24), weights(40, 24), weights(40, 24), weights(24, 40), most=4)
+    assert calls == 2 * ["quantize_i8"] + ["settle cpu"]
