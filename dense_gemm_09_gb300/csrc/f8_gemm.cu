@@ -262,8 +262,12 @@ F8Config f8_take_tune()
     return cfg;
 }
 
-const char *launch_gemm_f8(const F8Params &p, const F8Config &tune, cudaStream_t stream, const DeviceInfo &dev)
+const char *launch_gemm_f8(const F8Params &q, const F8Config &tune, cudaStream_t stream, const DeviceInfo &dev)
 {
+    F8Params p = q;
+    // the pitch of a single row is never used
+    if (p.M == 1) p.a.ld = (p.K + 15) / 16 * 16;
+    if (p.N == 1) p.b.ld = (p.K + 15) / 16 * 16;
     // TMA's conditions, but for C's; the kernels that use it count rows in 32 bits, to the end of a tile
     constexpr int64_t kMost = INT32_MAX - 512;
     const bool tma = p.K > 0 && p.M <= kMost && p.N <= kMost && p.K <= kMost && aligned(p.a.p, p.a.ld, 1, 16) && aligned(p.b.p, p.b.ld, 1, 16) &&
