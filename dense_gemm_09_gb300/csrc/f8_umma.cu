@@ -605,6 +605,9 @@ __device__ __forceinline__ bool sum_blocks(const Params &p, Ctrl *ctrl, uint32_t
         tmem_load<kChunk>(src, d[0]);
         e.acc.next(S::kAccs);
         ready = test(acc_full + e.acc.slot * 8, e.acc.phase);
+        // (the scales' product has to be a normal number, or 0: a multiplication of every value by
+        // either scale takes 334 us for 8192 x 8192 x 4096, and a choice between the two, for each
+        // block or for eight, 272 to 293 for 234, since its code moves this loop's registers)
         const float rc = S::kUniform ? r * c : r;
         const uint64_t r2 = pack2(rc, rc);
         const uint32_t cols = slot + (kRows * kRowPitch + j * S::kBn + group * S::kWgCols) * 4;

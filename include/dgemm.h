@@ -428,10 +428,13 @@ int dequantize_f8(int64_t rows, int64_t cols, const dgemm_f8 *Q, void *X, int64_
  * stands, dY W on W's transposed data and scales, and dY^T X on quantize_f8's
  * transposed form of both (block 1, beta = 1 to add to a gradient).
  * Sums within a block of 128 are formed by the tensor cores from exact products,
- * in FP32 arithmetic that truncates; sums over blocks in FP32.  Two blocks' scales
- * may be multiplied with each other first: their product has to be in FP32's normal
- * range (or 0).  One row of A
- * gives the same bits in any batch that takes the same kernel (dgemm_last_kernel).
+ * in FP32 arithmetic that truncates; sums over blocks in FP32.  A block's sum is
+ * multiplied by one scale and then by the other, but by the CTA pairs, with a B in
+ * bands of 128 rows, by the scales' product.  Which kernel runs depends on the sizes,
+ * so products of two blocks' scales should be in FP32's normal range, or 0: past it
+ * a row's results may lose bits or become 0, infinite or NaN (no other row's).
+ * One row of A gives the same bits in any batch that takes the same kernel
+ * (dgemm_last_kernel).
  * K == 0 gives bias + beta * C.  DGEMM_ERR_INVALID_ARG as above, and for more
  * than 2^31 - 1 tiles of 16 x 64 of C.
  */
