@@ -373,12 +373,17 @@ int gemm_i8_tn(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, co
  * zeros, so everything that is made from it is NaN.
  * Conventions, beyond those at the top: row-major, leading dimensions in
  *   elements, at least the row length; sizes of 0 return DGEMM_OK and write
- *   nothing; DGEMM_ERR_INVALID_ARG for negative sizes, more than 2^31 - 1 rows or
- *   columns, leading dimensions below the row length, negative scale strides
- *   (where the scales are written: also 0, if there are several along it), an
- *   unknown type or block, or a NULL pointer that is not said to be optional.  Pointers are aligned to their
- *   element type; rows on 16-byte boundaries take the fastest kernels.  Writes
- *   stay within the rows.  Outputs must not overlap inputs, except where a call allows it.
+ *   nothing but what does not depend on them (gemm_f8_tn without K: bias + beta C, and
+ *   gemm_f8_tn_experts the experts' rows as 0; sort_by_expert without pairs: the offsets;
+ *   combine_experts without choices or sorted rows: beta X; combine_experts_grad without
+ *   columns or sorted rows: dweights); DGEMM_ERR_INVALID_ARG for negative sizes,
+ *   more than 2^31 - 1 rows or columns, leading dimensions below the row length,
+ *   negative scale strides (where the scales are written: also 0, if there are
+ *   several along it), an unknown type or block, or a NULL pointer that is not said to
+ *   be optional.  Pointers are aligned to their element type; rows on 16-byte
+ *   boundaries take the fastest kernels (a single row that begins on one, at any
+ *   pitch).  Writes stay within the rows.  Outputs must not overlap inputs, except
+ *   where a call allows it.
  * Source: none on the pages (their products take 16- and 32-bit operands).
  */
 typedef enum {
