@@ -13,8 +13,8 @@
 // shuffles, stores of 8 bytes a lane, without shared memory or barriers.
 //
 // 8192 x 8192, and the time of its bytes at the measured copy rate: bf16 rows 38.1 us
-// (30.1), FP32 50.1 (50), gated bf16 59.7 (50), blocks of 128 x 128 bf16 33.6 (29.8) and FP32
-// 56 (49.6), transposed bf16 42.1 (30.1), back to bf16 32.3 (30.1).  Of the 16-bit forms the
+// (30.1), FP32 50.1 (50), gated bf16 59.7 (50), blocks of 128 x 128 bf16 31.3 (29.8) and FP32
+// 51 (49.6), transposed bf16 39.3 (30.1), back to bf16 32.3 (30.1).  Of the 16-bit forms the
 // instructions bound the rest: the conversion to 8 bits takes 21 values a clock and SM.
 #include <cstdint>
 #include <type_traits>
@@ -201,7 +201,8 @@ constexpr size_t tile_smem()
 
 // The columns that a thread has of a tile: eight in a row, or (FP32) four and, 64 on, four more,
 // so that the 16-byte words of neighbouring threads lie side by side: copies of every other
-// word read each sector of L2 twice (16384 x 8192 in blocks 169 us, and 110).
+// word read each sector of L2 twice (16384 x 8192 in blocks 169 us, and 110; 99 with the words'
+// places worked out once a tile instead of once a row).
 template <typename T>
 struct TileCols {
     static constexpr bool kSplit = sizeof(T) == 4;
@@ -258,15 +259,22 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) f8_tile_kern
         if (kAligned && tile < p.tiles) {
             int64_t r0, c0;
             origin(tile, r0, c0);
+            int64_t col[kWords];  // of this thread's words, and the elements there: the same in every row
+            int in[kWords];
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+                col[w] = c0 + Cols::at(lane, w * kPer);
+                const int64_t left = p.cols - col[w];
+                in[w] = left >= kPer ? kPer : left > 0 ? static_cast<int>(left) : 0;
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int64_t row = r0 + row_of(i);
-                const T *src = static_cast<const T *>(p.x) + (row < p.rows ? row * p.ldx : 0);
 #pragma unroll
                 for (int w = 0; w < kWords; ++w) {
-                    const int64_t col = c0 + Cols::at(lane, w * kPer), left = row < p.rows ? p.cols - col : 0;
-                    const int in = left >= kPer ? kPer : left > 0 ? static_cast<int>(left) : 0;
-                    copy_async16(slot_of(slot, i, w), in > 0 ? src + col : src, in * static_cast<int>(sizeof(T)));
+                    const int n = row < p.rows ? in[w] : 0;
+                    const T *src = static_cast<const T *>(p.x) + (n > 0 ? row * p.ldx + col[w] : 0);
+                    copy_async16(slot_of(slot, i, w), src, n * static_cast<int>(sizeof(T)));
                 }
             }
         }
