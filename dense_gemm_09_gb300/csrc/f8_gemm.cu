@@ -176,12 +176,12 @@ const char *launch_any(const F8Params &p, cudaStream_t stream, const DeviceInfo 
 // The kernels' times, fitted to GB300 sweeps: a start, then waves of tiles, each of which takes
 // a CTA (pair) `block` for every 128 of K and `tile` besides; never less than the operands'
 // bytes.  In microseconds, K = 4096, measured and as estimated here: pair 256 x 256 for 8192 x
-// 8192 235 (236), and with a scale a row 354 (357); pair 256 x 128 for 512 x 4096 14.4 (14.4),
-// for 2048 x 4096 of 512 values with the old C, to FP32, 20.1 (19.4), where 256 x 256 takes
-// 29.9 (28.5); 128 channels x 64 tokens for 128 x 8192 13.4 (13.1), for 256 x 8192 22.0 (21.7);
-// x 32 for 20 x 8192 10.6 (11.1); x 16 for 16 x 8192 11.4 (11.1), for 9 x 512, K = 1664, split
-// in four 5.3 (6.9); dot products for one token, 8192 channels 8.9 (8.9), 4096 channels 6.4
-// (7.9).
+// 8192 233 (236), and with a scale a row 355 (357); pair 256 x 128 for 512 x 4096 14.6 (14.4),
+// for 2048 x 4096 of 512 values with the old C, to FP32, 19.8 (19.4), where 256 x 256 takes
+// 29.8 (28.5); 128 channels x 64 tokens for 128 x 8192 13.5 (13.1), for 256 x 8192 22.4 (21.7);
+// x 32 for 20 x 8192 10.8 (11.1), split in two 10.9 (9.9); x 16 for 16 x 8192 11.4 (11.1), split
+// in two 10.3 (9.9), for 9 x 512, K = 1664, split in two, as chosen, 5.4 (7.1), in four 5.3
+// (7.4); dot products for one token, 8192 channels 8.9 (8.9), 4096 channels 6.4 (7.9).
 struct Kernel {
     F8Config cfg;
     int tokens, channels, ctas;  // of a tile
@@ -190,7 +190,7 @@ struct Kernel {
     double join;                 // of split sums, for every doubling of the CTAs
 };
 // (Narrow tiles first: of kernels that the bytes bound they do best, one token, 8 of 64 experts
-// of 4096 x 2048, x 16 11.3 us, x 32 12.6, x 64 15.1.)
+// of 4096 x 2048, x 16 11.5 us, x 32 13.0, x 64 15.4.)
 constexpr Kernel kKernels[] = {{{kF8Channels, 16, 1}, 16, 128, 1, 0.19, 0.19, {{0.5, 0.5}, {0.9, 0.9}}, 0.8},
                                {{kF8Channels, 32, 1}, 32, 128, 1, 0.19, 0.19, {{0.5, 0.5}, {1.0, 1.0}}, 1.2},
                                {{kF8Channels, 64, 1}, 64, 128, 1, 0.25, 0.25, {{0.6, 0.6}, {2.2, 2.2}}, 0.0},

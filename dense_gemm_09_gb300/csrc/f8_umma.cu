@@ -8,13 +8,14 @@
 // the accumulator is read back block by block, multiplied by its row's and column's
 // scales and added to sums in registers, in FP32, while the MMAs fill the next one.
 //
-// What bounds it.  For many tokens the card's power.  8192 x 8192 x 4096 takes 235 to 247
-// us (2230 to 2340 TFLOP/s) at 1390 of 1400 W and 1950 MHz: ~1000 clocks a block of a 256 x
-// 256 tile, where the MMAs alone take 512 (8192 products a clock and SM) and the packed FMAs
-// of a CTA 256 beside them.  Operands of zeros run in the same number of clocks, at 2070 MHz.
+// What bounds it.  For many tokens the epilogue: 8192 x 8192 x 4096 takes 233 us (2360 TFLOP/s),
+// ~1000 clocks a block of a 256 x 256 tile, where the MMAs alone take 512 (8192 products a clock
+// and SM) and the packed FMAs of a CTA 256 beside them; each of eight warps reads its 128 columns
+// in eight dependent pieces.  In a long run the card's power limit takes the clock to 1957 of
+// 2070 MHz, 248 us; zeros, which stay below the limit (740 of 1400 W), take 230 all the same.
 // Of 137 us for 4864 x 8192 x 4096, 32 go without the FMAs and another 2 without reading the
-// accumulators; fewer clocks a block were not less time (larger pieces of the accumulator
-// read at once, or the next block's first piece ahead: 145 to 159 us, with spilled sums).
+// accumulators (1.25 x the time of the operations).  Larger pieces of the accumulator read at
+// once, or the next block's first piece ahead, spilled sums (145 to 159 us).
 // For few tokens the weights' bytes: there the channels are the MMA's rows and the tokens its
 // columns (kSwap), so that no row of the tensor cores' work is padding that is loaded: 16
 // tokens, 8 of 64 experts of 4096 x 2048 take 66 us, 7.2 TB/s (reads alone go faster than copies).
@@ -105,7 +106,8 @@ struct Params {
 // tokens; kBn columns to a tile; kUniform: the scales of a group's columns are one number
 // (bands of 128 channels); kExtra: the call may have a bias or a beta (a kernel of their own
 // for the CTA pairs: without, the sums of 256 columns just fit the registers, and 8 bytes a
-// thread that do not cost 8192 x 8192 x 4096 20 of 237 us).
+// thread that do not cost 8192 x 8192 x 4096 20 of 237 us; with it 256 columns spill 44 bytes, or
+// 64 with a scale a row, and a bias takes 269 us where 233 are without, 397 where 355).
 template <int kCtas_, bool kSwap_, int kBn_, bool kUniform_, bool kExtra_>
 struct Shape {
     static constexpr int kCtas = kCtas_, kBn = kBn_;
