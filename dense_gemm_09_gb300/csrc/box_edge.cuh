@@ -2,7 +2,11 @@
 //
 // A TMA store leaves out whole 16-byte words outside the tensor, not elements: where N
 // elements end inside a word, the rest of that word is written too (N = 257 to FP32 at a
-// pitch of 272: three elements a row), which may be a neighbouring matrix's.
+// pitch of 272: three elements a row), which may be a neighbouring matrix's.  Storing such
+// boxes by their warp costs 300 x 257 x 512 in bf16 0.8 of 6.6 us and 2048 x 2047 x 512 0.2 to
+// 0.9 of 10 to 11; a tensor of N's whole words and the last word's elements by the lanes of their
+// rows was slower (4096 x 4097 x 2048 of 8 bits to FP32, with the old C, 81.9 for 76.3 us), the
+// loop below unrolled or called no faster.
 #pragma once
 
 #include <cstdint>
